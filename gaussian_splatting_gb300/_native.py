@@ -24,7 +24,9 @@ EXPORTS = ["gs_last_error", "gs_version", "gs_project", "gs_project_batch", "gs_
            "gs_render_fwd", "gs_tile_order", "gs_loss_workspace_size", "gs_loss", "gs_loss_noalloc", "gs_render_bwd", "gs_project_bwd",
            "gs_visible_sets_workspace_size", "gs_visible_sets", "gs_sparse_adam", "gs_project_bwd_adam",
            "gs_tile_split", "gs_view_order", "gs_prune_workspace_size", "gs_prune", "gs_densify_workspace_size",
-           "gs_densify", "gs_probe_ffma",
+           "gs_densify", "gs_probe_ffma", "gs_linear_fwd_workspace_size", "gs_linear_fwd",
+           "gs_linear_bwd_workspace_size", "gs_linear_bwd", "gs_layernorm_fwd", "gs_layernorm_bwd_workspace_size",
+           "gs_layernorm_bwd",
            "gs_debug_set_wait_limit",
            "gs_debug_drop_publish"]
 
@@ -39,6 +41,24 @@ class Camera(C.Structure):
     _fields_ = [("R", C.c_float * 9), ("t", C.c_float * 3), ("fx", C.c_float), ("fy", C.c_float),
                 ("cx", C.c_float), ("cy", C.c_float), ("znear", C.c_float), ("width", C.c_int32),
                 ("height", C.c_int32)]
+
+
+GS_F32, GS_BF16 = 0, 1
+GS_ACT_NONE, GS_ACT_RELU, GS_ACT_GELU, GS_ACT_SILU = 0, 1, 2, 3
+
+
+class LinearDesc(C.Structure):
+    """gs_linear_desc."""
+    _fields_ = [("rows", C.c_int64), ("ldx", C.c_int64), ("ldw", C.c_int64), ("ldr", C.c_int64), ("ldy", C.c_int64),
+                ("ldz", C.c_int64), ("lddx", C.c_int64), ("lddw", C.c_int64), ("in_features", C.c_int32),
+                ("out_features", C.c_int32), ("dtype", C.c_int32), ("act", C.c_int32)]
+
+
+class LayerNormDesc(C.Structure):
+    """gs_layernorm_desc."""
+    _fields_ = [("rows", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64), ("lddy", C.c_int64),
+                ("ldskip", C.c_int64), ("lddx", C.c_int64), ("width", C.c_int32), ("dtype", C.c_int32),
+                ("eps", C.c_float)]
 
 
 def camera(cam) -> Camera:
@@ -94,6 +114,13 @@ def load() -> C.CDLL:
         "gs_densify_workspace_size": ([i64], sz),
         "gs_densify": ([vp, vp, vp, i64, vp, f32, f32, vp, vp, vp, vp, i64, vp, sz, vp, vp, vp], i32),
         "gs_probe_ffma": ([vp, i32, i32, vp], i32),
+        "gs_linear_fwd_workspace_size": ([vp], sz),
+        "gs_linear_fwd": ([vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp], i32),
+        "gs_linear_bwd_workspace_size": ([vp], sz),
+        "gs_linear_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp], i32),
+        "gs_layernorm_fwd": ([vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        "gs_layernorm_bwd_workspace_size": ([vp], sz),
+        "gs_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
         "gs_debug_set_wait_limit": ([i64], None),
         "gs_debug_drop_publish": ([i32], None),
     }
@@ -328,3 +355,37 @@ def gs_debug_set_wait_limit(iterations: int):
 def gs_debug_drop_publish(mode: int):
     """0 disarms; 1 drops CTA 0's first barrier arrival in the tile sort, 2 in the depth sort."""
     load().gs_debug_drop_publish(int(mode))
+
+
+def gs_linear_fwd_workspace_size(desc) -> int:
+    return load().gs_linear_fwd_workspace_size(C.addressof(desc))
+
+
+def gs_linear_fwd(desc, x, w, bias, residual, y, z, workspace, workspace_bytes, status=None, stream=None):
+    _check(load().gs_linear_fwd(C.addressof(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z),
+                                _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)), "gs_linear_fwd")
+
+
+def gs_linear_bwd_workspace_size(desc) -> int:
+    return load().gs_linear_bwd_workspace_size(C.addressof(desc))
+
+
+def gs_linear_bwd(desc, dy, x, w, z, dx, dw, dbias, workspace, workspace_bytes, status=None, stream=None):
+    _check(load().gs_linear_bwd(C.addressof(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z), _ptr(dx), _ptr(dw),
+                                _ptr(dbias), _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
+           "gs_linear_bwd")
+
+
+def gs_layernorm_fwd(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None):
+    _check(load().gs_layernorm_fwd(C.addressof(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean),
+                                   _ptr(rstd), _stream(stream)), "gs_layernorm_fwd")
+
+
+def gs_layernorm_bwd_workspace_size(desc) -> int:
+    return load().gs_layernorm_bwd_workspace_size(C.addressof(desc))
+
+
+def gs_layernorm_bwd(desc, dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, workspace, workspace_bytes, stream=None):
+    _check(load().gs_layernorm_bwd(C.addressof(desc), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                   _ptr(skip), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace_bytes,
+                                   _stream(stream)), "gs_layernorm_bwd")

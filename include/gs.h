@@ -444,6 +444,97 @@ gs_status gs_densify(const float* params, const float* exp_avg, const float* exp
                      int64_t out_stride, void* workspace, size_t workspace_bytes, int64_t* counts,
                      int64_t* counts_host, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense layers of a per-Gaussian attribute head: the linear layer and layer normalisation,
+ * forward and backward.  A head maps a row of features per Gaussian (an embedding, a time, a
+ * decoded anchor) to corrections of its record, before gs_project reads it and after
+ * gs_project_bwd has given the record's gradient.  The pages have no counterpart; the
+ * appearance models of large-scene training are the use.
+ *
+ * Matrices are row-major with a stride between rows, in elements (ld*; at least the width), of
+ * one element type for every array of a call unless a comment says otherwise.  Any width,
+ * stride and element-aligned address is valid; calls whose rows all start on 16-byte boundaries
+ * run faster.  Sums, products, activations and statistics are computed in 32 bits (bfloat16
+ * products are exact, their sums 32-bit) and rounded once when stored.
+ */
+typedef enum { GS_F32 = 0, GS_BF16 = 1 } gs_dtype;
+typedef enum {
+  GS_ACT_NONE = 0, /* v */
+  GS_ACT_RELU = 1, /* max(v, 0) (NaN stays NaN); slope 1 for v > 0, else 0 */
+  GS_ACT_GELU = 2, /* v Phi(v), Phi the standard normal distribution function (erf form) */
+  GS_ACT_SILU = 3  /* v / (1 + exp(-v)) */
+} gs_act;
+
+/* ---------------------------------------------------------------------------
+ * gs_linear_fwd -- z = x w^T + bias, y = act(z) + residual.
+ *   x [rows][in] stride ldx; w [out][in] stride ldw; bias [out] or NULL;
+ *   residual [rows][out] stride ldr, or NULL; y [rows][out] stride ldy;
+ *   z [rows][out] stride ldz, or NULL: the sum before the activation, which gs_linear_bwd
+ *   reads (not needed with GS_ACT_NONE).
+ *   y may be the residual itself (same address and stride); no other output may overlap an input.
+ *   workspace  gs_linear_fwd_workspace_size(d) bytes, 16-byte aligned (may be 0: NULL).
+ *   status     device int32 or NULL: bit 1 (value 2) is set if a bounded device-side wait gave
+ *              up, in which case the outputs are not valid.  Never cleared by the library.
+ * rows == 0 is a no-op.  in and out are 1..2^20, rows at most 2^31 - 1.
+ *
+ * gs_linear_bwd -- the gradient, from dy [rows][out] (stride ldy) and the forward's x, w and z:
+ *   dz = dy act'(z); dx = dz w; dw = dz^T x; dbias = sum over rows of dz.
+ *   z          stride ldz; may be NULL with GS_ACT_NONE only.
+ *   dx [rows][in] stride lddx, dw [out][in] stride lddw, dbias [out]: outputs, each may be NULL
+ *              (not computed).  They are overwritten, not added to.  The residual's gradient
+ *              is dy itself.
+ *   With GS_BF16, dz is rounded to bfloat16 where it enters the products (dbias sums it
+ *   unrounded).  rows == 0 writes zeros to dw and dbias.
+ *   Results do not depend on the launch order: no atomics touch them.
+ */
+typedef struct {
+  int64_t rows;
+  int64_t ldx, ldw, ldr, ldy, ldz, lddx, lddw; /* strides in elements; those a call does not use are ignored */
+  int32_t in_features, out_features;
+  int32_t dtype; /* gs_dtype */
+  int32_t act;   /* gs_act */
+} gs_linear_desc;
+
+size_t gs_linear_fwd_workspace_size(const gs_linear_desc* d);
+gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias,
+                        const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream);
+size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d);
+gs_status gs_linear_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z,
+                        void* dx, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gs_layernorm_fwd -- per row of x [rows][width] (stride ldx): mean, rstd = (var + eps)^-1/2 with
+ * var the mean squared distance from the mean, y = (x - mean) rstd gamma + beta (stride ldy).
+ *   gamma, beta [width]; mean, rstd [rows] float32 outputs, each may be NULL.  y may be x itself.
+ * rows == 0 is a no-op; width is 1..2^24.
+ *
+ * gs_layernorm_bwd -- with h = (x - mean) rstd and g = dy gamma:
+ *   dx = rstd (g - mean(g) - h mean(g h)) + skip, dgamma = sum over rows of dy h,
+ *   dbeta = sum over rows of dy.
+ *   dy stride lddy; skip [rows][width] stride ldskip, or NULL: a gradient that reaches x by
+ *   another path (the residual connection around the layer); dx stride lddx.  dx, dgamma [width],
+ *   dbeta [width] may each be NULL (not computed); dx may be dy or skip itself.
+ *   workspace  gs_layernorm_bwd_workspace_size(d) bytes, 16-byte aligned; not needed (NULL) when
+ *              dgamma and dbeta are both NULL.
+ * rows == 0 writes zeros to dgamma and dbeta.  Sums are taken in a fixed order: no atomics.
+ */
+typedef struct {
+  int64_t rows;
+  int64_t ldx, ldy, lddy, ldskip, lddx; /* strides in elements; those a call does not use are ignored */
+  int32_t width;
+  int32_t dtype; /* gs_dtype */
+  float eps;     /* forward only */
+} gs_layernorm_desc;
+
+gs_status gs_layernorm_fwd(const gs_layernorm_desc* d, const void* x, const void* gamma, const void* beta,
+                           void* y, float* mean, float* rstd, void* stream);
+size_t gs_layernorm_bwd_workspace_size(const gs_layernorm_desc* d);
+gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy, const void* x, const void* gamma,
+                           const float* mean, const float* rstd, const void* skip, void* dx, void* dgamma,
+                           void* dbeta, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,442 @@
+"""The dense-layer entry points (gs_linear_*, gs_layernorm_*) against the same formulas in 64 bits.
+
+Tolerances are derived from the arithmetic, elementwise.  With u = 2^-24 (32-bit rounding):
+ - a sum of k terms whose signs vary: each of the k additions is off by at most 2u of the partial sum,
+   which grows as sqrt(k): (8 + 2 sqrt(k)) u times the sum of the terms' absolute values covers it, even
+   where every addition rounds the same way;
+ - the type's own rounding of a stored value: v = 2^-8 (bfloat16: 8 significant bits, half a unit of the last) or 2^-24 (float32) of it;
+ - the activations are evaluated to a few u of their argument (their slopes are at most 1.13);
+ - in bfloat16 a linear layer's dz is rounded once more where it enters the products (when there is
+   an activation): v times the products' absolute values.
+"""
+import math
+import os
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+sys.path.insert(0, ROOT)
+
+from gaussian_splatting_gb300 import _native as N  # noqa: E402
+from gaussian_splatting_gb300 import dense  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+ROUND = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+ACTS = ["none", "relu", "gelu", "silu"]
+
+
+def _sum_u(k):
+    return (8 + 2 * math.sqrt(k)) * U
+
+
+def _rand(shape, dtype, seed, std=1.0, pad=0, shift=0):
+    """A normal matrix or vector; `pad` extra elements between rows, `shift` elements off the allocation."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    v = (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+    if not pad and not shift:
+        return v
+    if len(shape) == 1:
+        out = torch.zeros(shape[0] + shift, dtype=dtype, device="cuda")[shift:]
+    else:
+        out = torch.zeros(shape[0] * (shape[1] + pad) + shift, dtype=dtype, device="cuda")[shift:].view(
+            shape[0], shape[1] + pad)[:, :shape[1]]
+    out.copy_(v)
+    return out
+
+
+def _twin(t):
+    """A copy with the same strides and alignment (another layout may sum in another order)."""
+    return torch.empty(0, dtype=t.dtype, device=t.device).set_(t.untyped_storage().clone(), t.storage_offset(), t.size(),
+                                                               t.stride())
+
+
+def _act(z, act):
+    if act == "relu":
+        return torch.where(z > 0, z, torch.zeros_like(z))
+    if act == "gelu":
+        return z * 0.5 * torch.erfc(-z / math.sqrt(2.0))
+    if act == "silu":
+        return z * torch.sigmoid(z)
+    return z
+
+
+def _slope(z, act):
+    if act == "relu":
+        return (z > 0).double()
+    if act == "gelu":
+        return 0.5 * torch.erfc(-z / math.sqrt(2.0)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return s * (1 + z * (1 - s))
+    return torch.ones_like(z)
+
+
+def _close(got, want, tol, what):
+    off = (got.double() - want).abs()
+    assert torch.isfinite(got.double()).all(), f"{what}: not finite"
+    worst = (off - tol).max().item() if off.numel() else -1.0
+    assert worst <= 0, f"{what}: {int((off > tol).sum())} of {off.numel()} out, worst ratio {(off / tol).max().item():.3g}"
+
+
+def _linear_tolerances(x, w, b, r, act):
+    X, W = x.double(), w.double()
+    z = X @ W.T
+    mag = X.abs() @ W.abs().T
+    if b is not None:
+        z = z + b.double()
+        mag = mag + b.double().abs()
+    ez = _sum_u(x.shape[1]) * mag
+    y = _act(z, act)
+    ey = 1.13 * ez + 8 * U * z.abs() + 4 * U * y.abs()
+    if r is not None:
+        ey = ey + 2 * U * (y.abs() + r.double().abs())
+        y = y + r.double()
+    v = ROUND[x.dtype]
+    tiny = 2.0 ** -126
+    return y, ey + 1.01 * v * y.abs() + tiny, z, ez + 1.01 * v * z.abs() + tiny
+
+
+# rows, in, out: one of everything, widths around the tiles' edges, odd ones, a long reduction, few
+# rows with many features (split reductions), many rows with few
+SHAPES = [(1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 1024, 512), (3, 5, 7), (16, 32, 128), (17, 4096, 40), (64, 64, 1),
+          (127, 129, 65), (128, 64, 256), (129, 256, 59), (300, 45, 3), (1000, 1, 33), (257, 1100, 17), (2048, 64, 64),
+          (77, 513, 300), (640, 256, 264), (5000, 128, 128), (1111, 72, 520)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_forward(shape, dtype):
+    rows, n_in, n_out = shape
+    k = SHAPES.index(shape)
+    for i, act in enumerate(ACTS):
+        has_b, has_r, keep = (k + i) % 3 != 0, (k + i) % 2 == 0, (k + i) % 4 != 1
+        x, w = _rand((rows, n_in), dtype, 1), _rand((n_out, n_in), dtype, 2, 1 / math.sqrt(n_in))
+        b = _rand((n_out,), dtype, 3, 0.3) if has_b else None
+        r = _rand((rows, n_out), dtype, 4) if has_r else None
+        y, z = dense.linear_fwd(x, w, b, r, act=act, keep_z=keep)
+        Y, ey, Z, ez = _linear_tolerances(x, w, b, r, act)
+        _close(y, Y, ey, f"y {act} bias={has_b} residual={has_r}")
+        assert (z is not None) == keep
+        if keep:
+            _close(z, Z, ez, f"z {act}")
+
+
+def _linear_grads(dy, x, w, z, act):
+    DY, X, W = dy.double(), x.double(), w.double()
+    if act == "none":
+        s, d = torch.ones_like(DY), DY
+    else:
+        s = _slope(z.double(), act)
+        d = DY * s
+    v = ROUND[dy.dtype]
+    ed = 0 * d if act == "none" else 16 * U * (DY * (1 + z.double().abs())).abs()  # the slope's evaluation
+    ein = ed + (1.01 * v * d.abs() if act != "none" and dy.dtype == BF16 else 0)
+    tiny = 2.0 ** -126
+    out = {}
+    out["dx"] = (d @ W, ein @ W.abs() + _sum_u(dy.shape[1]) * (d.abs() @ W.abs()))
+    out["dw"] = (d.T @ X, ein.T @ X.abs() + _sum_u(dy.shape[0]) * (d.abs().T @ X.abs()))
+    out["db"] = (d.sum(0), ed.sum(0) + _sum_u(dy.shape[0]) * d.abs().sum(0))
+    return {k: (g, e + 1.01 * v * g.abs() + tiny) for k, (g, e) in out.items()}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_backward(shape, dtype):
+    rows, n_in, n_out = shape
+    for act in ACTS:
+        dy, x = _rand((rows, n_out), dtype, 5, 1e-3), _rand((rows, n_in), dtype, 6)
+        w = _rand((n_out, n_in), dtype, 7, 1 / math.sqrt(n_in))
+        z = None if act == "none" else _rand((rows, n_out), dtype, 8)
+        dx, dw, db = dense.linear_bwd(dy, x, w, z, act=act)
+        want = _linear_grads(dy, x, w, z, act)
+        _close(dx, *want["dx"], f"dx {act}")
+        _close(dw, *want["dw"], f"dw {act}")
+        _close(db, *want["db"], f"db {act}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (24, 8), (1, 0), (3, 1), (2, 0)])
+def test_linear_takes_any_stride_and_alignment_and_leaves_the_gaps(dtype, pad, shift):
+    rows, n_in, n_out = 389, 136, 72
+    x = _rand((rows, n_in), dtype, 1, 1.0, pad, shift)
+    w = _rand((n_out, n_in), dtype, 2, 0.1, pad, shift)
+    b = _rand((n_out,), dtype, 3, 0.3, 0, shift)
+    r = _rand((rows, n_out), dtype, 4, 1.0, pad, shift)
+
+    def canvas(m, n):
+        full = torch.full((m * (n + pad) + shift,), 7.0, dtype=dtype, device="cuda")
+        return full, full[shift:].view(m, n + pad)[:, :n]
+
+    def gaps_kept(full, m, n):
+        body = full[shift:].view(m, n + pad)
+        assert (full[:shift] == 7).all() and (body[:, n:] == 7).all()
+
+    fy, y = canvas(rows, n_out)
+    fz, z = canvas(rows, n_out)
+    dense.linear_fwd(x, w, b, r, act="gelu", out=y, z=z)
+    Y, ey, Z, ez = _linear_tolerances(x, w, b, r, "gelu")
+    _close(y, Y, ey, "y")
+    _close(z, Z, ez, "z")
+    gaps_kept(fy, rows, n_out)
+    gaps_kept(fz, rows, n_out)
+    fdx, dx = canvas(rows, n_in)
+    fdw, dw = canvas(n_out, n_in)
+    dy = _rand((rows, n_out), dtype, 5, 1e-2, pad, shift)
+    _, _, db = dense.linear_bwd(dy, x, w, z, act="gelu", dx=dx, dw=dw)
+    want = _linear_grads(dy, x, w, z, "gelu")
+    for k, v in (("dx", dx), ("dw", dw), ("db", db)):
+        _close(v, *want[k], k)
+    gaps_kept(fdx, rows, n_in)
+    gaps_kept(fdw, n_out, n_in)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_linear_residual_in_place_and_partial_outputs(dtype):
+    rows, n = 1500, 96
+    x, w, r = _rand((rows, n), dtype, 1), _rand((n, n), dtype, 2, 0.1), _rand((rows, n), dtype, 3)
+    y, _ = dense.linear_fwd(x, w, None, r, act="silu")
+    h = r.clone()
+    out, _ = dense.linear_fwd(x, w, None, h, act="silu", out=h)
+    assert out is h and torch.equal(h, y)
+    dy, z = _rand((rows, n), dtype, 4, 1e-3), _rand((rows, n), dtype, 5)
+    full = dense.linear_bwd(dy, x, w, z, act="silu")
+    for kw, kept in ((dict(need_dx=False), (1, 2)), (dict(need_dw=False), (0, 2)), (dict(bias=False), (0, 1)),
+                     (dict(need_dx=False, need_dw=False), (2,))):
+        part = dense.linear_bwd(dy, x, w, z, act="silu", **kw)
+        for i in range(3):
+            assert (part[i] is not None) == (i in kept)
+            if i in kept:
+                assert torch.equal(part[i], full[i])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_no_rows(dtype):
+    x, w = torch.empty((0, 24), dtype=dtype, device="cuda"), _rand((16, 24), dtype, 1)
+    y, z = dense.linear_fwd(x, w, None, None, act="relu", keep_z=True)
+    assert y.shape == (0, 16) and z.shape == (0, 16)
+    wide = torch.full((16, 40), 7.0, dtype=dtype, device="cuda")
+    dx, dw, db = dense.linear_bwd(y, x, w, z, act="relu", dw=wide[:, :24])
+    assert dx.shape == (0, 24) and not dw.any() and not db.any() and (wide[:, 24:] == 7).all()
+    y, mean, rstd = dense.layernorm_fwd(x, w[0].contiguous(), w[1].contiguous())
+    assert y.shape == (0, 24) and mean.shape == (0,)
+    dx, dg, db = dense.layernorm_bwd(y, x, w[0].contiguous(), mean, rstd)
+    assert dx.shape == (0, 24) and not dg.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(640, 256, 256), (640, 75, 35), (5, 256, 64)], ids=str)
+def test_what_is_not_finite_stays_in_its_row(dtype, shape):
+    """A row of x (or dy) with an infinity or a NaN makes that row of y (dx) not finite and leaves the bits of
+    every other row."""
+    rows, n_in, n_out = shape
+    x, w = _rand((rows, n_in), dtype, 1), _rand((n_out, n_in), dtype, 2, 0.1)
+    y, _ = dense.linear_fwd(x, w, act="gelu")
+    bad = x.clone()
+    bad[1, 3], bad[4, 0], bad[rows - 2, n_in - 1] = math.inf, math.nan, -math.inf
+    yb, zb = dense.linear_fwd(bad, w, act="gelu", keep_z=True)
+    hit = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    hit[[1, 4, rows - 2]] = True
+    assert torch.equal(yb[~hit], y[~hit])
+    assert not torch.isfinite(zb[hit].float()).any()
+    dy = _rand((rows, n_out), dtype, 3, 1e-3)
+    dx, _, _ = dense.linear_bwd(dy, x, w)
+    dy[4, n_out - 1] = math.nan
+    dxb, dwb, dbb = dense.linear_bwd(dy, x, w)
+    keep = torch.arange(rows, device="cuda") != 4
+    assert torch.equal(dxb[keep], dx[keep]) and torch.isnan(dxb[4].float()).all()
+    assert torch.isnan(dwb[n_out - 1].float()).all() and torch.isfinite(dwb[:n_out - 1].float()).all()
+    assert torch.isnan(dbb[n_out - 1].float()) and torch.isfinite(dbb[:n_out - 1].float()).all()
+
+
+# widths: every form (part of a warp, a warp, a block, wider than its registers), odd ones
+WIDTHS = [1, 2, 7, 8, 24, 64, 100, 128, 256, 257, 500, 512, 1000, 1024, 2048, 2049, 4096, 6000, 8192, 20000, 70001]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_layernorm_forward_and_backward(width, dtype):
+    for rows, pad, shift in ((1, 0, 0), (37, 8, 0), (301, 3, 1)):
+        _check_norm(rows, width, dtype, pad, shift)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(40_000, 64), (30_001, 96), (12_345, 129), (9_000, 1024)])
+def test_layernorm_with_many_rows(rows, width, dtype):
+    _check_norm(rows, width, dtype, 0, 0)
+
+
+def _check_norm(rows, width, dtype, pad, shift):
+    eps, v = 1e-5, ROUND[dtype]
+    x = _rand((rows, width), dtype, 1, 1.5, pad, shift)
+    x += 2.0  # a mean that a one-pass variance would lose digits to
+    gamma, beta = _rand((width,), dtype, 2, 0.3) + 1, _rand((width,), dtype, 3, 0.3)
+    y, mean, rstd = dense.layernorm_fwd(x, gamma, beta, eps=eps)
+    X, G, B = x.double(), gamma.double(), beta.double()
+    m = X.mean(1, keepdim=True)
+    var = (X - m).square().mean(1, keepdim=True)
+    rs = (var + eps) ** -0.5
+    h = (X - m) * rs
+    su = _sum_u(width)
+    em = su * X.abs().mean(1, keepdim=True)
+    ers = rs * (su + 4 * U) + 0.5 * rs ** 3 * (2 * em * (X - m).abs().mean(1, keepdim=True) + em * em)  # of rstd
+    eh = rs * (em + 2 * U * (X.abs() + m.abs())) + (X - m).abs() * ers
+    _close(mean, m[:, 0], em[:, 0] + U * m[:, 0].abs(), "mean")
+    _close(rstd, rs[:, 0], ers[:, 0], "rstd")
+    Y = h * G + B
+    _close(y, Y, G.abs() * eh + 4 * U * (h.abs() * G.abs() + B.abs()) + 1.01 * v * Y.abs(), "y")
+    # backward, from the stored statistics
+    dy, skip = _rand((rows, width), dtype, 4, 1e-3, pad, shift), _rand((rows, width), dtype, 5, 1e-3, pad, shift)
+    D, M, R = dy.double(), mean.double()[:, None], rstd.double()[:, None]
+    H = (X - M) * R
+    eH = 4 * U * R * (X.abs() + M.abs())
+    g = D * G
+    s1, s2 = g.mean(1, keepdim=True), (g * H).mean(1, keepdim=True)
+    es1 = (su + 2 * U) * g.abs().mean(1, keepdim=True)
+    es2 = (su + 2 * U) * (g * H).abs().mean(1, keepdim=True) + (g.abs() * eH).mean(1, keepdim=True)
+    dxx = R * (g - s1 - H * s2)
+    edx = R * (es1 + H.abs() * es2 + eH * s2.abs() + 4 * U * (g.abs() + s1.abs() + (H * s2).abs()))
+    DG, DB = (D * H).sum(0), D.sum(0)
+    rsum = _sum_u(rows)
+    edg = (D.abs() * eH).sum(0) + (rsum + 2 * U) * (D * H).abs().sum(0) + 1.01 * v * DG.abs()
+    edb = rsum * D.abs().sum(0) + 1.01 * v * DB.abs()
+    for sk in (None, skip):
+        want = dxx if sk is None else dxx + skip.double()
+        e = edx + 2 * U * want.abs() + (0 if sk is None else 2 * U * (skip.double().abs() + dxx.abs()))
+        dx, dgamma, dbeta = dense.layernorm_bwd(dy, x, gamma, mean, rstd, skip=sk)
+        _close(dx, want, e + 1.01 * v * want.abs(), "dx")
+        _close(dgamma, DG, edg, "dgamma")
+        _close(dbeta, DB, edb, "dbeta")
+    # in place of dy, and each output alone
+    own = _twin(dy)
+    dx2, none, _ = dense.layernorm_bwd(own, x, gamma, mean, rstd, skip=skip, dx=own, need_dparams=False)
+    assert none is None and torch.equal(dx2, dx)
+    none, dg2, db2 = dense.layernorm_bwd(dy, x, gamma, mean, rstd, need_dx=False)
+    assert none is None and torch.equal(dg2, dgamma) and torch.equal(db2, dbeta)
+    xi = _twin(x)
+    yi, _, _ = dense.layernorm_fwd(xi, gamma, beta, eps=eps, out=xi, stats=False)
+    assert torch.equal(yi, y)
+
+
+def test_layernorm_of_constant_and_extreme_rows():
+    x = torch.zeros((6, 48), device="cuda")
+    x[1] = 3.0
+    x[2] = 1e18
+    x[3, 5] = math.inf
+    x[4, 7] = math.nan
+    x[5] = torch.arange(48, device="cuda") * 1e-30
+    gamma, beta = _rand((48,), F32, 1) + 1, _rand((48,), F32, 2)
+    y, mean, rstd = dense.layernorm_fwd(x, gamma, beta)
+    assert torch.equal(y[0], beta) and torch.allclose(y[1], beta, atol=1e-3) and rstd[0].item() == pytest.approx(1e-5 ** -0.5)
+    assert mean[2].item() == pytest.approx(1e18, rel=1e-6) and torch.isfinite(y[5]).all()
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4]).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_against_differences(act):
+    """The directional derivative of sum(c * y), y = linear(layernorm(x)) + x, by central differences of the
+    64-bit forward, against the kernels' gradients (float32).  Step 1e-5: the differences are good to about
+    1e-9 of the terms, the kernels to the bounds above; 2e-5 of the sum of the terms' absolute values covers both."""
+    rows, n = 53, 40
+    x, gamma, beta = _rand((rows, n), F32, 1), _rand((n,), F32, 2, 0.2) + 1, _rand((n,), F32, 3, 0.2)
+    w, b, c = _rand((n, n), F32, 4, 0.3), _rand((n,), F32, 5, 0.3), _rand((rows, n), F32, 6)
+    h, mean, rstd = dense.layernorm_fwd(x, gamma, beta)
+    y, z = dense.linear_fwd(h, w, b, x, act=act, keep_z=True)
+    dh, dw, db = dense.linear_bwd(c, h, w, z, act=act)
+    dx, dg, dbeta = dense.layernorm_bwd(dh, x, gamma, mean, rstd, skip=c)
+
+    def loss(p):
+        X, G, B, W, b_ = p
+        m = X.mean(1, keepdim=True)
+        hh = (X - m) * ((X - m).square().mean(1, keepdim=True) + 1e-5) ** -0.5 * G + B
+        return ((_act(hh @ W.T + b_, act) + X) * c.double()).sum()
+
+    p = [t.double() for t in (x, gamma, beta, w, b)]
+    grads = (dx, dg, dbeta, dw, db)
+    for i, g in enumerate(grads):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(100 + i)
+        v = torch.randn(p[i].shape, generator=gen, device="cuda", dtype=torch.float64)
+        e = 1e-5 if act != "relu" else 1e-7  # a kink within the step would show
+        lo, hi = list(p), list(p)
+        lo[i], hi[i] = p[i] - e * v, p[i] + e * v
+        num = (loss(hi) - loss(lo)) / (2 * e)
+        ours = (g.double() * v).sum()
+        assert abs(num - ours) <= 2e-5 * (g.double() * v).abs().sum(), (i, float(num), float(ours))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_the_same_call_gives_the_same_bits(dtype):
+    dy, x = _rand((20_000, 72), dtype, 1, 1e-3), _rand((20_000, 200), dtype, 2)
+    w, z = _rand((72, 200), dtype, 3, 0.1), _rand((20_000, 72), dtype, 4)
+    first = dense.linear_bwd(dy, x, w, z, act="silu")
+    gamma = _rand((200,), dtype, 5)
+    _, mean, rstd = dense.layernorm_fwd(x, gamma, gamma)
+    n1 = dense.layernorm_bwd(x, x, gamma, mean, rstd)
+    for _ in range(3):
+        for a, b in zip(first, dense.linear_bwd(dy, x, w, z, act="silu")):
+            assert torch.equal(a, b)
+        for a, b in zip(n1, dense.layernorm_bwd(x, x, gamma, mean, rstd)):
+            assert torch.equal(a, b)
+
+
+def test_calls_run_on_the_stream_they_are_given():
+    """Work behind a long copy on a side stream: the results are there once that stream is done, and the
+    outputs' memory is not handed out early."""
+    s = torch.cuda.Stream()
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    x, w = _rand((5000, 64), BF16, 1), _rand((64, 64), BF16, 2, 0.1)
+    want, wz = dense.linear_fwd(x, w, act="gelu", keep_z=True)
+    wdx, wdw, wdb = dense.linear_bwd(want, x, w, wz, act="gelu")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            big.add_(1)
+        late = x.clone()
+    for st in (s, s.cuda_stream):
+        y, z = dense.linear_fwd(late, w, act="gelu", keep_z=True, stream=st)
+        dx, dw, db = dense.linear_bwd(y, late, w, z, act="gelu", stream=st)
+        n, mean, rstd = dense.layernorm_fwd(y, w[0], w[1], stream=st)
+        dense.layernorm_bwd(y, y, w[0], mean, rstd, stream=st)
+        s.synchronize()
+        assert torch.equal(y, want) and torch.equal(dx, wdx) and torch.equal(dw, wdw) and torch.equal(db, wdb)
+
+
+def test_offsets_beyond_32_bits():
+    """Arrays of more than 2^31 elements (rows far apart): the last rows are read and written in place."""
+    rows, n, ld = 70_000, 64, 40_000
+    big = torch.zeros((rows, ld), dtype=BF16, device="cuda")
+    x = big[:, 128:128 + n]
+    x.copy_(_rand((rows, n), BF16, 1))
+    out = big[:, 256:256 + n]
+    small = x.contiguous()
+    w = _rand((n, n), BF16, 2, 0.1)
+    y, _ = dense.linear_fwd(x, w, None, x, act="relu", out=out)
+    want, _ = dense.linear_fwd(small, w, None, small, act="relu")
+    assert torch.equal(y, want)
+    got = dense.linear_bwd(out, x, w, out, act="relu", dx=big[:, 512:512 + n])
+    for a, b in zip(got, dense.linear_bwd(want, small, w, want, act="relu")):
+        assert torch.equal(a, b)
+    y, m, r = dense.layernorm_fwd(x, w[0], w[1], out=out)
+    want, m2, r2 = dense.layernorm_fwd(small, w[0], w[1])
+    assert torch.equal(y, want) and torch.equal(m, m2)
+    a = dense.layernorm_bwd(out, x, w[0], m, r, skip=x, dx=big[:, 512:512 + n])
+    for p, q in zip(a, dense.layernorm_bwd(want, small, w[0], m, r, skip=small)):
+        assert torch.equal(p, q)
+    assert not big[:, :128].any() and not big[:, 1024:1032].any()
+
+
+def test_status_stays_clear():
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, w = _rand((3000, 64), BF16, 1), _rand((64, 64), BF16, 2)
+    y, _ = dense.linear_fwd(x, w, status=status)
+    dense.linear_bwd(y, x, w, status=status)
+    assert status.item() == 0
