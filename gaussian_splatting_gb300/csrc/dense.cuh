@@ -89,3 +89,26 @@ struct VecIO<__nv_bfloat16, 8> {
         make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
   }
 };
+
+// ------------------------------------------------------------------ activations and their slopes
+__device__ __forceinline__ float act_value(float v, int act) {
+  switch (act) {
+    case GS_ACT_RELU: return v < 0.f ? 0.f : v;
+    case GS_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    case GS_ACT_SILU: return v / (1.f + expf(-v));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float act_slope(float v, int act) {
+  switch (act) {
+    case GS_ACT_RELU: return v > 0.f ? 1.f : 0.f;
+    case GS_ACT_GELU:
+      return 0.5f * (1.f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+    case GS_ACT_SILU: {
+      const float s = 1.f / (1.f + expf(-v));
+      return s * (1.f + v * (1.f - s));
+    }
+    default: return 1.f;
+  }
+}

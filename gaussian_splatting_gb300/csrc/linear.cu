@@ -6,33 +6,11 @@
 //   dx       dx = dz w     A = dz, B = w read along its other axis
 //   dw       dw = dz^T x   A = dz and x both read along their other axes
 // with dz = dy act'(z) formed as its elements are loaded.
-#include "dense.cuh"
+#include "mma.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float act_value(float v, int act) {
-  switch (act) {
-    case GS_ACT_RELU: return v < 0.f ? 0.f : v;
-    case GS_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case GS_ACT_SILU: return v / (1.f + expf(-v));
-    default: return v;
-  }
-}
-
-__device__ __forceinline__ float act_slope(float v, int act) {
-  switch (act) {
-    case GS_ACT_RELU: return v > 0.f ? 1.f : 0.f;
-    case GS_ACT_GELU:
-      return 0.5f * (1.f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
-    case GS_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-v));
-      return s * (1.f + v * (1.f - s));
-    }
-    default: return 1.f;
-  }
-}
 
 struct Product {
   const void* a;   // A(m, k) = a[m * am + k * ak], times act'(az(m, k)) if az
@@ -119,36 +97,76 @@ __global__ void __launch_bounds__(kThreads) k_product_fold(const Product p, int 
   finish<T>(p, e / p.n, e % p.n, v);
 }
 
-// column sums of dz: 32 columns by 8 rows per block, gridDim.y row ranges
+// dz = dy act'(z) to `dz` (if wanted), and its column sums over this block's rows to part[blockIdx.x].
+// A thread owns VE columns; CX threads lie along a row, kThreads / CX rows side by side.
+template <typename T, bool VEC, int CX>
+__global__ void __launch_bounds__(kThreads) k_act_grad(const T* dy, const T* z, int64_t rows, int n, int64_t lddy,
+                                                       int64_t ldz, int act, T* dz, int64_t lddz, float* part) {
+  constexpr int VE = 16 / sizeof(T), kRows = kThreads / CX;
+  using IO = VecIO<T, VE>;
+  const int cx = threadIdx.x % CX, ry = threadIdx.x / CX;
+  const int c = (blockIdx.y * CX + cx) * VE;
+  const bool in = c < n;
+  float sum[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) sum[e] = 0.f;
+  if (in) {
+#pragma unroll 2
+    for (int64_t r = (int64_t)blockIdx.x * kRows + ry; r < rows; r += (int64_t)gridDim.x * kRows) {
+      float d[VE], v[VE];
+      if (VEC) {
+        const auto rd = IO::load(dy + r * lddy + c);
+        if (z) {
+          const auto rz = IO::load(z + r * ldz + c);
+          IO::unpack(rz, v);
+        }
+        IO::unpack(rd, d);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          d[e] = c + e < n ? to_f32<T>(dy[r * lddy + c + e]) : 0.f;
+          v[e] = z && c + e < n ? to_f32<T>(z[r * ldz + c + e]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        if (z) d[e] *= act_slope(v[e], act);
+        sum[e] += d[e];
+      }
+      if (dz) IO::store(dz + r * lddz + c, d);
+    }
+  }
+  if (!part) return;
+  __shared__ float fold[kRows][CX * VE + 1];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) fold[ry][cx * VE + e] = sum[e];
+  __syncthreads();
+  for (int k = threadIdx.x; k < CX * VE; k += kThreads) {
+    const int col = blockIdx.y * CX * VE + k;
+    if (col >= n) continue;
+    float t = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < kRows; ++r) t += fold[r][k];
+    part[(int64_t)blockIdx.x * n + col] = t;
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_bias_grad(const T* dy, const T* z, int64_t rows, int n, int64_t lddy,
-                                                        int64_t ldz, int act, float* part) {
+__global__ void __launch_bounds__(kThreads) k_bias_fold(const float* part, int parts, int n, T* out) {
   __shared__ float s[8][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < n)
-    for (int64_t r = (int64_t)blockIdx.y * 8 + w; r < rows; r += (int64_t)gridDim.y * 8) {
-      const float d = to_f32<T>(dy[r * lddy + c]);
-      v += z ? d * act_slope(to_f32<T>(z[r * ldz + c]), act) : d;
-    }
+    for (int p = w; p < parts; p += 8) v += part[(int64_t)p * n + c];
   s[w][lane] = v;
   __syncthreads();
   if (w == 0 && c < n) {
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v += s[i][lane];
-    part[(int64_t)blockIdx.y * n + c] = v;
+    out[c] = from_f32<T>(v);
   }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_bias_fold(const float* part, int parts, int n, T* out) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= n) return;
-  float v = 0.f;
-  for (int p = 0; p < parts; ++p) v += part[(int64_t)p * n + c];
-  out[c] = from_f32<T>(v);
 }
 
 // ---------------------------------------------------------------- host side
@@ -167,10 +185,51 @@ size_t part_bytes(int64_t m, int64_t n, int64_t k) {
   return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
 }
 
-int bias_parts(int64_t rows, int n) {
-  int64_t s = ceil_div(4 * 152, ceil_div(n, 32));
-  if (s > ceil_div(rows, 64)) s = ceil_div(rows, 64);
-  return (int)(s < 1 ? 1 : s);
+// threads along a row of n columns in k_act_grad, and its blocks down the rows
+template <typename T>
+int row_threads(int n) {
+  const int nv = (int)ceil_div(n, 16 / sizeof(T));
+  return nv <= 4 ? 4 : nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+}
+template <typename T>
+int act_grad_parts(int64_t rows, int n) {
+  const int cx = row_threads<T>(n);
+  const int64_t across = ceil_div(n, cx * (16 / (int64_t)sizeof(T)));
+  int64_t s = ceil_div(8 * 152, across);
+  const int64_t most = ceil_div(rows, 4 * (kThreads / cx));
+  return (int)(s < most ? s : most);
+}
+int parts_of(const gs_linear_desc* d) {
+  return d->dtype == GS_F32 ? act_grad_parts<float>(d->rows, d->out_features)
+                            : act_grad_parts<__nv_bfloat16>(d->rows, d->out_features);
+}
+
+template <typename T>
+gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, int64_t lddz, float* part, T* dbias,
+                       cudaStream_t st, const char* where) {
+  const int n = d->out_features, parts = act_grad_parts<T>(d->rows, n);
+  const bool vec = gs::rows_aligned16(dy, d->rows, d->ldy, d->dtype) && n % (16 / sizeof(T)) == 0 &&
+                   (!z || gs::rows_aligned16(z, d->rows, d->ldz, d->dtype));
+  const int cx = row_threads<T>(n);
+  const dim3 grid(parts, (unsigned)ceil_div(n, cx * (16 / (int64_t)sizeof(T))));
+#define GS_GO(V, CX)                                                                                                  \
+  k_act_grad<T, V, CX><<<grid, kThreads, 0, st>>>(dy, z, d->rows, n, d->ldy, d->ldz, d->act, dz, lddz, dbias ? part : nullptr)
+  if (vec) {
+    if (cx == 4) GS_GO(true, 4);
+    else if (cx == 8) GS_GO(true, 8);
+    else if (cx == 16) GS_GO(true, 16);
+    else GS_GO(true, 32);
+  } else {
+    if (cx == 4) GS_GO(false, 4);
+    else if (cx == 8) GS_GO(false, 8);
+    else if (cx == 16) GS_GO(false, 16);
+    else GS_GO(false, 32);
+  }
+#undef GS_GO
+  if (gs_status s = gs::check_launch(where)) return s;
+  if (!dbias) return GS_OK;
+  k_bias_fold<T><<<(unsigned)ceil_div(n, 32), kThreads, 0, st>>>(part, parts, n, dbias);
+  return gs::check_launch(where);
 }
 
 template <typename T>
@@ -190,7 +249,12 @@ gs_status run_product(Product& p, int slope_act, void* workspace, cudaStream_t s
 
 template <typename T>
 gs_status run_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
-                  void* z, void* workspace, cudaStream_t st) {
+                  void* z, void* workspace, int32_t* status, cudaStream_t st) {
+  if (d->dtype == GS_BF16) {
+    const gs::MmaProduct q{x, w, d->ldx, d->ldw, false, false, d->rows, d->out_features, d->in_features,
+                           bias, residual, y, z, d->ldr, d->ldy, d->ldz, d->act};
+    if (gs::mma_takes(q)) return gs::mma_run(q, workspace, status, st, "gs_linear_fwd");
+  }
   Product p{};
   p.a = x, p.am = d->ldx, p.ak = 1;
   p.b = w, p.bn = d->ldw, p.bk = 1;
@@ -200,34 +264,77 @@ gs_status run_fwd(const gs_linear_desc* d, const void* x, const void* w, const v
   return run_product<T>(p, GS_ACT_NONE, workspace, st, "gs_linear_fwd");
 }
 
+// The backward's scratch: dz where the products read a copy of it (bfloat16: after an activation, or where
+// dy's rows do not start on 16-byte boundaries), the bias gradient's parts, the products' parts.
+struct BwdSpace {
+  size_t dz, bias, part, total;
+  int64_t lddz;
+};
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+BwdSpace bwd_space(const gs_linear_desc* d) {
+  BwdSpace s{};
+  s.lddz = ceil_div(d->out_features, 8) * 8;
+  const bool copy = d->dtype == GS_BF16 && (d->act != GS_ACT_NONE || (d->ldy * 2) % 16 != 0);
+  s.dz = copy ? up256((size_t)d->rows * s.lddz * 2) : 0;
+  s.bias = up256((size_t)parts_of(d) * d->out_features * sizeof(float));
+  auto most = [](size_t a, size_t b) { return a > b ? a : b; };
+  s.part = most(part_bytes(d->rows, d->in_features, d->out_features), part_bytes(d->out_features, d->in_features, d->rows));
+  if (d->dtype == GS_BF16)
+    s.part = most(s.part, most(gs::mma_workspace(d->rows, d->in_features, d->out_features),
+                               gs::mma_workspace(d->out_features, d->in_features, d->rows)));
+  s.total = s.dz + s.bias + s.part;
+  return s;
+}
+
 template <typename T>
 gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
-                  void* dbias, void* workspace, cudaStream_t st) {
+                  void* dbias, void* workspace, int32_t* status, cudaStream_t st) {
   const char* where = "gs_linear_bwd";
-  if (dx) {
+  const BwdSpace space = bwd_space(d);
+  unsigned char* at = static_cast<unsigned char*>(workspace);
+  T* dz_copy = space.dz ? reinterpret_cast<T*>(at) : nullptr;
+  float* bias_part = reinterpret_cast<float*>(at + space.dz);
+  void* part = at + space.dz + space.bias;
+  const void* dz = dz_copy ? dz_copy : dy;
+  const int64_t lddz = dz_copy ? space.lddz : d->ldy;
+  gs::MmaProduct qx{}, qw{};
+  bool mx = false, mw = false;
+  if (d->dtype == GS_BF16) {
+    if (dx) {
+      qx = {dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
+            nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE};
+      mx = gs::mma_takes(qx);
+    }
+    if (dw) {
+      qw = {dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
+            nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE};
+      mw = gs::mma_takes(qw);
+    }
+  }
+  T* write_dz = dz_copy && (mx || mw) ? dz_copy : nullptr;
+  if (write_dz || dbias)
+    if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), write_dz, lddz, bias_part,
+                                      static_cast<T*>(dbias), st, where))
+      return s;
+  if (mx)
+    if (gs_status s = gs::mma_run(qx, part, status, st, where)) return s;
+  if (mw)
+    if (gs_status s = gs::mma_run(qw, part, status, st, where)) return s;
+  if (dx && !mx) {
     Product p{};
     p.a = dy, p.am = d->ldy, p.ak = 1, p.az = z, p.azm = d->ldz, p.azk = 1;
     p.b = w, p.bn = 1, p.bk = d->ldw;
     p.m = d->rows, p.n = d->in_features, p.k = d->out_features;
     p.y = dx, p.ldy = d->lddx;
-    if (gs_status s = run_product<T>(p, d->act, workspace, st, where)) return s;
+    if (gs_status s = run_product<T>(p, d->act, part, st, where)) return s;
   }
-  if (dw) {
+  if (dw && !mw) {
     Product p{};
     p.a = dy, p.am = 1, p.ak = d->ldy, p.az = z, p.azm = 1, p.azk = d->ldz;
     p.b = x, p.bn = 1, p.bk = d->ldx;
     p.m = d->out_features, p.n = d->in_features, p.k = d->rows;
     p.y = dw, p.ldy = d->lddw;
-    if (gs_status s = run_product<T>(p, d->act, workspace, st, where)) return s;
-  }
-  if (dbias) {
-    const int n = d->out_features, parts = bias_parts(d->rows, n);
-    float* part = static_cast<float*>(workspace);
-    k_bias_grad<T><<<dim3((unsigned)ceil_div(n, 32), parts), kThreads, 0, st>>>(
-        (const T*)dy, (const T*)z, d->rows, n, d->ldy, d->ldz, d->act, part);
-    if (gs_status s = gs::check_launch(where)) return s;
-    k_bias_fold<T><<<(unsigned)ceil_div(n, kThreads), kThreads, 0, st>>>(part, parts, n, (T*)dbias);
-    return gs::check_launch(where);
+    if (gs_status s = run_product<T>(p, d->act, part, st, where)) return s;
   }
   return GS_OK;
 }
@@ -257,7 +364,9 @@ gs_status check_workspace(const char* where, const void* workspace, size_t have,
 
 extern "C" size_t gs_linear_fwd_workspace_size(const gs_linear_desc* d) {
   if (check_desc("gs_linear_fwd_workspace_size", d) || d->rows == 0) return 0;
-  return part_bytes(d->rows, d->out_features, d->in_features);
+  const size_t a = part_bytes(d->rows, d->out_features, d->in_features);
+  const size_t b = d->dtype == GS_BF16 ? gs::mma_workspace(d->rows, d->out_features, d->in_features) : 0;
+  return a > b ? a : b;
 }
 
 extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias,
@@ -276,17 +385,13 @@ extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const
   if (z)
     if (gs_status s = gs::check_matrix(where, "z", z, d->rows, d->out_features, d->ldz, d->dtype)) return s;
   if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_linear_fwd_workspace_size(d))) return s;
-  if (d->dtype == GS_F32) return run_fwd<float>(d, x, w, bias, residual, y, z, workspace, gs::as_stream(stream));
-  return run_fwd<__nv_bfloat16>(d, x, w, bias, residual, y, z, workspace, gs::as_stream(stream));
+  if (d->dtype == GS_F32) return run_fwd<float>(d, x, w, bias, residual, y, z, workspace, status, gs::as_stream(stream));
+  return run_fwd<__nv_bfloat16>(d, x, w, bias, residual, y, z, workspace, status, gs::as_stream(stream));
 }
 
 extern "C" size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d) {
   if (check_desc("gs_linear_bwd_workspace_size", d) || d->rows == 0) return 0;
-  const size_t a = part_bytes(d->rows, d->in_features, d->out_features);
-  const size_t b = part_bytes(d->out_features, d->in_features, d->rows);
-  const size_t c = (size_t)bias_parts(d->rows, d->out_features) * d->out_features * sizeof(float);
-  const size_t ab = a > b ? a : b;
-  return ab > c ? ab : c;
+  return bwd_space(d).total;
 }
 
 extern "C" gs_status gs_linear_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z,
@@ -318,6 +423,6 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_desc* d, const void* dy, cons
   if (d->act == GS_ACT_NONE) z = nullptr;
   else if (gs_status s = gs::check_matrix(where, "z", z, d->rows, d->out_features, d->ldz, d->dtype)) return s;
   if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_linear_bwd_workspace_size(d))) return s;
-  if (d->dtype == GS_F32) return run_bwd<float>(d, dy, x, w, z, dx, dw, dbias, workspace, st);
-  return run_bwd<__nv_bfloat16>(d, dy, x, w, z, dx, dw, dbias, workspace, st);
+  if (d->dtype == GS_F32) return run_bwd<float>(d, dy, x, w, z, dx, dw, dbias, workspace, status, st);
+  return run_bwd<__nv_bfloat16>(d, dy, x, w, z, dx, dw, dbias, workspace, status, st);
 }

@@ -1,0 +1,536 @@
+// bfloat16 products on the 5th-generation tensor cores, with the linear layer's epilogue.
+//
+// C(m, n) = sum over k of A(m, k) B(n, k), 32-bit sums, then z = C + bias, y = act(z) + residual.
+// One persistent block per SM walks over 128 x BN tiles of C (BN = 64 .. 256, and ranges of k where
+// there are few tiles).  Its warps work as a pipeline:
+//   warp 8        issues TMA copies of 128 x 64 (A) and BN x 64 (B) pieces into a ring of shared-memory
+//                 stages (128-byte swizzle).  An operand stored along its other axis ([k][m]) is copied
+//                 as 64 x 64 boxes and handed to the tensor core as it lies: no transpose.  B stays
+//                 resident where all of its k fits: the weights are then read once per block.
+//   warp 9        issues tcgen05.mma, 128 x BN x 16 each, into one of two accumulators in TMEM
+//   warps 0 - 7   read the finished accumulator, 32 rows x 128 bytes of columns at a time, and write it
+//                 through shared memory with TMA stores (or, where rows do not start on 16-byte
+//                 boundaries, with plain coalesced stores) while the next tile is being summed
+// Every wait is bounded (see tc::Guard).
+#include <cuda.h>
+
+#include <atomic>
+
+#include "mma.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kTileM = 128, kTileK = 64;
+constexpr int kMaxStages = 8;
+constexpr int kABytes = kTileM * kTileK * 2;
+constexpr int kBufBytes = 32 * 128;   // one warp's 32 rows x 128 bytes
+constexpr int kBufCols = 64;          // columns of one such buffer
+constexpr int kSmemMost = 232448;     // 227 KB
+constexpr int kSmemCtl = 1024;        // barriers, TMEM address, dead flag
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t resident, acc_full[2], acc_empty[2], drain;
+  uint64_t res[kEpiWarps];
+  uint32_t tmem, dead;
+};
+static_assert(sizeof(Ctl) <= kSmemCtl, "control block");
+
+struct Args {
+  CUtensorMap a, b, y, z, r;
+  int64_t m, n;
+  int m_tiles, n_tiles, splits, kblocks, kb_per_split;
+  int bn, stages, tmem_cols;
+  int a_mn, b_mn, resident;
+  int bufs_y, has_z, has_r, act;  // bufs_y: buffers per warp for y and the residual (1, or 2 with a residual)
+  const bf16* bias;
+  float* part;  // [splits][m][ldp] when splits > 1: no epilogue
+  int64_t ldp;
+  int32_t* status;
+  int64_t wait_limit;
+  int drop;
+};
+
+// ---------------------------------------------------------------- epilogue
+// y and z of 8 columns of a row from the sums v: bias (already 32 bits), activation, residual.
+template <int ACT>
+__device__ __forceinline__ void epilogue8(const float* v, const float* bias, const uint4* res, uint4& y, uint4& z) {
+  float t[8], r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = v[i] + bias[i];
+  z = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = act_value(t[i], ACT);
+  if (res) {
+    VecIO<bf16, 8>::unpack(*res, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] += r[i];
+  }
+  y = make_uint4(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]), pack_bf16(t[4], t[5]), pack_bf16(t[6], t[7]));
+}
+
+struct EpiState {
+  uint32_t buf;        // this warp's buffers in shared memory (address)
+  unsigned char* ptr;  // the same, generic
+  float* bias;         // 64 floats of this warp
+  uint32_t res_bar;
+  uint32_t loads, issued;  // residual pieces waited for and asked for so far
+  int lane, quad, half;
+};
+
+__device__ __forceinline__ void tile_of(const Args& p, int64_t t, int64_t& m0, int64_t& n0, int& split) {
+  const int64_t nt = t % p.n_tiles, rest = t / p.n_tiles;
+  n0 = nt * p.bn;
+  m0 = rest % p.m_tiles * kTileM;
+  split = (int)(rest / p.m_tiles);
+}
+
+// whether this warp writes anything of chunk c of the tile at (m0, n0)
+__device__ __forceinline__ bool chunk_in(const Args& p, const EpiState& e, int64_t m0, int64_t n0, int c) {
+  return m0 + e.quad * 32 < p.m && n0 + c * kBufCols < p.n;
+}
+
+template <int ACT>
+__device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, int64_t t, int64_t total, uint32_t tmem,
+                              uint32_t acc_full, uint32_t parity) {
+  int64_t m0, n0;
+  int split;
+  tile_of(p, t, m0, n0, split);
+  bool waited = false;
+  for (int c = e.half; c * kBufCols < p.bn; c += 2) {
+    const bool in = chunk_in(p, e, m0, n0, c);
+    uint32_t slot = 0;
+    if (in) {
+      // every store that reads these buffers is done reading
+      if (e.lane == 0) tc::bulk_wait_read0();
+      __syncwarp();
+      const int col = (int)n0 + c * kBufCols;
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t cc = col + e.lane + 32 * i;
+          e.bias[e.lane + 32 * i] = cc < p.n ? __bfloat162float(p.bias[cc]) : 0.f;
+        }
+      }
+      if (p.has_r) {
+        slot = e.loads & 1;
+        // the residual piece of the next chunk goes to the other buffer
+        int64_t t2 = t, nm, nn;
+        int c2 = c, s2;
+        c2 += 2;
+        if (c2 * kBufCols >= p.bn) c2 = e.half, t2 += gridDim.x;
+        while (t2 < total) {  // skips the chunks that lie outside of C
+          tile_of(p, t2, nm, nn, s2);
+          if (chunk_in(p, e, nm, nn, c2)) break;
+          c2 += 2;
+          if (c2 * kBufCols >= p.bn) c2 = e.half, t2 += gridDim.x;
+        }
+        if (t2 < total && e.lane == 0) {
+          tc::mbar_expect_tx(e.res_bar + 8 * (slot ^ 1), kBufBytes);
+          tc::tma_load_2d(e.buf + (slot ^ 1) * kBufBytes, &p.r, (int)nn + c2 * kBufCols, (int)(nm + e.quad * 32),
+                          e.res_bar + 8 * (slot ^ 1));
+        }
+        if (t2 < total) ++e.issued;
+        if (!tc::mbar_wait(e.res_bar + 8 * slot, (e.loads >> 1) & 1, g)) return false;
+        ++e.loads;
+      }
+      __syncwarp();
+    }
+    if (!waited) {
+      if (!tc::mbar_wait(acc_full, parity, g)) return false;
+      tc::fence_after();
+      waited = true;
+    }
+    if (!in) continue;
+    unsigned char* yb = e.ptr + slot * kBufBytes;
+    unsigned char* zb = e.ptr + p.bufs_y * kBufBytes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * kBufCols + h * 32, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int unit = h * 4 + q, at = e.lane * 128 + ((unit ^ (e.lane & 7)) << 4);
+        float b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = p.bias ? e.bias[unit * 8 + i] : 0.f;
+        uint4 y, z, r;
+        if (p.has_r) r = *reinterpret_cast<uint4*>(yb + at);
+        epilogue8<ACT>(v + q * 8, b, p.has_r ? &r : nullptr, y, z);
+        *reinterpret_cast<uint4*>(yb + at) = y;
+        if (p.has_z) *reinterpret_cast<uint4*>(zb + at) = z;
+      }
+    }
+    tc::fence_async_smem();
+    __syncwarp();
+    if (e.lane == 0) {
+      tc::tma_store_2d(&p.y, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.buf + slot * kBufBytes);
+      if (p.has_z)
+        tc::tma_store_2d(&p.z, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.buf + p.bufs_y * kBufBytes);
+      tc::bulk_commit();
+    }
+  }
+  if (!waited && !tc::mbar_wait(acc_full, parity, g)) return false;
+  return true;
+}
+
+// A range of k: the sums as they are, 32 bits, to this split's part (rows of ldp, a multiple of 8).
+__device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& g, int64_t t, uint32_t tmem,
+                             uint32_t acc_full, uint32_t parity) {
+  int64_t m0, n0;
+  int split;
+  tile_of(p, t, m0, n0, split);
+  if (!tc::mbar_wait(acc_full, parity, g)) return false;
+  tc::fence_after();
+  const int64_t row = m0 + e.quad * 32 + e.lane;
+  float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + n0;
+  for (int c = e.half; c * 32 < p.bn; c += 2) {
+    if (n0 + c * 32 >= p.ldp) break;
+    float v[32];
+    tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * 32, v);
+    if (row < p.m) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (n0 + c * 32 + q * 4 < p.ldp)
+          *reinterpret_cast<float4*>(out + c * 32 + q * 4) = make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
+    }
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Args p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
+  const uint32_t base = tc::smem_addr(smem);
+  const uint32_t b_bytes = (uint32_t)p.bn * kTileK * 2;
+  const uint32_t res_b = base + kSmemCtl;
+  const uint32_t ring = res_b + (p.resident ? b_bytes * p.kblocks : 0);
+  const uint32_t stage_bytes = kABytes + (p.resident ? 0 : b_bytes);
+  const uint32_t epi = ring + stage_bytes * p.stages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      tc::mbar_init(bar(ctl.full[s]), 1);
+      tc::mbar_init(bar(ctl.empty[s]), 1);
+    }
+    tc::mbar_init(bar(ctl.resident), 1);
+    tc::mbar_init(bar(ctl.drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(ctl.acc_full[i]), 1);
+      tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps);
+    }
+    ctl.dead = 0;
+    tc::fence_mbar_init();
+  }
+  const tc::Guard g{&ctl.dead, p.status, p.wait_limit};
+  const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  if (warp == 9) tc::tmem_alloc(bar(reinterpret_cast<uint64_t&>(ctl.tmem)), p.tmem_cols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = ctl.tmem;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0 && !p.drop) {
+      tc::prefetch_map(&p.a);
+      tc::prefetch_map(&p.b);
+      auto load_b = [&](uint32_t dst, int64_t n0, int kb, uint32_t full) {
+        if (!p.b_mn) tc::tma_load_2d(dst, &p.b, kb * kTileK, (int)n0, full);
+        else
+          for (int c = 0; c < p.bn; c += 64) tc::tma_load_2d(dst + c * 128, &p.b, (int)n0 + c, kb * kTileK, full);
+      };
+      int64_t it = 0;
+      bool ok = true;
+      if (p.resident && blockIdx.x < total) {
+        tc::mbar_expect_tx(bar(ctl.resident), b_bytes * p.kblocks);
+        for (int kb = 0; kb < p.kblocks; ++kb)
+          load_b(res_b + b_bytes * kb, (int64_t)(blockIdx.x % p.n_tiles) * p.bn, kb, bar(ctl.resident));
+      }
+      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        int64_t m0, n0;
+        int split;
+        tile_of(p, t, m0, n0, split);
+        const int k_lo = split * p.kb_per_split;
+        const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
+        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+          const int s = (int)(it % p.stages);
+          ok = tc::mbar_wait(bar(ctl.empty[s]), (uint32_t)(it / p.stages & 1) ^ 1, g);
+          if (!ok) break;
+          const uint32_t dst = ring + stage_bytes * s, full = bar(ctl.full[s]);
+          tc::mbar_expect_tx(full, stage_bytes);
+          if (!p.a_mn) tc::tma_load_2d(dst, &p.a, kb * kTileK, (int)m0, full);
+          else
+            for (int c = 0; c < kTileM; c += 64) tc::tma_load_2d(dst + c * 128, &p.a, (int)m0 + c, kb * kTileK, full);
+          if (!p.resident) load_b(dst + kABytes, n0, kb, full);
+        }
+      }
+      if (!ok) {  // gave up: no copy may be in flight when the block ends
+        for (int64_t i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
+          for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1)); ++j) {}
+        if (p.resident)
+          for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.resident), 0); ++j) {}
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ matrix instructions
+    if (lane == 0) {
+      // bfloat16 operands, f32 sums, 128 x bn
+      const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
+                             (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+      // 16 of k further: 32 bytes along a row, or 16 rows of 128 bytes
+      const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
+      int64_t it = 0, n_acc = 0;
+      bool ok = true;
+      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
+      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+        int64_t m0, n0;
+        int split;
+        tile_of(p, t, m0, n0, split);
+        const int k_lo = split * p.kb_per_split;
+        const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
+        const int acc = (int)(n_acc & 1);
+        ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = tmem + acc * (p.tmem_cols / 2);
+        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+          const int s = (int)(it % p.stages);
+          ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t a = ring + stage_bytes * s;
+          const uint32_t b = p.resident ? res_b + b_bytes * kb : a + kABytes;
+#pragma unroll
+          for (int i = 0; i < kTileK / 16; ++i)
+            tc::mma_bf16(d, tc::smem_desc(a + i * a_step, 64 * 128, 1024), tc::smem_desc(b + i * b_step, 64 * 128, 1024), idesc,
+                         kb > k_lo || i > 0);
+          tc::mma_commit(bar(ctl.empty[s]));
+        }
+        if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+      }
+      if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
+        tc::mma_commit(bar(ctl.drain));
+        for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    EpiState e;
+    e.lane = lane, e.quad = warp & 3, e.half = warp >> 2;
+    const int bufs = p.bufs_y + p.has_z;
+    e.buf = epi + warp * bufs * kBufBytes;
+    e.ptr = smem + (e.buf - base);
+    e.bias = reinterpret_cast<float*>(smem + (epi - base) + kEpiWarps * bufs * kBufBytes) + warp * 64;
+    e.res_bar = bar(ctl.res[0]) + warp * 16;
+    e.loads = e.issued = 0;
+    int64_t n_acc = 0;
+    bool ok = true;
+    if (p.has_r) {
+      // the first chunk's residual piece
+      if (lane == 0) {
+        tc::mbar_init(e.res_bar, 1);
+        tc::mbar_init(e.res_bar + 8, 1);
+        tc::fence_mbar_init();
+        tc::fence_async_smem();
+      }
+      __syncwarp();
+      int c = e.half;
+      for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+        int64_t m0, n0;
+        int split;
+        tile_of(p, t, m0, n0, split);
+        for (c = e.half; c * kBufCols < p.bn && !chunk_in(p, e, m0, n0, c);) c += 2;
+        if (c * kBufCols >= p.bn) continue;
+        if (lane == 0) {
+          tc::mbar_expect_tx(e.res_bar, kBufBytes);
+          tc::tma_load_2d(e.buf, &p.r, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.res_bar);
+        }
+        e.issued = 1;
+        break;
+      }
+    }
+    for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+      const int acc = (int)(n_acc & 1);
+      const uint32_t parity = (uint32_t)(n_acc >> 1 & 1), d = tmem + acc * (p.tmem_cols / 2), full = bar(ctl.acc_full[acc]);
+      if (p.part) ok = partial_tile(p, e, g, t, d, full, parity);
+      else if (p.act == GS_ACT_RELU) ok = epilogue_tile<GS_ACT_RELU>(p, e, g, t, total, d, full, parity);
+      else if (p.act == GS_ACT_GELU) ok = epilogue_tile<GS_ACT_GELU>(p, e, g, t, total, d, full, parity);
+      else if (p.act == GS_ACT_SILU) ok = epilogue_tile<GS_ACT_SILU>(p, e, g, t, total, d, full, parity);
+      else ok = epilogue_tile<GS_ACT_NONE>(p, e, g, t, total, d, full, parity);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
+    }
+    if (!ok && lane == 0) {  // gave up: the pieces in flight land before the block ends
+      for (uint32_t i = e.loads; i < e.issued; ++i)
+        for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(e.res_bar + 8 * (i & 1), i >> 1 & 1); ++j) {}
+    }
+    if (lane == 0) tc::bulk_wait0();
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 9) tc::tmem_dealloc(tmem, p.tmem_cols);
+}
+
+// The splits' parts added in order, then the epilogue: one thread per 4 columns of a row.
+__global__ void __launch_bounds__(256) k_mma_fold(const float* __restrict__ part, int splits, int64_t m, int n, int64_t ldp,
+                                                  const bf16* bias, const bf16* residual, bf16* y, bf16* z, int64_t ldr,
+                                                  int64_t ldy, int64_t ldz, int act) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = ldp / 4;
+  if (e >= m * quads) return;
+  const int64_t row = e / quads;
+  const int col = (int)(e % quads) * 4;
+  float v[4] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 f = *reinterpret_cast<const float4*>(part + ((int64_t)s * m + row) * ldp + col);
+    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (col + i >= n) break;
+    float t = v[i] + (bias ? __bfloat162float(bias[col + i]) : 0.f);
+    if (z) z[row * ldz + col + i] = __float2bfloat16_rn(t);
+    t = act_value(t, act);
+    if (residual) t += __bfloat162float(residual[row * ldr + col + i]);
+    y[row * ldy + col + i] = __float2bfloat16_rn(t);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's encoder, asked for once per process (a function's address, the same for every device)
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> cached{nullptr};
+  EncodeFn f = cached.load();
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeFn>(p);
+  cached.store(f);
+  return f;
+}
+
+// a [rows][cols] bfloat16 matrix in boxes of box_rows x 64 columns (128 bytes, swizzled)
+bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  const EncodeFn f = encoder();
+  if (!f) return false;
+  if (rows == 1) ld = (cols + 7) / 8 * 8;  // the stride of a single row is never used
+  const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, stride, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  int bn, m_tiles, n_tiles, splits, kblocks, kb_per_split;
+  int64_t ldp;
+};
+
+constexpr int kSms = 152;  // the device's; only speed depends on it
+
+// Tiles as wide as they go (256 columns: the fewest reads of A) while there are enough of them for the
+// device; narrower ones, then ranges of k of at least four blocks (256), while there are not.
+Plan plan_of(int64_t m, int64_t n, int64_t k) {
+  Plan p;
+  p.m_tiles = (int)ceil_div(m, kTileM);
+  p.kblocks = (int)ceil_div(k, kTileK);
+  int n_tiles = (int)ceil_div(n, 256);
+  int bn = (int)(ceil_div(ceil_div(n, n_tiles), 64) * 64);
+  while (bn > 64 && (int64_t)p.m_tiles * ceil_div(n, bn) < kSms / 2 && p.kblocks < 16) bn -= 64;
+  p.bn = bn;
+  p.n_tiles = (int)ceil_div(n, bn);
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+  int64_t splits = tiles >= kSms ? 1 : kSms / tiles;
+  if (splits > p.kblocks / 4) splits = p.kblocks / 4;
+  if (splits < 1) splits = 1;
+  p.kb_per_split = (int)ceil_div(p.kblocks, splits);
+  p.splits = (int)ceil_div(p.kblocks, p.kb_per_split);
+  p.ldp = ceil_div(n, 8) * 8;
+  return p;
+}
+
+}  // namespace
+
+namespace gs {
+
+bool mma_takes(const MmaProduct& p) {
+  const int64_t a_rows = p.a_mn ? p.k : p.m, b_rows = p.b_mn ? p.k : p.n;
+  return rows_aligned16(p.a, a_rows, p.lda, GS_BF16) && rows_aligned16(p.b, b_rows, p.ldb, GS_BF16) &&
+         rows_aligned16(p.y, p.m, p.ldy, GS_BF16) && (!p.z || rows_aligned16(p.z, p.m, p.ldz, GS_BF16)) &&
+         (!p.residual || rows_aligned16(p.residual, p.m, p.ldr, GS_BF16));
+}
+
+size_t mma_workspace(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_of(m, n, k);
+  return p.splits > 1 ? (size_t)p.splits * m * p.ldp * sizeof(float) : 0;
+}
+
+gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+  const Plan pl = plan_of(q.m, q.n, q.k);
+  Args p{};
+  p.m = q.m, p.n = q.n;
+  p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
+  p.kb_per_split = pl.kb_per_split, p.bn = pl.bn;
+  p.a_mn = q.a_mn, p.b_mn = q.b_mn;
+  p.tmem_cols = pl.bn <= 64 ? 128 : pl.bn <= 128 ? 256 : 512;
+  p.act = q.act, p.bias = static_cast<const bf16*>(q.bias);
+  p.status = status, p.wait_limit = wait_limit(), p.drop = 0;
+  p.ldp = pl.ldp;
+  p.bufs_y = 1;
+  if (pl.splits > 1) p.part = static_cast<float*>(workspace);
+  else p.has_z = q.z != nullptr, p.has_r = q.residual != nullptr, p.bufs_y = q.residual ? 2 : 1;
+  // shared memory: control, epilogue buffers, then resident weights if they leave three stages, then stages
+  const int epi = p.part ? 0 : kEpiWarps * ((p.bufs_y + p.has_z) * kBufBytes + 256);
+  const int room = kSmemMost - 1024 - kSmemCtl - epi;
+  const int b_bytes = pl.bn * kTileK * 2;
+  const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
+  int grid = (int)(total < num_sms() ? total : num_sms());
+  p.resident = 0;
+  if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && (int64_t)b_bytes * pl.kblocks + 3 * kABytes <= room) {
+    p.resident = 1;
+    grid -= grid % pl.n_tiles;  // a block keeps to one range of columns
+  }
+  const int stage = kABytes + (p.resident ? 0 : b_bytes);
+  int stages = (room - (p.resident ? b_bytes * pl.kblocks : 0)) / stage;
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  const int smem = 1024 + kSmemCtl + (p.resident ? b_bytes * pl.kblocks : 0) + p.stages * stage + epi;
+  bool ok = q.a_mn ? encode(&p.a, q.a, q.k, q.m, q.lda, 64) : encode(&p.a, q.a, q.m, q.k, q.lda, kTileM);
+  ok = ok && (q.b_mn ? encode(&p.b, q.b, q.k, q.n, q.ldb, 64) : encode(&p.b, q.b, q.n, q.k, q.ldb, pl.bn));
+  if (!p.part) {
+    ok = ok && encode(&p.y, q.y, q.m, q.n, q.ldy, 32);
+    if (q.z) ok = ok && encode(&p.z, q.z, q.m, q.n, q.ldz, 32);
+    if (q.residual) ok = ok && encode(&p.r, q.residual, q.m, q.n, q.ldr, 32);
+  }
+  if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
+  const cudaError_t e = max_dynamic_smem((const void*)k_mma, kSmemMost);
+  if (e != cudaSuccess) return set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  k_mma<<<grid, kThreads, smem, st>>>(p);
+  if (gs_status s = check_launch(where)) return s;
+  if (!p.part) return GS_OK;
+  k_mma_fold<<<(unsigned)ceil_div(q.m * (pl.ldp / 4), 256), 256, 0, st>>>(
+      p.part, pl.splits, q.m, (int)q.n, pl.ldp, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
+      static_cast<bf16*>(q.z), q.ldr, q.ldy, q.ldz, q.act);
+  return check_launch(where);
+}
+
+}  // namespace gs

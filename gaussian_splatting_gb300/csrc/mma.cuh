@@ -1,0 +1,30 @@
+// The tensor-core product behind the linear layer (mma.cu).
+#pragma once
+
+#include "dense.cuh"
+
+namespace gs {
+
+// C(m, n) = sum over k of A(m, k) B(n, k), then y = act(C + bias) + residual, z = C + bias.
+// An operand lies in memory as [m][k] with `ld` elements between rows, or, `*_mn`, as [k][m].
+struct MmaProduct {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;
+  bool a_mn, b_mn;
+  int64_t m, n, k;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  int64_t ldr, ldy, ldz;
+  int act;
+};
+
+// whether every array of the product starts its rows on 16-byte boundaries (bfloat16)
+bool mma_takes(const MmaProduct& p);
+// bytes of scratch for a product of these sizes (0: none), whatever its arrays
+size_t mma_workspace(int64_t m, int64_t n, int64_t k);
+gs_status mma_run(const MmaProduct& p, void* workspace, int32_t* status, cudaStream_t st, const char* where);
+
+}  // namespace gs
