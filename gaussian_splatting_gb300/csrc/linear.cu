@@ -1,101 +1,17 @@
 // The linear layer y = act(x w^T + bias) + residual and its gradient (gs_linear_fwd, gs_linear_bwd).
 //
-// Three products share one kernel, C(m, n) = sum over k of A(m, k) B(n, k) with A and B given by
-// their two strides:
+// Three products, each C(m, n) = sum over k of A(m, k) B(n, k) on the tensor cores:
 //   forward  z  = x w^T    A = x,  B = w
-//   dx       dx = dz w     A = dz, B = w read along its other axis
-//   dw       dw = dz^T x   A = dz and x both read along their other axes
-// with dz = dy act'(z) formed as its elements are loaded.
+//   dx       dx = dz w     A = dz, B = w along its other axis
+//   dw       dw = dz^T x   A = dz and B = x, both along their other axes
+// bfloat16 arrays whose rows start on 16-byte boundaries go to mma.cu, everything else to mma_staged.cu.
+// dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
+// sums, and kept in the workspace for the two products that read it.
 #include "mma.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
-
-struct Product {
-  const void* a;   // A(m, k) = a[m * am + k * ak], times act'(az(m, k)) if az
-  const void* az;
-  const void* b;   // B(n, k) = b[n * bn + k * bk]
-  int64_t am, ak, azm, azk, bn, bk;
-  int64_t m, n, k;
-  int64_t k_per_split;
-  int act;
-  // epilogue, when there is one split; otherwise C goes to part[split][m][n] as it is
-  const void* bias;
-  const void* residual;
-  void* y;
-  void* z;
-  int64_t ldr, ldy, ldz;
-  float* part;
-};
-
-template <typename T>
-__device__ __forceinline__ void finish(const Product& p, int64_t m, int64_t n, float v) {
-  if (p.bias) v += to_f32<T>(static_cast<const T*>(p.bias)[n]);
-  if (p.z) static_cast<T*>(p.z)[m * p.ldz + n] = from_f32<T>(v);
-  v = act_value(v, p.act);
-  if (p.residual) v += to_f32<T>(static_cast<const T*>(p.residual)[m * p.ldr + n]);
-  static_cast<T*>(p.y)[m * p.ldy + n] = from_f32<T>(v);
-}
-
-// 64 x 64 tile of C per block, 16 of k at a time through shared memory, 4 x 4 sums per thread.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_product(const Product p, int slope_act) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-  const int64_t k_lo = (int64_t)blockIdx.z * p.k_per_split;
-  const int64_t k_hi = k_lo + p.k_per_split < p.k ? k_lo + p.k_per_split : p.k;
-  float c[4][4] = {};
-  for (int64_t k0 = k_lo; k0 < k_hi; k0 += 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid + i * kThreads;
-      // the axis with unit stride runs over neighbouring threads
-      const int ka = p.ak == 1 ? e % 16 : e / 64, ma = p.ak == 1 ? e / 16 : e % 64;
-      const int kb = p.bk == 1 ? e % 16 : e / 64, nb = p.bk == 1 ? e / 16 : e % 64;
-      float va = 0.f, vb = 0.f;
-      if (m0 + ma < p.m && k0 + ka < k_hi) {
-        va = to_f32<T>(static_cast<const T*>(p.a)[(m0 + ma) * p.am + (k0 + ka) * p.ak]);
-        if (p.az) va *= act_slope(to_f32<T>(static_cast<const T*>(p.az)[(m0 + ma) * p.azm + (k0 + ka) * p.azk]), slope_act);
-      }
-      if (n0 + nb < p.n && k0 + kb < k_hi)
-        vb = to_f32<T>(static_cast<const T*>(p.b)[(n0 + nb) * p.bn + (k0 + kb) * p.bk]);
-      sa[ka][ma] = va;
-      sb[kb][nb] = vb;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = sa[k][ty + 16 * i], b[i] = sb[k][tx + 16 * i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a[i], b[j], c[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.m || n >= p.n) continue;
-      if (gridDim.z > 1) p.part[((int64_t)blockIdx.z * p.m + m) * p.n + n] = c[i][j];
-      else finish<T>(p, m, n, c[i][j]);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_product_fold(const Product p, int splits) {
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (e >= p.m * p.n) return;
-  float v = 0.f;
-  for (int s = 0; s < splits; ++s) v += p.part[s * p.m * p.n + e];
-  finish<T>(p, e / p.n, e % p.n, v);
-}
 
 // dz = dy act'(z) to `dz` (if wanted), and its column sums over this block's rows to part[blockIdx.x].
 // A thread owns VE columns; CX threads lie along a row, kThreads / CX rows side by side.
@@ -172,19 +88,6 @@ __global__ void __launch_bounds__(kThreads) k_bias_fold(const float* part, int p
 // ---------------------------------------------------------------- host side
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// splits of the k axis: enough blocks for the device, at least 512 of k each
-int splits_of(int64_t m, int64_t n, int64_t k) {
-  const int64_t tiles = ceil_div(m, 64) * ceil_div(n, 64);
-  int64_t s = ceil_div(4 * 152, tiles);
-  if (s > k / 512) s = k / 512;
-  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
-}
-
-size_t part_bytes(int64_t m, int64_t n, int64_t k) {
-  const int s = splits_of(m, n, k);
-  return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
-}
-
 // threads along a row of n columns in k_act_grad, and its blocks down the rows
 template <typename T>
 int row_threads(int n) {
@@ -232,40 +135,20 @@ gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, 
   return gs::check_launch(where);
 }
 
-template <typename T>
-gs_status run_product(Product& p, int slope_act, void* workspace, cudaStream_t st, const char* where) {
-  const int splits = splits_of(p.m, p.n, p.k);
-  p.k_per_split = ceil_div(ceil_div(p.k, splits), 16) * 16;
-  p.part = static_cast<float*>(workspace);
-  dim3 grid((unsigned)ceil_div(p.m, 64), (unsigned)ceil_div(p.n, 64), splits);
-  k_product<T><<<grid, kThreads, 0, st>>>(p, slope_act);
-  if (gs_status s = gs::check_launch(where)) return s;
-  if (splits > 1) {
-    k_product_fold<T><<<(unsigned)ceil_div(p.m * p.n, kThreads), kThreads, 0, st>>>(p, splits);
-    return gs::check_launch(where);
-  }
-  return GS_OK;
+gs_status run_product(const gs::MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st,
+                      const char* where) {
+  if (dtype == GS_BF16 && gs::mma_takes(q)) return gs::mma_run(q, workspace, status, st, where);
+  return gs::staged_run(q, dtype, workspace, status, st, where);
 }
 
-template <typename T>
-gs_status run_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
-                  void* z, void* workspace, int32_t* status, cudaStream_t st) {
-  if (d->dtype == GS_BF16) {
-    const gs::MmaProduct q{x, w, d->ldx, d->ldw, false, false, d->rows, d->out_features, d->in_features,
-                           bias, residual, y, z, d->ldr, d->ldy, d->ldz, d->act};
-    if (gs::mma_takes(q)) return gs::mma_run(q, workspace, status, st, "gs_linear_fwd");
-  }
-  Product p{};
-  p.a = x, p.am = d->ldx, p.ak = 1;
-  p.b = w, p.bn = d->ldw, p.bk = 1;
-  p.m = d->rows, p.n = d->out_features, p.k = d->in_features;
-  p.act = d->act, p.bias = bias, p.residual = residual, p.ldr = d->ldr;
-  p.y = y, p.ldy = d->ldy, p.z = z, p.ldz = d->ldz;
-  return run_product<T>(p, GS_ACT_NONE, workspace, st, "gs_linear_fwd");
+// scratch of a product of these sizes, whichever kernel its arrays' alignment takes it to
+size_t product_space(int64_t m, int64_t n, int64_t k, int32_t dtype) {
+  const size_t a = gs::staged_workspace(m, n, k), b = dtype == GS_BF16 ? gs::mma_workspace(m, n, k) : 0;
+  return a > b ? a : b;
 }
 
-// The backward's scratch: dz where the products read a copy of it (bfloat16: after an activation, or where
-// dy's rows do not start on 16-byte boundaries), the bias gradient's parts, the products' parts.
+// The backward's scratch: a copy of dz (after an activation, or where bfloat16 rows of dy do not start on
+// 16-byte boundaries), the bias gradient's parts, the products' parts.
 struct BwdSpace {
   size_t dz, bias, part, total;
   int64_t lddz;
@@ -274,14 +157,12 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 BwdSpace bwd_space(const gs_linear_desc* d) {
   BwdSpace s{};
   s.lddz = ceil_div(d->out_features, 8) * 8;
-  const bool copy = d->dtype == GS_BF16 && (d->act != GS_ACT_NONE || (d->ldy * 2) % 16 != 0);
-  s.dz = copy ? up256((size_t)d->rows * s.lddz * 2) : 0;
+  const bool copy = d->act != GS_ACT_NONE || (d->dtype == GS_BF16 && (d->ldy * 2) % 16 != 0);
+  s.dz = copy ? up256((size_t)d->rows * s.lddz * gs::dtype_size(d->dtype)) : 0;
   s.bias = up256((size_t)parts_of(d) * d->out_features * sizeof(float));
-  auto most = [](size_t a, size_t b) { return a > b ? a : b; };
-  s.part = most(part_bytes(d->rows, d->in_features, d->out_features), part_bytes(d->out_features, d->in_features, d->rows));
-  if (d->dtype == GS_BF16)
-    s.part = most(s.part, most(gs::mma_workspace(d->rows, d->in_features, d->out_features),
-                               gs::mma_workspace(d->out_features, d->in_features, d->rows)));
+  const size_t a = product_space(d->rows, d->in_features, d->out_features, d->dtype);
+  const size_t b = product_space(d->out_features, d->in_features, d->rows, d->dtype);
+  s.part = a > b ? a : b;
   s.total = s.dz + s.bias + s.part;
   return s;
 }
@@ -292,49 +173,24 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   const char* where = "gs_linear_bwd";
   const BwdSpace space = bwd_space(d);
   unsigned char* at = static_cast<unsigned char*>(workspace);
-  T* dz_copy = space.dz ? reinterpret_cast<T*>(at) : nullptr;
+  T* copy = space.dz && (dx || dw) ? reinterpret_cast<T*>(at) : nullptr;
   float* bias_part = reinterpret_cast<float*>(at + space.dz);
   void* part = at + space.dz + space.bias;
-  const void* dz = dz_copy ? dz_copy : dy;
-  const int64_t lddz = dz_copy ? space.lddz : d->ldy;
-  gs::MmaProduct qx{}, qw{};
-  bool mx = false, mw = false;
-  if (d->dtype == GS_BF16) {
-    if (dx) {
-      qx = {dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
-            nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE};
-      mx = gs::mma_takes(qx);
-    }
-    if (dw) {
-      qw = {dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
-            nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE};
-      mw = gs::mma_takes(qw);
-    }
-  }
-  T* write_dz = dz_copy && (mx || mw) ? dz_copy : nullptr;
-  if (write_dz || dbias)
-    if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), write_dz, lddz, bias_part,
+  const void* dz = copy ? copy : dy;
+  const int64_t lddz = copy ? space.lddz : d->ldy;
+  if (copy || dbias)
+    if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), copy, lddz, bias_part,
                                       static_cast<T*>(dbias), st, where))
       return s;
-  if (mx)
-    if (gs_status s = gs::mma_run(qx, part, status, st, where)) return s;
-  if (mw)
-    if (gs_status s = gs::mma_run(qw, part, status, st, where)) return s;
-  if (dx && !mx) {
-    Product p{};
-    p.a = dy, p.am = d->ldy, p.ak = 1, p.az = z, p.azm = d->ldz, p.azk = 1;
-    p.b = w, p.bn = 1, p.bk = d->ldw;
-    p.m = d->rows, p.n = d->in_features, p.k = d->out_features;
-    p.y = dx, p.ldy = d->lddx;
-    if (gs_status s = run_product<T>(p, d->act, part, st, where)) return s;
+  if (dx) {
+    const gs::MmaProduct q{dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
+                           nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE};
+    if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
-  if (dw && !mw) {
-    Product p{};
-    p.a = dy, p.am = 1, p.ak = d->ldy, p.az = z, p.azm = 1, p.azk = d->ldz;
-    p.b = x, p.bn = 1, p.bk = d->ldx;
-    p.m = d->out_features, p.n = d->in_features, p.k = d->rows;
-    p.y = dw, p.ldy = d->lddw;
-    if (gs_status s = run_product<T>(p, d->act, part, st, where)) return s;
+  if (dw) {
+    const gs::MmaProduct q{dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
+                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE};
+    if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
   return GS_OK;
 }
@@ -364,9 +220,7 @@ gs_status check_workspace(const char* where, const void* workspace, size_t have,
 
 extern "C" size_t gs_linear_fwd_workspace_size(const gs_linear_desc* d) {
   if (check_desc("gs_linear_fwd_workspace_size", d) || d->rows == 0) return 0;
-  const size_t a = part_bytes(d->rows, d->out_features, d->in_features);
-  const size_t b = d->dtype == GS_BF16 ? gs::mma_workspace(d->rows, d->out_features, d->in_features) : 0;
-  return a > b ? a : b;
+  return product_space(d->rows, d->out_features, d->in_features, d->dtype);
 }
 
 extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias,
@@ -385,8 +239,9 @@ extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const
   if (z)
     if (gs_status s = gs::check_matrix(where, "z", z, d->rows, d->out_features, d->ldz, d->dtype)) return s;
   if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_linear_fwd_workspace_size(d))) return s;
-  if (d->dtype == GS_F32) return run_fwd<float>(d, x, w, bias, residual, y, z, workspace, status, gs::as_stream(stream));
-  return run_fwd<__nv_bfloat16>(d, x, w, bias, residual, y, z, workspace, status, gs::as_stream(stream));
+  const gs::MmaProduct q{x, w, d->ldx, d->ldw, false, false, d->rows, d->out_features, d->in_features,
+                         bias, residual, y, z, d->ldr, d->ldy, d->ldz, d->act};
+  return run_product(q, d->dtype, workspace, status, gs::as_stream(stream), where);
 }
 
 extern "C" size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d) {

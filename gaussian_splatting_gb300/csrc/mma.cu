@@ -52,7 +52,7 @@ struct Args {
   float* part;  // [splits][m][ldp] when splits > 1: no epilogue
   int64_t ldp;
   int32_t* status;
-  int64_t wait_limit;
+  int wait_limit;
   int drop;
 };
 
@@ -83,11 +83,11 @@ struct EpiState {
   int lane, quad, half;
 };
 
-__device__ __forceinline__ void tile_of(const Args& p, int64_t t, int64_t& m0, int64_t& n0, int& split) {
-  const int64_t nt = t % p.n_tiles, rest = t / p.n_tiles;
-  n0 = nt * p.bn;
-  m0 = rest % p.m_tiles * kTileM;
-  split = (int)(rest / p.m_tiles);
+__device__ __forceinline__ void tile_of(const Args& p, int t, int64_t& m0, int64_t& n0, int& split) {
+  const int nt = t % p.n_tiles, rest = t / p.n_tiles;
+  n0 = (int64_t)nt * p.bn;
+  m0 = (int64_t)(rest % p.m_tiles) * kTileM;
+  split = rest / p.m_tiles;
 }
 
 // whether this warp writes anything of chunk c of the tile at (m0, n0)
@@ -96,7 +96,7 @@ __device__ __forceinline__ bool chunk_in(const Args& p, const EpiState& e, int64
 }
 
 template <int ACT>
-__device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, int64_t t, int64_t total, uint32_t tmem,
+__device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, int t, int total, uint32_t tmem,
                               uint32_t acc_full, uint32_t parity) {
   int64_t m0, n0;
   int split;
@@ -120,8 +120,8 @@ __device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, in
       if (p.has_r) {
         slot = e.loads & 1;
         // the residual piece of the next chunk goes to the other buffer
-        int64_t t2 = t, nm, nn;
-        int c2 = c, s2;
+        int64_t nm, nn;
+        int t2 = t, c2 = c, s2;
         c2 += 2;
         if (c2 * kBufCols >= p.bn) c2 = e.half, t2 += gridDim.x;
         while (t2 < total) {  // skips the chunks that lie outside of C
@@ -136,13 +136,13 @@ __device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, in
                           e.res_bar + 8 * (slot ^ 1));
         }
         if (t2 < total) ++e.issued;
-        if (!tc::mbar_wait(e.res_bar + 8 * slot, (e.loads >> 1) & 1, g)) return false;
+        if (!tc::mbar_wait_warp(e.res_bar + 8 * slot, (e.loads >> 1) & 1, g)) return false;
         ++e.loads;
       }
       __syncwarp();
     }
     if (!waited) {
-      if (!tc::mbar_wait(acc_full, parity, g)) return false;
+      if (!tc::mbar_wait_warp(acc_full, parity, g)) return false;
       tc::fence_after();
       waited = true;
     }
@@ -175,17 +175,17 @@ __device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, in
       tc::bulk_commit();
     }
   }
-  if (!waited && !tc::mbar_wait(acc_full, parity, g)) return false;
+  if (!waited && !tc::mbar_wait_warp(acc_full, parity, g)) return false;
   return true;
 }
 
 // A range of k: the sums as they are, 32 bits, to this split's part (rows of ldp, a multiple of 8).
-__device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& g, int64_t t, uint32_t tmem,
+__device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& g, int t, uint32_t tmem,
                              uint32_t acc_full, uint32_t parity) {
   int64_t m0, n0;
   int split;
   tile_of(p, t, m0, n0, split);
-  if (!tc::mbar_wait(acc_full, parity, g)) return false;
+  if (!tc::mbar_wait_warp(acc_full, parity, g)) return false;
   tc::fence_after();
   const int64_t row = m0 + e.quad * 32 + e.lane;
   float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + n0;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     tc::fence_mbar_init();
   }
   const tc::Guard g{&ctl.dead, p.status, p.wait_limit};
-  const int64_t total = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  const int total = p.m_tiles * p.n_tiles * p.splits;
   if (warp == 9) tc::tmem_alloc(bar(reinterpret_cast<uint64_t&>(ctl.tmem)), p.tmem_cols);
   tc::fence_before();
   __syncthreads();
@@ -247,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         else
           for (int c = 0; c < p.bn; c += 64) tc::tma_load_2d(dst + c * 128, &p.b, (int)n0 + c, kb * kTileK, full);
       };
-      int64_t it = 0;
+      int it = 0;
       bool ok = true;
       if (p.resident && blockIdx.x < total) {
         tc::mbar_expect_tx(bar(ctl.resident), b_bytes * p.kblocks);
         for (int kb = 0; kb < p.kblocks; ++kb)
           load_b(res_b + b_bytes * kb, (int64_t)(blockIdx.x % p.n_tiles) * p.bn, kb, bar(ctl.resident));
       }
-      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
         tile_of(p, t, m0, n0, split);
@@ -273,10 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         }
       }
       if (!ok) {  // gave up: no copy may be in flight when the block ends
-        for (int64_t i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
-          for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1)); ++j) {}
+        for (int i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
+          for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1)); ++j) {}
         if (p.resident)
-          for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.resident), 0); ++j) {}
+          for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.resident), 0); ++j) {}
       }
     }
   } else if (warp == 9) {
@@ -287,10 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
                              (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
       // 16 of k further: 32 bytes along a row, or 16 rows of 128 bytes
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
-      int64_t it = 0, n_acc = 0;
+      int it = 0, n_acc = 0;
       bool ok = true;
       if (p.resident && blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
-      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+      for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
         int64_t m0, n0;
         int split;
         tile_of(p, t, m0, n0, split);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
         tc::mma_commit(bar(ctl.drain));
-        for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+        for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
       }
     }
   } else {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     e.bias = reinterpret_cast<float*>(smem + (epi - base) + kEpiWarps * bufs * kBufBytes) + warp * 64;
     e.res_bar = bar(ctl.res[0]) + warp * 16;
     e.loads = e.issued = 0;
-    int64_t n_acc = 0;
+    int n_acc = 0;
     bool ok = true;
     if (p.has_r) {
       // the first chunk's residual piece
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
       }
       __syncwarp();
       int c = e.half;
-      for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+      for (int t = blockIdx.x; t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
         tile_of(p, t, m0, n0, split);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         break;
       }
     }
-    for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
       const int acc = (int)(n_acc & 1);
       const uint32_t parity = (uint32_t)(n_acc >> 1 & 1), d = tmem + acc * (p.tmem_cols / 2), full = bar(ctl.acc_full[acc]);
       if (p.part) ok = partial_tile(p, e, g, t, d, full, parity);
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     }
     if (!ok && lane == 0) {  // gave up: the pieces in flight land before the block ends
       for (uint32_t i = e.loads; i < e.issued; ++i)
-        for (int64_t j = 0; j < p.wait_limit && !tc::mbar_try(e.res_bar + 8 * (i & 1), i >> 1 & 1); ++j) {}
+        for (int j = 0; j < p.wait_limit && !tc::mbar_try(e.res_bar + 8 * (i & 1), i >> 1 & 1); ++j) {}
     }
     if (lane == 0) tc::bulk_wait0();
   }
@@ -487,6 +487,7 @@ size_t mma_workspace(int64_t m, int64_t n, int64_t k) {
 
 gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
   const Plan pl = plan_of(q.m, q.n, q.k);
+  if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff) return set_error(GS_ERR_INVALID, "%s: too many tiles", where);
   Args p{};
   p.m = q.m, p.n = q.n;
   p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
@@ -494,7 +495,7 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   p.a_mn = q.a_mn, p.b_mn = q.b_mn;
   p.tmem_cols = pl.bn <= 64 ? 128 : pl.bn <= 128 ? 256 : 512;
   p.act = q.act, p.bias = static_cast<const bf16*>(q.bias);
-  p.status = status, p.wait_limit = wait_limit(), p.drop = 0;
+  p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
   p.ldp = pl.ldp;
   p.bufs_y = 1;
   if (pl.splits > 1) p.part = static_cast<float*>(workspace);

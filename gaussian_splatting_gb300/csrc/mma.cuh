@@ -21,6 +21,16 @@ struct MmaProduct {
   int act;
 };
 
+// The general product (mma_staged.cu): float32 in full precision, or bfloat16 whose rows start anywhere.
+size_t staged_workspace(int64_t m, int64_t n, int64_t k);
+gs_status staged_run(const MmaProduct& p, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where);
+
+// the bound of a device-side wait, in tries of about a microsecond
+inline int wait_tries() {
+  const int64_t n = wait_limit();
+  return n < 0x7fffffff ? (int)n : 0x7fffffff;
+}
+
 // whether every array of the product starts its rows on 16-byte boundaries (bfloat16)
 bool mma_takes(const MmaProduct& p);
 // bytes of scratch for a product of these sizes (0: none), whatever its arrays

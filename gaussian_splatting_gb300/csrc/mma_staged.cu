@@ -1,0 +1,536 @@
+// Products whose operands pass through registers on their way to the tensor cores: float32 in full
+// precision, and bfloat16 whose rows do not start on 16-byte boundaries.
+//
+// C(m, n) = sum over k of A(m, k) B(n, k) as in mma.cu.  A float32 value is split into three bfloat16
+// parts, a = a0 + a1 + a2 (each the rounding of what the ones before it leave: 8 + 8 + 8 significant
+// bits, the 24 of the value), and the product is summed from the six pairs whose weight is 2^-16 or more,
+//   a0 b0 | a0 b1 + a1 b0 + a1 b1 + a0 b2 + a2 b0
+// each exact in 32 bits; what is left out is below 2^-25 of |a b|.  The tensor core adds a product of
+// 16 terms to its sum with the low bits cut off (measured: 2.3e-7 of the result after 256 terms, 4.4e-6
+// after 4096, always towards zero), so the pairs of the second group, 2^-8 smaller, have an accumulator of
+// their own, and every 256 of k both are read back and added in registers with ordinary rounding.  Six
+// bfloat16 products at 2.2 PFLOP/s nominal leave about 375 TFLOP/s; the FP32 pipe has 75.
+//
+// Warps of the one persistent block per SM:
+//   warps 8 - 15  load pieces of A and B (16-byte loads where rows start on such boundaries, single
+//                 elements where not), split them and store the parts to a shared-memory stage in the
+//                 tensor core's 128-byte-swizzled layout; the next piece's loads are in flight meanwhile.
+//                 B stays resident where all of its k fits.
+//   warp 16       issues tcgen05.mma
+//   warps 0 - 7   add up the accumulators and write C: 32 x 32 pieces through shared memory, so that the
+//                 epilogue reads and writes whole rows of 32 columns at any alignment
+#include "mma.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kEpiWarps = 8, kLoadWarps = 8;
+constexpr int kLoaders = 32 * kLoadWarps;
+constexpr int kThreads = 32 * (kEpiWarps + kLoadWarps + 1);
+constexpr int kTileM = 128, kTileK = 64;
+constexpr int kMaxStages = 6;
+constexpr int kSmemMost = 232448;  // 227 KB
+constexpr int kSmemCtl = 1024;
+constexpr int kPitch = 33;         // floats per row of an epilogue buffer: rows and columns both hit distinct banks
+constexpr int kBufBytes = 32 * kPitch * 4;
+constexpr int kChunk = 4;          // k blocks between two additions in registers (float32)
+
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t resident, acc_full[2], acc_empty[2], drain;
+  uint32_t tmem, dead;
+};
+
+struct Args {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;
+  int64_t m, n, k;
+  int m_tiles, n_tiles, splits, kblocks, kb_per_split, chunk;
+  int stages, resident;
+  int a_mn, b_mn, a_vec, b_vec;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  int64_t ldr, ldy, ldz;
+  int act;
+  float* part;  // [splits][m][ldp] when splits > 1: no epilogue
+  int64_t ldp;
+  int32_t* status;
+  int wait_limit;
+  int drop;
+};
+
+__device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m0, int64_t& n0, int& split) {
+  const int nt = t % p.n_tiles, rest = t / p.n_tiles;
+  n0 = (int64_t)nt * bn;
+  m0 = (int64_t)(rest % p.m_tiles) * kTileM;
+  split = rest / p.m_tiles;
+}
+
+// 8 consecutive elements at p, those at or past `left` as zeros
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t left, bool vec, float* f) {
+  if (vec && left >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+      f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+    } else {
+      VecIO<bf16, 8>::unpack(*reinterpret_cast<const uint4*>(p), f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < left ? to_f32<T>(p[i]) : 0.f;
+  }
+}
+
+// The parts of 8 values, each part to its plane of the stage (16 bytes at `dst`, `plane` bytes apart).
+template <int PARTS>
+__device__ __forceinline__ void store_parts(unsigned char* dst, int plane, float* f) {
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    uint4 u;
+    uint32_t* w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+      if (q + 1 < PARTS) {
+        f[2 * i] -= bf16_lo(w[i]);  // exact: what the rounding left
+        f[2 * i + 1] -= bf16_hi(w[i]);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + q * plane) = u;
+  }
+}
+
+// One operand as the loaders see it: pieces of EXT (m or n) x 16 (one step of the tensor core), a unit
+// of 8 elements per thread.
+constexpr int kPieces = kTileK / 16;  // of a k block
+constexpr int kDepth = 3;             // pieces of a thread in registers, all but one of them in flight
+
+template <typename T, int EXT>
+struct Operand {
+  static constexpr int kPlane = EXT * kTileK * 2;
+  static_assert(EXT * 2 <= kLoaders, "one unit per thread");
+  const T* p;
+  int64_t ld, ext, k;
+  bool mn, vec;
+
+  // the unit of thread tid: its row or column x, its k, and its place in a plane; whether it has one
+  __device__ __forceinline__ bool place(int tid, int piece, int& x, int& kk, int& at) const {
+    if (!mn) {
+      x = tid >> 1;
+      const int u = (tid & 1) + 2 * piece;
+      kk = u * 8;
+      at = x * 128 + ((u ^ (x & 7)) << 4);
+    } else {
+      const int u = tid % (EXT / 8);
+      kk = tid / (EXT / 8) + 16 * piece;
+      x = u * 8;
+      at = (u >> 3) * (kTileK * 128) + kk * 128 + (((u & 7) ^ (kk & 7)) << 4);
+    }
+    return tid < EXT * 2;
+  }
+  __device__ __forceinline__ void load(int tid, int piece, int64_t x0, int64_t k0, float* f) const {
+    int x, kk, at;
+    if (!place(tid, piece, x, kk, at)) return;
+    const int64_t gx = x0 + x, gk = k0 + kk;
+    if (gx >= ext) return;
+    if (!mn) load8<T>(p + gx * ld + gk, k - gk, vec, f);
+    else load8<T>(p + gk * ld + gx, gk < k ? ext - gx : 0, vec, f);
+  }
+  // Rows and columns outside of the matrix are not written: they only reach sums that are not stored.
+  __device__ __forceinline__ void store(int tid, int piece, int64_t x0, unsigned char* stage, float* f) const {
+    int x, kk, at;
+    if (!place(tid, piece, x, kk, at)) return;
+    if (x0 + x < ext) store_parts<kParts<T>>(stage + at, kPlane, f);
+  }
+};
+
+// Where a loader stands: tile t, k block kb of [.., k_hi), piece h.
+struct Cursor {
+  int64_t m0, n0;
+  int t, kb, k_hi, h;
+};
+
+__device__ __forceinline__ void seek(const Args& p, int bn, Cursor& c, int total) {
+  if (c.t >= total) return;
+  int split;
+  tile_of(p, bn, c.t, c.m0, c.n0, split);
+  c.kb = split * p.kb_per_split;
+  c.k_hi = min(c.kb + p.kb_per_split, p.kblocks);
+  c.h = 0;
+}
+
+__device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int total) {
+  if (++c.h < kPieces) return;
+  c.h = 0;
+  if (++c.kb == c.k_hi) {
+    c.t += gridDim.x;
+    seek(p, bn, c, total);
+  }
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constant__ Args p) {
+  constexpr int PARTS = kParts<T>;
+  constexpr int kAPlane = kTileM * kTileK * 2, kBPlane = BN * kTileK * 2;
+  constexpr int kABytes = kAPlane * PARTS, kBBytes = kBPlane * PARTS;
+  constexpr int kAccs = PARTS == 1 ? 1 : 2;          // accumulators of one k chunk
+  constexpr int kTmem = BN * kAccs * 2;              // columns, two chunks in flight
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
+  unsigned char* res_b = smem + kSmemCtl;
+  unsigned char* ring = res_b + (p.resident ? (size_t)kBBytes * p.kblocks : 0);
+  const int stage_bytes = kABytes + (p.resident ? 0 : kBBytes);
+  unsigned char* epi = ring + (size_t)stage_bytes * p.stages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      tc::mbar_init(bar(ctl.full[s]), kLoadWarps);
+      tc::mbar_init(bar(ctl.empty[s]), 1);
+    }
+    tc::mbar_init(bar(ctl.resident), kLoadWarps);
+    tc::mbar_init(bar(ctl.drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(ctl.acc_full[i]), 1);
+      tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps);
+    }
+    ctl.dead = 0;
+    tc::fence_mbar_init();
+  }
+  const tc::Guard g{&ctl.dead, p.status, p.wait_limit};
+  const int total = p.m_tiles * p.n_tiles * p.splits;
+  if (warp == kEpiWarps + kLoadWarps) tc::tmem_alloc(tc::smem_addr(&ctl.tmem), kTmem);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = ctl.tmem;
+
+  if (warp >= kEpiWarps && warp < kEpiWarps + kLoadWarps) {
+    // ------------------------------------------------------------ loaders
+    const int tid = threadIdx.x - 32 * kEpiWarps;
+    using OpA = Operand<T, kTileM>;
+    using OpB = Operand<T, BN>;
+    const OpA a{static_cast<const T*>(p.a), p.lda, p.m, p.k, p.a_mn != 0, p.a_vec != 0};
+    const OpB b{static_cast<const T*>(p.b), p.ldb, p.n, p.k, p.b_mn != 0, p.b_vec != 0};
+    if (!p.drop) {
+      if (p.resident) {
+        const int64_t n0 = (int64_t)(blockIdx.x % p.n_tiles) * BN;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          float f[kPieces][8];
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) b.load(tid, h, n0, (int64_t)kb * kTileK, f[h]);
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) b.store(tid, h, n0, res_b + (size_t)kBBytes * kb, f[h]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(ctl.resident));
+      }
+      Cursor cur;
+      cur.t = blockIdx.x;
+      seek(p, BN, cur, total);
+      Cursor ahead = cur;
+      float fa[kDepth][8], fb[kDepth][8];
+      auto load = [&](int w) {
+        if (ahead.t >= total) return;
+        a.load(tid, ahead.h, ahead.m0, (int64_t)ahead.kb * kTileK, fa[w]);
+        if (!p.resident) b.load(tid, ahead.h, ahead.n0, (int64_t)ahead.kb * kTileK, fb[w]);
+        advance(p, BN, ahead, total);
+      };
+      int s = 0;
+      uint32_t parity = 1;
+      bool ok = true;
+#pragma unroll
+      for (int w = 0; w + 1 < kDepth; ++w) load(w);
+      while (ok && cur.t < total) {
+#pragma unroll
+        for (int w = 0; w < kDepth; ++w) {  // the register sets alternate
+          if (!ok || cur.t >= total) break;
+          load((w + kDepth - 1) % kDepth);
+          if (cur.h == 0) ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
+          if (!ok) break;
+          unsigned char* st = ring + (size_t)stage_bytes * s;
+          a.store(tid, cur.h, cur.m0, st, fa[w]);
+          if (!p.resident) b.store(tid, cur.h, cur.n0, st + kABytes, fb[w]);
+          if (cur.h == kPieces - 1) {
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(ctl.full[s]));
+            if (++s == p.stages) s = 0, parity ^= 1;
+          }
+          advance(p, BN, cur, total);
+        }
+      }
+    }
+  } else if (warp == kEpiWarps + kLoadWarps) {
+    // ------------------------------------------------------------ matrix instructions
+    if (lane == 0) {
+      const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
+                             (uint32_t)(BN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+      const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
+      int it = 0, n_acc = 0;
+      bool ok = true;
+      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
+      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        int64_t m0, n0;
+        int split;
+        tile_of(p, BN, t, m0, n0, split);
+        int kb = split * p.kb_per_split;
+        const int k_hi = min(kb + p.kb_per_split, p.kblocks);
+        for (; ok && kb < k_hi; ++n_acc) {  // a chunk of k: one set of accumulators
+          const int acc = (int)(n_acc & 1), c_hi = min(kb + p.chunk, k_hi);
+          ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t d = tmem + acc * (kTmem / 2);
+          for (bool first = true; kb < c_hi; ++kb, ++it, first = false) {
+            const int s = (int)(it % p.stages);
+            ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
+            const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
+#pragma unroll
+            for (int i = 0; i < kTileK / 16; ++i) {
+              uint64_t da[PARTS], db[PARTS];
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q) {
+                da[q] = tc::smem_desc(as + q * kAPlane + i * a_step, kTileK * 128, 1024);
+                db[q] = tc::smem_desc(bs + q * kBPlane + i * b_step, kTileK * 128, 1024);
+              }
+              const uint32_t add = !first || i > 0;
+              tc::mma_bf16(d, da[0], db[0], idesc, add);
+              if constexpr (PARTS == 3) {
+                tc::mma_bf16(d + BN, da[0], db[2], idesc, add);
+                tc::mma_bf16(d + BN, da[2], db[0], idesc, 1);
+                tc::mma_bf16(d + BN, da[1], db[1], idesc, 1);
+                tc::mma_bf16(d + BN, da[0], db[1], idesc, 1);
+                tc::mma_bf16(d + BN, da[1], db[0], idesc, 1);
+              }
+            }
+            tc::mma_commit(bar(ctl.empty[s]));
+          }
+          if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+        }
+      }
+      if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
+        tc::mma_commit(bar(ctl.drain));
+        for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    constexpr int kCols = BN / 2;  // of this warp: 32 rows x kCols
+    const int quad = warp & 3, half = warp >> 2;
+    float* buf = reinterpret_cast<float*>(epi + warp * kBufBytes);
+    int n_acc = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      int64_t m0, n0;
+      int split;
+      tile_of(p, BN, t, m0, n0, split);
+      const int k_lo = split * p.kb_per_split, k_hi = min(k_lo + p.kb_per_split, p.kblocks);
+      const int64_t row0 = m0 + quad * 32, col0 = n0 + half * kCols;
+      const bool in = row0 < p.m && col0 < (p.part ? p.ldp : p.n);
+      float sum[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+      for (int kb = k_lo; kb < k_hi; kb += p.chunk, ++n_acc) {
+        const int acc = (int)(n_acc & 1);
+        ok = tc::mbar_wait_warp(bar(ctl.acc_full[acc]), (uint32_t)(n_acc >> 1 & 1), g);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = tmem + acc * (kTmem / 2) + ((uint32_t)(quad * 32) << 16) + half * kCols;
+        if (in) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 8) {
+            float v[8];
+            if constexpr (kAccs == 2) {
+              tc::tmem_load8(d + BN + c, v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
+            }
+            tc::tmem_load8(d + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
+          }
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
+      }
+      if (!ok || !in) continue;
+      if (p.part) {
+        const int64_t row = row0 + lane;
+        if (row < p.m) {
+          float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + col0;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4)
+            if (col0 + c < p.ldp) *reinterpret_cast<float4*>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+        }
+        continue;
+      }
+      const int rows = (int)min((int64_t)32, p.m - row0);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        const int64_t col = col0 + c + lane;
+        const bool ci = col < p.n;
+        const float bias = p.bias && ci ? to_f32<T>(static_cast<const T*>(p.bias)[col]) : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = sum[c + i] + __shfl_sync(0xffffffffu, bias, i);
+        __syncwarp();
+        // a lane owns a column; short separate loops keep the sums of the other pieces in registers
+        if (!ci) continue;
+        if (p.act != GS_ACT_NONE || p.z) {
+          T* z = static_cast<T*>(p.z) + row0 * p.ldz + col;
+#pragma unroll 1
+          for (int r = 0; r < rows; ++r) {
+            const float v = buf[r * kPitch + lane];
+            if (p.z) z[r * p.ldz] = from_f32<T>(v);
+            buf[r * kPitch + lane] = act_value(v, p.act);
+          }
+        }
+        if (p.residual) {
+          const T* res = static_cast<const T*>(p.residual) + row0 * p.ldr + col;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 8) {
+            float rr[8];  // loads in flight
+#pragma unroll
+            for (int r = 0; r < 8; ++r) rr[r] = r0 + r < rows ? to_f32<T>(res[(r0 + r) * p.ldr]) : 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) buf[(r0 + r) * kPitch + lane] += rr[r];
+          }
+        }
+        T* y = static_cast<T*>(p.y) + row0 * p.ldy + col;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) y[r * p.ldy] = from_f32<T>(buf[r * kPitch + lane]);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kEpiWarps + kLoadWarps) tc::tmem_dealloc(tmem, kTmem);
+}
+
+// The splits' parts added in order, then the epilogue: one thread per column of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) k_staged_fold(const float* __restrict__ part, int splits, int64_t m, int n, int64_t ldp,
+                                                     const T* bias, const T* residual, T* y, T* z, int64_t ldr, int64_t ldy,
+                                                     int64_t ldz, int act) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= m * n) return;
+  const int64_t row = e / n;
+  const int col = (int)(e % n);
+  float v = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) v += part[((int64_t)s * m + row) * ldp + col];
+  if (bias) v += to_f32<T>(bias[col]);
+  if (z) z[row * ldz + col] = from_f32<T>(v);
+  v = act_value(v, act);
+  if (residual) v += to_f32<T>(residual[row * ldr + col]);
+  y[row * ldy + col] = from_f32<T>(v);
+}
+
+// ---------------------------------------------------------------- host side
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  int bn, m_tiles, n_tiles, splits, kblocks, kb_per_split;
+  int64_t ldp;
+};
+
+constexpr int kSms = 152;  // the device's; only speed depends on it
+
+// 128 columns per tile where there are more than 64 and enough tiles; ranges of k of at least two blocks
+// (128) where there are too few tiles for the device.
+Plan plan_of(int64_t m, int64_t n, int64_t k) {
+  Plan p;
+  p.m_tiles = (int)ceil_div(m, kTileM);
+  p.kblocks = (int)ceil_div(k, kTileK);
+  p.bn = n <= 64 || (int64_t)p.m_tiles * ceil_div(n, 128) < kSms / 2 ? 64 : 128;
+  p.n_tiles = (int)ceil_div(n, p.bn);
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+  int64_t splits = tiles >= kSms ? 1 : kSms / tiles;
+  if (splits > p.kblocks / 2) splits = p.kblocks / 2;
+  if (splits < 1) splits = 1;
+  p.kb_per_split = (int)ceil_div(p.kblocks, splits);
+  p.splits = (int)ceil_div(p.kblocks, p.kb_per_split);
+  p.ldp = ceil_div(n, 4) * 4;
+  return p;
+}
+
+template <typename T, int BN>
+gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
+  constexpr int kA = kTileM * kTileK * 2 * kParts<T>, kB = BN * kTileK * 2 * kParts<T>;
+  const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
+  int grid = (int)(total < gs::num_sms() ? total : gs::num_sms());
+  const int room = kSmemMost - 1024 - kSmemCtl - kEpiWarps * kBufBytes;
+  // resident B: one range of columns per block, and at least two stages of A beside it
+  if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && (int64_t)kB * pl.kblocks + 2 * kA <= room) {
+    p.resident = 1;
+    grid -= grid % pl.n_tiles;
+  }
+  const int stage = kA + (p.resident ? 0 : kB);
+  const int stages = (room - (p.resident ? kB * pl.kblocks : 0)) / stage;
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  const int smem = kSmemMost - room + (p.resident ? kB * pl.kblocks : 0) + p.stages * stage;
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<T, BN>, kSmemMost);
+  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  k_mma_staged<T, BN><<<grid, kThreads, smem, st>>>(p);
+  return gs::check_launch(where);
+}
+
+template <typename T>
+gs_status run(const gs::MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+  const Plan pl = plan_of(q.m, q.n, q.k);
+  if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff)
+    return gs::set_error(GS_ERR_INVALID, "%s: too many tiles", where);
+  Args p{};
+  p.a = q.a, p.b = q.b, p.lda = q.lda, p.ldb = q.ldb, p.m = q.m, p.n = q.n, p.k = q.k;
+  p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
+  p.kb_per_split = pl.kb_per_split;
+  p.chunk = sizeof(T) == 4 ? kChunk : pl.kblocks;
+  p.a_mn = q.a_mn, p.b_mn = q.b_mn;
+  p.a_vec = gs::rows_aligned16(q.a, q.a_mn ? q.k : q.m, q.lda, dtype);
+  p.b_vec = gs::rows_aligned16(q.b, q.b_mn ? q.k : q.n, q.ldb, dtype);
+  p.bias = q.bias, p.residual = q.residual, p.y = q.y, p.z = q.z, p.ldr = q.ldr, p.ldy = q.ldy, p.ldz = q.ldz;
+  p.act = q.act;
+  p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.ldp = pl.ldp;
+  p.status = status, p.wait_limit = gs::wait_tries(), p.drop = 0;
+  if (gs_status s = pl.bn == 64 ? launch<T, 64>(p, pl, st, where) : launch<T, 128>(p, pl, st, where)) return s;
+  if (!p.part) return GS_OK;
+  k_staged_fold<T><<<(unsigned)ceil_div(q.m * q.n, 256), 256, 0, st>>>(
+      p.part, pl.splits, q.m, (int)q.n, pl.ldp, static_cast<const T*>(q.bias), static_cast<const T*>(q.residual),
+      static_cast<T*>(q.y), static_cast<T*>(q.z), q.ldr, q.ldy, q.ldz, q.act);
+  return gs::check_launch(where);
+}
+
+}  // namespace
+
+namespace gs {
+
+size_t staged_workspace(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_of(m, n, k);
+  return p.splits > 1 ? (size_t)p.splits * m * p.ldp * sizeof(float) : 0;
+}
+
+gs_status staged_run(const MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+  return dtype == GS_F32 ? run<float>(q, dtype, workspace, status, st, where)
+                         : run<bf16>(q, dtype, workspace, status, st, where);
+}
+
+}  // namespace gs

@@ -38,19 +38,24 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 struct Guard {
   volatile uint32_t* dead;
   int32_t* status;
-  int64_t limit;  // tries of one wait
+  int limit;  // tries of one wait
 };
 
 // Waits for the phase with this parity; false if the limit ran out here or elsewhere in the block.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Guard& g) {
   if (mbar_try(bar, parity)) return true;
-  for (int64_t i = 1; i < g.limit; ++i) {
+  for (int i = 1; i < g.limit; ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 15) == 15 && *g.dead) return false;
   }
   *g.dead = 1u;
   if (g.status) atomicOr(g.status, 2);
   return false;
+}
+
+// The same for a whole warp that goes on together: one answer for all its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Guard& g) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, g));
 }
 
 __device__ __forceinline__ void fence_mbar_init() {
@@ -126,6 +131,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// the same for 8 columns
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 }  // namespace tc
