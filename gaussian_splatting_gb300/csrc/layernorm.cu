@@ -48,31 +48,30 @@ struct BwdArgs {
   int width;
 };
 
-// Sums over the G threads that share a row.  A block-wide sum alternates between two buffers,
+// Sums over the G threads that share a row.  A sum over several warps alternates between two buffers,
 // so that one barrier per sum is enough.
+__shared__ float2 s_fold[2][kWarps];
 template <int G>
 struct RowSum {
+  int turn = 0;
   __device__ __forceinline__ void operator()(float& a, float& b) {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) {
+    for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
     }
-  }
-};
-__shared__ float2 s_fold[2][kWarps];
-template <>
-struct RowSum<kThreads> {
-  int turn = 0;
-  __device__ __forceinline__ void operator()(float& a, float& b) {
-    RowSum<32> warp;
-    warp(a, b);
-    if ((threadIdx.x & 31) == 0) s_fold[turn][threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.f;
+    if constexpr (G > 32) {
+      const int warp = threadIdx.x >> 5;
+      if ((threadIdx.x & 31) == 0) s_fold[turn][warp] = make_float2(a, b);
+      __syncthreads();
+      a = b = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) a += s_fold[turn][w].x, b += s_fold[turn][w].y;
-    turn ^= 1;
+      for (int w = 0; w < G / 32; ++w) {
+        const float2 f = s_fold[turn][warp / (G / 32) * (G / 32) + w];
+        a += f.x, b += f.y;
+      }
+      turn ^= 1;
+    }
   }
 };
 
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd(const BwdArgs a) {
         ab[i][e] += __shfl_xor_sync(0xffffffffu, ab[i][e], o);
       }
   }
-  if constexpr (G == kThreads) {
+  if constexpr (G == kThreads) {  // a column belongs to one thread
 #pragma unroll
     for (int i = 0; i < IT; ++i)
       if (in[i]) {
@@ -288,18 +287,20 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd(const BwdArgs a) {
         }
       }
   } else {
-    __shared__ float fold[kWarps][2][32 * VE];
-    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+    // one slot per group of threads that owns all columns: a warp's groups are folded already
+    constexpr int kSlots = G < 32 ? kWarps : kRows, kOwners = G;
+    __shared__ float fold[kSlots][2][kOwners * VE];
+    const int slot = G < 32 ? threadIdx.x >> 5 : sub;
     for (int i = 0; i < IT; ++i) {
       __syncthreads();
       // register arrays are indexed by constants only: the unrolled select keeps them there
 #pragma unroll
       for (int j = 0; j < IT; ++j)
-        if (j == i && wl < G) {
+        if (j == i && (threadIdx.x & 31) < G) {
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            fold[warp][0][lane * VE + e] = ag[j][e];
-            fold[warp][1][lane * VE + e] = ab[j][e];
+            fold[slot][0][lane * VE + e] = ag[j][e];
+            fold[slot][1][lane * VE + e] = ab[j][e];
           }
         }
       __syncthreads();
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd(const BwdArgs a) {
         if (c < a.width) {
           float s = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) s += fold[w][which][e];
+          for (int w = 0; w < kSlots; ++w) s += fold[w][which][e];
           out[which * a.width + c] = s;
         }
       }
@@ -361,8 +362,10 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fold(const float* __rest
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < 2 * width)
+  if (c < 2 * width) {
+#pragma unroll 8
     for (int p = warp; p < n_part; p += kWarps) v += partials[(int64_t)p * 2 * width + c];
+  }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < 2 * width) {
@@ -383,15 +386,25 @@ struct Form {
   int vec, g, it;
 };
 
-// A row gets as few threads as hold it in at most four 16-byte vectors (eight single elements) each,
-// so that narrow rows keep whole warps busy; beyond a warp's reach a block shares it.
-Form form_of(int width, bool vec, int32_t dtype) {
+// Forward: a row gets as few threads as hold it in at most four 16-byte vectors (eight single elements)
+// each, so that narrow rows keep whole warps busy; beyond a warp's reach a block shares it.
+Form fwd_form(int width, bool vec, int32_t dtype) {
   const int ve = vec ? (dtype == GS_F32 ? 4 : 8) : 1;
   const int n = width / ve, most = vec ? 4 : 8;
   for (int g : {8, 16, 32})
     if (n <= g) return {vec, g, 1};
   for (int it = 2; it <= most; it *= 2)
     if (n <= 32 * it) return {vec, 32, it};
+  for (int it = 1; it <= (vec ? 4 : 16); it *= 2)
+    if (n <= kThreads * it) return {vec, kThreads, it};
+  return {vec, kThreads, 0};
+}
+// Backward: every value a thread holds also has two sums in its registers, so a row is spread over as
+// many threads as it has vectors before any thread takes a second one.
+Form bwd_form(int width, bool vec, int32_t dtype) {
+  const int n = width / (vec ? (dtype == GS_F32 ? 4 : 8) : 1);
+  for (int g : {8, 16, 32, 64, 128})
+    if (n <= g) return {vec, g, 1};
   for (int it = 1; it <= (vec ? 4 : 16); it *= 2)
     if (n <= kThreads * it) return {vec, kThreads, it};
   return {vec, kThreads, 0};
@@ -411,35 +424,6 @@ void launch_fwd(const FwdArgs& a, cudaStream_t st) {
   constexpr int U = G == kThreads ? 1 : IT == 1 ? 2 : 1;
   k_layernorm_fwd<T, VE, G, IT, U><<<grid_of(a.rows, kThreads / G * U, kFwdPerSm), kThreads, 0, st>>>(a);
 }
-template <typename T, int VE, int G, int IT>
-int launch_bwd(const BwdArgs& a, cudaStream_t st, int grid) {
-  k_layernorm_bwd<T, VE, G, IT, 1><<<grid, kThreads, 0, st>>>(a);
-  return 0;
-}
-
-#define GS_LN_FORMS(CALL)                                                                           \
-  if (f.vec) {                                                                                      \
-    if (f.g == 8) CALL(VE, 8, 1);                                                                   \
-    else if (f.g == 16) CALL(VE, 16, 1);                                                            \
-    else if (f.g == 32 && f.it == 1) CALL(VE, 32, 1);                                               \
-    else if (f.g == 32 && f.it == 2) CALL(VE, 32, 2);                                               \
-    else if (f.g == 32) CALL(VE, 32, 4);                                                            \
-    else if (f.it == 1) CALL(VE, 256, 1);                                                           \
-    else if (f.it == 2) CALL(VE, 256, 2);                                                           \
-    else CALL(VE, 256, 4);                                                                          \
-  } else {                                                                                          \
-    if (f.g == 8) CALL(1, 8, 1);                                                                    \
-    else if (f.g == 16) CALL(1, 16, 1);                                                             \
-    else if (f.g == 32 && f.it == 1) CALL(1, 32, 1);                                                \
-    else if (f.g == 32 && f.it == 2) CALL(1, 32, 2);                                                \
-    else if (f.g == 32 && f.it == 4) CALL(1, 32, 4);                                                \
-    else if (f.g == 32) CALL(1, 32, 8);                                                             \
-    else if (f.it == 2) CALL(1, 256, 2);                                                            \
-    else if (f.it == 4) CALL(1, 256, 4);                                                            \
-    else if (f.it == 8) CALL(1, 256, 8);                                                            \
-    else CALL(1, 256, 16);                                                                          \
-  }
-
 template <typename T>
 void run_fwd(const FwdArgs& a, Form f, cudaStream_t st) {
   constexpr int VE = 16 / sizeof(T);
@@ -447,9 +431,16 @@ void run_fwd(const FwdArgs& a, Form f, cudaStream_t st) {
     k_layernorm_fwd_wide<T><<<grid_of(a.rows, 1, kFwdPerSm), kThreads, 0, st>>>(a);
     return;
   }
-#define GS_CALL(ve, g, it) launch_fwd<T, ve, g, it>(a, st)
-  GS_LN_FORMS(GS_CALL)
-#undef GS_CALL
+  const int key = (f.vec ? 10000 : 0) + f.g * 20 + f.it;
+  switch (key) {
+#define GS_FORM(v, g, it) \
+  case (v ? 10000 : 0) + g * 20 + it: launch_fwd<T, v ? VE : 1, g, it>(a, st); break;
+    GS_FORM(1, 8, 1) GS_FORM(1, 16, 1) GS_FORM(1, 32, 1) GS_FORM(1, 32, 2) GS_FORM(1, 32, 4)
+    GS_FORM(1, 256, 1) GS_FORM(1, 256, 2) GS_FORM(1, 256, 4)
+    GS_FORM(0, 8, 1) GS_FORM(0, 16, 1) GS_FORM(0, 32, 1) GS_FORM(0, 32, 2) GS_FORM(0, 32, 4) GS_FORM(0, 32, 8)
+    GS_FORM(0, 256, 2) GS_FORM(0, 256, 4) GS_FORM(0, 256, 8) GS_FORM(0, 256, 16)
+#undef GS_FORM
+  }
 }
 
 template <typename T>
@@ -459,9 +450,16 @@ void run_bwd(const BwdArgs& a, Form f, int grid, cudaStream_t st) {
     k_layernorm_bwd_wide<T><<<grid, kThreads, 0, st>>>(a);
     return;
   }
-#define GS_CALL(ve, g, it) launch_bwd<T, ve, g, it>(a, st, grid)
-  GS_LN_FORMS(GS_CALL)
-#undef GS_CALL
+  const int key = (f.vec ? 10000 : 0) + f.g * 20 + f.it;
+  switch (key) {
+#define GS_FORM(v, g, it) \
+  case (v ? 10000 : 0) + g * 20 + it: k_layernorm_bwd<T, v ? VE : 1, g, it, 1><<<grid, kThreads, 0, st>>>(a); break;
+    GS_FORM(1, 8, 1) GS_FORM(1, 16, 1) GS_FORM(1, 32, 1) GS_FORM(1, 64, 1) GS_FORM(1, 128, 1)
+    GS_FORM(1, 256, 1) GS_FORM(1, 256, 2) GS_FORM(1, 256, 4)
+    GS_FORM(0, 8, 1) GS_FORM(0, 16, 1) GS_FORM(0, 32, 1) GS_FORM(0, 64, 1) GS_FORM(0, 128, 1)
+    GS_FORM(0, 256, 1) GS_FORM(0, 256, 2) GS_FORM(0, 256, 4) GS_FORM(0, 256, 8) GS_FORM(0, 256, 16)
+#undef GS_FORM
+  }
 }
 
 gs_status check_desc(const char* where, const gs_layernorm_desc* d) {
@@ -497,7 +495,7 @@ extern "C" gs_status gs_layernorm_fwd(const gs_layernorm_desc* d, const void* x,
   const bool vec = d->width % ve == 0 && gs::rows_aligned16(x, d->rows, d->ldx, d->dtype) &&
                    gs::rows_aligned16(y, d->rows, d->ldy, d->dtype) && gs::aligned16(gamma) && gs::aligned16(beta);
   const FwdArgs a{x, gamma, beta, y, mean, rstd, d->rows, d->ldx, d->ldy, d->width, d->eps};
-  const Form f = form_of(d->width, vec, d->dtype);
+  const Form f = fwd_form(d->width, vec, d->dtype);
   if (d->dtype == GS_F32) run_fwd<float>(a, f, gs::as_stream(stream));
   else run_fwd<__nv_bfloat16>(a, f, gs::as_stream(stream));
   return gs::check_launch(where);
@@ -508,7 +506,7 @@ extern "C" size_t gs_layernorm_bwd_workspace_size(const gs_layernorm_desc* d) {
   // the scalar and the vector form need not have the same number of blocks: the larger
   int most = 1;
   for (int vec = 0; vec < 2; ++vec) {
-    const int g = bwd_grid(d->rows, form_of(d->width, vec, d->dtype), d->width);
+    const int g = bwd_grid(d->rows, bwd_form(d->width, vec, d->dtype), d->width);
     most = g > most ? g : most;
   }
   return sizeof(float) * 2 * (size_t)d->width * most;
@@ -552,7 +550,7 @@ extern "C" gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy
                    gs::rows_aligned16(dy, d->rows, d->lddy, d->dtype) && gs::aligned16(gamma) &&
                    (!skip || gs::rows_aligned16(skip, d->rows, d->ldskip, d->dtype)) &&
                    (!dx || gs::rows_aligned16(dx, d->rows, d->lddx, d->dtype));
-  const Form f = form_of(d->width, vec, d->dtype);
+  const Form f = bwd_form(d->width, vec, d->dtype);
   const int grid = bwd_grid(d->rows, f, d->width);
   float* part = sums ? static_cast<float*>(workspace) : nullptr;
   const BwdArgs a{dy, x, gamma, mean, rstd, skip, dx, part, d->rows, d->lddy, d->ldx, d->ldskip, d->lddx, d->width};

@@ -73,8 +73,10 @@ __global__ void __launch_bounds__(kThreads) k_bias_fold(const float* part, int p
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < n)
+  if (c < n) {
+#pragma unroll 8
     for (int p = w; p < parts; p += 8) v += part[(int64_t)p * n + c];
+  }
   s[w][lane] = v;
   __syncthreads();
   if (w == 0 && c < n) {
@@ -98,7 +100,7 @@ template <typename T>
 int act_grad_parts(int64_t rows, int n) {
   const int cx = row_threads<T>(n);
   const int64_t across = ceil_div(n, cx * (16 / (int64_t)sizeof(T)));
-  int64_t s = ceil_div(8 * 152, across);
+  int64_t s = ceil_div(4 * 152, across);
   const int64_t most = ceil_div(rows, 4 * (kThreads / cx));
   return (int)(s < most ? s : most);
 }

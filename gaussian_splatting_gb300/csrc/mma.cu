@@ -382,31 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
   if (warp == 9) tc::tmem_dealloc(tmem, p.tmem_cols);
 }
 
-// The splits' parts added in order, then the epilogue: one thread per 4 columns of a row.
-__global__ void __launch_bounds__(256) k_mma_fold(const float* __restrict__ part, int splits, int64_t m, int n, int64_t ldp,
-                                                  const bf16* bias, const bf16* residual, bf16* y, bf16* z, int64_t ldr,
-                                                  int64_t ldy, int64_t ldz, int act) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = ldp / 4;
-  if (e >= m * quads) return;
-  const int64_t row = e / quads;
-  const int col = (int)(e % quads) * 4;
-  float v[4] = {};
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 f = *reinterpret_cast<const float4*>(part + ((int64_t)s * m + row) * ldp + col);
-    v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (col + i >= n) break;
-    float t = v[i] + (bias ? __bfloat162float(bias[col + i]) : 0.f);
-    if (z) z[row * ldz + col + i] = __float2bfloat16_rn(t);
-    t = act_value(t, act);
-    if (residual) t += __bfloat162float(residual[row * ldr + col + i]);
-    y[row * ldy + col + i] = __float2bfloat16_rn(t);
-  }
-}
-
 // ---------------------------------------------------------------- host side
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -528,9 +503,9 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   k_mma<<<grid, kThreads, smem, st>>>(p);
   if (gs_status s = check_launch(where)) return s;
   if (!p.part) return GS_OK;
-  k_mma_fold<<<(unsigned)ceil_div(q.m * (pl.ldp / 4), 256), 256, 0, st>>>(
-      p.part, pl.splits, q.m, (int)q.n, pl.ldp, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
-      static_cast<bf16*>(q.z), q.ldr, q.ldy, q.ldz, q.act);
+  launch_fold(FoldArgs<bf16>{p.part, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
+                             static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+              st);
   return check_launch(where);
 }
 

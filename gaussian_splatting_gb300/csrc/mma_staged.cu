@@ -425,25 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
   if (warp == kEpiWarps + kLoadWarps) tc::tmem_dealloc(tmem, kTmem);
 }
 
-// The splits' parts added in order, then the epilogue: one thread per column of a row.
-template <typename T>
-__global__ void __launch_bounds__(256) k_staged_fold(const float* __restrict__ part, int splits, int64_t m, int n, int64_t ldp,
-                                                     const T* bias, const T* residual, T* y, T* z, int64_t ldr, int64_t ldy,
-                                                     int64_t ldz, int act) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= m * n) return;
-  const int64_t row = e / n;
-  const int col = (int)(e % n);
-  float v = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) v += part[((int64_t)s * m + row) * ldp + col];
-  if (bias) v += to_f32<T>(bias[col]);
-  if (z) z[row * ldz + col] = from_f32<T>(v);
-  v = act_value(v, act);
-  if (residual) v += to_f32<T>(residual[row * ldr + col]);
-  y[row * ldy + col] = from_f32<T>(v);
-}
-
 // ---------------------------------------------------------------- host side
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -513,9 +494,9 @@ gs_status run(const gs::MmaProduct& q, int32_t dtype, void* workspace, int32_t* 
   p.status = status, p.wait_limit = gs::wait_tries(), p.drop = 0;
   if (gs_status s = pl.bn == 64 ? launch<T, 64>(p, pl, st, where) : launch<T, 128>(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
-  k_staged_fold<T><<<(unsigned)ceil_div(q.m * q.n, 256), 256, 0, st>>>(
-      p.part, pl.splits, q.m, (int)q.n, pl.ldp, static_cast<const T*>(q.bias), static_cast<const T*>(q.residual),
-      static_cast<T*>(q.y), static_cast<T*>(q.z), q.ldr, q.ldy, q.ldz, q.act);
+  launch_fold(FoldArgs<T>{p.part, static_cast<const T*>(q.bias), static_cast<const T*>(q.residual), static_cast<T*>(q.y),
+                          static_cast<T*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+              st);
   return gs::check_launch(where);
 }
 

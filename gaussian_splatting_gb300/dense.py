@@ -22,7 +22,7 @@ _ACTS = {"none": N.GS_ACT_NONE, "relu": N.GS_ACT_RELU, "gelu": N.GS_ACT_GELU, "s
 
 def _matrix(t, name, rows, cols, like):
     """Row stride of a matrix argument, checked against the call's shape, type and device."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape [{rows}, {cols}], got {list(t.shape)}")
     if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
@@ -37,7 +37,7 @@ def _matrix(t, name, rows, cols, like):
 
 
 def _vector(t, name, n, like):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n}, got {list(t.shape)}")
     if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
@@ -54,25 +54,49 @@ def _start(x, name):
 
 
 class _On:
-    """The device of a call's tensors, and its stream as torch's current one, for the call's span."""
+    """The stream of a call as a handle, with its device and stream made torch's current ones for the call's span."""
 
     def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        self.index = device.index
 
     def __enter__(self):
-        self.guards = []
-        if self.device.index is not None and self.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(self.device))
-        if isinstance(self.stream, int):
-            self.stream = torch.cuda.ExternalStream(self.stream, device=self.device)
-        if self.stream is not None:
-            self.guards.append(torch.cuda.stream(self.stream))
         for g in self.guards:
             g.__enter__()
+        return _raw_stream(self.index)
 
     def __exit__(self, *e):
         for g in reversed(self.guards):
             g.__exit__(*e)
+
+
+class _Here:
+    """_On for the usual call: the current device and its current stream, nothing to enter."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *e):
+        pass
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # a handle without the Stream object around it
+_current = torch._C._cuda_getDevice
+
+
+def _on(device, stream):
+    if stream is None and device.index == _current():
+        return _Here(_raw_stream(device.index))
+    return _On(device, stream)
 
 
 def _scratch(n, device):
@@ -93,7 +117,7 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", keep_z=False, out=Non
         _vector(bias, "bias", n_out, x)
     if residual is not None:
         d.ldr = _matrix(residual, "residual", rows, n_out, x)
-    with _On(x.device, stream):
+    with _on(x.device, stream) as st:
         if out is None:
             out = torch.empty((rows, n_out), dtype=x.dtype, device=x.device)
         d.ldy = _matrix(out, "out", rows, n_out, x)
@@ -102,7 +126,7 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", keep_z=False, out=Non
         if z is not None:
             d.ldz = _matrix(z, "z", rows, n_out, x)
         need = N.gs_linear_fwd_workspace_size(d)
-        N.gs_linear_fwd(d, x, w, bias, residual, out, z, _scratch(need, x.device), need, status)
+        N.gs_linear_fwd(d, x, w, bias, residual, out, z, _scratch(need, x.device), need, status, st)
     return out, z
 
 
@@ -124,7 +148,7 @@ def linear_bwd(dy, x, w, z=None, act="none", bias=True, dx=None, dw=None, dbias=
         raise ValueError(f"z is needed for the gradient of {act}")
     else:
         d.ldz = _matrix(z, "z", rows, n_out, dy)
-    with _On(dy.device, stream):
+    with _on(dy.device, stream) as st:
         if dx is None and need_dx:
             dx = torch.empty((rows, n_in), dtype=dy.dtype, device=dy.device)
         if dw is None and need_dw:
@@ -138,7 +162,7 @@ def linear_bwd(dy, x, w, z=None, act="none", bias=True, dx=None, dw=None, dbias=
         if dbias is not None:
             _vector(dbias, "dbias", n_out, dy)
         need = N.gs_linear_bwd_workspace_size(d)
-        N.gs_linear_bwd(d, dy, x, w, z, dx, dw, dbias, _scratch(need, dy.device), need, status)
+        N.gs_linear_bwd(d, dy, x, w, z, dx, dw, dbias, _scratch(need, dy.device), need, status, st)
     return dx, dw, dbias
 
 
@@ -151,13 +175,13 @@ def layernorm_fwd(x, gamma, beta, eps=1e-5, out=None, stats=True, stream=None):
     d.ldx = _matrix(x, "x", rows, n, x)
     _vector(gamma, "gamma", n, x)
     _vector(beta, "beta", n, x)
-    with _On(x.device, stream):
+    with _on(x.device, stream) as st:
         if out is None:
             out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
         d.ldy = _matrix(out, "out", rows, n, x)
         mean = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
-        N.gs_layernorm_fwd(d, x, gamma, beta, out, mean, rstd)
+        N.gs_layernorm_fwd(d, x, gamma, beta, out, mean, rstd, st)
     return out, mean, rstd
 
 
@@ -175,7 +199,7 @@ def layernorm_bwd(dy, x, gamma, mean, rstd, skip=None, dx=None, dgamma=None, dbe
             raise ValueError(f"{name} must be a contiguous float32 vector of {rows} on {dy.device}")
     if skip is not None:
         d.ldskip = _matrix(skip, "skip", rows, n, dy)
-    with _On(dy.device, stream):
+    with _on(dy.device, stream) as st:
         if dx is None and need_dx:
             dx = torch.empty((rows, n), dtype=dy.dtype, device=dy.device)
         if dgamma is None and need_dparams:
@@ -188,5 +212,5 @@ def layernorm_bwd(dy, x, gamma, mean, rstd, skip=None, dx=None, dgamma=None, dbe
             if t is not None:
                 _vector(t, name, n, dy)
         need = N.gs_layernorm_bwd_workspace_size(d) if dgamma is not None or dbeta is not None else 0
-        N.gs_layernorm_bwd(d, dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, _scratch(need, dy.device), need)
+        N.gs_layernorm_bwd(d, dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, _scratch(need, dy.device), need, st)
     return dx, dgamma, dbeta
