@@ -4,7 +4,8 @@
 //   forward  z  = x w^T    A = x,  B = w
 //   dx       dx = dz w     A = dz, B = w along its other axis
 //   dw       dw = dz^T x   A = dz and B = x, both along their other axes
-// bfloat16 arrays whose rows start on 16-byte boundaries go to mma.cu, everything else to mma_staged.cu.
+// bfloat16 arrays whose rows start on 16-byte boundaries go to mma.cu, other bfloat16 ones to mma_staged.cu,
+// float32 to mma_f32.cu.
 // dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
 // sums, and kept in the workspace for the two products that read it.
 #include "mma.cuh"
@@ -139,13 +140,15 @@ gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, 
 
 gs_status run_product(const gs::MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st,
                       const char* where) {
-  if (dtype == GS_BF16 && gs::mma_takes(q)) return gs::mma_run(q, workspace, status, st, where);
-  return gs::staged_run(q, dtype, workspace, status, st, where);
+  if (dtype == GS_F32) return gs::f32_run(q, workspace, status, st, where);
+  if (gs::mma_takes(q)) return gs::mma_run(q, workspace, status, st, where);
+  return gs::staged_run(q, workspace, status, st, where);
 }
 
 // scratch of a product of these sizes, whichever kernel its arrays' alignment takes it to
 size_t product_space(int64_t m, int64_t n, int64_t k, int32_t dtype) {
-  const size_t a = gs::staged_workspace(m, n, k), b = dtype == GS_BF16 ? gs::mma_workspace(m, n, k) : 0;
+  if (dtype == GS_F32) return gs::f32_workspace(m, n, k);
+  const size_t a = gs::staged_workspace(m, n, k), b = gs::mma_workspace(m, n, k);
   return a > b ? a : b;
 }
 

@@ -402,18 +402,6 @@ EncodeFn encoder() {
   return f;
 }
 
-// a [rows][cols] bfloat16 matrix in boxes of box_rows x 64 columns (128 bytes, swizzled)
-bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  const EncodeFn f = encoder();
-  if (!f) return false;
-  if (rows == 1) ld = (cols + 7) / 8 * 8;  // the stride of a single row is never used
-  const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, stride, box, step,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
@@ -447,6 +435,18 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
 }  // namespace
 
 namespace gs {
+
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype) {
+  const EncodeFn f = encoder();
+  if (!f) return false;
+  const int size = (int)dtype_size(dtype), unit = 16 / size;
+  if (rows == 1) ld = (cols + unit - 1) / unit * unit;  // the stride of a single row is never used
+  const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return f(map, dtype == GS_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+           const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool mma_takes(const MmaProduct& p) {
   const int64_t a_rows = p.a_mn ? p.k : p.m, b_rows = p.b_mn ? p.k : p.n;
@@ -490,12 +490,12 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   int stages = (room - (p.resident ? b_bytes * pl.kblocks : 0)) / stage;
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   const int smem = 1024 + kSmemCtl + (p.resident ? b_bytes * pl.kblocks : 0) + p.stages * stage + epi;
-  bool ok = q.a_mn ? encode(&p.a, q.a, q.k, q.m, q.lda, 64) : encode(&p.a, q.a, q.m, q.k, q.lda, kTileM);
-  ok = ok && (q.b_mn ? encode(&p.b, q.b, q.k, q.n, q.ldb, 64) : encode(&p.b, q.b, q.n, q.k, q.ldb, pl.bn));
+  bool ok = q.a_mn ? encode_map(&p.a, q.a, q.k, q.m, q.lda, 64, GS_BF16) : encode_map(&p.a, q.a, q.m, q.k, q.lda, kTileM, GS_BF16);
+  ok = ok && (q.b_mn ? encode_map(&p.b, q.b, q.k, q.n, q.ldb, 64, GS_BF16) : encode_map(&p.b, q.b, q.n, q.k, q.ldb, pl.bn, GS_BF16));
   if (!p.part) {
-    ok = ok && encode(&p.y, q.y, q.m, q.n, q.ldy, 32);
-    if (q.z) ok = ok && encode(&p.z, q.z, q.m, q.n, q.ldz, 32);
-    if (q.residual) ok = ok && encode(&p.r, q.residual, q.m, q.n, q.ldr, 32);
+    ok = ok && encode_map(&p.y, q.y, q.m, q.n, q.ldy, 32, GS_BF16);
+    if (q.z) ok = ok && encode_map(&p.z, q.z, q.m, q.n, q.ldz, 32, GS_BF16);
+    if (q.residual) ok = ok && encode_map(&p.r, q.residual, q.m, q.n, q.ldr, 32, GS_BF16);
   }
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   const cudaError_t e = max_dynamic_smem((const void*)k_mma, kSmemMost);

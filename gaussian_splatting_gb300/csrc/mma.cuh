@@ -1,6 +1,8 @@
 // The tensor-core product behind the linear layer (mma.cu).
 #pragma once
 
+#include <cuda.h>
+
 #include "dense.cuh"
 
 namespace gs {
@@ -21,9 +23,17 @@ struct MmaProduct {
   int act;
 };
 
-// The general product (mma_staged.cu): float32 in full precision, or bfloat16 whose rows start anywhere.
+// bfloat16 whose rows start anywhere (mma_staged.cu).
 size_t staged_workspace(int64_t m, int64_t n, int64_t k);
-gs_status staged_run(const MmaProduct& p, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where);
+gs_status staged_run(const MmaProduct& p, void* workspace, int32_t* status, cudaStream_t st, const char* where);
+
+// float32 in full precision (mma_f32.cu).
+size_t f32_workspace(int64_t m, int64_t n, int64_t k);
+gs_status f32_run(const MmaProduct& p, void* workspace, int32_t* status, cudaStream_t st, const char* where);
+
+// A tensor map of a [rows][cols] matrix in boxes of box_rows rows x 128 bytes, 128-byte swizzle; false if the
+// driver refuses it.
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype);
 
 // the bound of a device-side wait, in tries of about a microsecond
 inline int wait_tries() {

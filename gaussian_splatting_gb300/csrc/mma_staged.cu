@@ -1,23 +1,14 @@
-// Products whose operands pass through registers on their way to the tensor cores: float32 in full
-// precision, and bfloat16 whose rows do not start on 16-byte boundaries.
+// bfloat16 products whose operands pass through registers on their way to the tensor cores: those whose
+// rows do not start on 16-byte boundaries, which TMA cannot copy.
 //
-// C(m, n) = sum over k of A(m, k) B(n, k) as in mma.cu.  A float32 value is split into three bfloat16
-// parts, a = a0 + a1 + a2 (each the rounding of what the ones before it leave: 8 + 8 + 8 significant
-// bits, the 24 of the value), and the product is summed from the six pairs whose weight is 2^-16 or more,
-//   a0 b0 | a0 b1 + a1 b0 + a1 b1 + a0 b2 + a2 b0
-// each exact in 32 bits; what is left out is below 2^-25 of |a b|.  The tensor core adds a product of
-// 16 terms to its sum with the low bits cut off (measured: 2.3e-7 of the result after 256 terms, 4.4e-6
-// after 4096, always towards zero), so the pairs of the second group, 2^-8 smaller, have an accumulator of
-// their own, and every 256 of k both are read back and added in registers with ordinary rounding.  Six
-// bfloat16 products at 2.2 PFLOP/s nominal leave about 375 TFLOP/s; the FP32 pipe has 75.
-//
+// C(m, n) = sum over k of A(m, k) B(n, k) and the epilogue as in mma.cu.
 // Warps of the one persistent block per SM:
 //   warps 8 - 15  load pieces of A and B (16-byte loads where rows start on such boundaries, single
-//                 elements where not), split them and store the parts to a shared-memory stage in the
-//                 tensor core's 128-byte-swizzled layout; the next piece's loads are in flight meanwhile.
-//                 B stays resident where all of its k fits.
+//                 elements where not) and store them to a shared-memory stage in the tensor core's
+//                 128-byte-swizzled layout; the next pieces' loads are in flight meanwhile.  B stays
+//                 resident where all of its k fits.
 //   warp 16       issues tcgen05.mma
-//   warps 0 - 7   add up the accumulators and write C: 32 x 32 pieces through shared memory, so that the
+//   warps 0 - 7   read the accumulators and write C: 32 x 32 pieces through shared memory, so that the
 //                 epilogue reads and writes whole rows of 32 columns at any alignment
 #include "mma.cuh"
 #include "tcgen05.cuh"
@@ -35,10 +26,6 @@ constexpr int kSmemMost = 232448;  // 227 KB
 constexpr int kSmemCtl = 1024;
 constexpr int kPitch = 33;         // floats per row of an epilogue buffer: rows and columns both hit distinct banks
 constexpr int kBufBytes = 32 * kPitch * 4;
-constexpr int kChunk = 4;          // k blocks between two additions in registers (float32)
-
-template <typename T>
-constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -47,17 +34,17 @@ struct Ctl {
 };
 
 struct Args {
-  const void* a;
-  const void* b;
+  const bf16* a;
+  const bf16* b;
   int64_t lda, ldb;
   int64_t m, n, k;
-  int m_tiles, n_tiles, splits, kblocks, kb_per_split, chunk;
+  int m_tiles, n_tiles, splits, kblocks, kb_per_split;
   int stages, resident;
   int a_mn, b_mn, a_vec, b_vec;
-  const void* bias;
-  const void* residual;
-  void* y;
-  void* z;
+  const bf16* bias;
+  const bf16* residual;
+  bf16* y;
+  bf16* z;
   int64_t ldr, ldy, ldz;
   int act;
   float* part;  // [splits][m][ldp] when splits > 1: no epilogue
@@ -75,50 +62,24 @@ __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m
 }
 
 // 8 consecutive elements at p, those at or past `left` as zeros
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t left, bool vec, float* f) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-      f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
-    } else {
-      VecIO<bf16, 8>::unpack(*reinterpret_cast<const uint4*>(p), f);
-    }
-  } else {
+__device__ __forceinline__ uint4 load8(const bf16* p, int64_t left, bool vec) {
+  if (vec && left >= 8) return *reinterpret_cast<const uint4*>(p);
+  uint16_t e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < left ? to_f32<T>(p[i]) : 0.f;
-  }
-}
-
-// The parts of 8 values, each part to its plane of the stage (16 bytes at `dst`, `plane` bytes apart).
-template <int PARTS>
-__device__ __forceinline__ void store_parts(unsigned char* dst, int plane, float* f) {
-#pragma unroll
-  for (int q = 0; q < PARTS; ++q) {
-    uint4 u;
-    uint32_t* w = &u.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-      if (q + 1 < PARTS) {
-        f[2 * i] -= bf16_lo(w[i]);  // exact: what the rounding left
-        f[2 * i + 1] -= bf16_hi(w[i]);
-      }
-    }
-    *reinterpret_cast<uint4*>(dst + q * plane) = u;
-  }
+  for (int i = 0; i < 8; ++i) e[i] = i < left ? reinterpret_cast<const uint16_t*>(p)[i] : 0;
+  return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                    e[6] | (uint32_t)e[7] << 16);
 }
 
 // One operand as the loaders see it: pieces of EXT (m or n) x 16 (one step of the tensor core), a unit
 // of 8 elements per thread.
 constexpr int kPieces = kTileK / 16;  // of a k block
-constexpr int kDepth = 3;             // pieces of a thread in registers, all but one of them in flight
+constexpr int kDepth = 4;             // pieces of a thread in registers, all but one of them in flight
 
-template <typename T, int EXT>
+template <int EXT>
 struct Operand {
-  static constexpr int kPlane = EXT * kTileK * 2;
   static_assert(EXT * 2 <= kLoaders, "one unit per thread");
-  const T* p;
+  const bf16* p;
   int64_t ld, ext, k;
   bool mn, vec;
 
@@ -137,19 +98,18 @@ struct Operand {
     }
     return tid < EXT * 2;
   }
-  __device__ __forceinline__ void load(int tid, int piece, int64_t x0, int64_t k0, float* f) const {
+  __device__ __forceinline__ uint4 load(int tid, int piece, int64_t x0, int64_t k0) const {
     int x, kk, at;
-    if (!place(tid, piece, x, kk, at)) return;
+    const bool mine = place(tid, piece, x, kk, at);
     const int64_t gx = x0 + x, gk = k0 + kk;
-    if (gx >= ext) return;
-    if (!mn) load8<T>(p + gx * ld + gk, k - gk, vec, f);
-    else load8<T>(p + gk * ld + gx, gk < k ? ext - gx : 0, vec, f);
+    if (!mine || gx >= ext) return make_uint4(0u, 0u, 0u, 0u);
+    if (!mn) return load8(p + gx * ld + gk, k - gk, vec);
+    return load8(p + gk * ld + gx, gk < k ? ext - gx : 0, vec);
   }
   // Rows and columns outside of the matrix are not written: they only reach sums that are not stored.
-  __device__ __forceinline__ void store(int tid, int piece, int64_t x0, unsigned char* stage, float* f) const {
+  __device__ __forceinline__ void store(int tid, int piece, int64_t x0, unsigned char* stage, uint4 v) const {
     int x, kk, at;
-    if (!place(tid, piece, x, kk, at)) return;
-    if (x0 + x < ext) store_parts<kParts<T>>(stage + at, kPlane, f);
+    if (place(tid, piece, x, kk, at) && x0 + x < ext) *reinterpret_cast<uint4*>(stage + at) = v;
   }
 };
 
@@ -177,13 +137,10 @@ __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int to
   }
 }
 
-template <typename T, int BN>
+template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constant__ Args p) {
-  constexpr int PARTS = kParts<T>;
-  constexpr int kAPlane = kTileM * kTileK * 2, kBPlane = BN * kTileK * 2;
-  constexpr int kABytes = kAPlane * PARTS, kBBytes = kBPlane * PARTS;
-  constexpr int kAccs = PARTS == 1 ? 1 : 2;          // accumulators of one k chunk
-  constexpr int kTmem = BN * kAccs * 2;              // columns, two chunks in flight
+  constexpr int kABytes = kTileM * kTileK * 2, kBBytes = BN * kTileK * 2;
+  constexpr int kTmem = BN * 2;  // columns, two tiles in flight
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
@@ -218,17 +175,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
   if (warp >= kEpiWarps && warp < kEpiWarps + kLoadWarps) {
     // ------------------------------------------------------------ loaders
     const int tid = threadIdx.x - 32 * kEpiWarps;
-    using OpA = Operand<T, kTileM>;
-    using OpB = Operand<T, BN>;
-    const OpA a{static_cast<const T*>(p.a), p.lda, p.m, p.k, p.a_mn != 0, p.a_vec != 0};
-    const OpB b{static_cast<const T*>(p.b), p.ldb, p.n, p.k, p.b_mn != 0, p.b_vec != 0};
+    const Operand<kTileM> a{p.a, p.lda, p.m, p.k, p.a_mn != 0, p.a_vec != 0};
+    const Operand<BN> b{p.b, p.ldb, p.n, p.k, p.b_mn != 0, p.b_vec != 0};
     if (!p.drop) {
       if (p.resident) {
         const int64_t n0 = (int64_t)(blockIdx.x % p.n_tiles) * BN;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          float f[kPieces][8];
+          uint4 f[kPieces];
 #pragma unroll
-          for (int h = 0; h < kPieces; ++h) b.load(tid, h, n0, (int64_t)kb * kTileK, f[h]);
+          for (int h = 0; h < kPieces; ++h) f[h] = b.load(tid, h, n0, (int64_t)kb * kTileK);
 #pragma unroll
           for (int h = 0; h < kPieces; ++h) b.store(tid, h, n0, res_b + (size_t)kBBytes * kb, f[h]);
         }
@@ -240,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       cur.t = blockIdx.x;
       seek(p, BN, cur, total);
       Cursor ahead = cur;
-      float fa[kDepth][8], fb[kDepth][8];
+      uint4 fa[kDepth], fb[kDepth];
       auto load = [&](int w) {
         if (ahead.t >= total) return;
-        a.load(tid, ahead.h, ahead.m0, (int64_t)ahead.kb * kTileK, fa[w]);
-        if (!p.resident) b.load(tid, ahead.h, ahead.n0, (int64_t)ahead.kb * kTileK, fb[w]);
+        fa[w] = a.load(tid, ahead.h, ahead.m0, (int64_t)ahead.kb * kTileK);
+        if (!p.resident) fb[w] = b.load(tid, ahead.h, ahead.n0, (int64_t)ahead.kb * kTileK);
         advance(p, BN, ahead, total);
       };
       int s = 0;
@@ -287,41 +242,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
         tile_of(p, BN, t, m0, n0, split);
         int kb = split * p.kb_per_split;
         const int k_hi = min(kb + p.kb_per_split, p.kblocks);
-        for (; ok && kb < k_hi; ++n_acc) {  // a chunk of k: one set of accumulators
-          const int acc = (int)(n_acc & 1), c_hi = min(kb + p.chunk, k_hi);
-          ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+        const int acc = n_acc & 1;
+        ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (bool first = true; kb < k_hi; ++kb, ++it, first = false) {
+          const int s = it % p.stages;
+          ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t d = tmem + acc * (kTmem / 2);
-          for (bool first = true; kb < c_hi; ++kb, ++it, first = false) {
-            const int s = (int)(it % p.stages);
-            ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
-            if (!ok) break;
-            tc::fence_after();
-            const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
-            const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
+          const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
+          const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
 #pragma unroll
-            for (int i = 0; i < kTileK / 16; ++i) {
-              uint64_t da[PARTS], db[PARTS];
-#pragma unroll
-              for (int q = 0; q < PARTS; ++q) {
-                da[q] = tc::smem_desc(as + q * kAPlane + i * a_step, kTileK * 128, 1024);
-                db[q] = tc::smem_desc(bs + q * kBPlane + i * b_step, kTileK * 128, 1024);
-              }
-              const uint32_t add = !first || i > 0;
-              tc::mma_bf16(d, da[0], db[0], idesc, add);
-              if constexpr (PARTS == 3) {
-                tc::mma_bf16(d + BN, da[0], db[2], idesc, add);
-                tc::mma_bf16(d + BN, da[2], db[0], idesc, 1);
-                tc::mma_bf16(d + BN, da[1], db[1], idesc, 1);
-                tc::mma_bf16(d + BN, da[0], db[1], idesc, 1);
-                tc::mma_bf16(d + BN, da[1], db[0], idesc, 1);
-              }
-            }
-            tc::mma_commit(bar(ctl.empty[s]));
-          }
-          if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+          for (int i = 0; i < kTileK / 16; ++i)
+            tc::mma_bf16(d, tc::smem_desc(as + i * a_step, kTileK * 128, 1024), tc::smem_desc(bs + i * b_step, kTileK * 128, 1024),
+                         idesc, !first || i > 0);
+          tc::mma_commit(bar(ctl.empty[s]));
         }
+        if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+        ++n_acc;
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
         tc::mma_commit(bar(ctl.drain));
@@ -339,83 +279,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       int64_t m0, n0;
       int split;
       tile_of(p, BN, t, m0, n0, split);
-      const int k_lo = split * p.kb_per_split, k_hi = min(k_lo + p.kb_per_split, p.kblocks);
       const int64_t row0 = m0 + quad * 32, col0 = n0 + half * kCols;
       const bool in = row0 < p.m && col0 < (p.part ? p.ldp : p.n);
-      float sum[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
-      for (int kb = k_lo; kb < k_hi; kb += p.chunk, ++n_acc) {
-        const int acc = (int)(n_acc & 1);
-        ok = tc::mbar_wait_warp(bar(ctl.acc_full[acc]), (uint32_t)(n_acc >> 1 & 1), g);
-        if (!ok) break;
-        tc::fence_after();
-        const uint32_t d = tmem + acc * (kTmem / 2) + ((uint32_t)(quad * 32) << 16) + half * kCols;
-        if (in) {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 8) {
-            float v[8];
-            if constexpr (kAccs == 2) {
-              tc::tmem_load8(d + BN + c, v);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
-            }
-            tc::tmem_load8(d + c, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
-          }
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
-      }
-      if (!ok || !in) continue;
-      if (p.part) {
-        const int64_t row = row0 + lane;
-        if (row < p.m) {
-          float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + col0;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4)
-            if (col0 + c < p.ldp) *reinterpret_cast<float4*>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
-        }
-        continue;
-      }
+      const int acc = n_acc & 1;
+      ok = tc::mbar_wait_warp(bar(ctl.acc_full[acc]), (uint32_t)(n_acc >> 1 & 1), g);
+      if (!ok) break;
+      ++n_acc;
+      tc::fence_after();
+      const uint32_t d = tmem + acc * BN + ((uint32_t)(quad * 32) << 16) + half * kCols;
       const int rows = (int)min((int64_t)32, p.m - row0);
+      for (int c = 0; in && c < kCols; c += 32) {
+        float sum[32];
+        tc::tmem_load32(d + c, sum);
+        if (p.part) {
+          const int64_t row = row0 + lane;
+          if (row < p.m) {
+            float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + col0 + c;
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
+            for (int i = 0; i < 32; i += 4)
+              if (col0 + c + i < p.ldp)
+                *reinterpret_cast<float4*>(out + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+          }
+          continue;
+        }
+        // a lane owns a column from here on
         const int64_t col = col0 + c + lane;
         const bool ci = col < p.n;
-        const float bias = p.bias && ci ? to_f32<T>(static_cast<const T*>(p.bias)[col]) : 0.f;
+        const float bias = p.bias && ci ? __bfloat162float(p.bias[col]) : 0.f;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = sum[c + i] + __shfl_sync(0xffffffffu, bias, i);
+        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = sum[i];
         __syncwarp();
-        // a lane owns a column; short separate loops keep the sums of the other pieces in registers
         if (!ci) continue;
-        if (p.act != GS_ACT_NONE || p.z) {
-          T* z = static_cast<T*>(p.z) + row0 * p.ldz + col;
-#pragma unroll 1
-          for (int r = 0; r < rows; ++r) {
-            const float v = buf[r * kPitch + lane];
-            if (p.z) z[r * p.ldz] = from_f32<T>(v);
-            buf[r * kPitch + lane] = act_value(v, p.act);
+        const bf16* res = p.residual + row0 * p.ldr + col;
+        bf16* y = p.y + row0 * p.ldy + col;
+        bf16* z = p.z + row0 * p.ldz + col;
+        for (int r0 = 0; r0 < rows; r0 += 16) {
+          bf16 rr[16];  // loads in flight
+          if (p.residual) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (r0 + r < rows) rr[r] = res[(r0 + r) * p.ldr];
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            if (r0 + r >= rows) break;
+            float v = buf[(r0 + r) * kPitch + lane] + bias;
+            if (p.z) z[(r0 + r) * p.ldz] = __float2bfloat16_rn(v);
+            v = act_value(v, p.act);
+            if (p.residual) v += __bfloat162float(rr[r]);
+            y[(r0 + r) * p.ldy] = __float2bfloat16_rn(v);
           }
         }
-        if (p.residual) {
-          const T* res = static_cast<const T*>(p.residual) + row0 * p.ldr + col;
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 8) {
-            float rr[8];  // loads in flight
-#pragma unroll
-            for (int r = 0; r < 8; ++r) rr[r] = r0 + r < rows ? to_f32<T>(res[(r0 + r) * p.ldr]) : 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) buf[(r0 + r) * kPitch + lane] += rr[r];
-          }
-        }
-        T* y = static_cast<T*>(p.y) + row0 * p.ldy + col;
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) y[r * p.ldy] = from_f32<T>(buf[r * kPitch + lane]);
       }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
     }
   }
   __syncwarp();
@@ -453,9 +372,9 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-template <typename T, int BN>
+template <int BN>
 gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
-  constexpr int kA = kTileM * kTileK * 2 * kParts<T>, kB = BN * kTileK * 2 * kParts<T>;
+  constexpr int kA = kTileM * kTileK * 2, kB = BN * kTileK * 2;
   const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = (int)(total < gs::num_sms() ? total : gs::num_sms());
   const int room = kSmemMost - 1024 - kSmemCtl - kEpiWarps * kBufBytes;
@@ -468,35 +387,9 @@ gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
   const int stages = (room - (p.resident ? kB * pl.kblocks : 0)) / stage;
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   const int smem = kSmemMost - room + (p.resident ? kB * pl.kblocks : 0) + p.stages * stage;
-  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<T, BN>, kSmemMost);
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN>, kSmemMost);
   if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  k_mma_staged<T, BN><<<grid, kThreads, smem, st>>>(p);
-  return gs::check_launch(where);
-}
-
-template <typename T>
-gs_status run(const gs::MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
-  const Plan pl = plan_of(q.m, q.n, q.k);
-  if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff)
-    return gs::set_error(GS_ERR_INVALID, "%s: too many tiles", where);
-  Args p{};
-  p.a = q.a, p.b = q.b, p.lda = q.lda, p.ldb = q.ldb, p.m = q.m, p.n = q.n, p.k = q.k;
-  p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
-  p.kb_per_split = pl.kb_per_split;
-  p.chunk = sizeof(T) == 4 ? kChunk : pl.kblocks;
-  p.a_mn = q.a_mn, p.b_mn = q.b_mn;
-  p.a_vec = gs::rows_aligned16(q.a, q.a_mn ? q.k : q.m, q.lda, dtype);
-  p.b_vec = gs::rows_aligned16(q.b, q.b_mn ? q.k : q.n, q.ldb, dtype);
-  p.bias = q.bias, p.residual = q.residual, p.y = q.y, p.z = q.z, p.ldr = q.ldr, p.ldy = q.ldy, p.ldz = q.ldz;
-  p.act = q.act;
-  p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  p.ldp = pl.ldp;
-  p.status = status, p.wait_limit = gs::wait_tries(), p.drop = 0;
-  if (gs_status s = pl.bn == 64 ? launch<T, 64>(p, pl, st, where) : launch<T, 128>(p, pl, st, where)) return s;
-  if (!p.part) return GS_OK;
-  launch_fold(FoldArgs<T>{p.part, static_cast<const T*>(q.bias), static_cast<const T*>(q.residual), static_cast<T*>(q.y),
-                          static_cast<T*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
-              st);
+  k_mma_staged<BN><<<grid, kThreads, smem, st>>>(p);
   return gs::check_launch(where);
 }
 
@@ -509,9 +402,28 @@ size_t staged_workspace(int64_t m, int64_t n, int64_t k) {
   return p.splits > 1 ? (size_t)p.splits * m * p.ldp * sizeof(float) : 0;
 }
 
-gs_status staged_run(const MmaProduct& q, int32_t dtype, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
-  return dtype == GS_F32 ? run<float>(q, dtype, workspace, status, st, where)
-                         : run<bf16>(q, dtype, workspace, status, st, where);
+gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+  const Plan pl = plan_of(q.m, q.n, q.k);
+  if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff)
+    return set_error(GS_ERR_INVALID, "%s: too many tiles", where);
+  Args p{};
+  p.a = static_cast<const bf16*>(q.a), p.b = static_cast<const bf16*>(q.b), p.lda = q.lda, p.ldb = q.ldb, p.m = q.m, p.n = q.n, p.k = q.k;
+  p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
+  p.kb_per_split = pl.kb_per_split;
+  p.a_mn = q.a_mn, p.b_mn = q.b_mn;
+  p.a_vec = rows_aligned16(q.a, q.a_mn ? q.k : q.m, q.lda, GS_BF16);
+  p.b_vec = rows_aligned16(q.b, q.b_mn ? q.k : q.n, q.ldb, GS_BF16);
+  p.bias = static_cast<const bf16*>(q.bias), p.residual = static_cast<const bf16*>(q.residual);
+  p.y = static_cast<bf16*>(q.y), p.z = static_cast<bf16*>(q.z), p.ldr = q.ldr, p.ldy = q.ldy, p.ldz = q.ldz;
+  p.act = q.act;
+  p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.ldp = pl.ldp;
+  p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
+  if (gs_status s = pl.bn == 64 ? launch<64>(p, pl, st, where) : launch<128>(p, pl, st, where)) return s;
+  if (!p.part) return GS_OK;
+  launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+              st);
+  return check_launch(where);
 }
 
 }  // namespace gs

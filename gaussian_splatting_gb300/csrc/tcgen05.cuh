@@ -101,6 +101,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
   return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
+// The same for rows of 64 bytes along k, 64-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc_64(uint32_t addr, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 4ull << 61;
+}
+
 // D (TMEM, f32) = A B^T (+ D), bfloat16 operands in shared memory
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
