@@ -354,29 +354,30 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd_wide(const BwdArgs a
   }
 }
 
-// out[c] = sum over the partial rows, in order: 32 columns by 8 interleaved row sets per block.
+// out[c] = sum over the partial rows: 32 columns by 32 interleaved sets of rows per block, in order.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_layernorm_fold(const float* __restrict__ partials, int n_part, int width,
-                                                             T* __restrict__ dgamma, T* __restrict__ dbeta) {
-  __shared__ float s[kWarps][32];
+__global__ void __launch_bounds__(1024) k_layernorm_fold(const float* __restrict__ partials, int n_part, int width,
+                                                         T* __restrict__ dgamma, T* __restrict__ dbeta) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < 2 * width) {
 #pragma unroll 8
-    for (int p = warp; p < n_part; p += kWarps) v += partials[(int64_t)p * 2 * width + c];
+    for (int p = warp; p < n_part; p += 32) v += partials[(int64_t)p * 2 * width + c];
   }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < 2 * width) {
-    v = 0.f;
+  // warp w: column w of the block
+  v = s[lane][warp];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s[w][lane];
-    if (c < width) {
-      if (dgamma) dgamma[c] = from_f32<T>(v);
-    } else if (dbeta) {
-      dbeta[c - width] = from_f32<T>(v);
-    }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane != 0 || col >= 2 * width) return;
+  if (col < width) {
+    if (dgamma) dgamma[col] = from_f32<T>(v);
+  } else if (dbeta) {
+    dbeta[col - width] = from_f32<T>(v);
   }
 }
 
@@ -560,9 +561,9 @@ extern "C" gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy
   if (!sums) return GS_OK;
   const int blocks = (2 * d->width + 31) / 32;
   if (d->dtype == GS_F32)
-    k_layernorm_fold<float><<<blocks, kThreads, 0, st>>>(part, grid, d->width, (float*)dgamma, (float*)dbeta);
+    k_layernorm_fold<float><<<blocks, 1024, 0, st>>>(part, grid, d->width, (float*)dgamma, (float*)dbeta);
   else
-    k_layernorm_fold<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(part, grid, d->width, (__nv_bfloat16*)dgamma,
+    k_layernorm_fold<__nv_bfloat16><<<blocks, 1024, 0, st>>>(part, grid, d->width, (__nv_bfloat16*)dgamma,
                                                                  (__nv_bfloat16*)dbeta);
   return gs::check_launch(where);
 }

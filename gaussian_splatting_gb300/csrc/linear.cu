@@ -68,24 +68,25 @@ __global__ void __launch_bounds__(kThreads) k_act_grad(const T* dy, const T* z, 
   }
 }
 
+// the parts added in order: 32 columns by 32 interleaved sets of parts per block
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_bias_fold(const float* part, int parts, int n, T* out) {
-  __shared__ float s[8][32];
+__global__ void __launch_bounds__(1024) k_bias_fold(const float* part, int parts, int n, T* out) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < n) {
 #pragma unroll 8
-    for (int p = w; p < parts; p += 8) v += part[(int64_t)p * n + c];
+    for (int p = w; p < parts; p += 32) v += part[(int64_t)p * n + c];
   }
   s[w][lane] = v;
   __syncthreads();
-  if (w == 0 && c < n) {
-    v = 0.f;
+  // warp w: column w of the block
+  v = s[lane][w];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
-    out[c] = from_f32<T>(v);
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 32 + w;
+  if (lane == 0 && col < n) out[col] = from_f32<T>(v);
 }
 
 // ---------------------------------------------------------------- host side
@@ -134,7 +135,7 @@ gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, 
 #undef GS_GO
   if (gs_status s = gs::check_launch(where)) return s;
   if (!dbias) return GS_OK;
-  k_bias_fold<T><<<(unsigned)ceil_div(n, 32), kThreads, 0, st>>>(part, parts, n, dbias);
+  k_bias_fold<T><<<(unsigned)ceil_div(n, 32), 1024, 0, st>>>(part, parts, n, dbias);
   return gs::check_launch(where);
 }
 

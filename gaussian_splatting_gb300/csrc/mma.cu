@@ -84,10 +84,18 @@ struct EpiState {
 };
 
 __device__ __forceinline__ void tile_of(const Args& p, int t, int64_t& m0, int64_t& n0, int& split) {
-  const int nt = t % p.n_tiles, rest = t / p.n_tiles;
+  int nt = 0, mt = t;
+  split = 0;
+  if (p.n_tiles > 1) {
+    mt = t / p.n_tiles;
+    nt = t - mt * p.n_tiles;
+  }
+  if (p.splits > 1) {
+    split = mt / p.m_tiles;
+    mt -= split * p.m_tiles;
+  }
   n0 = (int64_t)nt * p.bn;
-  m0 = (int64_t)(rest % p.m_tiles) * kTileM;
-  split = rest / p.m_tiles;
+  m0 = (int64_t)mt * kTileM;
 }
 
 // whether this warp writes anything of chunk c of the tile at (m0, n0)
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
   const uint32_t ring = res_b + (p.resident ? b_bytes * p.kblocks : 0);
   const uint32_t stage_bytes = kABytes + (p.resident ? 0 : b_bytes);
   const uint32_t epi = ring + stage_bytes * p.stages;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -239,21 +247,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
 
   if (warp == 8) {
     // ------------------------------------------------------------ producer
-    if (lane == 0 && !p.drop) {
-      tc::prefetch_map(&p.a);
-      tc::prefetch_map(&p.b);
+    if (!p.drop) {
       auto load_b = [&](uint32_t dst, int64_t n0, int kb, uint32_t full) {
         if (!p.b_mn) tc::tma_load_2d(dst, &p.b, kb * kTileK, (int)n0, full);
         else
           for (int c = 0; c < p.bn; c += 64) tc::tma_load_2d(dst + c * 128, &p.b, (int)n0 + c, kb * kTileK, full);
       };
-      int it = 0;
+      int it = 0, s = 0;
+      uint32_t parity = 1;
       bool ok = true;
-      if (p.resident && blockIdx.x < total) {
+      if (p.resident && (int)blockIdx.x < total && tc::elect_one()) {
         tc::mbar_expect_tx(bar(ctl.resident), b_bytes * p.kblocks);
         for (int kb = 0; kb < p.kblocks; ++kb)
           load_b(res_b + b_bytes * kb, (int64_t)(blockIdx.x % p.n_tiles) * p.bn, kb, bar(ctl.resident));
       }
+      __syncwarp();
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
@@ -261,15 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         const int k_lo = split * p.kb_per_split;
         const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
         for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-          const int s = (int)(it % p.stages);
-          ok = tc::mbar_wait(bar(ctl.empty[s]), (uint32_t)(it / p.stages & 1) ^ 1, g);
+          ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
           if (!ok) break;
-          const uint32_t dst = ring + stage_bytes * s, full = bar(ctl.full[s]);
-          tc::mbar_expect_tx(full, stage_bytes);
-          if (!p.a_mn) tc::tma_load_2d(dst, &p.a, kb * kTileK, (int)m0, full);
-          else
-            for (int c = 0; c < kTileM; c += 64) tc::tma_load_2d(dst + c * 128, &p.a, (int)m0 + c, kb * kTileK, full);
-          if (!p.resident) load_b(dst + kABytes, n0, kb, full);
+          if (tc::elect_one()) {
+            const uint32_t dst = ring + stage_bytes * s, full = bar(ctl.full[s]);
+            tc::mbar_expect_tx(full, stage_bytes);
+            if (!p.a_mn) tc::tma_load_2d(dst, &p.a, kb * kTileK, (int)m0, full);
+            else
+              for (int c = 0; c < kTileM; c += 64) tc::tma_load_2d(dst + c * 128, &p.a, (int)m0 + c, kb * kTileK, full);
+            if (!p.resident) load_b(dst + kABytes, n0, kb, full);
+          }
+          __syncwarp();
+          if (++s == p.stages) s = 0, parity ^= 1;
         }
       }
       if (!ok) {  // gave up: no copy may be in flight when the block ends
@@ -281,15 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ matrix instructions
-    if (lane == 0) {
+    {
       // bfloat16 operands, f32 sums, 128 x bn
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
                              (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
       // 16 of k further: 32 bytes along a row, or 16 rows of 128 bytes
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
-      int it = 0, n_acc = 0;
+      int s = 0, n_acc = 0;
+      uint32_t parity = 0;
       bool ok = true;
-      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
+      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
         int64_t m0, n0;
         int split;
@@ -297,27 +309,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         const int k_lo = split * p.kb_per_split;
         const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
         const int acc = (int)(n_acc & 1);
-        ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+        ok = tc::mbar_wait_warp(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * (p.tmem_cols / 2);
-        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-          const int s = (int)(it % p.stages);
-          ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          ok = tc::mbar_wait_warp(bar(ctl.full[s]), parity, g);
           if (!ok) break;
           tc::fence_after();
           const uint32_t a = ring + stage_bytes * s;
           const uint32_t b = p.resident ? res_b + b_bytes * kb : a + kABytes;
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kTileK / 16; ++i)
+            for (int i = 0; i < kTileK / 16; ++i)
             tc::mma_bf16(d, tc::smem_desc(a + i * a_step, 64 * 128, 1024), tc::smem_desc(b + i * b_step, 64 * 128, 1024), idesc,
                          kb > k_lo || i > 0);
-          tc::mma_commit(bar(ctl.empty[s]));
+            tc::mma_commit(bar(ctl.empty[s]));
+          }
+          __syncwarp();
+          if (++s == p.stages) s = 0, parity ^= 1;
         }
-        if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+        if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
+        __syncwarp();
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
-        tc::mma_commit(bar(ctl.drain));
+        if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
+        __syncwarp();
         for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
       }
     }

@@ -19,9 +19,9 @@
 //                 its k fits.  (Loading straight to registers instead kept 16 KB in flight per SM: 312 us for
 //                 the 300,000 x 59 x 128 weight gradient.)
 //   warp 16       issues tcgen05.mma
-//   warps 0 - 7   add up the accumulators and write C: 32 x 32 pieces through shared memory, so that the
-//                 epilogue reads and writes whole rows of 32 columns at any alignment; the residual is
-//                 copied ahead while the tile is being summed
+//   warps 0 - 7   add up the accumulators and write C in 32 x 32 pieces through shared memory: by bulk copies
+//                 where the arrays' layout allows (see Way), a column per lane where not; the residual is
+//                 copied ahead while the tile before is written
 // Every wait is bounded (see tc::Guard).
 #include <cuda.h>
 
@@ -39,11 +39,16 @@ constexpr int kStages = 2;         // of split parts
 constexpr int kMaxRaw = 6;
 constexpr int kSmemMost = 232448;  // 227 KB
 constexpr int kSmemCtl = 1024;
-constexpr int kPitch = 33;         // floats per row of an epilogue buffer: rows and columns both hit distinct banks
-constexpr int kBufBytes = 32 * kPitch * 4;
+constexpr int kBufBytes = 32 * 32 * 4;  // an epilogue warp's 32 x 32 piece
 constexpr int kChunk = 8;          // k blocks between two additions in registers
 
+// How an array of the epilogue is read or written: a column per lane; 32 x 32 boxes by TMA, where its rows start
+// on 16-byte boundaries; or 32 whole rows at a time as one run of bytes, where they follow each other without
+// gaps and one tile holds all columns (a 59-column record).
+enum Way { kPlain, kBox, kDense };
+
 struct Ctl {
+  uint64_t res[kEpiWarps];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t full[kStages], empty[kStages];
   uint64_t resident, acc_full[2], acc_empty[2], drain;
@@ -52,7 +57,8 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= kSmemCtl, "control block");
 
 struct Args {
-  CUtensorMap map_a, map_b;
+  CUtensorMap map_a, map_b, map_y, map_z, map_r;
+  int y_way, z_way, r_way;
   const float* a;
   const float* b;
   int64_t lda, ldb;
@@ -74,10 +80,25 @@ struct Args {
 };
 
 __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m0, int64_t& n0, int& split) {
-  const int nt = t % p.n_tiles, rest = t / p.n_tiles;
+  int nt = 0, mt = t;
+  split = 0;
+  if (p.n_tiles > 1) {
+    mt = t / p.n_tiles;
+    nt = t - mt * p.n_tiles;
+  }
+  if (p.splits > 1) {
+    split = mt / p.m_tiles;
+    mt -= split * p.m_tiles;
+  }
   n0 = (int64_t)nt * bn;
-  m0 = (int64_t)(rest % p.m_tiles) * kTileM;
-  split = rest / p.m_tiles;
+  m0 = (int64_t)mt * kTileM;
+}
+
+// barrier of one team
+template <int TEAM>
+__device__ __forceinline__ void team_sync(int group) {
+  if (group == 0) asm volatile("bar.sync 1, %0;" ::"n"(TEAM) : "memory");
+  else asm volatile("bar.sync 2, %0;" ::"n"(TEAM) : "memory");
 }
 
 // cp.async of one word, or a zero
@@ -89,10 +110,10 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const float* src, bool i
 //  raw    [x][k]: rows of 128 bytes; [k][x]: EXT / 32 boxes of 32 rows of 128 bytes.  16-byte units of a row are
 //         swizzled (unit ^ row % 8), by TMA's 128-byte mode or by the copying threads.
 //  parts  [x][k]: rows of 64 bytes, 64-byte swizzle; [k][x]: EXT / 64 chunks of 32 rows of 128 bytes, 128-byte swizzle.
-template <int EXT>
+template <int EXT, int TEAM>
 struct Operand {
   static constexpr int kRaw = EXT * 128, kPlane = EXT * 64;
-  static constexpr int kUnits = EXT * 4 / kSplitters;  // of 8 values, per thread and piece
+  static constexpr int kUnits = EXT * 4 / TEAM;  // of 8 values, per thread and piece
   const float* p;
   int64_t ld, ext, k;
   bool mn;
@@ -103,66 +124,80 @@ struct Operand {
     else
       for (int c = 0; c < EXT; c += 32) tc::tma_load_2d(dst + c * 128, map, (int)x0 + c, kb * kTileK, full);
   }
-  // and by the splitters, a word per thread at a time: rows outside of the matrix are left as they are
+  // and by a team of splitters, a word per thread at a time, neighbouring threads along a row; rows outside of
+  // the matrix are left as they are, k outside of it becomes zero
   __device__ __forceinline__ void copy_words(int tid, int64_t x0, int kb, uint32_t dst) const {
-    const int lane = tid & 31;
+    constexpr int kWarps = TEAM / 32;
+    const int lane = tid & 31, w = tid >> 5;
     const int64_t k0 = (int64_t)kb * kTileK;
+    // rows w, w + kWarps, ...: their swizzle has at most two forms
+    uint32_t at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) at[h] = dst + w * 128 + (((lane >> 2) ^ ((w + kWarps * h) & 7)) << 4) + (lane & 3) * 4;
+    const int64_t step = ld * kWarps;
     if (!mn) {
       const bool in = k0 + lane < k;
-      const float* src = p + x0 * ld + k0 + lane;
-#pragma unroll 4
-      for (int r = tid >> 5; r < EXT; r += kSplitWarps) {
-        if (x0 + r >= ext) break;
-        copy_word(dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4, in ? src + r * ld : p, in);
-      }
+      const float* src = in ? p + (x0 + w) * ld + k0 + lane : p;
+      const int64_t by = in ? step : 0;
+      const int rows = (int)min((int64_t)EXT, ext - x0) - w;
+#pragma unroll 8
+      for (int t = 0; t < EXT / kWarps; ++t, src += by)
+        if (t * kWarps < rows) copy_word(at[t & 1] + t * (kWarps * 128), src, in);
     } else {
-#pragma unroll 4
-      for (int i = tid >> 5; i < EXT; i += kSplitWarps) {
-        const int r = i & 31, c = i & ~31;  // row of k, first column of the box
-        const bool in = k0 + r < k && x0 + c + lane < ext;
-        copy_word(dst + c * 128 + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4,
-                  in ? p + (k0 + r) * ld + x0 + c + lane : p, in);
+      const int rows = (int)min((int64_t)32, k - k0) - w;
+      for (int c = 0; c < EXT && x0 + c < ext; c += 32) {
+        const bool ci = x0 + c + lane < ext;
+        const float* src = ci ? p + (k0 + w) * ld + x0 + c + lane : p;
+        const int64_t by = ci ? step : 0;
+#pragma unroll
+        for (int t = 0; t < 32 / kWarps; ++t, src += by) {
+          const bool in = t * kWarps < rows;
+          copy_word(at[t & 1] + c * 128 + t * (kWarps * 128), in ? src : p, in && ci);
+        }
       }
     }
   }
   // this thread's units of a raw piece, split: 8 values to 16 bytes in each of three planes
   __device__ __forceinline__ void split(int tid, const unsigned char* raw, unsigned char* parts) const {
+    // unit i lies a fixed distance from unit 0: the swizzles repeat every 8 rows
+    int from, to, from_step, to_step;
+    bool swap = false;
+    if (!mn) {
+      const int x = tid >> 2, u = tid & 3;
+      from = x * 128 + (((2 * u) ^ (x & 7)) << 4);
+      to = x * 64 + ((u ^ (x >> 1 & 3)) << 4);
+      from_step = TEAM / 4 * 128, to_step = TEAM / 4 * 64;
+    } else {
+      const int u = tid % (EXT / 8), r = tid / (EXT / 8), v = 2 * (u & 3);
+      from = (u >> 2) * 4096 + r * 128 + ((v ^ (r & 7)) << 4);
+      to = (u >> 3) * 4096 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+      from_step = to_step = TEAM / (EXT / 8) * 128;
+      swap = u >> 2 & 1;  // neighbouring boxes read their two halves in opposite order: distinct banks
+    }
+    float4 f[kUnits][2];
+    const int first = swap ? from ^ 16 : from;  // the two halves differ in the unit's lowest bit
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int j = tid + i * kSplitters;
-      int from0, from1, to;
-      if (!mn) {
-        const int x = j >> 2, u = j & 3;
-        from0 = x * 128 + (((2 * u) ^ (x & 7)) << 4);
-        from1 = x * 128 + (((2 * u + 1) ^ (x & 7)) << 4);
-        to = x * 64 + ((u ^ (x >> 1 & 3)) << 4);
-      } else {
-        const int u = j % (EXT / 8), r = j / (EXT / 8);
-        const int at = (u >> 2) * 4096 + r * 128, v = 2 * (u & 3);
-        from0 = at + ((v ^ (r & 7)) << 4);
-        from1 = at + (((v + 1) ^ (r & 7)) << 4);
-        to = (u >> 3) * 4096 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-      }
-      float f[8];
-      // neighbouring boxes read their two halves in opposite order: distinct banks
-      const bool swap = mn && ((j % (EXT / 8)) >> 2 & 1);
-      const float4 s = *reinterpret_cast<const float4*>(raw + (swap ? from1 : from0));
-      const float4 t = *reinterpret_cast<const float4*>(raw + (swap ? from0 : from1));
-      const float4 lo = swap ? t : s, hi = swap ? s : t;
-      f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w, f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
+      f[i][0] = *reinterpret_cast<const float4*>(raw + first + i * from_step);
+      f[i][1] = *reinterpret_cast<const float4*>(raw + (first ^ 16) + i * from_step);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const float4 lo = swap ? f[i][1] : f[i][0], hi = swap ? f[i][0] : f[i][1];
+      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
         uint4 o;
         uint32_t* w = &o.x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+          w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
           if (q < 2) {
-            f[2 * e] -= bf16_lo(w[e]);  // exact: what the rounding left
-            f[2 * e + 1] -= bf16_hi(w[e]);
+            v[2 * e] -= bf16_lo(w[e]);  // exact: what the rounding left
+            v[2 * e + 1] -= bf16_hi(w[e]);
           }
         }
-        *reinterpret_cast<uint4*>(parts + q * kPlane + to) = o;
+        *reinterpret_cast<uint4*>(parts + q * kPlane + to + i * to_step) = o;
       }
     }
   }
@@ -187,13 +222,25 @@ __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int to
   }
 }
 
-template <int BN>
+template <int ACT>
+__device__ __forceinline__ void activate(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], ACT);
+}
+
+// GROUPS: the splitters work as one or two teams that take the pieces in turn.  Two hide a team's latency
+// behind the other's, but each wants two raw buffers of its own.
+template <int BN, int GROUPS>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__ Args p) {
-  using OpA = Operand<kTileM>;
-  using OpB = Operand<BN>;
+  constexpr int TEAM = kSplitters / GROUPS;
+  static_assert(kStages % GROUPS == 0, "stages per team");
+  using OpA = Operand<kTileM, TEAM>;
+  using OpB = Operand<BN, TEAM>;
   constexpr int kAPlane = OpA::kPlane, kBPlane = OpB::kPlane;
   constexpr int kABytes = 3 * kAPlane, kBBytes = 3 * kBPlane;
-  constexpr int kTmem = BN * 4;  // two accumulators of two chunks of k
+  // Accumulators of a chunk of k, two chunks in flight: a0 b0, and one (128 columns) or two (64 columns) for the
+  // smaller pairs
+  constexpr int kAccs = BN == 64 ? 3 : 2, kTmem = 512;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
@@ -203,21 +250,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
   unsigned char* raws = ring + stage_bytes * kStages;
   const int raw_bytes = OpA::kRaw + (p.resident ? 0 : OpB::kRaw);
   unsigned char* epi = raws + raw_bytes * p.raws;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
   const bool a_words = !p.a_tma, b_words = !p.b_tma && !p.resident;
   const bool words = a_words || b_words;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.raws; ++s) {
-      tc::mbar_init(bar(ctl.raw_full[s]), 1 + (words ? kSplitters : 0));
-      tc::mbar_init(bar(ctl.raw_empty[s]), kSplitWarps);
+      tc::mbar_init(bar(ctl.raw_full[s]), 1 + (words ? TEAM : 0));
+      tc::mbar_init(bar(ctl.raw_empty[s]), TEAM / 32);
     }
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(bar(ctl.full[s]), kSplitWarps);
+      tc::mbar_init(bar(ctl.full[s]), TEAM / 32);
       tc::mbar_init(bar(ctl.empty[s]), 1);
     }
     tc::mbar_init(bar(ctl.resident), kSplitWarps);
     tc::mbar_init(bar(ctl.drain), 1);
+    for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(bar(ctl.res[i]), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(ctl.acc_full[i]), 1);
       tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps);
@@ -237,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
 
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ raw copies by TMA
-    if (lane == 0 && !p.drop) {
+    if (!p.drop) {
       Cursor c;
       c.t = blockIdx.x;
       seek(p, BN, c, total);
@@ -246,13 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       uint32_t parity = 1;
       bool ok = true;
       while (c.t < total) {
-        ok = tc::mbar_wait(bar(ctl.raw_empty[s]), parity, g);
+        ok = tc::mbar_wait_warp(bar(ctl.raw_empty[s]), parity, g);
         if (!ok) break;
-        const uint32_t dst = tc::smem_addr(raws) + raw_bytes * s, full = bar(ctl.raw_full[s]);
-        if (bytes) tc::mbar_expect_tx(full, bytes);
-        else tc::mbar_arrive(full);
-        if (p.a_tma) a.copy_tma(&p.map_a, c.m0, c.kb, dst, full);
-        if (p.b_tma && !p.resident) b.copy_tma(&p.map_b, c.n0, c.kb, dst + OpA::kRaw, full);
+        if (tc::elect_one()) {
+          const uint32_t dst = tc::smem_addr(raws) + raw_bytes * s, full = bar(ctl.raw_full[s]);
+          if (bytes) tc::mbar_expect_tx(full, bytes);
+          else tc::mbar_arrive(full);
+          if (p.a_tma) a.copy_tma(&p.map_a, c.m0, c.kb, dst, full);
+          if (p.b_tma && !p.resident) b.copy_tma(&p.map_b, c.n0, c.kb, dst + OpA::kRaw, full);
+        }
+        __syncwarp();
         advance(p, BN, c, total);
         ++it;
         if (++s == p.raws) s = 0, parity ^= 1;
@@ -264,71 +315,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
     }
   } else if (warp >= kEpiWarps && warp < kEpiWarps + kSplitWarps) {
     // ------------------------------------------------------------ splitters
-    const int tid = threadIdx.x - 32 * kEpiWarps;
+    const int group = (warp - kEpiWarps) / (TEAM / 32), tid = (threadIdx.x - 32 * kEpiWarps) % TEAM;
     if (!p.drop) {
       if (p.resident && (int)blockIdx.x < total) {
         // B's parts, once, its words a piece at a time through the room of the epilogue, which waits for it
         const int64_t n0 = (int64_t)(blockIdx.x % p.n_tiles) * BN;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          unsigned char* to = res_b + kBBytes * kb;
-          b.copy_words(tid, n0, kb, tc::smem_addr(epi));
+        unsigned char* room = epi + group * OpB::kRaw;
+        for (int kb = group; kb < p.kblocks; kb += GROUPS) {
+          b.copy_words(tid, n0, kb, tc::smem_addr(room));
           asm volatile("cp.async.wait_all;" ::: "memory");
-          asm volatile("bar.sync 1, %0;" ::"n"(kSplitters) : "memory");
-          b.split(tid, epi, to);
-          asm volatile("bar.sync 1, %0;" ::"n"(kSplitters) : "memory");
+          team_sync<TEAM>(group);
+          b.split(tid, room, res_b + kBBytes * kb);
+          team_sync<TEAM>(group);
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.resident));
       }
+      // a place in a ring that this group's pieces take GROUPS further each time
+      struct Ring {
+        int s;
+        uint32_t parity;
+        __device__ __forceinline__ void step(int n, int size) {
+          s += n;
+          while (s >= size) s -= size, parity ^= 1;
+        }
+      };
       Cursor cur;
       cur.t = blockIdx.x;
       seek(p, BN, cur, total);
+      Ring from{0, 0}, to{0, 1}, next{0, 1};
+      auto skip = [&](Cursor& c, int n) {
+        for (int i = 0; i < n && c.t < total; ++i) advance(p, BN, c, total);
+      };
+      skip(cur, group);
+      from.step(group, p.raws), to.step(group, kStages), next.step(group, p.raws);
       Cursor ahead = cur;
-      int ahead_s = 0;
-      uint32_t ahead_parity = 1;
       bool ok = true;
       // the next piece's words, when its raw buffer is free; its arrival follows the words
       auto copy_ahead = [&]() {
         if (!words || ahead.t >= total || !ok) return;
-        ok = tc::mbar_wait_warp(bar(ctl.raw_empty[ahead_s]), ahead_parity, g);
+        ok = tc::mbar_wait_warp(bar(ctl.raw_empty[next.s]), next.parity, g);
         if (!ok) return;
-        const uint32_t dst = tc::smem_addr(raws) + raw_bytes * ahead_s;
+        const uint32_t dst = tc::smem_addr(raws) + raw_bytes * next.s;
         if (a_words) a.copy_words(tid, ahead.m0, ahead.kb, dst);
         if (b_words) b.copy_words(tid, ahead.n0, ahead.kb, dst + OpA::kRaw);
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.raw_full[ahead_s])) : "memory");
-        advance(p, BN, ahead, total);
-        if (++ahead_s == p.raws) ahead_s = 0, ahead_parity ^= 1;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(ctl.raw_full[next.s])) : "memory");
+        skip(ahead, GROUPS);
+        next.step(GROUPS, p.raws);
       };
-      for (int i = 0; i + 1 < p.raws; ++i) copy_ahead();
-      int r = 0, s = 0;
-      uint32_t r_parity = 0, s_parity = 1;
+      // its share of the ring, less the piece that is being split
+      for (int i = 0; i < p.raws / GROUPS - 1; ++i) copy_ahead();
       while (cur.t < total) {
         copy_ahead();
-        ok = ok && tc::mbar_wait_warp(bar(ctl.raw_full[r]), r_parity, g);
-        ok = ok && tc::mbar_wait_warp(bar(ctl.empty[s]), s_parity, g);
+        ok = ok && tc::mbar_wait_warp(bar(ctl.raw_full[from.s]), from.parity, g);
+        ok = ok && tc::mbar_wait_warp(bar(ctl.empty[to.s]), to.parity, g);
         if (!ok) break;
-        unsigned char* to = ring + stage_bytes * s;
-        const unsigned char* from = raws + raw_bytes * r;
-        a.split(tid, from, to);
-        if (!p.resident) b.split(tid, from + OpA::kRaw, to + kABytes);
+        unsigned char* st = ring + stage_bytes * to.s;
+        const unsigned char* raw = raws + raw_bytes * from.s;
+        a.split(tid, raw, st);
+        if (!p.resident) b.split(tid, raw + OpA::kRaw, st + kABytes);
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(bar(ctl.raw_empty[r]));
-          tc::mbar_arrive(bar(ctl.full[s]));
+          tc::mbar_arrive(bar(ctl.raw_empty[from.s]));
+          tc::mbar_arrive(bar(ctl.full[to.s]));
         }
-        advance(p, BN, cur, total);
-        if (++r == p.raws) r = 0, r_parity ^= 1;
-        if (++s == kStages) s = 0, s_parity ^= 1;
+        skip(cur, GROUPS);
+        from.step(GROUPS, p.raws), to.step(GROUPS, kStages);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ matrix instructions
-    if (lane == 0) {
+    {
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
                              (uint32_t)(BN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+      constexpr uint32_t kStepN = (uint32_t)(BN >> 3) << 17;  // BN columns more
       // 16 of k further: 32 bytes along a row, or 16 rows of 128 bytes; rows of 64 or of 128 bytes
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
       const uint64_t a_desc = p.a_mn ? tc::smem_desc(0, 4096, 1024) : tc::smem_desc_64(0, 512);
@@ -336,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       int s = 0, n_acc = 0;
       uint32_t parity = 0;
       bool ok = true;
-      if (p.resident && (int)blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
+      if (p.resident && (int)blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
@@ -345,16 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         const int k_hi = min(kb + p.kb_per_split, p.kblocks);
         for (; ok && kb < k_hi; ++n_acc) {  // a chunk of k: one pair of accumulators
           const int acc = n_acc & 1, c_hi = min(kb + kChunk, k_hi);
-          ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+          ok = tc::mbar_wait_warp(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
           if (!ok) break;
           tc::fence_after();
           const uint32_t d = tmem + acc * (kTmem / 2);
           for (bool first = true; kb < c_hi; ++kb, first = false) {
-            ok = tc::mbar_wait(bar(ctl.full[s]), parity, g);
+            ok = tc::mbar_wait_warp(bar(ctl.full[s]), parity, g);
             if (!ok) break;
             tc::fence_after();
             const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
             const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
+            if (tc::elect_one()) {
 #pragma unroll
             for (int i = 0; i < kTileK / 16; ++i) {
               uint64_t da[3], db[3];
@@ -363,51 +427,101 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
                 da[q] = a_desc | ((as + q * kAPlane + i * a_step) & 0x3ffff) >> 4;
                 db[q] = b_desc | ((bs + q * kBPlane + i * b_step) & 0x3ffff) >> 4;
               }
+              // B's parts lie one behind the other, as one operand of up to 256 columns: several pairs per
+              // instruction, and A read from shared memory half as often
               const uint32_t add = !first || i > 0;
-              tc::mma_bf16(d, da[0], db[0], idesc, add);
-              tc::mma_bf16(d + BN, da[0], db[2], idesc, add);
-              tc::mma_bf16(d + BN, da[2], db[0], idesc, 1);
-              tc::mma_bf16(d + BN, da[1], db[1], idesc, 1);
-              tc::mma_bf16(d + BN, da[0], db[1], idesc, 1);
-              tc::mma_bf16(d + BN, da[1], db[0], idesc, 1);
+              if constexpr (BN == 64) {
+                tc::mma_bf16(d, da[0], db[0], idesc + 2 * kStepN, add);           // a0 (b0 b1 b2)
+                tc::mma_bf16(d + BN, da[1], db[0], idesc + kStepN, 1);            // a1 (b0 b1)
+                tc::mma_bf16(d + 2 * BN, da[2], db[0], idesc, 1);                 // a2 b0
+              } else {
+                tc::mma_bf16(d, da[0], db[0], idesc + kStepN, add);               // a0 (b0 b1)
+                tc::mma_bf16(d + BN, da[1], db[0], idesc, 1);
+                tc::mma_bf16(d + BN, da[0], db[2], idesc, 1);
+                tc::mma_bf16(d + BN, da[1], db[1], idesc, 1);
+                tc::mma_bf16(d + BN, da[2], db[0], idesc, 1);
+              }
             }
             tc::mma_commit(bar(ctl.empty[s]));
+            }
+            __syncwarp();
             if (++s == kStages) s = 0, parity ^= 1;
           }
-          if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+          if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
+          __syncwarp();
         }
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
-        tc::mma_commit(bar(ctl.drain));
+        if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
+        __syncwarp();
         for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     constexpr int kCols = BN / 2;  // of this warp: 32 rows x kCols
-    const int quad = warp & 3, half = warp >> 2;
-    float* buf = reinterpret_cast<float*>(epi + warp * kBufBytes);
-    float* res_buf = reinterpret_cast<float*>(epi + (kEpiWarps + warp) * kBufBytes);
-    int n_acc = 0;
+    constexpr int kLoad = BN == 64 ? 32 : 8;  // columns per read of an accumulator: what the registers hold
+    const int quad = warp & 3, half = warp >> 2, n = (int)p.n, m = (int)p.m;  // below 2^31
+    // y, the residual, z: 32 KB each, 8 KB for the two warps that share 32 rows, 4 KB of it for this one
+    unsigned char* const y_buf = epi + quad * (2 * kBufBytes);
+    unsigned char* const r_buf = y_buf + kEpiWarps * kBufBytes;
+    // (z and the residual: tiles of 64 columns only)
+    unsigned char* const z_buf = r_buf + (p.residual ? kEpiWarps * kBufBytes : 0);
+    const bool with_res = BN == 64 && p.residual && !p.part;
+    const bool dense = BN == 64 && !p.part && (p.y_way == kDense || (p.z && p.z_way == kDense) || (with_res && p.r_way == kDense));
+    const uint32_t res_bar = bar(ctl.res[with_res && p.r_way == kDense ? quad : warp]);
+    auto quad_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(4 + quad) : "memory"); };
+    int n_acc = 0, res_used = 0;
+    bool res_flying = false;
     bool ok = true;
     if (p.resident && (int)blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    // this warp's piece of tile t
+    auto place = [&](int t, uint32_t& row0, uint32_t& col0, int& split) {
       int64_t m0, n0;
-      int split;
       tile_of(p, BN, t, m0, n0, split);
+      row0 = (uint32_t)m0 + quad * 32;
+      col0 = (uint32_t)n0 + half * kCols;
+    };
+    // the residual of tile t on its way to the buffer, while the tile before is written
+    auto ask_residual = [&](int t) {
+      if (t >= total) return;
+      uint32_t row0, col0;
+      int split;
+      place(t, row0, col0, split);
+      const int rows = min(32, (int)((int64_t)m - row0));
+      if (rows <= 0) return;
+      if (BN == 64 && p.r_way == kDense) {
+        if (rows < 32) return;  // read where it is used
+        if (half == 0 && tc::elect_one()) {
+          tc::mbar_expect_tx(res_bar, 128 * n);
+          tc::bulk_load(tc::smem_addr(r_buf), p.residual + (int64_t)row0 * n, 128 * n, res_bar);
+        }
+        res_flying = true;
+      } else if (col0 < (uint32_t)n) {
+        if (p.r_way == kBox) {
+          if (tc::elect_one()) {
+            tc::mbar_expect_tx(res_bar, kBufBytes);
+            tc::tma_load_2d(tc::smem_addr(r_buf) + half * kBufBytes, &p.map_r, (int)col0, (int)row0, res_bar);
+          }
+          res_flying = true;
+        } else if (col0 + lane < (uint32_t)n) {
+          const float* src = p.residual + (int64_t)row0 * p.ldr + col0 + lane;
+          const uint32_t dst = tc::smem_addr(r_buf) + half * kBufBytes;
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r, src += p.ldr)
+            if (r < rows) copy_word(dst + r * 128 + (lane ^ r) * 4, src, true);
+        }
+      }
+      __syncwarp();
+    };
+    if (with_res && ok) ask_residual(blockIdx.x);
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      uint32_t row0, col0;
+      int split;
+      place(t, row0, col0, split);
       const int k_lo = split * p.kb_per_split, k_hi = min(k_lo + p.kb_per_split, p.kblocks);
-      const int64_t row0 = m0 + quad * 32, col0 = n0 + half * kCols;
-      const bool in = row0 < p.m && col0 < (p.part ? p.ldp : p.n);
-      const int rows = (int)min((int64_t)32, p.m - row0);
-      // the residual of 32 columns from c on, a column per lane
-      auto copy_residual = [&](int c) {
-        const bool ci = col0 + c + lane < p.n;
-        const float* src = p.residual + row0 * p.ldr + col0 + c + lane;
-        const uint32_t dst = tc::smem_addr(res_buf) + lane * 4;
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) copy_word(dst + r * (kPitch * 4), ci ? src + r * p.ldr : p.residual, ci);
-      };
-      if (in && !p.part && p.residual) copy_residual(0);
+      const bool in = row0 < (uint32_t)m && (dense || col0 < (uint32_t)(p.part ? p.ldp : n));
+      const int rows = min(32, (int)((int64_t)m - row0));
       float sum[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
@@ -419,64 +533,146 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         const uint32_t d = tmem + acc * (kTmem / 2) + ((uint32_t)(quad * 32) << 16) + half * kCols;
         if (in) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 8) {
-            float v[8];
-            tc::tmem_load8(d + BN + c, v);
+          for (int c = 0; c < kCols; c += kLoad) {
+            float v[kLoad];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
-            tc::tmem_load8(d + c, v);
+            for (int q = kAccs - 1; q >= 0; --q) {
+              tc::tmem_load<kLoad>(d + q * BN + c, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[c + i] += v[i];
+              for (int i = 0; i < kLoad; ++i) sum[c + i] += v[i];
+            }
           }
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
       }
-      if (!ok || !in) continue;
+      if (!ok) break;
+      if (!in) {
+        if (with_res) ask_residual(t + gridDim.x);
+        continue;
+      }
       if (p.part) {
         const int64_t row = row0 + lane;
-        if (row < p.m) {
-          float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + col0;
+        if (row < m) {
+          float* out = p.part + ((int64_t)split * m + row) * p.ldp + col0;
 #pragma unroll
           for (int c = 0; c < kCols; c += 4)
             if (col0 + c < p.ldp) *reinterpret_cast<float4*>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
         }
         continue;
       }
+      // a piece v (a lane: 32 columns of a row) through a buffer to its array
+      auto write_piece = [&](const float* v, int way, unsigned char* b8, const CUtensorMap* map, float* out, int64_t ld, int c) {
+        float* b = reinterpret_cast<float*>(b8 + half * kBufBytes);
+        if (way == kBox) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(b) + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          tc::fence_async_smem();
+          __syncwarp();
+          if (col0 + c < (uint32_t)n && tc::elect_one()) {
+            tc::tma_store_2d(map, (int)col0 + c, (int)row0, tc::smem_addr(b));
+            tc::bulk_commit();
+          }
+          __syncwarp();
+        } else if (BN == 64 && way == kDense) {
+          float* d = reinterpret_cast<float*>(b8) + lane * n + half * 32;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (half * 32 + i < n) d[i] = v[i];
+          tc::fence_async_smem();
+          quad_sync();
+          out += (int64_t)row0 * n;
+          if (rows == 32) {
+            if (half == 0 && tc::elect_one()) {
+              tc::bulk_store(out, tc::smem_addr(b8), 128 * n);
+              tc::bulk_commit();
+            }
+            __syncwarp();
+          } else {
+            for (int e = half * 32 + lane; e < rows * n; e += 64) out[e] = reinterpret_cast<const float*>(b8)[e];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) b[lane * 32 + (i ^ lane)] = v[i];
+          __syncwarp();
+          if (col0 + c + lane < (uint32_t)n) {
+            out += (int64_t)row0 * ld + col0 + c + lane;
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r, out += ld)
+              if (r < rows) *out = b[r * 32 + (lane ^ r)];
+          }
+          __syncwarp();
+        }
+      };
 #pragma unroll
       for (int c = 0; c < kCols; c += 32) {
-        const int64_t col = col0 + c + lane;
-        const bool ci = col < p.n;
-        const float bias = p.bias && ci ? p.bias[col] : 0.f;
-        __syncwarp();
+        if (col0 + c >= (uint32_t)n && !dense) break;
+        // stores of the last piece have read the buffers; a bulk store is its issuer's to wait for, and the
+        // same lane of a warp issues all of that warp's
+        if (tc::elect_one()) tc::bulk_wait_read0();
+        if (dense) quad_sync();
+        else __syncwarp();
+        float* v = sum + c;
+        if (p.bias) {
+          const float bias = col0 + c + lane < (uint32_t)n ? p.bias[col0 + c + lane] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = sum[c + i] + __shfl_sync(0xffffffffu, bias, i);
-        __syncwarp();
-        // a lane owns a column; short separate loops keep the sums of the other pieces in registers
-        if (ci && (p.act != GS_ACT_NONE || p.z)) {
-          float* z = p.z + row0 * p.ldz + col;
-#pragma unroll 1
-          for (int r = 0; r < rows; ++r) {
-            const float v = buf[r * kPitch + lane];
-            if (p.z) z[r * p.ldz] = v;
-            buf[r * kPitch + lane] = act_value(v, p.act);
+          for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+        }
+        if (BN == 64 && p.z) write_piece(v, p.z_way, z_buf, &p.map_z, p.z, p.ldz, c);
+        if (p.act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
+        else if (p.act == GS_ACT_GELU) activate<GS_ACT_GELU>(v);
+        else if (p.act == GS_ACT_SILU) activate<GS_ACT_SILU>(v);
+        if (with_res) {
+          const float* b = reinterpret_cast<const float*>(r_buf + half * kBufBytes);
+          if (p.r_way == kDense && rows < 32) {
+            const float* src = p.residual + (int64_t)(row0 + lane) * n + col0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (lane < rows && col0 + i < (uint32_t)n) v[i] += src[i];
+          } else {
+            if (p.r_way == kPlain) {
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] += b[lane * 32 + (i ^ lane)];
+            } else {
+              if (p.r_way == kDense || col0 < (uint32_t)n) {
+                ok = tc::mbar_wait_warp(res_bar, (uint32_t)(res_used & 1), g);
+                if (!ok) break;
+                ++res_used;
+                res_flying = false;
+              }
+              if (p.r_way == kDense) {
+                const float* d = reinterpret_cast<const float*>(r_buf) + lane * n + half * 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (half * 32 + i < n) v[i] += d[i];
+              } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  const float4 f = *reinterpret_cast<const float4*>(reinterpret_cast<const unsigned char*>(b) + lane * 128 +
+                                                                    ((q ^ (lane & 7)) << 4));
+                  v[4 * q] += f.x, v[4 * q + 1] += f.y, v[4 * q + 2] += f.z, v[4 * q + 3] += f.w;
+                }
+              }
+            }
           }
+          tc::fence_async_smem();  // the reads above come before the next copy into the buffer
+          if (dense) quad_sync();
+          else __syncwarp();
+          ask_residual(t + gridDim.x);
         }
-        if (p.residual) {  // a lane reads the words that it copied itself
-          asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r) buf[r * kPitch + lane] += res_buf[r * kPitch + lane];
-          if (c + 32 < kCols) copy_residual(c + 32);
-        }
-        if (ci) {
-          float* y = p.y + row0 * p.ldy + col;
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r) y[r * p.ldy] = buf[r * kPitch + lane];
-        }
+        write_piece(v, p.y_way, y_buf, &p.map_y, p.y, p.ldy, c);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok)  // gave up: the copies in flight land before the block ends
+      if (res_flying)
+        for (int j = 0; j < p.wait_limit && !tc::mbar_try(res_bar, (uint32_t)(res_used & 1)); ++j) {}
+    if (tc::elect_one()) tc::bulk_wait0();
   }
   __syncwarp();
   tc::fence_before();
@@ -513,28 +709,49 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-template <int BN>
-gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
-  constexpr int kA = 3 * Operand<kTileM>::kPlane, kB = 3 * Operand<BN>::kPlane;
+// The shared memory of a launch: bytes of everything but the raw buffers, and how many of those fit.
+struct Room {
+  int fixed, raw, raws;
+};
+Room room_of(const Plan& pl, bool resident, int bufs) {
+  const int a = 3 * kTileM * 64, b = 3 * pl.bn * 64;  // bytes of a block's parts
+  Room r;
+  r.fixed = 1024 + kSmemCtl + kEpiWarps * kBufBytes * bufs;
+  const int64_t parts = resident ? (int64_t)b * pl.kblocks + kStages * a : kStages * (a + b);
+  r.raw = kTileM * 128 + (resident ? 0 : pl.bn * 128);
+  if (parts > kSmemMost - r.fixed) return {0, 0, 0};
+  r.fixed += (int)parts;
+  r.raws = (kSmemMost - r.fixed) / r.raw;
+  if (r.raws > kMaxRaw) r.raws = kMaxRaw;
+  return r;
+}
+
+template <int BN, int GROUPS>
+gs_status launch(Args& p, const Room& r, int grid, cudaStream_t st, const char* where) {
+  // every team of splitters has raw buffers of its own: a wait for a buffer's next phase is then always made
+  // by those who have seen the phase before it, as the phases' one bit of parity demands
+  p.raws = r.raws - r.raws % GROUPS;
+  if (p.raws < GROUPS) return gs::set_error(GS_ERR_INVALID, "%s: no room for raw buffers", where);
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_f32<BN, GROUPS>, kSmemMost);
+  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  k_mma_f32<BN, GROUPS><<<grid, kThreads, r.fixed + p.raws * r.raw, st>>>(p);
+  return gs::check_launch(where);
+}
+
+gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
   const int total = pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = total < gs::num_sms() ? total : gs::num_sms();
-  const int epi = kEpiWarps * kBufBytes * (p.residual && !p.part ? 2 : 1);
-  const int room = kSmemMost - 1024 - kSmemCtl - epi;
-  // resident B: one range of columns per block, and at least three raw buffers of A beside it
-  if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid &&
-      (int64_t)kB * pl.kblocks + kStages * kA + 3 * Operand<kTileM>::kRaw <= room) {
+  const int bufs = p.part ? 1 : 1 + (p.residual != nullptr) + (p.z != nullptr);
+  Room r = room_of(pl, true, bufs);
+  // resident B: one range of columns per block, and three raw buffers of A beside it
+  if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && r.raws >= 3) {
     p.resident = 1;
     grid -= grid % pl.n_tiles;
+  } else {
+    r = room_of(pl, false, bufs);
   }
-  const int fixed = p.resident ? kB * pl.kblocks + kStages * kA : kStages * (kA + kB);
-  const int raw = Operand<kTileM>::kRaw + (p.resident ? 0 : Operand<BN>::kRaw);
-  const int raws = (room - fixed) / raw;
-  p.raws = raws < kMaxRaw ? raws : kMaxRaw;
-  const int smem = kSmemMost - room + fixed + p.raws * raw;
-  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_f32<BN>, kSmemMost);
-  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  k_mma_f32<BN><<<grid, kThreads, smem, st>>>(p);
-  return gs::check_launch(where);
+  if (pl.bn == 128) return launch<128, 1>(p, r, grid, st, where);
+  return r.raws >= 4 ? launch<64, 2>(p, r, grid, st, where) : launch<64, 1>(p, r, grid, st, where);
 }
 
 }  // namespace
@@ -547,7 +764,11 @@ size_t f32_workspace(int64_t m, int64_t n, int64_t k) {
 }
 
 gs_status f32_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
-  const Plan pl = plan_of(q.m, q.n, q.k);
+  Plan pl = plan_of(q.m, q.n, q.k);
+  if (pl.bn == 128 && pl.splits == 1 && (q.residual || q.z)) {  // their buffers and registers leave no room for 128 columns
+    pl.bn = 64;
+    pl.n_tiles = (int)ceil_div(q.n, 64);
+  }
   if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff) return set_error(GS_ERR_INVALID, "%s: too many tiles", where);
   Args p{};
   p.a = static_cast<const float*>(q.a), p.b = static_cast<const float*>(q.b), p.lda = q.lda, p.ldb = q.ldb;
@@ -569,8 +790,22 @@ gs_status f32_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   p.act = q.act;
   p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   p.ldp = pl.ldp;
+  if (!p.part) {
+    auto way = [&](const void* at, int64_t ld, CUtensorMap* map, int& w) {
+      w = kPlain;
+      if (!at) return true;
+      if (rows_aligned16(at, q.m, ld, GS_F32)) {
+        w = kBox;
+        return encode_map(map, at, q.m, q.n, ld, 32, GS_F32);
+      }
+      if (pl.bn == 64 && pl.n_tiles == 1 && ld == q.n && aligned16(at)) w = kDense;
+      return true;
+    };
+    if (!way(q.y, q.ldy, &p.map_y, p.y_way) || !way(q.z, q.ldz, &p.map_z, p.z_way) || !way(q.residual, q.ldr, &p.map_r, p.r_way))
+      return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
+  }
   p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
-  if (gs_status s = pl.bn == 64 ? launch<64>(p, pl, st, where) : launch<128>(p, pl, st, where)) return s;
+  if (gs_status s = launch_any(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
               st);

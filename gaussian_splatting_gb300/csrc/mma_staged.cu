@@ -55,10 +55,18 @@ struct Args {
 };
 
 __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m0, int64_t& n0, int& split) {
-  const int nt = t % p.n_tiles, rest = t / p.n_tiles;
+  int nt = 0, mt = t;
+  split = 0;
+  if (p.n_tiles > 1) {
+    mt = t / p.n_tiles;
+    nt = t - mt * p.n_tiles;
+  }
+  if (p.splits > 1) {
+    split = mt / p.m_tiles;
+    mt -= split * p.m_tiles;
+  }
   n0 = (int64_t)nt * bn;
-  m0 = (int64_t)(rest % p.m_tiles) * kTileM;
-  split = rest / p.m_tiles;
+  m0 = (int64_t)mt * kTileM;
 }
 
 // 8 consecutive elements at p, those at or past `left` as zeros
@@ -74,7 +82,7 @@ __device__ __forceinline__ uint4 load8(const bf16* p, int64_t left, bool vec) {
 // One operand as the loaders see it: pieces of EXT (m or n) x 16 (one step of the tensor core), a unit
 // of 8 elements per thread.
 constexpr int kPieces = kTileK / 16;  // of a k block
-constexpr int kDepth = 4;             // pieces of a thread in registers, all but one of them in flight
+constexpr int kDepth = 3;             // pieces of a thread in registers, all but one of them in flight
 
 template <int EXT>
 struct Operand {
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
   unsigned char* ring = res_b + (p.resident ? (size_t)kBBytes * p.kblocks : 0);
   const int stage_bytes = kABytes + (p.resident ? 0 : kBBytes);
   unsigned char* epi = ring + (size_t)stage_bytes * p.stages;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -229,13 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
     }
   } else if (warp == kEpiWarps + kLoadWarps) {
     // ------------------------------------------------------------ matrix instructions
-    if (lane == 0) {
+    {
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
                              (uint32_t)(BN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
       int it = 0, n_acc = 0;
       bool ok = true;
-      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait(bar(ctl.resident), 0, g);
+      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
@@ -243,28 +251,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
         int kb = split * p.kb_per_split;
         const int k_hi = min(kb + p.kb_per_split, p.kblocks);
         const int acc = n_acc & 1;
-        ok = tc::mbar_wait(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
+        ok = tc::mbar_wait_warp(bar(ctl.acc_empty[acc]), (uint32_t)(n_acc >> 1 & 1) ^ 1, g);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + acc * BN;
         for (bool first = true; kb < k_hi; ++kb, ++it, first = false) {
           const int s = it % p.stages;
-          ok = tc::mbar_wait(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
+          ok = tc::mbar_wait_warp(bar(ctl.full[s]), (uint32_t)(it / p.stages & 1), g);
           if (!ok) break;
           tc::fence_after();
           const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
           const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kTileK / 16; ++i)
+            for (int i = 0; i < kTileK / 16; ++i)
             tc::mma_bf16(d, tc::smem_desc(as + i * a_step, kTileK * 128, 1024), tc::smem_desc(bs + i * b_step, kTileK * 128, 1024),
                          idesc, !first || i > 0);
-          tc::mma_commit(bar(ctl.empty[s]));
+            tc::mma_commit(bar(ctl.empty[s]));
+          }
+          __syncwarp();
         }
-        if (ok) tc::mma_commit(bar(ctl.acc_full[acc]));
+        if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
+        __syncwarp();
         ++n_acc;
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
-        tc::mma_commit(bar(ctl.drain));
+        if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
+        __syncwarp();
         for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
       }
     }
@@ -314,15 +327,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
         const bf16* res = p.residual + row0 * p.ldr + col;
         bf16* y = p.y + row0 * p.ldy + col;
         bf16* z = p.z + row0 * p.ldz + col;
-        for (int r0 = 0; r0 < rows; r0 += 16) {
-          bf16 rr[16];  // loads in flight
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          bf16 rr[8];  // loads in flight
           if (p.residual) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
+            for (int r = 0; r < 8; ++r)
               if (r0 + r < rows) rr[r] = res[(r0 + r) * p.ldr];
           }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < 8; ++r) {
             if (r0 + r >= rows) break;
             float v = buf[(r0 + r) * kPitch + lane] + bias;
             if (p.z) z[(r0 + r) * p.ldz] = __float2bfloat16_rn(v);
