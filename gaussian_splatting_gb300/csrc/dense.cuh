@@ -142,7 +142,8 @@ __device__ __forceinline__ float act_slope(float v, int act) {
 }
 
 // ------------------------------------------------------------------ folds of split sums
-// The splits' parts [splits][m][ldp] (32-bit sums) added in order, then z = sum + bias, y = act(z) + residual.
+// The splits' parts [splits][m][ldp] (32-bit sums) added in order, then z = sum + bias, y = act(z) + residual;
+// `transposed`: the parts hold the transpose of what is written.
 // A block takes 128 neighbouring sums; WAYS warps each add every WAYS-th split of them, four a lane, and
 // the warps' sums are added in order.
 template <typename T>
@@ -154,6 +155,7 @@ struct FoldArgs {
   T* z;
   int64_t m, ldp, ldr, ldy, ldz;
   int splits, n, act;
+  bool transposed;
 };
 template <typename T, int WAYS>
 __global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
@@ -174,9 +176,12 @@ __global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
   for (int e = threadIdx.x; e < kGroups * 128; e += 256) {
     const int64_t i = (int64_t)blockIdx.x * kGroups * 128 + e;
     if (i >= size) break;
-    const int64_t row = i / a.ldp;
-    const int col = (int)(i % a.ldp);
+    int64_t row = i / a.ldp, col = i % a.ldp;
     if (col >= a.n) continue;
+    if (a.transposed) {
+      const int64_t r = row;
+      row = col, col = r;
+    }
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < WAYS; ++w) t += reinterpret_cast<const float*>(s[e / 128 * WAYS + w])[e % 128];

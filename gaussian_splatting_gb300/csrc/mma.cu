@@ -3,14 +3,15 @@
 // C(m, n) = sum over k of A(m, k) B(n, k), 32-bit sums, then z = C + bias, y = act(z) + residual.
 // One persistent block per SM walks over 128 x BN tiles of C (BN = 64 .. 256, and ranges of k where
 // there are few tiles).  Its warps work as a pipeline:
-//   warp 8        issues TMA copies of 128 x 64 (A) and BN x 64 (B) pieces into a ring of shared-memory
+//   warp 16       issues TMA copies of 128 x 64 (A) and BN x 64 (B) pieces into a ring of shared-memory
 //                 stages (128-byte swizzle).  An operand stored along its other axis ([k][m]) is copied
 //                 as 64 x 64 boxes and handed to the tensor core as it lies: no transpose.  B stays
 //                 resident where all of its k fits: the weights are then read once per block.
-//   warp 9        issues tcgen05.mma, 128 x BN x 16 each, into one of two accumulators in TMEM
-//   warps 0 - 7   read the finished accumulator, 32 rows x 128 bytes of columns at a time, and write it
-//                 through shared memory with TMA stores (or, where rows do not start on 16-byte
-//                 boundaries, with plain coalesced stores) while the next tile is being summed
+//   warp 17       issues tcgen05.mma, 128 x BN x 16 each, into one of two accumulators in TMEM
+//   warps 0 - 15  read the finished accumulator in pieces of 32 rows x 32 columns and write them through
+//                 shared memory with TMA stores while the next tile is being summed; the residual's piece
+//                 is copied in one piece ahead.  The epilogue is latency: with eight warps it took longer
+//                 than the products (16,384 x 1024 -> 4096 with GELU and z: 114 us, the products alone 82)
 // Every wait is bounded (see tc::Guard).
 #include <cuda.h>
 
@@ -23,13 +24,15 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;         // four to a quadrant of 32 rows
+constexpr int kParts = kEpiWarps / 4;  // which take its pieces of 32 columns in turn
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kTileM = 128, kTileK = 64;
 constexpr int kMaxStages = 8;
 constexpr int kABytes = kTileM * kTileK * 2;
-constexpr int kBufBytes = 32 * 128;   // one warp's 32 rows x 128 bytes
-constexpr int kBufCols = 64;          // columns of one such buffer
+constexpr int kBufCols = 32;          // columns of one warp's piece
+constexpr int kBufBytes = 32 * 64;    // and its bytes: 32 rows of 64, 64-byte swizzle
 constexpr int kSmemMost = 232448;     // 227 KB
 constexpr int kSmemCtl = 1024;        // barriers, TMEM address, dead flag
 
@@ -77,13 +80,16 @@ __device__ __forceinline__ void epilogue8(const float* v, const float* bias, con
 struct EpiState {
   uint32_t buf;        // this warp's buffers in shared memory (address)
   unsigned char* ptr;  // the same, generic
-  float* bias;         // 64 floats of this warp
+  bf16* bias;          // 32 values of this warp's own
   uint32_t res_bar;
   uint32_t loads, issued;  // residual pieces waited for and asked for so far
-  int lane, quad, half;
+  int lane, quad, part;
+  int rank, step;      // of the block in its pair; tiles between two of this pair
 };
 
-__device__ __forceinline__ void tile_of(const Args& p, int t, int64_t& m0, int64_t& n0, int& split) {
+// The tile t of a pair (or, CTAS = 1, a block): the rows of the block of this rank.
+template <int CTAS>
+__device__ __forceinline__ void tile_of(const Args& p, int rank, int t, int64_t& m0, int64_t& n0, int& split) {
   int nt = 0, mt = t;
   split = 0;
   if (p.n_tiles > 1) {
@@ -95,7 +101,7 @@ __device__ __forceinline__ void tile_of(const Args& p, int t, int64_t& m0, int64
     mt -= split * p.m_tiles;
   }
   n0 = (int64_t)nt * p.bn;
-  m0 = (int64_t)mt * kTileM;
+  m0 = ((int64_t)mt * CTAS + rank) * kTileM;
 }
 
 // whether this warp writes anything of chunk c of the tile at (m0, n0)
@@ -103,47 +109,42 @@ __device__ __forceinline__ bool chunk_in(const Args& p, const EpiState& e, int64
   return m0 + e.quad * 32 < p.m && n0 + c * kBufCols < p.n;
 }
 
-template <int ACT>
+template <int CTAS, int ACT>
 __device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, int t, int total, uint32_t tmem,
                               uint32_t acc_full, uint32_t parity) {
   int64_t m0, n0;
   int split;
-  tile_of(p, t, m0, n0, split);
+  tile_of<CTAS>(p, e.rank, t, m0, n0, split);
   bool waited = false;
-  for (int c = e.half; c * kBufCols < p.bn; c += 2) {
+  for (int c = e.part; c * kBufCols < p.bn; c += kParts) {
     const bool in = chunk_in(p, e, m0, n0, c);
     uint32_t slot = 0;
     if (in) {
+      const int64_t col = n0 + c * kBufCols + e.lane;
+      const bf16 bias = p.bias && col < p.n ? p.bias[col] : __float2bfloat16_rn(0.f);
       // every store that reads these buffers is done reading
-      if (e.lane == 0) tc::bulk_wait_read0();
+      if (tc::elect_one()) tc::bulk_wait_read0();
       __syncwarp();
-      const int col = (int)n0 + c * kBufCols;
-      if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t cc = col + e.lane + 32 * i;
-          e.bias[e.lane + 32 * i] = cc < p.n ? __bfloat162float(p.bias[cc]) : 0.f;
-        }
-      }
+      e.bias[e.lane] = bias;
       if (p.has_r) {
         slot = e.loads & 1;
         // the residual piece of the next chunk goes to the other buffer
-        int64_t nm, nn;
+        int64_t nm = 0, nn = 0;
         int t2 = t, c2 = c, s2;
-        c2 += 2;
-        if (c2 * kBufCols >= p.bn) c2 = e.half, t2 += gridDim.x;
-        while (t2 < total) {  // skips the chunks that lie outside of C
-          tile_of(p, t2, nm, nn, s2);
-          if (chunk_in(p, e, nm, nn, c2)) break;
-          c2 += 2;
-          if (c2 * kBufCols >= p.bn) c2 = e.half, t2 += gridDim.x;
+        do {  // skips the chunks that lie outside of C
+          c2 += kParts;
+          if (c2 * kBufCols >= p.bn) c2 = e.part, t2 += e.step;
+          if (t2 >= total) break;
+          tile_of<CTAS>(p, e.rank, t2, nm, nn, s2);
+        } while (!chunk_in(p, e, nm, nn, c2));
+        if (t2 < total) {
+          if (tc::elect_one()) {
+            tc::mbar_expect_tx(e.res_bar + 8 * (slot ^ 1), kBufBytes);
+            tc::tma_load_2d(e.buf + (slot ^ 1) * kBufBytes, &p.r, (int)nn + c2 * kBufCols, (int)(nm + e.quad * 32),
+                            e.res_bar + 8 * (slot ^ 1));
+          }
+          ++e.issued;
         }
-        if (t2 < total && e.lane == 0) {
-          tc::mbar_expect_tx(e.res_bar + 8 * (slot ^ 1), kBufBytes);
-          tc::tma_load_2d(e.buf + (slot ^ 1) * kBufBytes, &p.r, (int)nn + c2 * kBufCols, (int)(nm + e.quad * 32),
-                          e.res_bar + 8 * (slot ^ 1));
-        }
-        if (t2 < total) ++e.issued;
         if (!tc::mbar_wait_warp(e.res_bar + 8 * slot, (e.loads >> 1) & 1, g)) return false;
         ++e.loads;
       }
@@ -157,47 +158,45 @@ __device__ bool epilogue_tile(const Args& p, EpiState& e, const tc::Guard& g, in
     if (!in) continue;
     unsigned char* yb = e.ptr + slot * kBufBytes;
     unsigned char* zb = e.ptr + p.bufs_y * kBufBytes;
+    float v[32];
+    tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * kBufCols, v);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[32];
-      tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * kBufCols + h * 32, v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int unit = h * 4 + q, at = e.lane * 128 + ((unit ^ (e.lane & 7)) << 4);
-        float b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = p.bias ? e.bias[unit * 8 + i] : 0.f;
-        uint4 y, z, r;
-        if (p.has_r) r = *reinterpret_cast<uint4*>(yb + at);
-        epilogue8<ACT>(v + q * 8, b, p.has_r ? &r : nullptr, y, z);
-        *reinterpret_cast<uint4*>(yb + at) = y;
-        if (p.has_z) *reinterpret_cast<uint4*>(zb + at) = z;
-      }
+    for (int q = 0; q < 4; ++q) {
+      const int at = e.lane * 64 + ((q ^ (e.lane >> 1 & 3)) << 4);
+      float b[8];
+      VecIO<bf16, 8>::unpack(reinterpret_cast<const uint4*>(e.bias)[q], b);
+      uint4 y, z, r;
+      if (p.has_r) r = *reinterpret_cast<uint4*>(yb + at);
+      epilogue8<ACT>(v + q * 8, b, p.has_r ? &r : nullptr, y, z);
+      *reinterpret_cast<uint4*>(yb + at) = y;
+      if (p.has_z) *reinterpret_cast<uint4*>(zb + at) = z;
     }
     tc::fence_async_smem();
     __syncwarp();
-    if (e.lane == 0) {
+    if (tc::elect_one()) {
       tc::tma_store_2d(&p.y, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.buf + slot * kBufBytes);
       if (p.has_z)
         tc::tma_store_2d(&p.z, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.buf + p.bufs_y * kBufBytes);
       tc::bulk_commit();
     }
+    __syncwarp();
   }
   if (!waited && !tc::mbar_wait_warp(acc_full, parity, g)) return false;
   return true;
 }
 
 // A range of k: the sums as they are, 32 bits, to this split's part (rows of ldp, a multiple of 8).
+template <int CTAS>
 __device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& g, int t, uint32_t tmem,
                              uint32_t acc_full, uint32_t parity) {
   int64_t m0, n0;
   int split;
-  tile_of(p, t, m0, n0, split);
+  tile_of<CTAS>(p, e.rank, t, m0, n0, split);
   if (!tc::mbar_wait_warp(acc_full, parity, g)) return false;
   tc::fence_after();
   const int64_t row = m0 + e.quad * 32 + e.lane;
   float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + n0;
-  for (int c = e.half; c * 32 < p.bn; c += 2) {
+  for (int c = e.part; c * 32 < p.bn; c += kParts) {
     if (n0 + c * 32 >= p.ldp) break;
     float v[32];
     tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * 32, v);
@@ -211,12 +210,14 @@ __device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& 
   return true;
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Args p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
   const uint32_t base = tc::smem_addr(smem);
-  const uint32_t b_bytes = (uint32_t)p.bn * kTileK * 2;
+  const int rank = CTAS == 2 ? (int)tc::cluster_rank() : 0, first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+  const uint32_t b_bytes = (uint32_t)p.bn / CTAS * kTileK * 2;  // this block's part of B
   const uint32_t res_b = base + kSmemCtl;
   const uint32_t ring = res_b + (p.resident ? b_bytes * p.kblocks : 0);
   const uint32_t stage_bytes = kABytes + (p.resident ? 0 : b_bytes);
@@ -232,80 +233,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     tc::mbar_init(bar(ctl.drain), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(ctl.acc_full[i]), 1);
-      tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps);
+      tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps * CTAS);
     }
     ctl.dead = 0;
     tc::fence_mbar_init();
   }
   const tc::Guard g{&ctl.dead, p.status, p.wait_limit};
   const int total = p.m_tiles * p.n_tiles * p.splits;
-  if (warp == 9) tc::tmem_alloc(bar(reinterpret_cast<uint64_t&>(ctl.tmem)), p.tmem_cols);
+  if (warp == kMmaWarp) tc::tmem_alloc<CTAS>(bar(reinterpret_cast<uint64_t&>(ctl.tmem)), p.tmem_cols);
   tc::fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) tc::cluster_sync();
   tc::fence_after();
   const uint32_t tmem = ctl.tmem;
 
-  if (warp == 8) {
+  if (warp == kLoadWarp) {
     // ------------------------------------------------------------ producer
     if (!p.drop) {
+      // in a pair, the barriers that count the copies of both blocks are those of rank 0
+      auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t full) {
+        if constexpr (CTAS == 2) tc::tma_load_2d_pair(dst, map, x, y, full);
+        else tc::tma_load_2d(dst, map, x, y, full);
+      };
+      auto lead = [&](uint32_t b) { return CTAS == 2 ? tc::map_rank(b, 0) : b; };
       auto load_b = [&](uint32_t dst, int64_t n0, int kb, uint32_t full) {
-        if (!p.b_mn) tc::tma_load_2d(dst, &p.b, kb * kTileK, (int)n0, full);
+        n0 += rank * (p.bn / CTAS);
+        if (!p.b_mn) load(dst, &p.b, kb * kTileK, (int)n0, full);
         else
-          for (int c = 0; c < p.bn; c += 64) tc::tma_load_2d(dst + c * 128, &p.b, (int)n0 + c, kb * kTileK, full);
+          for (int c = 0; c < p.bn / CTAS; c += 64) load(dst + c * 128, &p.b, (int)n0 + c, kb * kTileK, full);
       };
       int it = 0, s = 0;
       uint32_t parity = 1;
       bool ok = true;
-      if (p.resident && (int)blockIdx.x < total && tc::elect_one()) {
-        tc::mbar_expect_tx(bar(ctl.resident), b_bytes * p.kblocks);
+      if (p.resident && first < total && tc::elect_one()) {
+        if (rank == 0) tc::mbar_expect_tx(bar(ctl.resident), b_bytes * p.kblocks * CTAS);
         for (int kb = 0; kb < p.kblocks; ++kb)
-          load_b(res_b + b_bytes * kb, (int64_t)(blockIdx.x % p.n_tiles) * p.bn, kb, bar(ctl.resident));
+          load_b(res_b + b_bytes * kb, (int64_t)(first % p.n_tiles) * p.bn, kb, lead(bar(ctl.resident)));
       }
       __syncwarp();
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      for (int t = first; ok && t < total; t += step) {
         int64_t m0, n0;
         int split;
-        tile_of(p, t, m0, n0, split);
+        tile_of<CTAS>(p, rank, t, m0, n0, split);
         const int k_lo = split * p.kb_per_split;
         const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
         for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
           ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
           if (!ok) break;
           if (tc::elect_one()) {
-            const uint32_t dst = ring + stage_bytes * s, full = bar(ctl.full[s]);
-            tc::mbar_expect_tx(full, stage_bytes);
-            if (!p.a_mn) tc::tma_load_2d(dst, &p.a, kb * kTileK, (int)m0, full);
+            const uint32_t dst = ring + stage_bytes * s, full = lead(bar(ctl.full[s]));
+            if (rank == 0) tc::mbar_expect_tx(bar(ctl.full[s]), stage_bytes * CTAS);
+            if (!p.a_mn) load(dst, &p.a, kb * kTileK, (int)m0, full);
             else
-              for (int c = 0; c < kTileM; c += 64) tc::tma_load_2d(dst + c * 128, &p.a, (int)m0 + c, kb * kTileK, full);
+              for (int c = 0; c < kTileM; c += 64) load(dst + c * 128, &p.a, (int)m0 + c, kb * kTileK, full);
             if (!p.resident) load_b(dst + kABytes, n0, kb, full);
           }
           __syncwarp();
           if (++s == p.stages) s = 0, parity ^= 1;
         }
       }
-      if (!ok) {  // gave up: no copy may be in flight when the block ends
+      if (!ok && rank == 0) {  // gave up: no copy, of either block, may be in flight when it ends
         for (int i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
           for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1)); ++j) {}
         if (p.resident)
           for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.resident), 0); ++j) {}
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ matrix instructions
-    {
-      // bfloat16 operands, f32 sums, 128 x bn
+    if (rank == 0) {
+      // bfloat16 operands, f32 sums, 128 (256) x bn
       const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)p.a_mn << 15 | (uint32_t)p.b_mn << 16 |
-                             (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+                             (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM * CTAS >> 4) << 24;
       // 16 of k further: 32 bytes along a row, or 16 rows of 128 bytes
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
       int s = 0, n_acc = 0;
       uint32_t parity = 0;
       bool ok = true;
-      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+      if (p.resident && first < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
+      for (int t = first; ok && t < total; t += step, ++n_acc) {
         int64_t m0, n0;
         int split;
-        tile_of(p, t, m0, n0, split);
+        tile_of<CTAS>(p, rank, t, m0, n0, split);
         const int k_lo = split * p.kb_per_split;
         const int k_hi = min(k_lo + p.kb_per_split, p.kblocks);
         const int acc = (int)(n_acc & 1);
@@ -321,19 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
           const uint32_t b = p.resident ? res_b + b_bytes * kb : a + kABytes;
           if (tc::elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kTileK / 16; ++i)
-            tc::mma_bf16(d, tc::smem_desc(a + i * a_step, 64 * 128, 1024), tc::smem_desc(b + i * b_step, 64 * 128, 1024), idesc,
-                         kb > k_lo || i > 0);
-            tc::mma_commit(bar(ctl.empty[s]));
+            for (int i = 0; i < kTileK / 16; ++i) {
+              const uint64_t da = tc::smem_desc(a + i * a_step, 64 * 128, 1024), db = tc::smem_desc(b + i * b_step, 64 * 128, 1024);
+              if constexpr (CTAS == 2) tc::mma_bf16_pair(d, da, db, idesc, kb > k_lo || i > 0);
+              else tc::mma_bf16(d, da, db, idesc, kb > k_lo || i > 0);
+            }
+            tc::mma_commit<CTAS>(bar(ctl.empty[s]));
           }
           __syncwarp();
           if (++s == p.stages) s = 0, parity ^= 1;
         }
-        if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
+        if (ok && tc::elect_one()) tc::mma_commit<CTAS>(bar(ctl.acc_full[acc]));
         __syncwarp();
       }
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
-        if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
+        if (tc::elect_one()) tc::mma_commit<CTAS>(bar(ctl.drain));
         __syncwarp();
         for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
       }
@@ -341,11 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
   } else {
     // ------------------------------------------------------------ epilogue
     EpiState e;
-    e.lane = lane, e.quad = warp & 3, e.half = warp >> 2;
+    e.lane = lane, e.quad = warp & 3, e.part = warp >> 2, e.rank = rank, e.step = step;
     const int bufs = p.bufs_y + p.has_z;
     e.buf = epi + warp * bufs * kBufBytes;
     e.ptr = smem + (e.buf - base);
-    e.bias = reinterpret_cast<float*>(smem + (epi - base) + kEpiWarps * bufs * kBufBytes) + warp * 64;
+    e.bias = reinterpret_cast<bf16*>(smem + (epi - base) + kEpiWarps * bufs * kBufBytes) + warp * 32;
     e.res_bar = bar(ctl.res[0]) + warp * 16;
     e.loads = e.issued = 0;
     int n_acc = 0;
@@ -359,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         tc::fence_async_smem();
       }
       __syncwarp();
-      int c = e.half;
-      for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      int c = e.part;
+      for (int t = first; t < total; t += step) {
         int64_t m0, n0;
         int split;
-        tile_of(p, t, m0, n0, split);
-        for (c = e.half; c * kBufCols < p.bn && !chunk_in(p, e, m0, n0, c);) c += 2;
+        tile_of<CTAS>(p, rank, t, m0, n0, split);
+        for (c = e.part; c * kBufCols < p.bn && !chunk_in(p, e, m0, n0, c);) c += kParts;
         if (c * kBufCols >= p.bn) continue;
-        if (lane == 0) {
+        if (tc::elect_one()) {
           tc::mbar_expect_tx(e.res_bar, kBufBytes);
           tc::tma_load_2d(e.buf, &p.r, (int)n0 + c * kBufCols, (int)(m0 + e.quad * 32), e.res_bar);
         }
@@ -374,29 +385,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
         break;
       }
     }
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++n_acc) {
+    for (int t = first; ok && t < total; t += step, ++n_acc) {
       const int acc = (int)(n_acc & 1);
       const uint32_t parity = (uint32_t)(n_acc >> 1 & 1), d = tmem + acc * (p.tmem_cols / 2), full = bar(ctl.acc_full[acc]);
-      if (p.part) ok = partial_tile(p, e, g, t, d, full, parity);
-      else if (p.act == GS_ACT_RELU) ok = epilogue_tile<GS_ACT_RELU>(p, e, g, t, total, d, full, parity);
-      else if (p.act == GS_ACT_GELU) ok = epilogue_tile<GS_ACT_GELU>(p, e, g, t, total, d, full, parity);
-      else if (p.act == GS_ACT_SILU) ok = epilogue_tile<GS_ACT_SILU>(p, e, g, t, total, d, full, parity);
-      else ok = epilogue_tile<GS_ACT_NONE>(p, e, g, t, total, d, full, parity);
+      if (p.part) ok = partial_tile<CTAS>(p, e, g, t, d, full, parity);
+      else if (p.act == GS_ACT_RELU) ok = epilogue_tile<CTAS, GS_ACT_RELU>(p, e, g, t, total, d, full, parity);
+      else if (p.act == GS_ACT_GELU) ok = epilogue_tile<CTAS, GS_ACT_GELU>(p, e, g, t, total, d, full, parity);
+      else if (p.act == GS_ACT_SILU) ok = epilogue_tile<CTAS, GS_ACT_SILU>(p, e, g, t, total, d, full, parity);
+      else ok = epilogue_tile<CTAS, GS_ACT_NONE>(p, e, g, t, total, d, full, parity);
       tc::fence_before();
       __syncwarp();
-      if (lane == 0 && ok) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
+      if (lane == 0 && ok) {
+        if constexpr (CTAS == 2) tc::mbar_arrive_cluster(tc::map_rank(bar(ctl.acc_empty[acc]), 0));
+        else tc::mbar_arrive(bar(ctl.acc_empty[acc]));
+      }
     }
     if (!ok && lane == 0) {  // gave up: the pieces in flight land before the block ends
       for (uint32_t i = e.loads; i < e.issued; ++i)
         for (int j = 0; j < p.wait_limit && !tc::mbar_try(e.res_bar + 8 * (i & 1), i >> 1 & 1); ++j) {}
     }
-    if (lane == 0) tc::bulk_wait0();
+    if (tc::elect_one()) tc::bulk_wait0();
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) tc::cluster_sync();  // nothing of this block is in use by the other any more
   tc::fence_after();
-  if (warp == 9) tc::tmem_dealloc(tmem, p.tmem_cols);
+  if (warp == kMmaWarp) tc::tmem_dealloc<CTAS>(tmem, p.tmem_cols);
 }
 
 // ---------------------------------------------------------------- host side
@@ -422,25 +437,30 @@ EncodeFn encoder() {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
-  int bn, m_tiles, n_tiles, splits, kblocks, kb_per_split;
+  int ctas, bn, m_tiles, n_tiles, splits, kblocks, kb_per_split;
   int64_t ldp;
 };
 
 constexpr int kSms = 152;  // the device's; only speed depends on it
 
-// Tiles as wide as they go (256 columns: the fewest reads of A) while there are enough of them for the
-// device; narrower ones, then ranges of k of at least four blocks (256), while there are not.
-Plan plan_of(int64_t m, int64_t n, int64_t k) {
+// A pair of blocks takes a 256-row tile together where the tiles, or their ranges of k, are enough for all
+// pairs: each then holds half of B, and shared memory, which a single block's 128 x 256 tile keeps busy for
+// 768 cycles per 512 of the tensor core, is no longer what bounds it.  Tiles as wide as they go (256 columns:
+// the fewest reads of A); with fewer tiles than that single blocks, narrower tiles, then ranges of k of at
+// least four blocks (256).
+Plan plan_as(int ctas, int64_t m, int64_t n, int64_t k) {
   Plan p;
-  p.m_tiles = (int)ceil_div(m, kTileM);
+  p.ctas = ctas;
+  const int units = kSms / ctas;
+  p.m_tiles = (int)ceil_div(m, kTileM * ctas);
   p.kblocks = (int)ceil_div(k, kTileK);
-  int n_tiles = (int)ceil_div(n, 256);
-  int bn = (int)(ceil_div(ceil_div(n, n_tiles), 64) * 64);
-  while (bn > 64 && (int64_t)p.m_tiles * ceil_div(n, bn) < kSms / 2 && p.kblocks < 16) bn -= 64;
+  const int n_tiles = (int)ceil_div(n, 256), grain = 64 * ctas;
+  int bn = (int)(ceil_div(ceil_div(n, n_tiles), grain) * grain);
+  while (ctas == 1 && bn > 64 && (int64_t)p.m_tiles * ceil_div(n, bn) < units / 2 && p.kblocks < 16) bn -= 64;
   p.bn = bn;
   p.n_tiles = (int)ceil_div(n, bn);
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-  int64_t splits = tiles >= kSms ? 1 : kSms / tiles;
+  int64_t splits = tiles >= units ? 1 : units / tiles;
   if (splits > p.kblocks / 4) splits = p.kblocks / 4;
   if (splits < 1) splits = 1;
   p.kb_per_split = (int)ceil_div(p.kblocks, splits);
@@ -448,20 +468,43 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
   p.ldp = ceil_div(n, 8) * 8;
   return p;
 }
+Plan plan_of(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_as(2, m, n, k);
+  // (short k: the copies of x and y bound it, and two blocks that wait for each other gain nothing: 300K x 256 ->
+  // 256 with residual, 114 us by single blocks, 128 us by pairs)
+  return n > 64 && m > 128 && p.kblocks >= 8 && (int64_t)p.m_tiles * p.n_tiles * p.splits * 5 >= kSms / 2 * 4 ? p : plan_as(1, m, n, k);
+}
+
+template <int CTAS>
+gs_status launch(const Args& p, int grid, int smem, cudaStream_t st, const char* where) {
+  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma<CTAS>, kSmemMost);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid), c.blockDim = dim3(kThreads), c.dynamicSmemBytes = smem, c.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CTAS, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at, c.numAttrs = CTAS == 2;
+    e = cudaLaunchKernelEx(&c, k_mma<CTAS>, p);
+  }
+  return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
 
 }  // namespace
 
 namespace gs {
 
-bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype) {
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype,
+                int row_bytes) {
   const EncodeFn f = encoder();
   if (!f) return false;
   const int size = (int)dtype_size(dtype), unit = 16 / size;
   if (rows == 1) ld = (cols + unit - 1) / unit * unit;  // the stride of a single row is never used
   const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * size};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)(row_bytes / size), (cuuint32_t)box_rows}, step[2] = {1, 1};
   return f(map, dtype == GS_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-           const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -493,11 +536,12 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   if (pl.splits > 1) p.part = static_cast<float*>(workspace);
   else p.has_z = q.z != nullptr, p.has_r = q.residual != nullptr, p.bufs_y = q.residual ? 2 : 1;
   // shared memory: control, epilogue buffers, then resident weights if they leave three stages, then stages
-  const int epi = p.part ? 0 : kEpiWarps * ((p.bufs_y + p.has_z) * kBufBytes + 256);
+  const int epi = p.part ? 0 : kEpiWarps * ((p.bufs_y + p.has_z) * kBufBytes + 64);
   const int room = kSmemMost - 1024 - kSmemCtl - epi;
-  const int b_bytes = pl.bn * kTileK * 2;
+  const int b_bytes = pl.bn / pl.ctas * kTileK * 2;
   const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
-  int grid = (int)(total < num_sms() ? total : num_sms());
+  const int units = num_sms() / pl.ctas;
+  int grid = (int)(total < units ? total : units);  // blocks, or pairs
   p.resident = 0;
   if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && (int64_t)b_bytes * pl.kblocks + 3 * kABytes <= room) {
     p.resident = 1;
@@ -508,20 +552,17 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   const int smem = 1024 + kSmemCtl + (p.resident ? b_bytes * pl.kblocks : 0) + p.stages * stage + epi;
   bool ok = q.a_mn ? encode_map(&p.a, q.a, q.k, q.m, q.lda, 64, GS_BF16) : encode_map(&p.a, q.a, q.m, q.k, q.lda, kTileM, GS_BF16);
-  ok = ok && (q.b_mn ? encode_map(&p.b, q.b, q.k, q.n, q.ldb, 64, GS_BF16) : encode_map(&p.b, q.b, q.n, q.k, q.ldb, pl.bn, GS_BF16));
+  ok = ok && (q.b_mn ? encode_map(&p.b, q.b, q.k, q.n, q.ldb, 64, GS_BF16) : encode_map(&p.b, q.b, q.n, q.k, q.ldb, pl.bn / pl.ctas, GS_BF16));
   if (!p.part) {
-    ok = ok && encode_map(&p.y, q.y, q.m, q.n, q.ldy, 32, GS_BF16);
-    if (q.z) ok = ok && encode_map(&p.z, q.z, q.m, q.n, q.ldz, 32, GS_BF16);
-    if (q.residual) ok = ok && encode_map(&p.r, q.residual, q.m, q.n, q.ldr, 32, GS_BF16);
+    ok = ok && encode_map(&p.y, q.y, q.m, q.n, q.ldy, 32, GS_BF16, 64);
+    if (q.z) ok = ok && encode_map(&p.z, q.z, q.m, q.n, q.ldz, 32, GS_BF16, 64);
+    if (q.residual) ok = ok && encode_map(&p.r, q.residual, q.m, q.n, q.ldr, 32, GS_BF16, 64);
   }
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
-  const cudaError_t e = max_dynamic_smem((const void*)k_mma, kSmemMost);
-  if (e != cudaSuccess) return set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  k_mma<<<grid, kThreads, smem, st>>>(p);
-  if (gs_status s = check_launch(where)) return s;
+  if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, st, where) : launch<1>(p, grid, smem, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
-                             static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+                             static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
               st);
   return check_launch(where);
 }

@@ -31,9 +31,10 @@ gs_status staged_run(const MmaProduct& p, void* workspace, int32_t* status, cuda
 size_t f32_workspace(int64_t m, int64_t n, int64_t k);
 gs_status f32_run(const MmaProduct& p, void* workspace, int32_t* status, cudaStream_t st, const char* where);
 
-// A tensor map of a [rows][cols] matrix in boxes of box_rows rows x 128 bytes, 128-byte swizzle; false if the
-// driver refuses it.
-bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype);
+// A tensor map of a [rows][cols] matrix in boxes of box_rows rows x 128 (or 64) bytes, swizzled over them; false
+// if the driver refuses it.
+bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype,
+                int row_bytes = 128);
 
 // the bound of a device-side wait, in tries of about a microsecond
 inline int wait_tries() {

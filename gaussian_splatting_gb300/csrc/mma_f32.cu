@@ -25,6 +25,8 @@
 // Every wait is bounded (see tc::Guard).
 #include <cuda.h>
 
+#include <utility>
+
 #include "mma.cuh"
 #include "tcgen05.cuh"
 
@@ -158,7 +160,7 @@ struct Operand {
     }
   }
   // this thread's units of a raw piece, split: 8 values to 16 bytes in each of three planes
-  __device__ __forceinline__ void split(int tid, const unsigned char* raw, unsigned char* parts) const {
+  __device__ __forceinline__ void split(int tid, int64_t x0, const unsigned char* raw, unsigned char* parts) const {
     // unit i lies a fixed distance from unit 0: the swizzles repeat every 8 rows
     int from, to, from_step, to_step;
     bool swap = false;
@@ -169,6 +171,7 @@ struct Operand {
       from_step = TEAM / 4 * 128, to_step = TEAM / 4 * 64;
     } else {
       const int u = tid % (EXT / 8), r = tid / (EXT / 8), v = 2 * (u & 3);
+      if (x0 + u * 8 >= ext) return;  // reaches only sums that are not stored
       from = (u >> 2) * 4096 + r * 128 + ((v ^ (r & 7)) << 4);
       to = (u >> 3) * 4096 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
       from_step = to_step = TEAM / (EXT / 8) * 128;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
           b.copy_words(tid, n0, kb, tc::smem_addr(room));
           asm volatile("cp.async.wait_all;" ::: "memory");
           team_sync<TEAM>(group);
-          b.split(tid, room, res_b + kBBytes * kb);
+          b.split(tid, n0, room, res_b + kBBytes * kb);
           team_sync<TEAM>(group);
         }
         tc::fence_async_smem();
@@ -373,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         if (!ok) break;
         unsigned char* st = ring + stage_bytes * to.s;
         const unsigned char* raw = raws + raw_bytes * from.s;
-        a.split(tid, raw, st);
-        if (!p.resident) b.split(tid, raw + OpA::kRaw, st + kABytes);
+        a.split(tid, cur.m0, raw, st);
+        if (!p.resident) b.split(tid, cur.n0, raw + OpA::kRaw, st + kABytes);
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -687,14 +690,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct Plan {
   int bn, m_tiles, n_tiles, splits, kblocks, kb_per_split;
   int64_t ldp;
+  bool swap;  // A and B change places: the parts hold C transposed
 };
 
 constexpr int kSms = 152;  // the device's; only speed depends on it
 
 // Tiles of 128 columns where there are more than 64 and the tiles, or their ranges of k (at least four
 // blocks, 128, each), are enough for the device; else of 64.
-Plan plan_of(int64_t m, int64_t n, int64_t k) {
+Plan plan_as(int64_t m, int64_t n, int64_t k) {
   Plan p;
+  p.swap = false;
   p.m_tiles = (int)ceil_div(m, kTileM);
   p.kblocks = (int)ceil_div(k, kTileK);
   const int64_t ranges = p.kblocks / 4 > 1 ? p.kblocks / 4 : 1;
@@ -707,6 +712,16 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
   p.splits = (int)ceil_div(p.kblocks, p.kb_per_split);
   p.ldp = ceil_div(n, 4) * 4;
   return p;
+}
+
+// With ranges of k the sums go through the fold kernel, which can as well transpose: then the operands stand
+// so that the tiles' padding is least (a 59 x 128 weight gradient: one tile of 128 x 64, not of 128 x 128).
+Plan plan_of(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_as(m, n, k);
+  Plan q = plan_as(n, m, k);
+  q.swap = true;
+  auto area = [](const Plan& r) { return (int64_t)r.m_tiles * r.n_tiles * r.bn; };
+  return p.splits > 1 && q.splits > 1 && area(q) < area(p) ? q : p;
 }
 
 // The shared memory of a launch: bytes of everything but the raw buffers, and how many of those fit.
@@ -741,7 +756,7 @@ gs_status launch(Args& p, const Room& r, int grid, cudaStream_t st, const char* 
 gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
   const int total = pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = total < gs::num_sms() ? total : gs::num_sms();
-  const int bufs = p.part ? 1 : 1 + (p.residual != nullptr) + (p.z != nullptr);
+  const int bufs = p.part ? 0 : 1 + (p.residual != nullptr) + (p.z != nullptr);
   Room r = room_of(pl, true, bufs);
   // resident B: one range of columns per block, and three raw buffers of A beside it
   if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && r.raws >= 3) {
@@ -760,11 +775,18 @@ namespace gs {
 
 size_t f32_workspace(int64_t m, int64_t n, int64_t k) {
   const Plan p = plan_of(m, n, k);
-  return p.splits > 1 ? (size_t)p.splits * m * p.ldp * sizeof(float) : 0;
+  return p.splits > 1 ? (size_t)p.splits * (p.swap ? n : m) * p.ldp * sizeof(float) : 0;
 }
 
-gs_status f32_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
+  MmaProduct q = product;
   Plan pl = plan_of(q.m, q.n, q.k);
+  if (pl.swap) {
+    std::swap(q.a, q.b);
+    std::swap(q.lda, q.ldb);
+    std::swap(q.a_mn, q.b_mn);
+    std::swap(q.m, q.n);
+  }
   if (pl.bn == 128 && pl.splits == 1 && (q.residual || q.z)) {  // their buffers and registers leave no room for 128 columns
     pl.bn = 64;
     pl.n_tiles = (int)ceil_div(q.n, 64);
@@ -807,7 +829,7 @@ gs_status f32_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
   if (gs_status s = launch_any(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
-  launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+  launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, pl.swap},
               st);
   return check_launch(where);
 }

@@ -434,7 +434,7 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
   p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
   if (gs_status s = pl.bn == 64 ? launch<64>(p, pl, st, where) : launch<128>(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
-  launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act},
+  launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
               st);
   return check_launch(where);
 }

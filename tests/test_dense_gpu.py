@@ -163,6 +163,31 @@ def test_linear_backward(shape, dtype):
         _close(db, *want["db"], f"db {act}")
 
 
+# enough tiles for every kernel's persistent walk to take several, ranges of k in the weight gradient, ragged
+# last tiles in each direction, widths on and off 16-byte rows
+MANY = [(33_000, 136, 264), (20_011, 256, 200), (40_000, 64, 59), (25_000, 59, 61), (19_999, 520, 131), (16_500, 264, 512)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_linear_with_many_rows(shape, dtype):
+    rows, n_in, n_out = shape
+    for act, has_r, keep in (("gelu", True, True), ("none", True, False), ("relu", False, False), ("silu", False, True)):
+        x, w = _rand((rows, n_in), dtype, 1), _rand((n_out, n_in), dtype, 2, 1 / math.sqrt(n_in))
+        b, r = _rand((n_out,), dtype, 3, 0.3), _rand((rows, n_out), dtype, 4) if has_r else None
+        y, z = dense.linear_fwd(x, w, b, r, act=act, keep_z=keep)
+        Y, ey, Z, ez = _linear_tolerances(x, w, b, r, act)
+        _close(y, Y, ey, f"y {act}")
+        if keep:
+            _close(z, Z, ez, f"z {act}")
+        dy = _rand((rows, n_out), dtype, 5, 1e-3)
+        z = None if act == "none" else _rand((rows, n_out), dtype, 8)
+        dx, dw, db = dense.linear_bwd(dy, x, w, z, act=act)
+        want = _linear_grads(dy, x, w, z, act)
+        for k, v in (("dx", dx), ("dw", dw), ("db", db)):
+            _close(v, *want[k], f"{k} {act}")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("pad,shift", [(8, 0), (24, 8), (1, 0), (3, 1), (2, 0)])
 def test_linear_takes_any_stride_and_alignment_and_leaves_the_gaps(dtype, pad, shift):
