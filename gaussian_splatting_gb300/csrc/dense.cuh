@@ -25,9 +25,12 @@ inline gs_status check_matrix(const char* where, const char* what, const void* p
   return GS_OK;
 }
 
-// whether 16-byte accesses at multiples of 16 bytes reach every row of a matrix
+// whether every row of a matrix starts at a multiple of `bytes`
+inline bool rows_aligned(const void* p, int64_t rows, int64_t ld, int32_t dtype, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || (ld * (int64_t)dtype_size(dtype)) % bytes == 0);
+}
 inline bool rows_aligned16(const void* p, int64_t rows, int64_t ld, int32_t dtype) {
-  return aligned16(p) && (rows <= 1 || (ld * (int64_t)dtype_size(dtype)) % 16 == 0);
+  return rows_aligned(p, rows, ld, dtype, 16);
 }
 
 }  // namespace gs
@@ -56,7 +59,7 @@ __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // VE consecutive elements of type T as 32-bit floats: one 16-byte access (VE = 16 / sizeof T)
-// or one element (VE = 1)
+// a pair of bfloat16, or one element (VE = 1)
 template <typename T, int VE>
 struct VecIO {
   using Raw = T;
@@ -64,6 +67,16 @@ struct VecIO {
   static __device__ __forceinline__ Raw zero() { return from_f32<T>(0.f); }
   static __device__ __forceinline__ void unpack(const Raw& r, float* f) { f[0] = to_f32<T>(r); }
   static __device__ __forceinline__ void store(T* p, const float* f) { *p = from_f32<T>(f[0]); }
+};
+template <>
+struct VecIO<__nv_bfloat16, 2> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ Raw zero() { return 0u; }
+  static __device__ __forceinline__ void unpack(const Raw& r, float* f) { f[0] = bf16_lo(r), f[1] = bf16_hi(r); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(f[0], f[1]);
+  }
 };
 template <>
 struct VecIO<float, 4> {

@@ -16,6 +16,8 @@
 // column sums are kept in the registers of the threads that own the columns over all rows of a
 // persistent block, folded over the block's warps in shared memory, written as one partial row
 // per block and added up by a second kernel in block order: no atomics, the same bits each run.
+#include <atomic>
+
 #include "dense.cuh"
 
 namespace {
@@ -54,6 +56,15 @@ __shared__ float2 s_fold[2][kWarps];
 template <int G>
 struct RowSum {
   int turn = 0;
+  __device__ __forceinline__ void operator()(float& a) {
+    if constexpr (G <= 32) {
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    } else {
+      float none = 0.f;
+      (*this)(a, none);
+    }
+  }
   __device__ __forceinline__ void operator()(float& a, float& b) {
 #pragma unroll
     for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
@@ -77,7 +88,7 @@ struct RowSum {
 
 // G threads per row, IT vectors of VE elements per thread, U rows in flight per thread.
 template <typename T, int VE, int G, int IT, int U>
-__global__ void __launch_bounds__(kThreads) k_layernorm_fwd(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, U == 4 ? 2 : 1) k_layernorm_fwd(const FwdArgs a) {
   using IO = VecIO<T, VE>;
   constexpr int kRows = kThreads / G;  // rows a block takes side by side
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
@@ -94,41 +105,58 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fwd(const FwdArgs a) {
   }
   const float inv = 1.f / (float)a.width;
   RowSum<G> sum;
-  for (int64_t r0 = (int64_t)blockIdx.x * (kRows * U); r0 < a.rows; r0 += (int64_t)gridDim.x * (kRows * U)) {
-    typename IO::Raw rx[U][IT];
+  const int64_t step = (int64_t)gridDim.x * (kRows * U);
+  typename IO::Raw rx[U][IT], next[U][IT];
+  auto load = [&](int64_t r0, typename IO::Raw (&to)[U][IT]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * kRows + sub;
 #pragma unroll
       for (int i = 0; i < IT; ++i)
-        rx[u][i] = in[i] && r < a.rows ? IO::load(x + r * a.ldx + (lane + i * G) * VE) : IO::zero();
+        to[u][i] = in[i] && r < a.rows ? IO::load(x + r * a.ldx + (lane + i * G) * VE) : IO::zero();
     }
+  };
+  auto sum_rows = [&](float (&v)[U]) {  // two rows at a time
+#pragma unroll
+    for (int u = 0; u + 1 < U; u += 2) sum(v[u], v[u + 1]);
+    if constexpr (U == 1) sum(v[0]);
+  };
+  int64_t r0 = (int64_t)blockIdx.x * (kRows * U);
+  load(r0, rx);
+  for (; r0 < a.rows; r0 += step) {
+    load(r0 + step, next);  // in flight while these rows are summed and written
+    float mean[U], q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + u * kRows + sub;
-      float s = 0.f, q = 0.f;
+      mean[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         float f[VE];
         IO::unpack(rx[u][i], f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) s += f[e];  // values beyond the width are zero
+        for (int e = 0; e < VE; ++e) mean[u] += f[e];  // values beyond the width are zero
       }
-      sum(s, q);
-      const float mean = __fmul_rn(s, inv);  // the value that is stored: not folded into the differences below
-      q = 0.f;
+    }
+    sum_rows(mean);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mean[u] = __fmul_rn(mean[u], inv);  // the value that is stored: not folded into the differences below
+      q[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         float f[VE];
         IO::unpack(rx[u][i], f);
         if (in[i]) {
 #pragma unroll
-          for (int e = 0; e < VE; ++e) q = fmaf(f[e] - mean, f[e] - mean, q);
+          for (int e = 0; e < VE; ++e) q[u] = fmaf(f[e] - mean[u], f[e] - mean[u], q[u]);
         }
       }
-      s = 0.f;
-      sum(q, s);
-      const float rstd = 1.f / sqrtf(q * inv + a.eps);
+    }
+    sum_rows(q);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * kRows + sub;
+      const float rstd = 1.f / sqrtf(q[u] * inv + a.eps);
       if (r < a.rows) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -138,14 +166,16 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fwd(const FwdArgs a) {
           IO::unpack(rg[i], g);
           IO::unpack(rb[i], b);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) f[e] = fmaf((f[e] - mean) * rstd, g[e], b[e]);
+          for (int e = 0; e < VE; ++e) f[e] = fmaf((f[e] - mean[u]) * rstd, g[e], b[e]);
           IO::store(y + r * a.ldy + (lane + i * G) * VE, f);
         }
         if (lane == 0) {
-          if (a.mean) a.mean[r] = mean;
+          if (a.mean) a.mean[r] = mean[u];
           if (a.rstd) a.rstd[r] = rstd;
         }
       }
+#pragma unroll
+      for (int i = 0; i < IT; ++i) rx[u][i] = next[u][i];
     }
   }
 }
@@ -182,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fwd_wide(const FwdArgs a
   }
 }
 
-template <typename T, int VE, int G, int IT, int U>
-__global__ void __launch_bounds__(kThreads) k_layernorm_bwd(const BwdArgs a) {
+template <typename T, int VE, int G, int IT>
+__global__ void __launch_bounds__(kThreads, VE * IT <= 4 ? 3 : VE == 8 && IT == 1 ? 2 : 1) k_layernorm_bwd(const BwdArgs a) {
   using IO = VecIO<T, VE>;
   constexpr int kRows = kThreads / G;
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
@@ -204,63 +234,65 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd(const BwdArgs a) {
   }
   const float inv = 1.f / (float)a.width;
   RowSum<G> sum;
-  for (int64_t r0 = (int64_t)blockIdx.x * (kRows * U); r0 < a.rows; r0 += (int64_t)gridDim.x * (kRows * U)) {
-    typename IO::Raw rx[U][IT], ry[U][IT], rs[U][IT];
-    float mean[U], rstd[U];
+  struct Row {
+    typename IO::Raw x[IT], dy[IT], skip[IT];
+    float mean, rstd;
+  } cur, next;
+  auto load = [&](int64_t r, Row& to) {
+    const bool ok = r < a.rows;
+    to.mean = ok ? a.mean[r] : 0.f;
+    to.rstd = ok ? a.rstd[r] : 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + u * kRows + sub;
-      const bool ok = r < a.rows;
-      mean[u] = ok ? a.mean[r] : 0.f;
-      rstd[u] = ok ? a.rstd[r] : 0.f;
+    for (int i = 0; i < IT; ++i) {
+      const int c = (lane + i * G) * VE;
+      to.x[i] = in[i] && ok ? IO::load(x + r * a.ldx + c) : IO::zero();
+      to.dy[i] = in[i] && ok ? IO::load(dy + r * a.lddy + c) : IO::zero();
+      to.skip[i] = in[i] && ok && skip ? IO::load(skip + r * a.ldskip + c) : IO::zero();
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r0 = (int64_t)blockIdx.x * kRows;
+  load(r0 + sub, cur);
+  for (; r0 < a.rows; r0 += step) {
+    const int64_t r = r0 + sub;
+    load(r + step, next);  // in flight while this row is summed and written
+    float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int c = (lane + i * G) * VE;
-        rx[u][i] = in[i] && ok ? IO::load(x + r * a.ldx + c) : IO::zero();
-        ry[u][i] = in[i] && ok ? IO::load(dy + r * a.lddy + c) : IO::zero();
-        rs[u][i] = in[i] && ok && skip ? IO::load(skip + r * a.ldskip + c) : IO::zero();
+    for (int i = 0; i < IT; ++i) {
+      float f[VE], d[VE], g[VE];
+      IO::unpack(cur.x[i], f);
+      IO::unpack(cur.dy[i], d);
+      IO::unpack(rg[i], g);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float h = (f[e] - cur.mean) * cur.rstd, ge = d[e] * g[e];
+        s1 += ge;  // beyond the width and the rows dy is zero: nothing is added
+        s2 = fmaf(ge, h, s2);
+        ag[i][e] = fmaf(d[e], h, ag[i][e]);
+        ab[i][e] += d[e];
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + u * kRows + sub;
-      float s1 = 0.f, s2 = 0.f;
+    sum(s1, s2);
+    s1 *= inv;
+    s2 *= inv;
+    if (dx && r < a.rows) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        float f[VE], d[VE], g[VE];
-        IO::unpack(rx[u][i], f);
-        IO::unpack(ry[u][i], d);
+        if (!in[i]) continue;
+        float f[VE], d[VE], g[VE], k[VE];
+        IO::unpack(cur.x[i], f);
+        IO::unpack(cur.dy[i], d);
         IO::unpack(rg[i], g);
+        IO::unpack(cur.skip[i], k);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const float h = (f[e] - mean[u]) * rstd[u], ge = d[e] * g[e];
-          s1 += ge;  // beyond the width and the rows dy is zero: nothing is added
-          s2 = fmaf(ge, h, s2);
-          ag[i][e] = fmaf(d[e], h, ag[i][e]);
-          ab[i][e] += d[e];
+          const float h = (f[e] - cur.mean) * cur.rstd;
+          f[e] = fmaf(cur.rstd, d[e] * g[e] - s1 - h * s2, k[e]);
         }
-      }
-      sum(s1, s2);
-      s1 *= inv;
-      s2 *= inv;
-      if (dx && r < a.rows) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          if (!in[i]) continue;
-          float f[VE], d[VE], g[VE], k[VE];
-          IO::unpack(rx[u][i], f);
-          IO::unpack(ry[u][i], d);
-          IO::unpack(rg[i], g);
-          IO::unpack(rs[u][i], k);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const float h = (f[e] - mean[u]) * rstd[u];
-            f[e] = fmaf(rstd[u], d[e] * g[e] - s1 - h * s2, k[e]);
-          }
-          IO::store(dx + r * a.lddx + (lane + i * G) * VE, f);
-        }
+        IO::store(dx + r * a.lddx + (lane + i * G) * VE, f);
       }
     }
+    cur = next;
   }
   if (!a.partials) return;
   // fold the column sums over the block's rows: the groups of a warp by shuffles, the warps in
@@ -382,85 +414,143 @@ __global__ void __launch_bounds__(1024) k_layernorm_fold(const float* __restrict
 }
 
 // ---------------------------------------------------------------- host side
-// Which form a width takes: G threads per row, IT vectors per thread (0: the wide kernel).
+// Which form a width takes: VE elements per vector, G threads per row, IT vectors per thread (0: the wide
+// kernel).  The vector is 16 bytes where every array's rows and the width allow it, else a pair of bfloat16,
+// else one element.
 struct Form {
-  int vec, g, it;
+  int ve, g, it;
 };
 
-// Forward: a row gets as few threads as hold it in at most four 16-byte vectors (eight single elements)
-// each, so that narrow rows keep whole warps busy; beyond a warp's reach a block shares it.
-Form fwd_form(int width, bool vec, int32_t dtype) {
-  const int ve = vec ? (dtype == GS_F32 ? 4 : 8) : 1;
-  const int n = width / ve, most = vec ? 4 : 8;
+// A row gets as few threads as hold it in one vector each, then whole warps, then the block; a thread takes a
+// second vector only where that keeps the row's sums inside a warp (64 vectors), or beyond 256.  Rows of pairs
+// or single elements hold more of them per thread before they leave the warp: a thread's work would otherwise
+// be mostly the sums (1M x 100 bfloat16 backward with single elements: 533 us at one per thread).  The
+// backward, which keeps two sums per value in registers, prefers more threads to a second 16-byte vector.
+Form form_of(int width, int ve, int32_t dtype, bool backward) {
+  const bool full = ve == 16 / (int)gs::dtype_size(dtype);
+  const int n = (width + ve - 1) / ve;
   for (int g : {8, 16, 32})
-    if (n <= g) return {vec, g, 1};
-  for (int it = 2; it <= most; it *= 2)
-    if (n <= 32 * it) return {vec, 32, it};
-  for (int it = 1; it <= (vec ? 4 : 16); it *= 2)
-    if (n <= kThreads * it) return {vec, kThreads, it};
-  return {vec, kThreads, 0};
-}
-// Backward: every value a thread holds also has two sums in its registers, so a row is spread over as
-// many threads as it has vectors before any thread takes a second one.
-Form bwd_form(int width, bool vec, int32_t dtype) {
-  const int n = width / (vec ? (dtype == GS_F32 ? 4 : 8) : 1);
-  for (int g : {8, 16, 32, 64, 128})
-    if (n <= g) return {vec, g, 1};
-  for (int it = 1; it <= (vec ? 4 : 16); it *= 2)
-    if (n <= kThreads * it) return {vec, kThreads, it};
-  return {vec, kThreads, 0};
+    if (n <= g) return {ve, g, 1};
+  if (full) {
+    if (n <= 64) return backward ? Form{ve, 64, 1} : Form{ve, 32, 2};
+    // (forward, float32: 423 us per 700K x 512 with four vectors per lane, 459 with one for each of 128 threads;
+    // bfloat16, twice as many values per vector: 234 and 216 us per 300K x 1024)
+    if (n <= 128) return !backward && dtype == GS_F32 ? Form{ve, 32, 4} : Form{ve, 128, 1};
+  } else {
+    for (int it : {2, 4, 8})
+      if (n <= 32 * it) return {ve, 32, it};
+  }
+  for (int it = full ? 1 : 2; it <= (full ? 4 : backward && ve == 2 ? 8 : 16); it *= 2)  // what the registers hold
+    if (n <= kThreads * it) return {ve, kThreads, it};
+  return {ve, kThreads, 0};
 }
 
-// blocks that fill the device at 8 resident blocks per SM, or fewer when the rows are few
+// blocks for these rows, no more than are resident at once: a persistent block takes the rest of the rows
 int grid_of(int64_t rows, int rows_per_block, int per_sm) {
   const int64_t need = (rows + rows_per_block - 1) / rows_per_block;
   const int64_t most = (int64_t)gs::num_sms() * per_sm;
   return (int)(need < most ? (need > 0 ? need : 1) : most);
 }
 
-constexpr int kFwdPerSm = 8, kBwdPerSm = 4;
+// Resident blocks of a kernel per SM, asked for once per kernel (a property of its code: devices of one
+// architecture do not differ).
+template <typename Args, void (*K)(const Args)>
+int resident() {
+  static std::atomic<int> known{0};
+  int n = known.load();
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, K, kThreads, 0) != cudaSuccess || n < 1) n = 1;
+    known.store(n);
+  }
+  return n;
+}
+
+constexpr int kFwdPerSm = 8, kBwdPerSm = 4;  // at most; the backward's is what its workspace is sized for
 
 template <typename T, int VE, int G, int IT>
 void launch_fwd(const FwdArgs& a, cudaStream_t st) {
-  constexpr int U = G == kThreads ? 1 : IT == 1 ? 2 : 1;
-  k_layernorm_fwd<T, VE, G, IT, U><<<grid_of(a.rows, kThreads / G * U, kFwdPerSm), kThreads, 0, st>>>(a);
+  // rows in flight per thread: narrow rows need several for the memory's latency
+  constexpr int U = IT == 1 ? 4 : IT == 2 ? 2 : 1;
+  const int per_sm = resident<FwdArgs, k_layernorm_fwd<T, VE, G, IT, U>>();
+  const int grid = grid_of(a.rows, kThreads / G * U, per_sm < kFwdPerSm ? per_sm : kFwdPerSm);
+  k_layernorm_fwd<T, VE, G, IT, U><<<grid, kThreads, 0, st>>>(a);
 }
-template <typename T>
-void run_fwd(const FwdArgs& a, Form f, cudaStream_t st) {
-  constexpr int VE = 16 / sizeof(T);
-  if (f.it == 0) {
-    k_layernorm_fwd_wide<T><<<grid_of(a.rows, 1, kFwdPerSm), kThreads, 0, st>>>(a);
-    return;
+// returns the number of blocks: the partial rows that it writes
+template <typename T, int VE, int G, int IT>
+int launch_bwd(const BwdArgs& a, cudaStream_t st) {
+  const int per_sm = resident<BwdArgs, k_layernorm_bwd<T, VE, G, IT>>();
+  const int grid = grid_of(a.rows, kThreads / G, per_sm < kBwdPerSm ? per_sm : kBwdPerSm);
+  k_layernorm_bwd<T, VE, G, IT><<<grid, kThreads, 0, st>>>(a);
+  return grid;
+}
+
+// The forms of 16-byte vectors, and of smaller ones.
+#define GS_FULL_FORMS(F) F(8, 1) F(16, 1) F(32, 1) F(256, 1) F(256, 2) F(256, 4)
+#define GS_PART_FORMS(F) \
+  F(8, 1) F(16, 1) F(32, 1) F(32, 2) F(32, 4) F(32, 8) F(256, 2) F(256, 4) F(256, 8)
+
+template <typename T, int VE>
+void run_fwd_ve(const FwdArgs& a, Form f, cudaStream_t st) {
+#define GS_FORM(G, IT) \
+  if (f.g == G && f.it == IT) return launch_fwd<T, VE, G, IT>(a, st);
+  if constexpr (VE * sizeof(T) == 16) {
+    GS_FULL_FORMS(GS_FORM) GS_FORM(32, 2)
+    if constexpr (sizeof(T) == 4) { GS_FORM(32, 4) } else { GS_FORM(128, 1) }
+  } else {
+    GS_PART_FORMS(GS_FORM) GS_FORM(256, 16)
   }
-  const int key = (f.vec ? 10000 : 0) + f.g * 20 + f.it;
-  switch (key) {
-#define GS_FORM(v, g, it) \
-  case (v ? 10000 : 0) + g * 20 + it: launch_fwd<T, v ? VE : 1, g, it>(a, st); break;
-    GS_FORM(1, 8, 1) GS_FORM(1, 16, 1) GS_FORM(1, 32, 1) GS_FORM(1, 32, 2) GS_FORM(1, 32, 4)
-    GS_FORM(1, 256, 1) GS_FORM(1, 256, 2) GS_FORM(1, 256, 4)
-    GS_FORM(0, 8, 1) GS_FORM(0, 16, 1) GS_FORM(0, 32, 1) GS_FORM(0, 32, 2) GS_FORM(0, 32, 4) GS_FORM(0, 32, 8)
-    GS_FORM(0, 256, 2) GS_FORM(0, 256, 4) GS_FORM(0, 256, 8) GS_FORM(0, 256, 16)
 #undef GS_FORM
-  }
 }
 
 template <typename T>
-void run_bwd(const BwdArgs& a, Form f, int grid, cudaStream_t st) {
-  constexpr int VE = 16 / sizeof(T);
-  if (f.it == 0) {
-    k_layernorm_bwd_wide<T><<<grid, kThreads, 0, st>>>(a);
-    return;
+void run_fwd(const FwdArgs& a, Form f, cudaStream_t st) {
+  if (f.it == 0) k_layernorm_fwd_wide<T><<<grid_of(a.rows, 1, kFwdPerSm), kThreads, 0, st>>>(a);
+  else if (f.ve == 1) run_fwd_ve<T, 1>(a, f, st);
+  else if (f.ve == 16 / (int)sizeof(T)) run_fwd_ve<T, 16 / sizeof(T)>(a, f, st);
+  else if constexpr (sizeof(T) == 2) run_fwd_ve<T, 2>(a, f, st);
+}
+
+// the most blocks that a backward launches, each with a partial row
+// (rows too wide for registers: no more than keep the partials within 256 MiB)
+int bwd_most(int64_t rows, Form f, int width) {
+  const int g = grid_of(rows, f.it == 0 ? 1 : kThreads / f.g, kBwdPerSm);
+  const int fit = (1 << 25) / width;
+  return f.it == 0 && g > fit ? fit : g;
+}
+
+template <typename T, int VE>
+int run_bwd_ve(const BwdArgs& a, Form f, cudaStream_t st) {
+#define GS_FORM(G, IT) \
+  if (f.g == G && f.it == IT) return launch_bwd<T, VE, G, IT>(a, st);
+  if constexpr (VE * sizeof(T) == 16) {
+    GS_FULL_FORMS(GS_FORM) GS_FORM(64, 1) GS_FORM(128, 1)
+  } else {
+    GS_PART_FORMS(GS_FORM)
+    if constexpr (VE == 1) { GS_FORM(256, 16) }
   }
-  const int key = (f.vec ? 10000 : 0) + f.g * 20 + f.it;
-  switch (key) {
-#define GS_FORM(v, g, it) \
-  case (v ? 10000 : 0) + g * 20 + it: k_layernorm_bwd<T, v ? VE : 1, g, it, 1><<<grid, kThreads, 0, st>>>(a); break;
-    GS_FORM(1, 8, 1) GS_FORM(1, 16, 1) GS_FORM(1, 32, 1) GS_FORM(1, 64, 1) GS_FORM(1, 128, 1)
-    GS_FORM(1, 256, 1) GS_FORM(1, 256, 2) GS_FORM(1, 256, 4)
-    GS_FORM(0, 8, 1) GS_FORM(0, 16, 1) GS_FORM(0, 32, 1) GS_FORM(0, 64, 1) GS_FORM(0, 128, 1)
-    GS_FORM(0, 256, 1) GS_FORM(0, 256, 2) GS_FORM(0, 256, 4) GS_FORM(0, 256, 8) GS_FORM(0, 256, 16)
 #undef GS_FORM
+  return 0;
+}
+
+template <typename T>
+int run_bwd(const BwdArgs& a, Form f, cudaStream_t st) {
+  if (f.it == 0) {
+    const int grid = bwd_most(a.rows, f, a.width);
+    k_layernorm_bwd_wide<T><<<grid, kThreads, 0, st>>>(a);
+    return grid;
   }
+  if (f.ve == 1) return run_bwd_ve<T, 1>(a, f, st);
+  if (f.ve == 16 / (int)sizeof(T)) return run_bwd_ve<T, 16 / sizeof(T)>(a, f, st);
+  if constexpr (sizeof(T) == 2) return run_bwd_ve<T, 2>(a, f, st);
+  return 0;
+}
+
+// elements per vector: what the width, and the alignment that `at` tells of (16 or 4 bytes), allow
+template <typename Aligned>
+int vector_of(int width, int32_t dtype, Aligned at) {
+  const int full = 16 / (int)gs::dtype_size(dtype);
+  if (width % full == 0 && at(16)) return full;
+  return dtype == GS_BF16 && width % 2 == 0 && at(4) ? 2 : 1;
 }
 
 gs_status check_desc(const char* where, const gs_layernorm_desc* d) {
@@ -470,14 +560,6 @@ gs_status check_desc(const char* where, const gs_layernorm_desc* d) {
   if (d->dtype != GS_F32 && d->dtype != GS_BF16)
     return gs::set_error(GS_ERR_INVALID, "%s: unknown element type %d", where, d->dtype);
   return GS_OK;
-}
-
-// blocks of the backward: the number of partial rows
-// (rows too wide for registers: no more than keep the partials within 256 MiB)
-int bwd_grid(int64_t rows, Form f, int width) {
-  const int g = grid_of(rows, f.it == 0 ? 1 : kThreads / f.g, kBwdPerSm);
-  const int fit = (1 << 25) / width;
-  return f.it == 0 && g > fit ? fit : g;
 }
 
 }  // namespace
@@ -492,11 +574,12 @@ extern "C" gs_status gs_layernorm_fwd(const gs_layernorm_desc* d, const void* x,
   if (gs_status s = gs::check_matrix(where, "y", y, d->rows, d->width, d->ldy, d->dtype)) return s;
   if (gs_status s = gs::check_matrix(where, "gamma", gamma, 1, d->width, d->width, d->dtype)) return s;
   if (gs_status s = gs::check_matrix(where, "beta", beta, 1, d->width, d->width, d->dtype)) return s;
-  const int ve = 16 / (int)gs::dtype_size(d->dtype);
-  const bool vec = d->width % ve == 0 && gs::rows_aligned16(x, d->rows, d->ldx, d->dtype) &&
-                   gs::rows_aligned16(y, d->rows, d->ldy, d->dtype) && gs::aligned16(gamma) && gs::aligned16(beta);
+  const int ve = vector_of(d->width, d->dtype, [&](int bytes) {
+    return gs::rows_aligned(x, d->rows, d->ldx, d->dtype, bytes) && gs::rows_aligned(y, d->rows, d->ldy, d->dtype, bytes) &&
+           gs::rows_aligned(gamma, 1, 0, d->dtype, bytes) && gs::rows_aligned(beta, 1, 0, d->dtype, bytes);
+  });
   const FwdArgs a{x, gamma, beta, y, mean, rstd, d->rows, d->ldx, d->ldy, d->width, d->eps};
-  const Form f = fwd_form(d->width, vec, d->dtype);
+  const Form f = form_of(d->width, ve, d->dtype, false);
   if (d->dtype == GS_F32) run_fwd<float>(a, f, gs::as_stream(stream));
   else run_fwd<__nv_bfloat16>(a, f, gs::as_stream(stream));
   return gs::check_launch(where);
@@ -504,10 +587,11 @@ extern "C" gs_status gs_layernorm_fwd(const gs_layernorm_desc* d, const void* x,
 
 extern "C" size_t gs_layernorm_bwd_workspace_size(const gs_layernorm_desc* d) {
   if (!d || d->rows < 0 || d->width < 1 || d->width > (1 << 24)) return 0;
-  // the scalar and the vector form need not have the same number of blocks: the larger
+  // the forms that the arrays' alignment may lead to need not have the same number of blocks: the largest
   int most = 1;
-  for (int vec = 0; vec < 2; ++vec) {
-    const int g = bwd_grid(d->rows, bwd_form(d->width, vec, d->dtype), d->width);
+  for (int ve : {1, 2, 4, 8}) {
+    if (d->width % ve || ve > 16 / (int)gs::dtype_size(d->dtype)) continue;
+    const int g = bwd_most(d->rows, form_of(d->width, ve, d->dtype, true), d->width);
     most = g > most ? g : most;
   }
   return sizeof(float) * 2 * (size_t)d->width * most;
@@ -546,17 +630,15 @@ extern "C" gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy
     if (workspace_bytes < need)
       return gs::set_error(GS_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", where, workspace_bytes, need);
   }
-  const int ve = 16 / (int)size;
-  const bool vec = d->width % ve == 0 && gs::rows_aligned16(x, d->rows, d->ldx, d->dtype) &&
-                   gs::rows_aligned16(dy, d->rows, d->lddy, d->dtype) && gs::aligned16(gamma) &&
-                   (!skip || gs::rows_aligned16(skip, d->rows, d->ldskip, d->dtype)) &&
-                   (!dx || gs::rows_aligned16(dx, d->rows, d->lddx, d->dtype));
-  const Form f = bwd_form(d->width, vec, d->dtype);
-  const int grid = bwd_grid(d->rows, f, d->width);
+  const int ve = vector_of(d->width, d->dtype, [&](int bytes) {
+    return gs::rows_aligned(x, d->rows, d->ldx, d->dtype, bytes) && gs::rows_aligned(dy, d->rows, d->lddy, d->dtype, bytes) &&
+           gs::rows_aligned(gamma, 1, 0, d->dtype, bytes) && (!skip || gs::rows_aligned(skip, d->rows, d->ldskip, d->dtype, bytes)) &&
+           (!dx || gs::rows_aligned(dx, d->rows, d->lddx, d->dtype, bytes));
+  });
+  const Form f = form_of(d->width, ve, d->dtype, true);
   float* part = sums ? static_cast<float*>(workspace) : nullptr;
   const BwdArgs a{dy, x, gamma, mean, rstd, skip, dx, part, d->rows, d->lddy, d->ldx, d->ldskip, d->lddx, d->width};
-  if (d->dtype == GS_F32) run_bwd<float>(a, f, grid, st);
-  else run_bwd<__nv_bfloat16>(a, f, grid, st);
+  const int grid = d->dtype == GS_F32 ? run_bwd<float>(a, f, st) : run_bwd<__nv_bfloat16>(a, f, st);
   if (gs_status s = gs::check_launch(where)) return s;
   if (!sums) return GS_OK;
   const int blocks = (2 * d->width + 31) / 32;

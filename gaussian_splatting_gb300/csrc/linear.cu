@@ -5,10 +5,11 @@
 //   dx       dx = dz w     A = dz, B = w along its other axis
 //   dw       dw = dz^T x   A = dz and B = x, both along their other axes
 // bfloat16 arrays whose rows start on 16-byte boundaries go to mma.cu, other bfloat16 ones to mma_staged.cu,
-// float32 to mma_f32.cu.
+// float32 to mma_f32.cu; small calls to linear_small.cu.
 // dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
 // sums, and kept in the workspace for the two products that read it.
 #include "mma.cuh"
+#include "small.cuh"
 
 namespace {
 
@@ -226,7 +227,7 @@ gs_status check_workspace(const char* where, const void* workspace, size_t have,
 
 extern "C" size_t gs_linear_fwd_workspace_size(const gs_linear_desc* d) {
   if (check_desc("gs_linear_fwd_workspace_size", d) || d->rows == 0) return 0;
-  return product_space(d->rows, d->out_features, d->in_features, d->dtype);
+  return gs::small_fwd_takes(d) ? 0 : product_space(d->rows, d->out_features, d->in_features, d->dtype);
 }
 
 extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias,
@@ -245,6 +246,7 @@ extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const
   if (z)
     if (gs_status s = gs::check_matrix(where, "z", z, d->rows, d->out_features, d->ldz, d->dtype)) return s;
   if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_linear_fwd_workspace_size(d))) return s;
+  if (gs::small_fwd_takes(d)) return gs::small_fwd(d, x, w, bias, residual, y, z, gs::as_stream(stream), where);
   const gs::MmaProduct q{x, w, d->ldx, d->ldw, false, false, d->rows, d->out_features, d->in_features,
                          bias, residual, y, z, d->ldr, d->ldy, d->ldz, d->act};
   return run_product(q, d->dtype, workspace, status, gs::as_stream(stream), where);
@@ -252,7 +254,7 @@ extern "C" gs_status gs_linear_fwd(const gs_linear_desc* d, const void* x, const
 
 extern "C" size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d) {
   if (check_desc("gs_linear_bwd_workspace_size", d) || d->rows == 0) return 0;
-  return bwd_space(d).total;
+  return gs::small_bwd_takes(d) ? gs::small_bwd_workspace(d) : bwd_space(d).total;
 }
 
 extern "C" gs_status gs_linear_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z,
@@ -284,6 +286,7 @@ extern "C" gs_status gs_linear_bwd(const gs_linear_desc* d, const void* dy, cons
   if (d->act == GS_ACT_NONE) z = nullptr;
   else if (gs_status s = gs::check_matrix(where, "z", z, d->rows, d->out_features, d->ldz, d->dtype)) return s;
   if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_linear_bwd_workspace_size(d))) return s;
+  if (gs::small_bwd_takes(d)) return gs::small_bwd(d, dy, x, w, z, dx, dw, dbias, workspace, st, where);
   if (d->dtype == GS_F32) return run_bwd<float>(d, dy, x, w, z, dx, dw, dbias, workspace, status, st);
   return run_bwd<__nv_bfloat16>(d, dy, x, w, z, dx, dw, dbias, workspace, status, st);
 }

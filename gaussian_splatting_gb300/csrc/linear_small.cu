@@ -1,0 +1,420 @@
+// The linear layer's small calls, where a launch's latency is the cost: a tensor-core product takes about
+// 11 us from its first instruction to its last whatever its size (tensor maps, TMEM, a pipeline that fills and
+// drains), plain kernels on the FP32 pipe 3 to 5.
+//
+//   few rows (at most 16): a group of lanes per output column reads a weight row once and keeps the rows' sums
+//     in registers (k_few_fwd); columns of the input gradient summed over slices of the outputs (k_few_dx);
+//     the weight gradient as a sum of at most 16 outer products (k_few_dw).  Bound by reading or writing w.
+//   small products (at most 2^26 multiply-adds): a 32 x 64 tile per block, 64 of k at a time (k_small_fwd)
+//   backward of narrow layers (64 x 64 at most) over up to 32,768 rows: dz, its column sums, dx and the
+//     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order
+// All sums in 32 bits in a fixed order.
+#include "small.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kThreads = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T>
+struct Fwd {
+  const T* x;
+  const T* w;
+  const T* bias;
+  const T* residual;
+  T* y;
+  T* z;
+  int64_t ldx, ldw, ldr, ldy, ldz;
+  int rows, in, out, act;
+};
+
+template <typename T>
+__device__ __forceinline__ void finish(const Fwd<T>& p, int r, int n, float v) {
+  if (p.bias) v += to_f32<T>(p.bias[n]);
+  if (p.z) p.z[r * p.ldz + n] = from_f32<T>(v);
+  v = act_value(v, p.act);
+  if (p.residual) v += to_f32<T>(p.residual[r * p.ldr + n]);
+  p.y[r * p.ldy + n] = from_f32<T>(v);
+}
+
+// ---------------------------------------------------------------- few rows
+constexpr int kFew = 8;  // rows of a block
+
+// LANES lanes per column, VE elements per lane and step
+template <typename T, int VE, int LANES>
+__global__ void __launch_bounds__(kThreads) k_few_fwd(const Fwd<T> p) {
+  using IO = VecIO<T, VE>;
+  const int lane = threadIdx.x % LANES, n = (blockIdx.x * kThreads + threadIdx.x) / LANES, r0 = blockIdx.y * kFew;
+  const int rows = min(kFew, p.rows - r0);
+  float acc[kFew];
+#pragma unroll
+  for (int r = 0; r < kFew; ++r) acc[r] = 0.f;
+  if (n < p.out) {
+    const T* w = p.w + n * p.ldw;
+    const T* x = p.x + r0 * p.ldx;
+#pragma unroll 2
+    for (int k = lane * VE; k < p.in; k += LANES * VE) {
+      float wf[VE];
+      IO::unpack(IO::load(w + k), wf);
+#pragma unroll
+      for (int r = 0; r < kFew; ++r) {
+        if (r >= rows) break;
+        float xf[VE];
+        IO::unpack(IO::load(x + r * p.ldx + k), xf);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[r] = fmaf(wf[e], xf[e], acc[r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kFew; ++r)
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+#pragma unroll
+  for (int r = 0; r < kFew; ++r)  // row r by the group's lane r
+    if (r == lane && r < rows && n < p.out) finish(p, r0 + r, n, acc[r]);
+}
+
+template <typename T>
+struct Bwd {
+  const T* dy;
+  const T* x;
+  const T* w;
+  const T* z;
+  T* dx;
+  T* dw;
+  T* db;
+  int64_t ldy, ldx, ldw, ldz, lddx, lddw;
+  int rows, in, out, act;
+};
+
+template <typename T>
+__device__ __forceinline__ float dz_at(const Bwd<T>& p, int64_t r, int n) {
+  const float d = to_f32<T>(p.dy[r * p.ldy + n]);
+  return p.z ? d * act_slope(to_f32<T>(p.z[r * p.ldz + n]), p.act) : d;
+}
+
+// dx of kFew rows and 4 VE columns: 64 slices of the outputs per block, added over the slices at the end
+template <typename T, int VE>
+__global__ void __launch_bounds__(kThreads) k_few_dx(const Bwd<T> p) {
+  using IO = VecIO<T, VE>;
+  constexpr int kChunk = 512, kSlices = kThreads / 4;
+  __shared__ float dz[kFew][kChunk];
+  __shared__ float part[kThreads / 32][4][kFew * VE];
+  const int tx = threadIdx.x % 4, slice = threadIdx.x / 4, r0 = blockIdx.y * kFew;
+  const int rows = min(kFew, p.rows - r0), k = (blockIdx.x * 4 + tx) * VE;
+  float acc[kFew][VE];
+#pragma unroll
+  for (int r = 0; r < kFew; ++r)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) acc[r][e] = 0.f;
+  for (int n0 = 0; n0 < p.out; n0 += kChunk) {
+    const int len = min(kChunk, p.out - n0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFew * kChunk; i += kThreads) {
+      const int r = i / kChunk, n = i % kChunk;
+      dz[r][n] = r < rows && n < len ? dz_at(p, r0 + r, n0 + n) : 0.f;
+    }
+    __syncthreads();
+    if (k < p.in) {
+#pragma unroll 4
+      for (int n = slice; n < len; n += kSlices) {
+        float wf[VE];
+        IO::unpack(IO::load(p.w + (int64_t)(n0 + n) * p.ldw + k), wf);
+#pragma unroll
+        for (int r = 0; r < kFew; ++r)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) acc[r][e] = fmaf(dz[r][n], wf[e], acc[r][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kFew; ++r)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) acc[r][e] += __shfl_xor_sync(0xffffffffu, acc[r][e], o);
+      if ((threadIdx.x & 31) < 4) part[threadIdx.x / 32][tx][r * VE + e] = acc[r][e];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4 * kFew * VE; i += kThreads) {
+    const int t = i / (kFew * VE), r = i / VE % kFew, e = i % VE, col = (blockIdx.x * 4 + t) * VE + e;
+    if (r >= rows || col >= p.in) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v += part[w][t][r * VE + e];
+    p.dx[(r0 + r) * p.lddx + col] = from_f32<T>(v);
+  }
+}
+
+// dw of 32 outputs x 32 VE inputs, and their bias gradient in the first block across
+template <typename T, int VE>
+__global__ void __launch_bounds__(kThreads) k_few_dw(const Bwd<T> p) {
+  using IO = VecIO<T, VE>;
+  constexpr int kRows = 2 * kFew, kOut = 32, kPer = kOut / (kThreads / 32);
+  __shared__ float dz[kRows][kOut];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n0 = blockIdx.y * kOut, k = (blockIdx.x * 32 + lane) * VE;
+  for (int i = threadIdx.x; i < kRows * kOut; i += kThreads) {
+    const int r = i / kOut, n = n0 + i % kOut;
+    dz[r][i % kOut] = r < p.rows && n < p.out ? dz_at(p, r, n) : 0.f;
+  }
+  __syncthreads();
+  if (p.db && blockIdx.x == 0 && threadIdx.x < kOut && n0 + threadIdx.x < p.out) {
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) v += dz[r][threadIdx.x];
+    p.db[n0 + threadIdx.x] = from_f32<T>(v);
+  }
+  if (!p.dw || k >= p.in) return;
+  float acc[kPer][VE];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) acc[j][e] = 0.f;
+#pragma unroll 4
+  for (int r = 0; r < p.rows; ++r) {
+    float xf[VE];
+    IO::unpack(IO::load(p.x + r * p.ldx + k), xf);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) acc[j][e] = fmaf(dz[r][warp * kPer + j], xf[e], acc[j][e]);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (n0 + warp * kPer + j < p.out) IO::store(p.dw + (int64_t)(n0 + warp * kPer + j) * p.lddw + k, acc[j]);
+}
+
+// ---------------------------------------------------------------- small products
+constexpr int kTileR = 32, kTileC = 64, kTileK = 64;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_small_fwd(const Fwd<T> p) {
+  __shared__ float xs[kTileR][kTileK + 1], ws[kTileC][kTileK + 1];
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;  // columns tx + 16 j, rows ty + 16 i
+  const int64_t r0 = (int64_t)blockIdx.x * kTileR;
+  const int n0 = blockIdx.y * kTileC;
+  float acc[2][4] = {};
+  for (int k0 = 0; k0 < p.in; k0 += kTileK) {
+    const int k = tid % kTileK;
+    const bool ki = k0 + k < p.in;
+    if (k0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTileR * kTileK / kThreads; ++i) {
+      const int r = tid / kTileK + i * (kThreads / kTileK);
+      xs[r][k] = ki && r0 + r < p.rows ? to_f32<T>(p.x[(r0 + r) * p.ldx + k0 + k]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kTileC * kTileK / kThreads; ++i) {
+      const int n = tid / kTileK + i * (kThreads / kTileK);
+      ws[n][k] = ki && n0 + n < p.out ? to_f32<T>(p.w[(int64_t)(n0 + n) * p.ldw + k0 + k]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int kk = 0; kk < kTileK; ++kk) {
+      float a[2], b[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = xs[ty + 16 * i][kk];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = ws[tx + 16 * j][kk];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (r0 + ty + 16 * i < p.rows && n0 + tx + 16 * j < p.out) finish(p, (int)r0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+}
+
+constexpr int kNarrow = 64;
+
+// parts: [gridDim.x][kNarrow + 1][kNarrow], the bias gradient's in the last row
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_small_bwd(const Bwd<T> p, float* parts) {
+  __shared__ float dz[kTileR][kNarrow + 1], xs[kTileR][kNarrow + 1], ws[kNarrow][kNarrow + 1];
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, c = tid % kNarrow, rr = tid / kNarrow;
+  float aw[4][4] = {}, ab = 0.f;
+  if (p.dx) {
+#pragma unroll
+    for (int i = 0; i < kNarrow * kNarrow / kThreads; ++i) {
+      const int n = rr + i * (kThreads / kNarrow);
+      ws[n][c] = n < p.out && c < p.in ? to_f32<T>(p.w[n * p.ldw + c]) : 0.f;
+    }
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * kTileR; r0 < p.rows; r0 += (int64_t)gridDim.x * kTileR) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTileR * kNarrow / kThreads; ++i) {
+      const int r = rr + i * (kThreads / kNarrow);
+      const bool in = r0 + r < p.rows;
+      dz[r][c] = in && c < p.out ? dz_at(p, r0 + r, c) : 0.f;
+      xs[r][c] = in && c < p.in ? to_f32<T>(p.x[(r0 + r) * p.ldx + c]) : 0.f;
+    }
+    __syncthreads();
+    if (p.dx) {
+      float acc[2][4] = {};
+#pragma unroll 8
+      for (int n = 0; n < kNarrow; ++n) {
+        float a[2], b[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[i] = dz[ty + 16 * i][n];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = ws[n][tx + 16 * j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r0 + ty + 16 * i < p.rows && tx + 16 * j < p.in)
+            p.dx[(r0 + ty + 16 * i) * p.lddx + tx + 16 * j] = from_f32<T>(acc[i][j]);
+    }
+#pragma unroll 8
+    for (int r = 0; r < kTileR; ++r) {
+      float a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = dz[r][ty + 16 * i], b[i] = xs[r][tx + 16 * i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) aw[i][j] = fmaf(a[i], b[j], aw[i][j]);
+    }
+    if (tid < kNarrow) {
+#pragma unroll 8
+      for (int r = 0; r < kTileR; ++r) ab += dz[r][tid];
+    }
+  }
+  float* out = parts + (int64_t)blockIdx.x * (kNarrow + 1) * kNarrow;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[(ty + 16 * i) * kNarrow + tx + 16 * j] = aw[i][j];
+  if (tid < kNarrow) out[kNarrow * kNarrow + tid] = ab;
+}
+
+// a row of dw (or, last, db) per block: 64 columns by 4 interleaved sets of parts
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_small_bwd_fold(const float* parts, int n_parts, int in, int out, T* dw, int64_t lddw,
+                                                             T* db) {
+  __shared__ float s[4][kNarrow];
+  const int c = threadIdx.x % kNarrow, way = threadIdx.x / kNarrow, row = blockIdx.x < out ? blockIdx.x : kNarrow;
+  float v = 0.f;
+#pragma unroll 8
+  for (int i = way; i < n_parts; i += 4) v += parts[((int64_t)i * (kNarrow + 1) + row) * kNarrow + c];
+  s[way][c] = v;
+  __syncthreads();
+  if (way) return;
+  v = ((s[0][c] + s[1][c]) + s[2][c]) + s[3][c];
+  if (row < kNarrow) {
+    if (dw && c < in) dw[row * lddw + c] = from_f32<T>(v);
+  } else if (db && c < out) {
+    db[c] = from_f32<T>(v);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kFewRows = 2 * kFew;
+constexpr int64_t kSmallWork = int64_t(1) << 26;  // multiply-adds
+constexpr int kNarrowRows = 32768;
+
+bool vec_ok(const void* p, int64_t rows, int64_t ld, int width, int32_t dtype) {
+  return width % (16 / (int)gs::dtype_size(dtype)) == 0 && gs::rows_aligned16(p, rows, ld, dtype);
+}
+
+int small_bwd_grid(int64_t rows) {
+  const int64_t tiles = ceil_div(rows, kTileR);
+  return (int)(tiles < 152 ? tiles : 152);
+}
+
+template <typename T>
+gs_status fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y, void* z,
+              cudaStream_t st, const char* where) {
+  const Fwd<T> p{(const T*)x, (const T*)w, (const T*)bias, (const T*)residual, (T*)y, (T*)z,
+                 d->ldx, d->ldw, d->ldr, d->ldy, d->ldz, (int)d->rows, d->in_features, d->out_features, d->act};
+  constexpr int VE = 16 / sizeof(T);
+  if (d->rows <= kFewRows) {
+    const unsigned groups = (unsigned)ceil_div(d->rows, kFew);
+    const bool vec = vec_ok(x, d->rows, d->ldx, d->in_features, d->dtype) &&
+                     vec_ok(w, d->out_features, d->ldw, d->in_features, d->dtype);
+    auto grid = [&](int lanes) { return dim3((unsigned)ceil_div((int64_t)d->out_features * lanes, kThreads), groups); };
+    if (!vec) k_few_fwd<T, 1, 32><<<grid(32), kThreads, 0, st>>>(p);
+    else if (d->in_features <= 8 * VE) k_few_fwd<T, VE, 8><<<grid(8), kThreads, 0, st>>>(p);
+    else k_few_fwd<T, VE, 32><<<grid(32), kThreads, 0, st>>>(p);
+  } else {
+    const dim3 grid((unsigned)ceil_div(d->rows, kTileR), (unsigned)ceil_div(d->out_features, kTileC));
+    k_small_fwd<T><<<grid, kThreads, 0, st>>>(p);
+  }
+  return gs::check_launch(where);
+}
+
+template <typename T>
+gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
+              void* dbias, void* workspace, cudaStream_t st, const char* where) {
+  const Bwd<T> p{(const T*)dy, (const T*)x, (const T*)w, (const T*)z, (T*)dx, (T*)dw, (T*)dbias,
+                 d->ldy, d->ldx, d->ldw, d->ldz, d->lddx, d->lddw, (int)d->rows, d->in_features, d->out_features, d->act};
+  constexpr int VE = 16 / sizeof(T);
+  if (d->rows <= kFewRows) {
+    if (dx) {
+      const bool vec = vec_ok(w, d->out_features, d->ldw, d->in_features, d->dtype);
+      const dim3 grid((unsigned)ceil_div(d->in_features, 4 * (vec ? VE : 1)), (unsigned)ceil_div(d->rows, kFew));
+      if (vec) k_few_dx<T, VE><<<grid, kThreads, 0, st>>>(p);
+      else k_few_dx<T, 1><<<grid, kThreads, 0, st>>>(p);
+      if (gs_status s = gs::check_launch(where)) return s;
+    }
+    if (dw || dbias) {
+      const bool vec = !dw || (vec_ok(x, d->rows, d->ldx, d->in_features, d->dtype) &&
+                               vec_ok(dw, d->out_features, d->lddw, d->in_features, d->dtype));
+      const dim3 grid(dw ? (unsigned)ceil_div(d->in_features, 32 * (vec ? VE : 1)) : 1, (unsigned)ceil_div(d->out_features, 32));
+      if (vec) k_few_dw<T, VE><<<grid, kThreads, 0, st>>>(p);
+      else k_few_dw<T, 1><<<grid, kThreads, 0, st>>>(p);
+    }
+    return gs::check_launch(where);
+  }
+  const int grid = small_bwd_grid(d->rows);
+  float* parts = static_cast<float*>(workspace);
+  k_small_bwd<T><<<grid, kThreads, 0, st>>>(p, parts);
+  if (gs_status s = gs::check_launch(where)) return s;
+  if (!dw && !dbias) return GS_OK;
+  k_small_bwd_fold<T><<<d->out_features + 1, kThreads, 0, st>>>(parts, grid, d->in_features, d->out_features, (T*)dw, d->lddw,
+                                                                (T*)dbias);
+  return gs::check_launch(where);
+}
+
+}  // namespace
+
+namespace gs {
+
+bool small_fwd_takes(const gs_linear_desc* d) {
+  // few rows of a long sum over few columns leave most of the device idle: the split product takes those
+  if (d->rows <= kFewRows) return d->in_features <= 8192;
+  return d->in_features <= 256 && d->rows * d->in_features * d->out_features <= kSmallWork;
+}
+gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
+                    void* z, cudaStream_t st, const char* where) {
+  return d->dtype == GS_F32 ? fwd<float>(d, x, w, bias, residual, y, z, st, where)
+                            : fwd<bf16>(d, x, w, bias, residual, y, z, st, where);
+}
+
+bool small_bwd_takes(const gs_linear_desc* d) {
+  if (d->rows <= kFewRows) return d->out_features <= 8192;
+  return d->in_features <= kNarrow && d->out_features <= kNarrow && d->rows <= kNarrowRows;
+}
+size_t small_bwd_workspace(const gs_linear_desc* d) {
+  return d->rows <= kFewRows ? 0 : (size_t)small_bwd_grid(d->rows) * (kNarrow + 1) * kNarrow * sizeof(float);
+}
+gs_status small_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
+                    void* dbias, void* workspace, cudaStream_t st, const char* where) {
+  return d->dtype == GS_F32 ? bwd<float>(d, dy, x, w, z, dx, dw, dbias, workspace, st, where)
+                            : bwd<bf16>(d, dy, x, w, z, dx, dw, dbias, workspace, st, where);
+}
+
+}  // namespace gs

@@ -12,6 +12,8 @@ Outputs and scratch that a call allocates belong to that stream.
 """
 from __future__ import annotations
 
+from ctypes import addressof
+
 import torch
 
 from . import _native as N
@@ -103,6 +105,30 @@ def _scratch(n, device):
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
+_entry = {}
+
+
+def _call(name, *args):
+    """A C entry point: its function looked up once, its status checked."""
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(N.load(), name)
+    status = f(*args)
+    if status:
+        N._check(status, name)
+
+
+def _size(name, desc):
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(N.load(), name)
+    return f(desc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def linear_fwd(x, w, bias=None, residual=None, act="none", keep_z=False, out=None, z=None, status=None, stream=None):
     """``(y, z)``: y = act(x w^T + bias) + residual, and z the sum before the activation (None unless
     ``keep_z`` or ``z`` asks for it).  x [rows, in], w [out, in], bias [out], residual [rows, out].
@@ -120,13 +146,19 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", keep_z=False, out=Non
     with _on(x.device, stream) as st:
         if out is None:
             out = torch.empty((rows, n_out), dtype=x.dtype, device=x.device)
-        d.ldy = _matrix(out, "out", rows, n_out, x)
-        if z is None and keep_z:
-            z = torch.empty((rows, n_out), dtype=x.dtype, device=x.device)
+            d.ldy = n_out
+        else:
+            d.ldy = _matrix(out, "out", rows, n_out, x)
         if z is not None:
             d.ldz = _matrix(z, "z", rows, n_out, x)
-        need = N.gs_linear_fwd_workspace_size(d)
-        N.gs_linear_fwd(d, x, w, bias, residual, out, z, _scratch(need, x.device), need, status, st)
+        elif keep_z:
+            z = torch.empty((rows, n_out), dtype=x.dtype, device=x.device)
+            d.ldz = n_out
+        at = addressof(d)
+        need = _size("gs_linear_fwd_workspace_size", at)
+        ws = _scratch(need, x.device)
+        _call("gs_linear_fwd", at, x.data_ptr(), w.data_ptr(), _at(bias), _at(residual), out.data_ptr(), _at(z), _at(ws), need,
+              _at(status), st)
     return out, z
 
 
@@ -149,20 +181,25 @@ def linear_bwd(dy, x, w, z=None, act="none", bias=True, dx=None, dw=None, dbias=
     else:
         d.ldz = _matrix(z, "z", rows, n_out, dy)
     with _on(dy.device, stream) as st:
-        if dx is None and need_dx:
-            dx = torch.empty((rows, n_in), dtype=dy.dtype, device=dy.device)
-        if dw is None and need_dw:
-            dw = torch.empty((n_out, n_in), dtype=dy.dtype, device=dy.device)
-        if dbias is None and bias:
-            dbias = torch.empty(n_out, dtype=dy.dtype, device=dy.device)
         if dx is not None:
             d.lddx = _matrix(dx, "dx", rows, n_in, dy)
+        elif need_dx:
+            dx = torch.empty((rows, n_in), dtype=dy.dtype, device=dy.device)
+            d.lddx = n_in
         if dw is not None:
             d.lddw = _matrix(dw, "dw", n_out, n_in, dy)
+        elif need_dw:
+            dw = torch.empty((n_out, n_in), dtype=dy.dtype, device=dy.device)
+            d.lddw = n_in
         if dbias is not None:
             _vector(dbias, "dbias", n_out, dy)
-        need = N.gs_linear_bwd_workspace_size(d)
-        N.gs_linear_bwd(d, dy, x, w, z, dx, dw, dbias, _scratch(need, dy.device), need, status, st)
+        elif bias:
+            dbias = torch.empty(n_out, dtype=dy.dtype, device=dy.device)
+        at = addressof(d)
+        need = _size("gs_linear_bwd_workspace_size", at)
+        ws = _scratch(need, dy.device)
+        _call("gs_linear_bwd", at, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _at(z), _at(dx), _at(dw), _at(dbias), _at(ws), need,
+              _at(status), st)
     return dx, dw, dbias
 
 
@@ -178,10 +215,13 @@ def layernorm_fwd(x, gamma, beta, eps=1e-5, out=None, stats=True, stream=None):
     with _on(x.device, stream) as st:
         if out is None:
             out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
-        d.ldy = _matrix(out, "out", rows, n, x)
+            d.ldy = n
+        else:
+            d.ldy = _matrix(out, "out", rows, n, x)
         mean = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if stats else None
-        N.gs_layernorm_fwd(d, x, gamma, beta, out, mean, rstd, st)
+        _call("gs_layernorm_fwd", addressof(d), x.data_ptr(), gamma.data_ptr(), beta.data_ptr(), out.data_ptr(), _at(mean),
+              _at(rstd), st)
     return out, mean, rstd
 
 
@@ -200,17 +240,22 @@ def layernorm_bwd(dy, x, gamma, mean, rstd, skip=None, dx=None, dgamma=None, dbe
     if skip is not None:
         d.ldskip = _matrix(skip, "skip", rows, n, dy)
     with _on(dy.device, stream) as st:
-        if dx is None and need_dx:
-            dx = torch.empty((rows, n), dtype=dy.dtype, device=dy.device)
-        if dgamma is None and need_dparams:
-            dgamma = torch.empty(n, dtype=dy.dtype, device=dy.device)
-        if dbeta is None and need_dparams:
-            dbeta = torch.empty(n, dtype=dy.dtype, device=dy.device)
         if dx is not None:
             d.lddx = _matrix(dx, "dx", rows, n, dy)
-        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
-            if t is not None:
-                _vector(t, name, n, dy)
-        need = N.gs_layernorm_bwd_workspace_size(d) if dgamma is not None or dbeta is not None else 0
-        N.gs_layernorm_bwd(d, dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, _scratch(need, dy.device), need, st)
+        elif need_dx:
+            dx = torch.empty((rows, n), dtype=dy.dtype, device=dy.device)
+            d.lddx = n
+        if dgamma is not None:
+            _vector(dgamma, "dgamma", n, dy)
+        elif need_dparams:
+            dgamma = torch.empty(n, dtype=dy.dtype, device=dy.device)
+        if dbeta is not None:
+            _vector(dbeta, "dbeta", n, dy)
+        elif need_dparams:
+            dbeta = torch.empty(n, dtype=dy.dtype, device=dy.device)
+        at = addressof(d)
+        need = _size("gs_layernorm_bwd_workspace_size", at) if dgamma is not None or dbeta is not None else 0
+        ws = _scratch(need, dy.device)
+        _call("gs_layernorm_bwd", at, dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _at(skip),
+              _at(dx), _at(dgamma), _at(dbeta), _at(ws), need, st)
     return dx, dgamma, dbeta

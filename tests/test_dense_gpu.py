@@ -163,6 +163,36 @@ def test_linear_backward(shape, dtype):
         _close(db, *want["db"], f"db {act}")
 
 
+# a few rows (odd numbers of them, one, the most that count as few, one more), long and short sums, any width
+FEW = [(1, 7, 9), (7, 2048, 96), (8, 40, 1000), (15, 1023, 77), (16, 4096, 256), (9, 300, 2050), (17, 96, 64), (33, 64, 64),
+       (500, 60, 64), (3000, 33, 17), (700, 200, 130), (40_000, 64, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", FEW, ids=str)
+def test_linear_small_calls(shape, dtype):
+    rows, n_in, n_out = shape
+    for act, has_r, keep, pad in (("gelu", True, True, 0), ("none", False, False, 3), ("silu", True, False, 8)):
+        x, w = _rand((rows, n_in), dtype, 1, 1.0, pad), _rand((n_out, n_in), dtype, 2, 1 / math.sqrt(n_in), pad)
+        b, r = _rand((n_out,), dtype, 3, 0.3), _rand((rows, n_out), dtype, 4, 1.0, pad) if has_r else None
+        y, z = dense.linear_fwd(x, w, b, r, act=act, keep_z=keep)
+        Y, ey, Z, ez = _linear_tolerances(x, w, b, r, act)
+        _close(y, Y, ey, f"y {act}")
+        if keep:
+            _close(z, Z, ez, f"z {act}")
+        dy = _rand((rows, n_out), dtype, 5, 1e-3, pad)
+        z = None if act == "none" else _rand((rows, n_out), dtype, 8, 1.0, pad)
+        full = dense.linear_bwd(dy, x, w, z, act=act)
+        want = _linear_grads(dy, x, w, z, act)
+        for k, v in zip(("dx", "dw", "db"), full):
+            _close(v, *want[k], f"{k} {act}")
+        for kw, kept in ((dict(need_dx=False), (1, 2)), (dict(need_dw=False), (0, 2)), (dict(bias=False), (0, 1))):
+            part = dense.linear_bwd(dy, x, w, z, act=act, **kw)
+            for i in range(3):
+                assert (part[i] is not None) == (i in kept)
+                assert i not in kept or torch.equal(part[i], full[i])
+
+
 # enough tiles for every kernel's persistent walk to take several, ranges of k in the weight gradient, ragged
 # last tiles in each direction, widths on and off 16-byte rows
 MANY = [(33_000, 136, 264), (20_011, 256, 200), (40_000, 64, 59), (25_000, 59, 61), (19_999, 520, 131), (16_500, 264, 512)]
