@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fwd_wide(const FwdArgs a
 }
 
 template <typename T, int VE, int G, int IT>
-__global__ void __launch_bounds__(kThreads, VE * IT <= 4 ? 3 : VE == 8 && IT == 1 ? 2 : 1) k_layernorm_bwd(const BwdArgs a) {
+__global__ void __launch_bounds__(kThreads, VE == 8 && IT == 1 ? 2 : VE * IT <= 4 ? (IT == 1 && G <= 32 ? 4 : 3) : 1) k_layernorm_bwd(const BwdArgs a) {
   using IO = VecIO<T, VE>;
   constexpr int kRows = kThreads / G;
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
