@@ -32,6 +32,12 @@ inline bool rows_aligned(const void* p, int64_t rows, int64_t ld, int32_t dtype,
 inline bool rows_aligned16(const void* p, int64_t rows, int64_t ld, int32_t dtype) {
   return rows_aligned(p, rows, ld, dtype, 16);
 }
+// Whether tiled bulk copies (TMA) may move a matrix: its rows also end on such boundaries.  Where the last
+// 16 bytes of a row are only in part its own, a store fills them all (a 59-wide view of 60-float rows lost
+// its 60th column), so neither direction is trusted with them.
+inline bool tma_takes(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtype) {
+  return rows_aligned16(p, rows, ld, dtype) && (width * (int64_t)dtype_size(dtype)) % 16 == 0;
+}
 
 }  // namespace gs
 

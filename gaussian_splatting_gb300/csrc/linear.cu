@@ -4,7 +4,7 @@
 //   forward  z  = x w^T    A = x,  B = w
 //   dx       dx = dz w     A = dz, B = w along its other axis
 //   dw       dw = dz^T x   A = dz and B = x, both along their other axes
-// bfloat16 arrays whose rows start on 16-byte boundaries go to mma.cu, other bfloat16 ones to mma_staged.cu,
+// bfloat16 arrays whose rows start and end on 16-byte boundaries go to mma.cu, other bfloat16 ones to mma_staged.cu,
 // float32 to mma_f32.cu; small calls to linear_small.cu.
 // dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
 // sums, and kept in the workspace for the two products that read it.
@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// dz = dy act'(z) to `dz` (if wanted), and its column sums over this block's rows to part[blockIdx.x].
+// dz = dy act'(z) to `dz` (if wanted; a row's last 16 bytes are filled up with zeros), and its column sums over this block's rows to part[blockIdx.x].
 // A thread owns VE columns; CX threads lie along a row, kThreads / CX rows side by side.
 template <typename T, bool VEC, int CX>
 __global__ void __launch_bounds__(kThreads) k_act_grad(const T* dy, const T* z, int64_t rows, int n, int64_t lddy,
@@ -154,8 +154,8 @@ size_t product_space(int64_t m, int64_t n, int64_t k, int32_t dtype) {
   return a > b ? a : b;
 }
 
-// The backward's scratch: a copy of dz (after an activation, or where bfloat16 rows of dy do not start on
-// 16-byte boundaries), the bias gradient's parts, the products' parts.
+// The backward's scratch: a copy of dz, its rows filled up with zeros to 16 bytes (after an activation, or
+// where bfloat16 rows of dy do not start and end on 16-byte boundaries), the bias gradient's parts, the products' parts.
 struct BwdSpace {
   size_t dz, bias, part, total;
   int64_t lddz;
@@ -164,7 +164,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 BwdSpace bwd_space(const gs_linear_desc* d) {
   BwdSpace s{};
   s.lddz = ceil_div(d->out_features, 8) * 8;
-  const bool copy = d->act != GS_ACT_NONE || (d->dtype == GS_BF16 && (d->ldy * 2) % 16 != 0);
+  const bool copy = d->act != GS_ACT_NONE || (d->dtype == GS_BF16 && (d->ldy % 8 != 0 || d->out_features % 8 != 0));
   s.dz = copy ? up256((size_t)d->rows * s.lddz * gs::dtype_size(d->dtype)) : 0;
   s.bias = up256((size_t)parts_of(d) * d->out_features * sizeof(float));
   const size_t a = product_space(d->rows, d->in_features, d->out_features, d->dtype);
@@ -185,18 +185,19 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   void* part = at + space.dz + space.bias;
   const void* dz = copy ? copy : dy;
   const int64_t lddz = copy ? space.lddz : d->ldy;
+  const int64_t unit = 16 / (int64_t)sizeof(T), pad = copy ? ceil_div(d->out_features, unit) * unit - d->out_features : 0;
   if (copy || dbias)
     if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), copy, lddz, bias_part,
                                       static_cast<T*>(dbias), st, where))
       return s;
   if (dx) {
     const gs::MmaProduct q{dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
-                           nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE};
+                           nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
   if (dw) {
     const gs::MmaProduct q{dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
-                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE};
+                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
   return GS_OK;

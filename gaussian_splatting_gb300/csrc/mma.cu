@@ -509,10 +509,10 @@ bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, 
 }
 
 bool mma_takes(const MmaProduct& p) {
-  const int64_t a_rows = p.a_mn ? p.k : p.m, b_rows = p.b_mn ? p.k : p.n;
-  return rows_aligned16(p.a, a_rows, p.lda, GS_BF16) && rows_aligned16(p.b, b_rows, p.ldb, GS_BF16) &&
-         rows_aligned16(p.y, p.m, p.ldy, GS_BF16) && (!p.z || rows_aligned16(p.z, p.m, p.ldz, GS_BF16)) &&
-         (!p.residual || rows_aligned16(p.residual, p.m, p.ldr, GS_BF16));
+  return tma_takes(p.a, p.a_mn ? p.k : p.m, (p.a_mn ? p.m : p.k) + p.a_pad, p.lda, GS_BF16) &&
+         tma_takes(p.b, p.b_mn ? p.k : p.n, (p.b_mn ? p.n : p.k) + p.b_pad, p.ldb, GS_BF16) &&
+         tma_takes(p.y, p.m, p.n, p.ldy, GS_BF16) && (!p.z || tma_takes(p.z, p.m, p.n, p.ldz, GS_BF16)) &&
+         (!p.residual || tma_takes(p.residual, p.m, p.n, p.ldr, GS_BF16));
 }
 
 size_t mma_workspace(int64_t m, int64_t n, int64_t k) {
@@ -551,8 +551,10 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   int stages = (room - (p.resident ? b_bytes * pl.kblocks : 0)) / stage;
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   const int smem = 1024 + kSmemCtl + (p.resident ? b_bytes * pl.kblocks : 0) + p.stages * stage + epi;
-  bool ok = q.a_mn ? encode_map(&p.a, q.a, q.k, q.m, q.lda, 64, GS_BF16) : encode_map(&p.a, q.a, q.m, q.k, q.lda, kTileM, GS_BF16);
-  ok = ok && (q.b_mn ? encode_map(&p.b, q.b, q.k, q.n, q.ldb, 64, GS_BF16) : encode_map(&p.b, q.b, q.n, q.k, q.ldb, pl.bn / pl.ctas, GS_BF16));
+  bool ok = q.a_mn ? encode_map(&p.a, q.a, q.k, q.m + q.a_pad, q.lda, 64, GS_BF16)
+                   : encode_map(&p.a, q.a, q.m, q.k + q.a_pad, q.lda, kTileM, GS_BF16);
+  ok = ok && (q.b_mn ? encode_map(&p.b, q.b, q.k, q.n + q.b_pad, q.ldb, 64, GS_BF16)
+                    : encode_map(&p.b, q.b, q.n, q.k + q.b_pad, q.ldb, pl.bn / pl.ctas, GS_BF16));
   if (!p.part) {
     ok = ok && encode_map(&p.y, q.y, q.m, q.n, q.ldy, 32, GS_BF16, 64);
     if (q.z) ok = ok && encode_map(&p.z, q.z, q.m, q.n, q.ldz, 32, GS_BF16, 64);

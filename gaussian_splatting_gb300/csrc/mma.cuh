@@ -21,6 +21,7 @@ struct MmaProduct {
   void* z;
   int64_t ldr, ldy, ldz;
   int act;
+  int64_t a_pad = 0, b_pad = 0;  // zeros that follow each of the operand's rows in memory
 };
 
 // bfloat16 whose rows start anywhere (mma_staged.cu).
@@ -42,7 +43,7 @@ inline int wait_tries() {
   return n < 0x7fffffff ? (int)n : 0x7fffffff;
 }
 
-// whether every array of the product starts its rows on 16-byte boundaries (bfloat16)
+// whether TMA takes every array of the product (bfloat16)
 bool mma_takes(const MmaProduct& p);
 // bytes of scratch for a product of these sizes (0: none), whatever its arrays
 size_t mma_workspace(int64_t m, int64_t n, int64_t k);

@@ -45,7 +45,7 @@ constexpr int kBufBytes = 32 * 32 * 4;  // an epilogue warp's 32 x 32 piece
 constexpr int kChunk = 8;          // k blocks between two additions in registers
 
 // How an array of the epilogue is read or written: a column per lane; 32 x 32 boxes by TMA, where its rows start
-// on 16-byte boundaries; or 32 whole rows at a time as one run of bytes, where they follow each other without
+// and end on 16-byte boundaries; or 32 whole rows at a time as one run of bytes, where they follow each other without
 // gaps and one tile holds all columns (a 59-column record).
 enum Way { kPlain, kBox, kDense };
 
@@ -786,6 +786,7 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
     std::swap(q.lda, q.ldb);
     std::swap(q.a_mn, q.b_mn);
     std::swap(q.m, q.n);
+    std::swap(q.a_pad, q.b_pad);
   }
   if (pl.bn == 128 && pl.splits == 1 && (q.residual || q.z)) {  // their buffers and registers leave no room for 128 columns
     pl.bn = 64;
@@ -798,14 +799,15 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
   p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
   p.kb_per_split = pl.kb_per_split;
   p.a_mn = q.a_mn, p.b_mn = q.b_mn;
-  p.a_tma = rows_aligned16(q.a, q.a_mn ? q.k : q.m, q.lda, GS_F32);
-  p.b_tma = rows_aligned16(q.b, q.b_mn ? q.k : q.n, q.ldb, GS_F32);
+  p.a_tma = tma_takes(q.a, q.a_mn ? q.k : q.m, (q.a_mn ? q.m : q.k) + q.a_pad, q.lda, GS_F32);
+  p.b_tma = tma_takes(q.b, q.b_mn ? q.k : q.n, (q.b_mn ? q.n : q.k) + q.b_pad, q.ldb, GS_F32);
   bool ok = true;
   if (p.a_tma)
-    ok = q.a_mn ? encode_map(&p.map_a, q.a, q.k, q.m, q.lda, 32, GS_F32) : encode_map(&p.map_a, q.a, q.m, q.k, q.lda, kTileM, GS_F32);
+    ok = q.a_mn ? encode_map(&p.map_a, q.a, q.k, q.m + q.a_pad, q.lda, 32, GS_F32)
+                : encode_map(&p.map_a, q.a, q.m, q.k + q.a_pad, q.lda, kTileM, GS_F32);
   if (p.b_tma)
-    ok = ok && (q.b_mn ? encode_map(&p.map_b, q.b, q.k, q.n, q.ldb, 32, GS_F32)
-                       : encode_map(&p.map_b, q.b, q.n, q.k, q.ldb, pl.bn, GS_F32));
+    ok = ok && (q.b_mn ? encode_map(&p.map_b, q.b, q.k, q.n + q.b_pad, q.ldb, 32, GS_F32)
+                       : encode_map(&p.map_b, q.b, q.n, q.k + q.b_pad, q.ldb, pl.bn, GS_F32));
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   p.bias = static_cast<const float*>(q.bias), p.residual = static_cast<const float*>(q.residual);
   p.y = static_cast<float*>(q.y), p.z = static_cast<float*>(q.z), p.ldr = q.ldr, p.ldy = q.ldy, p.ldz = q.ldz;
@@ -816,7 +818,7 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
     auto way = [&](const void* at, int64_t ld, CUtensorMap* map, int& w) {
       w = kPlain;
       if (!at) return true;
-      if (rows_aligned16(at, q.m, ld, GS_F32)) {
+      if (tma_takes(at, q.m, q.n, ld, GS_F32)) {
         w = kBox;
         return encode_map(map, at, q.m, q.n, ld, 32, GS_F32);
       }

@@ -453,8 +453,8 @@ gs_status gs_densify(const float* params, const float* exp_avg, const float* exp
  *
  * Matrices are row-major with a stride between rows, in elements (ld*; at least the width), of
  * one element type for every array of a call unless a comment says otherwise.  Any width,
- * stride and element-aligned address is valid; calls whose rows all start on 16-byte boundaries
- * run faster.  Sums, products, activations and statistics are computed in 32 bits (bfloat16
+ * stride and element-aligned address is valid; calls whose rows all start and end on 16-byte
+ * boundaries run faster.  Sums, products, activations and statistics are computed in 32 bits (bfloat16
  * products are exact, their sums 32-bit) and rounded once when stored.
  */
 typedef enum { GS_F32 = 0, GS_BF16 = 1 } gs_dtype;

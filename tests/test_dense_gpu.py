@@ -254,6 +254,61 @@ def test_linear_takes_any_stride_and_alignment_and_leaves_the_gaps(dtype, pad, s
     gaps_kept(fdw, n_out, n_in)
 
 
+def _view(m, n, ld, dtype, fill, seed=None, std=1.0):
+    """(whole, view): an [m, n] view of rows of ld elements whose other elements are `fill`."""
+    whole = torch.full((m, ld), fill, dtype=dtype, device="cuda")
+    view = whole[:, :n]
+    if seed is not None:
+        view.copy_(_rand((m, n), dtype, seed, std))
+    return whole, view
+
+
+# widths that end inside a 16-byte unit of rows that start on one, few rows and many, every kernel
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(9, 61, 59), (300, 57, 62), (40_000, 59, 61), (20_000, 125, 258), (9000, 270, 35)], ids=str)
+def test_what_lies_between_the_rows_is_neither_read_nor_written(shape, dtype):
+    rows, n_in, n_out = shape
+    up = lambda n: (n + 7) // 8 * 8 + 8  # noqa: E731
+    nan = math.nan
+    _, x = _view(rows, n_in, up(n_in), dtype, nan, 1)
+    _, w = _view(n_out, n_in, up(n_in), dtype, nan, 2, 1 / math.sqrt(n_in))
+    _, r = _view(rows, n_out, up(n_out), dtype, nan, 4)
+    _, dy = _view(rows, n_out, up(n_out), dtype, nan, 5, 1e-3)
+    b = _rand((n_out,), dtype, 3, 0.3)
+
+    def kept(whole, n):
+        assert (whole[:, n:] == 7).all()
+
+    for act in ("none", "gelu"):
+        wy, y = _view(rows, n_out, up(n_out), dtype, 7)
+        wz, z = _view(rows, n_out, up(n_out), dtype, 7)
+        dense.linear_fwd(x, w, b, r, act=act, out=y, z=z)
+        Y, ey, Z, ez = _linear_tolerances(x, w, b, r, act)
+        _close(y, Y, ey, "y")
+        _close(z, Z, ez, "z")
+        kept(wy, n_out)
+        kept(wz, n_out)
+        wz[:, n_out:] = nan
+        wdx, dx = _view(rows, n_in, up(n_in), dtype, 7)
+        wdw, dw = _view(n_out, n_in, up(n_in), dtype, 7)
+        _, _, db = dense.linear_bwd(dy, x, w, z, act=act, dx=dx, dw=dw)
+        want = _linear_grads(dy, x, w, z, act)
+        for k, v in (("dx", dx), ("dw", dw), ("db", db)):
+            _close(v, *want[k], k)
+        kept(wdx, n_in)
+        kept(wdw, n_in)
+    gamma, beta = _rand((n_in,), dtype, 6), _rand((n_in,), dtype, 7)
+    wy, y = _view(rows, n_in, up(n_in), dtype, 7)
+    _, mean, rstd = dense.layernorm_fwd(x, gamma, beta, out=y)
+    small, m2, r2 = dense.layernorm_fwd(x.contiguous(), gamma, beta)
+    assert torch.isfinite(y.float()).all() and torch.allclose(y.float(), small.float(), rtol=2e-2, atol=2e-2)
+    kept(wy, n_in)
+    wdx, dx = _view(rows, n_in, up(n_in), dtype, 7)
+    _, dg, db = dense.layernorm_bwd(x, x, gamma, mean, rstd, skip=x, dx=dx)
+    assert all(torch.isfinite(t.float()).all() for t in (dx, dg, db))
+    kept(wdx, n_in)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_linear_residual_in_place_and_partial_outputs(dtype):
     rows, n = 1500, 96
