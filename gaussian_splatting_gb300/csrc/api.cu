@@ -12,6 +12,7 @@ namespace {
 thread_local std::string g_last_error;
 std::atomic<int64_t> g_wait_limit{int64_t(1) << 22};
 std::atomic<int> g_drop_publish{0};
+std::atomic<int> g_drop_copy{0};
 }  // namespace
 
 namespace gs {
@@ -35,6 +36,7 @@ gs_status check_launch(const char* what) {
 int64_t wait_limit() { return g_wait_limit.load(); }
 
 int take_drop_publish() { return g_drop_publish.exchange(0); }
+int take_drop_copy() { return g_drop_copy.exchange(0); }
 
 cudaError_t max_dynamic_smem(const void* fn, int bytes) {
   // the attribute belongs to a device: remembered per device (and kernel, and size), so
@@ -84,6 +86,9 @@ void gs_debug_set_wait_limit(int64_t iterations) {
   g_wait_limit.store(iterations < 1 ? (int64_t(1) << 22) : iterations);
 }
 
-void gs_debug_drop_publish(int mode) { g_drop_publish.store(mode == 1 || mode == 2 ? mode : 0); }
+void gs_debug_drop_publish(int mode) {
+  g_drop_publish.store(mode == 1 || mode == 2 ? mode : 0);
+  g_drop_copy.store(mode == 3 ? 1 : 0);
+}
 
 }  // extern "C"

@@ -16,6 +16,7 @@ gs_status set_error(gs_status s, const char* fmt, ...);
 gs_status check_launch(const char* what);
 int64_t wait_limit();
 int take_drop_publish();
+int take_drop_copy();
 int num_sms();
 // cudaFuncSetAttribute(fn, MaxDynamicSharedMemorySize, bytes) for the current device, made once
 // per device (and kernel) -- the attribute is per device, so a second device gets its own call

@@ -55,8 +55,8 @@ struct Args {
   float* part;  // [splits][m][ldp] when splits > 1: no epilogue
   int64_t ldp;
   int32_t* status;
-  int wait_limit;
-  int drop;
+  int wait_limit;  // microseconds
+  int drop;        // test hook: nothing is copied in, every wait for it runs out
 };
 
 // ---------------------------------------------------------------- epilogue
@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
       }
       if (!ok && rank == 0) {  // gave up: no copy, of either block, may be in flight when it ends
         for (int i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
-          for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1)); ++j) {}
+          tc::mbar_drain(bar(ctl.full[i % p.stages]), (uint32_t)(i / p.stages & 1), p.wait_limit);
         if (p.resident)
-          for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.resident), 0); ++j) {}
+          tc::mbar_drain(bar(ctl.resident), 0, p.wait_limit);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
         if (tc::elect_one()) tc::mma_commit<CTAS>(bar(ctl.drain));
         __syncwarp();
-        for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+        tc::mbar_drain(bar(ctl.drain), 0, p.wait_limit);
       }
     }
   } else {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
     }
     if (!ok && lane == 0) {  // gave up: the pieces in flight land before the block ends
       for (uint32_t i = e.loads; i < e.issued; ++i)
-        for (int j = 0; j < p.wait_limit && !tc::mbar_try(e.res_bar + 8 * (i & 1), i >> 1 & 1); ++j) {}
+        tc::mbar_drain(e.res_bar + 8 * (i & 1), i >> 1 & 1, p.wait_limit);
     }
     if (tc::elect_one()) tc::bulk_wait0();
   }
@@ -530,7 +530,7 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   p.a_mn = q.a_mn, p.b_mn = q.b_mn;
   p.tmem_cols = pl.bn <= 64 ? 128 : pl.bn <= 128 ? 256 : 512;
   p.act = q.act, p.bias = static_cast<const bf16*>(q.bias);
-  p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
+  p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
   p.ldp = pl.ldp;
   p.bufs_y = 1;
   if (pl.splits > 1) p.part = static_cast<float*>(workspace);

@@ -37,8 +37,8 @@ gs_status f32_run(const MmaProduct& p, void* workspace, int32_t* status, cudaStr
 bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, int32_t dtype,
                 int row_bytes = 128);
 
-// the bound of a device-side wait, in tries of about a microsecond
-inline int wait_tries() {
+// the bound of a device-side wait in microseconds: the number of iterations that the sorts' waits have
+inline int wait_us() {
   const int64_t n = wait_limit();
   return n < 0x7fffffff ? (int)n : 0x7fffffff;
 }

@@ -77,8 +77,8 @@ struct Args {
   float* part;  // [splits][m][ldp] when splits > 1: no epilogue
   int64_t ldp;
   int32_t* status;
-  int wait_limit;
-  int drop;
+  int wait_limit;  // microseconds
+  int drop;        // test hook: nothing is copied in, every wait for it runs out
 };
 
 __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m0, int64_t& n0, int& split) {
@@ -151,7 +151,7 @@ struct Operand {
         const bool ci = x0 + c + lane < ext;
         const float* src = ci ? p + (k0 + w) * ld + x0 + c + lane : p;
         const int64_t by = ci ? step : 0;
-#pragma unroll
+#pragma unroll 4
         for (int t = 0; t < 32 / kWarps; ++t, src += by) {
           const bool in = t * kWarps < rows;
           copy_word(at[t & 1] + c * 128 + t * (kWarps * 128), in ? src : p, in && ci);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       }
       if (!ok && bytes) {  // gave up: no copy may be in flight when the block ends
         for (int i = it < p.raws ? 0 : it - p.raws; i < it; ++i)
-          for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.raw_full[i % p.raws]), (uint32_t)(i / p.raws & 1)); ++j) {}
+          tc::mbar_drain(bar(ctl.raw_full[i % p.raws]), (uint32_t)(i / p.raws & 1), p.wait_limit);
       }
     }
   } else if (warp >= kEpiWarps && warp < kEpiWarps + kSplitWarps) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
         if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
         __syncwarp();
-        for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+        tc::mbar_drain(bar(ctl.drain), 0, p.wait_limit);
       }
     }
   } else {
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok)  // gave up: the copies in flight land before the block ends
       if (res_flying)
-        for (int j = 0; j < p.wait_limit && !tc::mbar_try(res_bar, (uint32_t)(res_used & 1)); ++j) {}
+        tc::mbar_drain(res_bar, (uint32_t)(res_used & 1), p.wait_limit);
     if (tc::elect_one()) tc::bulk_wait0();
   }
   __syncwarp();
@@ -828,7 +828,7 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
     if (!way(q.y, q.ldy, &p.map_y, p.y_way) || !way(q.z, q.ldz, &p.map_z, p.z_way) || !way(q.residual, q.ldr, &p.map_r, p.r_way))
       return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   }
-  p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
+  p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
   if (gs_status s = launch_any(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, pl.swap},

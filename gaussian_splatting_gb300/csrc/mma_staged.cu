@@ -50,8 +50,8 @@ struct Args {
   float* part;  // [splits][m][ldp] when splits > 1: no epilogue
   int64_t ldp;
   int32_t* status;
-  int wait_limit;
-  int drop;
+  int wait_limit;  // microseconds
+  int drop;        // test hook: nothing is copied in, every wait for it runs out
 };
 
 __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m0, int64_t& n0, int& split) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
         if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
         __syncwarp();
-        for (int j = 0; j < p.wait_limit && !tc::mbar_try(bar(ctl.drain), 0); ++j) {}
+        tc::mbar_drain(bar(ctl.drain), 0, p.wait_limit);
       }
     }
   } else {
@@ -431,7 +431,7 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
   p.act = q.act;
   p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   p.ldp = pl.ldp;
-  p.status = status, p.wait_limit = wait_tries(), p.drop = 0;
+  p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
   if (gs_status s = pl.bn == 64 ? launch<64>(p, pl, st, where) : launch<128>(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},

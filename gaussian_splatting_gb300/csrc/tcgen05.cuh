@@ -49,23 +49,43 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
 // What a block's threads share about giving up: `dead` in shared memory, the caller's status word.
 struct Guard {
   volatile uint32_t* dead;
   int32_t* status;
-  int limit;  // tries of one wait
+  int limit;  // of one wait, in microseconds
 };
+
+// The phase with this parity, or `limit` microseconds
+__device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, int limit, const volatile uint32_t* dead) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t end = now_ns() + (uint64_t)limit * 1000;
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (dead && *dead) return false;
+  } while (now_ns() < end);
+  return false;
+}
 
 // Waits for the phase with this parity; false if the limit ran out here or elsewhere in the block.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Guard& g) {
-  if (mbar_try(bar, parity)) return true;
-  for (int i = 1; i < g.limit; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 15) == 15 && *g.dead) return false;
-  }
+  if (mbar_wait_for(bar, parity, g.limit, g.dead)) return true;
   *g.dead = 1u;
   if (g.status) atomicOr(g.status, 2);
   return false;
+}
+
+// After giving up: what is in flight on this barrier lands, or the limit runs out once more.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, int limit) {
+  mbar_wait_for(bar, parity, limit, nullptr);
 }
 
 // The same for a whole warp that goes on together: one answer for all its lanes.

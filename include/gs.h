@@ -348,10 +348,11 @@ gs_status gs_probe_ffma(float* out, int blocks, int iters, void* stream);
  * Test hooks (no counterpart in the method).
  * gs_debug_set_wait_limit: iterations a device-side wait (a grid barrier of gs_bin_sort's
  *   cooperative launches) spins before it gives up and reports status bit 2 (default
- *   1 << 22; values < 1 restore it).
+ *   1 << 22; values < 1 restore it).  The linear layers' waits take it as microseconds.
  * gs_debug_drop_publish: arms the next gs_bin_sort call only.  mode 1: CTA 0 of the tile
  *   sort never arrives at its first grid barrier; mode 2: the same in the depth sort; every
- *   other CTA's barrier wait then runs out; 0 disarms.  Used to test that the bounded waits
+ *   other CTA's barrier wait then runs out; 0 disarms.  mode 3 arms the next tensor-core
+ *   product of gs_linear_fwd / gs_linear_bwd instead: it never copies its operands in.  Used to test that the bounded waits
  *   report GS_ERR_TIMEOUT instead of hanging.
  */
 void gs_debug_set_wait_limit(int64_t iterations);

@@ -550,3 +550,30 @@ def test_status_stays_clear():
     y, _ = dense.linear_fwd(x, w, status=status)
     dense.linear_bwd(y, x, w, status=status)
     assert status.item() == 0
+
+
+@pytest.mark.parametrize("case", ["f32", "f32 residual", "bf16", "bf16 pair", "bf16 residual", "bf16 unaligned"])
+def test_a_wait_that_runs_out_sets_the_status_and_leaves_the_device_usable(case):
+    """A product whose operands never arrive (a test hook): every role gives up after 2 ms, the status word says
+    so, and the next call is right."""
+    dtype = F32 if case.startswith("f32") else BF16
+    rows, n_in, n_out = (20_000, 1024, 512) if "pair" in case else (3000, 304 if "unaligned" not in case else 301, 136)
+    x, w = _rand((rows, n_in), dtype, 1), _rand((n_out, n_in), dtype, 2, 0.05)
+    r = _rand((rows, n_out), dtype, 3) if "residual" in case else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want, _ = dense.linear_fwd(x, w, None, r, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    lib = N.load()
+    try:
+        lib.gs_debug_set_wait_limit(2000)
+        lib.gs_debug_drop_publish(3)
+        dense.linear_fwd(x, w, None, r, status=status)
+        torch.cuda.synchronize()
+    finally:
+        lib.gs_debug_set_wait_limit(0)
+        lib.gs_debug_drop_publish(0)
+    assert status.item() == 2
+    status.zero_()
+    y, _ = dense.linear_fwd(x, w, None, r, status=status)
+    assert status.item() == 0 and torch.equal(y, want)
