@@ -1,15 +1,16 @@
-// bfloat16 products whose operands pass through registers on their way to the tensor cores: those whose
-// rows do not start on 16-byte boundaries, which TMA cannot copy.
+// bfloat16 products whose operands TMA cannot copy: those whose rows do not start and end on 16-byte boundaries.
 //
 // C(m, n) = sum over k of A(m, k) B(n, k) and the epilogue as in mma.cu.
 // Warps of the one persistent block per SM:
-//   warps 8 - 15  load pieces of A and B (16-byte loads where rows start on such boundaries, single
-//                 elements where not) and store them to a shared-memory stage in the tensor core's
-//                 128-byte-swizzled layout; the next pieces' loads are in flight meanwhile.  B stays
+//   warps 8 - 15  load segments of 64 neighbouring elements of A and B by words (a word per lane, coalesced), shift
+//                 them to the segment's alignment and store them to a stage in the tensor core's
+//                 128-byte-swizzled layout; the next k block's words are in flight meanwhile.  B stays
 //                 resident where all of its k fits.
 //   warp 16       issues tcgen05.mma
 //   warps 0 - 7   read the accumulators and write C: 32 x 32 pieces through shared memory, so that the
 //                 epilogue reads and writes whole rows of 32 columns at any alignment
+// (What did not do, 300K x 255 -> 257: eight elements per lane, loaded one by one, 16 cache lines per load, 634 us;
+// cp.async by words, one per 13 cycles and SM, 481 us without epilogue.)
 #include "mma.cuh"
 #include "tcgen05.cuh"
 
@@ -18,7 +19,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kEpiWarps = 8, kLoadWarps = 8;
-constexpr int kLoaders = 32 * kLoadWarps;
 constexpr int kThreads = 32 * (kEpiWarps + kLoadWarps + 1);
 constexpr int kTileM = 128, kTileK = 64;
 constexpr int kMaxStages = 6;
@@ -39,8 +39,8 @@ struct Args {
   int64_t lda, ldb;
   int64_t m, n, k;
   int m_tiles, n_tiles, splits, kblocks, kb_per_split;
-  int stages, resident;
-  int a_mn, b_mn, a_vec, b_vec;
+  int stages;
+  int a_mn, b_mn;
   const bf16* bias;
   const bf16* residual;
   bf16* y;
@@ -69,62 +69,111 @@ __device__ __forceinline__ void tile_of(const Args& p, int bn, int t, int64_t& m
   m0 = (int64_t)mt * kTileM;
 }
 
-// 8 consecutive elements at p, those at or past `left` as zeros
-__device__ __forceinline__ uint4 load8(const bf16* p, int64_t left, bool vec) {
-  if (vec && left >= 8) return *reinterpret_cast<const uint4*>(p);
-  uint16_t e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = i < left ? reinterpret_cast<const uint16_t*>(p)[i] : 0;
-  return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
-                    e[6] | (uint32_t)e[7] << 16);
-}
-
-// One operand as the loaders see it: pieces of EXT (m or n) x 16 (one step of the tensor core), a unit
-// of 8 elements per thread.
-constexpr int kPieces = kTileK / 16;  // of a k block
-constexpr int kDepth = 3;             // pieces of a thread in registers, all but one of them in flight
+// One operand as the loaders see it.  A k block of EXT (m or n) x 64 (k) is EXT segments of 64 neighbouring
+// elements in memory, 128 bytes of the stage each: a row each of an operand stored [x][k]; of one stored
+// [k][x], 64 rows of each 64 columns.  Warp w has the segments w, w + 8, ...: eight of each 64.
+constexpr int kSegs = 64 / kLoadWarps;
 
 template <int EXT>
 struct Operand {
-  static_assert(EXT * 2 <= kLoaders, "one unit per thread");
+  static constexpr int kGroups = EXT / 64;
+  // a warp's words of a k block: word l of a segment in lane l, the 33rd of segment i in lane i
+  struct Words {
+    uint32_t word[kGroups][kSegs], last[kGroups];
+  };
   const bf16* p;
   int64_t ld, ext, k;
-  bool mn, vec;
+  bool mn;
+  uintptr_t lo, hi;  // the array's bytes
 
-  // the unit of thread tid: its row or column x, its k, and its place in a plane; whether it has one
-  __device__ __forceinline__ bool place(int tid, int piece, int& x, int& kk, int& at) const {
+  // A warp's segments of the c-th 64 of the block at (x0, k0): the first one's address, the bytes between two,
+  // how many elements of each are in the matrix, how many segments are.  `skip`: those that are not would only
+  // reach sums that are not stored, and are not written; else they are zeros.
+  struct View {
+    uintptr_t at;
+    int64_t step;
+    int left, rows;
+    bool skip, inside;  // inside: all segments are there, and all their words lie in the array
+  };
+  __device__ __forceinline__ View view(int warp, int c, int64_t x0, int64_t k0) const {
+    View v;
+    int64_t row, col, n, rows;
     if (!mn) {
-      x = tid >> 1;
-      const int u = (tid & 1) + 2 * piece;
-      kk = u * 8;
-      at = x * 128 + ((u ^ (x & 7)) << 4);
+      row = x0 + c * 64 + warp, col = k0;
+      n = k - k0, rows = ext - row, v.skip = true;
     } else {
-      const int u = tid % (EXT / 8);
-      kk = tid / (EXT / 8) + 16 * piece;
-      x = u * 8;
-      at = (u >> 3) * (kTileK * 128) + kk * 128 + (((u & 7) ^ (kk & 7)) << 4);
+      row = k0 + warp, col = x0 + c * 64;
+      n = ext - col, rows = k - row, v.skip = n <= 0;
     }
-    return tid < EXT * 2;
+    v.left = (int)min(n, (int64_t)64);
+    v.rows = n <= 0 || rows <= 0 ? 0 : (int)min((rows + kLoadWarps - 1) / kLoadWarps, (int64_t)kSegs);
+    v.at = reinterpret_cast<uintptr_t>(p + row * ld + col);
+    v.step = ld * (2 * kLoadWarps);
+    v.inside = v.rows == kSegs && v.at >= lo + 2 && v.at + (kSegs - 1) * v.step + 2 * 64 + 4 <= hi;
+    return v;
   }
-  __device__ __forceinline__ uint4 load(int tid, int piece, int64_t x0, int64_t k0) const {
-    int x, kk, at;
-    const bool mine = place(tid, piece, x, kk, at);
-    const int64_t gx = x0 + x, gk = k0 + kk;
-    if (!mine || gx >= ext) return make_uint4(0u, 0u, 0u, 0u);
-    if (!mn) return load8(p + gx * ld + gk, k - gk, vec);
-    return load8(p + gk * ld + gx, gk < k ? ext - gx : 0, vec);
+  __device__ __forceinline__ void load(int warp, int lane, int64_t x0, int64_t k0, Words& f) const {
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      const View v = view(warp, c, x0, k0);
+      uintptr_t at = v.at;
+      if (v.inside) {
+        // (elements past `left` are read too where they lie in the array, and cut off later)
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i, at += v.step)
+          f.word[c][i] = *reinterpret_cast<const uint32_t*>((at & ~uintptr_t(3)) + 4 * lane);
+        if (lane < kSegs)
+          f.last[c] = *reinterpret_cast<const uint32_t*>(((v.at + lane * v.step) & ~uintptr_t(3)) + 128);
+      } else {
+        // words that lie in the array as a whole; the two that may not are seen to in shift()
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i, at += v.step) {
+          const uintptr_t word = (at & ~uintptr_t(3)) + 4 * lane;
+          f.word[c][i] = 0;
+          if (i < v.rows && word >= lo && word + 4 <= hi) f.word[c][i] = *reinterpret_cast<const uint32_t*>(word);
+        }
+        const uintptr_t word = ((v.at + lane * v.step) & ~uintptr_t(3)) + 128;
+        f.last[c] = 0;
+        if (lane < v.rows && word + 4 <= hi) f.last[c] = *reinterpret_cast<const uint32_t*>(word);
+      }
+    }
   }
-  // Rows and columns outside of the matrix are not written: they only reach sums that are not stored.
-  __device__ __forceinline__ void store(int tid, int piece, int64_t x0, unsigned char* stage, uint4 v) const {
-    int x, kk, at;
-    if (place(tid, piece, x, kk, at) && x0 + x < ext) *reinterpret_cast<uint4*>(stage + at) = v;
+  __device__ __forceinline__ void shift(int warp, int lane, int64_t x0, int64_t k0, const Words& f, uint32_t stage) const {
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      const View v = view(warp, c, x0, k0);
+      if (v.skip && v.rows == 0) continue;
+      uintptr_t at = v.at;
+      // segments 8 further have the same swizzle
+      const uint32_t to = stage + (c * 64 + warp) * 128 + (((lane >> 2) ^ (warp & 7)) << 4) + (lane & 3) * 4;
+      const uint32_t keep = 2 * lane + 1 < v.left ? 0xffffffffu : 2 * lane < v.left ? 0xffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i, at += v.step) {
+        uint32_t next = __shfl_down_sync(0xffffffffu, f.word[c][i], 1);
+        const uint32_t last = __shfl_sync(0xffffffffu, f.last[c], i);
+        if (lane == 31) next = last;
+        uint32_t e = __funnelshift_r(f.word[c][i], next, (uint32_t)(at & 2) * 8) & keep;
+        if (!v.inside) {
+          if (i >= v.rows) {
+            e = 0;
+          } else if ((at & ~uintptr_t(3)) < lo || at + 2 * v.left + 2 > hi) {
+            // a segment with the array's first or last word: element by element
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(at) + 2 * lane;
+            e = 2 * lane < v.left ? q[0] : 0;
+            if (2 * lane + 1 < v.left) e |= (uint32_t)q[1] << 16;
+          }
+        }
+        if (i < v.rows || !v.skip)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * (kLoadWarps * 128)), "r"(e) : "memory");
+      }
+    }
   }
 };
 
-// Where a loader stands: tile t, k block kb of [.., k_hi), piece h.
+// Where a loader stands: tile t, k block kb of [.., k_hi).
 struct Cursor {
   int64_t m0, n0;
-  int t, kb, k_hi, h;
+  int t, kb, k_hi;
 };
 
 __device__ __forceinline__ void seek(const Args& p, int bn, Cursor& c, int total) {
@@ -133,19 +182,24 @@ __device__ __forceinline__ void seek(const Args& p, int bn, Cursor& c, int total
   tile_of(p, bn, c.t, c.m0, c.n0, split);
   c.kb = split * p.kb_per_split;
   c.k_hi = min(c.kb + p.kb_per_split, p.kblocks);
-  c.h = 0;
 }
 
 __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int total) {
-  if (++c.h < kPieces) return;
-  c.h = 0;
   if (++c.kb == c.k_hi) {
     c.t += gridDim.x;
     seek(p, bn, c, total);
   }
 }
 
-template <int BN>
+template <int ACT>
+__device__ __forceinline__ void activate(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], ACT);
+}
+
+// RESIDENT: B's parts are in shared memory from the start, and the loaders hold two k blocks of A's words in
+// turn; else one of A's and B's.
+template <int BN, bool RESIDENT>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constant__ Args p) {
   constexpr int kABytes = kTileM * kTileK * 2, kBBytes = BN * kTileK * 2;
   constexpr int kTmem = BN * 2;  // columns, two tiles in flight
@@ -153,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
   unsigned char* res_b = smem + kSmemCtl;
-  unsigned char* ring = res_b + (p.resident ? (size_t)kBBytes * p.kblocks : 0);
-  const int stage_bytes = kABytes + (p.resident ? 0 : kBBytes);
+  unsigned char* ring = res_b + (RESIDENT ? (size_t)kBBytes * p.kblocks : 0);
+  const int stage_bytes = kABytes + (RESIDENT ? 0 : kBBytes);
   unsigned char* epi = ring + (size_t)stage_bytes * p.stages;
   const int warp = tc::warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
@@ -182,18 +236,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
 
   if (warp >= kEpiWarps && warp < kEpiWarps + kLoadWarps) {
     // ------------------------------------------------------------ loaders
-    const int tid = threadIdx.x - 32 * kEpiWarps;
-    const Operand<kTileM> a{p.a, p.lda, p.m, p.k, p.a_mn != 0, p.a_vec != 0};
-    const Operand<BN> b{p.b, p.ldb, p.n, p.k, p.b_mn != 0, p.b_vec != 0};
+    const int lw = warp - kEpiWarps;
+    auto operand = [](auto op, const bf16* q, int64_t ld, int64_t ext, int64_t k, bool mn) {
+      op.p = q, op.ld = ld, op.ext = ext, op.k = k, op.mn = mn;
+      op.lo = reinterpret_cast<uintptr_t>(q);
+      op.hi = reinterpret_cast<uintptr_t>(q + ((mn ? k : ext) - 1) * ld + (mn ? ext : k));
+      return op;
+    };
+    using OpA = Operand<kTileM>;
+    using OpB = Operand<BN>;
+    const OpA a = operand(OpA{}, p.a, p.lda, p.m, p.k, p.a_mn != 0);
+    const OpB b = operand(OpB{}, p.b, p.ldb, p.n, p.k, p.b_mn != 0);
     if (!p.drop) {
-      if (p.resident) {
+      if (RESIDENT && (int)blockIdx.x < total) {
         const int64_t n0 = (int64_t)(blockIdx.x % p.n_tiles) * BN;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          uint4 f[kPieces];
-#pragma unroll
-          for (int h = 0; h < kPieces; ++h) f[h] = b.load(tid, h, n0, (int64_t)kb * kTileK);
-#pragma unroll
-          for (int h = 0; h < kPieces; ++h) b.store(tid, h, n0, res_b + (size_t)kBBytes * kb, f[h]);
+          typename OpB::Words f;
+          b.load(lw, lane, n0, (int64_t)kb * kTileK, f);
+          b.shift(lw, lane, n0, (int64_t)kb * kTileK, f, tc::smem_addr(res_b) + kBBytes * kb);
         }
         tc::fence_async_smem();
         __syncwarp();
@@ -203,34 +263,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       cur.t = blockIdx.x;
       seek(p, BN, cur, total);
       Cursor ahead = cur;
-      uint4 fa[kDepth], fb[kDepth];
+      constexpr int kSets = RESIDENT ? 2 : 1;
+      typename OpA::Words fa[kSets];
+      typename OpB::Words fb;
       auto load = [&](int w) {
         if (ahead.t >= total) return;
-        fa[w] = a.load(tid, ahead.h, ahead.m0, (int64_t)ahead.kb * kTileK);
-        if (!p.resident) fb[w] = b.load(tid, ahead.h, ahead.n0, (int64_t)ahead.kb * kTileK);
+        a.load(lw, lane, ahead.m0, (int64_t)ahead.kb * kTileK, fa[w]);
+        if (!RESIDENT) b.load(lw, lane, ahead.n0, (int64_t)ahead.kb * kTileK, fb);
         advance(p, BN, ahead, total);
       };
       int s = 0;
       uint32_t parity = 1;
       bool ok = true;
-#pragma unroll
-      for (int w = 0; w + 1 < kDepth; ++w) load(w);
+      load(0);
       while (ok && cur.t < total) {
 #pragma unroll
-        for (int w = 0; w < kDepth; ++w) {  // the register sets alternate
+        for (int w = 0; w < kSets; ++w) {
           if (!ok || cur.t >= total) break;
-          load((w + kDepth - 1) % kDepth);
-          if (cur.h == 0) ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
+          if constexpr (kSets == 2) load(w ^ 1);
+          ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
           if (!ok) break;
-          unsigned char* st = ring + (size_t)stage_bytes * s;
-          a.store(tid, cur.h, cur.m0, st, fa[w]);
-          if (!p.resident) b.store(tid, cur.h, cur.n0, st + kABytes, fb[w]);
-          if (cur.h == kPieces - 1) {
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(ctl.full[s]));
-            if (++s == p.stages) s = 0, parity ^= 1;
-          }
+          const uint32_t st = tc::smem_addr(ring) + stage_bytes * s;
+          a.shift(lw, lane, cur.m0, (int64_t)cur.kb * kTileK, fa[w], st);
+          if (!RESIDENT) b.shift(lw, lane, cur.n0, (int64_t)cur.kb * kTileK, fb, st + kABytes);
+          if constexpr (kSets == 1) load(0);
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(ctl.full[s]));
+          if (++s == p.stages) s = 0, parity ^= 1;
           advance(p, BN, cur, total);
         }
       }
@@ -243,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       const uint32_t a_step = p.a_mn ? 16 * 128 : 32, b_step = p.b_mn ? 16 * 128 : 32;
       int it = 0, n_acc = 0;
       bool ok = true;
-      if (p.resident && blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
+      if (RESIDENT && (int)blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
       for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
         int64_t m0, n0;
         int split;
@@ -261,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
           if (!ok) break;
           tc::fence_after();
           const uint32_t as = tc::smem_addr(ring) + stage_bytes * s;
-          const uint32_t bs = p.resident ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
+          const uint32_t bs = RESIDENT ? tc::smem_addr(res_b) + kBBytes * kb : as + kABytes;
           if (tc::elect_one()) {
 #pragma unroll
             for (int i = 0; i < kTileK / 16; ++i)
@@ -302,48 +362,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       const uint32_t d = tmem + acc * BN + ((uint32_t)(quad * 32) << 16) + half * kCols;
       const int rows = (int)min((int64_t)32, p.m - row0);
       for (int c = 0; in && c < kCols; c += 32) {
-        float sum[32];
-        tc::tmem_load32(d + c, sum);
+        float v[32];
+        tc::tmem_load32(d + c, v);
         if (p.part) {
           const int64_t row = row0 + lane;
           if (row < p.m) {
             float* out = p.part + ((int64_t)split * p.m + row) * p.ldp + col0 + c;
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              if (col0 + c + i < p.ldp)
-                *reinterpret_cast<float4*>(out + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+              if (col0 + c + i < p.ldp) *reinterpret_cast<float4*>(out + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
           continue;
         }
-        // a lane owns a column from here on
+        // a lane owns a column from here on; all 32 rows at each step, so that their accesses overlap
         const int64_t col = col0 + c + lane;
         const bool ci = col < p.n;
-        const float bias = p.bias && ci ? __bfloat162float(p.bias[col]) : 0.f;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = sum[i];
+        for (int i = 0; i < 32; ++i) buf[lane * kPitch + i] = v[i];
         __syncwarp();
         if (!ci) continue;
-        const bf16* res = p.residual + row0 * p.ldr + col;
-        bf16* y = p.y + row0 * p.ldy + col;
-        bf16* z = p.z + row0 * p.ldz + col;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          bf16 rr[8];  // loads in flight
-          if (p.residual) {
+        bf16 rr[32];
+        if (p.residual) {
+          const bf16* res = p.residual + row0 * p.ldr + col;
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-              if (r0 + r < rows) rr[r] = res[(r0 + r) * p.ldr];
-          }
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            if (r0 + r >= rows) break;
-            float v = buf[(r0 + r) * kPitch + lane] + bias;
-            if (p.z) z[(r0 + r) * p.ldz] = __float2bfloat16_rn(v);
-            v = act_value(v, p.act);
-            if (p.residual) v += __bfloat162float(rr[r]);
-            y[(r0 + r) * p.ldy] = __float2bfloat16_rn(v);
-          }
+          for (int r = 0; r < 32; ++r, res += p.ldr)
+            if (r < rows) rr[r] = *res;
         }
+        const float bias = p.bias ? __bfloat162float(p.bias[col]) : 0.f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) v[r] = buf[r * kPitch + lane] + bias;
+        if (p.z) {
+          bf16* z = p.z + row0 * p.ldz + col;
+#pragma unroll
+          for (int r = 0; r < 32; ++r, z += p.ldz)
+            if (r < rows) *z = __float2bfloat16_rn(v[r]);
+        }
+        if (p.act == GS_ACT_RELU) activate<GS_ACT_RELU>(v);
+        else if (p.act == GS_ACT_GELU) activate<GS_ACT_GELU>(v);
+        else if (p.act == GS_ACT_SILU) activate<GS_ACT_SILU>(v);
+        bf16* y = p.y + row0 * p.ldy + col;
+#pragma unroll
+        for (int r = 0; r < 32; ++r, y += p.ldy)
+          if (r < rows) *y = __float2bfloat16_rn(p.residual ? v[r] + __bfloat162float(rr[r]) : v[r]);
       }
       tc::fence_before();
       __syncwarp();
@@ -367,13 +428,12 @@ struct Plan {
 
 constexpr int kSms = 152;  // the device's; only speed depends on it
 
-// 128 columns per tile where there are more than 64 and enough tiles; ranges of k of at least two blocks
-// (128) where there are too few tiles for the device.
-Plan plan_of(int64_t m, int64_t n, int64_t k) {
+// Ranges of k of at least two blocks (128) where there are too few tiles for the device.
+Plan plan_as(int bn, int64_t m, int64_t n, int64_t k) {
   Plan p;
   p.m_tiles = (int)ceil_div(m, kTileM);
   p.kblocks = (int)ceil_div(k, kTileK);
-  p.bn = n <= 64 || (int64_t)p.m_tiles * ceil_div(n, 128) < kSms / 2 ? 64 : 128;
+  p.bn = bn;
   p.n_tiles = (int)ceil_div(n, p.bn);
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
   int64_t splits = tiles >= kSms ? 1 : kSms / tiles;
@@ -384,25 +444,32 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
   p.ldp = ceil_div(n, 4) * 4;
   return p;
 }
+// Tiles of 64 columns: the words of both operands' blocks fit a loader's registers twice.
+Plan plan_of(int64_t m, int64_t n, int64_t k) { return plan_as(64, m, n, k); }
 
+// bytes of shared memory beside the stages, with B resident or not
 template <int BN>
+int64_t fixed_bytes(const Plan& pl, bool resident) {
+  return (int64_t)1024 + kSmemCtl + kEpiWarps * kBufBytes + (resident ? (int64_t)BN * kTileK * 2 * pl.kblocks : 0);
+}
+// resident B: one range of columns per block, and at least three stages of A beside it
+template <int BN>
+bool fits_resident(const Plan& pl) {
+  return pl.splits == 1 && pl.n_tiles <= 4 && (int64_t)pl.m_tiles * pl.n_tiles >= 2 * gs::num_sms() &&
+         fixed_bytes<BN>(pl, true) + 3 * kTileM * kTileK * 2 <= kSmemMost;
+}
+
+template <int BN, bool RESIDENT>
 gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
-  constexpr int kA = kTileM * kTileK * 2, kB = BN * kTileK * 2;
   const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = (int)(total < gs::num_sms() ? total : gs::num_sms());
-  const int room = kSmemMost - 1024 - kSmemCtl - kEpiWarps * kBufBytes;
-  // resident B: one range of columns per block, and at least two stages of A beside it
-  if (pl.splits == 1 && pl.n_tiles <= 4 && total >= 2 * grid && (int64_t)kB * pl.kblocks + 2 * kA <= room) {
-    p.resident = 1;
-    grid -= grid % pl.n_tiles;
-  }
-  const int stage = kA + (p.resident ? 0 : kB);
-  const int stages = (room - (p.resident ? kB * pl.kblocks : 0)) / stage;
+  if (RESIDENT) grid -= grid % pl.n_tiles;
+  const int64_t fixed = fixed_bytes<BN>(pl, RESIDENT);
+  const int stage = (kTileM + (RESIDENT ? 0 : BN)) * kTileK * 2, stages = (int)((kSmemMost - fixed) / stage);
   p.stages = stages < kMaxStages ? stages : kMaxStages;
-  const int smem = kSmemMost - room + (p.resident ? kB * pl.kblocks : 0) + p.stages * stage;
-  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN>, kSmemMost);
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN, RESIDENT>, kSmemMost);
   if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  k_mma_staged<BN><<<grid, kThreads, smem, st>>>(p);
+  k_mma_staged<BN, RESIDENT><<<grid, kThreads, (int)fixed + p.stages * stage, st>>>(p);
   return gs::check_launch(where);
 }
 
@@ -416,7 +483,11 @@ size_t staged_workspace(int64_t m, int64_t n, int64_t k) {
 }
 
 gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStream_t st, const char* where) {
-  const Plan pl = plan_of(q.m, q.n, q.k);
+  // of 128 where B stays resident, and is no part of what they hold
+  Plan pl = plan_of(q.m, q.n, q.k);
+  const Plan wide = plan_as(128, q.m, q.n, q.k);
+  const bool resident = q.n > 64 && fits_resident<128>(wide);
+  if (resident) pl = wide;
   if ((int64_t)pl.m_tiles * pl.n_tiles * pl.splits > 0x7fffffff)
     return set_error(GS_ERR_INVALID, "%s: too many tiles", where);
   Args p{};
@@ -424,15 +495,16 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
   p.m_tiles = pl.m_tiles, p.n_tiles = pl.n_tiles, p.splits = pl.splits, p.kblocks = pl.kblocks;
   p.kb_per_split = pl.kb_per_split;
   p.a_mn = q.a_mn, p.b_mn = q.b_mn;
-  p.a_vec = rows_aligned16(q.a, q.a_mn ? q.k : q.m, q.lda, GS_BF16);
-  p.b_vec = rows_aligned16(q.b, q.b_mn ? q.k : q.n, q.ldb, GS_BF16);
   p.bias = static_cast<const bf16*>(q.bias), p.residual = static_cast<const bf16*>(q.residual);
   p.y = static_cast<bf16*>(q.y), p.z = static_cast<bf16*>(q.z), p.ldr = q.ldr, p.ldy = q.ldy, p.ldz = q.ldz;
   p.act = q.act;
   p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   p.ldp = pl.ldp;
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
-  if (gs_status s = pl.bn == 64 ? launch<64>(p, pl, st, where) : launch<128>(p, pl, st, where)) return s;
+  if (gs_status s = resident                  ? launch<128, true>(p, pl, st, where)
+                    : fits_resident<64>(pl) ? launch<64, true>(p, pl, st, where)
+                                            : launch<64, false>(p, pl, st, where))
+    return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
               st);
