@@ -86,36 +86,42 @@ struct Operand {
   bool mn;
   uintptr_t lo, hi;  // the array's bytes
 
-  // A warp's segments of the c-th 64 of the block at (x0, k0): the first one's address, the bytes between two,
-  // how many elements of each are in the matrix, how many segments are.  `skip`: those that are not would only
-  // reach sums that are not stored, and are not written; else they are zeros.
+  // Where a warp's segments of the tile at x0 start, and what is left of the operand from there on (m or n).
+  // Kept by the loaders from block to block.
+  struct Spot {
+    uintptr_t at;
+    int rest;
+  };
+  __device__ __forceinline__ Spot spot(int warp, int64_t x0) const {
+    if (!mn) return {reinterpret_cast<uintptr_t>(p + (x0 + warp) * ld), (int)(ext - x0) - warp};
+    return {reinterpret_cast<uintptr_t>(p + warp * ld + x0), (int)(ext - x0)};
+  }
+  // A warp's segments of the c-th 64 of k block kb: the first one's address, the bytes between two, how many
+  // elements of each are in the matrix, how many segments are.  `skip`: those that are not would only reach sums
+  // that are not stored, and are not written; else they are zeros.
   struct View {
     uintptr_t at;
     int64_t step;
     int left, rows;
     bool skip, inside;  // inside: all segments are there, and all their words lie in the array
   };
-  __device__ __forceinline__ View view(int warp, int c, int64_t x0, int64_t k0) const {
+  __device__ __forceinline__ View view(int warp, const Spot& o, int c, int kb) const {
     View v;
-    int64_t row, col, n, rows;
-    if (!mn) {
-      row = x0 + c * 64 + warp, col = k0;
-      n = k - k0, rows = ext - row, v.skip = true;
-    } else {
-      row = k0 + warp, col = x0 + c * 64;
-      n = ext - col, rows = k - row, v.skip = n <= 0;
-    }
-    v.left = (int)min(n, (int64_t)64);
-    v.rows = n <= 0 || rows <= 0 ? 0 : (int)min((rows + kLoadWarps - 1) / kLoadWarps, (int64_t)kSegs);
-    v.at = reinterpret_cast<uintptr_t>(p + row * ld + col);
     v.step = ld * (2 * kLoadWarps);
+    const int k_left = (int)k - kb * kTileK;
+    const int along = (mn ? o.rest : k_left) - (mn ? c * 64 : 0), across = mn ? k_left - warp : o.rest - c * 64;
+    v.left = min(along, 64);
+    v.rows = v.left <= 0 ? 0 : max(0, min((across + kLoadWarps - 1) / kLoadWarps, kSegs));
+    v.skip = !mn || v.left <= 0;
+    // 64 further along k, 64 further along the tile: bytes in a row, or rows
+    v.at = o.at + (mn ? (int64_t)kb * (kTileK / kLoadWarps) * v.step + c * 128 : (int64_t)kb * 128 + c * (64 / kLoadWarps) * v.step);
     v.inside = v.rows == kSegs && v.at >= lo + 2 && v.at + (kSegs - 1) * v.step + 2 * 64 + 4 <= hi;
     return v;
   }
-  __device__ __forceinline__ void load(int warp, int lane, int64_t x0, int64_t k0, Words& f) const {
+  __device__ __forceinline__ void load(int warp, int lane, const Spot& o, int kb, Words& f) const {
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
-      const View v = view(warp, c, x0, k0);
+      const View v = view(warp, o, c, kb);
       uintptr_t at = v.at;
       if (v.inside) {
         // (elements past `left` are read too where they lie in the array, and cut off later)
@@ -138,58 +144,68 @@ struct Operand {
       }
     }
   }
-  __device__ __forceinline__ void shift(int warp, int lane, int64_t x0, int64_t k0, const Words& f, uint32_t stage) const {
+  __device__ __forceinline__ void shift(int warp, int lane, const Spot& o, int kb, const Words& f, uint32_t stage) const {
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
-      const View v = view(warp, c, x0, k0);
+      const View v = view(warp, o, c, kb);
       if (v.skip && v.rows == 0) continue;
       uintptr_t at = v.at;
       // segments 8 further have the same swizzle
       const uint32_t to = stage + (c * 64 + warp) * 128 + (((lane >> 2) ^ (warp & 7)) << 4) + (lane & 3) * 4;
       const uint32_t keep = 2 * lane + 1 < v.left ? 0xffffffffu : 2 * lane < v.left ? 0xffffu : 0u;
+      uint32_t e[kSegs];  // all of them before the first is stored: the shuffles overlap
 #pragma unroll
       for (int i = 0; i < kSegs; ++i, at += v.step) {
         uint32_t next = __shfl_down_sync(0xffffffffu, f.word[c][i], 1);
         const uint32_t last = __shfl_sync(0xffffffffu, f.last[c], i);
         if (lane == 31) next = last;
-        uint32_t e = __funnelshift_r(f.word[c][i], next, (uint32_t)(at & 2) * 8) & keep;
-        if (!v.inside) {
+        e[i] = __funnelshift_r(f.word[c][i], next, (uint32_t)(at & 2) * 8) & keep;
+      }
+      if (!v.inside) {
+        at = v.at;
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i, at += v.step) {
           if (i >= v.rows) {
-            e = 0;
+            e[i] = 0;
           } else if ((at & ~uintptr_t(3)) < lo || at + 2 * v.left + 2 > hi) {
             // a segment with the array's first or last word: element by element
             const uint16_t* q = reinterpret_cast<const uint16_t*>(at) + 2 * lane;
-            e = 2 * lane < v.left ? q[0] : 0;
-            if (2 * lane + 1 < v.left) e |= (uint32_t)q[1] << 16;
+            e[i] = 2 * lane < v.left ? q[0] : 0;
+            if (2 * lane + 1 < v.left) e[i] |= (uint32_t)q[1] << 16;
           }
         }
-        if (i < v.rows || !v.skip)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * (kLoadWarps * 128)), "r"(e) : "memory");
       }
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i)
+        if (i < v.rows || !v.skip)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + i * (kLoadWarps * 128)), "r"(e[i]) : "memory");
     }
   }
 };
 
-// Where a loader stands: tile t, k block kb of [.., k_hi).
+// Where a loader stands: tile t, k block kb of [.., k_hi), its segments' places.
+template <int BN>
 struct Cursor {
-  int64_t m0, n0;
+  typename Operand<kTileM>::Spot a;
+  typename Operand<BN>::Spot b;
   int t, kb, k_hi;
-};
 
-__device__ __forceinline__ void seek(const Args& p, int bn, Cursor& c, int total) {
-  if (c.t >= total) return;
-  int split;
-  tile_of(p, bn, c.t, c.m0, c.n0, split);
-  c.kb = split * p.kb_per_split;
-  c.k_hi = min(c.kb + p.kb_per_split, p.kblocks);
-}
-
-__device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int total) {
-  if (++c.kb == c.k_hi) {
-    c.t += gridDim.x;
-    seek(p, bn, c, total);
+  __device__ __forceinline__ void seek(const Args& p, const Operand<kTileM>& oa, const Operand<BN>& ob, int warp, int total) {
+    if (t >= total) return;
+    int64_t m0, n0;
+    int split;
+    tile_of(p, BN, t, m0, n0, split);
+    kb = split * p.kb_per_split;
+    k_hi = min(kb + p.kb_per_split, p.kblocks);
+    a = oa.spot(warp, m0);
+    b = ob.spot(warp, n0);
   }
-}
+  __device__ __forceinline__ void advance(const Args& p, const Operand<kTileM>& oa, const Operand<BN>& ob, int warp, int total) {
+    if (++kb < k_hi) return;
+    t += gridDim.x;
+    seek(p, oa, ob, warp, total);
+  }
+};
 
 template <int ACT>
 __device__ __forceinline__ void activate(float* v) {
@@ -249,28 +265,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
     const OpB b = operand(OpB{}, p.b, p.ldb, p.n, p.k, p.b_mn != 0);
     if (!p.drop) {
       if (RESIDENT && (int)blockIdx.x < total) {
-        const int64_t n0 = (int64_t)(blockIdx.x % p.n_tiles) * BN;
+        const auto spot = b.spot(lw, (int64_t)(blockIdx.x % p.n_tiles) * BN);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           typename OpB::Words f;
-          b.load(lw, lane, n0, (int64_t)kb * kTileK, f);
-          b.shift(lw, lane, n0, (int64_t)kb * kTileK, f, tc::smem_addr(res_b) + kBBytes * kb);
+          b.load(lw, lane, spot, kb, f);
+          b.shift(lw, lane, spot, kb, f, tc::smem_addr(res_b) + kBBytes * kb);
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.resident));
       }
-      Cursor cur;
+      Cursor<BN> cur;
       cur.t = blockIdx.x;
-      seek(p, BN, cur, total);
-      Cursor ahead = cur;
+      cur.seek(p, a, b, lw, total);
+      Cursor<BN> ahead = cur;
       constexpr int kSets = RESIDENT ? 2 : 1;
       typename OpA::Words fa[kSets];
       typename OpB::Words fb;
       auto load = [&](int w) {
         if (ahead.t >= total) return;
-        a.load(lw, lane, ahead.m0, (int64_t)ahead.kb * kTileK, fa[w]);
-        if (!RESIDENT) b.load(lw, lane, ahead.n0, (int64_t)ahead.kb * kTileK, fb);
-        advance(p, BN, ahead, total);
+        a.load(lw, lane, ahead.a, ahead.kb, fa[w]);
+        if (!RESIDENT) b.load(lw, lane, ahead.b, ahead.kb, fb);
+        ahead.advance(p, a, b, lw, total);
       };
       int s = 0;
       uint32_t parity = 1;
@@ -284,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
           ok = tc::mbar_wait_warp(bar(ctl.empty[s]), parity, g);
           if (!ok) break;
           const uint32_t st = tc::smem_addr(ring) + stage_bytes * s;
-          a.shift(lw, lane, cur.m0, (int64_t)cur.kb * kTileK, fa[w], st);
-          if (!RESIDENT) b.shift(lw, lane, cur.n0, (int64_t)cur.kb * kTileK, fb, st + kABytes);
+          a.shift(lw, lane, cur.a, cur.kb, fa[w], st);
+          if (!RESIDENT) b.shift(lw, lane, cur.b, cur.kb, fb, st + kABytes);
           if constexpr (kSets == 1) load(0);
           tc::fence_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(ctl.full[s]));
           if (++s == p.stages) s = 0, parity ^= 1;
-          advance(p, BN, cur, total);
+          cur.advance(p, a, b, lw, total);
         }
       }
     }
