@@ -89,6 +89,7 @@ struct RowSum {
 // G threads per row, IT vectors of VE elements per thread, U rows in flight per thread.
 template <typename T, int VE, int G, int IT, int U>
 __global__ void __launch_bounds__(kThreads, U == 4 ? 2 : 1) k_layernorm_fwd(const FwdArgs a) {
+  follow();
   using IO = VecIO<T, VE>;
   constexpr int kRows = kThreads / G;  // rows a block takes side by side
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, U == 4 ? 2 : 1) k_layernorm_fwd(cons
 // (the second and third time mostly from L2).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_layernorm_fwd_wide(const FwdArgs a) {
+  follow();
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* beta = static_cast<const T*>(a.beta);
   const float inv = 1.f / (float)a.width;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_fwd_wide(const FwdArgs a
 
 template <typename T, int VE, int G, int IT>
 __global__ void __launch_bounds__(kThreads, VE == 8 && IT == 1 ? 2 : VE * IT <= 4 ? (IT == 1 && G <= 32 ? 4 : 3) : 1) k_layernorm_bwd(const BwdArgs a) {
+  follow();
   using IO = VecIO<T, VE>;
   constexpr int kRows = kThreads / G;
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, VE == 8 && IT == 1 ? 2 : VE * IT <= 
 // Wide rows: as the forward; the block keeps its column sums in its own partial row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_layernorm_bwd_wide(const BwdArgs a) {
+  follow();
   const T* gamma = static_cast<const T*>(a.gamma);
   float* out = a.partials ? a.partials + (int64_t)blockIdx.x * 2 * a.width : nullptr;
   const float inv = 1.f / (float)a.width;
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(kThreads) k_layernorm_bwd_wide(const BwdArgs a
 template <typename T>
 __global__ void __launch_bounds__(1024) k_layernorm_fold(const float* __restrict__ partials, int n_part, int width,
                                                          T* __restrict__ dgamma, T* __restrict__ dbeta) {
+  follow();
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -643,9 +648,10 @@ extern "C" gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy
   if (!sums) return GS_OK;
   const int blocks = (2 * d->width + 31) / 32;
   if (d->dtype == GS_F32)
-    k_layernorm_fold<float><<<blocks, 1024, 0, st>>>(part, grid, d->width, (float*)dgamma, (float*)dbeta);
+    gs::launch(k_layernorm_fold<float>, dim3(blocks), 1024, 0, st, true, (const float*)part, grid, (int)d->width, (float*)dgamma,
+               (float*)dbeta);
   else
-    k_layernorm_fold<__nv_bfloat16><<<blocks, 1024, 0, st>>>(part, grid, d->width, (__nv_bfloat16*)dgamma,
-                                                                 (__nv_bfloat16*)dbeta);
+    gs::launch(k_layernorm_fold<__nv_bfloat16>, dim3(blocks), 1024, 0, st, true, (const float*)part, grid, (int)d->width,
+               (__nv_bfloat16*)dgamma, (__nv_bfloat16*)dbeta);
   return gs::check_launch(where);
 }

@@ -45,6 +45,7 @@ constexpr int kFew = 8;  // rows of a block
 // LANES lanes per column, VE elements per lane and step
 template <typename T, int VE, int LANES>
 __global__ void __launch_bounds__(kThreads) k_few_fwd(const Fwd<T> p) {
+  follow();
   using IO = VecIO<T, VE>;
   const int lane = threadIdx.x % LANES, n = (blockIdx.x * kThreads + threadIdx.x) / LANES, r0 = blockIdx.y * kFew;
   const int rows = min(kFew, p.rows - r0);
@@ -99,6 +100,7 @@ __device__ __forceinline__ float dz_at(const Bwd<T>& p, int64_t r, int n) {
 // dx of kFew rows and 4 VE columns: 64 slices of the outputs per block, added over the slices at the end
 template <typename T, int VE>
 __global__ void __launch_bounds__(kThreads) k_few_dx(const Bwd<T> p) {
+  follow();
   using IO = VecIO<T, VE>;
   constexpr int kChunk = 512, kSlices = kThreads / 4;
   __shared__ float dz[kFew][kChunk];
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) k_few_dx(const Bwd<T> p) {
 // dw of 32 outputs x 32 VE inputs, and their bias gradient in the first block across
 template <typename T, int VE>
 __global__ void __launch_bounds__(kThreads) k_few_dw(const Bwd<T> p) {
+  follow();
   using IO = VecIO<T, VE>;
   constexpr int kRows = 2 * kFew, kOut = 32, kPer = kOut / (kThreads / 32);
   __shared__ float dz[kRows][kOut];
@@ -192,6 +195,7 @@ constexpr int kTileR = 32, kTileC = 64, kTileK = 64;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_small_fwd(const Fwd<T> p) {
+  follow();
   __shared__ float xs[kTileR][kTileK + 1], ws[kTileC][kTileK + 1];
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;  // columns tx + 16 j, rows ty + 16 i
   const int64_t r0 = (int64_t)blockIdx.x * kTileR;
@@ -237,6 +241,7 @@ constexpr int kNarrow = 64;
 // parts: [gridDim.x][kNarrow + 1][kNarrow], the bias gradient's in the last row
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_small_bwd(const Bwd<T> p, float* parts) {
+  follow();
   __shared__ float dz[kTileR][kNarrow + 1], xs[kTileR][kNarrow + 1], ws[kNarrow][kNarrow + 1];
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16, c = tid % kNarrow, rr = tid / kNarrow;
   float aw[4][4] = {}, ab = 0.f;
@@ -305,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_small_bwd(const Bwd<T> p, float
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_small_bwd_fold(const float* parts, int n_parts, int in, int out, T* dw, int64_t lddw,
                                                              T* db) {
+  follow();
   __shared__ float s[4][kNarrow];
   const int c = threadIdx.x % kNarrow, way = threadIdx.x / kNarrow, row = blockIdx.x < out ? blockIdx.x : kNarrow;
   float v = 0.f;
@@ -374,8 +380,7 @@ gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void
       const bool vec = !dw || (vec_ok(x, d->rows, d->ldx, d->in_features, d->dtype) &&
                                vec_ok(dw, d->out_features, d->lddw, d->in_features, d->dtype));
       const dim3 grid(dw ? (unsigned)ceil_div(d->in_features, 32 * (vec ? VE : 1)) : 1, (unsigned)ceil_div(d->out_features, 32));
-      if (vec) k_few_dw<T, VE><<<grid, kThreads, 0, st>>>(p);
-      else k_few_dw<T, 1><<<grid, kThreads, 0, st>>>(p);
+      gs::launch(vec ? k_few_dw<T, VE> : k_few_dw<T, 1>, grid, kThreads, 0, st, dx != nullptr, p);
     }
     return gs::check_launch(where);
   }
@@ -384,8 +389,8 @@ gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void
   k_small_bwd<T><<<grid, kThreads, 0, st>>>(p, parts);
   if (gs_status s = gs::check_launch(where)) return s;
   if (!dw && !dbias) return GS_OK;
-  k_small_bwd_fold<T><<<d->out_features + 1, kThreads, 0, st>>>(parts, grid, d->in_features, d->out_features, (T*)dw, d->lddw,
-                                                                (T*)dbias);
+  gs::launch(k_small_bwd_fold<T>, dim3(d->out_features + 1), kThreads, 0, st, true, (const float*)parts, grid,
+             (int)d->in_features, (int)d->out_features, (T*)dw, (int64_t)d->lddw, (T*)dbias);
   return gs::check_launch(where);
 }
 

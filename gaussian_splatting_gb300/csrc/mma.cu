@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Arg
   if constexpr (CTAS == 2) tc::cluster_sync();
   tc::fence_after();
   const uint32_t tmem = ctl.tmem;
+  follow();
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ producer
@@ -476,15 +477,17 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
 }
 
 template <int CTAS>
-gs_status launch(const Args& p, int grid, int smem, cudaStream_t st, const char* where) {
+gs_status launch(const Args& p, int grid, int smem, bool after, cudaStream_t st, const char* where) {
   cudaError_t e = gs::max_dynamic_smem((const void*)k_mma<CTAS>, kSmemMost);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(grid), c.blockDim = dim3(kThreads), c.dynamicSmemBytes = smem, c.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = CTAS, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    c.attrs = at, c.numAttrs = CTAS == 2;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as gs::launch
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at + (CTAS == 1), c.numAttrs = (CTAS == 2) + after;
     e = cudaLaunchKernelEx(&c, k_mma<CTAS>, p);
   }
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
@@ -561,7 +564,7 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
     if (q.residual) ok = ok && encode_map(&p.r, q.residual, q.m, q.n, q.ldr, 32, GS_BF16, 64);
   }
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
-  if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, st, where) : launch<1>(p, grid, smem, st, where)) return s;
+  if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, q.after, st, where) : launch<1>(p, grid, smem, q.after, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
                              static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},

@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = ctl.tmem;
+  follow();
 
   if (warp >= kEpiWarps && warp < kEpiWarps + kLoadWarps) {
     // ------------------------------------------------------------ loaders
@@ -476,17 +477,17 @@ bool fits_resident(const Plan& pl) {
 }
 
 template <int BN, bool RESIDENT>
-gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
+gs_status launch(Args& p, const Plan& pl, bool after, cudaStream_t st, const char* where) {
   const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = (int)(total < gs::num_sms() ? total : gs::num_sms());
   if (RESIDENT) grid -= grid % pl.n_tiles;
   const int64_t fixed = fixed_bytes<BN>(pl, RESIDENT);
   const int stage = (kTileM + (RESIDENT ? 0 : BN)) * kTileK * 2, stages = (int)((kSmemMost - fixed) / stage);
   p.stages = stages < kMaxStages ? stages : kMaxStages;
-  const cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN, RESIDENT>, kSmemMost);
-  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  k_mma_staged<BN, RESIDENT><<<grid, kThreads, (int)fixed + p.stages * stage, st>>>(p);
-  return gs::check_launch(where);
+  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN, RESIDENT>, kSmemMost);
+  if (e == cudaSuccess)
+    e = gs::launch(k_mma_staged<BN, RESIDENT>, dim3(grid), kThreads, (size_t)fixed + p.stages * stage, st, after, p);
+  return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -517,9 +518,9 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
   p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   p.ldp = pl.ldp;
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
-  if (gs_status s = resident                  ? launch<128, true>(p, pl, st, where)
-                    : fits_resident<64>(pl) ? launch<64, true>(p, pl, st, where)
-                                            : launch<64, false>(p, pl, st, where))
+  if (gs_status s = resident                  ? launch<128, true>(p, pl, q.after, st, where)
+                    : fits_resident<64>(pl) ? launch<64, true>(p, pl, q.after, st, where)
+                                            : launch<64, false>(p, pl, q.after, st, where))
     return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
