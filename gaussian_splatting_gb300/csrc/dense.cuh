@@ -41,24 +41,25 @@ inline bool tma_takes(const void* p, int64_t rows, int64_t width, int64_t ld, in
   return rows_aligned16(p, rows, ld, dtype) && (width * (int64_t)dtype_size(dtype)) % 16 == 0;
 }
 
-// Launches a kernel that comes after another of this call on the stream (`after`): its blocks may start while
-// that one ends (programmatic dependent launch) and wait for its results in follow().  Between the launches of a
-// call about 4 us pass otherwise, of which this saves half or more.
+// Launches a dense-layer kernel: its blocks may start while the kernel before it on the stream ends, if that is
+// another of these (programmatic dependent launch), and wait for its results in follow().  About 4 us pass from
+// one kernel to the next otherwise, of which this saves half or more.  (Kernels that end up slower with their blocks
+// placed early are launched with <<<>>>, which waits for everything before them, and say so there.)
 template <typename... P, typename... A>
-inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after, A&&... args) {
+inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at, c.numAttrs = after ? 1 : 0;
+  c.attrs = at, c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);
 }
 
 }  // namespace gs
 
 // ------------------------------------------------------------------ device helpers
-// Every dense-layer kernel: lets the kernel after it be set up, and waits until the one before it is done and
+// First in every dense-layer kernel: lets the kernel after it be set up, and waits until the one before it is done and
 // its writes are visible (at once where there is none to wait for).  Nothing in memory is touched before.
 __device__ __forceinline__ void follow() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -237,6 +238,6 @@ __global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
 template <typename T>
 inline void launch_fold(const FoldArgs<T>& a, cudaStream_t st) {
   const int64_t groups = (a.m * a.ldp + 127) / 128;
-  if (a.splits >= 16) gs::launch(k_fold<T, 8>, dim3((unsigned)groups), 256, 0, st, true, a);
-  else gs::launch(k_fold<T, 2>, dim3((unsigned)((groups + 3) / 4)), 256, 0, st, true, a);
+  if (a.splits >= 16) gs::launch(k_fold<T, 8>, dim3((unsigned)groups), 256, 0, st, a);
+  else gs::launch(k_fold<T, 2>, dim3((unsigned)((groups + 3) / 4)), 256, 0, st, a);
 }

@@ -478,14 +478,14 @@ void launch_fwd(const FwdArgs& a, cudaStream_t st) {
   constexpr int U = IT == 1 ? 4 : IT == 2 ? 2 : 1;
   const int per_sm = resident<FwdArgs, k_layernorm_fwd<T, VE, G, IT, U>>();
   const int grid = grid_of(a.rows, kThreads / G * U, per_sm < kFwdPerSm ? per_sm : kFwdPerSm);
-  k_layernorm_fwd<T, VE, G, IT, U><<<grid, kThreads, 0, st>>>(a);
+  gs::launch(k_layernorm_fwd<T, VE, G, IT, U>, dim3(grid), kThreads, 0, st, a);
 }
 // returns the number of blocks: the partial rows that it writes
 template <typename T, int VE, int G, int IT>
 int launch_bwd(const BwdArgs& a, cudaStream_t st) {
   const int per_sm = resident<BwdArgs, k_layernorm_bwd<T, VE, G, IT>>();
   const int grid = grid_of(a.rows, kThreads / G, per_sm < kBwdPerSm ? per_sm : kBwdPerSm);
-  k_layernorm_bwd<T, VE, G, IT><<<grid, kThreads, 0, st>>>(a);
+  gs::launch(k_layernorm_bwd<T, VE, G, IT>, dim3(grid), kThreads, 0, st, a);
   return grid;
 }
 
@@ -509,7 +509,7 @@ void run_fwd_ve(const FwdArgs& a, Form f, cudaStream_t st) {
 
 template <typename T>
 void run_fwd(const FwdArgs& a, Form f, cudaStream_t st) {
-  if (f.it == 0) k_layernorm_fwd_wide<T><<<grid_of(a.rows, 1, kFwdPerSm), kThreads, 0, st>>>(a);
+  if (f.it == 0) gs::launch(k_layernorm_fwd_wide<T>, dim3(grid_of(a.rows, 1, kFwdPerSm)), kThreads, 0, st, a);
   else if (f.ve == 1) run_fwd_ve<T, 1>(a, f, st);
   else if (f.ve == 16 / (int)sizeof(T)) run_fwd_ve<T, 16 / sizeof(T)>(a, f, st);
   else if constexpr (sizeof(T) == 2) run_fwd_ve<T, 2>(a, f, st);
@@ -541,7 +541,7 @@ template <typename T>
 int run_bwd(const BwdArgs& a, Form f, cudaStream_t st) {
   if (f.it == 0) {
     const int grid = bwd_most(a.rows, f, a.width);
-    k_layernorm_bwd_wide<T><<<grid, kThreads, 0, st>>>(a);
+    gs::launch(k_layernorm_bwd_wide<T>, dim3(grid), kThreads, 0, st, a);
     return grid;
   }
   if (f.ve == 1) return run_bwd_ve<T, 1>(a, f, st);
@@ -648,10 +648,10 @@ extern "C" gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy
   if (!sums) return GS_OK;
   const int blocks = (2 * d->width + 31) / 32;
   if (d->dtype == GS_F32)
-    gs::launch(k_layernorm_fold<float>, dim3(blocks), 1024, 0, st, true, (const float*)part, grid, (int)d->width, (float*)dgamma,
+    gs::launch(k_layernorm_fold<float>, dim3(blocks), 1024, 0, st, (const float*)part, grid, (int)d->width, (float*)dgamma,
                (float*)dbeta);
   else
-    gs::launch(k_layernorm_fold<__nv_bfloat16>, dim3(blocks), 1024, 0, st, true, (const float*)part, grid, (int)d->width,
+    gs::launch(k_layernorm_fold<__nv_bfloat16>, dim3(blocks), 1024, 0, st, (const float*)part, grid, (int)d->width,
                (__nv_bfloat16*)dgamma, (__nv_bfloat16*)dbeta);
   return gs::check_launch(where);
 }

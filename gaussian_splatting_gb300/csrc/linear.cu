@@ -122,6 +122,9 @@ gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, 
                    (!z || gs::rows_aligned16(z, d->rows, d->ldz, d->dtype));
   const int cx = row_threads<T>(n);
   const dim3 grid(parts, (unsigned)ceil_div(n, cx * (16 / (int64_t)sizeof(T))));
+  // Launched only when the kernel before it is done: blocks placed while another kernel holds part of some SMs
+  // lie unevenly, and each block has the same share of the rows (300K x 256 -> 256 bf16 backward 211 us, 220 with
+  // gs::launch).
 #define GS_GO(V, CX)                                                                                                  \
   k_act_grad<T, V, CX><<<grid, kThreads, 0, st>>>(dy, z, d->rows, n, d->ldy, d->ldz, d->act, dz, lddz, part)
   if (vec) {
@@ -189,26 +192,22 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   const void* dz = copy ? copy : dy;
   const int64_t lddz = copy ? space.lddz : d->ldy;
   const int64_t unit = 16 / (int64_t)sizeof(T), pad = copy ? ceil_div(d->out_features, unit) * unit - d->out_features : 0;
-  bool after = false;  // a kernel of this call is on the stream already
-  if (copy || dbias) {
+  if (copy || dbias)
     if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), copy, lddz,
                                       dbias ? bias_part : nullptr, st, where))
       return s;
-    after = true;
-  }
   if (dx) {
     const gs::MmaProduct q{dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
-                           nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad, 0, after};
+                           nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
-    after = true;
   }
   if (dw) {
     const gs::MmaProduct q{dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
-                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE, pad, 0, after};
+                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
   if (dbias) {
-    gs::launch(k_bias_fold<T>, dim3((unsigned)ceil_div(d->out_features, 32)), 1024, 0, st, true, (const float*)bias_part,
+    gs::launch(k_bias_fold<T>, dim3((unsigned)ceil_div(d->out_features, 32)), 1024, 0, st, (const float*)bias_part,
                act_grad_parts<T>(d->rows, d->out_features), (int)d->out_features, static_cast<T*>(dbias));
     return gs::check_launch(where);
   }

@@ -477,7 +477,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k) {
 }
 
 template <int CTAS>
-gs_status launch(const Args& p, int grid, int smem, bool after, cudaStream_t st, const char* where) {
+gs_status launch(const Args& p, int grid, int smem, cudaStream_t st, const char* where) {
   cudaError_t e = gs::max_dynamic_smem((const void*)k_mma<CTAS>, kSmemMost);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t c = {};
@@ -487,7 +487,7 @@ gs_status launch(const Args& p, int grid, int smem, bool after, cudaStream_t st,
     at[0].val.clusterDim.x = CTAS, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as gs::launch
     at[1].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = at + (CTAS == 1), c.numAttrs = (CTAS == 2) + after;
+    c.attrs = at + (CTAS == 1), c.numAttrs = CTAS;
     e = cudaLaunchKernelEx(&c, k_mma<CTAS>, p);
   }
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
@@ -564,7 +564,7 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
     if (q.residual) ok = ok && encode_map(&p.r, q.residual, q.m, q.n, q.ldr, 32, GS_BF16, 64);
   }
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
-  if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, q.after, st, where) : launch<1>(p, grid, smem, q.after, st, where)) return s;
+  if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, st, where) : launch<1>(p, grid, smem, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
                              static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},

@@ -22,7 +22,6 @@ struct MmaProduct {
   int64_t ldr, ldy, ldz;
   int act;
   int64_t a_pad = 0, b_pad = 0;  // zeros that follow each of the operand's rows in memory
-  bool after = false;            // another kernel of the same call comes before it on the stream
 };
 
 // bfloat16 whose rows start anywhere (mma_staged.cu).

@@ -743,17 +743,17 @@ Room room_of(const Plan& pl, bool resident, int bufs) {
 }
 
 template <int BN, int GROUPS>
-gs_status launch(Args& p, const Room& r, int grid, bool after, cudaStream_t st, const char* where) {
+gs_status launch(Args& p, const Room& r, int grid, cudaStream_t st, const char* where) {
   // every team of splitters has raw buffers of its own: a wait for a buffer's next phase is then always made
   // by those who have seen the phase before it, as the phases' one bit of parity demands
   p.raws = r.raws - r.raws % GROUPS;
   if (p.raws < GROUPS) return gs::set_error(GS_ERR_INVALID, "%s: no room for raw buffers", where);
   cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_f32<BN, GROUPS>, kSmemMost);
-  if (e == cudaSuccess) e = gs::launch(k_mma_f32<BN, GROUPS>, dim3(grid), kThreads, r.fixed + p.raws * r.raw, st, after, p);
+  if (e == cudaSuccess) e = gs::launch(k_mma_f32<BN, GROUPS>, dim3(grid), kThreads, r.fixed + p.raws * r.raw, st, p);
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-gs_status launch_any(Args& p, const Plan& pl, bool after, cudaStream_t st, const char* where) {
+gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
   const int total = pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = total < gs::num_sms() ? total : gs::num_sms();
   const int bufs = p.part ? 0 : 1 + (p.residual != nullptr) + (p.z != nullptr);
@@ -765,8 +765,8 @@ gs_status launch_any(Args& p, const Plan& pl, bool after, cudaStream_t st, const
   } else {
     r = room_of(pl, false, bufs);
   }
-  if (pl.bn == 128) return launch<128, 1>(p, r, grid, after, st, where);
-  return r.raws >= 4 ? launch<64, 2>(p, r, grid, after, st, where) : launch<64, 1>(p, r, grid, after, st, where);
+  if (pl.bn == 128) return launch<128, 1>(p, r, grid, st, where);
+  return r.raws >= 4 ? launch<64, 2>(p, r, grid, st, where) : launch<64, 1>(p, r, grid, st, where);
 }
 
 }  // namespace
@@ -829,7 +829,7 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
       return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   }
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
-  if (gs_status s = launch_any(p, pl, q.after, st, where)) return s;
+  if (gs_status s = launch_any(p, pl, st, where)) return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, pl.swap},
               st);

@@ -477,7 +477,7 @@ bool fits_resident(const Plan& pl) {
 }
 
 template <int BN, bool RESIDENT>
-gs_status launch(Args& p, const Plan& pl, bool after, cudaStream_t st, const char* where) {
+gs_status launch(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
   const int64_t total = (int64_t)pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = (int)(total < gs::num_sms() ? total : gs::num_sms());
   if (RESIDENT) grid -= grid % pl.n_tiles;
@@ -486,7 +486,7 @@ gs_status launch(Args& p, const Plan& pl, bool after, cudaStream_t st, const cha
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_staged<BN, RESIDENT>, kSmemMost);
   if (e == cudaSuccess)
-    e = gs::launch(k_mma_staged<BN, RESIDENT>, dim3(grid), kThreads, (size_t)fixed + p.stages * stage, st, after, p);
+    e = gs::launch(k_mma_staged<BN, RESIDENT>, dim3(grid), kThreads, (size_t)fixed + p.stages * stage, st, p);
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
@@ -518,9 +518,9 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
   p.part = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   p.ldp = pl.ldp;
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
-  if (gs_status s = resident                  ? launch<128, true>(p, pl, q.after, st, where)
-                    : fits_resident<64>(pl) ? launch<64, true>(p, pl, q.after, st, where)
-                                            : launch<64, false>(p, pl, q.after, st, where))
+  if (gs_status s = resident                  ? launch<128, true>(p, pl, st, where)
+                    : fits_resident<64>(pl) ? launch<64, true>(p, pl, st, where)
+                                            : launch<64, false>(p, pl, st, where))
     return s;
   if (!p.part) return GS_OK;
   launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},

@@ -520,6 +520,62 @@ def test_calls_run_on_the_stream_they_are_given():
         assert torch.equal(y, want) and torch.equal(dx, wdx) and torch.equal(dw, wdw) and torch.equal(db, wdb)
 
 
+def _chain(x, w, wide, gamma, back):
+    """Calls of every kind, each on what the one before it wrote, the buffers of some written again at once."""
+    n, mean, rstd = dense.layernorm_fwd(x, gamma, gamma)
+    y, z = dense.linear_fwd(n, w, gamma, residual=n, act="gelu", keep_z=True)
+    dy, _ = dense.linear_fwd(y, wide)
+    dy, _ = dense.linear_fwd(dy, back)
+    dx, dw, db = dense.linear_bwd(dy, n, w, z, act="gelu")
+    dense.linear_fwd(dx, w, out=dy)
+    dn, dg, dbeta = dense.layernorm_bwd(dy, x, gamma, mean, rstd)
+    few, _ = dense.linear_fwd(dn[:5], w, act="silu")
+    small, _ = dense.linear_fwd(dn[:2000], w[:40])
+    dense.linear_fwd(dn, w, out=dx)
+    return y, dx, dw, db, dy, dn, dg, dbeta, few, small
+
+
+@pytest.mark.parametrize("width", [64, 59])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_calls_follow_each_other_and_are_captured(dtype, width):
+    """A kernel may be set up while the one before it ends: what a chain of calls returns does not depend
+    on whether the host waits between them, nor on their being replayed as a graph on other inputs."""
+    w, back = _rand((width, width), dtype, 1, 0.1), _rand((width, 200), dtype, 2, 0.1)
+    wide, gamma = _rand((200, width), dtype, 3, 0.1), _rand((width,), dtype, 4)
+    inputs = [_rand((30_001, width), dtype, 5 + i) for i in range(3)]
+    x = inputs[0].clone()
+    names = ["layernorm_fwd", "layernorm_bwd", "linear_fwd", "linear_bwd"]
+    plain = {n: getattr(dense, n) for n in names}
+    want = []
+    try:
+        for n in names:
+            def waiting(*a, _call=plain[n], **k):
+                r = _call(*a, **k)
+                torch.cuda.synchronize()
+                return r
+            setattr(dense, n, waiting)
+        for v in inputs:
+            want.append(_chain(v, w, wide, gamma, back))
+    finally:
+        for n in names:
+            setattr(dense, n, plain[n])
+    for v, expect in zip(inputs, want):
+        for _ in range(4):
+            assert all(torch.equal(a, b) for a, b in zip(_chain(v, w, wide, gamma, back), expect))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _chain(x, w, wide, gamma, back)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = _chain(x, w, wide, gamma, back)
+    for v, expect in zip(inputs, want):
+        x.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, expect))
+
+
 def test_offsets_beyond_32_bits():
     """Arrays of more than 2^31 elements (rows far apart): the last rows are read and written in place."""
     rows, n, ld = 70_000, 64, 40_000
