@@ -51,8 +51,9 @@ BAD_SIZES = [dict(rows=-1), dict(rows=1 << 31), dict(in_features=0), dict(out_fe
 def test_linear_refuses_bad_descriptors(lib, bad):
     assert _fwd(lib, _linear(**bad)) == N.GS_ERR_INVALID
     assert _bwd(lib, _linear(**bad)) == N.GS_ERR_INVALID
-    assert lib.gs_linear_fwd_workspace_size(C.addressof(_linear(**bad))) == 0
-    assert lib.gs_linear_bwd_workspace_size(C.addressof(_linear(**bad))) == 0
+    d = _linear(**bad)
+    assert lib.gs_linear_fwd_workspace_size(C.addressof(d)) == 0
+    assert lib.gs_linear_bwd_workspace_size(C.addressof(d)) == 0
 
 
 def test_linear_refuses_missing_misaligned_and_overlapping_arrays(lib):
@@ -94,7 +95,8 @@ def test_calls_with_nothing_to_do_succeed_without_touching_memory(lib):
     assert _fwd(lib, _linear(rows=0), x=None, w=None, y=None, ws=None, n=0) == N.GS_OK
     assert _bwd(lib, _linear(), dy=None, x=None, w=None, dx=None, dw=None, dbias=None, ws=None, n=0) == N.GS_OK
     assert _bwd(lib, _linear(rows=0), dy=None, x=None, w=None, dw=None, dbias=None, ws=None, n=0) == N.GS_OK
-    assert lib.gs_linear_fwd_workspace_size(C.addressof(_linear(rows=0))) == 0
+    d = _linear(rows=0)
+    assert lib.gs_linear_fwd_workspace_size(C.addressof(d)) == 0
 
 
 def _norm(**kw):
@@ -134,7 +136,8 @@ def test_layernorm_refusals(lib):
     for f in ("ldx", "lddy", "lddx"):
         assert _nbwd(lib, _norm(**{f: 7})) == N.GS_ERR_INVALID
     assert _nbwd(lib, _norm(ldskip=7), skip=P) == N.GS_ERR_INVALID
-    need = lib.gs_layernorm_bwd_workspace_size(C.addressof(_norm()))
+    d = _norm()
+    need = lib.gs_layernorm_bwd_workspace_size(C.addressof(d))
     assert need > 0
     assert _nbwd(lib, _norm(), n=need - 1) == N.GS_ERR_INVALID
     assert _nbwd(lib, _norm(), ws=None) == N.GS_ERR_INVALID
