@@ -7,8 +7,12 @@
 // bfloat16 arrays whose rows start and end on 16-byte boundaries go to mma.cu, other bfloat16 ones to mma_staged.cu,
 // float32 to mma_f32.cu; small calls to linear_small.cu.
 // dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
-// sums, and kept in the workspace for the two products that read it.
+// sums, and kept in the workspace for the two products that read it.  A narrow bfloat16 layer's pass computes
+// dx as well (mma_grad.cu), with up to 256 inputs and outputs: the dw product's operands are then all that is
+// read twice (300K x 256 -> 256 with GELU 197 us, 211 as separate passes; 3M x 64 -> 64 399 and 510; the two
+// meet at 500 rows, 20 us).
 #include "mma.cuh"
+#include "mma_grad.cuh"
 #include "small.cuh"
 
 namespace {
@@ -123,7 +127,7 @@ gs_status run_act_grad(const gs_linear_desc* d, const T* dy, const T* z, T* dz, 
   const int cx = row_threads<T>(n);
   const dim3 grid(parts, (unsigned)ceil_div(n, cx * (16 / (int64_t)sizeof(T))));
   // Launched only when the kernel before it is done: blocks placed while another kernel holds part of some SMs
-  // lie unevenly, and each block has the same share of the rows (300K x 256 -> 256 bf16 backward 211 us, 220 with
+  // lie unevenly, and each block has the same share of the rows (300K x 128 -> 59 f32 backward 147 us, 149 with
   // gs::launch).
 #define GS_GO(V, CX)                                                                                                  \
   k_act_grad<T, V, CX><<<grid, kThreads, 0, st>>>(dy, z, d->rows, n, d->ldy, d->ldz, d->act, dz, lddz, part)
@@ -169,7 +173,8 @@ BwdSpace bwd_space(const gs_linear_desc* d) {
   const int unit = 16 / (int)gs::dtype_size(d->dtype);
   const bool copy = d->act != GS_ACT_NONE || d->ldy % unit != 0 || d->out_features % unit != 0;
   s.dz = copy ? up256((size_t)d->rows * s.lddz * gs::dtype_size(d->dtype)) : 0;
-  s.bias = up256((size_t)parts_of(d) * d->out_features * sizeof(float));
+  const int parts = parts_of(d), fused = gs::grad_parts(d->rows);
+  s.bias = up256((size_t)(parts > fused ? parts : fused) * d->out_features * sizeof(float));
   const size_t a = product_space(d->rows, d->in_features, d->out_features, d->dtype);
   const size_t b = product_space(d->out_features, d->in_features, d->rows, d->dtype);
   s.part = a > b ? a : b;
@@ -192,11 +197,19 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   const void* dz = copy ? copy : dy;
   const int64_t lddz = copy ? space.lddz : d->ldy;
   const int64_t unit = 16 / (int64_t)sizeof(T), pad = copy ? ceil_div(d->out_features, unit) * unit - d->out_features : 0;
-  if (copy || dbias)
+  int parts = act_grad_parts<T>(d->rows, d->out_features);
+  // (without an activation there is nothing to form, and it is used for the sums' sake alone)
+  const bool fused = (z || dbias) && gs::grad_takes(d, dy, z, w, dx);
+  if (fused) {
+    parts = gs::grad_parts(d->rows);
+    if (gs_status s = gs::grad_run(d, dy, z, w, dw ? copy : nullptr, space.lddz, dx, dbias ? bias_part : nullptr, status, st, where))
+      return s;
+  } else if (copy || dbias) {
     if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), copy, lddz,
                                       dbias ? bias_part : nullptr, st, where))
       return s;
-  if (dx) {
+  }
+  if (dx && !fused) {
     const gs::MmaProduct q{dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
                            nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
@@ -208,7 +221,7 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   }
   if (dbias) {
     gs::launch(k_bias_fold<T>, dim3((unsigned)ceil_div(d->out_features, 32)), 1024, 0, st, (const float*)bias_part,
-               act_grad_parts<T>(d->rows, d->out_features), (int)d->out_features, static_cast<T*>(dbias));
+               parts, (int)d->out_features, static_cast<T*>(dbias));
     return gs::check_launch(where);
   }
   return GS_OK;

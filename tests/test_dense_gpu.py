@@ -218,6 +218,33 @@ def test_linear_with_many_rows(shape, dtype):
             _close(v, *want[k], f"{k} {act}")
 
 
+# narrow layers, whose dz and dx come out of one pass: a tile, a row more, one and two buffers of dz, widths
+# that end inside blocks of 64 and of 16, the widest, one column of vectors
+NARROW = [(128, 256, 256), (129, 72, 8), (1, 256, 256), (20_000, 256, 256), (25_001, 8, 248), (40_000, 200, 128), (33_333, 128, 72),
+          (19_500, 40, 24), (3000, 250, 256)]
+
+
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("shape", NARROW, ids=str)
+def test_narrow_backward(shape, pad):
+    rows, n_in, n_out = shape
+    for act in ACTS:
+        dy, x = _rand((rows, n_out), BF16, 5, 1e-3, pad), _rand((rows, n_in), BF16, 6, 1.0, pad)
+        w = _rand((n_out, n_in), BF16, 7, 1 / math.sqrt(n_in), pad)
+        z = None if act == "none" else _rand((rows, n_out), BF16, 8, 1.0, pad)
+        out = torch.full((rows, n_in + 24), 7.0, dtype=BF16, device="cuda")
+        full = dense.linear_bwd(dy, x, w, z, act=act, dx=out[:, 8:8 + n_in])
+        assert (out[:, :8] == 7).all() and (out[:, 8 + n_in:] == 7).all()
+        want = _linear_grads(dy, x, w, z, act)
+        for k, v in zip(("dx", "dw", "db"), full):
+            _close(v, *want[k], f"{k} {act}")
+        for kw, kept in ((dict(need_dx=False), (1, 2)), (dict(need_dw=False), (0, 2)), (dict(bias=False), (0, 1)),
+                         (dict(need_dx=False, need_dw=False), (2,))):
+            part = dense.linear_bwd(dy, x, w, z, act=act, **kw)
+            for i in kept:
+                assert torch.equal(part[i], full[i])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("pad,shift", [(8, 0), (24, 8), (1, 0), (3, 1), (2, 0)])
 def test_linear_takes_any_stride_and_alignment_and_leaves_the_gaps(dtype, pad, shift):
@@ -633,3 +660,27 @@ def test_a_wait_that_runs_out_sets_the_status_and_leaves_the_device_usable(case)
     status.zero_()
     y, _ = dense.linear_fwd(x, w, None, r, status=status)
     assert status.item() == 0 and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("width", [256, 40])
+def test_a_wait_that_runs_out_in_a_narrow_backward(width):
+    """The same for the pass that forms dz: w never arrives, dz and dx wait for it in vain."""
+    x, w = _rand((60_000, width), BF16, 1), _rand((width, width), BF16, 2, 0.05)
+    z, status = _rand((60_000, width), BF16, 3), torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = dense.linear_bwd(x, x, w, z, act="gelu", status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    lib = N.load()
+    try:
+        lib.gs_debug_set_wait_limit(2000)
+        lib.gs_debug_drop_publish(3)
+        dense.linear_bwd(x, x, w, z, act="gelu", status=status)
+        torch.cuda.synchronize()
+    finally:
+        lib.gs_debug_set_wait_limit(0)
+        lib.gs_debug_drop_publish(0)
+    assert status.item() == 2
+    status.zero_()
+    for a, b in zip(dense.linear_bwd(x, x, w, z, act="gelu", status=status), want):
+        assert torch.equal(a, b)
+    assert status.item() == 0
