@@ -6,7 +6,10 @@
 // costs its own store only, and not another read of dz.  One persistent block per SM walks over tiles of 128
 // rows:
 //   warps 0 - 15   read dy and z (four vectors of 16 bytes of each in flight per thread), form dz, round it to
-//                  bfloat16 once, write it to memory and, swizzled, to shared memory, and add the columns up
+//                  bfloat16 once, write it to memory and, swizzled, to shared memory, and add the columns up.
+//                  Where w leaves no room for a second buffer of dz they work in four groups, one for each 64 of
+//                  the outputs, and a group waits only for the products of its own block of k: together they would
+//                  stand still for all of a tile's products
 //   warps 16 - 19  write the finished accumulator through shared memory with TMA stores
 //   warp 20        issues tcgen05.mma, 128 x in x 16 each, into one of two accumulators
 //   warp 21        copies w in, once
@@ -30,7 +33,7 @@ constexpr int kSmemMost = 232448, kSmemCtl = 1024;
 constexpr int kSms = 152;  // the most blocks; only speed depends on it
 
 struct Ctl {
-  uint64_t w, a_full[2], a_empty[2], acc_full[2], acc_empty[2], drain;
+  uint64_t w, a_full[2][4], a_empty[2][4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem, dead;
 };
 static_assert(sizeof(Ctl) <= kSmemCtl, "control block");
@@ -48,12 +51,13 @@ struct Args {
   int wait_limit, drop;  // microseconds; test hook: w is not copied in
 };
 
-// CX threads along a row, a vector of 8 columns each
-template <int CX>
+// GROUPS groups of warps side by side, CX threads of each along a row, with a vector of 8 columns each
+template <int CX, int GROUPS>
 __device__ void form(const Args& p, Ctl& ctl, unsigned char* a, float* fold, const tc::Guard& g) {
-  constexpr int kRows = kForm / CX, kSteps = kTileM / kRows, kAhead = 4;
+  constexpr int kSize = kForm / GROUPS, kRows = kSize / CX, kSteps = kTileM / kRows, kAhead = 4;
   using IO = VecIO<bf16, 8>;
-  const int cx = threadIdx.x % CX, ry = threadIdx.x / CX, c = cx * 8, lane = threadIdx.x & 31;
+  const int group = threadIdx.x / kSize, cx = threadIdx.x % CX, ry = threadIdx.x % kSize / CX, c = (group * CX + cx) * 8;
+  const int lane = threadIdx.x & 31;
   const bool in = c < p.n, used = c < p.kblocks * kTileK;  // the last block of k is filled up with zeros
   const int steps = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * kSteps;
   auto row_of = [&](int i) {
@@ -73,7 +77,7 @@ __device__ void form(const Args& p, Ctl& ctl, unsigned char* a, float* fold, con
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) fetch(u, d[u], z[u]);
-  unsigned char* mine = a + (c / kTileK) * kABytes;
+  unsigned char* mine = a + c / kTileK * kABytes;
   bool ok = true;
   int buf = 0;
   uint32_t parity = 1;
@@ -99,7 +103,7 @@ __device__ void form(const Args& p, Ctl& ctl, unsigned char* a, float* fold, con
       if (p.dz && in && r < p.rows) *reinterpret_cast<uint4*>(p.dz + r * p.lddz + c) = q;
       if (!p.has_dx) continue;
       if (s == 0) {
-        ok = tc::mbar_wait_warp(tc::smem_addr(&ctl.a_empty[buf]), parity, g);
+        ok = tc::mbar_wait_warp(tc::smem_addr(&ctl.a_empty[buf][group]), parity, g);
         if (!ok) break;
       }
       const int row = s * kRows + ry;
@@ -107,16 +111,16 @@ __device__ void form(const Args& p, Ctl& ctl, unsigned char* a, float* fold, con
       if (s == kSteps - 1) {
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_addr(&ctl.a_full[buf]));
+        if (lane == 0) tc::mbar_arrive(tc::smem_addr(&ctl.a_full[buf][group]));
         if (++buf == p.bufs) buf = 0, parity ^= 1;
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) fold[ry * CX * 8 + cx * 8 + e] = sum[e];
+  for (int e = 0; e < 8; ++e) fold[ry * GROUPS * CX * 8 + c + e] = sum[e];
 }
 
-template <int CX>
+template <int CX, int GROUPS>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant__ Args p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -132,8 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
     tc::mbar_init(bar(ctl.w), 1);
     tc::mbar_init(bar(ctl.drain), 1);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(bar(ctl.a_full[i]), kFormWarps);
-      tc::mbar_init(bar(ctl.a_empty[i]), 1);
+      for (int j = 0; j < GROUPS; ++j) {
+        tc::mbar_init(bar(ctl.a_full[i][j]), kFormWarps / GROUPS);
+        tc::mbar_init(bar(ctl.a_empty[i][j]), 1);
+      }
       tc::mbar_init(bar(ctl.acc_full[i]), 1);
       tc::mbar_init(bar(ctl.acc_empty[i]), kEpiWarps);
     }
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
   follow();
 
   if (warp < kFormWarps) {
-    form<CX>(p, ctl, a, fold, g);
+    form<CX, GROUPS>(p, ctl, a, fold, g);
   } else if (!p.has_dx) {
   } else if (warp == kLoadWarp) {
     if (!p.drop) {
@@ -170,21 +176,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
     bool ok = tc::mbar_wait_warp(bar(ctl.w), 0, g);
     for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
       ok = tc::mbar_wait_warp(bar(ctl.acc_empty[acc]), acc_parity, g);
-      if (ok) ok = tc::mbar_wait_warp(bar(ctl.a_full[buf]), parity, g);
-      if (!ok) break;
-      tc::fence_after();
       const uint32_t d = tmem + acc * (p.tmem_cols / 2);
-      if (tc::elect_one()) {
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        const int group = kb * 8 / CX;
+        if (ok) ok = tc::mbar_wait_warp(bar(ctl.a_full[buf][group]), parity, g);
+        if (!ok) break;
+        tc::fence_after();
+        if (tc::elect_one()) {
           const uint32_t at = tc::smem_addr(a) + (buf * p.kblocks + kb) * kABytes, bt = tc::smem_addr(w) + w_bytes * kb;
 #pragma unroll
           for (int i = 0; i < kTileK / 16; ++i)
             tc::mma_bf16(d, tc::smem_desc(at + i * 32, 64 * 128, 1024), tc::smem_desc(bt + i * 16 * 128, 64 * 128, 1024), idesc,
                          kb > 0 || i > 0);
+          if (kb + 1 == p.kblocks || (kb + 1) * 8 / CX != group) tc::mma_commit(bar(ctl.a_empty[buf][group]));
         }
-        tc::mma_commit(bar(ctl.a_empty[buf]));
-        tc::mma_commit(bar(ctl.acc_full[acc]));
+        __syncwarp();
       }
+      if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
       __syncwarp();
       if (++buf == p.bufs) buf = 0, parity ^= 1;
       acc ^= 1;
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
   if (p.part && threadIdx.x < p.n) {
     float t = 0.f;
 #pragma unroll 8
-    for (int r = 0; r < kForm / CX; ++r) t += fold[r * CX * 8 + threadIdx.x];
+    for (int r = 0; r < kForm / (GROUPS * CX); ++r) t += fold[r * GROUPS * CX * 8 + threadIdx.x];
     p.part[(int64_t)blockIdx.x * p.n + threadIdx.x] = t;
   }
 }
@@ -250,10 +258,10 @@ int grid_of(int64_t rows) {
   return (int)(tiles < kSms ? tiles : kSms);
 }
 
-template <int CX>
+template <int CX, int GROUPS>
 gs_status launch(const Args& p, int grid, int smem, cudaStream_t st, const char* where) {
-  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_grad<CX>, kSmemMost);
-  if (e == cudaSuccess) e = gs::launch(k_mma_grad<CX>, dim3(grid), kThreads, smem, st, p);
+  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_grad<CX, GROUPS>, kSmemMost);
+  if (e == cudaSuccess) e = gs::launch(k_mma_grad<CX, GROUPS>, dim3(grid), kThreads, smem, st, p);
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
@@ -289,10 +297,11 @@ gs_status grad_run(const gs_linear_desc* d, const void* dy, const void* z, const
               encode_map(&p.dx, dx, d->rows, d->in_features, d->lddx, 32, GS_BF16, 64)))
     return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   const int grid = grid_of(d->rows);
-  // as many threads along a row as its blocks of k need, all of which have to be written
-  if (p.n <= 64) return launch<8>(p, grid, smem, st, where);
-  if (p.n <= 128) return launch<16>(p, grid, smem, st, where);
-  return launch<32>(p, grid, smem, st, where);
+  // as many threads along a row as its blocks of k have columns (256 -> 256 with one buffer: 191 us in groups, 197
+  // without; 128 -> 256 with two: 382 and 365 for 1.2M rows)
+  if (p.n <= 64) return launch<8, 1>(p, grid, smem, st, where);
+  if (p.n <= 128) return launch<16, 1>(p, grid, smem, st, where);
+  return p.bufs == 1 && p.kblocks == 4 ? launch<8, 4>(p, grid, smem, st, where) : launch<32, 1>(p, grid, smem, st, where);
 }
 
 }  // namespace gs

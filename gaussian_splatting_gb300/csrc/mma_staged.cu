@@ -210,7 +210,7 @@ struct Cursor {
 template <int ACT>
 __device__ __forceinline__ void activate(float* v) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], ACT);
+  for (int i = 0; i < 32; i += 2) act_value2(v[i], v[i + 1], ACT);
 }
 
 // RESIDENT: B's parts are in shared memory from the start, and the loaders hold two k blocks of A's words in
