@@ -11,8 +11,7 @@
 //                  the outputs, and a group waits only for the products of its own block of k: together they would
 //                  stand still for all of a tile's products
 //   warps 16 - 19  write the finished accumulator through shared memory with TMA stores
-//   warp 20        issues tcgen05.mma, 128 x in x 16 each, into one of two accumulators
-//   warp 21        copies w in, once
+//   warp 20        copies w in, once, and issues tcgen05.mma, 128 x in x 16 each, into one of two accumulators
 // Bound by memory: 300K x 256 -> 256 with GELU reads 307 MB and writes as much.
 #include "mma_grad.cuh"
 
@@ -22,15 +21,15 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kFormWarps = 16, kEpiWarps = 4;
-constexpr int kMmaWarp = kFormWarps + kEpiWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kForm = 32 * kFormWarps, kThreads = 32 * (kLoadWarp + 1);
+constexpr int kFormWarps = 16, kEpiWarps = 4, kMmaWarp = kFormWarps + kEpiWarps;
+constexpr int kForm = 32 * kFormWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kTileM = 128, kTileK = 64, kMost = 256;
 constexpr int kABytes = kTileM * kTileK * 2;
 constexpr int kBufCols = 32, kBufBytes = 32 * 64;  // a warp's piece of dx: 32 rows of 64 bytes, 64-byte swizzle
 constexpr int kEpiBytes = kEpiWarps * 2 * kBufBytes, kFoldBytes = kForm * 8 * 4;
 constexpr int kSmemMost = 232448, kSmemCtl = 1024;
 constexpr int kSms = 152;  // the most blocks; only speed depends on it
+static_assert(1024 + kSmemCtl + kEpiBytes + kFoldBytes + 3 * (kMost * kTileK * 2 + 2 * kABytes) <= kSmemMost, "shared memory");
 
 struct Ctl {
   uint64_t w, a_full[2][4], a_empty[2][4], acc_full[2], acc_empty[2], drain;
@@ -44,75 +43,84 @@ struct Args {
   const bf16* z;   // NULL: dz = dy
   bf16* dz;        // NULL: not wanted
   float* part;     // [blocks][n]; NULL: no sums
-  int64_t rows, ldy, ldz, lddz;
-  int n, cols, act, tiles, kblocks, bn, bufs, tmem_cols;  // n outputs, cols inputs
+  uint32_t rows, dy_bytes, z_bytes, dz_bytes;  // of a row, to the next
+  int n, cols, act, tiles, kblocks, bn, tmem_cols;  // n outputs, cols inputs
   int has_dx;
   int32_t* status;
   int wait_limit, drop;  // microseconds; test hook: w is not copied in
 };
 
-// GROUPS groups of warps side by side, CX threads of each along a row, with a vector of 8 columns each
-template <int CX, int GROUPS>
+// Buffers of dz: two, so that the next tile's is written while this one's products run, or one and groups
+template <int GROUPS>
+constexpr int kBufs = GROUPS == 1 ? 2 : 1;
+
+// GROUPS groups of warps side by side, CX threads of each along a row, with a vector of 8 columns each.  (ACT is the
+// compiler's: a branch for each element would keep their evaluations from overlapping.)
+template <int CX, int GROUPS, int ACT>
 __device__ void form(const Args& p, Ctl& ctl, unsigned char* a, float* fold, const tc::Guard& g) {
   constexpr int kSize = kForm / GROUPS, kRows = kSize / CX, kSteps = kTileM / kRows, kAhead = 4;
   using IO = VecIO<bf16, 8>;
   const int group = threadIdx.x / kSize, cx = threadIdx.x % CX, ry = threadIdx.x % kSize / CX, c = (group * CX + cx) * 8;
   const int lane = threadIdx.x & 31;
-  const bool in = c < p.n, used = c < p.kblocks * kTileK;  // the last block of k is filled up with zeros
-  const int steps = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * kSteps;
-  auto row_of = [&](int i) {
-    return ((int64_t)blockIdx.x + (int64_t)(i / kSteps) * gridDim.x) * kTileM + i % kSteps * kRows + ry;
+  // the last block of k is filled up with zeros; of 256 columns it may be the third
+  const bool used = CX < 32 || c < p.kblocks * kTileK;
+  // the row of the next step: kRows further with each, and to this block's next tile with the last of a tile
+  const uint32_t rows = c < p.n ? p.rows : 0, next = gridDim.x * kTileM;
+  uint32_t at = blockIdx.x * kTileM + ry;
+  auto row_of = [&](const bf16* base, uint32_t r, uint32_t row_bytes) {
+    return reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(base + c) + (uint64_t)r * row_bytes);
   };
   uint4 d[kAhead], z[kAhead];
-  auto fetch = [&](int i, uint4& rd, uint4& rz) {
-    const int64_t r = row_of(i);
+  auto fetch = [&](uint32_t r, uint4& rd, uint4& rz) {
     rd = rz = make_uint4(0u, 0u, 0u, 0u);
-    if (in && i < steps && r < p.rows) {
-      rd = IO::load(p.dy + r * p.ldy + c);
-      if (p.z) rz = IO::load(p.z + r * p.ldz + c);
+    if (r < rows) {
+      rd = IO::load(row_of(p.dy, r, p.dy_bytes));
+      if (ACT != GS_ACT_NONE) rz = IO::load(row_of(p.z, r, p.z_bytes));
     }
   };
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) fetch(u, d[u], z[u]);
-  unsigned char* mine = a + c / kTileK * kABytes;
-  bool ok = true;
+  for (int u = 0; u < kAhead; ++u) fetch(at + u % kSteps * kRows + u / kSteps * next, d[u], z[u]);
+  static_assert(kRows % 8 == 0, "the swizzle of a thread's rows is the same");
+  unsigned char* mine = a + c / kTileK * kABytes + ry * 128 + (((cx ^ ry) & 7) << 4);
   int buf = 0;
   uint32_t parity = 1;
-  for (int i0 = 0; ok && i0 < steps; i0 += kAhead) {
+  const uint32_t end = (uint32_t)p.tiles * kTileM;
+  for (int i0 = 0; at < end; i0 ^= kSteps > kAhead ? kAhead : 0) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = i0 + u, s = i % kSteps;
-      if (i >= steps || !ok) break;
-      float f[8];
-      IO::unpack(d[u], f);
-      if (p.z) {
-        float v[8];
-        IO::unpack(z[u], v);
+    for (int u = 0; u < kAhead; ++u) {  // a tile's steps, half of them, or those of two tiles
+      const int s = (i0 + u) % kSteps;
+      if (u > 0 && u % kSteps == 0 && at >= end) break;
+      uint32_t q[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= act_slope(v[e], p.act);
+      for (int e = 0; e < 4; ++e) {
+        float lo = bf16_lo(q[e]), hi = bf16_hi(q[e]);
+        if (ACT != GS_ACT_NONE) lo *= act_slope(bf16_lo(zw[e]), ACT), hi *= act_slope(bf16_hi(zw[e]), ACT);
+        sum[2 * e] += lo, sum[2 * e + 1] += hi;
+        if (ACT != GS_ACT_NONE) q[e] = pack_bf16(lo, hi);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += f[e];
-      const int64_t r = row_of(i);
-      fetch(i + kAhead, d[u], z[u]);
-      uint4 q;
-      IO::store(reinterpret_cast<bf16*>(&q), f);
-      if (p.dz && in && r < p.rows) *reinterpret_cast<uint4*>(p.dz + r * p.lddz + c) = q;
+      const uint4 dz = make_uint4(q[0], q[1], q[2], q[3]);
+      // keeps the steps' evaluations apart, which with this many of a tile's steps need more than the 80 registers
+      // that there are; the others gain by overlapping them (1.2M x 256 -> 256: 326 us, 342 apart)
+      if (CX == 16) __syncwarp();
+      fetch(at + (kSteps > kAhead ? kAhead * kRows + (i0 ? next - kTileM : 0) : kAhead / kSteps * next), d[u], z[u]);
+      if (p.dz && at < rows) *reinterpret_cast<uint4*>(const_cast<bf16*>(row_of(p.dz, at, p.dz_bytes))) = dz;
+      at += kRows + (s == kSteps - 1 ? next - kTileM : 0);
       if (!p.has_dx) continue;
       if (s == 0) {
-        ok = tc::mbar_wait_warp(tc::smem_addr(&ctl.a_empty[buf][group]), parity, g);
-        if (!ok) break;
+        if (!tc::mbar_wait_warp(tc::smem_addr(&ctl.a_empty[buf][group]), parity, g)) {
+          at = end;
+          break;
+        }
       }
-      const int row = s * kRows + ry;
-      if (used) *reinterpret_cast<uint4*>(mine + buf * p.kblocks * kABytes + row * 128 + (((cx ^ row) & 7) << 4)) = q;
+      if (used) *reinterpret_cast<uint4*>(mine + buf * p.kblocks * kABytes + s * kRows * 128) = dz;
       if (s == kSteps - 1) {
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_addr(&ctl.a_full[buf][group]));
-        if (++buf == p.bufs) buf = 0, parity ^= 1;
+        if (++buf == kBufs<GROUPS>) buf = 0, parity ^= 1;
       }
     }
   }
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
   const uint32_t w_bytes = (uint32_t)p.bn * kTileK * 2;  // of a block of k
   unsigned char* w = smem + kSmemCtl;
   unsigned char* a = w + (p.has_dx ? w_bytes * p.kblocks : 0);
-  unsigned char* epi = a + (p.has_dx ? p.bufs * p.kblocks * kABytes : 0);
+  unsigned char* epi = a + (p.has_dx ? kBufs<GROUPS> * p.kblocks * kABytes : 0);
   float* fold = reinterpret_cast<float*>(epi + kEpiBytes);
   const int warp = tc::warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return tc::smem_addr(&b); };
@@ -155,20 +163,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
   follow();
 
   if (warp < kFormWarps) {
-    form<CX, GROUPS>(p, ctl, a, fold, g);
+    if (p.act == GS_ACT_GELU) form<CX, GROUPS, GS_ACT_GELU>(p, ctl, a, fold, g);
+    else if (p.act == GS_ACT_SILU) form<CX, GROUPS, GS_ACT_SILU>(p, ctl, a, fold, g);
+    else if (p.act == GS_ACT_RELU) form<CX, GROUPS, GS_ACT_RELU>(p, ctl, a, fold, g);
+    else form<CX, GROUPS, GS_ACT_NONE>(p, ctl, a, fold, g);
   } else if (!p.has_dx) {
-  } else if (warp == kLoadWarp) {
-    if (!p.drop) {
-      if (tc::elect_one()) {
-        tc::mbar_expect_tx(bar(ctl.w), w_bytes * p.kblocks);
-        for (int kb = 0; kb < p.kblocks; ++kb)
-          for (int c = 0; c < p.bn; c += 64)
-            tc::tma_load_2d(tc::smem_addr(w) + w_bytes * kb + c * 128, &p.w, c, kb * kTileK, bar(ctl.w));
-      }
-      __syncwarp();
-      tc::mbar_drain(bar(ctl.w), 0, p.wait_limit);  // no copy is in flight when the block ends
-    }
   } else if (warp == kMmaWarp) {
+    if (!p.drop && tc::elect_one()) {
+      tc::mbar_expect_tx(bar(ctl.w), w_bytes * p.kblocks);
+      for (int kb = 0; kb < p.kblocks; ++kb)
+        for (int c = 0; c < p.bn; c += 64)
+          tc::tma_load_2d(tc::smem_addr(w) + w_bytes * kb + c * 128, &p.w, c, kb * kTileK, bar(ctl.w));
+    }
+    __syncwarp();
     // bfloat16 operands, f32 sums, 128 x bn, w along its other axis
     const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 16 | (uint32_t)(p.bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
     int buf = 0, acc = 0;
@@ -189,31 +196,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_grad(const __grid_constant_
             tc::mma_bf16(d, tc::smem_desc(at + i * 32, 64 * 128, 1024), tc::smem_desc(bt + i * 16 * 128, 64 * 128, 1024), idesc,
                          kb > 0 || i > 0);
           if (kb + 1 == p.kblocks || (kb + 1) * 8 / CX != group) tc::mma_commit(bar(ctl.a_empty[buf][group]));
+          if (kb + 1 == p.kblocks) tc::mma_commit(bar(ctl.acc_full[acc]));
         }
         __syncwarp();
       }
-      if (ok && tc::elect_one()) tc::mma_commit(bar(ctl.acc_full[acc]));
-      __syncwarp();
-      if (++buf == p.bufs) buf = 0, parity ^= 1;
+      if (++buf == kBufs<GROUPS>) buf = 0, parity ^= 1;
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }
-    if (!ok) {  // gave up: nothing may be in flight when the tensor memory is freed
+    if (!ok) {  // gave up: nothing may be in flight when the block ends and the tensor memory is freed
       if (tc::elect_one()) tc::mma_commit(bar(ctl.drain));
       __syncwarp();
       tc::mbar_drain(bar(ctl.drain), 0, p.wait_limit);
+      if (!p.drop) tc::mbar_drain(bar(ctl.w), 0, p.wait_limit);
     }
   } else {
     const int quad = warp & 3;
     unsigned char* out = epi + quad * 2 * kBufBytes;
     int acc = 0, slot = 0;
     uint32_t parity = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      ok = tc::mbar_wait_warp(bar(ctl.acc_full[acc]), parity, g);
-      if (!ok) break;
+    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+      if (!tc::mbar_wait_warp(bar(ctl.acc_full[acc]), parity, g)) break;
       tc::fence_after();
-      const int64_t row = (int64_t)t * kTileM + quad * 32;
+      const uint32_t row = (uint32_t)t * kTileM + quad * 32;
       for (int c = 0; row < p.rows && c < p.cols; c += kBufCols, slot ^= 1) {
         float v[32];
         tc::tmem_load32(tmem + acc * (p.tmem_cols / 2) + ((uint32_t)(quad * 32) << 16) + c, v);
@@ -258,10 +263,14 @@ int grid_of(int64_t rows) {
   return (int)(tiles < kSms ? tiles : kSms);
 }
 
+int smem_of(const Args& p, int bufs) {
+  return 1024 + kSmemCtl + kEpiBytes + kFoldBytes + (p.has_dx ? p.kblocks * (p.bn * kTileK * 2 + bufs * kABytes) : 0);
+}
+
 template <int CX, int GROUPS>
-gs_status launch(const Args& p, int grid, int smem, cudaStream_t st, const char* where) {
+gs_status launch(const Args& p, int grid, cudaStream_t st, const char* where) {
   cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_grad<CX, GROUPS>, kSmemMost);
-  if (e == cudaSuccess) e = gs::launch(k_mma_grad<CX, GROUPS>, dim3(grid), kThreads, smem, st, p);
+  if (e == cudaSuccess) e = gs::launch(k_mma_grad<CX, GROUPS>, dim3(grid), kThreads, smem_of(p, kBufs<GROUPS>), st, p);
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
@@ -272,8 +281,11 @@ namespace gs {
 int grad_parts(int64_t rows) { return grid_of(rows); }
 
 bool grad_takes(const gs_linear_desc* d, const void* dy, const void* z, const void* w, const void* dx) {
+  // (32 bits for the bytes from one row to the next keep the addresses at one instruction each)
+  auto near = [&](int64_t ld) { return d->rows <= 1 || ld < (int64_t(1) << 31); };
   return d->dtype == GS_BF16 && d->out_features <= kMost && d->in_features <= kMost && d->out_features % 8 == 0 &&
-         rows_aligned16(dy, d->rows, d->ldy, GS_BF16) && (!z || rows_aligned16(z, d->rows, d->ldz, GS_BF16)) &&
+         near(d->ldy) && rows_aligned16(dy, d->rows, d->ldy, GS_BF16) &&
+         (!z || (near(d->ldz) && rows_aligned16(z, d->rows, d->ldz, GS_BF16))) &&
          (!dx || (tma_takes(w, d->out_features, d->in_features, d->ldw, GS_BF16) &&
                   tma_takes(dx, d->rows, d->in_features, d->lddx, GS_BF16)));
 }
@@ -283,25 +295,23 @@ gs_status grad_run(const gs_linear_desc* d, const void* dy, const void* z, const
   Args p{};
   p.dy = static_cast<const bf16*>(dy), p.z = static_cast<const bf16*>(z), p.dz = static_cast<bf16*>(dz);
   p.part = part;
-  p.rows = d->rows, p.ldy = d->ldy, p.ldz = d->ldz, p.lddz = lddz;
+  p.rows = (uint32_t)d->rows;
+  p.dy_bytes = (uint32_t)(2 * d->ldy), p.z_bytes = (uint32_t)(2 * d->ldz), p.dz_bytes = (uint32_t)(2 * lddz);
   p.n = d->out_features, p.cols = d->in_features, p.act = d->act, p.tiles = (int)ceil_div(d->rows, kTileM);
   p.kblocks = (int)ceil_div(p.n, kTileK), p.bn = (int)ceil_div(d->in_features, 64) * 64;
   p.tmem_cols = p.bn <= 64 ? 128 : p.bn <= 128 ? 256 : 512;
   p.has_dx = dx != nullptr;
   p.status = status, p.wait_limit = wait_us(), p.drop = dx ? take_drop_copy() : 0;
-  // two buffers of dz where they fit: the next tile's is written while this one's products run
-  const int fixed = 1024 + kSmemCtl + kEpiBytes + kFoldBytes + (dx ? p.kblocks * p.bn * kTileK * 2 : 0);
-  p.bufs = fixed + 2 * p.kblocks * kABytes <= kSmemMost ? 2 : 1;
-  const int smem = fixed + (dx ? p.bufs * p.kblocks * kABytes : 0);
   if (dx && !(encode_map(&p.w, w, p.n, d->in_features, d->ldw, 64, GS_BF16) &&
               encode_map(&p.dx, dx, d->rows, d->in_features, d->lddx, 32, GS_BF16, 64)))
     return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   const int grid = grid_of(d->rows);
-  // as many threads along a row as its blocks of k have columns (256 -> 256 with one buffer: 191 us in groups, 197
-  // without; 128 -> 256 with two: 382 and 365 for 1.2M rows)
-  if (p.n <= 64) return launch<8, 1>(p, grid, smem, st, where);
-  if (p.n <= 128) return launch<16, 1>(p, grid, smem, st, where);
-  return p.bufs == 1 && p.kblocks == 4 ? launch<8, 4>(p, grid, smem, st, where) : launch<32, 1>(p, grid, smem, st, where);
+  // As many threads along a row as its blocks of k have columns; in groups only where two buffers do not fit (an
+  // earlier form of the kernel, 300K x 256 -> 256, one buffer: 191 us in groups, 197 without; 1.2M x 128 -> 256, two
+  // buffers: 382 and 365).  Two buffers of up to three blocks always fit.
+  if (p.n <= 64) return launch<8, 1>(p, grid, st, where);
+  if (p.n <= 128) return launch<16, 1>(p, grid, st, where);
+  return smem_of(p, 2) <= kSmemMost ? launch<32, 1>(p, grid, st, where) : launch<8, 4>(p, grid, st, where);
 }
 
 }  // namespace gs
