@@ -252,10 +252,49 @@ __device__ __forceinline__ void act_value2(float& a, float& b, int act) {
   }
 }
 // ------------------------------------------------------------------ folds of split sums
+// Column sums in parts ([parts][n], 32 bits) added in order: 32 columns by 32 interleaved sets of parts a block, the
+// same sums for any whole number of warps.  part NULL: nothing.
+struct ColumnFold {
+  const float* part;
+  int parts, n;
+  void* out;
+};
+template <typename T>
+__device__ __forceinline__ void column_fold(const ColumnFold& a, int block) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, c = block * 32 + lane;
+  for (int w = threadIdx.x >> 5; w < 32; w += blockDim.x >> 5) {
+    float v = 0.f;
+    if (c < a.n) {
+#pragma unroll 8
+      for (int p = w; p < a.parts; p += 32) v += a.part[(int64_t)p * a.n + c];
+    }
+    s[w][lane] = v;
+  }
+  __syncthreads();
+  for (int w = threadIdx.x >> 5; w < 32; w += blockDim.x >> 5) {  // column w of the block
+    float v = s[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int col = block * 32 + w;
+    if (lane == 0 && col < a.n) static_cast<T*>(a.out)[col] = from_f32<T>(v);
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(1024) k_column_fold(const ColumnFold a) {
+  follow();
+  column_fold<T>(a, blockIdx.x);
+}
+template <typename T>
+inline void launch_column_fold(const ColumnFold& a, cudaStream_t st) {
+  gs::launch(k_column_fold<T>, dim3((unsigned)((a.n + 31) / 32)), 1024, 0, st, a);
+}
+
 // The splits' parts [splits][m][ldp] (32-bit sums) added in order, then z = sum + bias, y = act(z) + residual;
-// `transposed`: the parts hold the transpose of what is written.
-// A block takes 128 neighbouring sums; WAYS warps each add every WAYS-th split of them, four a lane, and
-// the warps' sums are added in order.
+// `transposed`: the parts hold the transpose of what is written.  The first `more`
+// blocks add up `also`, if there is one.
+// A block takes 128 neighbouring sums, or several times as many; WAYS warps each add every WAYS-th split of them, four
+// a lane, and the warps' sums are added in order.
 template <typename T>
 struct FoldArgs {
   const float* part;
@@ -266,14 +305,21 @@ struct FoldArgs {
   int64_t m, ldp, ldr, ldy, ldz;
   int splits, n, act;
   bool transposed;
+  ColumnFold also;
 };
+constexpr int fold_threads(int ways) { return ways > 8 ? 32 * ways : 256; }
 template <typename T, int WAYS>
-__global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
-  constexpr int kGroups = 8 / WAYS;  // groups of 128 sums per block
-  __shared__ float4 s[8][32];
+__global__ void __launch_bounds__(fold_threads(WAYS)) k_fold(const FoldArgs<T> a, unsigned more) {
+  constexpr int kThreads = fold_threads(WAYS), kGroups = kThreads / 32 / WAYS;  // groups of 128 sums per block
+  __shared__ float4 s[kThreads / 32][32];
   follow();
+  if (blockIdx.x < more) {
+    column_fold<T>(a.also, blockIdx.x);
+    return;
+  }
+  const unsigned block = blockIdx.x - more;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % WAYS;
-  const int64_t size = a.m * a.ldp, at = ((int64_t)blockIdx.x * kGroups + warp / WAYS) * 128 + lane * 4;
+  const int64_t size = a.m * a.ldp, at = ((int64_t)block * kGroups + warp / WAYS) * 128 + lane * 4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (at < size) {
 #pragma unroll 8
@@ -284,8 +330,8 @@ __global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
   }
   s[warp][lane] = v;
   __syncthreads();
-  for (int e = threadIdx.x; e < kGroups * 128; e += 256) {
-    const int64_t i = (int64_t)blockIdx.x * kGroups * 128 + e;
+  for (int e = threadIdx.x; e < kGroups * 128; e += kThreads) {
+    const int64_t i = (int64_t)block * kGroups * 128 + e;
     if (i >= size) break;
     int64_t row = i / a.ldp, col = i % a.ldp;
     if (col >= a.n) continue;
@@ -303,9 +349,16 @@ __global__ void __launch_bounds__(256) k_fold(const FoldArgs<T> a) {
     a.y[row * a.ldy + col] = from_f32<T>(t);
   }
 }
+// (32 ways where the sums are too few to fill the device otherwise: 59 x 128 in 152 parts)
 template <typename T>
 inline void launch_fold(const FoldArgs<T>& a, cudaStream_t st) {
   const int64_t groups = (a.m * a.ldp + 127) / 128;
-  if (a.splits >= 16) gs::launch(k_fold<T, 8>, dim3((unsigned)groups), 256, 0, st, a);
-  else gs::launch(k_fold<T, 2>, dim3((unsigned)((groups + 3) / 4)), 256, 0, st, a);
+  const unsigned more = a.also.part ? (unsigned)((a.also.n + 31) / 32) : 0;
+  auto go = [&](auto kernel, int ways) {
+    const int per = fold_threads(ways) / 32 / ways;
+    gs::launch(kernel, dim3((unsigned)((groups + per - 1) / per) + more), fold_threads(ways), 0, st, a, more);
+  };
+  if (a.splits >= 64 && groups <= 2 * 152) go(k_fold<T, 32>, 32);
+  else if (a.splits >= 16) go(k_fold<T, 8>, 8);
+  else go(k_fold<T, 2>, 2);
 }

@@ -74,28 +74,6 @@ __global__ void __launch_bounds__(kThreads) k_act_grad(const T* dy, const T* z, 
   }
 }
 
-// the parts added in order: 32 columns by 32 interleaved sets of parts per block
-template <typename T>
-__global__ void __launch_bounds__(1024) k_bias_fold(const float* part, int parts, int n, T* out) {
-  follow();
-  __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < n) {
-#pragma unroll 8
-    for (int p = w; p < parts; p += 32) v += part[(int64_t)p * n + c];
-  }
-  s[w][lane] = v;
-  __syncthreads();
-  // warp w: column w of the block
-  v = s[lane][w];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + w;
-  if (lane == 0 && col < n) out[col] = from_f32<T>(v);
-}
-
 // ---------------------------------------------------------------- host side
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -214,14 +192,14 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
                            nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
   }
+  const ColumnFold sums{dbias ? bias_part : nullptr, parts, d->out_features, dbias};
   if (dw) {
     const gs::MmaProduct q{dz, x, lddz, d->ldx, true, true, d->out_features, d->in_features, d->rows,
-                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE, pad};
-    if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;
+                           nullptr, nullptr, dw, nullptr, 0, d->lddw, 0, GS_ACT_NONE, pad, 0, sums};
+    return run_product(q, d->dtype, part, status, st, where);
   }
   if (dbias) {
-    gs::launch(k_bias_fold<T>, dim3((unsigned)ceil_div(d->out_features, 32)), 1024, 0, st, (const float*)bias_part,
-               parts, (int)d->out_features, static_cast<T*>(dbias));
+    launch_column_fold<T>(sums, st);
     return gs::check_launch(where);
   }
   return GS_OK;

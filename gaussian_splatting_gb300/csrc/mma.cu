@@ -565,9 +565,12 @@ gs_status mma_run(const MmaProduct& q, void* workspace, int32_t* status, cudaStr
   }
   if (!ok) return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   if (gs_status s = pl.ctas == 2 ? launch<2>(p, 2 * grid, smem, st, where) : launch<1>(p, grid, smem, st, where)) return s;
-  if (!p.part) return GS_OK;
+  if (!p.part) {
+    if (q.also.part) launch_column_fold<bf16>(q.also, st);
+    return check_launch(where);
+  }
   launch_fold(FoldArgs<bf16>{p.part, p.bias, static_cast<const bf16*>(q.residual), static_cast<bf16*>(q.y),
-                             static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
+                             static_cast<bf16*>(q.z), q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false, q.also},
               st);
   return check_launch(where);
 }

@@ -22,6 +22,7 @@ struct MmaProduct {
   int64_t ldr, ldy, ldz;
   int act;
   int64_t a_pad = 0, b_pad = 0;  // zeros that follow each of the operand's rows in memory
+  ColumnFold also = {};          // sums to fold when the product is done, in the launch that folds its splits if any
 };
 
 // bfloat16 whose rows start anywhere (mma_staged.cu).

@@ -830,8 +830,12 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
   }
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
   if (gs_status s = launch_any(p, pl, st, where)) return s;
-  if (!p.part) return GS_OK;
-  launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, pl.swap},
+  if (!p.part) {
+    if (q.also.part) launch_column_fold<float>(q.also, st);
+    return check_launch(where);
+  }
+  launch_fold(FoldArgs<float>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, pl.swap,
+                              q.also},
               st);
   return check_launch(where);
 }

@@ -522,8 +522,12 @@ gs_status staged_run(const MmaProduct& q, void* workspace, int32_t* status, cuda
                     : fits_resident<64>(pl) ? launch<64, true>(p, pl, st, where)
                                             : launch<64, false>(p, pl, st, where))
     return s;
-  if (!p.part) return GS_OK;
-  launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false},
+  if (!p.part) {
+    if (q.also.part) launch_column_fold<bf16>(q.also, st);
+    return check_launch(where);
+  }
+  launch_fold(FoldArgs<bf16>{p.part, p.bias, p.residual, p.y, p.z, q.m, pl.ldp, q.ldr, q.ldy, q.ldz, pl.splits, (int)q.n, q.act, false,
+                             q.also},
               st);
   return check_launch(where);
 }
