@@ -218,6 +218,15 @@ def test_linear_with_many_rows(shape, dtype):
             _close(v, *want[k], f"{k} {act}")
 
 
+# several rounds of tiles by pairs of blocks, the last one short, with columns of its tiles outside
+ROUNDS = [(13_100, 520, 600), (13_100, 600, 520), (13_057, 1024, 768), (4_900, 640, 2064)]
+
+
+@pytest.mark.parametrize("shape", ROUNDS, ids=str)
+def test_linear_with_a_short_last_round(shape):
+    test_linear_with_many_rows(shape, BF16)
+
+
 # narrow layers, whose dz and dx come out of one pass: a tile, a row more, one and two buffers of dz, widths
 # that end inside blocks of 64 and of 16, the widest, one column of vectors
 NARROW = [(128, 256, 256), (129, 72, 8), (1, 256, 256), (20_000, 256, 256), (25_001, 8, 248), (40_000, 200, 128), (33_333, 128, 72),
