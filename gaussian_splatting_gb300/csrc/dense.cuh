@@ -259,31 +259,38 @@ struct ColumnFold {
   int parts, n;
   void* out;
 };
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void column_fold(const ColumnFold& a, int block) {
+  constexpr int kWarps = THREADS / 32, kEach = 32 / kWarps;
   __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, c = block * 32 + lane;
-  for (int w = threadIdx.x >> 5; w < 32; w += blockDim.x >> 5) {
-    float v = 0.f;
-    if (c < a.n) {
-#pragma unroll 8
-      for (int p = w; p < a.parts; p += 32) v += a.part[(int64_t)p * a.n + c];
-    }
-    s[w][lane] = v;
-  }
-  __syncthreads();
-  for (int w = threadIdx.x >> 5; w < 32; w += blockDim.x >> 5) {  // column w of the block
-    float v = s[lane][w];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = block * 32 + lane;
+  float v[kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int col = block * 32 + w;
-    if (lane == 0 && col < a.n) static_cast<T*>(a.out)[col] = from_f32<T>(v);
+  for (int j = 0; j < kEach; ++j) v[j] = 0.f;
+  if (c < a.n) {
+#pragma unroll 8
+    for (int p = warp; p < a.parts; p += 32) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)  // sets warp, warp + kWarps, ..
+        if (p + j * kWarps < a.parts) v[j] += a.part[(int64_t)(p + j * kWarps) * a.n + c];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) s[warp + j * kWarps][lane] = v[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {  // columns warp, warp + kWarps, .. of the block
+    float t = s[lane][warp + j * kWarps];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const int col = block * 32 + warp + j * kWarps;
+    if (lane == 0 && col < a.n) static_cast<T*>(a.out)[col] = from_f32<T>(t);
   }
 }
 template <typename T>
 __global__ void __launch_bounds__(1024) k_column_fold(const ColumnFold a) {
   follow();
-  column_fold<T>(a, blockIdx.x);
+  column_fold<T, 1024>(a, blockIdx.x);
 }
 template <typename T>
 inline void launch_column_fold(const ColumnFold& a, cudaStream_t st) {
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(fold_threads(WAYS)) k_fold(const FoldArgs<T> a
   __shared__ float4 s[kThreads / 32][32];
   follow();
   if (blockIdx.x < more) {
-    column_fold<T>(a.also, blockIdx.x);
+    column_fold<T, kThreads>(a.also, blockIdx.x);
     return;
   }
   const unsigned block = blockIdx.x - more;
