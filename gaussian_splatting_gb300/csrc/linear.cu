@@ -9,7 +9,7 @@
 // dz = dy act'(z) is formed once, in a pass over dy and z that also takes the bias gradient's column
 // sums, and kept in the workspace for the two products that read it.  A narrow bfloat16 layer's pass computes
 // dx as well (mma_grad.cu), with up to 256 inputs and outputs: the dw product's operands are then all that is
-// read twice (300K x 256 -> 256 with GELU 179 us, 211 as separate passes; 3M x 64 -> 64 358 and 510; the two
+// read twice (300K x 256 -> 256 with GELU 174 us, 211 as separate passes; 3M x 64 -> 64 358 and 510; the two
 // meet at 500 rows, 20 us).
 #include "mma.cuh"
 #include "mma_grad.cuh"

