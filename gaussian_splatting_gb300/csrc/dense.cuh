@@ -183,9 +183,10 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   }
 }
 
-// The same for pairs of elements: sm_100 adds, multiplies and fma's two floats in one instruction.  For the epilogue
-// of mma_staged.cu (300K x 255 -> 257 bf16 with GELU and z: 425 us, 456 one by one); the other kernels, whose
-// registers are all taken, lose by the pairs' alignment.  The roundings are those of one element at a time.
+// The same for pairs of elements: sm_100 adds, multiplies and fma's two floats in one instruction.  For the epilogues
+// of mma_staged.cu (300K x 255 -> 257 bf16 with GELU and z: 425 us, 456 one by one) and of mma.cu's pairs of blocks; the
+// other kernels, whose registers are all taken, lose by the pairs' alignment.  The roundings are those of one element
+// at a time.
 struct F2 {
   uint64_t v;
   __device__ __forceinline__ F2() {}

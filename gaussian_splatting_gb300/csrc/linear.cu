@@ -19,11 +19,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// dz = dy act'(z) to `dz` (if wanted; a row's last 16 bytes are filled up with zeros), and its column sums over this block's rows to part[blockIdx.x].
-// A thread owns VE columns; CX threads lie along a row, kThreads / CX rows side by side.
-// (ACT is the compiler's: a branch for each element would keep their evaluations from overlapping; 15,965 x 4096 bf16
-// with GELU 60 us, 63.5 with branches.  Four blocks to an SM, or that layer's
-// whole backward takes 241 us, not 235.)
+// dz = dy act'(z) to `dz` (if wanted; a row's last 16 bytes are filled up with zeros), and its column sums over this
+// block's rows to part[blockIdx.x].  A thread owns VE columns; CX threads lie along a row, kThreads / CX rows side by
+// side.  (ACT is the compiler's: a branch for each element would keep their evaluations from overlapping; 15,965 x 4096
+// bf16 with GELU 60 us, 63.5 with branches.  Four blocks to an SM, or that layer's whole backward takes 241 us, not 235.)
 template <typename T, bool VEC, int CX, int ACT>
 __device__ __forceinline__ void act_grad_rows(const T* dy, const T* z, int64_t rows, int n, int64_t lddy, int64_t ldz, T* dz,
                                               int64_t lddz, int c, int ry, float* sum) {
