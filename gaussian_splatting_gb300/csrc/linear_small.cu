@@ -7,7 +7,8 @@
 //     the weight gradient as a sum of at most 16 outer products (k_few_dw).  Bound by reading or writing w.
 //   small products (at most 2^26 multiply-adds): a 32 x 64 tile per block, 64 of k at a time (k_small_fwd)
 //   backward of narrow layers (64 x 64 at most) over up to 32,768 rows: dz, its column sums, dx and the
-//     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order
+//     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order; of thin ones (16 x 16)
+//     over any number (k_thin_bwd)
 // All sums in 32 bits in a fixed order.
 #include "small.cuh"
 
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_small_bwd(const Bwd<T> p, float
       const int r = rr + i * (kThreads / kNarrow);
       const bool in = r0 + r < p.rows;
       dz[r][c] = in && c < p.out ? dz_at(p, r0 + r, c) : 0.f;
-      xs[r][c] = in && c < p.in ? to_f32<T>(p.x[(r0 + r) * p.ldx + c]) : 0.f;
+      xs[r][c] = p.x && in && c < p.in ? to_f32<T>(p.x[(r0 + r) * p.ldx + c]) : 0.f;
     }
     __syncthreads();
     if (p.dx) {
@@ -306,6 +307,63 @@ __global__ void __launch_bounds__(kThreads, 2) k_small_bwd(const Bwd<T> p, float
   if (tid < kNarrow) out[kNarrow * kNarrow + tid] = ab;
 }
 
+// Thin layers (16 x 16 at most) over any number of rows: 256 rows of dz and x at a time in shared memory, in which a
+// thread owns an entry of dw, then a row of dx.  parts as above; of a row only the first `in` are written.
+constexpr int kThin = 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_thin_bwd(const Bwd<T> p, float* parts) {
+  follow();
+  __shared__ float dz[kThreads][kThin + 1], xs[kThreads][kThin + 1], ws[kThin][kThin];
+  const int tid = threadIdx.x, n = tid / kThin, c = tid % kThin;
+  const bool own = n < p.out && c < p.in;
+  if (p.dx) ws[n][c] = own ? to_f32<T>(p.w[n * p.ldw + c]) : 0.f;
+  float aw = 0.f, ab = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * kThreads; r0 < p.rows; r0 += (int64_t)gridDim.x * kThreads) {
+    const int m = p.rows - r0 < kThreads ? (int)(p.rows - r0) : kThreads;
+    __syncthreads();
+#pragma unroll 4
+    for (int e = tid; e < kThreads * p.out; e += kThreads) {
+      const int r = e / p.out, k = e - r * p.out;
+      dz[r][k] = r < m ? dz_at(p, r0 + r, k) : 0.f;
+    }
+    if (p.x) {
+#pragma unroll 4
+      for (int e = tid; e < kThreads * p.in; e += kThreads) {
+        const int r = e / p.in, k = e - r * p.in;
+        xs[r][k] = r < m ? to_f32<T>(p.x[(r0 + r) * p.ldx + k]) : 0.f;
+      }
+    }
+    __syncthreads();
+    if (own && p.x) {
+#pragma unroll 8
+      for (int r = 0; r < kThreads; ++r) aw = fmaf(dz[r][n], xs[r][c], aw);
+    }
+    if (tid < p.out) {
+#pragma unroll 8
+      for (int r = 0; r < kThreads; ++r) ab += dz[r][tid];
+    }
+    if (!p.dx) continue;
+    __syncthreads();
+    float acc[kThin] = {};
+    for (int k = 0; k < p.out; ++k) {
+      const float d = dz[tid][k];
+#pragma unroll
+      for (int j = 0; j < kThin; ++j) acc[j] = fmaf(d, ws[k][j], acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kThin; ++j) xs[tid][j] = acc[j];
+    __syncthreads();
+#pragma unroll 4
+    for (int e = tid; e < m * p.in; e += kThreads) {
+      const int r = e / p.in, k = e - r * p.in;
+      p.dx[(r0 + r) * p.lddx + k] = from_f32<T>(xs[r][k]);
+    }
+  }
+  float* out = parts + (int64_t)blockIdx.x * (kNarrow + 1) * kNarrow;
+  if (own) out[n * kNarrow + c] = aw;
+  if (tid < p.out) out[kNarrow * kNarrow + tid] = ab;
+}
+
 // a row of dw (or, last, db) per block: 64 columns by 4 interleaved sets of parts
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_small_bwd_fold(const float* parts, int n_parts, int in, int out, T* dw, int64_t lddw,
@@ -336,9 +394,10 @@ bool vec_ok(const void* p, int64_t rows, int64_t ld, int width, int32_t dtype) {
   return width % (16 / (int)gs::dtype_size(dtype)) == 0 && gs::rows_aligned16(p, rows, ld, dtype);
 }
 
-int small_bwd_grid(int64_t rows) {
-  const int64_t tiles = ceil_div(rows, kTileR);
-  return (int)(tiles < 152 ? tiles : 152);
+int small_bwd_grid(const gs_linear_desc* d) {
+  const bool thin = d->rows > kNarrowRows;
+  const int64_t tiles = ceil_div(d->rows, thin ? kThreads : kTileR), most = thin ? 4 * 152 : 152;
+  return (int)(tiles < most ? tiles : most);
 }
 
 template <typename T>
@@ -365,7 +424,8 @@ gs_status fwd(const gs_linear_desc* d, const void* x, const void* w, const void*
 template <typename T>
 gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
               void* dbias, void* workspace, cudaStream_t st, const char* where) {
-  const Bwd<T> p{(const T*)dy, (const T*)x, (const T*)w, (const T*)z, (T*)dx, (T*)dw, (T*)dbias,
+  // x is read for dw alone
+  const Bwd<T> p{(const T*)dy, dw ? (const T*)x : nullptr, (const T*)w, (const T*)z, (T*)dx, (T*)dw, (T*)dbias,
                  d->ldy, d->ldx, d->ldw, d->ldz, d->lddx, d->lddw, (int)d->rows, d->in_features, d->out_features, d->act};
   constexpr int VE = 16 / sizeof(T);
   if (d->rows <= kFewRows) {
@@ -384,10 +444,11 @@ gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void
     }
     return gs::check_launch(where);
   }
-  const int grid = small_bwd_grid(d->rows);
+  const int grid = small_bwd_grid(d);
   float* parts = static_cast<float*>(workspace);
   // only when the kernel before it is done, as k_act_grad (2,048 x 64 f32: 12.3 us, 13.2 with gs::launch)
-  k_small_bwd<T><<<grid, kThreads, 0, st>>>(p, parts);
+  if (d->rows > kNarrowRows) k_thin_bwd<T><<<grid, kThreads, 0, st>>>(p, parts);
+  else k_small_bwd<T><<<grid, kThreads, 0, st>>>(p, parts);
   if (gs_status s = gs::check_launch(where)) return s;
   if (!dw && !dbias) return GS_OK;
   gs::launch(k_small_bwd_fold<T>, dim3(d->out_features + 1), kThreads, 0, st, (const float*)parts, grid,
@@ -412,10 +473,16 @@ gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const
 
 bool small_bwd_takes(const gs_linear_desc* d) {
   if (d->rows <= kFewRows) return d->out_features <= 8192;
-  return d->in_features <= kNarrow && d->out_features <= kNarrow && d->rows <= kNarrowRows;
+  if (d->rows <= kNarrowRows) return d->in_features <= kNarrow && d->out_features <= kNarrow;
+  // Thin layers over more rows, for which the tensor-core tiles are nearly empty (2.9M x 9 -> 5: 218 us, 750 by the
+  // tensor cores in bfloat16; 225 and 844 in float32); not bfloat16 in 16-byte vectors, which mma_grad.cu passes over
+  // faster (3M x 16 -> 16 with GELU: 281 us, 505 here).
+  const bool vectors = d->dtype == GS_BF16 && d->in_features % 8 == 0 && d->out_features % 8 == 0 && d->ldx % 8 == 0 &&
+                       d->ldw % 8 == 0 && d->ldy % 8 == 0 && d->lddx % 8 == 0 && (d->act == GS_ACT_NONE || d->ldz % 8 == 0);
+  return d->in_features <= kThin && d->out_features <= kThin && !vectors;
 }
 size_t small_bwd_workspace(const gs_linear_desc* d) {
-  return d->rows <= kFewRows ? 0 : (size_t)small_bwd_grid(d->rows) * (kNarrow + 1) * kNarrow * sizeof(float);
+  return d->rows <= kFewRows ? 0 : (size_t)small_bwd_grid(d) * (kNarrow + 1) * kNarrow * sizeof(float);
 }
 gs_status small_bwd(const gs_linear_desc* d, const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
                     void* dbias, void* workspace, cudaStream_t st, const char* where) {

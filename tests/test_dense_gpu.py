@@ -193,6 +193,31 @@ def test_linear_small_calls(shape, dtype):
                 assert i not in kept or torch.equal(part[i], full[i])
 
 
+# thin layers over more rows than the small backward takes: one entry, odd widths, the widest, one wider
+THIN = [(40_000, 1, 1), (33_001, 9, 5), (50_000, 16, 16), (200_000, 3, 16), (170_001, 16, 1), (40_000, 17, 4)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", THIN, ids=str)
+def test_linear_thin_layers(shape, dtype):
+    test_linear_small_calls(shape, dtype)
+
+
+def test_a_backward_without_dw_does_not_read_x():
+    for rows, n in ((2000, 40), (40_000, 9), (8, 24), (40_000, 72)):
+        dy, w = _rand((rows, n), F32, 1), _rand((n, n), F32, 2)
+        want, _, wb = dense.linear_bwd(dy, dy, w, need_dw=False)
+        d = N.LinearDesc()
+        d.rows, d.in_features, d.out_features, d.dtype, d.act = rows, n, n, N.GS_F32, N.GS_ACT_NONE
+        d.ldx = d.ldw = d.ldy = d.lddx = d.lddw = n
+        dx, db = torch.empty_like(dy), torch.empty(n, device="cuda")
+        need = N.gs_linear_bwd_workspace_size(d)
+        ws = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
+        N.gs_linear_bwd(d, dy, None, w, None, dx, None, db, ws, need)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want) and torch.equal(db, wb)
+
+
 # enough tiles for every kernel's persistent walk to take several, ranges of k in the weight gradient, ragged
 # last tiles in each direction, widths on and off 16-byte rows
 MANY = [(33_000, 136, 264), (20_011, 256, 200), (40_000, 64, 59), (25_000, 59, 61), (19_999, 520, 131), (16_500, 264, 512)]
