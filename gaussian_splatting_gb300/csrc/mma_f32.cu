@@ -474,11 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
     const bool with_res = BN == 64 && p.residual && !p.part;
     const bool dense = BN == 64 && !p.part && (p.y_way == kDense || (p.z && p.z_way == kDense) || (with_res && p.r_way == kDense));
     const uint32_t res_bar = bar(ctl.res[with_res && p.r_way == kDense ? quad : warp]);
-    auto quad_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(4 + quad) : "memory"); };
+    auto quad_sync = [&]() {
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(4 + quad) : "memory");
+    };
+    // Dense rows are written by the two warps of a quadrant together, which meet at a barrier without a limit.  Each
+    // of them may give up in a wait of its own, so they agree after every such wait on whether they go on: the other
+    // would wait for ever for one that has left.
+    auto quad_agree = [&](bool mine) {
+      uint32_t both;
+      __syncwarp();
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 p, %2, 0;\n\t"
+          "bar.red.and.pred q, %1, 64, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(both)
+          : "r"(4 + quad), "r"((uint32_t)mine)
+          : "memory");
+      return both != 0;
+    };
     int n_acc = 0, res_used = 0;
     bool res_flying = false;
     bool ok = true;
     if (p.resident && (int)blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
+    if (dense) ok = quad_agree(ok);
     // this warp's piece of tile t
     auto place = [&](int t, uint32_t& row0, uint32_t& col0, int& split) {
       int64_t m0, n0;
@@ -551,6 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
       }
+      if (dense) {
+        // stores of the last tile have read the buffers (as below) before either warp writes to them
+        if (tc::elect_one()) tc::bulk_wait_read0();
+        ok = quad_agree(ok);
+      }
       if (!ok) break;
       if (!in) {
         if (with_res) ask_residual(t + gridDim.x);
@@ -616,9 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         if (col0 + c >= (uint32_t)n && !dense) break;
         // stores of the last piece have read the buffers; a bulk store is its issuer's to wait for, and the
         // same lane of a warp issues all of that warp's
-        if (tc::elect_one()) tc::bulk_wait_read0();
-        if (dense) quad_sync();
-        else __syncwarp();
+        if (!dense) {
+          if (tc::elect_one()) tc::bulk_wait_read0();
+          __syncwarp();
+        }
         float* v = sum + c;
         if (p.bias) {
           const float bias = col0 + c + lane < (uint32_t)n ? p.bias[col0 + c + lane] : 0.f;
@@ -645,10 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
             } else {
               if (p.r_way == kDense || col0 < (uint32_t)n) {
                 ok = tc::mbar_wait_warp(res_bar, (uint32_t)(res_used & 1), g);
-                if (!ok) break;
-                ++res_used;
-                res_flying = false;
+                if (ok) {
+                  ++res_used;
+                  res_flying = false;
+                }
               }
+              if (dense) ok = quad_agree(ok);
+              if (!ok) break;
               if (p.r_way == kDense) {
                 const float* d = reinterpret_cast<const float*>(r_buf) + lane * n + half * 32;
 #pragma unroll

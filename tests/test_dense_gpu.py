@@ -718,3 +718,30 @@ def test_a_wait_that_runs_out_in_a_narrow_backward(width):
     for a, b in zip(dense.linear_bwd(x, x, w, z, act="gelu", status=status), want):
         assert torch.equal(a, b)
     assert status.item() == 0
+
+
+# rows of 59 columns without gaps, which the two warps of a quadrant write together: few tiles, and enough of them for
+# the weights to stay in shared memory
+@pytest.mark.parametrize("rows", [20_000, 60_000])
+@pytest.mark.parametrize("with_r,keep_z", [(True, False), (False, True), (True, True)])
+def test_a_wait_that_runs_out_where_warps_write_rows_together(rows, with_r, keep_z):
+    """Warps that meet at a barrier of their own agree on whether a wait ran out: no one is left waiting there."""
+    x, w = _rand((rows, 128), F32, 1), _rand((59, 128), F32, 2, 0.1)
+    r = _rand((rows, 59), F32, 3) if with_r else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want, wz = dense.linear_fwd(x, w, None, r, act="gelu", keep_z=keep_z, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    lib = N.load()
+    try:
+        lib.gs_debug_set_wait_limit(2000)
+        lib.gs_debug_drop_publish(3)
+        dense.linear_fwd(x, w, None, r, act="gelu", keep_z=keep_z, status=status)
+        torch.cuda.synchronize()
+    finally:
+        lib.gs_debug_set_wait_limit(0)
+        lib.gs_debug_drop_publish(0)
+    assert status.item() == 2
+    status.zero_()
+    y, z = dense.linear_fwd(x, w, None, r, act="gelu", keep_z=keep_z, status=status)
+    assert status.item() == 0 and torch.equal(y, want) and (not keep_z or torch.equal(z, wz))
