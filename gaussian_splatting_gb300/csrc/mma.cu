@@ -204,6 +204,7 @@ __device__ bool partial_tile(const Args& p, const EpiState& e, const tc::Guard& 
   for (int c = e.part; c * 32 < p.bn; c += kParts) {
     if (n0 + c * 32 >= p.ldp) break;
     float v[32];
+    __syncwarp();  // the load is the whole warp's: the lanes without a row of the piece before wait for the others
     tc::tmem_load32(tmem + ((uint32_t)(e.quad * 32) << 16) + c * 32, v);
     if (row < p.m) {
 #pragma unroll

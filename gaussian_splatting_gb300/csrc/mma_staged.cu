@@ -378,8 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_staged(const __grid_constan
       tc::fence_after();
       const uint32_t d = tmem + acc * BN + ((uint32_t)(quad * 32) << 16) + half * kCols;
       const int rows = (int)min((int64_t)32, p.m - row0);
-      for (int c = 0; in && c < kCols; c += 32) {
+      for (int c = 0; in && c < kCols && col0 + c < (p.part ? p.ldp : p.n); c += 32) {
         float v[32];
+        __syncwarp();  // the load is the whole warp's: the lanes that left the piece before early are waited for
         tc::tmem_load32(d + c, v);
         if (p.part) {
           const int64_t row = row0 + lane;

@@ -745,3 +745,10 @@ def test_a_wait_that_runs_out_where_warps_write_rows_together(rows, with_r, keep
     status.zero_()
     y, z = dense.linear_fwd(x, w, None, r, act="gelu", keep_z=keep_z, status=status)
     assert status.item() == 0 and torch.equal(y, want) and (not keep_z or torch.equal(z, wz))
+
+
+# bfloat16 off 16-byte rows: widths that end inside the first 32 columns of a warp's share of a tile, in it and at its end;
+# rows that end inside a warp's
+@pytest.mark.parametrize("shape", [(40_001, 59, 131), (40_010, 61, 97), (20_031, 73, 257), (39_999, 65, 160), (700, 130, 65)], ids=str)
+def test_unaligned_widths_that_end_inside_a_warps_columns(shape):
+    test_linear_with_many_rows(shape, BF16)
