@@ -233,7 +233,10 @@ __device__ __forceinline__ void activate(float* v) {
 
 // GROUPS: the splitters work as one or two teams that take the pieces in turn.  Two hide a team's latency
 // behind the other's, but each wants two raw buffers of its own.
-template <int BN, int GROUPS>
+// DENSE: some array of the epilogue takes whole rows (tiles of 64 columns only).  A kernel of its own, so that the others
+// do without the barriers between its warps (300K x 256 -> 256 with GELU and z: 448 us, 463 in one kernel; the 59-column
+// record 57.7 and 58.9).
+template <int BN, int GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__ Args p) {
   constexpr int TEAM = kSplitters / GROUPS;
   static_assert(kStages % GROUPS == 0, "stages per team");
@@ -472,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
     // (z and the residual: tiles of 64 columns only)
     unsigned char* const z_buf = r_buf + (p.residual ? kEpiWarps * kBufBytes : 0);
     const bool with_res = BN == 64 && p.residual && !p.part;
-    const bool dense = BN == 64 && !p.part && (p.y_way == kDense || (p.z && p.z_way == kDense) || (with_res && p.r_way == kDense));
-    const uint32_t res_bar = bar(ctl.res[with_res && p.r_way == kDense ? quad : warp]);
+    const uint32_t res_bar = bar(ctl.res[DENSE ? quad : warp]);
     auto quad_sync = [&]() {
       __syncwarp();
       asm volatile("bar.sync %0, 64;" ::"r"(4 + quad) : "memory");
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
     bool res_flying = false;
     bool ok = true;
     if (p.resident && (int)blockIdx.x < total) ok = tc::mbar_wait_warp(bar(ctl.resident), 0, g);
-    if (dense) ok = quad_agree(ok);
+    if (DENSE) ok = quad_agree(ok);
     // this warp's piece of tile t
     auto place = [&](int t, uint32_t& row0, uint32_t& col0, int& split) {
       int64_t m0, n0;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       place(t, row0, col0, split);
       const int rows = min(32, (int)((int64_t)m - row0));
       if (rows <= 0) return;
-      if (BN == 64 && p.r_way == kDense) {
+      if (DENSE && p.r_way == kDense) {
         if (rows < 32) return;  // read where it is used
         if (half == 0 && tc::elect_one()) {
           tc::mbar_expect_tx(res_bar, 128 * n);
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         }
         res_flying = true;
       } else if (col0 < (uint32_t)n) {
-        if (p.r_way == kBox) {
+        if (!DENSE && p.r_way == kBox) {
           if (tc::elect_one()) {
             tc::mbar_expect_tx(res_bar, kBufBytes);
             tc::tma_load_2d(tc::smem_addr(r_buf) + half * kBufBytes, &p.map_r, (int)col0, (int)row0, res_bar);
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       int split;
       place(t, row0, col0, split);
       const int k_lo = split * p.kb_per_split, k_hi = min(k_lo + p.kb_per_split, p.kblocks);
-      const bool in = row0 < (uint32_t)m && (dense || col0 < (uint32_t)(p.part ? p.ldp : n));
+      const bool in = row0 < (uint32_t)m && (DENSE || col0 < (uint32_t)(p.part ? p.ldp : n));
       const int rows = min(32, (int)((int64_t)m - row0));
       float sum[kCols];
 #pragma unroll
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(ctl.acc_empty[acc]));
       }
-      if (dense) {
+      if (DENSE) {
         // stores of the last tile have read the buffers (as below) before either warp writes to them
         if (tc::elect_one()) tc::bulk_wait_read0();
         ok = quad_agree(ok);
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       // a piece v (a lane: 32 columns of a row) through a buffer to its array
       auto write_piece = [&](const float* v, int way, unsigned char* b8, const CUtensorMap* map, float* out, int64_t ld, int c) {
         float* b = reinterpret_cast<float*>(b8 + half * kBufBytes);
-        if (way == kBox) {
+        if (!DENSE && way == kBox) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             *reinterpret_cast<float4*>(reinterpret_cast<unsigned char*>(b) + lane * 128 + ((q ^ (lane & 7)) << 4)) =
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
             tc::bulk_commit();
           }
           __syncwarp();
-        } else if (BN == 64 && way == kDense) {
+        } else if (DENSE && way == kDense) {
           float* d = reinterpret_cast<float*>(b8) + lane * n + half * 32;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -638,10 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
       };
 #pragma unroll
       for (int c = 0; c < kCols; c += 32) {
-        if (col0 + c >= (uint32_t)n && !dense) break;
+        if (col0 + c >= (uint32_t)n && !DENSE) break;
         // stores of the last piece have read the buffers; a bulk store is its issuer's to wait for, and the
         // same lane of a warp issues all of that warp's
-        if (!dense) {
+        if (!DENSE) {
           if (tc::elect_one()) tc::bulk_wait_read0();
           __syncwarp();
         }
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         else if (p.act == GS_ACT_SILU) activate<GS_ACT_SILU>(v);
         if (with_res) {
           const float* b = reinterpret_cast<const float*>(r_buf + half * kBufBytes);
-          if (p.r_way == kDense && rows < 32) {
+          if (DENSE && p.r_way == kDense && rows < 32) {
             const float* src = p.residual + (int64_t)(row0 + lane) * n + col0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -669,16 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] += b[lane * 32 + (i ^ lane)];
             } else {
-              if (p.r_way == kDense || col0 < (uint32_t)n) {
+              if (DENSE || col0 < (uint32_t)n) {
                 ok = tc::mbar_wait_warp(res_bar, (uint32_t)(res_used & 1), g);
                 if (ok) {
                   ++res_used;
                   res_flying = false;
                 }
               }
-              if (dense) ok = quad_agree(ok);
-              if (!ok) break;
-              if (p.r_way == kDense) {
+              if (!DENSE && !ok) break;  // (what a dense tile's warp reads below without its residual is not used)
+              if (DENSE) {
                 const float* d = reinterpret_cast<const float*>(r_buf) + lane * n + half * 32;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -694,8 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
             }
           }
           tc::fence_async_smem();  // the reads above come before the next copy into the buffer
-          if (dense) quad_sync();
+          if (DENSE) ok = quad_agree(ok);
           else __syncwarp();
+          if (!ok) break;
           ask_residual(t + gridDim.x);
         }
         write_piece(v, p.y_way, y_buf, &p.map_y, p.y, p.ldy, c);
@@ -771,14 +773,14 @@ Room room_of(const Plan& pl, bool resident, int bufs) {
   return r;
 }
 
-template <int BN, int GROUPS>
+template <int BN, int GROUPS, bool DENSE>
 gs_status launch(Args& p, const Room& r, int grid, cudaStream_t st, const char* where) {
   // every team of splitters has raw buffers of its own: a wait for a buffer's next phase is then always made
   // by those who have seen the phase before it, as the phases' one bit of parity demands
   p.raws = r.raws - r.raws % GROUPS;
   if (p.raws < GROUPS) return gs::set_error(GS_ERR_INVALID, "%s: no room for raw buffers", where);
-  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_f32<BN, GROUPS>, kSmemMost);
-  if (e == cudaSuccess) e = gs::launch(k_mma_f32<BN, GROUPS>, dim3(grid), kThreads, r.fixed + p.raws * r.raw, st, p);
+  cudaError_t e = gs::max_dynamic_smem((const void*)k_mma_f32<BN, GROUPS, DENSE>, kSmemMost);
+  if (e == cudaSuccess) e = gs::launch(k_mma_f32<BN, GROUPS, DENSE>, dim3(grid), kThreads, r.fixed + p.raws * r.raw, st, p);
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
@@ -794,8 +796,10 @@ gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where
   } else {
     r = room_of(pl, false, bufs);
   }
-  if (pl.bn == 128) return launch<128, 1>(p, r, grid, st, where);
-  return r.raws >= 4 ? launch<64, 2>(p, r, grid, st, where) : launch<64, 1>(p, r, grid, st, where);
+  const bool dense = !p.part && (p.y_way == kDense || p.z_way == kDense || p.r_way == kDense);
+  if (pl.bn == 128) return launch<128, 1, false>(p, r, grid, st, where);
+  if (dense) return r.raws >= 4 ? launch<64, 2, true>(p, r, grid, st, where) : launch<64, 1, true>(p, r, grid, st, where);
+  return r.raws >= 4 ? launch<64, 2, false>(p, r, grid, st, where) : launch<64, 1, false>(p, r, grid, st, where);
 }
 
 }  // namespace
