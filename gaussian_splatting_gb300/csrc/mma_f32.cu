@@ -11,6 +11,11 @@
 // their own, and every 256 of k both are read back and added in registers with ordinary rounding.  Six
 // bfloat16 products at 2.2 PFLOP/s nominal leave about 375 TFLOP/s; the FP32 pipe has 75.
 //
+// A value whose first part is not finite (infinities, NaN, and from 2^128 - 2^119 on, which rounds to infinity) has no
+// such parts: what the first leaves is inf - inf, and its sums come out as NaN.  A sum that is NaN is therefore taken
+// once more on the FP32 pipe (plain_sums), from the values themselves: an infinity stays one, the largest values give
+// what they should, and a true NaN stays.  The test for it costs half an instruction per sum of a tile.
+//
 // One persistent block per SM; its warps:
 //   warp 17       copies pieces of 32 of k of A and B, float32 as they are, to a ring of raw buffers by TMA
 //   warps 8 - 15  split a raw piece into the three parts and store them to a stage in the tensor core's
@@ -223,6 +228,57 @@ __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int to
     c.t += gridDim.x;
     seek(p, bn, c, total);
   }
+}
+
+// The sums of this lane's row and COLS columns that are NaN, again over the k blocks [kb, k_hi) by the FP32 pipe.  The
+// warp does it together, some columns at a time; rows and columns outside of C take the last one's values.  It is slow
+// (counted: 1,600 cycles per k and tile of 64 columns, 10,000 per tile of 128, where every row has a NaN), but far inside
+// the waits' limit of 4 s up to some 500,000 of k.
+template <int COLS>
+__device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t row, uint32_t col0, int kb, int k_hi) {
+  constexpr int kAt = COLS == 64 ? 2 : 8;  // what the registers hold beside the sums
+  const uint32_t r = min(row, (uint32_t)p.m - 1);
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += kAt) {
+    float v[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) v[j] = 0.f;
+#pragma unroll 1
+    for (uint32_t k = (uint32_t)kb * kTileK; k < min((uint32_t)k_hi * kTileK, (uint32_t)p.k); ++k) {
+      const float f = p.a[p.a_mn ? k * p.lda + r : r * p.lda + k];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const uint32_t col = min(col0 + c + j, (uint32_t)p.n - 1);
+        v[j] = fmaf(f, p.b[p.b_mn ? k * p.ldb + col : col * p.ldb + k], v[j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)  // register arrays are indexed by constants only
+      if (i / kAt * kAt == c && isnan(sum[i])) sum[i] = v[i % kAt];
+  }
+}
+
+// Whether one of the first `count` of COLS sums is NaN: the largest, by instructions that take three and keep a NaN.
+__device__ __forceinline__ float most(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int COLS>
+__device__ __forceinline__ bool any_nan(const float* sum, int count) {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};  // four at a time, for their latency
+#pragma unroll
+  for (int i = 0; i < COLS; i += 8) {
+    if (i + 8 <= count) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = most(v[j], sum[i + 2 * j], sum[i + 2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (i + j < count) v[j & 3] = most(v[j & 3], v[j & 3], sum[i + j]);
+    }
+  }
+  return isnan(most(most(v[0], v[1], v[2]), v[3], v[3]));
 }
 
 template <int ACT>
@@ -583,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
         if (with_res) ask_residual(t + gridDim.x);
         continue;
       }
+      if (__any_sync(0xffffffffu, row0 + lane < (uint32_t)m && any_nan<kCols>(sum, (int)(n - col0))))  // of what is stored
+        plain_sums<kCols>(p, sum, row0 + lane, col0, k_lo, k_hi);
       if (p.part) {
         const int64_t row = row0 + lane;
         if (row < m) {

@@ -752,3 +752,57 @@ def test_a_wait_that_runs_out_where_warps_write_rows_together(rows, with_r, keep
 @pytest.mark.parametrize("shape", [(40_001, 59, 131), (40_010, 61, 97), (20_031, 73, 257), (39_999, 65, 160), (700, 130, 65)], ids=str)
 def test_unaligned_widths_that_end_inside_a_warps_columns(shape):
     test_linear_with_many_rows(shape, BF16)
+
+
+# a product for every float32 kernel: few rows, tiles of 64 columns and of 128, operands by TMA and by words, whole rows
+# written together, ranges of k
+LIMITS = [(12, 40, 33), (640, 40, 33), (700, 300, 59), (20_000, 128, 200), (40_000, 128, 59), (9000, 270, 35), (200, 4096, 40),
+          (2000, 520, 264)]
+
+
+@pytest.mark.parametrize("shape", LIMITS, ids=str)
+def test_float32_infinities_and_the_largest_values_give_the_definitions(shape):
+    """Sums with an infinity are that infinity (or NaN: against a zero weight or the other infinity), the largest
+    finite values give finite sums, and all other rows keep their bits, whichever kernel takes the call."""
+    rows, n_in, n_out = shape
+    big = torch.finfo(F32).max
+    x, w = _rand((rows, n_in), F32, 1), _rand((n_out, n_in), F32, 2, 0.1)
+    w.clamp_(-0.45, 0.45)  # twice the largest value by a weight stays in range
+    w[1, 3] = 0.0
+    _, clean = dense.linear_fwd(x, w, keep_z=True)
+    bad = x.clone()
+    bad[0, 3], bad[1, 3], bad[2, 3] = math.inf, -math.inf, math.nan
+    bad[3, 3], bad[3, 5] = math.inf, -math.inf
+    bad[4, 3], bad[5, 3], bad[6, 3] = big, -big, 3.4e38
+    bad[7, 3], bad[7, 5] = big, -big
+    bad[rows - 1, n_in - 1] = -big
+    hit = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    hit[:8] = hit[rows - 1] = True
+    _, ey, Z, ez = _linear_tolerances(bad, w, None, None, "none")
+    for act in ("none", "relu"):
+        y, z = dense.linear_fwd(bad, w, act=act, keep_z=True)
+        Y = Z if act == "none" else Z.clamp(min=0)  # (a NaN stays NaN)
+        for got, want, what in ((z, Z, "z"), (y, Y, "y")):
+            finite = torch.isfinite(want)
+            assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+            assert torch.equal(got[~finite & ~torch.isnan(want)].double(), want[~finite & ~torch.isnan(want)]), what
+            _close(got[finite], want[finite], ez[finite], what)
+        assert torch.equal(z[~hit], clean[~hit])
+    alone, _ = dense.linear_fwd(bad, w)  # without z
+    finite = torch.isfinite(Z)
+    assert torch.equal(torch.isnan(alone), torch.isnan(Z))
+    _close(alone[finite], Z[finite], ez[finite], "y alone")
+    # and the gradients
+    dy = _rand((rows, n_out), F32, 3, 1e-3)
+    good = dense.linear_bwd(dy, x, w)
+    dy[0, 1], dy[4, 2], dy[5, 0], dy[rows - 1, n_out - 1] = math.inf, big, -big, math.nan
+    x.clamp_(-0.9, 0.9)
+    want = _linear_grads(dy, x, w, None, "none")
+    for got, (g, e), what in zip(dense.linear_bwd(dy, x, w), (want["dx"], want["dw"], want["db"]), ("dx", "dw", "db")):
+        finite = torch.isfinite(g)
+        assert torch.equal(torch.isnan(got), torch.isnan(g)), what
+        assert torch.equal(got[~finite & ~torch.isnan(g)].double(), g[~finite & ~torch.isnan(g)]), what
+        _close(got[finite], g[finite], e[finite], what)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[[0, 4, 5, rows - 1]] = False
+    assert torch.equal(dense.linear_bwd(dy, x, w)[0][keep], good[0][keep])
