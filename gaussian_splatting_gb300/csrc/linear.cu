@@ -187,17 +187,18 @@ gs_status run_bwd(const gs_linear_desc* d, const void* dy, const void* x, const 
   const int64_t unit = 16 / (int64_t)sizeof(T), pad = copy ? ceil_div(d->out_features, unit) * unit - d->out_features : 0;
   int parts = act_grad_parts<T>(d->rows, d->out_features);
   // (without an activation there is nothing to form, and it is used for the sums' sake alone)
-  const bool fused = (z || dbias) && gs::grad_takes(d, dy, z, w, dx);
+  const bool fused = (z || dbias) && gs::grad_takes(d, dy, z), fused_dx = fused && dx && gs::grad_takes_dx(d, w, dx);
   if (fused) {
     parts = gs::grad_parts(d->rows);
-    if (gs_status s = gs::grad_run(d, dy, z, w, dw ? copy : nullptr, space.lddz, dx, dbias ? bias_part : nullptr, status, st, where))
+    if (gs_status s = gs::grad_run(d, dy, z, w, dw || !fused_dx ? copy : nullptr, space.lddz, fused_dx ? dx : nullptr,
+                                   dbias ? bias_part : nullptr, status, st, where))
       return s;
   } else if (copy || dbias) {
     if (gs_status s = run_act_grad<T>(d, static_cast<const T*>(dy), static_cast<const T*>(z), copy, lddz,
                                       dbias ? bias_part : nullptr, st, where))
       return s;
   }
-  if (dx && !fused) {
+  if (dx && !fused_dx) {
     const gs::MmaProduct q{dz, w, lddz, d->ldw, false, true, d->rows, d->in_features, d->out_features,
                            nullptr, nullptr, dx, nullptr, 0, d->lddx, 0, GS_ACT_NONE, pad};
     if (gs_status s = run_product(q, d->dtype, part, status, st, where)) return s;

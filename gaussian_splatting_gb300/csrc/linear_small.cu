@@ -477,8 +477,9 @@ bool small_bwd_takes(const gs_linear_desc* d) {
   // Thin layers over more rows, for which the tensor-core tiles are nearly empty (2.9M x 9 -> 5: 218 us, 750 by the
   // tensor cores in bfloat16; 225 and 844 in float32); not bfloat16 in 16-byte vectors, which mma_grad.cu passes over
   // faster (3M x 16 -> 16 with GELU: 281 us, 505 here).
-  const bool vectors = d->dtype == GS_BF16 && d->in_features % 8 == 0 && d->out_features % 8 == 0 && d->ldx % 8 == 0 &&
-                       d->ldw % 8 == 0 && d->ldy % 8 == 0 && d->lddx % 8 == 0 && (d->act == GS_ACT_NONE || d->ldz % 8 == 0);
+  // (By what every call reads: which outputs are wanted, and their strides, must not change the sums' order.)
+  const bool vectors = d->dtype == GS_BF16 && d->in_features % 8 == 0 && d->out_features % 8 == 0 && d->ldy % 8 == 0 &&
+                       (d->act == GS_ACT_NONE || d->ldz % 8 == 0);
   return d->in_features <= kThin && d->out_features <= kThin && !vectors;
 }
 size_t small_bwd_workspace(const gs_linear_desc* d) {

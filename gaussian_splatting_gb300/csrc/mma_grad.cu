@@ -280,14 +280,16 @@ namespace gs {
 
 int grad_parts(int64_t rows) { return grid_of(rows); }
 
-bool grad_takes(const gs_linear_desc* d, const void* dy, const void* z, const void* w, const void* dx) {
+bool grad_takes(const gs_linear_desc* d, const void* dy, const void* z) {
   // (32 bits for the bytes from one row to the next keep the addresses at one instruction each)
   auto near = [&](int64_t ld) { return d->rows <= 1 || ld < (int64_t(1) << 31); };
   return d->dtype == GS_BF16 && d->out_features <= kMost && d->in_features <= kMost && d->out_features % 8 == 0 &&
          near(d->ldy) && rows_aligned16(dy, d->rows, d->ldy, GS_BF16) &&
-         (!z || (near(d->ldz) && rows_aligned16(z, d->rows, d->ldz, GS_BF16))) &&
-         (!dx || (tma_takes(w, d->out_features, d->in_features, d->ldw, GS_BF16) &&
-                  tma_takes(dx, d->rows, d->in_features, d->lddx, GS_BF16)));
+         (!z || (near(d->ldz) && rows_aligned16(z, d->rows, d->ldz, GS_BF16)));
+}
+bool grad_takes_dx(const gs_linear_desc* d, const void* w, const void* dx) {
+  return tma_takes(w, d->out_features, d->in_features, d->ldw, GS_BF16) &&
+         tma_takes(dx, d->rows, d->in_features, d->lddx, GS_BF16);
 }
 
 gs_status grad_run(const gs_linear_desc* d, const void* dy, const void* z, const void* w, void* dz, int64_t lddz, void* dx,

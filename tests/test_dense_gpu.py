@@ -806,3 +806,29 @@ def test_float32_infinities_and_the_largest_values_give_the_definitions(shape):
     keep = torch.ones(rows, dtype=torch.bool, device="cuda")
     keep[[0, 4, 5, rows - 1]] = False
     assert torch.equal(dense.linear_bwd(dy, x, w)[0][keep], good[0][keep])
+
+
+# narrow layers whose dx or w TMA cannot move, aligned ones, thin ones, others; dx into rows at odd distances
+ALONE = [(3000, 250, 256), (40_000, 252, 64), (30_000, 20, 40), (5000, 72, 72), (40_000, 8, 16), (40_000, 16, 8), (40_000, 9, 5),
+         (2000, 40, 24), (9000, 300, 264)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", ALONE, ids=str)
+def test_the_bias_gradient_does_not_depend_on_the_other_outputs(shape, dtype):
+    """Columns of dy that add up to almost nothing: another order of the sum would show even in bfloat16."""
+    rows, n_in, n_out = shape
+    half = _rand((rows // 2, n_out), dtype, 1)
+    perm = torch.randperm(rows // 2, generator=torch.Generator().manual_seed(2)).cuda()
+    dy = torch.cat([half, -half[perm]])
+    x, w = _rand((rows, n_in), dtype, 3), _rand((n_out, n_in), dtype, 4, 0.1)
+    strided = torch.zeros((rows, n_in + 1), dtype=dtype, device="cuda")[:, :n_in]
+    for act in ("none", "relu"):
+        z = None if act == "none" else torch.ones_like(dy)  # slope 1
+        dx, dw, db = dense.linear_bwd(dy, x, w, z, act=act)
+        for kw in (dict(need_dx=False), dict(need_dw=False), dict(need_dx=False, need_dw=False), dict(dx=strided)):
+            other = dense.linear_bwd(dy, x, w, z, act=act, **kw)
+            assert torch.equal(other[2], db), (act, kw.keys())
+            assert other[1] is None or torch.equal(other[1], dw)
+            assert "dx" in kw or other[0] is None or torch.equal(other[0], dx)
+        assert torch.equal(strided, dx) or dtype == BF16  # (another kernel: the last bit)
