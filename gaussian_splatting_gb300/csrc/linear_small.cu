@@ -1,11 +1,14 @@
-// The linear layer's small calls, where a launch's latency is the cost: a tensor-core product takes about
-// 11 us from its first instruction to its last whatever its size (tensor maps, TMEM, a pipeline that fills and
-// drains), plain kernels on the FP32 pipe 3 to 5.
+// The linear layer's small calls, where a launch's latency is the cost, on the FP32 pipe.
+//
+// (Forward products of more than 16 rows are all the tensor cores': a kernel on the FP32 pipe for up to 2^26
+// multiply-adds was slower from 32 columns on whatever the rows (float32 chains of dependent layers: 64 x 64 x 64 8.5 us
+// against 7.8, 2,048 x 128 -> 128 16.4 and 10.0; bfloat16 9.0 and 3.2, 17.0 and 3.9), and by more for thin layers of many
+// rows (300K x 64 -> 3 float32 123 and 51 us, 1M x 8 -> 8 394 and 129).  What it was faster at were chains of thin float32
+// layers of up to 4,096 rows, by 1 to 2 of 7 us, and not where the calls are independent.)
 //
 //   few rows (at most 16): a group of lanes per output column reads a weight row once and keeps the rows' sums
 //     in registers (k_few_fwd); columns of the input gradient summed over slices of the outputs (k_few_dx);
 //     the weight gradient as a sum of at most 16 outer products (k_few_dw).  Bound by reading or writing w.
-//   small products (at most 2^26 multiply-adds): a 32 x 64 tile per block, 64 of k at a time (k_small_fwd)
 //   backward of narrow layers (64 x 64 at most) over up to 32,768 rows: dz, its column sums, dx and the
 //     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order; of thin ones (16 x 16)
 //     over any number (k_thin_bwd)
@@ -191,52 +194,8 @@ __global__ void __launch_bounds__(kThreads) k_few_dw(const Bwd<T> p) {
     if (n0 + warp * kPer + j < p.out) IO::store(p.dw + (int64_t)(n0 + warp * kPer + j) * p.lddw + k, acc[j]);
 }
 
-// ---------------------------------------------------------------- small products
-constexpr int kTileR = 32, kTileC = 64, kTileK = 64;
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_small_fwd(const Fwd<T> p) {
-  follow();
-  __shared__ float xs[kTileR][kTileK + 1], ws[kTileC][kTileK + 1];
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;  // columns tx + 16 j, rows ty + 16 i
-  const int64_t r0 = (int64_t)blockIdx.x * kTileR;
-  const int n0 = blockIdx.y * kTileC;
-  float acc[2][4] = {};
-  for (int k0 = 0; k0 < p.in; k0 += kTileK) {
-    const int k = tid % kTileK;
-    const bool ki = k0 + k < p.in;
-    if (k0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kTileR * kTileK / kThreads; ++i) {
-      const int r = tid / kTileK + i * (kThreads / kTileK);
-      xs[r][k] = ki && r0 + r < p.rows ? to_f32<T>(p.x[(r0 + r) * p.ldx + k0 + k]) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kTileC * kTileK / kThreads; ++i) {
-      const int n = tid / kTileK + i * (kThreads / kTileK);
-      ws[n][k] = ki && n0 + n < p.out ? to_f32<T>(p.w[(int64_t)(n0 + n) * p.ldw + k0 + k]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll 8
-    for (int kk = 0; kk < kTileK; ++kk) {
-      float a[2], b[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) a[i] = xs[ty + 16 * i][kk];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = ws[tx + 16 * j][kk];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (r0 + ty + 16 * i < p.rows && n0 + tx + 16 * j < p.out) finish(p, (int)r0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
-}
-
+// ---------------------------------------------------------------- narrow layers
+constexpr int kTileR = 32;
 constexpr int kNarrow = 64;
 
 // parts: [gridDim.x][kNarrow + 1][kNarrow], the bias gradient's in the last row
@@ -387,7 +346,6 @@ __global__ void __launch_bounds__(kThreads) k_small_bwd_fold(const float* parts,
 
 // ---------------------------------------------------------------- host side
 constexpr int kFewRows = 2 * kFew;
-constexpr int64_t kSmallWork = int64_t(1) << 26;  // multiply-adds
 constexpr int kNarrowRows = 32768;
 
 bool vec_ok(const void* p, int64_t rows, int64_t ld, int width, int32_t dtype) {
@@ -406,18 +364,13 @@ gs_status fwd(const gs_linear_desc* d, const void* x, const void* w, const void*
   const Fwd<T> p{(const T*)x, (const T*)w, (const T*)bias, (const T*)residual, (T*)y, (T*)z,
                  d->ldx, d->ldw, d->ldr, d->ldy, d->ldz, (int)d->rows, d->in_features, d->out_features, d->act};
   constexpr int VE = 16 / sizeof(T);
-  if (d->rows <= kFewRows) {
-    const unsigned groups = (unsigned)ceil_div(d->rows, kFew);
-    const bool vec = vec_ok(x, d->rows, d->ldx, d->in_features, d->dtype) &&
-                     vec_ok(w, d->out_features, d->ldw, d->in_features, d->dtype);
-    auto grid = [&](int lanes) { return dim3((unsigned)ceil_div((int64_t)d->out_features * lanes, kThreads), groups); };
-    if (!vec) gs::launch(k_few_fwd<T, 1, 32>, grid(32), kThreads, 0, st, p);
-    else if (d->in_features <= 8 * VE) gs::launch(k_few_fwd<T, VE, 8>, grid(8), kThreads, 0, st, p);
-    else gs::launch(k_few_fwd<T, VE, 32>, grid(32), kThreads, 0, st, p);
-  } else {
-    const dim3 grid((unsigned)ceil_div(d->rows, kTileR), (unsigned)ceil_div(d->out_features, kTileC));
-    gs::launch(k_small_fwd<T>, grid, kThreads, 0, st, p);
-  }
+  const unsigned groups = (unsigned)ceil_div(d->rows, kFew);
+  const bool vec = vec_ok(x, d->rows, d->ldx, d->in_features, d->dtype) &&
+                   vec_ok(w, d->out_features, d->ldw, d->in_features, d->dtype);
+  auto grid = [&](int lanes) { return dim3((unsigned)ceil_div((int64_t)d->out_features * lanes, kThreads), groups); };
+  if (!vec) gs::launch(k_few_fwd<T, 1, 32>, grid(32), kThreads, 0, st, p);
+  else if (d->in_features <= 8 * VE) gs::launch(k_few_fwd<T, VE, 8>, grid(8), kThreads, 0, st, p);
+  else gs::launch(k_few_fwd<T, VE, 32>, grid(32), kThreads, 0, st, p);
   return gs::check_launch(where);
 }
 
@@ -462,8 +415,7 @@ namespace gs {
 
 bool small_fwd_takes(const gs_linear_desc* d) {
   // few rows of a long sum over few columns leave most of the device idle: the split product takes those
-  if (d->rows <= kFewRows) return d->in_features <= 8192;
-  return d->in_features <= 256 && d->rows * d->in_features * d->out_features <= kSmallWork;
+  return d->rows <= kFewRows && d->in_features <= 8192;
 }
 gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
                     void* z, cudaStream_t st, const char* where) {

@@ -832,3 +832,22 @@ def test_the_bias_gradient_does_not_depend_on_the_other_outputs(shape, dtype):
             assert other[1] is None or torch.equal(other[1], dw)
             assert "dx" in kw or other[0] is None or torch.equal(other[0], dx)
         assert torch.equal(strided, dx) or dtype == BF16  # (another kernel: the last bit)
+
+
+# one more row than the few-rows kernels take and up to many, widths of one column to several tiles, thin layers
+SMALL = [(17, 1, 1), (17, 256, 300), (40, 3, 5), (64, 64, 3), (333, 8, 8), (1000, 65, 129), (2048, 128, 128), (5000, 16, 9), (30_000, 64, 3),
+         (100_000, 8, 1), (25, 200, 4100)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", SMALL, ids=str)
+def test_small_forward_products(shape, dtype):
+    rows, n_in, n_out = shape
+    for act, has_r, keep, pad in (("gelu", True, True, 0), ("none", False, False, 5), ("relu", True, False, 8)):
+        x, w = _rand((rows, n_in), dtype, 1, 1.0, pad), _rand((n_out, n_in), dtype, 2, 1 / math.sqrt(n_in), pad)
+        b, r = _rand((n_out,), dtype, 3, 0.3), _rand((rows, n_out), dtype, 4, 1.0, pad) if has_r else None
+        y, z = dense.linear_fwd(x, w, b, r, act=act, keep_z=keep)
+        Y, ey, Z, ez = _linear_tolerances(x, w, b, r, act)
+        _close(y, Y, ey, f"y {act}")
+        if keep:
+            _close(z, Z, ez, f"z {act}")
