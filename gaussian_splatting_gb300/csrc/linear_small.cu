@@ -1,13 +1,8 @@
 // The linear layer's small calls, where a launch's latency is the cost, on the FP32 pipe.
 //
-// (Forward products of more than 16 rows are all the tensor cores': a kernel on the FP32 pipe for up to 2^26
-// multiply-adds was slower from 32 columns on whatever the rows (float32 chains of dependent layers: 64 x 64 x 64 8.5 us
-// against 7.8, 2,048 x 128 -> 128 16.4 and 10.0; bfloat16 9.0 and 3.2, 17.0 and 3.9), and by more for thin layers of many
-// rows (300K x 64 -> 3 float32 123 and 51 us, 1M x 8 -> 8 394 and 129).  What it was faster at were chains of thin float32
-// layers of up to 4,096 rows, by 1 to 2 of 7 us, and not where the calls are independent.)
-//
-//   few rows (at most 16): a group of lanes per output column reads a weight row once and keeps the rows' sums
-//     in registers (k_few_fwd); columns of the input gradient summed over slices of the outputs (k_few_dx);
+//   forward: a group of lanes per output column reads a weight row once and keeps the sums of eight rows in
+//     registers (k_few_fwd); few_takes says for which calls
+//   backward of few rows (at most 16): columns of the input gradient summed over slices of the outputs (k_few_dx);
 //     the weight gradient as a sum of at most 16 outer products (k_few_dw).  Bound by reading or writing w.
 //   backward of narrow layers (64 x 64 at most) over up to 32,768 rows: dz, its column sums, dx and the
 //     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order; of thin ones (16 x 16)
@@ -358,6 +353,28 @@ int small_bwd_grid(const gs_linear_desc* d) {
   return (int)(tiles < most ? tiles : most);
 }
 
+// Whether k_few_fwd takes a forward call, and not the tensor cores.  It takes 2.6 us and 0.24 us for each step of a lane,
+// a vector of w against one of its rows, while no more than four blocks are on an SM (chains of dependent layers: 64 rows
+// of 64 -> 64 float32 5.1, 256 -> 256 6.7, 1024 -> 1024 18.9).  The tensor cores' products take
+//   float32               7 to 9 us, 11 at 4096 inputs: 8.9, 8.8 and 9.2 for the same layers
+//   bfloat16 by TMA       3 to 4 us, 7 from 1024 inputs on (256 -> 256: 16 rows 5.6 here, 4.0 there; 1 row 2.1 and 3.9)
+//   bfloat16, other rows  5.3 us, 8.5 at 255 inputs (9 -> 5: 512 rows 3.8 and 4.9; 60 -> 64 6.4 and 5.4)
+// and where there are more blocks (float32 64 -> 64: 512 rows 6.3 and 9.1, 1,024 rows 10.5 and 9.0) they take the call.
+// Of eight rows at most w is read once, and a float32 product of many columns has fewer blocks on the tensor cores than
+// here (2048 -> 16384: 8 rows 97 and 117, 16 rows 208 and 116; 8192 -> 8192: 1 row 75 and 95, 4 rows 200 and 95).
+bool few_takes(const gs_linear_desc* d) {
+  const int ve = 16 / (int)gs::dtype_size(d->dtype);
+  auto whole = [&](int64_t rows, int64_t ld) { return rows <= 1 || ld % ve == 0; };
+  const bool vec = d->in_features % ve == 0 && whole(d->rows, d->ldx) && whole(d->out_features, d->ldw);
+  const bool tma = vec && d->out_features % ve == 0 && whole(d->rows, d->ldy);
+  const int lanes = vec && d->in_features <= 8 * ve ? 8 : 32;
+  const int64_t groups = ceil_div(d->rows, kFew), blocks = groups * ceil_div((int64_t)d->out_features * lanes, kThreads);
+  const int64_t steps = (d->rows < kFew ? d->rows : kFew) * ceil_div(d->in_features, lanes * (vec ? ve : 1));
+  if (d->dtype == GS_F32 && groups == 1 && d->out_features >= 8192) return steps <= 128;
+  const int64_t most = d->dtype == GS_F32 ? 16 + d->in_features / 256 : tma ? 4 + d->in_features / 256 : 8 + d->in_features / 32;
+  return d->in_features <= 4096 && steps <= most && blocks <= 4 * 152;
+}
+
 template <typename T>
 gs_status fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y, void* z,
               cudaStream_t st, const char* where) {
@@ -414,8 +431,7 @@ gs_status bwd(const gs_linear_desc* d, const void* dy, const void* x, const void
 namespace gs {
 
 bool small_fwd_takes(const gs_linear_desc* d) {
-  // few rows of a long sum over few columns leave most of the device idle: the split product takes those
-  return d->rows <= kFewRows && d->in_features <= 8192;
+  return few_takes(d);
 }
 gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
                     void* z, cudaStream_t st, const char* where) {

@@ -851,3 +851,15 @@ def test_small_forward_products(shape, dtype):
         _close(y, Y, ey, f"y {act}")
         if keep:
             _close(z, Z, ez, f"z {act}")
+
+
+# calls at either side of the forward's choice of a kernel: rows, inputs, columns and blocks that just fit, and do not
+EDGES = [(1, 4096, 33), (1, 4104, 33), (1, 8192, 70), (2, 1024, 64), (3, 1024, 64), (8, 256, 300), (8, 520, 40), (128, 256, 256), (136, 256, 256),
+         (512, 64, 64), (520, 64, 64), (1024, 32, 128), (4, 255, 257), (512, 9, 5), (4900, 9, 5), (8, 2048, 8200), (9, 2048, 8200),
+         (64, 60, 64), (16, 8, 16), (16, 1024, 1024), (5, 4096, 4096)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", EDGES, ids=str)
+def test_forward_products_of_few_rows(shape, dtype):
+    test_small_forward_products(shape, dtype)
