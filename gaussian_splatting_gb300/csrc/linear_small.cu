@@ -375,6 +375,17 @@ bool few_takes(const gs_linear_desc* d) {
   return d->in_features <= 4096 && steps <= most && blocks <= 4 * 152;
 }
 
+// Whether a backward of at most 16 rows is the plain kernels', of which k_few_dx walks over all outputs for eight rows at a
+// time, and not the tensor cores' (alone, 16 rows; float32 256 -> 256 13 us here, 21 there; 1024 -> 1024 21 and 23; 4096 ->
+// 1024 39 and 31, of 8 rows 25 and 31; 1024 -> 4096 56 and 30, of 1 row 27 and 30; 8192 -> 64 25 and 19, of 8 rows 17 and
+// 19; bfloat16 256 -> 256 14 and 19; 1024 -> 1024 23 and 19, of 4 rows 17 and 17; 1024 -> 4096 58 and 20, of 1 row 29 and 19;
+// 8192 -> 64 22 and 14, of 1 row 13 and 15).
+bool few_bwd_takes(const gs_linear_desc* d) {
+  const int64_t across = d->rows * d->in_features, deep = d->rows * d->out_features;
+  if (d->dtype == GS_F32) return deep <= 8192 && (d->rows <= kFew || d->in_features <= 4096);
+  return deep <= 4096 && d->out_features <= 2048 && across <= 16384;
+}
+
 template <typename T>
 gs_status fwd(const gs_linear_desc* d, const void* x, const void* w, const void* bias, const void* residual, void* y, void* z,
               cudaStream_t st, const char* where) {
@@ -440,7 +451,7 @@ gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const
 }
 
 bool small_bwd_takes(const gs_linear_desc* d) {
-  if (d->rows <= kFewRows) return d->out_features <= 8192;
+  if (d->rows <= kFewRows) return few_bwd_takes(d);
   if (d->rows <= kNarrowRows) return d->in_features <= kNarrow && d->out_features <= kNarrow;
   // Thin layers over more rows, for which the tensor-core tiles are nearly empty (2.9M x 9 -> 5: 218 us, 750 by the
   // tensor cores in bfloat16; 225 and 844 in float32); not bfloat16 in 16-byte vectors, which mma_grad.cu passes over

@@ -863,3 +863,25 @@ EDGES = [(1, 4096, 33), (1, 4104, 33), (1, 8192, 70), (2, 1024, 64), (3, 1024, 6
 @pytest.mark.parametrize("shape", EDGES, ids=str)
 def test_forward_products_of_few_rows(shape, dtype):
     test_small_forward_products(shape, dtype)
+
+
+# backwards of few rows at either side of their choice of kernels
+FEW_BACK = [(1, 4096, 4096), (2, 1000, 4100), (8, 4100, 1030), (16, 520, 512), (16, 256, 256), (16, 264, 264), (9, 4096, 900), (4, 1024, 1024),
+            (5, 2000, 1024), (1, 8200, 2048), (2, 8200, 64), (16, 1024, 8), (16, 1032, 8), (1, 16400, 40), (1, 64, 8200), (3, 255, 1400)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", FEW_BACK, ids=str)
+def test_backwards_of_few_rows(shape, dtype):
+    rows, n_in, n_out = shape
+    for act, pad in (("none", 0), ("gelu", 8), ("silu", 3)):
+        dy, x = _rand((rows, n_out), dtype, 5, 1e-3, pad), _rand((rows, n_in), dtype, 6, 1.0, pad)
+        w = _rand((n_out, n_in), dtype, 7, 1 / math.sqrt(n_in), pad)
+        z = None if act == "none" else _rand((rows, n_out), dtype, 8, 1.0, pad)
+        full = dense.linear_bwd(dy, x, w, z, act=act)
+        want = _linear_grads(dy, x, w, z, act)
+        for k, v in zip(("dx", "dw", "db"), full):
+            _close(v, *want[k], f"{k} {act}")
+        for kw, kept in ((dict(need_dx=False), (1, 2)), (dict(need_dw=False), (0, 2)), (dict(bias=False), (0, 1))):
+            part = dense.linear_bwd(dy, x, w, z, act=act, **kw)
+            assert all(torch.equal(part[i], full[i]) for i in kept)
