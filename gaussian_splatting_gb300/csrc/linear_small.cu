@@ -4,9 +4,9 @@
 //     registers (k_few_fwd); few_takes says for which calls
 //   backward of few rows (at most 16): columns of the input gradient summed over slices of the outputs (k_few_dx);
 //     the weight gradient as a sum of at most 16 outer products (k_few_dw).  Bound by reading or writing w.
-//   backward of narrow layers (64 x 64 at most) over up to 32,768 rows: dz, its column sums, dx and the
+//   backward of narrow layers (64 x 64 at most) over up to 4,864 rows: dz, its column sums, dx and the
 //     block's part of dw from one read of dy, z and x (k_small_bwd), then the parts in order; of thin ones (16 x 16)
-//     over any number (k_thin_bwd)
+//     over any number beyond (k_thin_bwd)
 // All sums in 32 bits in a fixed order.
 #include "small.cuh"
 
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) k_small_bwd_fold(const float* parts,
 
 // ---------------------------------------------------------------- host side
 constexpr int kFewRows = 2 * kFew;
-constexpr int kNarrowRows = 32768;
+constexpr int kNarrowRows = 152 * kTileR;  // one tile of k_small_bwd per block
 
 bool vec_ok(const void* p, int64_t rows, int64_t ld, int width, int32_t dtype) {
   return width % (16 / (int)gs::dtype_size(dtype)) == 0 && gs::rows_aligned16(p, rows, ld, dtype);
@@ -452,14 +452,18 @@ gs_status small_fwd(const gs_linear_desc* d, const void* x, const void* w, const
 
 bool small_bwd_takes(const gs_linear_desc* d) {
   if (d->rows <= kFewRows) return few_bwd_takes(d);
-  if (d->rows <= kNarrowRows) return d->in_features <= kNarrow && d->out_features <= kNarrow;
-  // Thin layers over more rows, for which the tensor-core tiles are nearly empty (2.9M x 9 -> 5: 218 us, 750 by the
-  // tensor cores in bfloat16; 225 and 844 in float32); not bfloat16 in 16-byte vectors, which mma_grad.cu passes over
-  // faster (3M x 16 -> 16 with GELU: 281 us, 505 here).
   // (By what every call reads: which outputs are wanted, and their strides, must not change the sums' order.)
   const bool vectors = d->dtype == GS_BF16 && d->in_features % 8 == 0 && d->out_features % 8 == 0 && d->ldy % 8 == 0 &&
                        (d->act == GS_ACT_NONE || d->ldz % 8 == 0);
-  return d->in_features <= kThin && d->out_features <= kThin && !vectors;
+  // A round of tiles takes k_small_bwd 9 to 11 us whatever the layer; two rounds take as long as the tensor cores (64 -> 64
+  // float32: 4,096 rows 11.5 us here, 17.8 there; 8,192 rows 19.4 and 19.0; 32,768 rows 88 and 28), but for bfloat16
+  // layers of 16-byte vectors, which mma_grad.cu passes over as fast from the start (64 -> 64: 512 rows 11.2 and 10.0;
+  // 2,048 rows 10.9 and 11.5; 4,096 rows 12.2 and 10.8).
+  if (d->rows <= kNarrowRows) return d->in_features <= kNarrow && d->out_features <= kNarrow && !vectors;
+  // Thin layers over more rows, for which the tensor cores' tiles are nearly empty (GELU, 3M rows: 9 -> 5 bfloat16 254 us
+  // here, 808 there; float32 8 -> 8 292 and 709, 16 -> 16 516 and 734; from 8,192 rows on: 16 -> 16 14.9 and 16.3); of the
+  // vectors of bfloat16 only the narrowest (8 -> 8 285 and 335; 8 -> 16 444 and 332; 16 -> 16 506 and 279).
+  return d->in_features <= kThin && d->out_features <= kThin && !(vectors && d->in_features * d->out_features > 64);
 }
 size_t small_bwd_workspace(const gs_linear_desc* d) {
   return d->rows <= kFewRows ? 0 : (size_t)small_bwd_grid(d) * (kNarrow + 1) * kNarrow * sizeof(float);

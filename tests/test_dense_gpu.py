@@ -885,3 +885,15 @@ def test_backwards_of_few_rows(shape, dtype):
         for kw, kept in ((dict(need_dx=False), (1, 2)), (dict(need_dw=False), (0, 2)), (dict(bias=False), (0, 1))):
             part = dense.linear_bwd(dy, x, w, z, act=act, **kw)
             assert all(torch.equal(part[i], full[i]) for i in kept)
+
+
+# narrow backwards at either side of their choice of kernels: the last row of one round of tiles and the next, the widest
+# thin layers, one wider
+NARROW_BACK = [(17, 16, 16), (4864, 64, 64), (4865, 64, 64), (4865, 16, 16), (4864, 9, 5), (4865, 9, 5), (32_000, 16, 16), (40_000, 8, 8),
+               (9000, 3, 16), (9000, 17, 16), (9000, 16, 17), (6000, 64, 3), (5000, 1, 1)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", NARROW_BACK, ids=str)
+def test_narrow_backwards_at_the_limits_of_their_kernels(shape, dtype):
+    test_linear_small_calls(shape, dtype)
