@@ -14,6 +14,10 @@ backward, and the base record is the last layer's residual, read and written in 
 layout (a plane of [N][4] floats, of which the head may own three).  The parameters are one float32 buffer laid
 out as 60-float records, so that gs_sparse_adam updates them.
 
+Every linear layer is given the head's status record, which ``step`` hands to gs_sparse_adam: after a device-side
+wait that gave up the update skips itself, as the trainer's does after a view that overflowed, and goes on skipping
+until ``ok`` has been asked.
+
 ``python -m gaussian_splatting_gb300.head`` trains a head on the smallest scene: the base colours are set grey
 and the head learns to restore them from the images.
 """
@@ -57,6 +61,9 @@ class AttributeHead:
         self.all = torch.arange(self.records, dtype=torch.int32, device=dev)
         self.n_all = torch.full((1,), self.records, dtype=torch.int64, device=dev)
         self.t = 0
+        # a record as gs_bin_sort's counts (count, status): the layers set the low word of the second entry
+        self.status = torch.zeros((1, 2), dtype=torch.int64, device=dev)
+        self._status_word = self.status.view(torch.int32)[0, 2:3]
         gen = torch.Generator(device=dev)
         gen.manual_seed(seed)
         for name, shape in shapes.items():
@@ -69,16 +76,16 @@ class AttributeHead:
     def forward(self, features: torch.Tensor, base: torch.Tensor, out: torch.Tensor | None = None, train: bool = True):
         """base + corrections, into ``out`` (which may be a strided view of a record plane, or ``base`` itself).
         ``train`` keeps what ``backward`` reads."""
-        p, kept = self.p, []
-        h, _ = dense.linear_fwd(features, p["w_in"], p["b_in"])
+        p, kept, st = self.p, [], self._status_word
+        h, _ = dense.linear_fwd(features, p["w_in"], p["b_in"], status=st)
         for k in range(self.blocks):
             n, mean, rstd = dense.layernorm_fwd(h, p[f"g{k}"], p[f"s{k}"], self.eps, stats=train)
-            a, z = dense.linear_fwd(n, p[f"w1_{k}"], p[f"b1_{k}"], act="gelu", keep_z=train)
-            after, _ = dense.linear_fwd(a, p[f"w2_{k}"], p[f"b2_{k}"], residual=h, out=None if train else h)
+            a, z = dense.linear_fwd(n, p[f"w1_{k}"], p[f"b1_{k}"], act="gelu", keep_z=train, status=st)
+            after, _ = dense.linear_fwd(a, p[f"w2_{k}"], p[f"b2_{k}"], residual=h, out=None if train else h, status=st)
             kept.append((h, mean, rstd, n, z, a))
             h = after
         n, mean, rstd = dense.layernorm_fwd(h, p["g_out"], p["s_out"], self.eps, stats=train)
-        y, _ = dense.linear_fwd(n, p["w_out"], p["b_out"], residual=base, out=out)
+        y, _ = dense.linear_fwd(n, p["w_out"], p["b_out"], residual=base, out=out, status=st)
         self.kept = (features, kept, (h, mean, rstd, n)) if train else None
         return y
 
@@ -87,24 +94,33 @@ class AttributeHead:
         the features' gradient if asked for.  The base's gradient is dy itself."""
         if self.kept is None:
             raise RuntimeError("backward needs a forward with train=True before it")
-        p, g = self.p, self.g
+        p, g, st = self.p, self.g, self._status_word
         features, kept, (h, mean, rstd, n) = self.kept
         self.kept = None
-        dn, _, _ = dense.linear_bwd(dy, n, p["w_out"], dw=g["w_out"], dbias=g["b_out"])
+        dn, _, _ = dense.linear_bwd(dy, n, p["w_out"], dw=g["w_out"], dbias=g["b_out"], status=st)
         dh, _, _ = dense.layernorm_bwd(dn, h, p["g_out"], mean, rstd, dgamma=g["g_out"], dbeta=g["s_out"])
         for k in reversed(range(self.blocks)):
             h, mean, rstd, n, z, a = kept[k]
-            da, _, _ = dense.linear_bwd(dh, a, p[f"w2_{k}"], dw=g[f"w2_{k}"], dbias=g[f"b2_{k}"])
-            dn, _, _ = dense.linear_bwd(da, n, p[f"w1_{k}"], z, act="gelu", dw=g[f"w1_{k}"], dbias=g[f"b1_{k}"])
+            da, _, _ = dense.linear_bwd(dh, a, p[f"w2_{k}"], dw=g[f"w2_{k}"], dbias=g[f"b2_{k}"], status=st)
+            dn, _, _ = dense.linear_bwd(da, n, p[f"w1_{k}"], z, act="gelu", dw=g[f"w1_{k}"], dbias=g[f"b1_{k}"], status=st)
             dh, _, _ = dense.layernorm_bwd(dn, h, p[f"g{k}"], mean, rstd, skip=dh, dx=dn, dgamma=g[f"g{k}"], dbeta=g[f"s{k}"])
-        df, _, _ = dense.linear_bwd(dh, features, p["w_in"], dw=g["w_in"], dbias=g["b_in"], need_dx=need_dfeatures)
+        df, _, _ = dense.linear_bwd(dh, features, p["w_in"], dw=g["w_in"], dbias=g["b_in"], need_dx=need_dfeatures, status=st)
         return df
 
-    def step(self, lr: float, betas=(0.9, 0.999), eps: float = 1e-8):
-        """Adam on all parameters (gs_sparse_adam with every record listed); the gradients are zero afterwards."""
+    def step(self, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, counts: torch.Tensor | None = None):
+        """Adam on all parameters (gs_sparse_adam with every record listed); the gradients are zero afterwards.
+        Leaves everything as it is where a layer's wait gave up, or where one of ``counts``, the status records of the
+        trainer's step that the gradient came from (``StepResult.status``), is set."""
         self.t += 1
+        records = self.status if counts is None else torch.cat([self.status, counts])
         N.gs_sparse_adam(self.flat, self.flat_grad, self.exp_avg, self.exp_avg_sq, self.records, self.all, self.n_all,
-                         self.records, lr, betas[0], betas[1], eps, 1, self.t)
+                         self.records, lr, betas[0], betas[1], eps, 1, self.t, records, records.shape[0])
+
+    def ok(self) -> bool:
+        """Whether no layer's wait has given up since the last time this was asked (synchronises)."""
+        set_ = bool(self.status[0, 1].item())
+        self.status.zero_()
+        return not set_
 
 
 def train_colours(steps: int = 60, lr: float = 3e-3, hidden: int = 64, seed: int = 0, report=None):
@@ -130,10 +146,12 @@ def train_colours(steps: int = 60, lr: float = 3e-3, hidden: int = 64, seed: int
         trainer.grads.zero_()
         result = trainer.step_async([cam], target, adam=False)
         head.backward(trainer.grads[3, :, :3])
-        head.step(lr)
+        head.step(lr, counts=result.status)
         losses.append(result.loss.clone())
         if report and k % 10 == 0:
             report(f"step {k}: loss {losses[-1].item():.5f}")
+    if not head.ok():
+        raise RuntimeError("a device-side wait of the head's layers gave up")
     return [float(v.item()) for v in losses]
 
 

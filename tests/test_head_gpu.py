@@ -87,3 +87,59 @@ def test_example_learns_the_colours():
     losses = train_colours(steps=60)
     assert all(math.isfinite(v) for v in losses)
     assert losses[-1] < 0.5 * losses[0], losses[::10]
+
+
+def _trained_step(head, features, base, dy, lr=1e-2):
+    head.forward(features, base)
+    head.backward(dy)
+    head.step(lr)
+
+
+@pytest.mark.parametrize("when", ["forward", "backward"])
+def test_a_wait_that_gives_up_leaves_the_parameters(when):
+    """A layer whose operands never arrive (the library's test hook): the head's record is set, the update and all
+    after it are skipped on the device until the head has been asked, and then go on."""
+    from gaussian_splatting_gb300 import _native as N
+    head = AttributeHead(24, 96, 3, blocks=1, seed=2)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    features, base = (torch.randn((20_000, n), generator=gen, device="cuda") for n in (24, 3))
+    dy = torch.randn((20_000, 3), generator=gen, device="cuda") * 1e-3
+    _trained_step(head, features, base, dy)
+    assert head.ok()
+    before = [t.clone() for t in (head.flat, head.exp_avg, head.exp_avg_sq)]
+    lib = N.load()
+    try:
+        lib.gs_debug_set_wait_limit(2000)
+        if when == "forward":
+            lib.gs_debug_drop_publish(3)
+        head.forward(features, base)
+        if when == "backward":
+            lib.gs_debug_drop_publish(3)
+        head.backward(dy)
+        torch.cuda.synchronize()
+    finally:
+        lib.gs_debug_set_wait_limit(0)
+        lib.gs_debug_drop_publish(0)
+    head.step(1e-2)
+    assert head.status[0, 1].item() == 2
+    _trained_step(head, features, base, dy)  # skipped too: nobody has asked
+    for a, b in zip(before, (head.flat, head.exp_avg, head.exp_avg_sq)):
+        assert torch.equal(a, b)
+    assert not head.ok() and head.ok()
+    _trained_step(head, features, base, dy)
+    assert head.ok() and torch.isfinite(head.flat).all() and not torch.equal(before[0], head.flat)
+
+
+def test_a_step_of_a_batch_that_overflowed_leaves_the_parameters():
+    head = AttributeHead(5, 16, 3, blocks=1, seed=1)
+    before = head.flat.clone()
+    for v in head.g.values():
+        v.fill_(0.5)
+    counts = torch.zeros((4, 2), dtype=torch.int64, device="cuda")
+    counts[2, 1] = 1
+    head.step(1e-2, counts=counts)
+    assert torch.equal(before, head.flat)
+    counts.zero_()
+    head.step(1e-2, counts=counts)
+    assert not torch.equal(before, head.flat) and head.ok()
