@@ -30,6 +30,13 @@ def _load():
     return _binding
 
 
+def _act(act):
+    try:
+        return _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}") from None
+
+
 def _handle(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
@@ -47,7 +54,7 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", keep_z=False, out=Non
     """``(y, z)``: y = act(x w^T + bias) + residual, and z the sum before the activation (None unless
     ``keep_z`` or ``z`` asks for it).  x [rows, in], w [out, in], bias [out], residual [rows, out].
     ``out`` / ``z`` receive the results when given; ``out`` may be ``residual``."""
-    return (_binding or _load()).linear_fwd(x, w, bias, residual, _ACTS[act], keep_z, out, z, status, _handle(stream))
+    return (_binding or _load()).linear_fwd(x, w, bias, residual, _act(act), keep_z, out, z, status, _handle(stream))
 
 
 def linear_bwd(dy, x, w, z=None, act="none", bias=True, dx=None, dw=None, dbias=None, need_dx=True, need_dw=True,
@@ -56,7 +63,7 @@ def linear_bwd(dy, x, w, z=None, act="none", bias=True, dx=None, dw=None, dbias=
     itself).  z is the forward's (``keep_z``), not needed with act "none".  ``bias=False``,
     ``need_dx=False`` and ``need_dw=False`` leave that output out (None).  ``dx`` / ``dw`` / ``dbias``
     receive the results (overwritten) when given."""
-    return (_binding or _load()).linear_bwd(dy, x, w, z, _ACTS[act], bias, dx, dw, dbias, need_dx, need_dw, status,
+    return (_binding or _load()).linear_bwd(dy, x, w, z, _act(act), bias, dx, dw, dbias, need_dx, need_dw, status,
                                             _handle(stream))
 
 

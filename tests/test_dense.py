@@ -164,3 +164,12 @@ def test_tensor_functions_refuse_what_the_library_cannot_take(lib):
     for bad in (torch.zeros(7), torch.zeros(1, 8), torch.zeros(16)[::2], torch.zeros(8).bfloat16()):
         with pytest.raises(ValueError):
             dense._vector(bad, "a", 8, like)
+
+
+@pytest.mark.parametrize("act", ["tanh", "", None, 2, ["relu"]])
+def test_tensor_functions_refuse_an_activation_that_there_is_not(lib, act):
+    x, w = torch.zeros(4, 8), torch.zeros(6, 8)
+    with pytest.raises(ValueError, match="act must be one of none, relu, gelu, silu"):
+        dense.linear_fwd(x, w, act=act)
+    with pytest.raises(ValueError, match="act must be one of"):
+        dense.linear_bwd(torch.zeros(4, 6), x, w, act=act)
