@@ -82,7 +82,8 @@ class AttributeHead:
             n, mean, rstd = dense.layernorm_fwd(h, p[f"g{k}"], p[f"s{k}"], self.eps, stats=train)
             a, z = dense.linear_fwd(n, p[f"w1_{k}"], p[f"b1_{k}"], act="gelu", keep_z=train, status=st)
             after, _ = dense.linear_fwd(a, p[f"w2_{k}"], p[f"b2_{k}"], residual=h, out=None if train else h, status=st)
-            kept.append((h, mean, rstd, n, z, a))
+            if train:
+                kept.append((h, mean, rstd, n, z, a))
             h = after
         n, mean, rstd = dense.layernorm_fwd(h, p["g_out"], p["s_out"], self.eps, stats=train)
         y, _ = dense.linear_fwd(n, p["w_out"], p["b_out"], residual=base, out=out, status=st)

@@ -143,3 +143,20 @@ def test_a_step_of_a_batch_that_overflowed_leaves_the_parameters():
     counts.zero_()
     head.step(1e-2, counts=counts)
     assert not torch.equal(before, head.flat) and head.ok()
+
+
+def test_a_forward_without_training_keeps_no_block():
+    """Its memory does not grow with the number of blocks."""
+    features, base = torch.randn((100_000, 16), device="cuda"), torch.randn((100_000, 3), device="cuda")
+    peaks = []
+    for blocks in (2, 8):
+        head = AttributeHead(16, 64, 3, blocks=blocks)
+        head.forward(features, base, train=False)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        start = torch.cuda.memory_allocated()
+        head.forward(features, base, train=False)
+        torch.cuda.synchronize()
+        peaks.append(torch.cuda.max_memory_allocated() - start)
+    assert peaks[1] <= peaks[0], peaks
+    assert peaks[0] <= 4 * 100_000 * 64 * 4  # h, its norm, the activations and the output
