@@ -231,13 +231,16 @@ __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int to
 }
 
 // The sums of this lane's row and COLS columns that are NaN, again over the k blocks [kb, k_hi) by the FP32 pipe.  The
-// warp does it together, some columns at a time; rows and columns outside of C take the last one's values.  It is slow
-// (counted: 1,600 cycles per k and tile of 64 columns, 10,000 per tile of 128, where every row has a NaN), but far inside
-// the waits' limit of 4 s up to some 500,000 of k.
+// warp does it together, eight columns at a time; rows and columns outside of C take the last one's values.  It is slow
+// (counted: 1,600 cycles per k and tile of 64 columns, 3,200 per tile of 128, where every row has a NaN), but inside the
+// waits' limit of 4 s up to a million of k.
 template <int COLS>
 __device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t row, uint32_t col0, int kb, int k_hi) {
-  constexpr int kAt = COLS == 64 ? 2 : 8;  // what the registers hold beside the sums
+  constexpr int kAt = 8;
   const uint32_t r = min(row, (uint32_t)p.m - 1);
+  float all[COLS];  // indexed by a variable, so in memory: its registers are the loop's
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) all[i] = sum[i];
 #pragma unroll 1
   for (int c = 0; c < COLS; c += kAt) {
     float v[kAt];
@@ -253,9 +256,11 @@ __device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t r
       }
     }
 #pragma unroll
-    for (int i = 0; i < COLS; ++i)  // register arrays are indexed by constants only
-      if (i / kAt * kAt == c && isnan(sum[i])) sum[i] = v[i % kAt];
+    for (int j = 0; j < kAt; ++j)
+      if (isnan(all[c + j])) all[c + j] = v[j];
   }
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) sum[i] = all[i];
 }
 
 // Whether one of the first `count` of COLS sums is NaN: the largest, by instructions that take three and keep a NaN.
@@ -290,8 +295,7 @@ __device__ __forceinline__ void activate(float* v) {
 // GROUPS: the splitters work as one or two teams that take the pieces in turn.  Two hide a team's latency
 // behind the other's, but each wants two raw buffers of its own.
 // DENSE: some array of the epilogue takes whole rows (tiles of 64 columns only).  A kernel of its own, so that the others
-// do without the barriers between its warps (300K x 256 -> 256 with GELU and z: 448 us, 463 in one kernel; the 59-column
-// record 57.7 and 58.9).
+// do without the barriers between its warps (the 59-column record with residual 57.6 us, 60.5 by one kernel for all).
 template <int BN, int GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__ Args p) {
   constexpr int TEAM = kSplitters / GROUPS;
@@ -726,8 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__
             if (p.r_way == kPlain) {
               asm volatile("cp.async.wait_all;" ::: "memory");
               __syncwarp();
+              int l = lane;  // not to be known: the 32 addresses would be kept from tile to tile, on the stack
+              asm volatile("" : "+r"(l));
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += b[lane * 32 + (i ^ lane)];
+              for (int i = 0; i < 32; ++i) v[i] += b[l * 32 + (i ^ l)];
             } else {
               if (DENSE || col0 < (uint32_t)n) {
                 ok = tc::mbar_wait_warp(res_bar, (uint32_t)(res_used & 1), g);
