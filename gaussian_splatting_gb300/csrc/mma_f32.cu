@@ -14,7 +14,7 @@
 // A value whose first part is not finite (infinities, NaN, and from 2^128 - 2^119 on, which rounds to infinity) has no
 // such parts: what the first leaves is inf - inf, and its sums come out as NaN.  A sum that is NaN is therefore taken
 // once more on the FP32 pipe (plain_sums), from the values themselves: an infinity stays one, the largest values give
-// what they should, and a true NaN stays.  The test for it costs half an instruction per sum of a tile.
+// what they should, and a true NaN stays.  The test for it costs 2 to 6 % of a product of few inputs.
 //
 // One persistent block per SM; its warps:
 //   warp 17       copies pieces of 32 of k of A and B, float32 as they are, to a ring of raw buffers by TMA
@@ -263,27 +263,27 @@ __device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t r
   for (int i = 0; i < COLS; ++i) sum[i] = all[i];
 }
 
-// Whether one of the first `count` of COLS sums is NaN: the largest, by instructions that take three and keep a NaN.
-__device__ __forceinline__ float most(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
+// Whether one of the first `count` of COLS sums is NaN, or two are infinities of either sign: the sum of all is NaN.  Two at
+// a time, on the pipe that the splitters leave alone (106,489 x 8 -> 848 input gradient, whose tiles are all epilogue: 13 us
+// of 207; 17 by largest values of three, 28 by comparisons).
 template <int COLS>
 __device__ __forceinline__ bool any_nan(const float* sum, int count) {
-  float v[4] = {0.f, 0.f, 0.f, 0.f};  // four at a time, for their latency
+  float r;
+  if (count >= COLS) {
+    F2 v[2] = {F2(0.f), F2(0.f)};
 #pragma unroll
-  for (int i = 0; i < COLS; i += 8) {
-    if (i + 8 <= count) {
+    for (int i = 0; i < COLS; i += 4) v[0] = add2(v[0], F2(sum[i], sum[i + 1])), v[1] = add2(v[1], F2(sum[i + 2], sum[i + 3]));
+    float a, b;
+    add2(v[0], v[1]).get(a, b);
+    r = a + b;
+  } else {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = most(v[j], sum[i + 2 * j], sum[i + 2 * j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (i + j < count) v[j & 3] = most(v[j & 3], v[j & 3], sum[i + j]);
-    }
+    for (int i = 0; i < COLS - 1; ++i)
+      if (i < count) v[i & 3] += sum[i];
+    r = (v[0] + v[1]) + (v[2] + v[3]);
   }
-  return isnan(most(most(v[0], v[1], v[2]), v[3], v[3]));
+  return isnan(r);
 }
 
 template <int ACT>
@@ -294,7 +294,7 @@ __device__ __forceinline__ void activate(float* v) {
 
 // GROUPS: the splitters work as one or two teams that take the pieces in turn.  Two hide a team's latency
 // behind the other's, but each wants two raw buffers of its own.
-// DENSE: some array of the epilogue takes whole rows (tiles of 64 columns only).  A kernel of its own, so that the others
+// DENSE: arrays of the epilogue may take whole rows (tiles of 64 columns only).  A kernel of its own, so that the others
 // do without the barriers between its warps (the 59-column record with residual 57.6 us, 60.5 by one kernel for all).
 template <int BN, int GROUPS, bool DENSE>
 __global__ void __launch_bounds__(kThreads, 1) k_mma_f32(const __grid_constant__ Args p) {
@@ -860,7 +860,10 @@ gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where
   } else {
     r = room_of(pl, false, bufs);
   }
-  const bool dense = !p.part && (p.y_way == kDense || p.z_way == kDense || p.r_way == kDense);
+  // A weight gradient's ranges of k, which write no array, follow an input gradient that is dense if they are as odd: by
+  // the same kernel, whose instructions are at hand (575 x 7 -> 214 backward 24.2 us, 28.3 by two kernels; 151,069 x 10 -> 67
+  // 79 and 85).
+  const bool dense = p.part ? p.m % 4 != 0 || p.n % 4 != 0 : p.y_way == kDense || p.z_way == kDense || p.r_way == kDense;
   if (pl.bn == 128) return launch<128, 1, false>(p, r, grid, st, where);
   if (dense) return r.raws >= 4 ? launch<64, 2, true>(p, r, grid, st, where) : launch<64, 1, true>(p, r, grid, st, where);
   return r.raws >= 4 ? launch<64, 2, false>(p, r, grid, st, where) : launch<64, 1, false>(p, r, grid, st, where);
