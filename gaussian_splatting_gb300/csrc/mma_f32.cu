@@ -848,7 +848,8 @@ gs_status launch(Args& p, const Room& r, int grid, cudaStream_t st, const char* 
   return e == cudaSuccess ? GS_OK : gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where) {
+// (cols: of the rows that are written, in the end)
+gs_status launch_any(Args& p, const Plan& pl, int64_t cols, cudaStream_t st, const char* where) {
   const int total = pl.m_tiles * pl.n_tiles * pl.splits;
   int grid = total < gs::num_sms() ? total : gs::num_sms();
   const int bufs = p.part ? 0 : 1 + (p.residual != nullptr) + (p.z != nullptr);
@@ -860,10 +861,10 @@ gs_status launch_any(Args& p, const Plan& pl, cudaStream_t st, const char* where
   } else {
     r = room_of(pl, false, bufs);
   }
-  // A weight gradient's ranges of k, which write no array, follow an input gradient that is dense if they are as odd: by
-  // the same kernel, whose instructions are at hand (575 x 7 -> 214 backward 24.2 us, 28.3 by two kernels; 151,069 x 10 -> 67
-  // 79 and 85).
-  const bool dense = p.part ? p.m % 4 != 0 || p.n % 4 != 0 : p.y_way == kDense || p.z_way == kDense || p.r_way == kDense;
+  // Ranges of k write no array, and take the kernel that the other product of a backward takes, whose instructions are at
+  // hand: both write rows of as many columns (575 x 7 -> 214 backward 24.2 us, 28.3 by two kernels; 151,069 x 10 -> 67 79
+  // and 85).
+  const bool dense = p.part ? cols % 4 != 0 && cols <= 64 : p.y_way == kDense || p.z_way == kDense || p.r_way == kDense;
   if (pl.bn == 128) return launch<128, 1, false>(p, r, grid, st, where);
   if (dense) return r.raws >= 4 ? launch<64, 2, true>(p, r, grid, st, where) : launch<64, 1, true>(p, r, grid, st, where);
   return r.raws >= 4 ? launch<64, 2, false>(p, r, grid, st, where) : launch<64, 1, false>(p, r, grid, st, where);
@@ -929,7 +930,7 @@ gs_status f32_run(const MmaProduct& product, void* workspace, int32_t* status, c
       return set_error(GS_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", where);
   }
   p.status = status, p.wait_limit = wait_us(), p.drop = take_drop_copy();
-  if (gs_status s = launch_any(p, pl, st, where)) return s;
+  if (gs_status s = launch_any(p, pl, product.n, st, where)) return s;
   if (!p.part) {
     if (q.also.part) launch_column_fold<float>(q.also, st);
     return check_launch(where);
