@@ -353,37 +353,51 @@ int small_bwd_grid(const gs_linear_desc* d) {
   return (int)(tiles < most ? tiles : most);
 }
 
+// Whether 16-byte vectors lie whole in every row of [rows][width] matrices `ld` apart, by what the descriptor says.
+bool whole(int64_t rows, int64_t ld, int width, int32_t dtype) {
+  const int ve = 16 / (int)gs::dtype_size(dtype);
+  return width % ve == 0 && (rows <= 1 || ld % ve == 0);
+}
+
+// Whether a backward of at most 16 rows is the plain kernels', of which k_few_dx walks over all outputs for eight rows at a
+// time, and not the tensor cores'.  Alone, in us, here and there:
+//   float32          256 -> 256, 16 rows: 13, 21; 1024 -> 1024, 16: 22, 23; 4096 -> 1024, 8: 25, 31, 16: 39, 31; 1024 -> 4096, 1: 27, 30,
+//                    4: 37, 29; 8192 -> 64, 8: 17, 19, 16: 25, 19; off 16-byte rows 145 -> 952, 16: 19, 26; 60 -> 2001, 4: 21, 23, 8: 29, 23
+//   bfloat16 by TMA  256 -> 256, 16: 14, 19; 1024 -> 1024, 2: 16, 17, 8: 21, 17; 1024 -> 4096, 1: 29, 19; 8 -> 1016, 2: 15, 15, 8: 20, 15;
+//                    8192 -> 64, 1: 13, 15, 8: 17, 14
+//   others           145 -> 952, 16: 19, 23; 2047 -> 100, 16: 17, 20; 60 -> 2001, 4: 20, 21, 8: 27, 21
+bool few_bwd_takes(const gs_linear_desc* d) {
+  const bool tma = d->in_features % (16 / (int)gs::dtype_size(d->dtype)) == 0 && whole(d->rows, d->ldy, d->out_features, d->dtype);
+  const int64_t deep = (d->rows < kFew ? d->rows : kFew) * d->out_features, across = d->rows * d->in_features;
+  const int64_t work = across * d->out_features;
+  if (d->dtype == GS_F32)
+    return deep <= (tma ? 8192 : 12288) && work <= (1 << 25) && (d->rows <= kFew || d->in_features <= 4096);
+  return tma ? deep <= 2048 && across <= 16384 && d->in_features <= 8192 : deep <= 8192 && work <= (1 << 23);
+}
+
 // Whether k_few_fwd takes a forward call, and not the tensor cores.  It takes 2.6 us and 0.24 us for each step of a lane,
-// a vector of w against one of its rows, while no more than four blocks are on an SM (chains of dependent layers: 64 rows
-// of 64 -> 64 float32 5.1, 256 -> 256 6.7, 1024 -> 1024 18.9).  The tensor cores' products take
-//   float32               7 to 9 us, 11 at 4096 inputs: 8.9, 8.8 and 9.2 for the same layers
-//   bfloat16 by TMA       3 to 4 us, 7 from 1024 inputs on (256 -> 256: 16 rows 5.6 here, 4.0 there; 1 row 2.1 and 3.9)
-//   bfloat16, other rows  5.3 us, 8.5 at 255 inputs (9 -> 5: 512 rows 3.8 and 4.9; 60 -> 64 6.4 and 5.4)
-// and where there are more blocks (float32 64 -> 64: 512 rows 6.3 and 9.1, 1,024 rows 10.5 and 9.0) they take the call.
+// a vector of w against one of its rows, while no more than four blocks are on an SM (independent calls: 64 rows of
+// 64 -> 64 float32 4.9, 256 -> 256 6.9, 16 rows of 1024 -> 1024 14.7).  The tensor cores' products take
+//   float32               7 to 10 us (8.2, 10.5 and 9.6 for the same layers), 11 from 4096 inputs on
+//     off 16-byte rows    10 to 13 (255 -> 257: 4 rows 9.0 here, 10.6 there, 8 rows 14.3 and 10.8)
+//   bfloat16 by TMA       3 to 4, 7 from 1024 inputs on (256 -> 256: 16 rows 5.0 and 4.1, 1 row 2.1 and 3.9)
+//     others              5.5 with few inputs, else 7 to 10 (9 -> 5: 512 rows 3.9 and 5.3; 60 -> 64: 16 rows 7.5 and 5.8; 236 -> 23: 2 rows
+//                         5.1 and 7.4, 8 rows 13.4 and 7.9)
+// and where there are more blocks (float32 64 -> 64: 512 rows 5.7 and 8.6, 1,024 rows 9.8 and 8.7) they take the call.
 // Of eight rows at most w is read once, and a float32 product of many columns has fewer blocks on the tensor cores than
 // here (2048 -> 16384: 8 rows 97 and 117, 16 rows 208 and 116; 8192 -> 8192: 1 row 75 and 95, 4 rows 200 and 95).
 bool few_takes(const gs_linear_desc* d) {
   const int ve = 16 / (int)gs::dtype_size(d->dtype);
-  auto whole = [&](int64_t rows, int64_t ld) { return rows <= 1 || ld % ve == 0; };
-  const bool vec = d->in_features % ve == 0 && whole(d->rows, d->ldx) && whole(d->out_features, d->ldw);
-  const bool tma = vec && d->out_features % ve == 0 && whole(d->rows, d->ldy);
+  const bool vec = whole(d->rows, d->ldx, d->in_features, d->dtype) && whole(d->out_features, d->ldw, d->in_features, d->dtype);
+  const bool tma = vec && whole(d->rows, d->ldy, d->out_features, d->dtype);
   const int lanes = vec && d->in_features <= 8 * ve ? 8 : 32;
   const int64_t groups = ceil_div(d->rows, kFew), blocks = groups * ceil_div((int64_t)d->out_features * lanes, kThreads);
   const int64_t steps = (d->rows < kFew ? d->rows : kFew) * ceil_div(d->in_features, lanes * (vec ? ve : 1));
   if (d->dtype == GS_F32 && groups == 1 && d->out_features >= 8192) return steps <= 128;
-  const int64_t most = d->dtype == GS_F32 ? 16 + d->in_features / 256 : tma ? 4 + d->in_features / 256 : 8 + d->in_features / 32;
+  int64_t most;
+  if (d->dtype == GS_F32) most = tma ? 16 + d->in_features / 128 : 40;
+  else most = tma ? 4 + d->in_features / 128 : d->in_features < 192 ? 8 + d->in_features / 8 : 32;
   return d->in_features <= 4096 && steps <= most && blocks <= 4 * 152;
-}
-
-// Whether a backward of at most 16 rows is the plain kernels', of which k_few_dx walks over all outputs for eight rows at a
-// time, and not the tensor cores' (alone, 16 rows; float32 256 -> 256 13 us here, 21 there; 1024 -> 1024 21 and 23; 4096 ->
-// 1024 39 and 31, of 8 rows 25 and 31; 1024 -> 4096 56 and 30, of 1 row 27 and 30; 8192 -> 64 25 and 19, of 8 rows 17 and
-// 19; bfloat16 256 -> 256 14 and 19; 1024 -> 1024 23 and 19, of 4 rows 17 and 17; 1024 -> 4096 58 and 20, of 1 row 29 and 19;
-// 8192 -> 64 22 and 14, of 1 row 13 and 15).
-bool few_bwd_takes(const gs_linear_desc* d) {
-  const int64_t across = d->rows * d->in_features, deep = d->rows * d->out_features;
-  if (d->dtype == GS_F32) return deep <= 8192 && (d->rows <= kFew || d->in_features <= 4096);
-  return deep <= 4096 && d->out_features <= 2048 && across <= 16384;
 }
 
 template <typename T>
