@@ -1,8 +1,8 @@
 // Python functions over the dense-layer entry points for torch tensors (module _dense, used by dense.py): argument
 // checks, allocation of the outputs that the caller did not hand in and of the workspace, the stream, the call.
 //
-// A small layer's kernels take 4 to 10 us.  The same steps written in Python took 15 to 17 us of host time per
-// call (three allocations through the dispatcher 5, checks 3, ctypes 4); here they take about a third.
+// A small layer's kernels take 4 to 10 us.  A call takes 3.4 us of host time here for the linear forward, 6.9 for its
+// backward and 5.0 for the norm; through torch.empty and ctypes, without any checks, 12.7, 19.9 and 20.6.
 #include <Python.h>
 
 #include <ATen/ATen.h>

@@ -5,7 +5,8 @@
 // significant bits, the 24 of the value), and the product is summed from the six pairs whose weight is 2^-16
 // or more,
 //   a0 b0 | a0 b1 + a1 b0 + a1 b1 + a0 b2 + a2 b0
-// each exact in 32 bits; what is left out is below 2^-25 of |a b|.  The tensor core adds a product of
+// each exact in 32 bits; what is left out, a1 b2 + a2 b1 + a2 b2, is at most about 2^-24 of |a b| (a1 is at most 2^-8
+// of a, a2 2^-17), half a unit in the last place of a product.  The tensor core adds a product of
 // 16 terms to its sum with the low bits cut off (measured: 2.3e-7 of the result after 256 terms, 4.4e-6
 // after 4096, always towards zero), so the pairs of the second group, 2^-8 smaller, have an accumulator of
 // their own, and every 256 of k both are read back and added in registers with ordinary rounding.  Six

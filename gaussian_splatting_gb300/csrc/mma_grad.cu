@@ -6,7 +6,7 @@
 // costs its own store only, and not another read of dz.  One persistent block per SM walks over tiles of 128
 // rows:
 //   warps 0 - 15   read dy and z (four vectors of 16 bytes of each in flight per thread), form dz, round it to
-//                  bfloat16 once, write it to memory and, swizzled, to shared memory, and add the columns up.
+//                  bfloat16 once (the operand's type; what that costs stands in linear.cu), write it to memory and, swizzled, to shared memory, and add the columns up.
 //                  Where w leaves no room for a second buffer of dz they work in four groups, one for each 64 of
 //                  the outputs, and a group waits only for the products of its own block of k: together they would
 //                  stand still for all of a tile's products

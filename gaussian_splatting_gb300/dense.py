@@ -9,7 +9,12 @@ the host, and nothing is kept between calls.
 
 Work is enqueued on ``stream`` (a ``torch.cuda.Stream``, a handle, or None: the current torch stream), on which
 the tensors must be ready.  Outputs and scratch that a call allocates belong to that stream.  ``status`` is an
-int32 CUDA tensor that is set to nonzero if a bounded wait on the device gave up, and is never cleared.
+int32 CUDA tensor that is set to nonzero if a bounded wait on the device gave up, and is never cleared: without it
+such a call's invalid outputs go unnoticed.  An output that a call is handed must not overlap its inputs or another
+output, but for the cases named below.
+
+Autograd does not see these calls: outputs never require a gradient, whatever the inputs do.  The backward functions
+are called by the program, as ``head.py`` does.
 """
 from __future__ import annotations
 

@@ -455,8 +455,14 @@ gs_status gs_densify(const float* params, const float* exp_avg, const float* exp
  * Matrices are row-major with a stride between rows, in elements (ld*; at least the width), of
  * one element type for every array of a call unless a comment says otherwise.  Any width,
  * stride and element-aligned address is valid; calls whose rows all start and end on 16-byte
- * boundaries run faster.  Sums, products, activations and statistics are computed in 32 bits (bfloat16
- * products are exact, their sums 32-bit) and rounded once when stored.
+ * boundaries run faster.  Sums, products, activations and statistics are computed in 32 bits and rounded once
+ * when stored.  float32 products are those of the definition over the whole range, infinities included.
+ * bfloat16 products are exact; on the tensor cores their sums are 32-bit and cut off, not rounded, after
+ * every 16 terms: up to n / 16 * 2^-23 of the terms' magnitudes for n terms (of a dw sum, those that one
+ * block takes), towards zero.
+ * The same call gives the same bits.  So do dx, dw and dbias whichever of the others are wanted.  y may
+ * differ in its last bits with z wanted or not, and any result with the alignment of the arrays, by which
+ * the kernel is chosen.
  */
 typedef enum { GS_F32 = 0, GS_BF16 = 1 } gs_dtype;
 typedef enum {
@@ -484,8 +490,9 @@ typedef enum {
  *   dx [rows][in] stride lddx, dw [out][in] stride lddw, dbias [out]: outputs, each may be NULL
  *              (not computed).  They are overwritten, not added to.  The residual's gradient
  *              is dy itself.
- *   With GS_BF16, dz is rounded to bfloat16 where it enters the products (dbias sums it
- *   unrounded).  rows == 0 writes zeros to dw and dbias.
+ *   With GS_BF16 and an activation, dz is rounded to bfloat16 where it enters a product on the tensor
+ *   cores (dbias sums it unrounded; few rows and narrow unaligned layers keep it in 32 bits).
+ *   No output may overlap an input or another output.  rows == 0 writes zeros to dw and dbias.
  *   Results do not depend on the launch order: no atomics touch them.
  */
 typedef struct {
