@@ -234,7 +234,8 @@ __device__ __forceinline__ void advance(const Args& p, int bn, Cursor& c, int to
 // The sums of this lane's row and COLS columns that are NaN, again over the k blocks [kb, k_hi) by the FP32 pipe.  The
 // warp does it together, eight columns at a time; rows and columns outside of C take the last one's values.  It is slow
 // (counted: 1,600 cycles per k and tile of 64 columns, 3,200 per tile of 128, where every row has a NaN), but inside the
-// waits' limit of 4 s up to a million of k.
+// waits' limit of 4 s up to a million of k.  Where all sums are NaN in earnest it ends with the first (20,000 x 1024 ->
+// 1024 of NaN alone: 0.72 ms, 16 to their ends; clean 0.28).
 template <int COLS>
 __device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t row, uint32_t col0, int kb, int k_hi) {
   constexpr int kAt = 8;
@@ -254,6 +255,12 @@ __device__ __forceinline__ void plain_sums(const Args& p, float* sum, uint32_t r
       for (int j = 0; j < kAt; ++j) {
         const uint32_t col = min(col0 + c + j, (uint32_t)p.n - 1);
         v[j] = fmaf(f, p.b[p.b_mn ? k * p.ldb + col : col * p.ldb + k], v[j]);
+      }
+      if (k % 32 == 31) {
+        bool lost = true;  // a NaN stays one
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) lost = lost && isnan(v[j]);
+        if (__all_sync(0xffffffffu, lost)) break;
       }
     }
 #pragma unroll
