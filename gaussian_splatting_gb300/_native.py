@@ -26,7 +26,9 @@ EXPORTS = ["gs_last_error", "gs_version", "gs_project", "gs_project_batch", "gs_
            "gs_tile_split", "gs_view_order", "gs_prune_workspace_size", "gs_prune", "gs_densify_workspace_size",
            "gs_densify", "gs_probe_ffma", "gs_linear_fwd_workspace_size", "gs_linear_fwd",
            "gs_linear_bwd_workspace_size", "gs_linear_bwd", "gs_layernorm_fwd", "gs_layernorm_bwd_workspace_size",
-           "gs_layernorm_bwd",
+           "gs_layernorm_bwd", "gs_embedding_fwd", "gs_embedding_bwd_workspace_size", "gs_embedding_bwd",
+           "gs_groupnorm_fwd_workspace_size", "gs_groupnorm_fwd", "gs_groupnorm_bwd_workspace_size", "gs_groupnorm_bwd",
+           "gs_adamw",
            "gs_debug_set_wait_limit",
            "gs_debug_drop_publish"]
 
@@ -59,6 +61,32 @@ class LayerNormDesc(C.Structure):
     _fields_ = [("rows", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64), ("lddy", C.c_int64),
                 ("ldskip", C.c_int64), ("lddx", C.c_int64), ("width", C.c_int32), ("dtype", C.c_int32),
                 ("eps", C.c_float)]
+
+
+class EmbeddingDesc(C.Structure):
+    """gs_embedding_desc."""
+    _fields_ = [("rows", C.c_int64), ("n", C.c_int64), ("ldt", C.c_int64), ("ldy", C.c_int64), ("width", C.c_int32),
+                ("dtype", C.c_int32), ("index_bits", C.c_int32), ("scale", C.c_float)]
+
+
+class GroupNormDesc(C.Structure):
+    """gs_groupnorm_desc."""
+    _fields_ = [("samples", C.c_int64), ("rows", C.c_int64), ("ldx", C.c_int64), ("ldy", C.c_int64),
+                ("lddy", C.c_int64), ("ldskip", C.c_int64), ("lddx", C.c_int64), ("width", C.c_int32),
+                ("groups", C.c_int32), ("dtype", C.c_int32), ("act", C.c_int32), ("eps", C.c_float)]
+
+
+class AdamWTensor(C.Structure):
+    """gs_adamw_tensor."""
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("exp_avg", C.c_void_p), ("exp_avg_sq", C.c_void_p),
+                ("exp_avg_scale", C.c_void_p), ("exp_avg_sq_scale", C.c_void_p), ("copy", C.c_void_p),
+                ("n", C.c_int64), ("lr", C.c_double), ("weight_decay", C.c_double)]
+
+
+class AdamWDesc(C.Structure):
+    """gs_adamw_desc."""
+    _fields_ = [("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("step", C.c_int64),
+                ("grad_dtype", C.c_int32), ("state_bits", C.c_int32), ("seed", C.c_uint32)]
 
 
 def camera(cam) -> Camera:
@@ -121,6 +149,14 @@ def load() -> C.CDLL:
         "gs_layernorm_fwd": ([vp, vp, vp, vp, vp, vp, vp, vp], i32),
         "gs_layernorm_bwd_workspace_size": ([vp], sz),
         "gs_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "gs_embedding_fwd": ([vp, vp, vp, vp, vp], i32),
+        "gs_embedding_bwd_workspace_size": ([vp], sz),
+        "gs_embedding_bwd": ([vp, vp, vp, vp, vp, sz, vp], i32),
+        "gs_groupnorm_fwd_workspace_size": ([vp], sz),
+        "gs_groupnorm_fwd": ([vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "gs_groupnorm_bwd_workspace_size": ([vp], sz),
+        "gs_groupnorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "gs_adamw": ([vp, vp, i32, vp, i32, vp], i32),
         "gs_debug_set_wait_limit": ([i64], None),
         "gs_debug_drop_publish": ([i32], None),
     }
@@ -389,3 +425,43 @@ def gs_layernorm_bwd(desc, dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, wo
     _check(load().gs_layernorm_bwd(C.addressof(desc), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
                                    _ptr(skip), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace_bytes,
                                    _stream(stream)), "gs_layernorm_bwd")
+
+
+def gs_embedding_fwd(desc, table, idx, y, stream=None):
+    _check(load().gs_embedding_fwd(C.addressof(desc), _ptr(table), _ptr(idx), _ptr(y), _stream(stream)), "gs_embedding_fwd")
+
+
+def gs_embedding_bwd_workspace_size(desc) -> int:
+    return load().gs_embedding_bwd_workspace_size(C.addressof(desc))
+
+
+def gs_embedding_bwd(desc, dy, idx, dtable, workspace, workspace_bytes, stream=None):
+    _check(load().gs_embedding_bwd(C.addressof(desc), _ptr(dy), _ptr(idx), _ptr(dtable), _ptr(workspace),
+                                   workspace_bytes, _stream(stream)), "gs_embedding_bwd")
+
+
+def gs_groupnorm_fwd_workspace_size(desc) -> int:
+    return load().gs_groupnorm_fwd_workspace_size(C.addressof(desc))
+
+
+def gs_groupnorm_fwd(desc, x, gamma, beta, y, mean, rstd, workspace, workspace_bytes, stream=None):
+    _check(load().gs_groupnorm_fwd(C.addressof(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd),
+                                   _ptr(workspace), workspace_bytes, _stream(stream)), "gs_groupnorm_fwd")
+
+
+def gs_groupnorm_bwd_workspace_size(desc) -> int:
+    return load().gs_groupnorm_bwd_workspace_size(C.addressof(desc))
+
+
+def gs_groupnorm_bwd(desc, dy, x, gamma, beta, mean, rstd, skip, dx, dgamma, dbeta, workspace, workspace_bytes,
+                     stream=None):
+    _check(load().gs_groupnorm_bwd(C.addressof(desc), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
+                                   _ptr(skip), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace_bytes,
+                                   _stream(stream)), "gs_groupnorm_bwd")
+
+
+def gs_adamw(desc, tensors, counts=None, n_counts=0, stream=None):
+    """tensors: a list of AdamWTensor."""
+    arr = (AdamWTensor * len(tensors))(*tensors)
+    _check(load().gs_adamw(C.addressof(desc), C.addressof(arr), len(tensors), _ptr(counts),
+                           n_counts if counts is not None else 0, _stream(stream)), "gs_adamw")

@@ -1,7 +1,8 @@
 """The dense layers of a per-Gaussian attribute head on torch tensors.
 
-``linear_fwd`` / ``linear_bwd`` (``y = act(x w^T + bias) + residual``) and ``layernorm_fwd`` /
-``layernorm_bwd`` check shapes, types, devices and strides (``ValueError``), allocate what the caller did not
+``linear_fwd`` / ``linear_bwd`` (``y = act(x w^T + bias) + residual``), ``layernorm_fwd`` / ``layernorm_bwd``,
+``groupnorm_fwd`` / ``groupnorm_bwd`` (channels-last feature maps, with an activation), ``embedding_fwd`` /
+``embedding_bwd`` (learned codes) and ``adamw`` (the update of all of a network's tensors) check shapes, types, devices and strides (``ValueError``), allocate what the caller did not
 hand in and call the entry points of the same names in libgs.so (``native.gs_linear_fwd`` and so on, which take
 addresses), where the formulas stand.  Matrices are 2-D CUDA tensors, float32 or bfloat16, whose rows may be any
 distance apart (``stride(1) == 1``); the arrays of one call share one type.  Nothing synchronises with
@@ -84,3 +85,67 @@ def layernorm_bwd(dy, x, gamma, mean, rstd, skip=None, dx=None, dgamma=None, dbe
     path around the layer).  Outputs given are overwritten; ``dx`` may be ``dy`` or ``skip``."""
     return (_binding or _load()).layernorm_bwd(dy, x, gamma, mean, rstd, skip, dx, dgamma, dbeta, need_dx, need_dparams,
                                                _handle(stream))
+
+
+def embedding_fwd(table, idx, scale=1.0, out=None, stream=None):
+    """y [rows, width]: ``scale`` times the rows of ``table`` [n, width] that ``idx`` (int32 or int64 [rows], contiguous)
+    names; zeros where an index is not in 0..n-1 (no code)."""
+    return (_binding or _load()).embedding_fwd(table, idx, scale, out, _handle(stream))
+
+
+def embedding_bwd(dy, idx, n, scale=1.0, dtable=None, stream=None):
+    """dtable [n, width] of ``embedding_fwd`` for the output gradient dy [rows, width]: ``scale`` times the sum of the
+    rows of each code, zeros for a code without rows.  ``dtable`` receives it (overwritten) when given."""
+    return (_binding or _load()).embedding_bwd(dy, idx, n, scale, dtable, _handle(stream))
+
+
+def groupnorm_fwd(x, gamma, beta, groups, samples=1, act="none", eps=1e-5, out=None, stats=True, stream=None):
+    """``(y, mean, rstd)``: y = act((x - mean) rstd gamma + beta) with mean and rstd over a map's rows and a group's
+    channels.  x [samples * rows, channels] holds ``samples`` maps of equally many rows (a batch of channels-last images:
+    ``images.permute(0, 2, 3, 1).reshape(-1, channels)``), its channels ``groups`` groups of neighbours.  mean and rstd
+    (float32 [samples, groups], what the backward reads) are None with ``stats=False``.  ``out`` may be ``x``, which the
+    backward then lacks."""
+    return (_binding or _load()).groupnorm_fwd(x, gamma, beta, groups, samples, _act(act), eps, out, stats, _handle(stream))
+
+
+def groupnorm_bwd(dy, x, gamma, beta, mean, rstd, act="none", skip=None, dx=None, dgamma=None, dbeta=None, need_dx=True,
+                  need_dparams=True, stream=None):
+    """``(dx, dgamma, dbeta)`` of ``groupnorm_fwd``; maps and groups are those of ``mean`` [samples, groups].  ``skip`` is
+    a gradient added to dx (the residual path around the layer).  Outputs given are overwritten; ``dx`` may be ``dy`` or
+    ``skip``."""
+    return (_binding or _load()).groupnorm_bwd(dy, x, gamma, beta, mean, rstd, _act(act), skip, dx, dgamma, dbeta, need_dx,
+                                               need_dparams, _handle(stream))
+
+
+def adamw_state(params, bits=32):
+    """``(exp_avg, exp_avg_sq, scales)`` for ``adamw``, all zero: a float32 tensor like each of ``params``, or with
+    ``bits=8`` a float8_e4m3fn one and, in ``scales``, the two lists of its float32 scales (None with 32 bits)."""
+    import torch
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 32 or 8, got {bits!r}")
+    params = list(params)
+
+    def zeros():
+        # (zeroed as bytes: not every operation takes the 8-bit type)
+        return [torch.zeros(p.shape, dtype=torch.float32, device=p.device) if bits == 32 else
+                torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn) for p in params]
+
+    def scale():
+        return [torch.zeros((p.numel() + 255) // 256, dtype=torch.float32, device=p.device) for p in params]
+
+    return zeros(), zeros(), None if bits == 32 else (scale(), scale())
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, scales=None,
+          copies=None, seed=0, counts=None, stream=None):
+    """One AdamW step, number ``step`` (from 1), over all tensors of the list ``params`` (float32), in place, from ``grads``
+    (float32 or bfloat16, all alike).  ``lr`` and ``weight_decay`` are numbers, or sequences of one for each tensor.
+
+    The moments (``adamw_state`` makes them) are float32, or with ``scales`` float8_e4m3fn: ``exp_avg_sq`` then holds the
+    root of the second moment, and each 256 neighbouring values of a tensor share a scale.  They are rounded at random, by
+    ``seed`` and ``step`` alone: the same call gives the same bits.  ``copies`` (bfloat16, like ``params``) receive the
+    updated parameters, for layers that compute in bfloat16.  With ``counts`` (int64 [records, 2], as
+    ``AttributeHead.status`` or ``StepResult.status``) the step is skipped on the device where any record's second
+    entry is not zero.  Tensors are contiguous; none may overlap another."""
+    (_binding or _load()).adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], eps, weight_decay, scales,
+                                copies, seed, counts, _handle(stream))

@@ -543,6 +543,116 @@ gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy, const voi
                            const float* mean, const float* rstd, const void* skip, void* dx, void* dgamma,
                            void* dbeta, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * gs_embedding_fwd -- rows of a table by their indices: y[r] = scale table[idx[r]].  The learned codes of a head: one
+ * per view, per Gaussian or per cluster of Gaussians.
+ *   table [n][width] stride ldt; idx [rows], int32 or int64 by index_bits; y [rows][width] stride ldy, not overlapping
+ *   the table.  A row whose index is not in 0..n-1 has no code: its y is zeros.
+ * rows == 0 is a no-op; n may be 0.  rows is at most 2^31 - 1024, n 2^31 - 2, width 1..2^20.
+ *
+ * gs_embedding_bwd -- the table's gradient, from dy [rows][width] (stride ldy):
+ *   dtable[v] = scale (sum of dy[r] over the rows r with idx[r] = v), n x width, stride ldt, every row overwritten (a
+ *   code that no row has gets zeros).  dtable must not overlap dy or idx.
+ *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the arguments' sizes alone
+ *   decide: no atomics on values, the same bits each run.
+ *   workspace  gs_embedding_bwd_workspace_size(d) bytes, 256-byte aligned.
+ * rows == 0 writes zeros.
+ */
+typedef struct {
+  int64_t rows, n;
+  int64_t ldt, ldy; /* strides in elements */
+  int32_t width;
+  int32_t dtype;      /* gs_dtype */
+  int32_t index_bits; /* 32 or 64 */
+  float scale;
+} gs_embedding_desc;
+
+gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* table, const void* idx, void* y, void* stream);
+size_t gs_embedding_bwd_workspace_size(const gs_embedding_desc* d);
+gs_status gs_embedding_bwd(const gs_embedding_desc* d, const void* dy, const void* idx, void* dtable, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gs_groupnorm_fwd -- group normalisation with an activation over channels-last feature maps.  x [samples * rows][width]
+ * (stride ldx) holds `samples` maps of `rows` pixels each, one after the other; the width's channels form `groups`
+ * groups of width / groups neighbours.  Per map and group, over its rows and channels: mean,
+ * rstd = (var + eps)^-1/2 with var the mean squared distance from the mean; then
+ *   z = (x - mean) rstd gamma + beta, y = act(z)   (y stride ldy).
+ *   gamma, beta [width]; mean, rstd [samples][groups] float32 outputs, each may be NULL.  y may be x itself.
+ *   workspace  gs_groupnorm_fwd_workspace_size(d) bytes, 16-byte aligned (may be 0: NULL).
+ * samples * rows == 0 is a no-op but for mean (0) and rstd (eps^-1/2).  width is 1..2^20, a multiple of groups;
+ * samples * rows at most 2^31 - 1.
+ *
+ * gs_groupnorm_bwd -- the gradient, from dy (stride lddy), with h = (x - mean) rstd, dz = dy act'(z) and g = dz gamma:
+ *   dx = rstd (g - mean(g) - h mean(g h)) + skip (means over the map's group), dgamma = sum of dz h, dbeta = sum of dz over
+ *   all rows of all maps.
+ *   skip [samples * rows][width] stride ldskip, or NULL: a gradient that reaches x by another path.  dx stride lddx.  dx,
+ *   dgamma [width], dbeta [width] may each be NULL (not computed); dx may be dy or skip itself.
+ *   workspace  gs_groupnorm_bwd_workspace_size(d) bytes, 16-byte aligned.
+ * samples * rows == 0 writes zeros to dgamma and dbeta.  Sums are taken in 32 bits in a fixed order: no atomics.
+ */
+typedef struct {
+  int64_t samples, rows;                /* maps, and rows (pixels) of each */
+  int64_t ldx, ldy, lddy, ldskip, lddx; /* strides in elements; those a call does not use are ignored */
+  int32_t width, groups;
+  int32_t dtype; /* gs_dtype */
+  int32_t act;   /* gs_act */
+  float eps;     /* forward only */
+} gs_groupnorm_desc;
+
+size_t gs_groupnorm_fwd_workspace_size(const gs_groupnorm_desc* d);
+gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
+                           float* mean, float* rstd, void* workspace, size_t workspace_bytes, void* stream);
+size_t gs_groupnorm_bwd_workspace_size(const gs_groupnorm_desc* d);
+gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy, const void* x, const void* gamma,
+                           const void* beta, const float* mean, const float* rstd, const void* skip, void* dx,
+                           void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gs_adamw -- one AdamW step over many tensors at once.  For every value of every tensor, with its own lr and
+ * weight_decay and t = step >= 1:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * Moments have 32 bits, or 8 (state_bits): then exp_avg holds m and exp_avg_sq the root of v as float8 e4m3 values, each
+ * run of 256 neighbouring values of a tensor with a float32 scale of its own ([ceil(n / 256)], the run's largest
+ * magnitude / 448): m = scale code.  Zeroed arrays are zero moments.  The update takes the new moments before they are
+ * rounded.  A moment is rounded to the type's four significant bits at random, up with the probability that leaves its
+ * expected value (a moment that changes by less than half a step of the type would never move otherwise), to the nearest
+ * value of the type where that is coarser (below 2^-6 / 448 of the run's largest).  A root that is not zero stays at least
+ * 2^-9 scale; a run whose largest magnitude is below 2^-100 becomes zeros.  The random bits are a function of seed, step
+ * and the value's place in the call, counting every tensor from a multiple of 256: with c that count,
+ *   h = c 0x9E3779B1 + seed 0x6A09E667 + step 0xBB67AE85; h = (h ^ h >> 16) 0x6A09E667; h = (h ^ h >> 15) 0xBB67AE85;
+ *   h = h ^ h >> 16  (modulo 2^32): its low half for m, its high half for v.
+ * The 8-bit moments' arithmetic is IEEE single precision, one rounding an operation, so that their bits are defined.  A
+ * NaN or an infinity in g spoils its value's moments, of 8 bits those of its whole run.
+ *   tensors    HOST array of `count` descriptions.  param float32; grad of grad_dtype; exp_avg, exp_avg_sq; their scales
+ *              (8 bits only); copy: bfloat16 [n], the updated parameters rounded (the layers' working copy), or NULL.
+ *              Contiguous, any element-aligned address (16-byte aligned ones run faster); n == 0 is allowed.  No array
+ *              may overlap another.
+ *   counts     as for gs_sparse_adam: if any of n_counts records' second word is nonzero, the whole step is skipped.
+ */
+typedef struct {
+  float* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  void* copy;
+  int64_t n;
+  double lr, weight_decay;
+} gs_adamw_tensor;
+typedef struct {
+  double beta1, beta2, eps;
+  int64_t step;
+  int32_t grad_dtype; /* gs_dtype */
+  int32_t state_bits; /* 32 or 8 */
+  uint32_t seed;      /* 8 bits only */
+} gs_adamw_desc;
+
+gs_status gs_adamw(const gs_adamw_desc* d, const gs_adamw_tensor* tensors, int count, const int64_t* counts,
+                   int n_counts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
