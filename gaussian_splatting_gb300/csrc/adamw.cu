@@ -82,22 +82,33 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h = (h ^ (h >> 15)) * 0xBB67AE85u;
   return h ^ (h >> 16);
 }
-// to four significant bits, up where 16 random bits carry
-__device__ __forceinline__ float at_random(float q, uint32_t bits16) {
-  q = q > kTop ? kTop : q < -kTop ? -kTop : q;
-  return __uint_as_float((__float_as_uint(q) + (bits16 << 4)) & 0xfff00000u);
+// To four significant bits, up where 16 random bits (at bits 4 to 19 of `noise`) carry.  The largest value's quotient may be
+// a unit in the last place above 448, and what that is rounded up to is saturated by the conversion.
+__device__ __forceinline__ float at_random(float q, uint32_t noise) {
+  return __uint_as_float((__float_as_uint(q) + (noise & 0xffff0u)) & 0xfff00000u);
+}
+// the larger of two magnitudes, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// (b is at least eps or the root of a float, or zero: never so large or small that the approximation flushes it)
+__device__ __forceinline__ float recip(float b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+  return r;
 }
 
-// The eight values of a lane, as two fours: lane * 4 + 128 k.  What lies beyond the tensor is taken as zeros.
-template <typename G, int BITS>
+// A run by a warp, eight values a lane: two fours (WIDE), or every 32nd one, what lies beyond the tensor taken as zeros.
+template <typename G, int BITS, bool WIDE>
 __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane, const float b1, const float c1, const float b2,
                                            const float c2, const float eps, const float root, const uint32_t key) {
   const G* gp = static_cast<const G*>(t.g);
   float p[8], g[8], m[8], v[8];
-  const bool wide = t.wide && at + kRun <= t.n;
-  auto place = [&](int i) { return at + (wide ? lane * 4 + (i >> 2) * 128 + (i & 3) : lane + 32 * i); };
+  auto place = [&](int i) { return at + lane + 32 * i; };
   uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
-  if (wide) {
+  if constexpr (WIDE) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t e = at + lane * 4 + k * 128;
@@ -145,29 +156,27 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
     m[i] = __fadd_rn(__fmul_rn(m[i], b1), __fmul_rn(g[i], c1));
     v[i] = __fadd_rn(__fmul_rn(v[i], b2), __fmul_rn(__fmul_rn(g[i], g[i]), c2));
     s[i] = __fsqrt_rn(v[i]);
-    p[i] = __fmul_rn(p[i], t.keep) - __fdividef(m[i] * t.step, fmaf(s[i], root, eps));
+    p[i] = fmaf(m[i] * -t.step, recip(fmaf(s[i], root, eps)), p[i] * t.keep);
   }
   uint32_t qm[2], qv[2];
   if constexpr (BITS == 8) {
-    // the bits of magnitudes order as their values do, NaN above all
-    uint32_t am = 0, av = 0;
+    float am = 0.f, av = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      am = max(am, __float_as_uint(m[i]) & 0x7fffffffu);
-      av = max(av, __float_as_uint(s[i]) & 0x7fffffffu);
-    }
-    am = __reduce_max_sync(0xffffffffu, am), av = __reduce_max_sync(0xffffffffu, av);
+    for (int i = 0; i < 8; ++i) am = max_nan(am, fabsf(m[i])), av = max_nan(av, s[i]);
+    // the bits of magnitudes order as their values do, NaN above all
+    const uint32_t bm = __reduce_max_sync(0xffffffffu, __float_as_uint(am)), bv = __reduce_max_sync(0xffffffffu, __float_as_uint(av));
     constexpr uint32_t kLeast = (127 - 100) << 23;  // 2^-100
-    const float tm = am >= kLeast ? __uint_as_float(am) : 0.f, tv = av >= kLeast ? __uint_as_float(av) : 0.f;
+    const float tm = bm >= kLeast ? __uint_as_float(bm) : 0.f, tv = bv >= kLeast ? __uint_as_float(bv) : 0.f;
     const float im = tm != 0.f ? __fmul_rn(__frcp_rn(tm), kTop) : 0.f, iv = tv != 0.f ? __fmul_rn(__frcp_rn(tv), kTop) : 0.f;
-    const uint32_t base = t.place + (uint32_t)at;
+    const float least = tv != 0.f ? 0x1p-9f : 0.f;
+    const uint32_t base = (t.place + (uint32_t)at + (WIDE ? lane * 4 : lane)) * 0x9E3779B1u + key;
     float a[8], b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t h = mix((base + (uint32_t)(place(i) - at)) * 0x9E3779B1u + key);
-      a[i] = at_random(__fmul_rn(m[i], im), h & 0xffffu);
-      b[i] = at_random(__fmul_rn(s[i], iv), h >> 16);
-      if (s[i] > 0.f && tv != 0.f) b[i] = b[i] < 0x1p-9f ? 0x1p-9f : b[i];
+      const uint32_t h = mix(base + (WIDE ? (uint32_t)((i >> 2) * 128 + (i & 3)) : (uint32_t)(32 * i)) * 0x9E3779B1u);
+      a[i] = at_random(__fmul_rn(m[i], im), h << 4);
+      b[i] = at_random(__fmul_rn(s[i], iv), h >> 12);
+      if (s[i] > 0.f) b[i] = fmaxf(b[i], least);
     }
     qm[0] = encode4(a), qm[1] = encode4(a + 4);
     qv[0] = encode4(b), qv[1] = encode4(b + 4);
@@ -176,7 +185,7 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
       t.vs[run] = __fmul_rn(tv, 1.f / kTop);
     }
   }
-  if (wide) {
+  if constexpr (WIDE) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t e = at + lane * 4 + k * 128;
@@ -223,7 +232,11 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Args
   }
   const Tensor& t = a.t[lo];
   const int64_t at = (int64_t)(blockIdx.x - t.tile) * kTile + (threadIdx.x >> 5) * kRun;
-  if (at < t.n) run_of_256<G, BITS>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
+  if (at >= t.n) return;
+  if (t.wide && at + kRun <= t.n)
+    run_of_256<G, BITS, true>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
+  else
+    run_of_256<G, BITS, false>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
 }
 
 template <int MOST>
