@@ -12,8 +12,7 @@
 // the statistics stay in registers and every access of a warp is a run of whole sectors.  The variance is taken about a value of the
 // thread's own rows (their first), so that it loses nothing where the mean is far from zero: a pivot p among n values with
 // squared distances M from their mean has n (p - mean)^2 <= n M.  Chunks' sums are joined about the joint mean, in a fixed order.
-// What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2, which is
-// cheaper than a kernel between the two.
+// What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2.
 #include <algorithm>
 #include <cmath>
 
@@ -22,7 +21,6 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 // A map's rows in chunks of blocks, its channels in slabs of columns.
 struct Shape {
@@ -61,132 +59,198 @@ struct BwdArgs {
   int64_t lddy, ldx, ldskip, lddx;
 };
 
-// What a block works on.
+// What a block works on: a chunk, by its number.
 struct Place {
-  int64_t sample, row, end;  // rows of the matrix
+  int64_t sample, row, end;     // rows of the matrix
   int chunk, slab, col0, col1;  // its slab's columns
   int g0, g1;                   // and the groups that they touch
-  __device__ __forceinline__ Place(const Shape& s, unsigned block) {
-    sample = block / s.chunks, chunk = block % s.chunks, slab = blockIdx.y;
+  __device__ __forceinline__ Place(const Shape& s, unsigned number) {
+    sample = number / s.chunks, chunk = number % s.chunks, slab = blockIdx.y;
     row = sample * s.rows + chunk * s.chunk;
     end = min(row + s.chunk, (sample + 1) * s.rows);
     col0 = slab * s.cols, col1 = min(col0 + s.cols, s.width);
     g0 = col0 / s.per, g1 = (col1 - 1) / s.per + 1;
   }
 };
+// The index of the first of a slab's parts of a group in the array of parts.
+__device__ __forceinline__ int64_t parts_of(const Shape& s, int64_t sample, int slab, int group) {
+  return ((sample * s.slabs + slab) * s.span + (group - slab * s.cols / s.per)) * s.chunks;
+}
 
-__device__ __forceinline__ float2 warp_sum(float2 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+// The rows of a thread in A arrays, through a ring of its own in shared memory: D rows ahead are copied asynchronously, which
+// takes no registers and, as nobody else reads the thread's slots, no barriers.
+extern __shared__ __align__(16) char s_ring[];
+constexpr int kRing = 40 << 10;  // with the group's statistics no more than a block has without asking
+template <int BYTES, int A>
+constexpr int ring_depth() {
+  constexpr int d = kRing / (kThreads * BYTES * A);
+  return d > 12 ? 12 : d;
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+template <typename T, int VE, int A>
+struct Rows {
+  using IO = VecIO<T, VE>;
+  using Raw = typename IO::Raw;
+  static constexpr bool kAsync = sizeof(Raw) >= 4;  // no copies of two bytes: those rows are read in batches
+  static constexpr int D = kAsync ? ring_depth<sizeof(Raw), A>() : 8;
+  const T* at[A];
+  int64_t step[A];
+  int count, next;
+  __device__ __forceinline__ Raw& slot(int stage, int i) {
+    return reinterpret_cast<Raw*>(s_ring)[(stage * A + i) * kThreads + threadIdx.x];
   }
+  __device__ __forceinline__ void issue(int stage) {
+    if (next < count) {
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        copy_async<sizeof(Raw)>(&slot(stage, i), at[i]);
+        at[i] += step[i];
+      }
+    }
+    ++next;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void start(int n) {
+    count = n, next = 0;
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int u = 0; u < D; ++u) issue(u);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+    for (int i = 0; i < count; i += D) {
+      Raw v[kAsync ? 1 : D][A];
+      if constexpr (!kAsync) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+#pragma unroll
+          for (int k = 0; k < A; ++k) {
+            v[u][k] = i + u < count ? IO::load(at[k]) : IO::zero();
+            at[k] += step[k];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        if (i + u >= count) break;
+        if constexpr (kAsync) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+#pragma unroll
+          for (int k = 0; k < A; ++k) v[0][k] = slot(u, k);
+        }
+        f(v[kAsync ? 0 : u]);
+        if constexpr (kAsync) issue(u);
+      }
+    }
+  }
+};
+// A vector's values as pairs, which sm_100 adds and multiplies in one instruction, or as one value (VE = 1).
+template <int VE>
+struct Pairs {
+  using E = F2;
+  static constexpr int N = VE / 2;
+  static __device__ __forceinline__ E of(const float* f, int i) { return F2(f[2 * i], f[2 * i + 1]); }
+  static __device__ __forceinline__ void get(const E& v, float* f, int i) { v.get(f[2 * i], f[2 * i + 1]); }
+};
+template <>
+struct Pairs<1> {
+  using E = float;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ E of(const float* f, int) { return f[0]; }
+  static __device__ __forceinline__ void get(const E& v, float* f, int) { f[0] = v; }
+};
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+
+// 1 / (1 + exp(-v)) of two values by one reciprocal, of the product of the denominators: a third fewer special-function
+// operations, which bound the activation (16 a cycle and SM).  The exponent is held to 60, so that the product stays
+// finite: below v = -41.6 the result is 2^-60.
+__device__ __forceinline__ F2 logistic_of(F2 v) {
+  float a, b, r;
+  mul2(v, F2(-1.4426950408889634f)).get(a, b);
+  const F2 d = add2(F2(fast_exp2(fminf(a, 60.f)), fast_exp2(fminf(b, 60.f))), F2(1.f));
+  d.get(a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+  return mul2(F2(r), F2(b, a));
+}
+template <int ACT>
+__device__ __forceinline__ F2 activate(F2 z) {
+  if constexpr (ACT == GS_ACT_SILU) return mul2(z, logistic_of(z));
+  float a, b;
+  z.get(a, b);
+  act_value2(a, b, ACT);
+  return F2(a, b);
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  return act_value(z, ACT);
+}
+template <int ACT>
+__device__ __forceinline__ F2 slope_of(F2 z) {
+  if constexpr (ACT == GS_ACT_SILU) {
+    const F2 s = logistic_of(z);
+    return mul2(s, fma2(z, fma2(s, F2(-1.f), F2(1.f)), F2(1.f)));
+  } else {
+    float a, b;
+    z.get(a, b);
+    return F2(act_slope(a, ACT), act_slope(b, ACT));
+  }
+}
+template <int ACT>
+__device__ __forceinline__ float slope_of(float z) {
+  return act_slope(z, ACT);
+}
+
+// Threads to each of n items, a power of two: all items at once if the block has as many.
+__device__ __forceinline__ int side_by_side(int n) {
+  int k = 32;
+  while (k > 1 && n * k > kThreads) k >>= 1;
+  return k;
+}
+__device__ __forceinline__ float sum_among(float v, int k) {
+  for (int o = k / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Mean and rstd of a group, from the parts of all chunks and slabs, by a warp.
-__device__ __forceinline__ float2 group_stats(const FwdArgs& a, int64_t sample, int group) {
+// ------------------------------------------------------------------ forward
+// at least zero, or NaN
+__device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
+
+// Means and rstds of the block's groups, from the parts of all chunks and slabs.  About the first part's mean k: n of the
+// N values have it, so n (k - mean)^2 is at most all squared distances, and little is lost to N (k - mean)^2.
+__device__ __forceinline__ void group_stats(const FwdArgs& a, const Place& at, float2* s_stat) {
   const Shape& s = a.s;
-  const int first = group * s.per / s.cols, last = ((group + 1) * s.per - 1) / s.cols;
-  const int lane = threadIdx.x & 31;
-  const float total = (float)s.rows * (float)s.per;
-  float mean = 0.f, m2 = 0.f;
-  for (int turn = 0; turn < 2; ++turn) {
-    float2 sum = make_float2(0.f, 0.f);
+  const int groups = at.g1 - at.g0, lanes = side_by_side(groups), lane = threadIdx.x % lanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
+    const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
+    const float k = a.part[parts_of(s, at.sample, first, g)].x;
+    float s1 = 0.f, s2 = 0.f;
     for (int b = first; b <= last; ++b) {
-      const int wide = min((group + 1) * s.per, (b + 1) * s.cols) - max(group * s.per, b * s.cols);
-      const float2* part = a.part + ((sample * s.slabs + b) * s.span + (group - b * s.cols / s.per)) * s.chunks;
-      for (int c = lane; c < s.chunks; c += 32) {
-        const float n = (float)(min(s.chunk, s.rows - c * s.chunk) * wide);
+      const int wide = min((g + 1) * s.per, (b + 1) * s.cols) - max(g * s.per, b * s.cols);
+      const float2* part = a.part + parts_of(s, at.sample, b, g);
+      const float full = (float)s.chunk * (float)wide, rest = (float)(s.rows - (s.chunks - 1) * s.chunk) * (float)wide;
+#pragma unroll 8
+      for (int c = lane; c < s.chunks; c += lanes) {
+        const float n = c == s.chunks - 1 ? rest : full;
         const float2 p = part[c];
-        if (turn == 0) sum.x = fmaf(n, p.x, sum.x);
-        else sum.x += fmaf(n * (p.x - mean), p.x - mean, p.y);
+        const float d = p.x - k;
+        s1 = fmaf(n, d, s1);
+        s2 += fmaf(n * d, d, p.y);
       }
     }
-    sum = warp_sum(sum);
-    if (turn == 0) mean = sum.x / total;
-    else m2 = sum.x;
-  }
-  return make_float2(mean, 1.f / sqrtf(m2 / total + a.eps));
-}
-
-template <typename T, int VE>
-__global__ void __launch_bounds__(kThreads) k_groupnorm_stats(const FwdArgs a) {
-  follow();
-  using IO = VecIO<T, VE>;
-  constexpr int U = 8;
-  __shared__ float2 s_part[kThreads * VE];
-  const Shape& s = a.s;
-  const Place at(s, blockIdx.x);
-  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
-  const int col = at.col0 + tx * VE;
-  const T* x = static_cast<const T*>(a.x) + col;
-  if (ty < ny && col < s.width) {
-    float pivot[VE], s1[VE], s2[VE];
-    int64_t r = at.row + ty;
-    const int count = r < at.end ? (int)((at.end - r + ny - 1) / ny) : 0;
-    if (count) IO::unpack(IO::load(x + r * a.ldx), pivot);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) s1[e] = s2[e] = 0.f;
-    auto add = [&](const typename IO::Raw& v) {
-      float f[VE];
-      IO::unpack(v, f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float d = f[e] - pivot[e];
-        s1[e] += d;
-        s2[e] = fmaf(d, d, s2[e]);
-      }
-    };
-    int i = 0;
-    for (; i + U <= count; i += U, r += (int64_t)U * ny) {
-      typename IO::Raw v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = IO::load(x + (r + (int64_t)u * ny) * a.ldx);
-#pragma unroll
-      for (int u = 0; u < U; ++u) add(v[u]);
-    }
-    for (; i < count; ++i, r += ny) add(IO::load(x + r * a.ldx));
-    const float inv = count ? 1.f / (float)count : 0.f;
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      s_part[ty * s.tx * VE + tx * VE + e] =
-          count ? make_float2(fmaf(s1[e], inv, pivot[e]), fmaxf(fmaf(-s1[e] * inv, s1[e], s2[e]), 0.f)) : make_float2(0.f, 0.f);
-  }
-  __syncthreads();
-  // the slab's part of each group: all threads' means about their mean
-  const int lane = threadIdx.x & 31, rows = (int)(at.end - at.row);
-  for (int g = at.g0 + (threadIdx.x >> 5); g < at.g1; g += kWarps) {
-    const int c0 = max(g * s.per, at.col0), c1 = min((g + 1) * s.per, at.col1), wide = c1 - c0;
-    float mean = 0.f;
-    for (int turn = 0; turn < 2; ++turn) {
-      float2 sum = make_float2(0.f, 0.f);
-      for (int i = lane; i < wide * ny; i += 32) {
-        const int y = i / wide, c = c0 - at.col0 + i % wide;
-        const float2 p = s_part[y * s.tx * VE + c];
-        const float n = (float)(y < rows ? (rows - y + ny - 1) / ny : 0);
-        if (turn == 0) sum.x = fmaf(n, p.x, sum.x);
-        else sum.x += fmaf(n * (p.x - mean), p.x - mean, p.y);
-      }
-      sum = warp_sum(sum);
-      if (turn == 0) mean = sum.x / ((float)rows * (float)wide);
-      else if (lane == 0)
-        a.part[((at.sample * s.slabs + at.slab) * s.span + (g - at.g0)) * s.chunks + at.chunk] = make_float2(mean, sum.x);
-    }
-  }
-}
-
-template <typename T, int VE, int ACT>
-__global__ void __launch_bounds__(kThreads) k_groupnorm_write(const FwdArgs a) {
-  follow();
-  using IO = VecIO<T, VE>;
-  constexpr int U = 4;
-  __shared__ float2 s_stat[kThreads * VE + 1];  // of the slab's groups
-  const Shape& s = a.s;
-  const Place at(s, gridDim.x - 1 - blockIdx.x);  // the rows that were read last are still in L2
-  for (int g = at.g0 + (threadIdx.x >> 5); g < at.g1; g += kWarps) {
-    const float2 st = group_stats(a, at.sample, g);
-    if ((threadIdx.x & 31) == 0) {
+    s1 = sum_among(s1, lanes), s2 = sum_among(s2, lanes);
+    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) {
+      const float total = (float)s.rows * (float)s.per, off = s1 / total;
+      const float var = not_negative(fmaf(-off, off, s2 / total));
+      const float2 st = make_float2(k + off, 1.f / sqrtf(var + a.eps));
       s_stat[g - at.g0] = st;
       if (at.chunk == 0 && g * s.per >= at.col0) {  // (one block of those that know it)
         if (a.mean) a.mean[at.sample * s.groups + g] = st.x;
@@ -194,204 +258,356 @@ __global__ void __launch_bounds__(kThreads) k_groupnorm_write(const FwdArgs a) {
       }
     }
   }
-  __syncthreads();
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void sum_chunk(const FwdArgs& a, const Place& at) {
+  using IO = VecIO<T, VE>;
+  const Shape& s = a.s;
   const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
-  const int col = at.col0 + tx * VE;
-  if (ty >= ny || col >= s.width) return;
-  float mean[VE], scale[VE], beta[VE];
+  const int col = at.col0 + tx * VE, rows = (int)(at.end - at.row);
+  const bool mine = ty < ny && col < s.width;
+  const int count = mine && ty < rows ? (rows - ty + ny - 1) / ny : 0;
+  const T* x = static_cast<const T*>(a.x) + (at.row + ty) * a.ldx + col;
+  Rows<T, VE, 1> r{{x}, {(int64_t)ny * a.ldx}};
+  r.start(count);
+  using V = Pairs<VE>;
+  float pivot[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) pivot[e] = 0.f;
+  if (count) IO::unpack(IO::load(x), pivot);
+  typename V::E less[V::N], s1[V::N], s2[V::N];
+#pragma unroll
+  for (int i = 0; i < V::N; ++i) {
+    less[i] = mul2(V::of(pivot, i), typename V::E(-1.f));
+    s1[i] = s2[i] = typename V::E(0.f);
+  }
+  r.each([&](const typename IO::Raw (&v)[1]) {
+    float f[VE];
+    IO::unpack(v[0], f);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+      const auto d = add2(V::of(f, i), less[i]);
+      s1[i] = add2(s1[i], d);
+      s2[i] = fma2(d, d, s2[i]);
+    }
+  });
+  __syncthreads();
+  // threads' means and squared distances; then columns', over the rows of threads; then groups', over their columns
+  float2* s_part = reinterpret_cast<float2*>(s_ring);
+  const float inv = count ? 1.f / (float)count : 0.f;
+  if (mine) {
+    float f1[VE], f2[VE];
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) V::get(s1[i], f1, i), V::get(s2[i], f2, i);
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      s_part[(ty * s.tx + tx) * VE + e] =
+          make_float2(fmaf(f1[e], inv, pivot[e]), not_negative(fmaf(-f1[e] * inv, f1[e], f2[e])));
+  }
+  __syncthreads();
+  const int cols = at.col1 - at.col0, lanes = side_by_side(cols), lane = threadIdx.x % lanes;
+  const float by_rows = 1.f / (float)rows, few = (float)(rows / ny);  // rows of a thread; the first `more` have one more
+  const int more = rows % ny;
+  for (int c0 = 0; c0 < cols; c0 += kThreads / lanes) {
+    const int c = c0 + (int)threadIdx.x / lanes, many = c < cols ? ny : 0;
+    float mean = 0.f, m2 = 0.f;
+    for (int y = lane; y < many; y += lanes) mean = fmaf(y < more ? few + 1.f : few, s_part[y * s.tx * VE + c].x, mean);
+    mean = sum_among(mean, lanes) * by_rows;
+    for (int y = lane; y < many; y += lanes) {
+      const float2 p = s_part[y * s.tx * VE + c];
+      m2 += fmaf((y < more ? few + 1.f : few) * (p.x - mean), p.x - mean, p.y);
+    }
+    m2 = sum_among(m2, lanes);
+    // (row 0 of the threads has been read by this column's threads alone)
+    if (lane == 0 && c < cols) s_part[c] = make_float2(mean, m2);
+  }
+  __syncthreads();
+  const int groups = at.g1 - at.g0, glanes = side_by_side(groups), gl = threadIdx.x % glanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / glanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / glanes, groups - 1);
+    const int c0 = max(g * s.per, at.col0) - at.col0, c1 = min((g + 1) * s.per, at.col1) - at.col0;
+    float mean = 0.f, m2 = 0.f;
+    for (int c = c0 + gl; c < c1; c += glanes) mean += s_part[c].x;
+    mean = sum_among(mean, glanes) / (float)(c1 - c0);
+    for (int c = c0 + gl; c < c1; c += glanes) {
+      const float2 p = s_part[c];
+      m2 += fmaf((float)rows * (p.x - mean), p.x - mean, p.y);
+    }
+    m2 = sum_among(m2, glanes);
+    if (gl == 0 && g0 + (int)threadIdx.x / glanes < groups)
+      a.part[parts_of(s, at.sample, at.slab, g) + at.chunk] = make_float2(mean, m2);
+  }
+}
+
+// ONE: a vector's channels are of one group
+template <typename T, int VE, bool ONE, int ACT>
+__device__ __forceinline__ void write_chunk(const FwdArgs& a, const Place& at) {
+  using IO = VecIO<T, VE>;
+  const Shape& s = a.s;
+  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
+  const int col = at.col0 + tx * VE, rows = (int)(at.end - at.row);
+  const int count = ty < ny && col < s.width && ty < rows ? (rows - ty + ny - 1) / ny : 0;
+  Rows<T, VE, 1> r{{static_cast<const T*>(a.x) + (at.row + ty) * a.ldx + col}, {(int64_t)ny * a.ldx}};
+  r.start(count);
+  float2* s_stat = reinterpret_cast<float2*>(s_ring + kRing);
+  group_stats(a, at, s_stat);
+  __syncthreads();
+  if (!count) return;
+  using V = Pairs<VE>;
+  using E = typename V::E;
+  E less[ONE ? 1 : V::N], scale[V::N], beta[V::N];
   {
-    float gamma[VE];
+    float gamma[VE], b[VE], m[VE], q[VE];
     IO::unpack(IO::load(static_cast<const T*>(a.gamma) + col), gamma);
-    IO::unpack(IO::load(static_cast<const T*>(a.beta) + col), beta);
+    IO::unpack(IO::load(static_cast<const T*>(a.beta) + col), b);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float2 st = s_stat[(col + e) / s.per - at.g0];
-      mean[e] = st.x, scale[e] = st.y * gamma[e];
+      const float2 st = s_stat[(ONE ? col : col + e) / s.per - at.g0];
+      m[e] = -st.x, q[e] = st.y * gamma[e];
+    }
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+      if (!ONE || i == 0) less[ONE ? 0 : i] = V::of(m, i);
+      scale[i] = V::of(q, i), beta[i] = V::of(b, i);
     }
   }
-  const T* x = static_cast<const T*>(a.x) + col;
-  T* y = static_cast<T*>(a.y) + col;
-  for (int64_t r0 = at.row + ty; r0 < at.end; r0 += (int64_t)U * ny) {
-    typename IO::Raw v[U];
+  T* y = static_cast<T*>(a.y) + (at.row + ty) * a.ldy + col;
+  const int64_t sy = (int64_t)ny * a.ldy;
+  r.each([&](const typename IO::Raw (&v)[1]) {
+    float f[VE];
+    IO::unpack(v[0], f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + (int64_t)u * ny;
-      v[u] = r < at.end ? IO::load(x + r * a.ldx) : IO::zero();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + (int64_t)u * ny;
-      if (r >= at.end) break;
-      float f[VE];
-      IO::unpack(v[u], f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) f[e] = act_value(fmaf(f[e] - mean[e], scale[e], beta[e]), ACT);
-      IO::store(y + r * a.ldy, f);
-    }
-  }
+    for (int i = 0; i < V::N; ++i)
+      V::get(activate<ACT>(fma2(add2(V::of(f, i), less[ONE ? 0 : i]), scale[i], beta[i])), f, i);
+    IO::store(y, f);
+    y += sy;
+  });
+}
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(kThreads, 4) k_groupnorm_sums(const FwdArgs a) {
+  follow();
+  sum_chunk<T, VE>(a, Place(a.s, blockIdx.x));
+}
+// (backwards: the rows that were read last are still in L2)
+template <typename T, int VE, bool ONE, int ACT>
+__global__ void __launch_bounds__(kThreads, 4) k_groupnorm_write(const FwdArgs a) {
+  follow();
+  write_chunk<T, VE, ONE, ACT>(a, Place(a.s, gridDim.x - 1 - blockIdx.x));
 }
 
 // ------------------------------------------------------------------ backward
-// A thread's channels: h = (x - mean) rstd, z = h gamma + beta.
-template <typename T, int VE>
-struct Channels {
-  float mean[VE], rstd[VE], gamma[VE], beta[VE];
-  __device__ __forceinline__ void load(const BwdArgs& a, const Place& at, int col) {
-    using IO = VecIO<T, VE>;
+// With d = x - mean and q = rstd gamma: z = d q + beta, h = d rstd.
+template <typename T, int VE, bool ONE, int ACT>
+__device__ __forceinline__ void grad_sums(const BwdArgs& a, const Place& at) {
+  using IO = VecIO<T, VE>;
+  const Shape& s = a.s;
+  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
+  const int col = at.col0 + tx * VE, rows = (int)(at.end - at.row);
+  const bool mine = ty < ny && col < s.width;
+  const int count = mine && ty < rows ? (rows - ty + ny - 1) / ny : 0;
+  Rows<T, VE, 2> r{{static_cast<const T*>(a.x) + (at.row + ty) * a.ldx + col, static_cast<const T*>(a.dy) + (at.row + ty) * a.lddy + col},
+                   {(int64_t)ny * a.ldx, (int64_t)ny * a.lddy}};
+  r.start(count);
+  using V = Pairs<VE>;
+  using E = typename V::E;
+  E less[ONE ? 1 : V::N], q[V::N], beta[V::N], sz[V::N], sd[V::N];
+  float rstd[ONE ? 1 : VE];
+  if (mine) {
+    float gamma[VE], b[VE], m[VE];
     IO::unpack(IO::load(static_cast<const T*>(a.gamma) + col), gamma);
-    IO::unpack(IO::load(static_cast<const T*>(a.beta) + col), beta);
+    IO::unpack(IO::load(static_cast<const T*>(a.beta) + col), b);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const int64_t g = at.sample * a.s.groups + (col + e) / a.s.per;
-      mean[e] = a.mean[g], rstd[e] = a.rstd[g];
+      const int64_t g = at.sample * s.groups + (ONE ? col : col + e) / s.per;
+      m[e] = -a.mean[g], rstd[ONE ? 0 : e] = a.rstd[g];
+      gamma[e] *= rstd[ONE ? 0 : e];
+    }
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+      if (!ONE || i == 0) less[ONE ? 0 : i] = V::of(m, i);
+      q[i] = V::of(gamma, i), beta[i] = V::of(b, i);
     }
   }
-};
-
-template <typename T, int VE, int ACT>
-__global__ void __launch_bounds__(kThreads) k_groupnorm_grad_sums(const BwdArgs a) {
-  follow();
-  using IO = VecIO<T, VE>;
-  constexpr int U = 4;
-  __shared__ float2 s_part[kThreads * VE];
-  const Shape& s = a.s;
-  const Place at(s, blockIdx.x);
-  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
-  const int col = at.col0 + tx * VE;
-  if (ty < ny && col < s.width) {
-    Channels<T, VE> ch;
-    ch.load(a, at, col);
-    const T* x = static_cast<const T*>(a.x) + col;
-    const T* dy = static_cast<const T*>(a.dy) + col;
-    float sz[VE], sh[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) sz[e] = sh[e] = 0.f;
-    for (int64_t r0 = at.row + ty; r0 < at.end; r0 += (int64_t)U * ny) {
-      typename IO::Raw vx[U], vd[U];
+  for (int i = 0; i < V::N; ++i) sz[i] = sd[i] = E(0.f);
+  r.each([&](const typename IO::Raw (&v)[2]) {
+    float f[VE], g[VE];
+    IO::unpack(v[0], f);
+    IO::unpack(v[1], g);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t r = r0 + (int64_t)u * ny;
-        vx[u] = r < at.end ? IO::load(x + r * a.ldx) : IO::zero();
-        vd[u] = r < at.end ? IO::load(dy + r * a.lddy) : IO::zero();
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 + (int64_t)u * ny >= at.end) break;
-        float f[VE], d[VE];
-        IO::unpack(vx[u], f);
-        IO::unpack(vd[u], d);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float h = (f[e] - ch.mean[e]) * ch.rstd[e];
-          float dz = d[e];
-          if constexpr (ACT != GS_ACT_NONE) dz *= act_slope(fmaf(h, ch.gamma[e], ch.beta[e]), ACT);
-          sz[e] += dz;
-          sh[e] = fmaf(dz, h, sh[e]);
-        }
-      }
+    for (int i = 0; i < V::N; ++i) {
+      const E d = add2(V::of(f, i), less[ONE ? 0 : i]);
+      E dz = V::of(g, i);
+      if constexpr (ACT != GS_ACT_NONE) dz = mul2(dz, slope_of<ACT>(fma2(d, q[i], beta[i])));
+      sz[i] = add2(sz[i], dz);
+      sd[i] = fma2(dz, d, sd[i]);
     }
+  });
+  __syncthreads();
+  // threads' sums; then columns', over the rows of threads; then groups', of the columns' times gamma
+  float2* s_part = reinterpret_cast<float2*>(s_ring);
+  if (mine) {
+    float fz[VE], fd[VE];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) s_part[ty * s.tx * VE + tx * VE + e] = make_float2(sz[e], sh[e]);
+    for (int i = 0; i < V::N; ++i) V::get(sz[i], fz, i), V::get(sd[i], fd, i);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) s_part[(ty * s.tx + tx) * VE + e] = make_float2(fz[e], fd[e] * rstd[ONE ? 0 : e]);
   }
   __syncthreads();
-  // columns: over the rows of threads; the first row of them keeps the sums, times gamma
-  const int cols = at.col1 - at.col0;
+  const int cols = at.col1 - at.col0, lanes = side_by_side(cols), lane = threadIdx.x % lanes;
   const int64_t part = at.sample * s.chunks + at.chunk;
-  for (int c = threadIdx.x; c < cols; c += kThreads) {
-    float2 t = s_part[c];
-    for (int y = 1; y < ny; ++y) {
+  for (int c0 = 0; c0 < cols; c0 += kThreads / lanes) {
+    const int c = c0 + (int)threadIdx.x / lanes, many = c < cols ? ny : 0;
+    float2 t = make_float2(0.f, 0.f);
+    for (int y = lane; y < many; y += lanes) {
       const float2 p = s_part[y * s.tx * VE + c];
       t.x += p.x, t.y += p.y;
     }
-    if (a.cols) {
-      a.cols[part * s.width + at.col0 + c] = t.x;
-      a.cols[(s.samples * s.chunks + part) * s.width + at.col0 + c] = t.y;
+    t.x = sum_among(t.x, lanes), t.y = sum_among(t.y, lanes);
+    if (lane == 0 && c < cols) {
+      if (a.cols) {
+        a.cols[part * s.width + at.col0 + c] = t.x;
+        a.cols[(s.samples * s.chunks + part) * s.width + at.col0 + c] = t.y;
+      }
+      const float gamma = to_f32<T>(static_cast<const T*>(a.gamma)[at.col0 + c]);
+      s_part[c] = make_float2(t.x * gamma, t.y * gamma);
     }
-    const float gamma = to_f32<T>(static_cast<const T*>(a.gamma)[at.col0 + c]);
-    s_part[c] = make_float2(t.x * gamma, t.y * gamma);
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  for (int g = at.g0 + (threadIdx.x >> 5); g < at.g1; g += kWarps) {
+  const int groups = at.g1 - at.g0, glanes = side_by_side(groups), gl = threadIdx.x % glanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / glanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / glanes, groups - 1);
     const int c0 = max(g * s.per, at.col0) - at.col0, c1 = min((g + 1) * s.per, at.col1) - at.col0;
     float2 t = make_float2(0.f, 0.f);
-    for (int c = c0 + lane; c < c1; c += 32) t.x += s_part[c].x, t.y += s_part[c].y;
-    t = warp_sum(t);
-    if (lane == 0) a.part[((at.sample * s.slabs + at.slab) * s.span + (g - at.g0)) * s.chunks + at.chunk] = t;
+    for (int c = c0 + gl; c < c1; c += glanes) t.x += s_part[c].x, t.y += s_part[c].y;
+    t.x = sum_among(t.x, glanes), t.y = sum_among(t.y, glanes);
+    if (gl == 0 && g0 + (int)threadIdx.x / glanes < groups) a.part[parts_of(s, at.sample, at.slab, g) + at.chunk] = t;
   }
 }
 
-template <typename T, int VE, int ACT>
-__global__ void __launch_bounds__(kThreads) k_groupnorm_grad_write(const BwdArgs a) {
-  follow();
+// dx = dz q - (rstd mean(g) + d rstd^2 mean(g h)) + skip; A = 3: with skip
+template <typename T, int VE, bool ONE, int ACT, int A>
+__device__ __forceinline__ void grad_write(const BwdArgs& a, const Place& at) {
   using IO = VecIO<T, VE>;
-  constexpr int U = 2;
-  __shared__ float2 s_mean[kThreads * VE + 1];  // of g and of g h, by the slab's groups
   const Shape& s = a.s;
-  const Place at(s, gridDim.x - 1 - blockIdx.x);
+  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
+  const int col = at.col0 + tx * VE, rows = (int)(at.end - at.row);
+  const int count = ty < ny && col < s.width && ty < rows ? (rows - ty + ny - 1) / ny : 0;
+  const int64_t row = at.row + ty;
+  Rows<T, VE, A> r;
+  r.at[0] = static_cast<const T*>(a.x) + row * a.ldx + col, r.step[0] = (int64_t)ny * a.ldx;
+  r.at[1] = static_cast<const T*>(a.dy) + row * a.lddy + col, r.step[1] = (int64_t)ny * a.lddy;
+  if constexpr (A == 3) r.at[2] = static_cast<const T*>(a.skip) + row * a.ldskip + col, r.step[2] = (int64_t)ny * a.ldskip;
+  r.start(count);
+  float2* s_mean = reinterpret_cast<float2*>(s_ring + kRing);  // of g and of g h, by the slab's groups
   const float inv = 1.f / ((float)s.rows * (float)s.per);
-  for (int g = at.g0 + (threadIdx.x >> 5); g < at.g1; g += kWarps) {
+  const int groups = at.g1 - at.g0, lanes = side_by_side(groups), lane = threadIdx.x % lanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
     const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
     float2 t = make_float2(0.f, 0.f);
     for (int b = first; b <= last; ++b) {
-      const float2* part = a.part + ((at.sample * s.slabs + b) * s.span + (g - b * s.cols / s.per)) * s.chunks;
-      for (int c = threadIdx.x & 31; c < s.chunks; c += 32) t.x += part[c].x, t.y += part[c].y;
+      const float2* part = a.part + parts_of(s, at.sample, b, g);
+#pragma unroll 8
+      for (int c = lane; c < s.chunks; c += lanes) {
+        const float2 p = part[c];
+        t.x += p.x, t.y += p.y;
+      }
     }
-    t = warp_sum(t);
-    if ((threadIdx.x & 31) == 0) s_mean[g - at.g0] = make_float2(t.x * inv, t.y * inv);
+    t.x = sum_among(t.x, lanes), t.y = sum_among(t.y, lanes);
+    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) s_mean[g - at.g0] = make_float2(t.x * inv, t.y * inv);
   }
   __syncthreads();
-  const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx, ny = kThreads / s.tx;
-  const int col = at.col0 + tx * VE;
-  if (ty >= ny || col >= s.width) return;
-  Channels<T, VE> ch;
-  ch.load(a, at, col);
-  float2 mean[VE];
+  if (!count) return;
+  using V = Pairs<VE>;
+  using E = typename V::E;
+  E less[ONE ? 1 : V::N], c1[ONE ? 1 : V::N], c2[ONE ? 1 : V::N], q[V::N], beta[V::N];
+  {
+    float gamma[VE], b[VE], m[VE], f1[VE], f2[VE];
+    IO::unpack(IO::load(static_cast<const T*>(a.gamma) + col), gamma);
+    IO::unpack(IO::load(static_cast<const T*>(a.beta) + col), b);
 #pragma unroll
-  for (int e = 0; e < VE; ++e) mean[e] = s_mean[(col + e) / s.per - at.g0];
-  const T* x = static_cast<const T*>(a.x) + col;
-  const T* dy = static_cast<const T*>(a.dy) + col;
-  const T* skip = a.skip ? static_cast<const T*>(a.skip) + col : nullptr;
-  T* dx = static_cast<T*>(a.dx) + col;
-  for (int64_t r0 = at.row + ty; r0 < at.end; r0 += (int64_t)U * ny) {
-    typename IO::Raw vx[U], vd[U], vs[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + (int64_t)u * ny;
-      vx[u] = r < at.end ? IO::load(x + r * a.ldx) : IO::zero();
-      vd[u] = r < at.end ? IO::load(dy + r * a.lddy) : IO::zero();
-      vs[u] = r < at.end && skip ? IO::load(skip + r * a.ldskip) : IO::zero();
+    for (int e = 0; e < VE; ++e) {
+      const int group = (ONE ? col : col + e) / s.per;
+      const float rstd = a.rstd[at.sample * s.groups + group];
+      const float2 t = s_mean[group - at.g0];
+      m[e] = -a.mean[at.sample * s.groups + group];
+      f1[e] = -rstd * t.x, f2[e] = -rstd * rstd * t.y;
+      gamma[e] *= rstd;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + (int64_t)u * ny;
-      if (r >= at.end) break;
-      float f[VE], d[VE], k[VE];
-      IO::unpack(vx[u], f);
-      IO::unpack(vd[u], d);
-      IO::unpack(vs[u], k);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float h = (f[e] - ch.mean[e]) * ch.rstd[e];
-        float g = d[e] * ch.gamma[e];
-        if constexpr (ACT != GS_ACT_NONE) g *= act_slope(fmaf(h, ch.gamma[e], ch.beta[e]), ACT);
-        f[e] = fmaf(ch.rstd[e], g - mean[e].x - h * mean[e].y, k[e]);
-      }
-      IO::store(dx + r * a.lddx, f);
+    for (int i = 0; i < V::N; ++i) {
+      if (!ONE || i == 0) less[ONE ? 0 : i] = V::of(m, i), c1[ONE ? 0 : i] = V::of(f1, i), c2[ONE ? 0 : i] = V::of(f2, i);
+      q[i] = V::of(gamma, i), beta[i] = V::of(b, i);
     }
   }
+  T* dx = static_cast<T*>(a.dx) + row * a.lddx + col;
+  const int64_t so = (int64_t)ny * a.lddx;
+  r.each([&](const typename IO::Raw (&v)[A]) {
+    float f[VE], g[VE], k[VE];
+    IO::unpack(v[0], f);
+    IO::unpack(v[1], g);
+    if constexpr (A == 3) IO::unpack(v[2], k);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) {
+      const E d = add2(V::of(f, i), less[ONE ? 0 : i]);
+      E dz = V::of(g, i);
+      if constexpr (ACT != GS_ACT_NONE) dz = mul2(dz, slope_of<ACT>(fma2(d, q[i], beta[i])));
+      E out = fma2(dz, q[i], fma2(d, c2[ONE ? 0 : i], c1[ONE ? 0 : i]));
+      if constexpr (A == 3) out = add2(out, V::of(k, i));
+      V::get(out, f, i);
+    }
+    IO::store(dx, f);
+    dx += so;
+  });
 }
 
-// dbeta, then dgamma, from the chunks' column sums
-template <typename T>
-__global__ void __launch_bounds__(1024) k_groupnorm_fold(const ColumnFold dbeta, const ColumnFold dgamma) {
+// blocks to an SM that the registers allow without spilling
+constexpr int grad_blocks(int ve, bool one) { return ve == 8 ? (one ? 3 : 2) : ve == 1 ? 3 : one ? 4 : 3; }
+template <typename T, int VE, bool ONE, int ACT>
+__global__ void __launch_bounds__(kThreads, grad_blocks(VE, ONE)) k_groupnorm_grad_sums(const BwdArgs a) {
   follow();
-  const int half = gridDim.x / 2;
-  if ((int)blockIdx.x < half) {
-    if (dbeta.out) column_fold<T, 1024>(dbeta, blockIdx.x);
-  } else if (dgamma.out) {
-    column_fold<T, 1024>(dgamma, blockIdx.x - half);
+  grad_sums<T, VE, ONE, ACT>(a, Place(a.s, blockIdx.x));
+}
+template <typename T, int VE, bool ONE, int ACT, int A>
+__global__ void __launch_bounds__(kThreads, grad_blocks(VE, ONE)) k_groupnorm_grad_write(const BwdArgs a) {
+  follow();
+  grad_write<T, VE, ONE, ACT, A>(a, Place(a.s, gridDim.x - 1 - blockIdx.x));
+}
+
+// dbeta and dgamma from the chunks' column sums: a block adds the parts of 8 columns, 128 of them side by side.
+struct SumFold {
+  const float* cols;
+  void* dbeta;
+  void* dgamma;
+  int64_t parts;
+  int width;
+};
+template <typename T>
+__global__ void __launch_bounds__(1024) k_groupnorm_fold(const SumFold a) {
+  follow();
+  __shared__ float s[32][8];
+  void* out = blockIdx.y ? a.dgamma : a.dbeta;
+  if (!out) return;
+  const int c = blockIdx.x * 8 + threadIdx.x % 8;
+  const float* from = a.cols + (blockIdx.y ? a.parts * a.width : 0) + c;
+  float v = 0.f;
+  if (c < a.width) {
+#pragma unroll 8
+    for (int64_t p = threadIdx.x / 8; p < a.parts; p += 128) v += from[p * a.width];
   }
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if ((threadIdx.x & 31) < 8) s[threadIdx.x >> 5][threadIdx.x & 7] = v;
+  __syncthreads();
+  if (threadIdx.x >= 256) return;
+  v = s[threadIdx.x & 31][threadIdx.x >> 5];  // a warp to a column
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if ((threadIdx.x & 31) == 0 && col < a.width) static_cast<T*>(out)[col] = from_f32<T>(v);
 }
 
 __global__ void k_groupnorm_empty(float* mean, float* rstd, int64_t n, float value) {
@@ -403,18 +619,25 @@ __global__ void k_groupnorm_empty(float* mean, float* rstd, int64_t n, float val
 }
 
 // ------------------------------------------------------------------ host
-// Blocks of all maps' chunks that fill the device twice over (152 SMs, 8 blocks each); a chunk's threads take 8 rows at least.
-Shape shape_of(const gs_groupnorm_desc* d, int ve) {
+// Chunks of about 256 KB of input, but as many as the device holds blocks of (152 SMs, 4 each, of the gradient's 3; 4 maps of
+// 3,927 x 200 float32 backward: 21 us with 3, 28 with 4), and of at least 4 rows a thread: a block's beginning and end take some 4 us, which smaller chunks repeat too often (16 maps of 15,965 x 256
+// bfloat16: 71 us with chunks of 215 KB, 93 with 54, 156 with 27), and the SMs do not get equal shares of the memory's rate,
+// which larger ones do not even out (4 images of 1236 x 820 x 64 backward: 404 us with 284 KB, 416 with 1.1 MB).
+constexpr int64_t kChunkBytes = 256 << 10;
+Shape shape_of(const gs_groupnorm_desc* d, int ve, int arrays) {
   Shape s{};
   s.samples = d->samples, s.rows = d->rows, s.width = d->width, s.groups = d->groups, s.per = d->width / d->groups;
   const int vectors = d->width / ve;
   s.tx = vectors < kThreads ? vectors : kThreads;
+  while (s.tx * ve / s.per > 960) s.tx /= 2;  // (their statistics' place beside the ring)
   s.cols = s.tx * ve;
   s.slabs = (d->width + s.cols - 1) / s.cols;
   s.span = std::min(s.groups, s.cols / s.per + 2);
   const int ny = kThreads / s.tx;
-  const int64_t want = std::max<int64_t>(1, 2 * 152 * 8 / (s.samples * s.slabs));
-  s.chunk = std::max<int64_t>((d->rows + want - 1) / want, (int64_t)8 * ny);
+  const double bytes = (double)d->samples * d->rows * d->width * gs::dtype_size(d->dtype) * arrays;
+  const int64_t wave = 152 * (arrays == 1 ? 4 : 3), waves = std::max<int64_t>(1, (int64_t)(bytes / (kChunkBytes * wave) + 0.5));
+  const int64_t want = std::max<int64_t>(1, waves * wave / (s.samples * s.slabs));
+  s.chunk = std::max<int64_t>((d->rows + want - 1) / want, (int64_t)4 * ny);
   s.chunks = (int)((d->rows + s.chunk - 1) / s.chunk);
   return s;
 }
@@ -423,10 +646,10 @@ size_t part_bytes(const Shape& s) {
 }
 // over the vectors that the arrays' alignment may lead to
 template <typename F>
-size_t most_bytes(const gs_groupnorm_desc* d, F f) {
+size_t most_bytes(const gs_groupnorm_desc* d, int arrays, F f) {
   size_t most = 0;
   for (int ve : {1, 2, 4, 8})
-    if (d->width % ve == 0 && ve * gs::dtype_size(d->dtype) <= 16) most = std::max(most, f(shape_of(d, ve)));
+    if (d->width % ve == 0 && ve * gs::dtype_size(d->dtype) <= 16) most = std::max(most, f(shape_of(d, ve, arrays)));
   return most;
 }
 
@@ -456,24 +679,29 @@ int vector_of(int width, int32_t dtype, Aligned at) {
   return dtype == GS_BF16 && width % 2 == 0 && at(4) ? 2 : 1;
 }
 
-// f of an element type, a vector's length and an activation
+// f of an element type, a vector's length, whether its channels are of one group, and an activation
 template <typename F>
 void by_form(const gs_groupnorm_desc* d, int ve, F f) {
-  auto act = [&](auto t, auto v) {
+  auto act = [&](auto t, auto v, auto one) {
     switch (d->act) {
-      case GS_ACT_RELU: return f(t, v, std::integral_constant<int, GS_ACT_RELU>{});
-      case GS_ACT_GELU: return f(t, v, std::integral_constant<int, GS_ACT_GELU>{});
-      case GS_ACT_SILU: return f(t, v, std::integral_constant<int, GS_ACT_SILU>{});
-      default: return f(t, v, std::integral_constant<int, GS_ACT_NONE>{});
+      case GS_ACT_RELU: return f(t, v, one, std::integral_constant<int, GS_ACT_RELU>{});
+      case GS_ACT_GELU: return f(t, v, one, std::integral_constant<int, GS_ACT_GELU>{});
+      case GS_ACT_SILU: return f(t, v, one, std::integral_constant<int, GS_ACT_SILU>{});
+      default: return f(t, v, one, std::integral_constant<int, GS_ACT_NONE>{});
     }
   };
+  auto vector = [&](auto t, auto v) {
+    if constexpr (decltype(v)::value == 1) act(t, v, std::true_type{});
+    else if (d->width / d->groups % decltype(v)::value == 0) act(t, v, std::true_type{});
+    else act(t, v, std::false_type{});
+  };
   if (d->dtype == GS_F32) {
-    if (ve == 4) act(float{}, std::integral_constant<int, 4>{});
-    else act(float{}, std::integral_constant<int, 1>{});
+    if (ve == 4) vector(float{}, std::integral_constant<int, 4>{});
+    else vector(float{}, std::integral_constant<int, 1>{});
   } else {
-    if (ve == 8) act(__nv_bfloat16{}, std::integral_constant<int, 8>{});
-    else if (ve == 2) act(__nv_bfloat16{}, std::integral_constant<int, 2>{});
-    else act(__nv_bfloat16{}, std::integral_constant<int, 1>{});
+    if (ve == 8) vector(__nv_bfloat16{}, std::integral_constant<int, 8>{});
+    else if (ve == 2) vector(__nv_bfloat16{}, std::integral_constant<int, 2>{});
+    else vector(__nv_bfloat16{}, std::integral_constant<int, 1>{});
   }
 }
 
@@ -481,7 +709,7 @@ void by_form(const gs_groupnorm_desc* d, int ve, F f) {
 
 extern "C" size_t gs_groupnorm_fwd_workspace_size(const gs_groupnorm_desc* d) {
   if (check_desc("gs_groupnorm_fwd_workspace_size", d) || d->samples * d->rows == 0) return 0;
-  return most_bytes(d, part_bytes);
+  return most_bytes(d, 1, part_bytes);
 }
 
 extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
@@ -508,20 +736,22 @@ extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x,
     return gs::rows_aligned(x, rows, d->ldx, d->dtype, bytes) && gs::rows_aligned(y, rows, d->ldy, d->dtype, bytes) &&
            gs::rows_aligned(gamma, 1, 0, d->dtype, bytes) && gs::rows_aligned(beta, 1, 0, d->dtype, bytes);
   });
-  const FwdArgs a{shape_of(d, ve), x, gamma, beta, y, mean, rstd, static_cast<float2*>(workspace), d->ldx, d->ldy, d->eps};
-  by_form(d, ve, [&](auto t, auto v, auto act) {
+  const Shape s = shape_of(d, ve, 1);
+  const FwdArgs a{s, x, gamma, beta, y, mean, rstd, static_cast<float2*>(workspace), d->ldx, d->ldy, d->eps};
+  const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
+  const size_t smem = kRing + sizeof(float2) * s.span;
+  by_form(d, ve, [&](auto t, auto v, auto one, auto act) {
     using T = decltype(t);
-    constexpr int VE = decltype(v)::value, ACT = decltype(act)::value;
-    const dim3 grid((unsigned)(a.s.samples * a.s.chunks), a.s.slabs);
-    gs::launch(k_groupnorm_stats<T, VE>, grid, kThreads, 0, st, a);
-    gs::launch(k_groupnorm_write<T, VE, ACT>, grid, kThreads, 0, st, a);
+    constexpr int VE = decltype(v)::value;
+    gs::launch(k_groupnorm_sums<T, VE>, grid, kThreads, smem, st, a);
+    gs::launch(k_groupnorm_write<T, VE, decltype(one)::value, decltype(act)::value>, grid, kThreads, smem, st, a);
   });
   return gs::check_launch(where);
 }
 
 extern "C" size_t gs_groupnorm_bwd_workspace_size(const gs_groupnorm_desc* d) {
   if (check_desc("gs_groupnorm_bwd_workspace_size", d) || d->samples * d->rows == 0) return 0;
-  return most_bytes(d, [&](const Shape& s) {
+  return most_bytes(d, 2, [&](const Shape& s) {
     return part_bytes(s) + sizeof(float) * 2 * (size_t)s.samples * s.chunks * s.width;
   });
 }
@@ -561,20 +791,21 @@ extern "C" gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy
            (!skip || gs::rows_aligned(skip, rows, d->ldskip, d->dtype, bytes)) &&
            (!dx || gs::rows_aligned(dx, rows, d->lddx, d->dtype, bytes));
   });
-  const Shape s = shape_of(d, ve);
+  const Shape s = shape_of(d, ve, 2);
   float* cols = dgamma || dbeta ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(s)) : nullptr;
   const BwdArgs a{s, dy, x, gamma, beta, mean, rstd, skip, dx, static_cast<float2*>(workspace), cols, d->lddy, d->ldx, d->ldskip, d->lddx};
-  const int parts = (int)(s.samples * s.chunks);
-  by_form(d, ve, [&](auto t, auto v, auto act) {
+  const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
+  const size_t smem = kRing + sizeof(float2) * s.span;
+  by_form(d, ve, [&](auto t, auto v, auto one, auto act) {
     using T = decltype(t);
     constexpr int VE = decltype(v)::value, ACT = decltype(act)::value;
-    const dim3 grid((unsigned)parts, s.slabs);
-    gs::launch(k_groupnorm_grad_sums<T, VE, ACT>, grid, kThreads, 0, st, a);
-    if (dx) gs::launch(k_groupnorm_grad_write<T, VE, ACT>, grid, kThreads, 0, st, a);
-    if (cols) {
-      const ColumnFold b{cols, parts, s.width, dbeta}, g{cols + (int64_t)parts * s.width, parts, s.width, dgamma};
-      gs::launch(k_groupnorm_fold<T>, dim3(2 * ((s.width + 31) / 32)), 1024, 0, st, b, g);
-    }
+    constexpr bool ONE = decltype(one)::value;
+    gs::launch(k_groupnorm_grad_sums<T, VE, ONE, ACT>, grid, kThreads, smem, st, a);
+    if (dx && skip) gs::launch(k_groupnorm_grad_write<T, VE, ONE, ACT, 3>, grid, kThreads, smem, st, a);
+    else if (dx) gs::launch(k_groupnorm_grad_write<T, VE, ONE, ACT, 2>, grid, kThreads, smem, st, a);
+    if (cols)
+      gs::launch(k_groupnorm_fold<T>, dim3((s.width + 7) / 8, 2), 1024, 0, st,
+                 SumFold{cols, dbeta, dgamma, s.samples * s.chunks, s.width});
   });
   return gs::check_launch(where);
 }
