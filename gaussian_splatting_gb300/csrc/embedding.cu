@@ -7,13 +7,16 @@
 // holds one vector of a row, four of them in flight.
 //
 // The backward must not add in whatever order atomics come, and one code may have any number of rows, so the rows are
-// first sorted by code: a radix sort of (code, row) pairs, stable, of up to eight bits a pass, each pass three kernels
-// (digit counts of tiles, their scan by digit, a scatter through shared memory).  Then equal parts of the sorted rows go to
-// groups of lanes ("walkers"), which add rows up in registers as long as the code stays the same.  A code whose rows lie
-// inside one walker's part is written at once; the sums at a part's ends are joined in order, first among the walkers of a
-// block in shared memory, then among blocks by a second kernel.  The part's length follows from the sizes alone, so the
-// same call gives the same bits.  Codes without rows are found in a bitmap that the first pass fills and are set to zero by
-// blocks of the summing kernel's launch.
+// first sorted by code, stably, and then added up in equal parts of the sorted rows by groups of lanes ("walkers"), in registers
+// as long as the code stays the same.  A code whose rows lie inside one walker's part is written at once; the sums at a
+// part's ends are joined in order, first among the walkers of a block in shared memory, then among blocks by another kernel.
+// The parts follow from the sizes and the indices alone, so the same call gives the same bits.  Three forms, by size:
+//   few rows     one kernel, whose blocks own runs of codes, pick their rows out of all indices and sort them in shared memory;
+//   more         a radix sort of (code, row) pairs, up to eight bits a pass, each pass three kernels (digit counts of tiles,
+//                their scan by digit, a scatter through shared memory), then the sums;
+//   many         one such pass into up to 2,048 buckets of neighbouring codes; the rest of the sort is done in shared memory by
+//                the blocks that add a bucket up.  11M rows of 32 float32, 2M codes: 402 us against 675 by the sort, of which
+//                the sums take 300 (their bytes at the copy's rate: 258), the pairs' scatter 60, counts and their scan 25.
 #include <algorithm>
 
 #include "dense.cuh"
@@ -22,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPartThreads = 512;  // of the backward's kernels by buckets
 
 // ------------------------------------------------------------------ forward
 struct FwdArgs {
@@ -287,66 +291,151 @@ __device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t code, int c
   VecIO<T, VE>::store(static_cast<T*>(a.dtable) + (int64_t)code * a.ldt + col, f);
 }
 
-constexpr int kBatch = 8;  // rows in flight
-
-// A walker's part [begin, end) of sorted rows, of `total` in all: codes inside it are written, the sums at its ends go to
-// `head` and `tail` (the lane's own VE floats).  Returns the flags; `code` is the last one.  `none`: the key of rows without a
-// code, behind all others; to_code: keys to codes; seen(code): the part has the code's first row.
-// (Parts begin at multiples of kBatch; the arrays are padded to one: what lies behind the last row is not used.)
-template <typename T, int VE, typename Code, typename Seen>
-__device__ __forceinline__ uint32_t walk(const SumArgs& a, const uint32_t* keys, const uint32_t* order, int64_t begin, int64_t end,
-                                         int64_t total, uint32_t none, int col, float* head, float* tail, uint32_t& code,
-                                         Code to_code, Seen seen) {
+constexpr int kBatch = 8;  // a walker's part begins at a multiple of it
+// A walker's rows, a lane's vector of each, by their sorted positions in lists that are padded to kBatch (what lies behind the
+// last row is not used).  A position has a key, or `none` from `end` on; rows with the key `none` read as zeros.
+// Lists in global memory: eight rows at once in registers, and the next eight's keys while these are added up.
+template <typename T, int VE>
+struct ListedRows {
   using IO = VecIO<T, VE>;
-  const T* dy = static_cast<const T*>(a.dy);
+  using Pos = int64_t;
+  static constexpr int B = 8;
+  const uint32_t *keys, *order;
+  const T* dy;  // at the lane's column
+  int64_t ldy, end;
+  uint32_t none;
+  bool there;  // such a column
+  uint32_t next_k[B], next_o[B], k[B];
+  typename IO::Raw v[B];
+  __device__ __forceinline__ void ahead(int64_t p) {
+#pragma unroll
+    for (int h = 0; h < B; h += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + p + h), o = *reinterpret_cast<const uint4*>(order + p + h);
+      next_k[h] = q.x, next_k[h + 1] = q.y, next_k[h + 2] = q.z, next_k[h + 3] = q.w;
+      next_o[h] = o.x, next_o[h + 1] = o.y, next_o[h + 2] = o.z, next_o[h + 3] = o.w;
+    }
+  }
+  __device__ __forceinline__ void start(int64_t p) { ahead(p); }
+  __device__ __forceinline__ void batch(int64_t p) {
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      k[u] = p + u < end ? next_k[u] : none;
+      v[u] = k[u] != none && there ? IO::load(dy + (int64_t)next_o[u] * ldy) : IO::zero();
+    }
+    if (p + B < end) ahead(p + B);
+  }
+  __device__ __forceinline__ uint32_t key(int u) const { return k[u]; }
+  __device__ __forceinline__ typename IO::Raw value(int u) { return v[u]; }
+  __device__ __forceinline__ void done(int) {}
+};
+
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+// Lists in shared memory: four rows are always in flight, through a ring of the thread's own in shared memory, which takes no
+// registers (16 bytes a vector; shorter ones take the registers of a batch of four).
+template <typename T, int VE>
+struct RingRows {
+  using IO = VecIO<T, VE>;
+  using Raw = typename IO::Raw;
+  using Pos = int;
+  static constexpr int B = 4;
+  static constexpr bool kRing = sizeof(Raw) == 16;
+  const uint16_t* keys;
+  const uint32_t* order;
+  const T* dy;
+  int64_t ldy;
+  int end;
+  bool there;
+  Raw* ring;  // [B][threads], at the thread's
+  uint32_t k[B], o[B];
+  Raw v[kRing ? 1 : B];
+  __device__ __forceinline__ void rows_at(int p) {
+    const uint4 q = *reinterpret_cast<const uint4*>(order + p);
+    o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+  }
+  __device__ __forceinline__ void issue(int p, int u) {
+    if (p + u < end && there) copy_async16(ring + u * kPartThreads, dy + (int64_t)o[u] * ldy);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int now;
+  __device__ __forceinline__ void start(int p) {
+    if constexpr (kRing) {
+      rows_at(p);
+#pragma unroll
+      for (int u = 0; u < B; ++u) issue(p, u);
+    }
+  }
+  __device__ __forceinline__ void batch(int p) {
+    const uint2 q = *reinterpret_cast<const uint2*>(keys + p);
+    const uint32_t t[B] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
+#pragma unroll
+    for (int u = 0; u < B; ++u) k[u] = p + u < end ? t[u] : 0xffffu;
+    now = p;
+    if constexpr (kRing) {
+      if (p + B < end) rows_at(p + B);
+    } else {
+      rows_at(p);
+#pragma unroll
+      for (int u = 0; u < B; ++u) v[u] = p + u < end && there ? IO::load(dy + (int64_t)o[u] * ldy) : IO::zero();
+    }
+  }
+  __device__ __forceinline__ uint32_t key(int u) const { return k[u]; }
+  __device__ __forceinline__ Raw value(int u) {
+    if constexpr (kRing) {
+      asm volatile("cp.async.wait_group 3;" ::: "memory");
+      return now + u < end && there ? ring[u * kPartThreads] : IO::zero();
+    } else {
+      return v[u];
+    }
+  }
+  __device__ __forceinline__ void done(int u) {
+    if constexpr (kRing) issue(now + B, u);
+  }
+};
+
+// A walker's part [begin, end) of sorted rows, of `total` in all: codes inside it are summed up and put(code, sums), the
+// sums at its ends go to `head` and `tail` (the lane's own VE floats).  Returns the flags; `code` is the last one.  `none`:
+// the key of rows without a code, behind all others; seen(code): the part has the code's first row.
+template <typename T, int VE, typename R, typename Key, typename Put, typename Seen>
+__device__ __forceinline__ uint32_t walk(R& rows, const Key* keys, typename R::Pos begin, typename R::Pos total, uint32_t none,
+                                         float* head, float* tail, uint32_t& code, Put put, Seen seen) {
+  using IO = VecIO<T, VE>;
+  const typename R::Pos end = rows.end;
   float acc[VE];
 #pragma unroll
   for (int e = 0; e < VE; ++e) acc[e] = 0.f;
   uint32_t flag = 0;
   code = none;
   if (begin >= end) return 0;
-  uint4 k4[2], o4[2];
-  auto load = [&](int64_t p) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      k4[h] = *reinterpret_cast<const uint4*>(keys + p + 4 * h);
-      o4[h] = *reinterpret_cast<const uint4*>(order + p + 4 * h);
-    }
-  };
-  load(begin);
-  code = k4[0].x;
+  rows.start(begin);
+  code = keys[begin];
   bool from_before = begin > 0 && code != none && keys[begin - 1] == code;
   if (!from_before && code != none) seen(code);
-  for (int64_t p = begin; p < end; p += kBatch) {
-    uint32_t k[kBatch] = {k4[0].x, k4[0].y, k4[0].z, k4[0].w, k4[1].x, k4[1].y, k4[1].z, k4[1].w};
-    const uint32_t o[kBatch] = {o4[0].x, o4[0].y, o4[0].z, o4[0].w, o4[1].x, o4[1].y, o4[1].z, o4[1].w};
-    typename IO::Raw v[kBatch];
+  for (typename R::Pos p = begin; p < end; p += R::B) {
+    rows.batch(p);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (p + u >= end) k[u] = none;
-      v[u] = k[u] != none && col < a.width ? IO::load(dy + (int64_t)o[u] * a.ldy + col) : IO::zero();
-    }
-    if (p + kBatch < end) load(p + kBatch);  // in flight while these rows are added
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (p + u < end && k[u] != code) {  // the sum of `code` is complete here
+    for (int u = 0; u < R::B; ++u) {
+      const uint32_t k = rows.key(u);
+      if (p + u < end && k != code) {  // the sum of `code` is complete here
         if (from_before) {
 #pragma unroll
           for (int e = 0; e < VE; ++e) head[e] = acc[e];
           flag |= kHead;
           from_before = false;
         } else {
-          write_sum<T, VE>(a, to_code(code), col, acc);
+          put(code, acc);
         }
-        code = k[u];
+        code = k;
         if (code != none) seen(code);
 #pragma unroll
         for (int e = 0; e < VE; ++e) acc[e] = 0.f;
       }
       float f[VE];
-      IO::unpack(v[u], f);
+      IO::unpack(rows.value(u), f);
 #pragma unroll
       for (int e = 0; e < VE; ++e) acc[e] += f[e];
+      rows.done(u);
     }
   }
   if (code != none) {
@@ -357,7 +446,7 @@ __device__ __forceinline__ uint32_t walk(const SumArgs& a, const uint32_t* keys,
       for (int e = 0; e < VE; ++e) to[e] = acc[e];
       flag |= from_before ? (goes_on ? kHead | kThrough : kHead) : kTail;
     } else {
-      write_sum<T, VE>(a, to_code(code), col, acc);
+      put(code, acc);
     }
   }
   return flag;
@@ -378,9 +467,10 @@ __device__ __forceinline__ bool join(const float* from, const float* heads, cons
   return open;
 }
 
+constexpr int sum_blocks(int ve) { return ve == 8 ? 2 : 3; }  // of an SM, by the registers
 // G lanes to a walker, a vector each; gridDim.y slabs of columns.
 template <typename T, int VE, int G>
-__global__ void __launch_bounds__(kThreads, VE == 8 ? 2 : 3) k_embedding_sum(const SumArgs a) {
+__global__ void __launch_bounds__(kThreads, sum_blocks(VE)) k_embedding_sum(const SumArgs a) {
   follow();
   constexpr int kWalkers = kThreads / G;
   __shared__ float s_end[2][kThreads * VE];  // heads and tails
@@ -392,8 +482,12 @@ __global__ void __launch_bounds__(kThreads, VE == 8 ? 2 : 3) k_embedding_sum(con
   float *head = s_end[0] + threadIdx.x * VE, *tail = s_end[1] + threadIdx.x * VE;
   uint32_t code, word = 0, bits = 0;  // codes seen, gathered to words of the bitmap
   const bool tells = lane == 0 && blockIdx.y == 0;
+  ListedRows<T, VE> list;
+  list.keys = a.keys, list.order = a.order, list.dy = static_cast<const T*>(a.dy) + col, list.ldy = a.ldy, list.end = end;
+  list.none = (uint32_t)a.n, list.there = col < a.width;
   const uint32_t flag = walk<T, VE>(
-      a, a.keys, a.order, begin, end, a.rows, (uint32_t)a.n, col, head, tail, code, [](uint32_t c) { return c; },
+      list, a.keys, begin, a.rows, (uint32_t)a.n, head, tail, code,
+      [&](uint32_t c, const float* sum) { write_sum<T, VE>(a, c, col, sum); },
       [&](uint32_t c) {
         if (c >> 5 != word) {
           if (tells && bits) atomicOr(a.bitmap + word, bits);
@@ -493,6 +587,375 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const SumArgs a) {
     for (int e = 0; e < VE; ++e) acc[e] += s[(w * G + lane) * VE + e];
   }
   write_sum<T, VE>(a, a.tail_code[blockIdx.x], col, acc);
+}
+
+// ------------------------------------------------------------------ backward: buckets
+// One pass of a sort puts (code, row) pairs into up to 2,048 buckets of 2^shift neighbouring codes each, in the order of the
+// rows.  A block of the second step takes a bucket, or a part of `cap` rows of one that has more, sorts it in shared memory
+// and sums it up as above.  Whole buckets are written at once, zeros included; the sums of parts go to the workspace, for a
+// third step that joins them in order.
+constexpr int kPartWarps = kPartThreads / 32, kPartItems = 16;  // pairs of a thread in a tile
+constexpr int kMostBuckets = 2048, kMostCodes = 2048;  // a thread has four of either
+constexpr int kMostRows = 6144;                        // of a part
+struct Part {
+  uint32_t bucket, begin, end, slot;  // its pairs; where the sums go, or kWhole
+};
+struct Bucket {  // of several parts
+  uint32_t bucket, slot, parts, unused;
+};
+constexpr uint32_t kWhole = 0xffffffffu;
+struct PartArgs {
+  SumArgs s;
+  uint2* pairs;        // codes and rows
+  uint32_t* counts;    // [tiles][padded buckets]
+  uint32_t* totals;    // of the buckets
+  Part* parts;
+  Bucket* many;        // buckets of several parts
+  uint32_t* numbers;   // of parts and of those buckets
+  float* sums;         // [parts of those][codes][ldp]
+  uint32_t* seen;      // [parts of those][words]: codes that have rows
+  int tiles, buckets, padded, shift, codes, cap;
+};
+
+// How many pairs with the same digit the warp had before, in its row of counters: what an atomic addition returns, unless
+// lanes share a digit, whose order is then that of the lanes.  (Votes on each bit of the digit, 50 instructions, took 88 us
+// for the scatter of 11M rows into 1,954 buckets.)
+__device__ __forceinline__ uint32_t rank_of(uint16_t* counters, uint32_t digit, bool in) {
+  const int shift = digit % 2 * 16;
+  uint32_t rank = 0, now = 0;
+  if (in) rank = atomicAdd(reinterpret_cast<uint32_t*>(counters) + digit / 2, 1u << shift) >> shift & 0xffffu;
+  __syncwarp();
+  if (in) now = *reinterpret_cast<volatile uint16_t*>(counters + digit);
+  uint32_t left = __ballot_sync(0xffffffffu, in && rank + 1 != now);  // a lane at least of each shared digit
+  while (left) {
+    const uint32_t d = __shfl_sync(0xffffffffu, digit, __ffs(left) - 1);
+    const uint32_t same = __ballot_sync(0xffffffffu, in && digit == d);
+    if (in && digit == d) rank = now - __popc(same) + __popc(same & ((1u << (threadIdx.x & 31)) - 1));
+    left &= ~same;
+  }
+  __syncwarp();
+  return rank;
+}
+// The warps' counters of the thread's four digits, from counts to how many the warps before have; `total`: of the four.
+__device__ __forceinline__ uint4 four_totals(uint16_t* counters, int digits) {
+  uint2 sum = make_uint2(0u, 0u);
+  if ((int)threadIdx.x * 4 < digits) {
+#pragma unroll
+    for (int w = 0; w < kPartWarps; ++w) {
+      uint2* p = reinterpret_cast<uint2*>(counters + w * digits) + threadIdx.x;
+      const uint2 v = *p;
+      *p = sum;
+      sum.x += v.x, sum.y += v.y;  // (no sum passes 16 bits)
+    }
+  }
+  return make_uint4(sum.x & 0xffffu, sum.x >> 16, sum.y & 0xffffu, sum.y >> 16);
+}
+__device__ __forceinline__ uint4 four_starts(uint4 t, uint32_t* s_sums, uint32_t& total) {
+  const uint32_t b = block_scan<kPartThreads>(t.x + t.y + t.z + t.w, s_sums, total);
+  return make_uint4(b, b + t.x, b + t.x + t.y, b + t.x + t.y + t.z);
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kPartThreads) k_embedding_bucket_count(const PartArgs a) {
+  follow();
+  __shared__ uint32_t s[kMostBuckets];
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < a.padded; i += kPartThreads) s[i] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * (kPartThreads * kPartItems) + (threadIdx.x >> 5) * (32 * kPartItems) + lane;
+  uint32_t key[kPartItems];
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i)
+    key[i] = base + i * 32 < a.s.rows ? code_of<I>(a.s.idx, base + i * 32, a.s.n) : (uint32_t)a.s.n;
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i) {
+    const bool in = key[i] < (uint32_t)a.s.n;
+    const uint32_t d = in ? key[i] >> a.shift : kMostBuckets;
+    int alike;  // a common bucket would be added to 32 times one after the other
+    __match_all_sync(0xffffffffu, d, &alike);
+    if (alike) {
+      if (in && lane == 0) atomicAdd(s + d, 32u);
+    } else if (in) {
+      atomicAdd(s + d, 1u);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.padded; i += kPartThreads) a.counts[(int64_t)blockIdx.x * a.padded + i] = s[i];
+}
+
+// Exclusive sums of the counts over the tiles: a block has 8 buckets, 128 runs of 8 tiles side by side.
+__global__ void __launch_bounds__(1024) k_embedding_bucket_scan(const PartArgs a) {
+  follow();
+  constexpr int kRun = 8;
+  __shared__ uint32_t s[2][32][8];
+  const int d = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bucket = blockIdx.x * 8 + d;
+  uint32_t* c = a.counts + bucket;
+  const int tiles = bucket < a.padded ? a.tiles : 0;
+  uint32_t carry = 0;
+  for (int r0 = 0, half = 0; r0 < a.tiles; r0 += 128 * kRun, half ^= 1) {
+    const int t0 = r0 + (threadIdx.x >> 3) * kRun;
+    uint32_t v[kRun], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) v[i] = t0 + i < tiles ? c[(int64_t)(t0 + i) * a.padded] : 0u;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) sum += v[i];
+    uint32_t x = sum;  // inclusive over the warp's four runs
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane >= 24) s[half][warp][d] = x;
+    __syncthreads();
+    uint32_t before = carry + x - sum;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+      const uint32_t y = s[half][w][d];
+      before += w < warp ? y : 0u;
+      carry += y;
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (t0 + i < tiles) c[(int64_t)(t0 + i) * a.padded] = before;
+      before += v[i];
+    }
+  }
+  if (threadIdx.x < 8 && tiles) a.totals[bucket] = carry;
+}
+
+// The list of parts, for the next step: of the thread's four buckets' sizes and beginnings.
+__device__ __forceinline__ void list_parts(const PartArgs& a, uint4 sizes, uint4 first, uint32_t* s_sums) {
+  const uint32_t size[4] = {sizes.x, sizes.y, sizes.z, sizes.w}, from[4] = {first.x, first.y, first.z, first.w};
+  uint32_t parts[4], all = 0, several = 0, buckets = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    parts[j] = (int)threadIdx.x * 4 + j >= a.buckets ? 0u : size[j] <= (uint32_t)a.cap ? 1u : (size[j] - 1) / (uint32_t)a.cap + 1;
+    all += parts[j];
+    if (parts[j] > 1) several += parts[j], ++buckets;
+  }
+  uint32_t sum_all, sum_several, sum_buckets;
+  uint32_t to = block_scan<kPartThreads>(all, s_sums, sum_all), slot = block_scan<kPartThreads>(several, s_sums, sum_several),
+           list = block_scan<kPartThreads>(buckets, s_sums, sum_buckets);
+  if (threadIdx.x == 0) a.numbers[0] = sum_all, a.numbers[1] = sum_buckets;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t d = threadIdx.x * 4 + j, n = parts[j];
+    if (n > 1) a.many[list++] = Bucket{d, slot, n, 0u};
+    const uint32_t rows = n ? (size[j] + n - 1) / n : 0u;
+    for (uint32_t p = 0; p < n; ++p)
+      a.parts[to++] = Part{d, from[j] + min(p * rows, size[j]), from[j] + min((p + 1) * rows, size[j]), n > 1 ? slot++ : kWhole};
+  }
+}
+
+size_t scatter_bytes(int padded) {
+  return std::max<size_t>((size_t)2 * kPartWarps * padded, (size_t)8 * kPartThreads * kPartItems) + (size_t)8 * padded;
+}
+template <typename I>
+__global__ void __launch_bounds__(kPartThreads, 2) k_embedding_bucket_scatter(const PartArgs a) {
+  follow();
+  extern __shared__ __align__(16) uint32_t s_dyn[];
+  __shared__ uint32_t s_sums[kPartWarps];
+  uint32_t *s_start = s_dyn, *s_out = s_dyn + a.padded;  // where a bucket's run begins in the tile; in the pairs, less s_start
+  uint16_t* counters = reinterpret_cast<uint16_t*>(s_dyn + 2 * a.padded);  // [warps][padded]
+  uint2* s_pair = reinterpret_cast<uint2*>(counters);                      // and, once they have been read, the tile's pairs
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kPartWarps * a.padded / 8; i += kPartThreads) reinterpret_cast<uint4*>(counters)[i] = uint4{};
+  const int64_t base = (int64_t)blockIdx.x * (kPartThreads * kPartItems) + warp * (32 * kPartItems) + lane;
+  uint32_t key[kPartItems], at[kPartItems / 2];  // (16 bits are enough for a place in the tile)
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i)
+    key[i] = base + i * 32 < a.s.rows ? code_of<I>(a.s.idx, base + i * 32, a.s.n) : (uint32_t)a.s.n;
+  uint4 in_all = make_uint4(0u, 0u, 0u, 0u), before = in_all;
+  if ((int)threadIdx.x * 4 < a.padded) {
+    in_all = reinterpret_cast<const uint4*>(a.totals)[threadIdx.x];
+    if ((int)blockIdx.x < a.tiles) before = reinterpret_cast<const uint4*>(a.counts + (int64_t)blockIdx.x * a.padded)[threadIdx.x];
+  }
+  uint32_t total;
+  const uint4 first = four_starts(in_all, s_sums, total);  // (its barriers also end the clearing above)
+  if ((int)blockIdx.x == a.tiles) return list_parts(a, in_all, first, s_sums);
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i) {
+    const uint32_t rank = rank_of(counters + warp * a.padded, key[i] >> a.shift, key[i] < (uint32_t)a.s.n);
+    at[i / 2] = i % 2 ? at[i / 2] | rank << 16 : rank;
+  }
+  __syncthreads();
+  const uint4 start = four_starts(four_totals(counters, a.padded), s_sums, total);
+  if ((int)threadIdx.x * 4 < a.padded) {
+    reinterpret_cast<uint4*>(s_start)[threadIdx.x] = start;
+    reinterpret_cast<uint4*>(s_out)[threadIdx.x] = make_uint4(first.x + before.x - start.x, first.y + before.y - start.y,
+                                                              first.z + before.z - start.z, first.w + before.w - start.w);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i) {
+    const uint32_t d = key[i] >> a.shift;
+    if (key[i] < (uint32_t)a.s.n) at[i / 2] += (s_start[d] + counters[warp * a.padded + d]) << (i % 2 * 16);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i)
+    if (key[i] < (uint32_t)a.s.n) s_pair[at[i / 2] >> (i % 2 * 16) & 0xffffu] = make_uint2(key[i], (uint32_t)(base + i * 32));
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < total; i += kPartThreads) {
+    const uint2 p = s_pair[i];
+    a.pairs[s_out[p.x >> a.shift] + i] = p;
+  }
+}
+
+// Shared memory of a block that sums a part up: where the codes' rows begin; the warps' counters and, once they have been
+// read, the sorted codes and rows and the walkers' ends.
+size_t part_bytes(int cap, int codes, int ve) {
+  const size_t digits = std::max(codes, 4), list = cap + 8;
+  const size_t ring = 4 * 16 * kPartThreads;  // (not used where vectors are shorter)
+  return 4 * (digits + 4) + std::max(2 * kPartWarps * digits, 6 * list + 4 * kPartThreads * (2 * (size_t)ve + 1) + ring);
+}
+template <typename T, int VE>
+__global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartArgs p, const int g) {
+  follow();
+  if (blockIdx.x >= p.numbers[0]) return;
+  extern __shared__ __align__(16) uint32_t s_dyn[];
+  __shared__ uint32_t s_sums[kPartWarps];
+  const SumArgs& a = p.s;
+  const Part part = p.parts[blockIdx.x];
+  const int m = (int)(part.end - part.begin), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int digits = max(p.codes, 4), list = p.cap + 8;
+  uint32_t* s_start = s_dyn;
+  uint16_t* counters = reinterpret_cast<uint16_t*>(s_dyn + digits + 4);
+  uint32_t* s_row = s_dyn + digits + 4;
+  float* ends = reinterpret_cast<float*>(s_row + list);  // [2][threads VE]
+  using Raw = typename VecIO<T, VE>::Raw;
+  Raw* ring = reinterpret_cast<Raw*>(ends + 2 * kPartThreads * VE);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(ends + 2 * kPartThreads * VE) + 16 * kPartThreads;
+  uint16_t* s_key = reinterpret_cast<uint16_t*>(flags + kPartThreads);
+  for (int i = threadIdx.x; i < kPartWarps * digits / 8; i += kPartThreads) reinterpret_cast<uint4*>(counters)[i] = uint4{};
+  constexpr int kItems = kMostRows / kPartThreads;
+  const int share = (m + kPartThreads - 1) / kPartThreads * 32, i0 = warp * share + lane;  // a warp's pairs
+  uint32_t key[kItems], row[kItems];  // local codes, their ranks above them
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    key[i] = 0u, row[i] = 0u;
+    if (i * 32 < share && i0 + i * 32 < m) {
+      const uint2 v = p.pairs[part.begin + i0 + i * 32];
+      key[i] = v.x & (uint32_t)(p.codes - 1), row[i] = v.y;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (i * 32 < share) key[i] |= rank_of(counters + warp * digits, key[i], i0 + i * 32 < m) << 16;
+  __syncthreads();
+  uint32_t total;
+  const uint4 start = four_starts(four_totals(counters, digits), s_sums, total);
+  if ((int)threadIdx.x * 4 < digits) reinterpret_cast<uint4*>(s_start)[threadIdx.x] = start;
+  if (threadIdx.x == 0) s_start[digits] = (uint32_t)m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (i * 32 < share && i0 + i * 32 < m) {
+      const uint32_t k = key[i] & 0xffffu;
+      key[i] += (s_start[k] + counters[warp * digits + k]) << 16;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (i * 32 < share && i0 + i * 32 < m) {
+      const uint32_t to = key[i] >> 16;
+      s_key[to] = (uint16_t)key[i], s_row[to] = row[i];
+    }
+  __syncthreads();
+  // the sums
+  const bool whole = part.slot == kWhole;
+  const int64_t code0 = (int64_t)part.bucket << p.shift;
+  const int walkers = kPartThreads / g, wl = threadIdx.x % g, walker = threadIdx.x / g;
+  const int col = ((int)blockIdx.y * g + wl) * VE;
+  const int per = (m + walkers * kBatch - 1) / (walkers * kBatch) * kBatch;
+  const int begin = min(walker * per, m), end = min(begin + per, m);
+  float *head = ends + threadIdx.x * VE, *tail = ends + (kPartThreads + threadIdx.x) * VE;
+  float* to = p.sums + (whole ? (int64_t)0 : (int64_t)part.slot * p.codes * a.ldp) + col;
+  auto put = [&](uint32_t c, const float* sum) {
+    if (whole) {
+      write_sum<T, VE>(a, (uint32_t)code0 + c, col, sum);
+    } else if (col < a.width) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) to[(int64_t)c * a.ldp + e] = sum[e];
+    }
+  };
+  uint32_t code;
+  RingRows<T, VE> rows;
+  rows.keys = s_key, rows.order = s_row, rows.dy = static_cast<const T*>(a.dy) + col, rows.ldy = a.ldy, rows.end = end;
+  rows.there = col < a.width, rows.ring = ring + threadIdx.x;
+  const uint32_t flag = walk<T, VE>(rows, s_key, begin, m, 0xffffu, head, tail, code, put, [](uint32_t) {});
+  if (wl == 0) flags[walker] = flag;
+  // codes without rows
+  const int words = (p.codes + 31) / 32;
+  for (int w = warp; w < words; w += kPartWarps) {
+    const int c = w * 32 + lane;
+    const bool there = c < p.codes && code0 + c < a.n;
+    const uint32_t have = __ballot_sync(0xffffffffu, there && s_start[min(c, digits - 1)] != s_start[min(c, digits - 1) + 1]);
+    if (whole) {
+      const uint32_t empty = __ballot_sync(0xffffffffu, there) & ~have;
+      if (empty) write_zeros<T, VE>(a, empty, code0 + w * 32, g, blockIdx.y);
+    } else if (lane == 0 && blockIdx.y == 0) {
+      p.seen[(int64_t)part.slot * words + w] = have;
+    }
+  }
+  __syncthreads();
+  if (flag & kTail) {
+    float acc[VE];
+    join<VE>(tail, ends, flags, true, walker, walkers, g, wl, acc);
+    put(code, acc);
+  }
+}
+
+// The buckets of several parts: their parts' sums in order, every `per`-th to a walker.
+template <typename T, int VE>
+__global__ void __launch_bounds__(kThreads) k_embedding_part_join(const PartArgs p, const int g) {
+  follow();
+  __shared__ float s[kThreads * VE];
+  const SumArgs& a = p.s;
+  const int walkers = kThreads / g, wl = threadIdx.x % g, walker = threadIdx.x / g;
+  const int col = ((int)blockIdx.y * g + wl) * VE;
+  const int per = max(walkers / p.codes, 1), codes = walkers / per, sub = walker % per;  // (powers of two)
+  const int runs = (p.codes + codes - 1) / codes, words = (p.codes + 31) / 32;
+  const uint32_t items = p.numbers[1] * (uint32_t)runs;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const Bucket b = p.many[item / runs];
+    const int c = (int)(item % runs) * codes + walker / per;
+    const int64_t code = ((int64_t)b.bucket << p.shift) + c;
+    const bool there = c < p.codes && code < a.n && col < a.width;
+    float acc[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+    const uint32_t* seen = p.seen + (int64_t)b.slot * words + (c >> 5);
+    const float* from = p.sums + ((int64_t)b.slot * p.codes + c) * a.ldp + col;
+    for (uint32_t q0 = sub; there && q0 < b.parts; q0 += 4 * per) {
+      uint32_t have[4];
+      float v[4][VE];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) have[u] = q0 + u * per < b.parts ? (seen[(int64_t)(q0 + u * per) * words] >> (c & 31)) & 1u : 0u;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v[u][e] = have[u] ? from[(int64_t)(q0 + u * per) * p.codes * a.ldp + e] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] += v[u][e];
+      }
+    }
+    if (per > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s[threadIdx.x * VE + e] = acc[e];
+      __syncthreads();
+      for (int w = 1; w < per && sub == 0; ++w) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] += s[(threadIdx.x + w * g) * VE + e];
+      }
+    }
+    if (there && sub == 0) write_sum<T, VE>(a, (uint32_t)code, col, acc);
+  }
 }
 
 // ------------------------------------------------------------------ backward: few rows
@@ -616,7 +1079,12 @@ __global__ void __launch_bounds__(kFewThreads) k_embedding_few(const FewArgs f) 
   const int begin = min(walker * per, (int)m), end = min(begin + per, (int)m);
   float *head = ends + threadIdx.x * VE, *tail = ends + (kFewThreads + threadIdx.x) * VE;
   uint32_t code;
-  const uint32_t flag = walk<T, VE>(a, key[from], row[from], begin, end, m, none, col, head, tail, code, to_code, [](uint32_t) {});
+  ListedRows<T, VE> rows_of;
+  rows_of.keys = key[from], rows_of.order = row[from], rows_of.dy = static_cast<const T*>(a.dy) + col, rows_of.ldy = a.ldy;
+  rows_of.end = end, rows_of.none = none, rows_of.there = col < a.width;
+  const uint32_t flag = walk<T, VE>(
+      rows_of, key[from], begin, m, none, head, tail, code,
+      [&](uint32_t c, const float* sum) { write_sum<T, VE>(a, to_code(c), col, sum); }, [](uint32_t) {});
   if (wl == 0) flags[walker] = flag;
   __syncthreads();
   if (flag & kTail) {
@@ -697,11 +1165,11 @@ Plan plan_of(const gs_embedding_desc* d) {
   p.ldp = (d->width + 7) / 8 * 8;
   return p;
 }
-// Rows of a walker: whole batches, blocks for 8 times what the device holds (152 SMs, 3 blocks each), or for once where
-// a walker would have few.
-constexpr int64_t kBlocks = 152 * 3;
-int per_walker_of(int64_t rows, int walkers) {
-  int64_t want = (rows + kBlocks * walkers - 1) / (kBlocks * walkers);
+// Rows of a walker: whole batches, blocks for 8 times what the device holds (152 SMs), or for once where a walker would have
+// few.
+int per_walker_of(int64_t rows, int walkers, int ve) {
+  const int64_t blocks = 152 * sum_blocks(ve);
+  int64_t want = (rows + blocks * walkers - 1) / (blocks * walkers);
   if (want > 64) want = std::max<int64_t>(64, want / 8);
   return (int)((want + kBatch - 1) / kBatch * kBatch);
 }
@@ -709,10 +1177,58 @@ int lanes_of(int width, int ve) {
   const int v = (width + ve - 1) / ve;
   return v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : 32;
 }
-int64_t blocks_of(int64_t rows, int g) {
+int64_t blocks_of(int64_t rows, int g, int ve) {
   const int walkers = kThreads / g;
-  const int64_t per = (int64_t)per_walker_of(rows, walkers) * walkers;
+  const int64_t per = (int64_t)per_walker_of(rows, walkers, ve) * walkers;
   return (rows + per - 1) / per;
+}
+
+struct Buckets {
+  int shift, count, padded, codes, cap, tiles;
+  int64_t parts, several, many, words;  // at most: parts, those of buckets with more than one, such buckets; of a part's codes
+};
+// Whether the buckets take a call, and how.  They save passes over the pairs, but the sort's shorter kernels are done sooner
+// where there is little to sort.  Us by the sort and by buckets: 4,096 codes of 64 bfloat16 1M rows 59 and 66, 2M 107 and 95,
+// 10M 459 and 358; 1M codes of 32 float32 500K rows 65 and 78, 1M 103 and 104, 10M 579 and 437; 300K codes of 32 float32 1M rows
+// 90 and 64; codes that the sort does in one pass (100 of 32 float32) 2M rows 91 and 101, 10M 376 and 390.
+bool buckets_take(const gs_embedding_desc* d, Buckets& b) {
+  if (d->n <= 256 || d->n > (int64_t)kMostBuckets * kMostCodes || d->rows < (d->n < 65536 ? 3 << 19 : 1 << 20)) return false;
+  // parts of up to 6,144 rows, or fewer, so that there are 608 of them (152 SMs, 2 blocks each, twice)
+  b.cap = (int)std::min<int64_t>((d->rows / 608 + 511) / 512 * 512, kMostRows);
+  // codes to a bucket so that an average one is nearly a part
+  b.shift = 0;
+  while (b.shift < 11 && (d->rows << (b.shift + 1)) / d->n <= b.cap * 15 / 16) ++b.shift;
+  while ((d->n - 1) >> b.shift >= kMostBuckets) ++b.shift;
+  b.count = (int)((d->n - 1) >> b.shift) + 1, b.padded = (b.count + 3) / 4 * 4, b.codes = 1 << b.shift;
+  b.tiles = (int)((d->rows + kPartThreads * kPartItems - 1) / (kPartThreads * kPartItems));
+  b.many = d->rows / b.cap, b.parts = b.count + b.many, b.several = 2 * b.many;
+  b.words = (b.codes + 31) / 32;
+  return true;
+}
+size_t carve(PartArgs* a, char* base, const gs_embedding_desc* d, const Buckets& b) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* q = base + at;
+    at += (bytes + 255) / 256 * 256;
+    return q;
+  };
+  PartArgs t{};
+  const int64_t ldp = (d->width + 7) / 8 * 8;
+  t.pairs = (uint2*)take(8 * (size_t)d->rows);
+  t.counts = (uint32_t*)take(4 * (size_t)b.tiles * b.padded);
+  t.totals = (uint32_t*)take(4 * (size_t)b.padded);
+  t.parts = (Part*)take(sizeof(Part) * (size_t)b.parts);
+  t.many = (Bucket*)take(sizeof(Bucket) * (size_t)b.many);
+  t.numbers = (uint32_t*)take(8);
+  t.sums = (float*)take(4 * (size_t)b.several * b.codes * ldp);
+  t.seen = (uint32_t*)take(4 * (size_t)b.several * b.words);
+  if (a) {
+    t.s = a->s;
+    t.s.ldp = ldp;
+    t.tiles = b.tiles, t.buckets = b.count, t.padded = b.padded, t.shift = b.shift, t.codes = b.codes, t.cap = b.cap;
+    *a = t;
+  }
+  return at;
 }
 
 struct Space {
@@ -722,7 +1238,7 @@ struct Space {
 size_t carve(Space* s, char* base, const gs_embedding_desc* d) {
   const Plan p = plan_of(d);
   int64_t blocks = 0;  // the most that any vector leads to
-  for (int ve : {1, 2, 4, 8}) blocks = std::max(blocks, blocks_of(d->rows, lanes_of(d->width, ve)));
+  for (int ve : {1, 2, 4, 8}) blocks = std::max(blocks, blocks_of(d->rows, lanes_of(d->width, ve), ve));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* q = base + at;
@@ -784,11 +1300,35 @@ gs_status launch_few(const char* where, FewArgs& f, cudaStream_t st) {
   return gs::check_launch(where);
 }
 
+template <typename I>
+gs_status launch_buckets(const char* where, const PartArgs& a, cudaStream_t st) {
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_embedding_bucket_scatter<I>, (int)scatter_bytes(kMostBuckets));
+  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  gs::launch(k_embedding_bucket_count<I>, dim3(a.tiles), kPartThreads, 0, st, a);
+  gs::launch(k_embedding_bucket_scan, dim3((a.padded + 7) / 8), 1024, 0, st, a);
+  gs::launch(k_embedding_bucket_scatter<I>, dim3(a.tiles + 1), kPartThreads, scatter_bytes(a.padded), st, a);
+  return gs::check_launch(where);
+}
+template <typename T, int VE>
+gs_status launch_parts(const char* where, const PartArgs& a, const Buckets& b, cudaStream_t st) {
+  const int g = lanes_of(a.s.width, VE), vectors = (a.s.width + VE - 1) / VE;
+  const unsigned slabs = (vectors + g - 1) / g;
+  const cudaError_t e = gs::max_dynamic_smem((const void*)k_embedding_part<T, VE>, (int)part_bytes(kMostRows, kMostCodes, VE));
+  if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+  gs::launch(k_embedding_part<T, VE>, dim3((unsigned)b.parts, slabs), kPartThreads, part_bytes(b.cap, b.codes, VE), st, a, g);
+  if (b.many) {
+    const int walkers = kThreads / g, codes = std::min(walkers, b.codes);
+    const int64_t runs = b.many * ((b.codes + codes - 1) / codes);
+    gs::launch(k_embedding_part_join<T, VE>, dim3((unsigned)std::min<int64_t>(runs, 152 * 8), slabs), kThreads, 0, st, a, g);
+  }
+  return gs::check_launch(where);
+}
+
 template <typename T, int VE>
 void launch_sums(SumArgs& a, cudaStream_t st) {
   const int g = lanes_of(a.width, VE), vectors = (a.width + VE - 1) / VE;
-  a.per_walker = per_walker_of(a.rows, kThreads / g);
-  a.blocks = (unsigned)blocks_of(a.rows, g);
+  a.per_walker = per_walker_of(a.rows, kThreads / g, VE);
+  a.blocks = (unsigned)blocks_of(a.rows, g, VE);
   const unsigned slabs = (vectors + g - 1) / g;
   const unsigned zeros = (unsigned)((a.n + kWarps * 32 - 1) / (kWarps * 32));
   auto go = [&](auto sum, auto join) {
@@ -830,7 +1370,8 @@ extern "C" gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* ta
 extern "C" size_t gs_embedding_bwd_workspace_size(const gs_embedding_desc* d) {
   FewArgs f{};
   if (check_desc("gs_embedding_bwd_workspace_size", d) || d->rows == 0 || d->n == 0 || few_takes(d, f)) return 0;
-  return carve(nullptr, nullptr, d);
+  Buckets b{};
+  return buckets_take(d, b) ? carve(nullptr, nullptr, d, b) : carve(nullptr, nullptr, d);
 }
 
 extern "C" gs_status gs_embedding_bwd(const gs_embedding_desc* d, const void* dy, const void* idx, void* dtable, void* workspace,
@@ -862,6 +1403,17 @@ extern "C" gs_status gs_embedding_bwd(const gs_embedding_desc* d, const void* dy
     return gs::set_error(GS_ERR_INVALID, "%s: workspace is NULL or misaligned", where);
   if (workspace_bytes < need)
     return gs::set_error(GS_ERR_INVALID, "%s: workspace %zu bytes < %zu needed", where, workspace_bytes, need);
+  Buckets b{};
+  if (buckets_take(d, b)) {
+    PartArgs a{};
+    a.s = f.s;
+    carve(&a, static_cast<char*>(workspace), d, b);
+    if (gs_status s = d->index_bits == 32 ? launch_buckets<int32_t>(where, a, st) : launch_buckets<int64_t>(where, a, st))
+      return s;
+    gs_status status = GS_OK;
+    by_vector(d, ve, [&](auto t, auto v) { status = launch_parts<decltype(t), decltype(v)::value>(where, a, b, st); });
+    return status;
+  }
   Space w;
   carve(&w, static_cast<char*>(workspace), d);
   const Plan p = plan_of(d);

@@ -159,6 +159,39 @@ def test_embedding_codes_of_many_rows(dtype):
         _check_embedding(rows, n, 20, dtype, kind)
 
 
+# many rows, which go to buckets of codes: one code a bucket, several, as many as fit, too many (again the sort); a common
+# bucket and a common code, which take several parts; rows of few and of many vectors
+MANY = [(1_600_000, 257, 3, "uniform"), (1_600_000, 300, 8, "skewed"), (1_700_000, 5000, 40, "skewed"),
+        (1_600_001, 70_001, 16, "gaps"), (2_000_000, 1_000_000, 24, "uniform"), (1_573_000, 1 << 22, 4, "skewed"),
+        (3_000_000, 4099, 5, "one"), (1_600_000, 3_000_000, 2, "sorted"), (1_600_000, 40_000, 300, "skewed"),
+        (1_600_000, (1 << 22) + 1, 3, "uniform"), (1_600_000, 1000, 6, "none"),
+        (1 << 20, 65_536, 12, "skewed"), ((1 << 20) - 1, 65_536, 12, "uniform")]
+
+
+@both
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_embedding_many_rows(case, dtype):
+    rows, n, width, kind = case
+    k = MANY.index(case)
+    _check_embedding(rows, n, width, dtype, kind, [1.0, -3.0][k % 2], [torch.int32, torch.int64][k // 2 % 2], seed=50 + k)
+    if width % 8 == 0:  # rows apart and off 16 bytes
+        _check_embedding(rows, n, width, dtype, kind, 1.0, pad=5, shift=1, seed=70 + k)
+
+
+def test_embedding_many_rows_infinities_stay_in_their_code():
+    rows, n = 1_600_000, 2000
+    idx = _indices(rows, n, "skewed", 3)
+    dy = _rand((rows, 16), F32, 4)
+    clean = dense.embedding_bwd(dy, idx, n)
+    dy[idx == 0] = float("inf")
+    dy[idx == 77] = float("nan")
+    got = dense.embedding_bwd(dy, idx, n)
+    assert torch.isinf(got[0]).all() and torch.isnan(got[77]).all()
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[[0, 77]] = False
+    assert torch.equal(got[others], clean[others])
+
+
 def test_embedding_with_nothing_to_do():
     table = _rand((5, 6), F32, 1)
     none = torch.zeros(0, dtype=torch.int64, device="cuda")
