@@ -5,7 +5,8 @@
 //   root = (1 - b2^t)^-1/2 from the host in 64 bits.
 // An 8-bit moment is code x scale; v is kept as its root, whose range the type holds (2^-9 to 448: of v 2^35).
 //
-// Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones.  The tensors' addresses are
+// Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones (176M values: 451 us, 417 at the
+// copy's rate; 17M with bfloat16 gradients and copies: 50 and 40).  The tensors' addresses are
 // launch parameters (no table in device memory to fill and wait for), a block looks its tensor up in them.  A warp takes
 // runs of 256 values, eight a lane: the run's largest magnitudes, by which its scales go, are one reduction over the warp.
 #include <algorithm>
@@ -82,10 +83,10 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h = (h ^ (h >> 15)) * 0xBB67AE85u;
   return h ^ (h >> 16);
 }
-// To four significant bits, up where 16 random bits (at bits 4 to 19 of `noise`) carry.  The largest value's quotient may be
+// To four significant bits, up where 16 random bits carry from the 16 below them.  The largest value's quotient may be
 // a unit in the last place above 448, and what that is rounded up to is saturated by the conversion.
 __device__ __forceinline__ float at_random(float q, uint32_t noise) {
-  return __uint_as_float((__float_as_uint(q) + (noise & 0xffff0u)) & 0xfff00000u);
+  return __uint_as_float((__float_as_uint(q) + (noise << 4)) & 0xfff00000u);
 }
 // the larger of two magnitudes, NaN if one is
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -100,6 +101,11 @@ __device__ __forceinline__ float recip(float b) {
   return r;
 }
 
+__device__ __forceinline__ void add_each(F2 x, F2 y, float& a, float& b) {
+  float x0, x1, y0, y1;
+  x.get(x0, x1), y.get(y0, y1);
+  a = __fadd_rn(x0, y0), b = __fadd_rn(x1, y1);
+}
 // A run by a warp, eight values a lane: two fours (WIDE), or every 32nd one, what lies beyond the tensor taken as zeros.
 template <typename G, int BITS, bool WIDE>
 __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane, const float b1, const float c1, const float b2,
@@ -144,19 +150,34 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
     decode4(mc[0], m), decode4(mc[1], m + 4);
     decode4(vc[0], v), decode4(vc[1], v + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = __fmul_rn(m[i], ms);
-      v[i] = __fmul_rn(v[i], vs);
-      v[i] = __fmul_rn(v[i], v[i]);
+    for (int i = 0; i < 8; i += 2) {
+      mul2(F2(m[i], m[i + 1]), F2(ms)).get(m[i], m[i + 1]);
+      const F2 r = mul2(F2(v[i], v[i + 1]), F2(vs));
+      mul2(r, r).get(v[i], v[i + 1]);
     }
   }
+  // (pairs of values, which sm_100 multiplies in one instruction; the sums are of one value at a time, since the compiler
+  // makes one rounding of a product and a sum of pairs, and the bits of 8-bit moments are those of two)
   float s[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = __fadd_rn(__fmul_rn(m[i], b1), __fmul_rn(g[i], c1));
-    v[i] = __fadd_rn(__fmul_rn(v[i], b2), __fmul_rn(__fmul_rn(g[i], g[i]), c2));
-    s[i] = __fsqrt_rn(v[i]);
-    p[i] = fmaf(m[i] * -t.step, recip(fmaf(s[i], root, eps)), p[i] * t.keep);
+  for (int i = 0; i < 8; i += 2) {
+    const F2 gi(g[i], g[i + 1]);
+    add_each(mul2(F2(m[i], m[i + 1]), F2(b1)), mul2(gi, F2(c1)), m[i], m[i + 1]);
+    add_each(mul2(F2(v[i], v[i + 1]), F2(b2)), mul2(mul2(gi, gi), F2(c2)), v[i], v[i + 1]);
+    s[i] = __fsqrt_rn(v[i]), s[i + 1] = __fsqrt_rn(v[i + 1]);
+    float d0, d1;
+    fma2(F2(s[i], s[i + 1]), F2(root), F2(eps)).get(d0, d1);
+    fma2(mul2(F2(m[i], m[i + 1]), F2(-t.step)), F2(recip(d0), recip(d1)), mul2(F2(p[i], p[i + 1]), F2(t.keep))).get(p[i], p[i + 1]);
+  }
+  if constexpr (WIDE) {  // (before the moments' bits, whose registers these then are)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t e = at + lane * 4 + k * 128;
+      *reinterpret_cast<float4*>(t.p + e) = make_float4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+      if (t.copy)
+        *reinterpret_cast<uint2*>(t.copy + e) =
+            make_uint2(pack_bf16(p[4 * k], p[4 * k + 1]), pack_bf16(p[4 * k + 2], p[4 * k + 3]));
+    }
   }
   uint32_t qm[2], qv[2];
   if constexpr (BITS == 8) {
@@ -174,8 +195,8 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t h = mix(base + (WIDE ? (uint32_t)((i >> 2) * 128 + (i & 3)) : (uint32_t)(32 * i)) * 0x9E3779B1u);
-      a[i] = at_random(__fmul_rn(m[i], im), h << 4);
-      b[i] = at_random(__fmul_rn(s[i], iv), h >> 12);
+      a[i] = at_random(__fmul_rn(m[i], im), h & 0xffffu);
+      b[i] = at_random(__fmul_rn(s[i], iv), h >> 16);
       if (s[i] > 0.f) b[i] = fmaxf(b[i], least);
     }
     qm[0] = encode4(a), qm[1] = encode4(a + 4);
@@ -189,7 +210,6 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t e = at + lane * 4 + k * 128;
-      *reinterpret_cast<float4*>(t.p + e) = make_float4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
       if constexpr (BITS == 32) {
         *reinterpret_cast<float4*>(static_cast<float*>(t.m) + e) = make_float4(m[4 * k], m[4 * k + 1], m[4 * k + 2], m[4 * k + 3]);
         *reinterpret_cast<float4*>(static_cast<float*>(t.v) + e) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -197,9 +217,6 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + e) = qm[k];
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + e) = qv[k];
       }
-      if (t.copy)
-        *reinterpret_cast<uint2*>(t.copy + e) =
-            make_uint2(pack_bf16(p[4 * k], p[4 * k + 1]), pack_bf16(p[4 * k + 2], p[4 * k + 3]));
     }
   } else {
 #pragma unroll
@@ -219,8 +236,10 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   }
 }
 
+// Five blocks to an SM, although some values spill: instructions bound the 8-bit form as much as memory does, and more warps
+// hide both (176M values with 8-bit moments: 451 us, 497 with four blocks, 498 with six).
 template <typename G, int BITS, int MOST>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Args<MOST> a) {
+__global__ void __launch_bounds__(kThreads, 5) k_adamw(const __grid_constant__ Args<MOST> a) {
   follow();
   for (int i = 0; i < a.n_counts; ++i)
     if (a.counts[2 * i + 1] != 0) return;
