@@ -4,7 +4,8 @@
 // Mathematics: y[r] = scale table[idx[r]]; dtable[v] = scale sum over {r: idx[r] = v} of dy[r].
 //
 // Both are bound by memory.  The forward reads the indices and what it needs of the table, and writes y once: a thread
-// holds one vector of a row, four of them in flight.
+// holds one vector of a row, four of them in flight (10M rows of 64 bfloat16: 228 us, 196 at the copy's rate; 242 with stores
+// that stay in L2).
 //
 // The backward must not add in whatever order atomics come, and one code may have any number of rows, so the rows are
 // first sorted by code, stably, and then added up in equal parts of the sorted rows by groups of lanes ("walkers"), in registers
@@ -28,6 +29,20 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPartThreads = 512;  // of the backward's kernels by buckets
 
 // ------------------------------------------------------------------ forward
+// Outputs of this size or more are not held by L2 (129 MB) until they are read: they are stored first to be evicted, and leave
+// it to the table.
+constexpr int64_t kStreamBytes = 64 << 20;
+template <typename T, int VE>
+__device__ __forceinline__ void store_row(T* p, const float* f, bool stream) {
+  if constexpr (sizeof(typename VecIO<T, VE>::Raw) == 16) {
+    if (stream) {
+      typename VecIO<T, VE>::Raw r;
+      VecIO<T, VE>::store(reinterpret_cast<T*>(&r), f);
+      return __stcs(reinterpret_cast<decltype(r)*>(p), r);
+    }
+  }
+  VecIO<T, VE>::store(p, f);
+}
 struct FwdArgs {
   const void* table;
   const void* idx;
@@ -35,6 +50,7 @@ struct FwdArgs {
   int64_t rows, n, ldt, ldy;
   uint32_t per_row, magic;  // vectors of a row; 2^32 / per_row rounded up
   float scale;
+  bool stream;
 };
 
 template <typename T, int VE, typename I>
@@ -72,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
     const bool there = code[u] >= 0 && code[u] < a.n;
 #pragma unroll
     for (int e = 0; e < VE; ++e) f[e] = there ? f[e] * a.scale : 0.f;
-    IO::store(y + row[u] * a.ldy + col[u] * VE, f);
+    store_row<T, VE>(y + row[u] * a.ldy + col[u] * VE, f, a.stream);
   }
 }
 
@@ -1357,7 +1373,8 @@ extern "C" gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* ta
   const int64_t blocks = (vectors + kThreads * 4 - 1) / (kThreads * 4);
   if (blocks > INT32_MAX) return gs::set_error(GS_ERR_INVALID, "%s: y is too large", where);
   const FwdArgs a{table, idx, y, d->rows, d->n, d->ldt, d->ldy, (uint32_t)per_row,
-                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), d->scale};
+                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), d->scale,
+                  d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) >= kStreamBytes};
   by_vector(d, ve, [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int VE = decltype(v)::value;
