@@ -40,7 +40,8 @@ struct FwdArgs {
   void* y;
   float* mean;
   float* rstd;
-  float2* part;  // [samples][slabs][span][chunks]: mean and squared distances
+  float2* part;    // [samples][slabs][span][chunks]: mean and squared distances
+  float2* joined;  // [samples][groups]: means and rstds, or NULL: every block joins the parts by itself
   int64_t ldx, ldy;
   float eps;
 };
@@ -54,7 +55,7 @@ struct BwdArgs {
   const float* rstd;
   const void* skip;
   void* dx;
-  float2* part;  // as the forward's: sums of g and of g h
+  float2 *part, *joined;  // as the forward's: sums of g and of g h, their means
   float* cols;   // [2][samples * chunks][width]: sums of dz and of dz h, or NULL
   int64_t lddy, ldx, ldskip, lddx;
 };
@@ -223,41 +224,63 @@ __device__ __forceinline__ float sum_among(float v, int k) {
 // at least zero, or NaN
 __device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
 
-// Means and rstds of the block's groups, from the parts of all chunks and slabs.  About the first part's mean k: n of the
-// N values have it, so n (k - mean)^2 is at most all squared distances, and little is lost to N (k - mean)^2.
-__device__ __forceinline__ void group_stats(const FwdArgs& a, const Place& at, float2* s_stat) {
+// A group's mean and rstd by `lanes` lanes, from the parts of all chunks and slabs.  About the first part's mean k: n of the N
+// values have it, so n (k - mean)^2 is at most all squared distances, and little is lost to N (k - mean)^2.
+__device__ __forceinline__ float2 join_stats(const FwdArgs& a, int64_t sample, int g, int lane, int lanes) {
   const Shape& s = a.s;
-  const int groups = at.g1 - at.g0, lanes = side_by_side(groups), lane = threadIdx.x % lanes;
-  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
-    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
-    const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
-    const float k = a.part[parts_of(s, at.sample, first, g)].x;
-    float s1 = 0.f, s2 = 0.f;
-    for (int b = first; b <= last; ++b) {
-      const int wide = min((g + 1) * s.per, (b + 1) * s.cols) - max(g * s.per, b * s.cols);
-      const float2* part = a.part + parts_of(s, at.sample, b, g);
-      const float full = (float)s.chunk * (float)wide, rest = (float)(s.rows - (s.chunks - 1) * s.chunk) * (float)wide;
+  const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
+  const float k = a.part[parts_of(s, sample, first, g)].x;
+  float s1 = 0.f, s2 = 0.f;
+  for (int b = first; b <= last; ++b) {
+    const int wide = min((g + 1) * s.per, (b + 1) * s.cols) - max(g * s.per, b * s.cols);
+    const float2* part = a.part + parts_of(s, sample, b, g);
+    const float full = (float)s.chunk * (float)wide, rest = (float)(s.rows - (s.chunks - 1) * s.chunk) * (float)wide;
 #pragma unroll 8
-      for (int c = lane; c < s.chunks; c += lanes) {
-        const float n = c == s.chunks - 1 ? rest : full;
-        const float2 p = part[c];
-        const float d = p.x - k;
-        s1 = fmaf(n, d, s1);
-        s2 += fmaf(n * d, d, p.y);
-      }
-    }
-    s1 = sum_among(s1, lanes), s2 = sum_among(s2, lanes);
-    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) {
-      const float total = (float)s.rows * (float)s.per, off = s1 / total;
-      const float var = not_negative(fmaf(-off, off, s2 / total));
-      const float2 st = make_float2(k + off, 1.f / sqrtf(var + a.eps));
-      s_stat[g - at.g0] = st;
-      if (at.chunk == 0 && g * s.per >= at.col0) {  // (one block of those that know it)
-        if (a.mean) a.mean[at.sample * s.groups + g] = st.x;
-        if (a.rstd) a.rstd[at.sample * s.groups + g] = st.y;
-      }
+    for (int c = lane; c < s.chunks; c += lanes) {
+      const float n = c == s.chunks - 1 ? rest : full;
+      const float2 p = part[c];
+      const float d = p.x - k;
+      s1 = fmaf(n, d, s1);
+      s2 += fmaf(n * d, d, p.y);
     }
   }
+  s1 = sum_among(s1, lanes), s2 = sum_among(s2, lanes);
+  const float total = (float)s.rows * (float)s.per, off = s1 / total;
+  const float var = not_negative(fmaf(-off, off, s2 / total));
+  return make_float2(k + off, 1.f / sqrtf(var + a.eps));
+}
+__device__ __forceinline__ void keep_stats(const FwdArgs& a, int64_t sample, int g, float2 st) {
+  if (a.mean) a.mean[sample * a.s.groups + g] = st.x;
+  if (a.rstd) a.rstd[sample * a.s.groups + g] = st.y;
+}
+// of the block's groups
+__device__ __forceinline__ void group_stats(const FwdArgs& a, const Place& at, float2* s_stat) {
+  const int groups = at.g1 - at.g0;
+  if (a.joined) {
+    for (int g = threadIdx.x; g < groups; g += kThreads) s_stat[g] = a.joined[at.sample * a.s.groups + at.g0 + g];
+    return;
+  }
+  const int lanes = side_by_side(groups), lane = threadIdx.x % lanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
+    const float2 st = join_stats(a, at.sample, g, lane, lanes);
+    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) {
+      s_stat[g - at.g0] = st;
+      if (at.chunk == 0 && g * a.s.per >= at.col0) keep_stats(a, at.sample, g, st);  // (one block of those that know it)
+    }
+  }
+}
+// of all groups, a warp to each
+__global__ void __launch_bounds__(kThreads) k_groupnorm_join(const FwdArgs a) {
+  follow();
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (i >= a.s.samples * a.s.groups) return;
+  const int64_t sample = i / a.s.groups;
+  const int g = (int)(i % a.s.groups), lane = threadIdx.x & 31;
+  const float2 st = join_stats(a, sample, g, lane, 32);
+  if (lane) return;
+  a.joined[i] = st;
+  keep_stats(a, sample, g, st);
 }
 
 template <typename T, int VE>
@@ -487,6 +510,43 @@ __device__ __forceinline__ void grad_sums(const BwdArgs& a, const Place& at) {
   }
 }
 
+// A group's means of g and of g h by `lanes` lanes; of the block's groups; of all groups, a warp to each.
+__device__ __forceinline__ float2 join_means(const BwdArgs& a, int64_t sample, int g, int lane, int lanes) {
+  const Shape& s = a.s;
+  const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
+  float2 t = make_float2(0.f, 0.f);
+  for (int b = first; b <= last; ++b) {
+    const float2* part = a.part + parts_of(s, sample, b, g);
+#pragma unroll 8
+    for (int c = lane; c < s.chunks; c += lanes) {
+      const float2 p = part[c];
+      t.x += p.x, t.y += p.y;
+    }
+  }
+  const float inv = 1.f / ((float)s.rows * (float)s.per);
+  return make_float2(sum_among(t.x, lanes) * inv, sum_among(t.y, lanes) * inv);
+}
+__device__ __forceinline__ void grad_means(const BwdArgs& a, const Place& at, float2* s_mean) {
+  const int groups = at.g1 - at.g0;
+  if (a.joined) {
+    for (int g = threadIdx.x; g < groups; g += kThreads) s_mean[g] = a.joined[at.sample * a.s.groups + at.g0 + g];
+    return;
+  }
+  const int lanes = side_by_side(groups), lane = threadIdx.x % lanes;
+  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
+    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
+    const float2 t = join_means(a, at.sample, g, lane, lanes);
+    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) s_mean[g - at.g0] = t;
+  }
+}
+__global__ void __launch_bounds__(kThreads) k_groupnorm_grad_join(const BwdArgs a) {
+  follow();
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (i >= a.s.samples * a.s.groups) return;
+  const float2 t = join_means(a, i / a.s.groups, (int)(i % a.s.groups), threadIdx.x & 31, 32);
+  if ((threadIdx.x & 31) == 0) a.joined[i] = t;
+}
+
 // dx = dz q - (rstd mean(g) + d rstd^2 mean(g h)) + skip; A = 3: with skip
 template <typename T, int VE, bool ONE, int ACT, int A>
 __device__ __forceinline__ void grad_write(const BwdArgs& a, const Place& at) {
@@ -502,23 +562,7 @@ __device__ __forceinline__ void grad_write(const BwdArgs& a, const Place& at) {
   if constexpr (A == 3) r.at[2] = static_cast<const T*>(a.skip) + row * a.ldskip + col, r.step[2] = (int64_t)ny * a.ldskip;
   r.start(count);
   float2* s_mean = reinterpret_cast<float2*>(s_ring + kRing);  // of g and of g h, by the slab's groups
-  const float inv = 1.f / ((float)s.rows * (float)s.per);
-  const int groups = at.g1 - at.g0, lanes = side_by_side(groups), lane = threadIdx.x % lanes;
-  for (int g0 = 0; g0 < groups; g0 += kThreads / lanes) {
-    const int g = at.g0 + min(g0 + (int)threadIdx.x / lanes, groups - 1);
-    const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
-    float2 t = make_float2(0.f, 0.f);
-    for (int b = first; b <= last; ++b) {
-      const float2* part = a.part + parts_of(s, at.sample, b, g);
-#pragma unroll 8
-      for (int c = lane; c < s.chunks; c += lanes) {
-        const float2 p = part[c];
-        t.x += p.x, t.y += p.y;
-      }
-    }
-    t.x = sum_among(t.x, lanes), t.y = sum_among(t.y, lanes);
-    if (lane == 0 && g0 + (int)threadIdx.x / lanes < groups) s_mean[g - at.g0] = make_float2(t.x * inv, t.y * inv);
-  }
+  grad_means(a, at, s_mean);
   __syncthreads();
   if (!count) return;
   using V = Pairs<VE>;
@@ -654,6 +698,18 @@ Shape shape_of(const gs_groupnorm_desc* d, int ve, int arrays) {
 size_t part_bytes(const Shape& s) {
   return (sizeof(float2) * (size_t)s.samples * s.slabs * s.span * s.chunks + 255) / 256 * 256;
 }
+size_t joined_bytes(const Shape& s) { return (sizeof(float2) * (size_t)s.samples * s.groups + 255) / 256 * 256; }
+// Whether a kernel between the passes joins the parts.  It costs a launch, some 3 us; without it each of an SM's blocks, one
+// after the other, waits for the parts, eight loads a lane at a time (12 maps of 13,604 x 952 float32 backward, 390 chunks of 119
+// groups: 471 us with it, 683 without; 4 images of 1236 x 820 x 64, 1,026 chunks of 8 groups: 392 either way).
+bool joins(const Shape& s, int arrays) {
+  int lanes = 32;
+  while (lanes > 1 && s.span * lanes > kThreads) lanes /= 2;
+  const int64_t held = 152 * (arrays == 1 ? 4 : 3), waves = (s.samples * s.chunks * s.slabs + held - 1) / held;
+  const int64_t turns = (s.chunks + 8 * lanes - 1) / (8 * lanes);
+  return turns > 1 && waves * turns * ((s.span * lanes + kThreads - 1) / kThreads) > 4;
+}
+dim3 join_grid(const Shape& s) { return dim3((unsigned)((s.samples * s.groups + kThreads / 32 - 1) / (kThreads / 32))); }
 // over the vectors that the arrays' alignment may lead to
 template <typename F>
 size_t most_bytes(const gs_groupnorm_desc* d, int arrays, F f) {
@@ -719,7 +775,7 @@ void by_form(const gs_groupnorm_desc* d, int ve, F f) {
 
 extern "C" size_t gs_groupnorm_fwd_workspace_size(const gs_groupnorm_desc* d) {
   if (check_desc("gs_groupnorm_fwd_workspace_size", d) || d->samples * d->rows == 0) return 0;
-  return most_bytes(d, 1, part_bytes);
+  return most_bytes(d, 1, [](const Shape& s) { return part_bytes(s) + joined_bytes(s); });
 }
 
 extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x, const void* gamma, const void* beta, void* y,
@@ -747,13 +803,16 @@ extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x,
            gs::rows_aligned(gamma, 1, 0, d->dtype, bytes) && gs::rows_aligned(beta, 1, 0, d->dtype, bytes);
   });
   const Shape s = shape_of(d, ve, 1);
-  const FwdArgs a{s, x, gamma, beta, y, mean, rstd, static_cast<float2*>(workspace), d->ldx, d->ldy, d->eps};
+  float2* parts = static_cast<float2*>(workspace);
+  const FwdArgs a{s, x, gamma, beta, y, mean, rstd, parts, joins(s, 1) ? parts + part_bytes(s) / sizeof(float2) : nullptr,
+                  d->ldx, d->ldy, d->eps};
   const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
   const size_t smem = kRing + sizeof(float2) * s.span;
   by_form(d, ve, [&](auto t, auto v, auto one, auto act) {
     using T = decltype(t);
     constexpr int VE = decltype(v)::value;
     gs::launch(k_groupnorm_sums<T, VE>, grid, kThreads, smem, st, a);
+    if (a.joined) gs::launch(k_groupnorm_join, join_grid(s), kThreads, 0, st, a);
     gs::launch(k_groupnorm_write<T, VE, decltype(one)::value, decltype(act)::value>, grid, kThreads, smem, st, a);
   });
   return gs::check_launch(where);
@@ -762,7 +821,7 @@ extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x,
 extern "C" size_t gs_groupnorm_bwd_workspace_size(const gs_groupnorm_desc* d) {
   if (check_desc("gs_groupnorm_bwd_workspace_size", d) || d->samples * d->rows == 0) return 0;
   return most_bytes(d, 2, [&](const Shape& s) {
-    return part_bytes(s) + sizeof(float) * 2 * (size_t)s.samples * s.chunks * s.width;
+    return part_bytes(s) + joined_bytes(s) + sizeof(float) * 2 * (size_t)s.samples * s.chunks * s.width;
   });
 }
 
@@ -802,8 +861,9 @@ extern "C" gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy
            (!dx || gs::rows_aligned(dx, rows, d->lddx, d->dtype, bytes));
   });
   const Shape s = shape_of(d, ve, 2);
-  float* cols = dgamma || dbeta ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(s)) : nullptr;
-  const BwdArgs a{s, dy, x, gamma, beta, mean, rstd, skip, dx, static_cast<float2*>(workspace), cols, d->lddy, d->ldx, d->ldskip, d->lddx};
+  float* cols = dgamma || dbeta ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(s) + joined_bytes(s)) : nullptr;
+  float2* parts = static_cast<float2*>(workspace);
+  const BwdArgs a{s, dy, x, gamma, beta, mean, rstd, skip, dx, parts, joins(s, 2) ? parts + part_bytes(s) / sizeof(float2) : nullptr, cols, d->lddy, d->ldx, d->ldskip, d->lddx};
   const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
   const size_t smem = kRing + sizeof(float2) * s.span;
   by_form(d, ve, [&](auto t, auto v, auto one, auto act) {
@@ -811,6 +871,7 @@ extern "C" gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy
     constexpr int VE = decltype(v)::value, ACT = decltype(act)::value;
     constexpr bool ONE = decltype(one)::value;
     gs::launch(k_groupnorm_grad_sums<T, VE, ONE, ACT>, grid, kThreads, smem, st, a);
+    if (dx && a.joined) gs::launch(k_groupnorm_grad_join, join_grid(s), kThreads, 0, st, a);
     const SumFold f{cols, dbeta, dgamma, s.samples * s.chunks, s.width};
     const unsigned all = cols ? fold_blocks(s.width) : 0u, folds = dx && grid.x + all <= INT32_MAX ? all : 0u;
     const dim3 more(grid.x + folds, grid.y);
