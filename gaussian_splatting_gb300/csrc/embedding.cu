@@ -4,7 +4,7 @@
 // Mathematics: y[r] = scale table[idx[r]]; dtable[v] = scale sum over {r: idx[r] = v} of dy[r].
 //
 // Both are bound by memory.  The forward reads the indices and what it needs of the table, and writes y once: a thread
-// holds one vector of a row, four of them in flight (10M rows of 64 bfloat16: 228 us, 196 at the copy's rate; 242 with stores
+// holds 16 bytes of a row, four times in flight (10M rows of 64 bfloat16: 228 us, 196 at the copy's rate; 242 with stores
 // that stay in L2).
 //
 // The backward must not add in whatever order atomics come, and one code may have any number of rows, so the rows are
@@ -48,16 +48,20 @@ struct FwdArgs {
   const void* idx;
   void* y;
   int64_t rows, n, ldt, ldy;
-  uint32_t per_row, magic;  // vectors of a row; 2^32 / per_row rounded up
+  uint32_t per_row, magic;  // units of a row; 2^32 / per_row rounded up
+  uint32_t width;
   float scale;
   bool stream;
 };
 
+// Vectors of a thread's unit: short ones share the arithmetic of their place, four of 4 bytes (33K rows of 322 float32: 13.0
+// us, 19.4 alone) or two of 2 (332K rows of 393 bfloat16: 164 us, 290 with eight, 274 alone).
+constexpr int unit_of(int vector_bytes) { return vector_bytes == 16 ? 1 : vector_bytes == 4 ? 4 : 2; }
 template <typename T, int VE, typename I>
 __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
   follow();
   using IO = VecIO<T, VE>;
-  constexpr int U = 4;
+  constexpr int K = unit_of(sizeof(typename IO::Raw)), U = K == 4 ? 2 : 4;
   const int64_t first = (int64_t)blockIdx.x * (kThreads * U);
   const int64_t r0 = first / a.per_row;
   const uint32_t c0 = (uint32_t)(first - r0 * a.per_row);
@@ -70,25 +74,33 @@ __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t o = c0 + u * kThreads + threadIdx.x;  // < per_row + 1024
-    // rows of more than 1024 vectors: at most one further row; else o per_row < 2^22 and the product is exact
+    // rows of more than 1024 units: at most one further row; else o per_row < 2^22 and the product is exact
     const uint32_t q = a.per_row > 1024 ? (o >= a.per_row) : a.per_row == 1 ? o : __umulhi(o, a.magic);
-    row[u] = r0 + q, col[u] = o - q * a.per_row;
+    row[u] = r0 + q, col[u] = (o - q * a.per_row) * (K * VE);
     const bool in = row[u] < a.rows;
     code[u] = in ? idx[row[u]] : (I)-1;
   }
-  typename IO::Raw v[U];
+  typename IO::Raw v[U][K];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    v[u] = code[u] >= 0 && code[u] < a.n ? IO::load(table + (int64_t)code[u] * a.ldt + col[u] * VE) : IO::zero();
+  for (int u = 0; u < U; ++u) {
+    const bool there = code[u] >= 0 && code[u] < a.n;
+    const T* from = table + (there ? (int64_t)code[u] : (int64_t)0) * a.ldt + col[u];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[u][k] = there && (K == 1 || col[u] + k * VE < a.width) ? IO::load(from + k * VE) : IO::zero();
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (row[u] >= a.rows) continue;
-    float f[VE];
-    IO::unpack(v[u], f);
     const bool there = code[u] >= 0 && code[u] < a.n;
+    T* to = y + row[u] * a.ldy + col[u];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) f[e] = there ? f[e] * a.scale : 0.f;
-    store_row<T, VE>(y + row[u] * a.ldy + col[u] * VE, f, a.stream);
+    for (int k = 0; k < K; ++k) {
+      float f[VE];
+      IO::unpack(v[u][k], f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[e] = there ? f[e] * a.scale : 0.f;
+      if (K == 1 || col[u] + k * VE < a.width) store_row<T, VE>(to + k * VE, f, a.stream);
+    }
   }
 }
 
@@ -349,14 +361,14 @@ __device__ __forceinline__ void copy_async16(void* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 // Lists in shared memory: four rows are always in flight, through a ring of the thread's own in shared memory, which takes no
-// registers (16 bytes a vector; shorter ones take the registers of a batch of four).
+// registers (16 bytes a vector; shorter ones take the registers of a batch of eight).
 template <typename T, int VE>
 struct RingRows {
   using IO = VecIO<T, VE>;
   using Raw = typename IO::Raw;
   using Pos = int;
-  static constexpr int B = 4;
   static constexpr bool kRing = sizeof(Raw) == 16;
+  static constexpr int B = kRing ? 4 : 8;
   const uint16_t* keys;
   const uint32_t* order;
   const T* dy;
@@ -367,8 +379,11 @@ struct RingRows {
   uint32_t k[B], o[B];
   Raw v[kRing ? 1 : B];
   __device__ __forceinline__ void rows_at(int p) {
-    const uint4 q = *reinterpret_cast<const uint4*>(order + p);
-    o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+#pragma unroll
+    for (int h = 0; h < B; h += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(order + p + h);
+      o[h] = q.x, o[h + 1] = q.y, o[h + 2] = q.z, o[h + 3] = q.w;
+    }
   }
   __device__ __forceinline__ void issue(int p, int u) {
     if (p + u < end && there) copy_async16(ring + u * kPartThreads, dy + (int64_t)o[u] * ldy);
@@ -383,10 +398,13 @@ struct RingRows {
     }
   }
   __device__ __forceinline__ void batch(int p) {
-    const uint2 q = *reinterpret_cast<const uint2*>(keys + p);
-    const uint32_t t[B] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
 #pragma unroll
-    for (int u = 0; u < B; ++u) k[u] = p + u < end ? t[u] : 0xffffu;
+    for (int h = 0; h < B; h += 4) {
+      const uint2 q = *reinterpret_cast<const uint2*>(keys + p + h);
+      k[h] = q.x & 0xffffu, k[h + 1] = q.x >> 16, k[h + 2] = q.y & 0xffffu, k[h + 3] = q.y >> 16;
+    }
+#pragma unroll
+    for (int u = 0; u < B; ++u) k[u] = p + u < end ? k[u] : 0xffffu;
     now = p;
     if constexpr (kRing) {
       if (p + B < end) rows_at(p + B);
@@ -542,7 +560,7 @@ template <typename T, int VE>
 __device__ __forceinline__ void write_zeros(const SumArgs& a, uint32_t empty, int64_t first, int g, int slab) {
   const int lane = threadIdx.x & 31, col = (slab * g + lane % g) * VE;
   const float none[VE] = {};
-  if (col >= a.width) return;
+  if (col >= a.width || lane >= 32 / g * g) return;
   for (int r = lane / g; r < 32; r += 32 / g)
     if ((empty >> r) & 1u) VecIO<T, VE>::store(static_cast<T*>(a.dtable) + (first + r) * a.ldt + col, none);
 }
@@ -882,10 +900,10 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   // the sums
   const bool whole = part.slot == kWhole;
   const int64_t code0 = (int64_t)part.bucket << p.shift;
-  const int walkers = kPartThreads / g, wl = threadIdx.x % g, walker = threadIdx.x / g;
+  const int walkers = kPartThreads / g, wl = threadIdx.x % g, walker = threadIdx.x / g;  // (threads may be left over)
   const int col = ((int)blockIdx.y * g + wl) * VE;
   const int per = (m + walkers * kBatch - 1) / (walkers * kBatch) * kBatch;
-  const int begin = min(walker * per, m), end = min(begin + per, m);
+  const int begin = walker < walkers ? min(walker * per, m) : m, end = min(begin + per, m);
   float *head = ends + threadIdx.x * VE, *tail = ends + (kPartThreads + threadIdx.x) * VE;
   float* to = p.sums + (whole ? (int64_t)0 : (int64_t)part.slot * p.codes * a.ldp) + col;
   auto put = [&](uint32_t c, const float* sum) {
@@ -901,7 +919,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   rows.keys = s_key, rows.order = s_row, rows.dy = static_cast<const T*>(a.dy) + col, rows.ldy = a.ldy, rows.end = end;
   rows.there = col < a.width, rows.ring = ring + threadIdx.x;
   const uint32_t flag = walk<T, VE>(rows, s_key, begin, m, 0xffffu, head, tail, code, put, [](uint32_t) {});
-  if (wl == 0) flags[walker] = flag;
+  if (wl == 0 && walker < walkers) flags[walker] = flag;
   // codes without rows
   const int words = (p.codes + 31) / 32;
   for (int w = warp; w < words; w += kPartWarps) {
@@ -1327,15 +1345,17 @@ gs_status launch_buckets(const char* where, const PartArgs& a, cudaStream_t st) 
 }
 template <typename T, int VE>
 gs_status launch_parts(const char* where, const PartArgs& a, const Buckets& b, cudaStream_t st) {
-  const int g = lanes_of(a.s.width, VE), vectors = (a.s.width + VE - 1) / VE;
-  const unsigned slabs = (vectors + g - 1) / g;
+  const int vectors = (a.s.width + VE - 1) / VE;
   const cudaError_t e = gs::max_dynamic_smem((const void*)k_embedding_part<T, VE>, (int)part_bytes(kMostRows, kMostCodes, VE));
   if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-  gs::launch(k_embedding_part<T, VE>, dim3((unsigned)b.parts, slabs), kPartThreads, part_bytes(b.cap, b.codes, VE), st, a, g);
+  // as many lanes to a walker as a row has vectors, or equal slabs of up to 32
+  const int slabs = (vectors + 31) / 32, lanes = (vectors + slabs - 1) / slabs;
+  gs::launch(k_embedding_part<T, VE>, dim3((unsigned)b.parts, (unsigned)slabs), kPartThreads, part_bytes(b.cap, b.codes, VE), st, a, lanes);
   if (b.many) {
-    const int walkers = kThreads / g, codes = std::min(walkers, b.codes);
+    const int g = lanes_of(a.s.width, VE), walkers = kThreads / g, codes = std::min(walkers, b.codes);
     const int64_t runs = b.many * ((b.codes + codes - 1) / codes);
-    gs::launch(k_embedding_part_join<T, VE>, dim3((unsigned)std::min<int64_t>(runs, 152 * 8), slabs), kThreads, 0, st, a, g);
+    gs::launch(k_embedding_part_join<T, VE>, dim3((unsigned)std::min<int64_t>(runs, 152 * 8), (unsigned)((vectors + g - 1) / g)), kThreads, 0,
+               st, a, g);
   }
   return gs::check_launch(where);
 }
@@ -1369,11 +1389,12 @@ extern "C" gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* ta
   if (gs_status s = gs::check_matrix(where, "y", y, d->rows, d->width, d->ldy, d->dtype)) return s;
   if (gs_status s = check_idx(where, d, idx)) return s;
   const int ve = vector_of(d, table, y);
-  const int64_t per_row = d->width / ve, vectors = d->rows * per_row;
-  const int64_t blocks = (vectors + kThreads * 4 - 1) / (kThreads * 4);
+  const int k = unit_of(ve * (int)gs::dtype_size(d->dtype));
+  const int64_t per_row = (d->width + k * ve - 1) / (k * ve), units = d->rows * per_row, of_block = kThreads * (k == 4 ? 2 : 4);
+  const int64_t blocks = (units + of_block - 1) / of_block;
   if (blocks > INT32_MAX) return gs::set_error(GS_ERR_INVALID, "%s: y is too large", where);
   const FwdArgs a{table, idx, y, d->rows, d->n, d->ldt, d->ldy, (uint32_t)per_row,
-                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), d->scale,
+                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), (uint32_t)d->width, d->scale,
                   d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) >= kStreamBytes};
   by_vector(d, ve, [&](auto t, auto v) {
     using T = decltype(t);
