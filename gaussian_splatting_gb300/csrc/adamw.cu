@@ -5,8 +5,8 @@
 //   root = (1 - b2^t)^-1/2 from the host in 64 bits.
 // An 8-bit moment is code x scale; v is kept as its root, whose range the type holds (2^-9 to 448: of v 2^35).
 //
-// Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones (176M values: 451 us, 417 at the
-// copy's rate; 17M with bfloat16 gradients and copies: 50 and 40).  The tensors' addresses are
+// Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones (176M values: 453 us, 417 at the
+// copy's rate; 17M with bfloat16 gradients and copies: 48 and 40).  The tensors' addresses are
 // launch parameters (no table in device memory to fill and wait for), a block looks its tensor up in them.  A warp takes
 // runs of 256 values, eight a lane: the run's largest magnitudes, by which its scales go, are one reduction over the warp.
 #include <algorithm>
@@ -18,7 +18,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kRun = 256;                   // values that share a scale
 constexpr int kTile = kThreads / 32 * kRun; // values of a block
 constexpr float kTop = 448.f;               // the largest float8 e4m3
@@ -118,7 +118,6 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t e = at + lane * 4 + k * 128;
-      load4(t.p + e, p + 4 * k);
       load4(gp + e, g + 4 * k);
       if constexpr (BITS == 32) {
         load4(static_cast<const float*>(t.m) + e, m + 4 * k);
@@ -165,19 +164,10 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
     add_each(mul2(F2(m[i], m[i + 1]), F2(b1)), mul2(gi, F2(c1)), m[i], m[i + 1]);
     add_each(mul2(F2(v[i], v[i + 1]), F2(b2)), mul2(mul2(gi, gi), F2(c2)), v[i], v[i + 1]);
     s[i] = __fsqrt_rn(v[i]), s[i + 1] = __fsqrt_rn(v[i + 1]);
-    float d0, d1;
-    fma2(F2(s[i], s[i + 1]), F2(root), F2(eps)).get(d0, d1);
-    fma2(mul2(F2(m[i], m[i + 1]), F2(-t.step)), F2(recip(d0), recip(d1)), mul2(F2(p[i], p[i + 1]), F2(t.keep))).get(p[i], p[i + 1]);
   }
-  if constexpr (WIDE) {  // (before the moments' bits, whose registers these then are)
+  if constexpr (WIDE) {  // (in flight while the moments are rounded)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t e = at + lane * 4 + k * 128;
-      *reinterpret_cast<float4*>(t.p + e) = make_float4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-      if (t.copy)
-        *reinterpret_cast<uint2*>(t.copy + e) =
-            make_uint2(pack_bf16(p[4 * k], p[4 * k + 1]), pack_bf16(p[4 * k + 2], p[4 * k + 3]));
-    }
+    for (int k = 0; k < 2; ++k) load4(t.p + at + lane * 4 + k * 128, p + 4 * k);
   }
   uint32_t qm[2], qv[2];
   if constexpr (BITS == 8) {
@@ -191,25 +181,38 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
     const float im = tm != 0.f ? __fmul_rn(__frcp_rn(tm), kTop) : 0.f, iv = tv != 0.f ? __fmul_rn(__frcp_rn(tv), kTop) : 0.f;
     const float least = tv != 0.f ? 0x1p-9f : 0.f;
     const uint32_t base = (t.place + (uint32_t)at + (WIDE ? lane * 4 : lane)) * 0x9E3779B1u + key;
-    float a[8], b[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = mix(base + (WIDE ? (uint32_t)((i >> 2) * 128 + (i & 3)) : (uint32_t)(32 * i)) * 0x9E3779B1u);
-      a[i] = at_random(__fmul_rn(m[i], im), h & 0xffffu);
-      b[i] = at_random(__fmul_rn(s[i], iv), h >> 16);
-      if (s[i] > 0.f) b[i] = fmaxf(b[i], least);
+    for (int k = 0; k < 2; ++k) {
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * k + j;
+        const uint32_t h = mix(base + (WIDE ? (uint32_t)(k * 128 + j) : (uint32_t)(32 * i)) * 0x9E3779B1u);
+        a[j] = at_random(__fmul_rn(m[i], im), h & 0xffffu);
+        b[j] = at_random(__fmul_rn(s[i], iv), h >> 16);
+        if (s[i] > 0.f) b[j] = fmaxf(b[j], least);
+      }
+      qm[k] = encode4(a), qv[k] = encode4(b);
     }
-    qm[0] = encode4(a), qm[1] = encode4(a + 4);
-    qv[0] = encode4(b), qv[1] = encode4(b + 4);
     if (lane == 0) {
       t.ms[run] = __fmul_rn(tm, 1.f / kTop);
       t.vs[run] = __fmul_rn(tv, 1.f / kTop);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    float d0, d1;
+    fma2(F2(s[i], s[i + 1]), F2(root), F2(eps)).get(d0, d1);
+    fma2(mul2(F2(m[i], m[i + 1]), F2(-t.step)), F2(recip(d0), recip(d1)), mul2(F2(p[i], p[i + 1]), F2(t.keep))).get(p[i], p[i + 1]);
+  }
   if constexpr (WIDE) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t e = at + lane * 4 + k * 128;
+      *reinterpret_cast<float4*>(t.p + e) = make_float4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+      if (t.copy)
+        *reinterpret_cast<uint2*>(t.copy + e) =
+            make_uint2(pack_bf16(p[4 * k], p[4 * k + 1]), pack_bf16(p[4 * k + 2], p[4 * k + 3]));
       if constexpr (BITS == 32) {
         *reinterpret_cast<float4*>(static_cast<float*>(t.m) + e) = make_float4(m[4 * k], m[4 * k + 1], m[4 * k + 2], m[4 * k + 3]);
         *reinterpret_cast<float4*>(static_cast<float*>(t.v) + e) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -236,10 +239,16 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   }
 }
 
-// Five blocks to an SM, although some values spill: instructions bound the 8-bit form as much as memory does, and more warps
-// hide both (176M values with 8-bit moments: 451 us, 497 with four blocks, 498 with six).
+// 40 warps to an SM for 8-bit moments, 48 registers: instructions bound that form as much as memory does, and more warps hide
+// both (176M values: 453 us, 475 with 32 warps and 64 registers).
+// (a call of its own: inlined, the two forms together make the kernel spill)
+template <typename G, int BITS>
+__device__ __noinline__ void last_run(const Tensor& t, int64_t at, const float b1, const float c1, const float b2, const float c2,
+                                      const float eps, const float root, const uint32_t key) {
+  run_of_256<G, BITS, false>(t, at, threadIdx.x & 31, b1, c1, b2, c2, eps, root, key);
+}
 template <typename G, int BITS, int MOST>
-__global__ void __launch_bounds__(kThreads, 5) k_adamw(const __grid_constant__ Args<MOST> a) {
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 10 : 8) k_adamw(const __grid_constant__ Args<MOST> a) {
   follow();
   for (int i = 0; i < a.n_counts; ++i)
     if (a.counts[2 * i + 1] != 0) return;
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_adamw(const __grid_constant__ A
   if (t.wide && at + kRun <= t.n)
     run_of_256<G, BITS, true>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
   else
-    run_of_256<G, BITS, false>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
+    last_run<G, BITS>(t, at, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
 }
 
 template <int MOST>
