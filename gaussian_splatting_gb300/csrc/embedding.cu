@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding_scan(const SortArgs a) {
 }
 
 template <typename I, int ITEMS>
-__global__ void __launch_bounds__(kThreads, 3) k_embedding_scatter(const SortArgs a) {
+__global__ void __launch_bounds__(kThreads, ITEMS == 16 ? 2 : 3) k_embedding_scatter(const SortArgs a) {
   follow();
   __shared__ uint32_t s_count[kWarps][256];  // of each warp's digits; then where its first of them goes in the tile
   __shared__ uint32_t s_start[256];          // where a digit's run begins in the tile
@@ -238,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_embedding_scatter(const SortArg
   const uint32_t mask = (1u << a.bits) - 1;
   for (int i = threadIdx.x; i < kWarps * 256; i += kThreads) s_count[i / 256][i % 256] = 0, s_key[i] = 0;
   const int64_t base = (int64_t)blockIdx.x * (kThreads * ITEMS) + warp * (32 * ITEMS) + lane;
-  uint32_t key[ITEMS], row[ITEMS];
-  uint16_t rank[ITEMS];
+  uint32_t key[ITEMS], row[ITEMS], rank[ITEMS / 2];  // (16 bits are enough for a rank)
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int64_t r = base + i * 32;
@@ -257,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_embedding_scatter(const SortArg
     const uint32_t d = (key[i] >> a.shift) & mask;
     const uint32_t same = peers_of(peers, d, in);
     const uint32_t before = s_count[warp][d];
-    rank[i] = (uint16_t)(before + __popc(same & ((1u << lane) - 1)));
+    const uint32_t mine = before + __popc(same & ((1u << lane) - 1));
+    rank[i / 2] = i % 2 ? rank[i / 2] | mine << 16 : mine;
     __syncwarp();
     if (in) s_count[warp][d] = before + __popc(same);  // (every peer stores the same)
     __syncwarp();
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_embedding_scatter(const SortArg
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     if (base + i * 32 >= a.rows) continue;
-    const uint32_t d = (key[i] >> a.shift) & mask, at = s_start[d] + s_count[warp][d] + rank[i];
+    const uint32_t d = (key[i] >> a.shift) & mask, at = s_start[d] + s_count[warp][d] + (rank[i / 2] >> (i % 2 * 16) & 0xffffu);
     s_key[at] = key[i], s_row[at] = row[i];
   }
   __syncthreads();
@@ -323,19 +323,20 @@ constexpr int kBatch = 8;  // a walker's part begins at a multiple of it
 // A walker's rows, a lane's vector of each, by their sorted positions in lists that are padded to kBatch (what lies behind the
 // last row is not used).  A position has a key, or `none` from `end` on; rows with the key `none` read as zeros.
 // Lists in global memory: eight rows at once in registers, and the next eight's keys while these are added up.
-template <typename T, int VE>
+template <typename T, int VE, typename P>
 struct ListedRows {
   using IO = VecIO<T, VE>;
-  using Pos = int64_t;
+  using Pos = P;
   static constexpr int B = 8;
   const uint32_t *keys, *order;
   const T* dy;  // at the lane's column
-  int64_t ldy, end;
+  int64_t ldy;
+  Pos end;
   uint32_t none;
   bool there;  // such a column
   uint32_t next_k[B], next_o[B], k[B];
   typename IO::Raw v[B];
-  __device__ __forceinline__ void ahead(int64_t p) {
+  __device__ __forceinline__ void ahead(Pos p) {
 #pragma unroll
     for (int h = 0; h < B; h += 4) {
       const uint4 q = *reinterpret_cast<const uint4*>(keys + p + h), o = *reinterpret_cast<const uint4*>(order + p + h);
@@ -343,8 +344,8 @@ struct ListedRows {
       next_o[h] = o.x, next_o[h + 1] = o.y, next_o[h + 2] = o.z, next_o[h + 3] = o.w;
     }
   }
-  __device__ __forceinline__ void start(int64_t p) { ahead(p); }
-  __device__ __forceinline__ void batch(int64_t p) {
+  __device__ __forceinline__ void start(Pos p) { ahead(p); }
+  __device__ __forceinline__ void batch(Pos p) {
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       k[u] = p + u < end ? next_k[u] : none;
@@ -365,8 +366,8 @@ __device__ __forceinline__ void copy_async16(void* to, const void* from) {
 template <typename T, int VE>
 struct RingRows {
   using IO = VecIO<T, VE>;
-  using Raw = typename IO::Raw;
   using Pos = int;
+  using Raw = typename IO::Raw;
   static constexpr bool kRing = sizeof(Raw) == 16;
   static constexpr int B = kRing ? 4 : 8;
   const uint16_t* keys;
@@ -501,7 +502,7 @@ __device__ __forceinline__ bool join(const float* from, const float* heads, cons
   return open;
 }
 
-constexpr int sum_blocks(int ve) { return ve == 8 ? 2 : 3; }  // of an SM, by the registers
+constexpr int sum_blocks(int ve) { return ve >= 4 ? 2 : 3; }  // of an SM, by the registers
 // G lanes to a walker, a vector each; gridDim.y slabs of columns.
 template <typename T, int VE, int G>
 __global__ void __launch_bounds__(kThreads, sum_blocks(VE)) k_embedding_sum(const SumArgs a) {
@@ -511,16 +512,16 @@ __global__ void __launch_bounds__(kThreads, sum_blocks(VE)) k_embedding_sum(cons
   __shared__ uint32_t s_flag[kWalkers], s_block;
   const int lane = threadIdx.x % G, walker = threadIdx.x / G;
   const int col = ((int)blockIdx.y * G + lane) * VE;
-  const int64_t begin = ((int64_t)blockIdx.x * kWalkers + walker) * a.per_walker;
-  const int64_t end = begin + a.per_walker < a.rows ? begin + a.per_walker : a.rows;
+  const int64_t from = ((int64_t)blockIdx.x * kWalkers + walker) * a.per_walker;
+  const int begin = (int)min(from, a.rows), end = (int)min(from + a.per_walker, a.rows);  // (at most 2^31 - 1024 rows)
   float *head = s_end[0] + threadIdx.x * VE, *tail = s_end[1] + threadIdx.x * VE;
   uint32_t code, word = 0, bits = 0;  // codes seen, gathered to words of the bitmap
   const bool tells = lane == 0 && blockIdx.y == 0;
-  ListedRows<T, VE> list;
+  ListedRows<T, VE, int> list;
   list.keys = a.keys, list.order = a.order, list.dy = static_cast<const T*>(a.dy) + col, list.ldy = a.ldy, list.end = end;
   list.none = (uint32_t)a.n, list.there = col < a.width;
   const uint32_t flag = walk<T, VE>(
-      list, a.keys, begin, a.rows, (uint32_t)a.n, head, tail, code,
+      list, a.keys, begin, (int)a.rows, (uint32_t)a.n, head, tail, code,
       [&](uint32_t c, const float* sum) { write_sum<T, VE>(a, c, col, sum); },
       [&](uint32_t c) {
         if (c >> 5 != word) {
@@ -757,8 +758,9 @@ __global__ void __launch_bounds__(1024) k_embedding_bucket_scan(const PartArgs a
   if (threadIdx.x < 8 && tiles) a.totals[bucket] = carry;
 }
 
-// The list of parts, for the next step: of the thread's four buckets' sizes and beginnings.
-__device__ __forceinline__ void list_parts(const PartArgs& a, uint4 sizes, uint4 first, uint32_t* s_sums) {
+// The list of parts, for the next step: of the thread's four buckets' sizes and beginnings.  (A call of its
+// own: inlined, it makes the kernel spill.)
+__device__ __noinline__ void list_parts(const PartArgs& a, uint4 sizes, uint4 first, uint32_t* s_sums) {
   const uint32_t size[4] = {sizes.x, sizes.y, sizes.z, sizes.w}, from[4] = {first.x, first.y, first.z, first.w};
   uint32_t parts[4], all = 0, several = 0, buckets = 0;
 #pragma unroll
@@ -794,19 +796,22 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_bucket_scatter(co
   uint2* s_pair = reinterpret_cast<uint2*>(counters);                      // and, once they have been read, the tile's pairs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kPartWarps * a.padded / 8; i += kPartThreads) reinterpret_cast<uint4*>(counters)[i] = uint4{};
-  const int64_t base = (int64_t)blockIdx.x * (kPartThreads * kPartItems) + warp * (32 * kPartItems) + lane;
+  const uint32_t base = blockIdx.x * (kPartThreads * kPartItems) + warp * (32 * kPartItems) + lane, rows = (uint32_t)a.s.rows;  // (rows < 2^31)
   uint32_t key[kPartItems], at[kPartItems / 2];  // (16 bits are enough for a place in the tile)
 #pragma unroll
   for (int i = 0; i < kPartItems; ++i)
-    key[i] = base + i * 32 < a.s.rows ? code_of<I>(a.s.idx, base + i * 32, a.s.n) : (uint32_t)a.s.n;
-  uint4 in_all = make_uint4(0u, 0u, 0u, 0u), before = in_all;
-  if ((int)threadIdx.x * 4 < a.padded) {
-    in_all = reinterpret_cast<const uint4*>(a.totals)[threadIdx.x];
-    if ((int)blockIdx.x < a.tiles) before = reinterpret_cast<const uint4*>(a.counts + (int64_t)blockIdx.x * a.padded)[threadIdx.x];
-  }
+    key[i] = base + i * 32 < rows ? code_of<I>(a.s.idx, base + i * 32, a.s.n) : (uint32_t)a.s.n;
+  const bool mine = (int)threadIdx.x * 4 < a.padded;  // four buckets
   uint32_t total;
-  const uint4 first = four_starts(in_all, s_sums, total);  // (its barriers also end the clearing above)
-  if ((int)blockIdx.x == a.tiles) return list_parts(a, in_all, first, s_sums);
+  {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u), in_all = mine ? reinterpret_cast<const uint4*>(a.totals)[threadIdx.x] : none;
+    uint4 before = none;
+    if (mine && (int)blockIdx.x < a.tiles) before = reinterpret_cast<const uint4*>(a.counts + (int64_t)blockIdx.x * a.padded)[threadIdx.x];
+    const uint4 first = four_starts(in_all, s_sums, total);  // (its barriers also end the clearing above)
+    if ((int)blockIdx.x == a.tiles) return list_parts(a, in_all, first, s_sums);
+    if (mine)
+      reinterpret_cast<uint4*>(s_out)[threadIdx.x] = make_uint4(first.x + before.x, first.y + before.y, first.z + before.z, first.w + before.w);
+  }
 #pragma unroll
   for (int i = 0; i < kPartItems; ++i) {
     const uint32_t rank = rank_of(counters + warp * a.padded, key[i] >> a.shift, key[i] < (uint32_t)a.s.n);
@@ -814,10 +819,10 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_bucket_scatter(co
   }
   __syncthreads();
   const uint4 start = four_starts(four_totals(counters, a.padded), s_sums, total);
-  if ((int)threadIdx.x * 4 < a.padded) {
+  if (mine) {
     reinterpret_cast<uint4*>(s_start)[threadIdx.x] = start;
-    reinterpret_cast<uint4*>(s_out)[threadIdx.x] = make_uint4(first.x + before.x - start.x, first.y + before.y - start.y,
-                                                              first.z + before.z - start.z, first.w + before.w - start.w);
+    const uint4 to = reinterpret_cast<uint4*>(s_out)[threadIdx.x];
+    reinterpret_cast<uint4*>(s_out)[threadIdx.x] = make_uint4(to.x - start.x, to.y - start.y, to.z - start.z, to.w - start.w);
   }
   __syncthreads();
 #pragma unroll
@@ -828,7 +833,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_bucket_scatter(co
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPartItems; ++i)
-    if (key[i] < (uint32_t)a.s.n) s_pair[at[i / 2] >> (i % 2 * 16) & 0xffffu] = make_uint2(key[i], (uint32_t)(base + i * 32));
+    if (key[i] < (uint32_t)a.s.n) s_pair[at[i / 2] >> (i % 2 * 16) & 0xffffu] = make_uint2(key[i], base + i * 32);
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < total; i += kPartThreads) {
     const uint2 p = s_pair[i];
@@ -864,13 +869,13 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   for (int i = threadIdx.x; i < kPartWarps * digits / 8; i += kPartThreads) reinterpret_cast<uint4*>(counters)[i] = uint4{};
   constexpr int kItems = kMostRows / kPartThreads;
   const int share = (m + kPartThreads - 1) / kPartThreads * 32, i0 = warp * share + lane;  // a warp's pairs
-  uint32_t key[kItems], row[kItems];  // local codes, their ranks above them
+  uint32_t key[kItems];  // local codes, their ranks above them (rows are read when they are placed: registers)
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    key[i] = 0u, row[i] = 0u;
+    key[i] = 0u;
     if (i * 32 < share && i0 + i * 32 < m) {
-      const uint2 v = p.pairs[part.begin + i0 + i * 32];
-      key[i] = v.x & (uint32_t)(p.codes - 1), row[i] = v.y;
+      const uint32_t v = p.pairs[part.begin + i0 + i * 32].x;
+      key[i] = v & (uint32_t)(p.codes - 1);
     }
   }
   __syncthreads();
@@ -894,24 +899,24 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   for (int i = 0; i < kItems; ++i)
     if (i * 32 < share && i0 + i * 32 < m) {
       const uint32_t to = key[i] >> 16;
-      s_key[to] = (uint16_t)key[i], s_row[to] = row[i];
+      s_key[to] = (uint16_t)key[i], s_row[to] = p.pairs[part.begin + i0 + i * 32].y;
     }
   __syncthreads();
   // the sums
   const bool whole = part.slot == kWhole;
-  const int64_t code0 = (int64_t)part.bucket << p.shift;
+  const uint32_t code0 = part.bucket << p.shift;  // (n <= 2^22)
   const int walkers = kPartThreads / g, wl = threadIdx.x % g, walker = threadIdx.x / g;  // (threads may be left over)
   const int col = ((int)blockIdx.y * g + wl) * VE;
   const int per = (m + walkers * kBatch - 1) / (walkers * kBatch) * kBatch;
   const int begin = walker < walkers ? min(walker * per, m) : m, end = min(begin + per, m);
   float *head = ends + threadIdx.x * VE, *tail = ends + (kPartThreads + threadIdx.x) * VE;
-  float* to = p.sums + (whole ? (int64_t)0 : (int64_t)part.slot * p.codes * a.ldp) + col;
   auto put = [&](uint32_t c, const float* sum) {
     if (whole) {
-      write_sum<T, VE>(a, (uint32_t)code0 + c, col, sum);
+      write_sum<T, VE>(a, code0 + c, col, sum);
     } else if (col < a.width) {
+      float* to = p.sums + ((int64_t)part.slot * p.codes + c) * a.ldp + col;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) to[(int64_t)c * a.ldp + e] = sum[e];
+      for (int e = 0; e < VE; ++e) to[e] = sum[e];
     }
   };
   uint32_t code;
@@ -924,7 +929,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   const int words = (p.codes + 31) / 32;
   for (int w = warp; w < words; w += kPartWarps) {
     const int c = w * 32 + lane;
-    const bool there = c < p.codes && code0 + c < a.n;
+    const bool there = c < p.codes && code0 + c < (uint32_t)a.n;
     const uint32_t have = __ballot_sync(0xffffffffu, there && s_start[min(c, digits - 1)] != s_start[min(c, digits - 1) + 1]);
     if (whole) {
       const uint32_t empty = __ballot_sync(0xffffffffu, there) & ~have;
@@ -1113,7 +1118,7 @@ __global__ void __launch_bounds__(kFewThreads) k_embedding_few(const FewArgs f) 
   const int begin = min(walker * per, (int)m), end = min(begin + per, (int)m);
   float *head = ends + threadIdx.x * VE, *tail = ends + (kFewThreads + threadIdx.x) * VE;
   uint32_t code;
-  ListedRows<T, VE> rows_of;
+  ListedRows<T, VE, int64_t> rows_of;  // (32 bits spill)
   rows_of.keys = key[from], rows_of.order = row[from], rows_of.dy = static_cast<const T*>(a.dy) + col, rows_of.ldy = a.ldy;
   rows_of.end = end, rows_of.none = none, rows_of.there = col < a.width;
   const uint32_t flag = walk<T, VE>(

@@ -692,6 +692,72 @@ def test_adamw_seed_and_step_decide_the_bits():
     assert torch.equal(a, once(1, 4)) and not torch.equal(a, once(2, 4)) and torch.equal(a, once(1 + (1 << 32), 4))
 
 
+# ------------------------------------------------------------------ together
+def _step_of_all(p, views, at, pixel, maps, want, groups, scale):
+    """A head's training step: codes and normalised image features into two linear layers, a loss, every gradient.
+    p: table, gamma, beta, w1, b1, w2, b2."""
+    table, gamma, beta, w1, b1, w2, b2 = p
+    f, mean, rstd = dense.groupnorm_fwd(maps, gamma, beta, groups, views, "silu")
+    e = dense.embedding_fwd(table, at, scale)
+    q = dense.embedding_fwd(f, pixel)  # the pixel's features; zeros where no view saw the Gaussian
+    h, z = dense.linear_fwd(e, w1, b1, q, "gelu", keep_z=True)
+    out, _ = dense.linear_fwd(h, w2, b2)
+    dout = out - want  # of half the squared distance
+    dh, dw2, db2 = dense.linear_bwd(dout, h, w2)
+    de, dw1, db1 = dense.linear_bwd(dh, e, w1, z, "gelu")
+    df = dense.embedding_bwd(dh, pixel, f.shape[0])  # the residual's gradient is dh
+    dmaps, dgamma, dbeta = dense.groupnorm_bwd(df, maps, gamma, beta, mean, rstd, "silu")
+    return out, [dense.embedding_bwd(de, at, table.shape[0], scale), dgamma, dbeta, dw1, db1, dw2, db2], dmaps
+
+
+def _step_of_all_64(p, views, at, pixel, maps, want, groups, scale):
+    p = [t.double().requires_grad_() for t in p]
+    maps = maps.double().requires_grad_()
+    table, gamma, beta, w1, b1, w2, b2 = p
+    x = maps.view(views, -1, groups, maps.shape[1] // groups)
+    mu = x.mean((1, 3), keepdim=True)
+    h = (x - mu) * ((x - mu).square().mean((1, 3), keepdim=True) + 1e-5) ** -0.5
+    f = _act(h.view(maps.shape) * gamma + beta, "silu")
+
+    def rows(t, idx, by):
+        i = idx.long()
+        there = (i >= 0) & (i < t.shape[0])
+        return t[torch.where(there, i, 0)] * there[:, None] * by
+
+    e, q = rows(table, at, scale), rows(f, pixel, 1.0)
+    h = _act(e @ w1.t() + b1, "gelu") + q
+    out = h @ w2.t() + b2
+    (0.5 * (out - want.double()).square().sum()).backward()
+    return out.detach(), [t.grad for t in p], maps.grad
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("gaussians,codes,views,pixels", [(3000, 200, 5, 150), (1, 1, 1, 1), (9001, 70_000, 2, 1537)])
+def test_codes_norm_layers_and_update_together(gaussians, codes, views, pixels, bits):
+    width, groups, outs, scale = 32, 4, 11, 2.0
+    p = [_rand((codes, width), F32, 80, 0.3), _rand((width,), F32, 81, 0.1, mean=1.0), _rand((width,), F32, 82, 0.1),
+         _rand((width, width), F32, 83, 0.2), _rand((width,), F32, 84, 0.1), _rand((outs, width), F32, 85, 0.2),
+         _rand((outs,), F32, 86, 0.1)]
+    maps = _rand((views * pixels, width), F32, 87)
+    at, pixel = _indices(gaussians, codes, "skewed", 88), _indices(gaussians, views * pixels, "gaps", 89)
+    want = _rand((gaussians, outs), F32, 90)
+    m, v, scales = dense.adamw_state(p, bits)
+    for step in (1, 2, 3):
+        out, grads, dmaps = _step_of_all(p, views, at, pixel, maps, want, groups, scale)
+        out64, grads64, dmaps64 = _step_of_all_64(p, views, at, pixel, maps, want, groups, scale)
+        # Each of at most ten stages is off by 2^-17 of its output's norm or less (128 roundings of 2^-24 in a row, more than
+        # any of its sums takes one after the other), and hands an error on no more than four times as large.
+        for got, ref in zip([out, *grads, dmaps], [out64, *grads64, dmaps64]):
+            assert (got - ref).norm() <= 40 * 2.0 ** -17 * ref.norm() + TINY
+        before = [t.clone() for t in p]
+        state = [[_decode(t.view(-1), s).view(t.shape) for t, s in zip(x, scales[k])] if bits == 8 else [t.double() for t in x]
+                 for k, x in enumerate((m, v))]
+        dense.adamw(p, grads, m, v, step, 1e-2, BETAS, EPS, 0.05, scales=scales, seed=4)
+        for new, old, g, m0, v0 in zip(p, before, grads, *state):
+            wp, _, _, tp, _, _ = _adamw_64(old, g, m0, v0.square() if bits == 8 else v0, step, 1e-2, 0.05)
+            _close(new, wp, tp, f"step {step}")
+
+
 # ------------------------------------------------------------------ streams, graphs
 def _everything(seed):
     """One call of each operator on inputs of its own; the inputs, and what the calls return."""
