@@ -16,7 +16,7 @@
 //   more         a radix sort of (code, row) pairs, up to eight bits a pass, each pass three kernels (digit counts of tiles,
 //                their scan by digit, a scatter through shared memory), then the sums;
 //   many         one such pass into up to 2,048 buckets of neighbouring codes; the rest of the sort is done in shared memory by
-//                the blocks that add a bucket up.  11M rows of 32 float32, 2M codes: 402 us against 675 by the sort, of which
+//                the blocks that add a bucket up.  11M rows of 32 float32, 2M codes: 398 us against 675 by the sort, of which
 //                the sums take 300 (their bytes at the copy's rate: 258), the pairs' scatter 60, counts and their scan 25.
 #include <algorithm>
 
@@ -1227,17 +1227,19 @@ struct Buckets {
   int64_t parts, several, many, words;  // at most: parts, those of buckets with more than one, such buckets; of a part's codes
 };
 // Whether the buckets take a call, and how.  They save passes over the pairs, but the sort's shorter kernels are done sooner
-// where there is little to sort.  Us by the sort and by buckets: 4,096 codes of 64 bfloat16 1M rows 59 and 66, 2M 107 and 95,
-// 10M 459 and 358; 1M codes of 32 float32 500K rows 65 and 78, 1M 103 and 104, 10M 579 and 437; 300K codes of 32 float32 1M rows
-// 90 and 64; codes that the sort does in one pass (100 of 32 float32) 2M rows 91 and 101, 10M 376 and 390.
+// where there is little to sort.  Us by the sort and by buckets: 4,096 codes of 64 bfloat16 1M rows 60 and 66, 2M 107 and 94,
+// 10M 462 and 356; 100K codes of 32 float32 1M rows 73 and 82, 2M 125 and 118, 10M 524 and 421; 1M codes of 32 float32 1M rows 91
+// and 104, 2M 150 and 139, 10M 567 and 437; codes that the sort does in one pass (100 of 32 float32) 2M rows 87 and 101.
 bool buckets_take(const gs_embedding_desc* d, Buckets& b) {
-  if (d->n <= 256 || d->n > (int64_t)kMostBuckets * kMostCodes || d->rows < (d->n < 65536 ? 3 << 19 : 1 << 20)) return false;
-  // parts of up to 6,144 rows, or fewer, so that there are 608 of them (152 SMs, 2 blocks each, twice)
-  b.cap = (int)std::min<int64_t>((d->rows / 608 + 511) / 512 * 512, kMostRows);
+  if (d->n <= 256 || d->n > (int64_t)kMostBuckets * kMostCodes || d->rows < (3 << 19)) return false;
+  int least = 0;  // codes to a bucket, as a shift, by the number of buckets
+  while ((d->n - 1) >> least >= kMostBuckets) ++least;
+  // parts of up to 6,144 rows, or fewer, so that there are 608 of them (152 SMs, 2 blocks each, twice), but of several times a
+  // bucket's codes: the sums of parts are kept for each of these
+  b.cap = (int)std::min<int64_t>(std::max<int64_t>((d->rows / 608 + 511) / 512 * 512, 4 << least), kMostRows);
   // codes to a bucket so that an average one is nearly a part
-  b.shift = 0;
-  while (b.shift < 11 && (d->rows << (b.shift + 1)) / d->n <= b.cap * 15 / 16) ++b.shift;
-  while ((d->n - 1) >> b.shift >= kMostBuckets) ++b.shift;
+  b.shift = least;
+  while (b.shift < 11 && (d->rows << (b.shift + 1)) / d->n <= b.cap * 15 / 16 && (8 << b.shift) <= b.cap) ++b.shift;
   b.count = (int)((d->n - 1) >> b.shift) + 1, b.padded = (b.count + 3) / 4 * 4, b.codes = 1 << b.shift;
   b.tiles = (int)((d->rows + kPartThreads * kPartItems - 1) / (kPartThreads * kPartItems));
   b.many = d->rows / b.cap, b.parts = b.count + b.many, b.several = 2 * b.many;

@@ -553,9 +553,10 @@ gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy, const voi
  * gs_embedding_bwd -- the table's gradient, from dy [rows][width] (stride ldy):
  *   dtable[v] = scale (sum of dy[r] over the rows r with idx[r] = v), n x width, stride ldt, every row overwritten (a
  *   code that no row has gets zeros).  dtable must not overlap dy or idx.
- *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the arguments' sizes alone
+ *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the sizes and the indices
  *   decide: no atomics on values, the same bits each run.
- *   workspace  gs_embedding_bwd_workspace_size(d) bytes, 256-byte aligned.
+ *   workspace  gs_embedding_bwd_workspace_size(d) bytes, 256-byte aligned (may be 0: NULL).  From 1.5M rows on it may
+ *              hold float32 sums, two thirds as many rows of them as dy has.
  * rows == 0 writes zeros.
  */
 typedef struct {

@@ -68,11 +68,13 @@ def test_embedding_refuses_missing_and_misaligned_arrays(lib):
             assert _grad(lib, _codes(), **{name: at}) == N.GS_ERR_INVALID
             assert name.encode() in lib.gs_last_error()
     assert _look(lib, _codes(index_bits=64), idx=P + 4) == N.GS_ERR_INVALID
-    need = _size(lib.gs_embedding_bwd_workspace_size, _codes())
-    assert need > 0
-    assert _grad(lib, _codes(), n=need - 1) == N.GS_ERR_INVALID
-    assert _grad(lib, _codes(), ws=None) == N.GS_ERR_INVALID
-    assert _grad(lib, _codes(), ws=P + 16) == N.GS_ERR_INVALID
+    assert _size(lib.gs_embedding_bwd_workspace_size, _codes()) == 0  # few rows need none
+    for many in (dict(rows=20_000), dict(rows=2_000_000, n=5000)):
+        need = _size(lib.gs_embedding_bwd_workspace_size, _codes(**many))
+        assert need > 0
+        assert _grad(lib, _codes(**many), n=need - 1) == N.GS_ERR_INVALID
+        assert _grad(lib, _codes(**many), ws=None) == N.GS_ERR_INVALID
+        assert _grad(lib, _codes(**many), ws=P + 16) == N.GS_ERR_INVALID
     # nothing to do
     assert _look(lib, _codes(rows=0), table=None, idx=None, y=None) == N.GS_OK
     assert _grad(lib, _codes(n=0), dy=None, idx=None, dtable=None, ws=None, n=0) == N.GS_OK
