@@ -78,6 +78,21 @@ __device__ __forceinline__ int64_t parts_of(const Shape& s, int64_t sample, int 
   return ((sample * s.slabs + slab) * s.span + (group - slab * s.cols / s.per)) * s.chunks;
 }
 
+// The second pass's kernel copies its first rows before it waits for the first one's sums.  What it reads then is the call's
+// input, which the kernel before the first pass may have written: the first pass lets the second begin only when that one is
+// done.  (Copies of 16 bytes, which go past L1; shorter ones wait.)
+__device__ __forceinline__ void wait_for_inputs() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename R>
+__device__ __forceinline__ void start_and_follow(R& r, int count) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (sizeof(typename R::Raw) == 16) r.start(count);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (sizeof(typename R::Raw) != 16) r.start(count);
+}
+
 // The rows of a thread in A arrays, through a ring of its own in shared memory: D rows ahead are copied asynchronously, which
 // takes no registers and, as nobody else reads the thread's slots, no barriers.
 extern __shared__ __align__(16) char s_ring[];
@@ -372,7 +387,7 @@ __device__ __forceinline__ void write_chunk(const FwdArgs& a, const Place& at) {
   const int col = at.col0 + tx * VE, rows = (int)(at.end - at.row);
   const int count = ty < ny && col < s.width && ty < rows ? (rows - ty + ny - 1) / ny : 0;
   Rows<T, VE, 1> r{{static_cast<const T*>(a.x) + (at.row + ty) * a.ldx + col}, {(int64_t)ny * a.ldx}};
-  r.start(count);
+  start_and_follow(r, count);
   float2* s_stat = reinterpret_cast<float2*>(s_ring + kRing);
   group_stats(a, at, s_stat);
   __syncthreads();
@@ -410,13 +425,12 @@ __device__ __forceinline__ void write_chunk(const FwdArgs& a, const Place& at) {
 
 template <typename T, int VE>
 __global__ void __launch_bounds__(kThreads, 4) k_groupnorm_sums(const FwdArgs a) {
-  follow();
+  wait_for_inputs();
   sum_chunk<T, VE>(a, Place(a.s, blockIdx.x));
 }
 // (backwards: the rows that were read last are still in L2)
 template <typename T, int VE, bool ONE, int ACT>
 __global__ void __launch_bounds__(kThreads, 4) k_groupnorm_write(const FwdArgs a) {
-  follow();
   write_chunk<T, VE, ONE, ACT>(a, Place(a.s, gridDim.x - 1 - blockIdx.x));
 }
 
@@ -560,7 +574,7 @@ __device__ __forceinline__ void grad_write(const BwdArgs& a, const Place& at) {
   r.at[0] = static_cast<const T*>(a.x) + row * a.ldx + col, r.step[0] = (int64_t)ny * a.ldx;
   r.at[1] = static_cast<const T*>(a.dy) + row * a.lddy + col, r.step[1] = (int64_t)ny * a.lddy;
   if constexpr (A == 3) r.at[2] = static_cast<const T*>(a.skip) + row * a.ldskip + col, r.step[2] = (int64_t)ny * a.ldskip;
-  r.start(count);
+  start_and_follow(r, count);
   float2* s_mean = reinterpret_cast<float2*>(s_ring + kRing);  // of g and of g h, by the slab's groups
   grad_means(a, at, s_mean);
   __syncthreads();
@@ -649,13 +663,13 @@ __global__ void __launch_bounds__(kThreads) k_groupnorm_fold(const SumFold f) {
 constexpr int grad_blocks(int ve, bool one) { return ve == 8 ? (one ? 3 : 2) : ve == 1 ? 3 : one ? 4 : 3; }
 template <typename T, int VE, bool ONE, int ACT>
 __global__ void __launch_bounds__(kThreads, grad_blocks(VE, ONE)) k_groupnorm_grad_sums(const BwdArgs a) {
-  follow();
+  wait_for_inputs();
   grad_sums<T, VE, ONE, ACT>(a, Place(a.s, blockIdx.x));
 }
 template <typename T, int VE, bool ONE, int ACT, int A>
 __global__ void __launch_bounds__(kThreads, grad_blocks(VE, ONE)) k_groupnorm_grad_write(const BwdArgs a, const SumFold f, const unsigned folds) {
-  follow();
   if (blockIdx.x < folds) {  // beside the chunks, rather than behind them
+    follow();
     if (blockIdx.y == 0) fold<T>(f, blockIdx.x);
     return;
   }
@@ -701,13 +715,14 @@ size_t part_bytes(const Shape& s) {
 size_t joined_bytes(const Shape& s) { return (sizeof(float2) * (size_t)s.samples * s.groups + 255) / 256 * 256; }
 // Whether a kernel between the passes joins the parts.  It costs a launch, some 3 us; without it each of an SM's blocks, one
 // after the other, waits for the parts, eight loads a lane at a time (12 maps of 13,604 x 952 float32 backward, 390 chunks of 119
-// groups: 471 us with it, 683 without; 4 images of 1236 x 820 x 64, 1,026 chunks of 8 groups: 392 either way).
+// groups: 275 turns in a row, 471 us with it, 683 without; 4 images of 1236 x 820 x 64, 1,026 chunks of 8 groups: 45 turns, 394
+// with it, 392 without).
 bool joins(const Shape& s, int arrays) {
   int lanes = 32;
   while (lanes > 1 && s.span * lanes > kThreads) lanes /= 2;
   const int64_t held = 152 * (arrays == 1 ? 4 : 3), waves = (s.samples * s.chunks * s.slabs + held - 1) / held;
   const int64_t turns = (s.chunks + 8 * lanes - 1) / (8 * lanes);
-  return turns > 1 && waves * turns * ((s.span * lanes + kThreads - 1) / kThreads) > 4;
+  return turns > 1 && waves * turns * ((s.span * lanes + kThreads - 1) / kThreads) > 64;
 }
 dim3 join_grid(const Shape& s) { return dim3((unsigned)((s.samples * s.groups + kThreads / 32 - 1) / (kThreads / 32))); }
 // over the vectors that the arrays' alignment may lead to
