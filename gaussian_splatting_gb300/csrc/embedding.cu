@@ -54,14 +54,14 @@ struct FwdArgs {
   bool stream;
 };
 
-// Vectors of a thread's unit: short ones share the arithmetic of their place, four of 4 bytes (33K rows of 322 float32: 13.0
-// us, 19.4 alone) or two of 2 (332K rows of 393 bfloat16: 164 us, 290 with eight, 274 alone).
-constexpr int unit_of(int vector_bytes) { return vector_bytes == 16 ? 1 : vector_bytes == 4 ? 4 : 2; }
+// Vectors of a thread's unit: two of less than 16 bytes share the arithmetic of their place (300K rows of 394 bfloat16: 87 us,
+// 117 with four, 114 alone; of 393 float32: 162, 150 with four, 263 alone; 332K of 393 bfloat16: 164, 290 with eight, 274 alone).
+constexpr int unit_of(int vector_bytes) { return vector_bytes == 16 ? 1 : 2; }
 template <typename T, int VE, typename I>
 __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
   follow();
   using IO = VecIO<T, VE>;
-  constexpr int K = unit_of(sizeof(typename IO::Raw)), U = K == 4 ? 2 : 4;
+  constexpr int K = unit_of(sizeof(typename IO::Raw)), U = 4;
   const int64_t first = (int64_t)blockIdx.x * (kThreads * U);
   const int64_t r0 = first / a.per_row;
   const uint32_t c0 = (uint32_t)(first - r0 * a.per_row);
@@ -1397,7 +1397,7 @@ extern "C" gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* ta
   if (gs_status s = check_idx(where, d, idx)) return s;
   const int ve = vector_of(d, table, y);
   const int k = unit_of(ve * (int)gs::dtype_size(d->dtype));
-  const int64_t per_row = (d->width + k * ve - 1) / (k * ve), units = d->rows * per_row, of_block = kThreads * (k == 4 ? 2 : 4);
+  const int64_t per_row = (d->width + k * ve - 1) / (k * ve), units = d->rows * per_row, of_block = kThreads * 4;
   const int64_t blocks = (units + of_block - 1) / of_block;
   if (blocks > INT32_MAX) return gs::set_error(GS_ERR_INVALID, "%s: y is too large", where);
   const FwdArgs a{table, idx, y, d->rows, d->n, d->ldt, d->ldy, (uint32_t)per_row,

@@ -12,7 +12,12 @@
 // the statistics stay in registers and every access of a warp is a run of whole sectors.  The variance is taken about a value of the
 // thread's own rows (their first), so that it loses nothing where the mean is far from zero: a pivot p among n values with
 // squared distances M from their mean has n (p - mean)^2 <= n M.  Chunks' sums are joined about the joint mean, in a fixed order.
-// What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2.
+// What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2, or a small kernel
+// between the passes does.
+//
+// 16 maps of 15,965 x 256 bfloat16, SiLU: 68 us, 58 for two readings and a writing at the copy's rate (in one pass, a slab of
+// groups held in the shared memory of a cluster of blocks, it took 124: 16 to 24 warps an SM do not hide the arithmetic's
+// latency).  4 images of 1236 x 820 x 64 bfloat16 backward: 390 us, 382 for the two passes' bytes.
 #include <algorithm>
 #include <cmath>
 
@@ -686,9 +691,10 @@ __global__ void k_groupnorm_empty(float* mean, float* rstd, int64_t n, float val
 
 // ------------------------------------------------------------------ host
 // Chunks of about 256 KB of input, but as many as the device holds blocks of (152 SMs, 4 each, of the gradient's 3; 4 maps of
-// 3,927 x 200 float32 backward: 21 us with 3, 28 with 4), and of at least 4 rows a thread: a block's beginning and end take some 4 us, which smaller chunks repeat too often (16 maps of 15,965 x 256
-// bfloat16: 71 us with chunks of 215 KB, 93 with 54, 156 with 27), and the SMs do not get equal shares of the memory's rate,
-// which larger ones do not even out (4 images of 1236 x 820 x 64 backward: 404 us with 284 KB, 416 with 1.1 MB).
+// 3,927 x 200 float32 backward: 21 us with 3, 28 with 4), and of at least 4 rows a thread: a block's beginning and
+// end take some 4 us, which smaller chunks repeat too often (16 maps of 15,965 x 256 bfloat16: 71 us with chunks of 215 KB, 93 with
+// 54, 156 with 27), and the SMs do not get equal shares of the memory's rate, which larger ones do not even out (4 images of 1236 x
+// 820 x 64 backward: 404 us with 284 KB, 416 with 1.1 MB).
 constexpr int64_t kChunkBytes = 256 << 10;
 Shape shape_of(const gs_groupnorm_desc* d, int ve, int arrays) {
   Shape s{};

@@ -2,8 +2,8 @@
 
 ``linear_fwd`` / ``linear_bwd`` (``y = act(x w^T + bias) + residual``), ``layernorm_fwd`` / ``layernorm_bwd``,
 ``groupnorm_fwd`` / ``groupnorm_bwd`` (channels-last feature maps, with an activation), ``embedding_fwd`` /
-``embedding_bwd`` (learned codes) and ``adamw`` (the update of all of a network's tensors) check shapes, types, devices and strides (``ValueError``), allocate what the caller did not
-hand in and call the entry points of the same names in libgs.so (``native.gs_linear_fwd`` and so on, which take
+``embedding_bwd`` (learned codes) and ``adamw`` (the update of all of a network's tensors) check shapes, types, devices
+and strides (``ValueError``), allocate what the caller did not hand in and call the entry points of the same names in libgs.so (``native.gs_linear_fwd`` and so on, which take
 addresses), where the formulas stand.  Matrices are 2-D CUDA tensors, float32 or bfloat16, whose rows may be any
 distance apart (``stride(1) == 1``); the arrays of one call share one type.  Nothing synchronises with
 the host, and nothing is kept between calls.
