@@ -342,7 +342,7 @@ extern "C" gs_status gs_adamw(const gs_adamw_desc* d, const gs_adamw_tensor* ten
     return gs::set_error(GS_ERR_INVALID, "%s: state_bits must be 32 or 8, got %d", where, d->state_bits);
   for (int i = 0; i < count; ++i) {
     const gs_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n > (int64_t(1) << 41)) return gs::set_error(GS_ERR_INVALID, "%s: bad size of tensor %d", where, i);
+    if (t.n < 0 || t.n > (int64_t(1) << 40)) return gs::set_error(GS_ERR_INVALID, "%s: bad size of tensor %d", where, i);
     if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
       return gs::set_error(GS_ERR_INVALID, "%s: lr or weight_decay of tensor %d is not finite", where, i);
     if (t.n == 0) continue;

@@ -4,7 +4,7 @@
 // Mathematics: y[r] = scale table[idx[r]]; dtable[v] = scale sum over {r: idx[r] = v} of dy[r].
 //
 // Both are bound by memory.  The forward reads the indices and what it needs of the table, and writes y once: a thread
-// holds 16 bytes of a row, four times in flight (10M rows of 64 bfloat16: 228 us, 196 at the copy's rate; 242 with stores
+// holds 16 bytes of a row, four times in flight (10M rows of 64 bfloat16: 230 us, 196 at the copy's rate; 242 with stores
 // that stay in L2).
 //
 // The backward must not add in whatever order atomics come, and one code may have any number of rows, so the rows are
@@ -16,8 +16,8 @@
 //   more         a radix sort of (code, row) pairs, up to eight bits a pass, each pass three kernels (digit counts of tiles,
 //                their scan by digit, a scatter through shared memory), then the sums;
 //   many         one such pass into up to 2,048 buckets of neighbouring codes; the rest of the sort is done in shared memory by
-//                the blocks that add a bucket up.  11M rows of 32 float32, 2M codes: 398 us against 675 by the sort, of which
-//                the sums take 300 (their bytes at the copy's rate: 258), the pairs' scatter 60, counts and their scan 25.
+//                the blocks that add a bucket up.  11M rows of 32 float32, 2M codes: 396 us against 675 by the sort, of which
+//                the sums take 300 (their bytes at the copy's rate: 258), the pairs' scatter 60, counts and their scan 22.
 #include <algorithm>
 
 #include "dense.cuh"
@@ -30,18 +30,14 @@ constexpr int kPartThreads = 512;  // of the backward's kernels by buckets
 
 // ------------------------------------------------------------------ forward
 // Outputs of this size or more are not held by L2 (129 MB) until they are read: they are stored first to be evicted, and leave
-// it to the table.
+// it to the table, in vectors of 16 bytes (shorter ones take longer so).
 constexpr int64_t kStreamBytes = 64 << 20;
-template <typename T, int VE>
-__device__ __forceinline__ void store_row(T* p, const float* f, bool stream) {
-  if constexpr (sizeof(typename VecIO<T, VE>::Raw) == 16) {
-    if (stream) {
-      typename VecIO<T, VE>::Raw r;
-      VecIO<T, VE>::store(reinterpret_cast<T*>(&r), f);
-      return __stcs(reinterpret_cast<decltype(r)*>(p), r);
-    }
-  }
-  VecIO<T, VE>::store(p, f);
+__device__ __forceinline__ void store_first_out(float* p, const float* f) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+}
+__device__ __forceinline__ void store_first_out(__nv_bfloat16* p, const float* f) {
+  __stcs(reinterpret_cast<uint4*>(p),
+         make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
 }
 struct FwdArgs {
   const void* table;
@@ -51,13 +47,12 @@ struct FwdArgs {
   uint32_t per_row, magic;  // units of a row; 2^32 / per_row rounded up
   uint32_t width;
   float scale;
-  bool stream;
 };
 
 // Vectors of a thread's unit: two of less than 16 bytes share the arithmetic of their place (300K rows of 394 bfloat16: 87 us,
 // 117 with four, 114 alone; of 393 float32: 162, 150 with four, 263 alone; 332K of 393 bfloat16: 164, 290 with eight, 274 alone).
 constexpr int unit_of(int vector_bytes) { return vector_bytes == 16 ? 1 : 2; }
-template <typename T, int VE, typename I>
+template <typename T, int VE, bool STREAM, typename I>
 __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
   follow();
   using IO = VecIO<T, VE>;
@@ -99,7 +94,8 @@ __global__ void __launch_bounds__(kThreads) k_embedding_fwd(const FwdArgs a) {
       IO::unpack(v[u][k], f);
 #pragma unroll
       for (int e = 0; e < VE; ++e) f[e] = there ? f[e] * a.scale : 0.f;
-      if (K == 1 || col[u] + k * VE < a.width) store_row<T, VE>(to + k * VE, f, a.stream);
+      if constexpr (STREAM) store_first_out(to, f);
+      else if (K == 1 || col[u] + k * VE < a.width) IO::store(to + k * VE, f);
     }
   }
 }
@@ -697,11 +693,24 @@ __global__ void __launch_bounds__(kPartThreads) k_embedding_bucket_count(const P
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < a.padded; i += kPartThreads) s[i] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * (kPartThreads * kPartItems) + (threadIdx.x >> 5) * (32 * kPartItems) + lane;
+  // (in any order: four neighbours a thread)
+  const int64_t base = (int64_t)blockIdx.x * (kPartThreads * kPartItems) + threadIdx.x * 4;
   uint32_t key[kPartItems];
+  if (base - threadIdx.x * 4 + kPartThreads * kPartItems <= a.s.rows && reinterpret_cast<uintptr_t>(a.s.idx) % (4 * sizeof(I)) == 0) {
 #pragma unroll
-  for (int i = 0; i < kPartItems; ++i)
-    key[i] = base + i * 32 < a.s.rows ? code_of<I>(a.s.idx, base + i * 32, a.s.n) : (uint32_t)a.s.n;
+    for (int i = 0; i < kPartItems; i += 4) {
+      struct alignas(sizeof(I) == 4 ? 16 : 32) Four { I v[4]; };
+      const Four f = *reinterpret_cast<const Four*>(static_cast<const I*>(a.s.idx) + base + i * kPartThreads);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) key[i + j] = code_of<I>(f.v, j, a.s.n);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPartItems; ++i) {
+      const int64_t r = base + i / 4 * (4 * kPartThreads) + i % 4;
+      key[i] = r < a.s.rows ? code_of<I>(a.s.idx, r, a.s.n) : (uint32_t)a.s.n;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kPartItems; ++i) {
     const bool in = key[i] < (uint32_t)a.s.n;
@@ -1397,17 +1406,21 @@ extern "C" gs_status gs_embedding_fwd(const gs_embedding_desc* d, const void* ta
   if (gs_status s = check_idx(where, d, idx)) return s;
   const int ve = vector_of(d, table, y);
   const int k = unit_of(ve * (int)gs::dtype_size(d->dtype));
-  const int64_t per_row = (d->width + k * ve - 1) / (k * ve), units = d->rows * per_row, of_block = kThreads * 4;
+  const int64_t per_row = (d->width + k * ve - 1) / (k * ve), units = d->rows * per_row;
+  const bool large = k == 1 && d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) >= kStreamBytes;
+  const int64_t of_block = kThreads * 4;
   const int64_t blocks = (units + of_block - 1) / of_block;
   if (blocks > INT32_MAX) return gs::set_error(GS_ERR_INVALID, "%s: y is too large", where);
   const FwdArgs a{table, idx, y, d->rows, d->n, d->ldt, d->ldy, (uint32_t)per_row,
-                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), (uint32_t)d->width, d->scale,
-                  d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) >= kStreamBytes};
+                  (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row), (uint32_t)d->width, d->scale};
   by_vector(d, ve, [&](auto t, auto v) {
     using T = decltype(t);
     constexpr int VE = decltype(v)::value;
-    if (d->index_bits == 32) gs::launch(k_embedding_fwd<T, VE, int32_t>, dim3((unsigned)blocks), kThreads, 0, gs::as_stream(stream), a);
-    else gs::launch(k_embedding_fwd<T, VE, int64_t>, dim3((unsigned)blocks), kThreads, 0, gs::as_stream(stream), a);
+    auto go = [&](auto kernel) { gs::launch(kernel, dim3((unsigned)blocks), kThreads, 0, gs::as_stream(stream), a); };
+    if constexpr (VE * sizeof(T) == 16) {
+      if (large) return d->index_bits == 32 ? go(k_embedding_fwd<T, VE, true, int32_t>) : go(k_embedding_fwd<T, VE, true, int64_t>);
+    }
+    d->index_bits == 32 ? go(k_embedding_fwd<T, VE, false, int32_t>) : go(k_embedding_fwd<T, VE, false, int64_t>);
   });
   return gs::check_launch(where);
 }
