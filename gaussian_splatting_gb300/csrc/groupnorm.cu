@@ -7,7 +7,8 @@
 //             dgamma = sum of dz h, dbeta = sum of dz, per channel over all rows of all maps
 // All of it in 32 bits, rounded once when stored.
 //
-// Both directions are bound by memory, and both need two passes over a map: one for its sums, one for its output.  Blocks
+// Both directions are bound by memory, and both need two passes over a map: one for its sums, one for its output (but a small
+// map's group fits in a block's registers, and one kernel does: 16 maps of 32 x 32 x 64 float32 6.4 us, 10.2 in two).  Blocks
 // take chunks of a map's rows; a thread owns one vector of neighbouring channels and walks down the rows, so that gamma, beta and
 // the statistics stay in registers and every access of a warp is a run of whole sectors.  The variance is taken about a value of the
 // thread's own rows (their first), so that it loses nothing where the mean is far from zero: a pivot p among n values with
@@ -439,6 +440,79 @@ __global__ void __launch_bounds__(kThreads, 4) k_groupnorm_write(const FwdArgs a
   write_chunk<T, VE, ONE, ACT>(a, Place(a.s, gridDim.x - 1 - blockIdx.x));
 }
 
+// ------------------------------------------------------------------ forward, small maps
+// One kernel: a block takes a map's group and holds it in registers, up to small_rows vectors a thread, from the mean to the
+// variance (about that mean) to the output.
+struct SmallArgs {
+  FwdArgs f;
+  int tx;  // threads side by side: vectors of a group
+};
+constexpr int kSmallThreads = 512;
+constexpr int small_rows(int ve) { return ve >= 4 ? 8 : 32; }  // 32 registers
+// Of the block's threads, in a fixed order; s: a float for each warp.
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = sum_among(v, 32);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return sum_among((threadIdx.x & 31) < blockDim.x / 32 ? s[threadIdx.x & 31] : 0.f, 32);
+}
+template <typename T, int VE, int ACT>
+__global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallArgs a) {
+  follow();
+  using IO = VecIO<T, VE>;
+  constexpr int K = small_rows(VE);
+  __shared__ float s_sum[32], s_squares[32];
+  const Shape& s = a.f.s;
+  const int g = blockIdx.x % s.groups, tx = threadIdx.x % a.tx, ty = threadIdx.x / a.tx, ny = blockDim.x / a.tx;
+  const int64_t sample = blockIdx.x / s.groups, row = sample * s.rows + ty;
+  const int col = g * s.per + tx * VE, count = ty < ny && ty < s.rows ? ((int)s.rows - ty + ny - 1) / ny : 0;
+  const T* x = static_cast<const T*>(a.f.x) + row * a.f.ldx + col;
+  typename IO::Raw v[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = k < count ? IO::load(x + (int64_t)k * ny * a.f.ldx) : IO::zero();
+  float gamma[VE], beta[VE], sum = 0.f;
+  IO::unpack(IO::load(static_cast<const T*>(a.f.gamma) + col), gamma);
+  IO::unpack(IO::load(static_cast<const T*>(a.f.beta) + col), beta);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float f[VE];
+    IO::unpack(v[k], f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sum += f[e];
+  }
+  const float n = (float)s.rows * (float)s.per, mean = block_sum(sum, s_sum) / n;
+  float squares = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float f[VE];
+    IO::unpack(v[k], f);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float d = k < count ? f[e] - mean : 0.f;
+      squares = fmaf(d, d, squares);
+    }
+  }
+  const float rstd = 1.f / sqrtf(block_sum(squares, s_squares) / n + a.f.eps);
+  if (threadIdx.x == 0) keep_stats(a.f, sample, g, make_float2(mean, rstd));
+  using V = Pairs<VE>;
+  typename V::E scale[V::N], shift[V::N];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) gamma[e] *= rstd;
+#pragma unroll
+  for (int i = 0; i < V::N; ++i) scale[i] = V::of(gamma, i), shift[i] = V::of(beta, i);
+  T* y = static_cast<T*>(a.f.y) + row * a.f.ldy + col;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k >= count) break;
+    float f[VE];
+    IO::unpack(v[k], f);
+#pragma unroll
+    for (int i = 0; i < V::N; ++i)
+      V::get(activate<ACT>(fma2(add2(V::of(f, i), typename V::E(-mean)), scale[i], shift[i])), f, i);
+    IO::store(y + (int64_t)k * ny * a.f.ldy, f);
+  }
+}
+
 // ------------------------------------------------------------------ backward
 // With d = x - mean and q = rstd gamma: z = d q + beta, h = d rstd.
 template <typename T, int VE, bool ONE, int ACT>
@@ -792,10 +866,36 @@ void by_form(const gs_groupnorm_desc* d, int ve, F f) {
   }
 }
 
+// Whether the kernel for small maps takes a call, with how many threads to a block.  Up to 16 MB, whose blocks come in a
+// wave or two, and not where a block would have next to nothing (us with it and without: 16 maps of 32 x 32 x 64 float32 in 8
+// groups 5.6 and 8.5, of 1,024 x 256 in 32 groups 7.2 and 13.0, of 300 x 834 bfloat16 in 278 groups 18.5 and 25.8; 64 of
+// 1,024 x 256 bfloat16, 32 MB, 23.4 and 20.8; 8 of 16 x 1,024 float32 in as many groups 8.7 and 6.3).
+constexpr int64_t kSmallBytes = 16 << 20, kSmallBlocks = 152 * 40;
+template <typename Aligned>
+bool small_takes(const gs_groupnorm_desc* d, Aligned aligned, int& ve, int& tx, int& threads) {
+  const int per = d->width / d->groups;
+  if (d->samples * d->groups > kSmallBlocks || d->samples * d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) > kSmallBytes)
+    return false;
+  ve = vector_of(per, d->dtype, aligned);
+  tx = per / ve;
+  if (tx > kSmallThreads) return false;
+  threads = 32;
+  auto rows = [&] { return (d->rows + threads / tx - 1) / (threads / tx); };
+  while (threads < kSmallThreads && (threads < tx || rows() > (ve >= 4 ? 8 : 16))) threads *= 2;
+  return rows() <= small_rows(ve);
+}
+// whatever the arrays' alignment
+bool small_takes(const gs_groupnorm_desc* d) {
+  int ve, tx, threads;
+  for (int bytes : {16, 4, 0})
+    if (!small_takes(d, [&](int b) { return b <= bytes; }, ve, tx, threads)) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" size_t gs_groupnorm_fwd_workspace_size(const gs_groupnorm_desc* d) {
-  if (check_desc("gs_groupnorm_fwd_workspace_size", d) || d->samples * d->rows == 0) return 0;
+  if (check_desc("gs_groupnorm_fwd_workspace_size", d) || d->samples * d->rows == 0 || small_takes(d)) return 0;
   return most_bytes(d, 1, [](const Shape& s) { return part_bytes(s) + joined_bytes(s); });
 }
 
@@ -818,11 +918,25 @@ extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x,
   if (gs_status s = gs::check_matrix(where, "y", y, rows, d->width, d->ldy, d->dtype)) return s;
   if (gs_status s = gs::check_matrix(where, "gamma", gamma, 1, d->width, d->width, d->dtype)) return s;
   if (gs_status s = gs::check_matrix(where, "beta", beta, 1, d->width, d->width, d->dtype)) return s;
-  if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_groupnorm_fwd_workspace_size(d))) return s;
-  const int ve = vector_of(d->width, d->dtype, [&](int bytes) {
+  auto aligned = [&](int bytes) {
     return gs::rows_aligned(x, rows, d->ldx, d->dtype, bytes) && gs::rows_aligned(y, rows, d->ldy, d->dtype, bytes) &&
            gs::rows_aligned(gamma, 1, 0, d->dtype, bytes) && gs::rows_aligned(beta, 1, 0, d->dtype, bytes);
-  });
+  };
+  int tx, threads, small_ve;
+  if (small_takes(d, aligned, small_ve, tx, threads)) {
+    SmallArgs a{};
+    a.f.s.rows = d->rows, a.f.s.groups = d->groups, a.f.s.per = d->width / d->groups, a.tx = tx;
+    a.f.x = x, a.f.gamma = gamma, a.f.beta = beta, a.f.y = y, a.f.mean = mean, a.f.rstd = rstd;
+    a.f.ldx = d->ldx, a.f.ldy = d->ldy, a.f.eps = d->eps;
+    by_form(d, small_ve, [&](auto t, auto v, auto one, auto act) {
+      if constexpr (decltype(one)::value)
+        gs::launch(k_groupnorm_small<decltype(t), decltype(v)::value, decltype(act)::value>, dim3((unsigned)(d->samples * d->groups)),
+                   threads, 0, st, a);
+    });
+    return gs::check_launch(where);
+  }
+  if (gs_status s = check_workspace(where, workspace, workspace_bytes, gs_groupnorm_fwd_workspace_size(d))) return s;
+  const int ve = vector_of(d->width, d->dtype, aligned);
   const Shape s = shape_of(d, ve, 1);
   float2* parts = static_cast<float2*>(workspace);
   const FwdArgs a{s, x, gamma, beta, y, mean, rstd, parts, joins(s, 1) ? parts + part_bytes(s) / sizeof(float2) : nullptr,

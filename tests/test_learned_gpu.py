@@ -307,6 +307,28 @@ def test_groupnorm_forward(shape, dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+# maps whose groups a block holds, at the edges of that: as many rows as fit (512 threads, 8 vectors of 16 bytes or 32 shorter
+# ones each) and one more, groups as wide as the block and wider, next to 16 MB, next to 6,080 blocks, mean and rstd either way
+SMALL = [(2, 2048, 16, 2), (2, 2049, 16, 2), (1, 4096, 16, 4), (3, 5461, 9, 3), (3, 5462, 9, 3), (1, 8, 4096, 1), (2, 3, 8192, 2),
+         (1, 33, 1028, 2), (16, 1024, 256, 32), (17, 1024, 256, 32), (380, 3, 32, 16), (381, 3, 32, 16), (7, 100, 30, 3),
+         (1, 4095, 32, 1)]
+
+
+@both
+@pytest.mark.parametrize("shape", SMALL, ids=str)
+def test_groupnorm_small_maps(shape, dtype):
+    samples, rows, width, groups = shape
+    for act, pad, shift in (("silu", 0, 0), ("gelu", 3, 1)):
+        x, gamma, beta = _norm_case(samples, rows, width, groups, dtype, 60 + SMALL.index(shape), pad, shift, 3.0)
+        got = dense.groupnorm_fwd(x, gamma, beta, groups, samples, act, 1e-5)
+        _check_norm_fwd(samples, rows, groups, x, gamma, beta, act, 1e-5, got)
+        y, mean, rstd = dense.groupnorm_fwd(x, gamma, beta, groups, samples, act, 1e-5, stats=False)
+        assert mean is None and rstd is None and torch.equal(y, got[0])
+        out = x.clone()
+        assert torch.equal(dense.groupnorm_fwd(out, gamma, beta, groups, samples, act, 1e-5, out=out)[0],
+                           dense.groupnorm_fwd(x.clone(), gamma, beta, groups, samples, act, 1e-5)[0])
+
+
 @both
 @pytest.mark.parametrize("mean", [0.0, 30.0, -1000.0])
 def test_groupnorm_far_from_zero(mean, dtype):
