@@ -793,16 +793,13 @@ size_t part_bytes(const Shape& s) {
   return (sizeof(float2) * (size_t)s.samples * s.slabs * s.span * s.chunks + 255) / 256 * 256;
 }
 size_t joined_bytes(const Shape& s) { return (sizeof(float2) * (size_t)s.samples * s.groups + 255) / 256 * 256; }
-// Whether a kernel between the passes joins the parts.  It costs a launch, some 3 us; without it each of an SM's blocks, one
-// after the other, waits for the parts, eight loads a lane at a time (12 maps of 13,604 x 952 float32 backward, 390 chunks of 119
-// groups: 275 turns in a row, 471 us with it, 683 without; 4 images of 1236 x 820 x 64, 1,026 chunks of 8 groups: 45 turns, 394
-// with it, 392 without).
-bool joins(const Shape& s, int arrays) {
+// Whether a kernel between the passes joins the parts.  It costs a launch, some 3 us; without it a block waits for the parts in
+// turns of eight loads a lane (12 maps of 13,604 x 952 float32 backward, 390 chunks of 119 groups: 25 turns, 471 us with it and
+// 683 without; 4 images of 1236 x 820 x 64, 1,026 chunks of 8 groups: 5 turns, 394 and 392).
+bool joins(const Shape& s) {
   int lanes = 32;
   while (lanes > 1 && s.span * lanes > kThreads) lanes /= 2;
-  const int64_t held = 152 * (arrays == 1 ? 4 : 3), waves = (s.samples * s.chunks * s.slabs + held - 1) / held;
-  const int64_t turns = (s.chunks + 8 * lanes - 1) / (8 * lanes);
-  return turns > 1 && waves * turns * ((s.span * lanes + kThreads - 1) / kThreads) > 64;
+  return (s.chunks + 8 * lanes - 1) / (8 * lanes) * ((s.span * lanes + kThreads - 1) / kThreads) > 5;
 }
 dim3 join_grid(const Shape& s) { return dim3((unsigned)((s.samples * s.groups + kThreads / 32 - 1) / (kThreads / 32))); }
 // over the vectors that the arrays' alignment may lead to
@@ -939,7 +936,7 @@ extern "C" gs_status gs_groupnorm_fwd(const gs_groupnorm_desc* d, const void* x,
   const int ve = vector_of(d->width, d->dtype, aligned);
   const Shape s = shape_of(d, ve, 1);
   float2* parts = static_cast<float2*>(workspace);
-  const FwdArgs a{s, x, gamma, beta, y, mean, rstd, parts, joins(s, 1) ? parts + part_bytes(s) / sizeof(float2) : nullptr,
+  const FwdArgs a{s, x, gamma, beta, y, mean, rstd, parts, joins(s) ? parts + part_bytes(s) / sizeof(float2) : nullptr,
                   d->ldx, d->ldy, d->eps};
   const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
   const size_t smem = kRing + sizeof(float2) * s.span;
@@ -998,7 +995,7 @@ extern "C" gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy
   const Shape s = shape_of(d, ve, 2);
   float* cols = dgamma || dbeta ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(s) + joined_bytes(s)) : nullptr;
   float2* parts = static_cast<float2*>(workspace);
-  const BwdArgs a{s, dy, x, gamma, beta, mean, rstd, skip, dx, parts, joins(s, 2) ? parts + part_bytes(s) / sizeof(float2) : nullptr, cols, d->lddy, d->ldx, d->ldskip, d->lddx};
+  const BwdArgs a{s, dy, x, gamma, beta, mean, rstd, skip, dx, parts, joins(s) ? parts + part_bytes(s) / sizeof(float2) : nullptr, cols, d->lddy, d->ldx, d->ldskip, d->lddx};
   const dim3 grid((unsigned)(s.samples * s.chunks), s.slabs);
   const size_t smem = kRing + sizeof(float2) * s.span;
   by_form(d, ve, [&](auto t, auto v, auto one, auto act) {
