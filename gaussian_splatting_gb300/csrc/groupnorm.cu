@@ -192,15 +192,18 @@ __device__ __forceinline__ float mul2(float a, float b) { return a * b; }
 __device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
 
 // 1 / (1 + exp(-v)) of two values by one reciprocal, of the product of the denominators: a third fewer special-function
-// operations, which bound the activation (16 a cycle and SM).  The exponent is held to 60, so that the product stays
-// finite: below v = -41.6 the result is 2^-60.
+// operations, which bound the activation (16 a cycle and SM).  The denominators are scaled by 2^-63 (exactly), so that the
+// product of two of up to 2^126.5 is a float whose reciprocal is one, and nobody's value is lost to a neighbour far below zero.
+// Exponents are held to 126.5: a result below 2^-126 becomes zero, as logistic's does, so that z times it vanishes.
 __device__ __forceinline__ F2 logistic_of(F2 v) {
   float a, b, r;
   mul2(v, F2(-1.4426950408889634f)).get(a, b);
-  const F2 d = add2(F2(fast_exp2(fminf(a, 60.f)), fast_exp2(fminf(b, 60.f))), F2(1.f));
+  const F2 d = fma2(F2(fast_exp2(fminf(a, 126.5f)), fast_exp2(fminf(b, 126.5f))), F2(0x1p-63f), F2(0x1p-63f));
   d.get(a, b);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-  return mul2(F2(r), F2(b, a));
+  F2 s;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(s.v) : "l"(F2(r).v), "l"(mul2(F2(b, a), F2(0x1p-63f)).v));
+  return s;
 }
 template <int ACT>
 __device__ __forceinline__ F2 activate(F2 z) {
