@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_groupnorm_write(const FwdArgs a
 
 // ------------------------------------------------------------------ forward, small maps
 // One kernel: a block takes a map's group and holds it in registers, up to small_rows vectors a thread, from the mean to the
-// variance (about that mean) to the output.
+// variance (about that mean, in two floats) to the output.
 struct SmallArgs {
   FwdArgs f;
   int tx;  // threads side by side: vectors of a group
@@ -453,10 +453,11 @@ struct SmallArgs {
 constexpr int kSmallThreads = 512;
 constexpr int small_rows(int ve) { return ve >= 4 ? 8 : 32; }  // 32 registers
 // Of the block's threads, in a fixed order; s: a float for each warp.
-__device__ __forceinline__ float block_sum(float v, float* s) {
+__device__ __forceinline__ void sum_of_warp(float v, float* s) {
   v = sum_among(v, 32);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
+}
+__device__ __forceinline__ float sum_of_warps(const float* s) {
   return sum_among((threadIdx.x & 31) < blockDim.x / 32 ? s[threadIdx.x & 31] : 0.f, 32);
 }
 template <typename T, int VE, int ACT>
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallAr
   follow();
   using IO = VecIO<T, VE>;
   constexpr int K = small_rows(VE);
-  __shared__ float s_sum[32], s_squares[32];
+  __shared__ float s_sum[3][32];
   const Shape& s = a.f.s;
   const int g = blockIdx.x % s.groups, tx = threadIdx.x % a.tx, ty = threadIdx.x / a.tx, ny = blockDim.x / a.tx;
   const int64_t sample = blockIdx.x / s.groups, row = sample * s.rows + ty;
@@ -473,6 +474,8 @@ __global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallAr
   typename IO::Raw v[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = k < count ? IO::load(x + (int64_t)k * ny * a.f.ldx) : IO::zero();
+  // about the group's first value, so that a mean far from zero costs no digits of the spread
+  const float pivot = to_f32<T>(static_cast<const T*>(a.f.x)[sample * s.rows * a.f.ldx + g * s.per]);
   float gamma[VE], beta[VE], sum = 0.f;
   IO::unpack(IO::load(static_cast<const T*>(a.f.gamma) + col), gamma);
   IO::unpack(IO::load(static_cast<const T*>(a.f.beta) + col), beta);
@@ -481,22 +484,33 @@ __global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallAr
     float f[VE];
     IO::unpack(v[k], f);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) sum += f[e];
+    for (int e = 0; e < VE; ++e) sum += k < count ? f[e] - pivot : 0.f;
   }
-  const float n = (float)s.rows * (float)s.per, mean = block_sum(sum, s_sum) / n;
-  float squares = 0.f;
+  sum_of_warp(sum, s_sum[0]);
+  __syncthreads();
+  const float n = (float)s.rows * (float)s.per, off = sum_of_warps(s_sum[0]) / n;
+  // the mean as a float and what that float lacks, to which the distances' own mean is added: the first value may be the one
+  // that is far from the others
+  const float mean = pivot + off, up = mean - pivot;
+  float low = (pivot - (mean - up)) + (off - up), squares = 0.f;
+  sum = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float f[VE];
     IO::unpack(v[k], f);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float d = k < count ? f[e] - mean : 0.f;
+      const float d = k < count ? f[e] - mean - low : 0.f;
+      sum += d;
       squares = fmaf(d, d, squares);
     }
   }
-  const float rstd = 1.f / sqrtf(block_sum(squares, s_squares) / n + a.f.eps);
-  if (threadIdx.x == 0) keep_stats(a.f, sample, g, make_float2(mean, rstd));
+  sum_of_warp(sum, s_sum[1]), sum_of_warp(squares, s_sum[2]);
+  __syncthreads();
+  const float more = sum_of_warps(s_sum[1]) / n;
+  const float rstd = 1.f / sqrtf(not_negative(fmaf(-more, more, sum_of_warps(s_sum[2]) / n)) + a.f.eps);
+  low += more;
+  if (threadIdx.x == 0) keep_stats(a.f, sample, g, make_float2(mean + low, rstd));
   using V = Pairs<VE>;
   typename V::E scale[V::N], shift[V::N];
 #pragma unroll
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallAr
     IO::unpack(v[k], f);
 #pragma unroll
     for (int i = 0; i < V::N; ++i)
-      V::get(activate<ACT>(fma2(add2(V::of(f, i), typename V::E(-mean)), scale[i], shift[i])), f, i);
+      V::get(activate<ACT>(fma2(add2(add2(V::of(f, i), typename V::E(-mean)), typename V::E(-low)), scale[i], shift[i])), f, i);
     IO::store(y + (int64_t)k * ny * a.f.ldy, f);
   }
 }

@@ -17,7 +17,7 @@ sys.path.insert(0, ROOT)
 sys.path.insert(0, os.path.join(ROOT, "tests"))
 
 from gaussian_splatting_gb300 import dense  # noqa: E402
-from test_learned_gpu import BF16, F32, ROUND, TINY, U, _close, _norm_case, _norm_grads, _rand  # noqa: E402
+from test_learned_gpu import BF16, CHAIN, F32, ROUND, TINY, U, _close, _norm_case, _norm_grads, _rand, _sum_u  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 both = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
@@ -80,3 +80,59 @@ def test_groupnorm_silu_infinities_and_nan_stay_in_their_channel(rows, pad, shif
     want = clean[:, others].double()
     _close(y[:, others], want, (10.1 * U + 2.02 * ROUND[dtype]) * want.abs() + TINY, "others")
     assert torch.isnan(y[:, [3, 8]]).all() and (y[:, 14] == math.inf).all()
+
+
+@both
+@vectors
+@pytest.mark.parametrize("value", [1000.1, 12345.678, -99999.9])
+def test_groupnorm_constant_maps_whose_sums_round(value, pad, shift, dtype):
+    """No spread at all, and sums that 32 bits do not hold: h is zero all the same."""
+    samples, rows, groups, width = 3, 50, 2, 16
+    x = _rand((samples * rows, width), dtype, 1, 0.0, pad, shift, value)
+    gamma, beta = _rand((width,), dtype, 2, 0.3, 0, shift, 1.0), _rand((width,), dtype, 3, 0.3, 0, shift)
+    y, mean, rstd = dense.groupnorm_fwd(x, gamma, beta, groups, samples, eps=1e-6)
+    assert torch.equal(mean, torch.full_like(mean, x[0, 0].item()))
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e3), rtol=1e-6)
+    assert torch.equal(y, beta.expand(samples * rows, width))
+
+
+@vectors
+@pytest.mark.parametrize("mean", [3e3, -1e5])
+def test_groupnorm_small_maps_far_from_zero(mean, pad, shift):
+    """Distances from a value of the group are exact here (of neighbours in a factor of two), their mean is off by
+    _sum_u(CHAIN) D, D the largest distance of two values; the mean as it is kept has its own rounding besides."""
+    samples, rows, width, groups = 3, 300, 40, 5
+    x, gamma, beta = _norm_case(samples, rows, width, groups, F32, 6, pad, shift, mean)
+    y, mu, rstd = dense.groupnorm_fwd(x, gamma, beta, groups, samples)
+    X = x.double().reshape(samples, rows, groups, -1)
+    want = X.mean((1, 3), keepdim=True)
+    var = (X - want).square().mean((1, 3), keepdim=True)
+    D = X.amax((1, 3), keepdim=True) - X.amin((1, 3), keepdim=True)
+    r = (var + 1e-5) ** -0.5
+    emu = _sum_u(CHAIN) * D
+    er = (0.5 * (_sum_u(CHAIN) * D * D + emu * emu) / (var + 1e-5) + 4 * U) * r
+    _close(mu, want[:, 0, :, 0], (emu + U * want.abs())[:, 0, :, 0], "mean")
+    _close(rstd, r[:, 0, :, 0], er[:, 0, :, 0], "rstd")
+    G, B = gamma.double().view(groups, -1), beta.double().view(groups, -1)
+    h = (X - want) * r
+    ez = (emu * r + (X - want).abs() * er) * G.abs() + 4 * U * ((h * G).abs() + B.abs())
+    _close(y, (h * G + B).reshape(x.shape), ez.reshape(x.shape) + TINY, "y")
+
+
+@vectors
+def test_groupnorm_small_maps_whose_first_value_is_far(pad, shift):
+    """A value far from all others, among which the spread of a channel is small: their distances from the mean, which is
+    next to them, are off by 4 u of themselves and of the mean, whatever the first value is."""
+    samples, rows, width, groups = 3, 300, 40, 5
+    x, gamma, beta = _norm_case(samples, rows, width, groups, F32, 6, pad, shift, 0.0)
+    beta.zero_()
+    x.view(samples, rows, width)[:, 0, ::width // groups] = 1e4 if not pad else -1e6
+    y, mu, rstd = dense.groupnorm_fwd(x, gamma, beta, groups, samples)
+    X = x.double().reshape(samples, rows, groups, -1)
+    want = X.mean((1, 3), keepdim=True)
+    var = (X - want).square().mean((1, 3), keepdim=True)
+    _close(mu, want[:, 0, :, 0], 8 * U * X.abs().mean((1, 3)), "mean")
+    _close(rstd.double() ** -2 - 1e-5, var[:, 0, :, 0], 32 * U * var[:, 0, :, 0], "variance")
+    h = (X - want) * (var + 1e-5) ** -0.5 * gamma.double().view(groups, -1)
+    off = (16 * U * X.abs().mean((1, 3), keepdim=True)) * (var + 1e-5) ** -0.5 * gamma.double().abs().view(groups, -1)
+    _close(y, h.reshape(x.shape), (off + 24 * U * h.abs()).reshape(x.shape) + TINY, "y")
