@@ -358,32 +358,37 @@ __device__ __forceinline__ void sum_chunk(const FwdArgs& a, const Place& at) {
   const int more = rows % ny;
   for (int c0 = 0; c0 < cols; c0 += kThreads / lanes) {
     const int c = c0 + (int)threadIdx.x / lanes, many = c < cols ? ny : 0;
-    float mean = 0.f, m2 = 0.f;
-    for (int y = lane; y < many; y += lanes) mean = fmaf(y < more ? few + 1.f : few, s_part[y * s.tx * VE + c].x, mean);
-    mean = sum_among(mean, lanes) * by_rows;
+    // about the first thread's mean, and the groups' about their first column's: like values have exactly theirs
+    const float k = many ? s_part[c].x : 0.f;
+    float off = 0.f, m2 = 0.f;
+    for (int y = lane; y < many; y += lanes) off = fmaf(y < more ? few + 1.f : few, s_part[y * s.tx * VE + c].x - k, off);
+    off = sum_among(off, lanes) * by_rows;
     for (int y = lane; y < many; y += lanes) {
       const float2 p = s_part[y * s.tx * VE + c];
-      m2 += fmaf((y < more ? few + 1.f : few) * (p.x - mean), p.x - mean, p.y);
+      const float d = p.x - k - off;
+      m2 += fmaf((y < more ? few + 1.f : few) * d, d, p.y);
     }
     m2 = sum_among(m2, lanes);
     // (row 0 of the threads has been read by this column's threads alone)
-    if (lane == 0 && c < cols) s_part[c] = make_float2(mean, m2);
+    if (lane == 0 && c < cols) s_part[c] = make_float2(k + off, m2);
   }
   __syncthreads();
   const int groups = at.g1 - at.g0, glanes = side_by_side(groups), gl = threadIdx.x % glanes;
   for (int g0 = 0; g0 < groups; g0 += kThreads / glanes) {
     const int g = at.g0 + min(g0 + (int)threadIdx.x / glanes, groups - 1);
     const int c0 = max(g * s.per, at.col0) - at.col0, c1 = min((g + 1) * s.per, at.col1) - at.col0;
-    float mean = 0.f, m2 = 0.f;
-    for (int c = c0 + gl; c < c1; c += glanes) mean += s_part[c].x;
-    mean = sum_among(mean, glanes) / (float)(c1 - c0);
+    const float k = s_part[c0].x;
+    float off = 0.f, m2 = 0.f;
+    for (int c = c0 + gl; c < c1; c += glanes) off += s_part[c].x - k;
+    off = sum_among(off, glanes) / (float)(c1 - c0);
     for (int c = c0 + gl; c < c1; c += glanes) {
       const float2 p = s_part[c];
-      m2 += fmaf((float)rows * (p.x - mean), p.x - mean, p.y);
+      const float d = p.x - k - off;
+      m2 += fmaf((float)rows * d, d, p.y);
     }
     m2 = sum_among(m2, glanes);
     if (gl == 0 && g0 + (int)threadIdx.x / glanes < groups)
-      a.part[parts_of(s, at.sample, at.slab, g) + at.chunk] = make_float2(mean, m2);
+      a.part[parts_of(s, at.sample, at.slab, g) + at.chunk] = make_float2(k + off, m2);
   }
 }
 
