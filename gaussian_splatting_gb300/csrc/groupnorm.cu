@@ -11,8 +11,9 @@
 // map's group fits in a block's registers, and one kernel does: 16 maps of 32 x 32 x 64 float32 6.4 us, 10.2 in two).  Blocks
 // take chunks of a map's rows; a thread owns one vector of neighbouring channels and walks down the rows, so that gamma, beta and
 // the statistics stay in registers and every access of a warp is a run of whole sectors.  The variance is taken about a value of the
-// thread's own rows (their first), so that it loses nothing where the mean is far from zero: a pivot p among n values with
-// squared distances M from their mean has n (p - mean)^2 <= n M.  Chunks' sums are joined about the joint mean, in a fixed order.
+// thread's own rows (their first), so that a mean far from zero costs nothing: a pivot p among a thread's n values with
+// squared distances M from their mean has n (p - mean)^2 <= n M, which costs log2(n) / 2 digits where the spread is p's alone (n
+// is some 64, of rows off 16 bytes some 500).  Threads', columns' and chunks' sums are joined about their joint mean, in a fixed order.
 // What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2, or a small kernel
 // between the passes does.
 //
@@ -248,30 +249,38 @@ __device__ __forceinline__ float sum_among(float v, int k) {
 // at least zero, or NaN
 __device__ __forceinline__ float not_negative(float v) { return v < 0.f ? 0.f : v; }
 
-// A group's mean and rstd by `lanes` lanes, from the parts of all chunks and slabs.  About the first part's mean k: n of the N
-// values have it, so n (k - mean)^2 is at most all squared distances, and little is lost to N (k - mean)^2.
+// a + b as a float, and what that float lacks
+__device__ __forceinline__ float2 exact_sum(float a, float b) {
+  const float sum = a + b, up = sum - a;
+  return make_float2(sum, (a - (sum - up)) + (b - up));
+}
+// A group's mean and rstd by `lanes` lanes, from the parts of all chunks and slabs: their joint mean first, as a distance from
+// the first part's, then the squares about it and the distances' own mean, by which it is corrected (about the first part's mean,
+// a first chunk far from the others would cost as many digits as there are chunks).
 __device__ __forceinline__ float2 join_stats(const FwdArgs& a, int64_t sample, int g, int lane, int lanes) {
   const Shape& s = a.s;
   const int first = g * s.per / s.cols, last = ((g + 1) * s.per - 1) / s.cols;
-  const float k = a.part[parts_of(s, sample, first, g)].x;
-  float s1 = 0.f, s2 = 0.f;
-  for (int b = first; b <= last; ++b) {
-    const int wide = min((g + 1) * s.per, (b + 1) * s.cols) - max(g * s.per, b * s.cols);
-    const float2* part = a.part + parts_of(s, sample, b, g);
-    const float full = (float)s.chunk * (float)wide, rest = (float)(s.rows - (s.chunks - 1) * s.chunk) * (float)wide;
+  auto each = [&](auto add) {
+    for (int b = first; b <= last; ++b) {
+      const int wide = min((g + 1) * s.per, (b + 1) * s.cols) - max(g * s.per, b * s.cols);
+      const float2* part = a.part + parts_of(s, sample, b, g);
+      const float full = (float)s.chunk * (float)wide, rest = (float)(s.rows - (s.chunks - 1) * s.chunk) * (float)wide;
 #pragma unroll 8
-    for (int c = lane; c < s.chunks; c += lanes) {
-      const float n = c == s.chunks - 1 ? rest : full;
-      const float2 p = part[c];
-      const float d = p.x - k;
-      s1 = fmaf(n, d, s1);
-      s2 += fmaf(n * d, d, p.y);
+      for (int c = lane; c < s.chunks; c += lanes) add(part[c], c == s.chunks - 1 ? rest : full);
     }
-  }
-  s1 = sum_among(s1, lanes), s2 = sum_among(s2, lanes);
-  const float total = (float)s.rows * (float)s.per, off = s1 / total;
-  const float var = not_negative(fmaf(-off, off, s2 / total));
-  return make_float2(k + off, 1.f / sqrtf(var + a.eps));
+  };
+  const float k = a.part[parts_of(s, sample, first, g)].x, total = (float)s.rows * (float)s.per;
+  float s1 = 0.f, s2 = 0.f;
+  each([&](float2 p, float n) { s1 = fmaf(n, p.x - k, s1); });
+  const float2 mean = exact_sum(k, sum_among(s1, lanes) / total);
+  s1 = 0.f;
+  each([&](float2 p, float n) {
+    const float d = p.x - mean.x - mean.y;
+    s1 = fmaf(n, d, s1);
+    s2 += fmaf(n * d, d, p.y);
+  });
+  s1 = sum_among(s1, lanes) / total, s2 = sum_among(s2, lanes) / total;
+  return make_float2(mean.x + (mean.y + s1), 1.f / sqrtf(not_negative(fmaf(-s1, s1, s2)) + a.eps));
 }
 __device__ __forceinline__ void keep_stats(const FwdArgs& a, int64_t sample, int g, float2 st) {
   if (a.mean) a.mean[sample * a.s.groups + g] = st.x;
@@ -496,8 +505,9 @@ __global__ void __launch_bounds__(kSmallThreads) k_groupnorm_small(const SmallAr
   const float n = (float)s.rows * (float)s.per, off = sum_of_warps(s_sum[0]) / n;
   // the mean as a float and what that float lacks, to which the distances' own mean is added: the first value may be the one
   // that is far from the others
-  const float mean = pivot + off, up = mean - pivot;
-  float low = (pivot - (mean - up)) + (off - up), squares = 0.f;
+  const float2 two = exact_sum(pivot, off);
+  const float mean = two.x;
+  float low = two.y, squares = 0.f;
   sum = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {

@@ -137,3 +137,19 @@ def test_groupnorm_small_maps_whose_first_value_is_far(pad, shift):
     h = (X - want) * (var + 1e-5) ** -0.5 * gamma.double().view(groups, -1)
     off = (16 * U * X.abs().mean((1, 3), keepdim=True)) * (var + 1e-5) ** -0.5 * gamma.double().abs().view(groups, -1)
     _close(y, h.reshape(x.shape), (off + 24 * U * h.abs()).reshape(x.shape) + TINY, "y")
+
+
+@pytest.mark.parametrize("shape", [(1, 600_000, 8, 1), (2, 200_000, 24, 3), (40, 15_000, 64, 32)], ids=str)
+def test_groupnorm_first_rows_unlike_the_others(shape):
+    """A strip of a map far from the rest of it (less than a chunk of rows): the variance to 128 u of itself.  Of that 57 u are
+    _sum_u(600) for a sum of squares, twice 4 u the roundings of a chunk's mean of like values and of its distance from the
+    joint mean, which is itself off by less than 57 u of the distances' mean; the rest is room."""
+    samples, rows, width, groups = shape
+    x = _rand((samples * rows, width), F32, 7, 0.5)
+    strip = 64
+    x.view(samples, rows, width)[:, :strip] = 900.1 + _rand((samples, strip, width), F32, 8, 1e-3)
+    _, mean, rstd = dense.groupnorm_fwd(x, torch.ones(width, device="cuda"), torch.zeros(width, device="cuda"), groups, samples)
+    X = x.double().view(samples, rows, groups, -1)
+    var = X.var((1, 3), correction=0)
+    _close(rstd.double() ** -2 - 1e-5, var, 128 * U * var, "variance")
+    _close(mean, X.mean((1, 3)), 57 * U * X.abs().mean((1, 3)), "mean")
