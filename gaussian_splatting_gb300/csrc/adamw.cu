@@ -2,7 +2,8 @@
 //
 // Mathematics, per value: m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2,
 //   p = p keep - m step / (sqrt(v) root + eps), with keep = 1 - lr decay, step = lr / (1 - b1^t) and
-//   root = (1 - b2^t)^-1/2 from the host in 64 bits.
+//   root = (1 - b2^t)^-1/2 from the host in 64 bits.  keep comes as two floats, since lr decay may be less than the last place
+//   of one: what the second adds to p joins the step, and that sum p keep, with one rounding of p's size.
 // An 8-bit moment is code x scale; v is kept as its root, whose range the type holds (2^-9 to 448: of v 2^35).
 //
 // Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones (176M values: 453 us, 417 at the
@@ -34,7 +35,7 @@ struct Tensor {
   int64_t n;
   uint32_t tile;  // the launch's first tile of this tensor
   uint32_t place; // of its first value, for the random bits
-  float keep, step;
+  float keep, rest, step;  // keep + rest: 1 - lr decay
   int wide;       // whether every array is aligned to four of its values
 };
 // Launch parameters hold up to 32,764 bytes; the small form keeps the copying of them short.
@@ -203,7 +204,8 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   for (int i = 0; i < 8; i += 2) {
     float d0, d1;
     fma2(F2(s[i], s[i + 1]), F2(root), F2(eps)).get(d0, d1);
-    fma2(mul2(F2(m[i], m[i + 1]), F2(-t.step)), F2(recip(d0), recip(d1)), mul2(F2(p[i], p[i + 1]), F2(t.keep))).get(p[i], p[i + 1]);
+    const F2 old(p[i], p[i + 1]), less = fma2(mul2(F2(m[i], m[i + 1]), F2(-t.step)), F2(recip(d0), recip(d1)), mul2(old, F2(t.rest)));
+    fma2(old, F2(t.keep), less).get(p[i], p[i + 1]);
   }
   if constexpr (WIDE) {
 #pragma unroll
@@ -302,9 +304,10 @@ gs_status run_all(const char* where, const gs_adamw_desc* d, const gs_adamw_tens
     const size_t ss = d->state_bits / 8;
     const bool wide = at4(s.param, 4) && at4(s.grad, gs::dtype_size(d->grad_dtype)) && at4(s.exp_avg, ss) &&
                       at4(s.exp_avg_sq, ss) && at4(s.copy, 2);
+    const double keep = 1.0 - s.lr * s.weight_decay;
     a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_scale, s.exp_avg_sq_scale,
                             static_cast<__nv_bfloat16*>(s.copy), s.n, (uint32_t)tiles, (uint32_t)place,
-                            (float)(1.0 - s.lr * s.weight_decay), (float)(s.lr / bc1), wide};
+                            (float)keep, (float)(keep - (float)keep), (float)(s.lr / bc1), wide};
     tiles += need;
     place += (uint64_t)(s.n + kRun - 1) / kRun * kRun;
   }

@@ -153,3 +153,29 @@ def test_groupnorm_first_rows_unlike_the_others(shape):
     var = X.var((1, 3), correction=0)
     _close(rstd.double() ** -2 - 1e-5, var, 128 * U * var, "variance")
     _close(mean, X.mean((1, 3)), 57 * U * X.abs().mean((1, 3)), "mean")
+
+
+# ------------------------------------------------------------------ AdamW
+def _off(n, dtype, shift):
+    return torch.zeros(n + shift, dtype=dtype, device="cuda")[shift:]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("decay", [1e-7, 2e-8, 3e-6, 1e-3, 0.3, 0.5, 0.9990001, 1.0, 1.7, -1e-7])
+def test_adamw_decay_is_not_rounded(decay, bits, shift):
+    """p (1 - lr weight_decay) - step is off by half a unit in the last place (the rounding of p), by what two floats leave
+    of the factor (2^-48) and by 16 u of the step, which at the first one is lr."""
+    n, lr = 5001, 1e-6
+    for moves in (False, True):
+        p, g = _off(n, F32, shift), _off(n, F32, shift)
+        p.copy_(_rand((n,), F32, 1))
+        if moves:
+            g.copy_(_rand((n,), F32, 2))
+        step = lr * g.double() / (g.double().abs() + 1e-8)
+        want = p.double() * (1 - lr * (decay / lr)) - step
+        unit = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30))) - 23)
+        last = 0.5 * unit + 2.0 ** -48 * p.double().abs() + 16 * U * lr * moves + TINY
+        m, v, scales = dense.adamw_state([p], bits)
+        dense.adamw([p], [g], m, v, 1, lr, weight_decay=decay / lr, scales=scales)
+        _close(p, want, last, f"p {moves}")
