@@ -11,6 +11,7 @@
 // launch parameters (no table in device memory to fill and wait for), a block looks its tensor up in them.  A warp takes
 // runs of 256 values, eight a lane: the run's largest magnitudes, by which its scales go, are one reduction over the warp.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -95,7 +96,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// (b is at least eps or the root of a float, or zero: never so large or small that the approximation flushes it)
+// (b is a normal float, infinite, or zero where eps is: eps is raised to 2^-126, and the root of the smallest float is 2^-74.5.
+// Beyond 2^126, where only eps or an overflowing root can be, the result is flushed to zero.)
 __device__ __forceinline__ float recip(float b) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
@@ -282,7 +284,7 @@ gs_status run_all(const char* where, const gs_adamw_desc* d, const gs_adamw_tens
                   int n_counts, cudaStream_t st) {
   Args<MOST> a;
   a.b1 = (float)d->beta1, a.c1 = (float)(1.0 - d->beta1), a.b2 = (float)d->beta2, a.c2 = (float)(1.0 - d->beta2);
-  a.eps = (float)d->eps;
+  a.eps = d->eps > 0.0 ? std::max((float)d->eps, FLT_MIN) : 0.f;
   const double bc1 = 1.0 - std::pow(d->beta1, (double)d->step), bc2 = 1.0 - std::pow(d->beta2, (double)d->step);
   a.root = (float)(1.0 / std::sqrt(bc2));
   a.key = d->seed * 0x6A09E667u + (uint32_t)d->step * 0xBB67AE85u;

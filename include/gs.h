@@ -614,6 +614,7 @@ gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy, const voi
  * weight_decay and t = step >= 1:
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
  *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * An eps between 0 and 2^-126 counts as 2^-126; with eps = 0 a value that no gradient has reached becomes NaN.
  * Moments have 32 bits, or 8 (state_bits): then exp_avg holds m and exp_avg_sq the root of v as float8 e4m3 values, each
  * run of 256 neighbouring values of a tensor with a float32 scale of its own ([ceil(n / 256)], the run's largest
  * magnitude / 448): m = scale code.  Zeroed arrays are zero moments.  The update takes the new moments before they are

@@ -179,3 +179,16 @@ def test_adamw_decay_is_not_rounded(decay, bits, shift):
         m, v, scales = dense.adamw_state([p], bits)
         dense.adamw([p], [g], m, v, 1, lr, weight_decay=decay / lr, scales=scales)
         _close(p, want, last, f"p {moves}")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-46, 1e-40, 1.1e-38, 1e-30])
+def test_adamw_smallest_eps(eps, bits):
+    """A value that no gradient has reached yet stays where it is, and others move by lr at the first step."""
+    p, g = [_rand((600,), F32, 1)], [_rand((600,), F32, 2)]
+    g[0][::3] = 0.0
+    before = p[0].clone()
+    m, v, scales = dense.adamw_state(p, bits)
+    dense.adamw(p, g, m, v, 1, 1e-3, eps=eps, weight_decay=0.0, scales=scales)
+    assert torch.equal(p[0][::3], before[::3])
+    _close(p[0], before.double() - 1e-3 * g[0].sign().double(), 16 * U * 1e-3 + 2 * U * before.double().abs(), "p")
