@@ -316,15 +316,45 @@ gs_status run_all(const char* where, const gs_adamw_desc* d, const gs_adamw_tens
   return flush();
 }
 
-// whether two tensors' parameters share memory: their updates would race
-bool overlap(const gs_adamw_tensor* tensors, int count) {
-  std::vector<std::pair<uintptr_t, uintptr_t>> at;
-  at.reserve(count);
+// Whether an array that is written shares memory with any other: their updates would race.
+constexpr int kKinds = 7;
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+// f(kind, array's range) of a tensor's arrays
+template <typename F>
+void each_array(const gs_adamw_desc* d, const gs_adamw_tensor& t, F f) {
+  const size_t n = t.n, grad = gs::dtype_size(d->grad_dtype), state = d->state_bits / 8;
+  auto one = [&](int kind, const void* p, size_t bytes) { f(kind, Range{(uintptr_t)p, (uintptr_t)p + bytes, kind != 1}); };
+  if (!n) return;
+  one(0, t.param, 4 * n), one(1, t.grad, grad * n), one(2, t.exp_avg, state * n), one(3, t.exp_avg_sq, state * n);
+  if (d->state_bits == 8) one(4, t.exp_avg_scale, 4 * ((n + kRun - 1) / kRun)), one(5, t.exp_avg_sq_scale, 4 * ((n + kRun - 1) / kRun));
+  if (t.copy) one(6, t.copy, 2 * n);
+}
+bool overlap(const gs_adamw_desc* d, const gs_adamw_tensor* tensors, int count) {
+  // Arrays of a kind mostly ascend, as parts of a buffer or as they were allocated, and kinds often lie apart.
+  Range span[kKinds] = {};
+  bool apart = true;
   for (int i = 0; i < count; ++i)
-    if (tensors[i].n) at.emplace_back((uintptr_t)tensors[i].param, (uintptr_t)tensors[i].param + 4 * (uintptr_t)tensors[i].n);
-  std::sort(at.begin(), at.end());
-  for (size_t i = 1; i < at.size(); ++i)
-    if (at[i].first < at[i - 1].second) return true;
+    each_array(d, tensors[i], [&](int kind, Range r) {
+      apart &= r.begin >= span[kind].end;
+      if (!span[kind].end) span[kind].begin = r.begin;
+      span[kind].end = r.end;
+    });
+  for (int i = 0; i < kKinds; ++i)
+    for (int j = 0; j < i; ++j) apart &= span[i].begin >= span[j].end || span[j].begin >= span[i].end;
+  if (apart) return false;
+  std::vector<Range> all;
+  all.reserve((size_t)count * kKinds);
+  for (int i = 0; i < count; ++i) each_array(d, tensors[i], [&](int, Range r) { all.push_back(r); });
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end = 0, written = 0;  // of those so far, and of those that are written
+  for (const Range& r : all) {
+    if (r.begin < (r.written ? end : written)) return true;
+    end = std::max(end, r.end);
+    if (r.written) written = std::max(written, r.end);
+  }
   return false;
 }
 
@@ -361,7 +391,8 @@ extern "C" gs_status gs_adamw(const gs_adamw_desc* d, const gs_adamw_tensor* ten
       return gs::set_error(GS_ERR_INVALID, "%s: 8-bit moments of tensor %d need their scales", where, i);
   }
   try {
-    if (overlap(tensors, count)) return gs::set_error(GS_ERR_INVALID, "%s: two tensors' parameters overlap", where);
+    if (overlap(d, tensors, count))
+      return gs::set_error(GS_ERR_INVALID, "%s: arrays overlap of which at least one is written", where);
   } catch (const std::bad_alloc&) {
     return gs::set_error(GS_ERR_INVALID, "%s: no host memory for %d tensors", where, count);
   }

@@ -146,6 +146,7 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999),
     ``seed`` and ``step`` alone: the same call gives the same bits.  ``copies`` (bfloat16, like ``params``) receive the
     updated parameters, for layers that compute in bfloat16.  With ``counts`` (int64 [records, 2], as
     ``AttributeHead.status`` or ``StepResult.status``) the step is skipped on the device where any record's second
-    entry is not zero.  Tensors are contiguous; none may overlap another."""
+    entry is not zero.  Tensors are contiguous; none may overlap another, but for gradients among
+    themselves."""
     (_binding or _load()).adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], eps, weight_decay, scales,
                                 copies, seed, counts, _handle(stream))

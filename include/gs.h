@@ -630,7 +630,7 @@ gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy, const voi
  *   tensors    HOST array of `count` descriptions.  param float32; grad of grad_dtype; exp_avg, exp_avg_sq; their scales
  *              (8 bits only); copy: bfloat16 [n], the updated parameters rounded (the layers' working copy), or NULL.
  *              Contiguous, any element-aligned address (16-byte aligned ones run faster); n == 0 is allowed.  No array
- *              may overlap another.
+ *              may overlap another (refused), but gradients, which are only read, may overlap each other.
  *   counts     as for gs_sparse_adam: if any of n_counts records' second word is nonzero, the whole step is skipped.
  */
 typedef struct {

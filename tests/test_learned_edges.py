@@ -1,0 +1,60 @@
+"""Refusals, sizes and builds of code lookup, group norm and AdamW at the ends of their ranges, on the host (no GPU needed)."""
+import ctypes as C
+import os
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+sys.path.insert(0, ROOT)
+
+from gaussian_splatting_gb300 import _native as N  # noqa: E402
+
+P = 1 << 30  # an address that is never followed: the checks come first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gaussian_splatting_gb300 import build
+    build.build()
+    return N.load()
+
+
+# arrays of a tensor of 1,000 values: their bytes with 32-bit and with 8-bit moments
+ARRAYS = {"param": (4000, 4000), "grad": (4000, 4000), "exp_avg": (4000, 1000), "exp_avg_sq": (4000, 1000),
+          "exp_avg_scale": (0, 16), "exp_avg_sq_scale": (0, 16), "copy": (2000, 2000)}
+
+
+def _tensors(bits, apart):
+    """Three tensors, arrays 8 KB from each other: tensor by tensor (the last one first), or each kind `apart` from the others."""
+    out, at = [N.AdamWTensor(n=1000, lr=1e-3) for _ in range(3)], P
+    kinds = [(k, t) for k in ARRAYS for t in out] if apart else [(k, t) for t in reversed(out) for k in ARRAYS]
+    for k, t in kinds:
+        size = ARRAYS[k][bits == 8]
+        setattr(t, k, at if size else None)
+        at += 8192
+    return out
+
+
+def _step(lib, bits, tensors):
+    d = N.AdamWDesc(0.9, 0.999, 1e-8, 1, N.GS_F32, bits, 0)
+    arr = (N.AdamWTensor * len(tensors))(*tensors)
+    return lib.gs_adamw(C.addressof(d), C.addressof(arr), len(tensors), None, 0, None)
+
+
+@pytest.mark.parametrize("apart", [True, False])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("one", list(ARRAYS))
+@pytest.mark.parametrize("other", list(ARRAYS))
+def test_adamw_refuses_arrays_that_overlap(lib, one, other, bits, apart):
+    """An array of the second tensor whose last element is the first element of one of the third's, and the other way round."""
+    sizes = {k: v[bits == 8] for k, v in ARRAYS.items()}
+    if not sizes[one] or not sizes[other] or one == other == "grad":
+        pytest.skip("no such arrays, or both only read")
+    for forward in (True, False):
+        t = _tensors(bits, apart)
+        a, b = (one, other) if forward else (other, one)
+        end = getattr(t[2], b) + (sizes[b] - 4 if not forward else 4)
+        setattr(t[1], a, end // 4 * 4 - (sizes[a] // 4 * 4 if forward else 0))
+        assert _step(lib, bits, t) == N.GS_ERR_INVALID
+        assert b"overlap" in lib.gs_last_error()

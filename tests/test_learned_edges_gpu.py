@@ -17,6 +17,7 @@ sys.path.insert(0, ROOT)
 sys.path.insert(0, os.path.join(ROOT, "tests"))
 
 from gaussian_splatting_gb300 import dense  # noqa: E402
+from gaussian_splatting_gb300._native import GSError  # noqa: E402
 from test_learned_gpu import BF16, CHAIN, F32, ROUND, TINY, U, _close, _norm_case, _norm_grads, _rand, _sum_u  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -192,3 +193,24 @@ def test_adamw_smallest_eps(eps, bits):
     dense.adamw(p, g, m, v, 1, 1e-3, eps=eps, weight_decay=0.0, scales=scales)
     assert torch.equal(p[0][::3], before[::3])
     _close(p[0], before.double() - 1e-3 * g[0].sign().double(), 16 * U * 1e-3 + 2 * U * before.double().abs(), "p")
+
+
+def test_adamw_refuses_arrays_that_overlap():
+    def args(**kw):
+        a = dict(params=[torch.zeros(900, device="cuda") for _ in range(2)], grads=[torch.zeros(900, device="cuda") for _ in range(2)],
+                 exp_avg=[torch.zeros(900, device="cuda") for _ in range(2)],
+                 exp_avg_sq=[torch.zeros(900, device="cuda") for _ in range(2)])
+        return {**a, **kw}
+
+    dense.adamw(**args(), step=1)
+    one = torch.zeros(2000, device="cuda")
+    a = args()
+    bad = [args(exp_avg=a["exp_avg"], exp_avg_sq=a["exp_avg"]), args(exp_avg=[one[:900], one[899:1799]]),
+           args(grads=[one[:900], one[900:1800]], exp_avg=[one[1000:1900], a["exp_avg"][0]]),
+           args(params=a["params"], grads=[a["params"][1], a["grads"][0]]), args(params=[one[:900], one[1:901]])]
+    for b in bad:
+        with pytest.raises(GSError, match="overlap"):
+            dense.adamw(**b, step=1)
+    # a gradient is only read: two tensors may share one; what lies side by side does not overlap
+    dense.adamw(**args(grads=[one[:900], one[:900]]), step=1)
+    dense.adamw(**args(params=[one[:900], one[900:1800]]), step=1)
