@@ -115,7 +115,7 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
                                            const float c2, const float eps, const float root, const uint32_t key) {
   const G* gp = static_cast<const G*>(t.g);
   float p[8], g[8], m[8], v[8];
-  auto place = [&](int i) { return at + lane + 32 * i; };
+  [[maybe_unused]] const int left = (int)min(t.n - at, (int64_t)kRun) - lane;  // 32 i < left: the lane has an i-th value
   uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
   if constexpr (WIDE) {
 #pragma unroll
@@ -133,9 +133,8 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t e = place(i);
-      const bool in = e < t.n;
-      p[i] = in ? t.p[e] : 0.f;
+      const bool in = 32 * i < left;
+      const int64_t e = at + lane + 32 * i;
       g[i] = in ? to_f32<G>(gp[e]) : 0.f;
       if constexpr (BITS == 32) {
         m[i] = in ? static_cast<const float*>(t.m)[e] : 0.f;
@@ -171,6 +170,9 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   if constexpr (WIDE) {  // (in flight while the moments are rounded)
 #pragma unroll
     for (int k = 0; k < 2; ++k) load4(t.p + at + lane * 4 + k * 128, p + 4 * k);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = 32 * i < left ? t.p[at + lane + 32 * i] : 0.f;
   }
   uint32_t qm[2], qv[2];
   if constexpr (BITS == 8) {
@@ -228,8 +230,8 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t e = place(i);
-      if (e >= t.n) continue;
+      if (32 * i >= left) continue;
+      const int64_t e = at + lane + 32 * i;
       t.p[e] = p[i];
       if constexpr (BITS == 32) {
         static_cast<float*>(t.m)[e] = m[i];
@@ -245,12 +247,6 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
 
 // 40 warps to an SM for 8-bit moments, 48 registers: instructions bound that form as much as memory does, and more warps hide
 // both (176M values: 453 us, 475 with 32 warps and 64 registers).
-// (a call of its own: inlined, the two forms together make the kernel spill)
-template <typename G, int BITS>
-__device__ __noinline__ void last_run(const Tensor& t, int64_t at, const float b1, const float c1, const float b2, const float c2,
-                                      const float eps, const float root, const uint32_t key) {
-  run_of_256<G, BITS, false>(t, at, threadIdx.x & 31, b1, c1, b2, c2, eps, root, key);
-}
 template <typename G, int BITS, int MOST>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 10 : 8) k_adamw(const __grid_constant__ Args<MOST> a) {
   follow();
@@ -268,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 10 : 8) k_adamw(const __
   if (t.wide && at + kRun <= t.n)
     run_of_256<G, BITS, true>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
   else
-    last_run<G, BITS>(t, at, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
+    run_of_256<G, BITS, false>(t, at, threadIdx.x & 31, a.b1, a.c1, a.b2, a.c2, a.eps, a.root, a.key);
 }
 
 template <int MOST>

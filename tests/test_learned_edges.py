@@ -1,7 +1,11 @@
 """Refusals, sizes and builds of code lookup, group norm and AdamW at the ends of their ranges, on the host (no GPU needed)."""
 import ctypes as C
 import os
+import re
+import shutil
+import subprocess
 import sys
+import tempfile
 
 import pytest
 
@@ -58,3 +62,26 @@ def test_adamw_refuses_arrays_that_overlap(lib, one, other, bits, apart):
         setattr(t[1], a, end // 4 * 4 - (sizes[a] // 4 * 4 if forward else 0))
         assert _step(lib, bits, t) == N.GS_ERR_INVALID
         assert b"overlap" in lib.gs_last_error()
+
+
+@pytest.mark.parametrize("name", ["adamw", "embedding", "groupnorm"])
+def test_no_function_spills(name):
+    """Not the kernels alone: what they call out of line neither."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not available")
+    from gaussian_splatting_gb300 import build
+    with tempfile.TemporaryDirectory() as out:
+        r = subprocess.run([nvcc, *build.NVCC_FLAGS, "-Xptxas", "-v", "-c", os.path.join(build.CSRC, name + ".cu"), "-o",
+                            os.path.join(out, "o")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    seen, spilling, function = 0, [], None
+    for line in (r.stdout + r.stderr).splitlines():
+        m = re.search(r"Function properties for (\S+)", line)
+        function = m.group(1) if m else function
+        m = re.search(r"(\d+) bytes spill stores, (\d+) bytes spill loads", line)
+        if m and "warning" not in line:
+            seen += 1
+            if m.group(1) != "0" or m.group(2) != "0":
+                spilling.append((function, line.strip()))
+    assert seen and not spilling, spilling
