@@ -4,7 +4,9 @@
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "common.cuh"
 
@@ -41,28 +43,30 @@ int take_drop_copy() { return g_drop_copy.exchange(0); }
 cudaError_t max_dynamic_smem(const void* fn, int bytes) {
   // the attribute belongs to a device: remembered per device (and kernel, and size), so
   // that the driver call is made once per device rather than on every launch
-  constexpr int kMaxDev = 64, kMaxEntries = 32;
+  constexpr int kMaxDev = 64;
   struct Entry {
     const void* fn;
     int bytes;
   };
   static std::mutex mu;
-  static Entry done[kMaxDev][kMaxEntries];
-  static int used[kMaxDev] = {0};
+  static std::vector<Entry> done[kMaxDev];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used[dev]; ++i)
-    if (done[dev][i].fn == fn && done[dev][i].bytes >= bytes) return cudaSuccess;
+  Entry* known = nullptr;
+  for (Entry& e : done[dev])
+    if (e.fn == fn) known = &e;
+  if (known && known->bytes >= bytes) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) {
-    for (int i = 0; i < used[dev]; ++i)
-      if (done[dev][i].fn == fn) {
-        done[dev][i].bytes = bytes;
-        return e;
-      }
-    if (used[dev] < kMaxEntries) done[dev][used[dev]++] = Entry{fn, bytes};
+  if (e != cudaSuccess) return e;
+  if (known) {
+    known->bytes = bytes;
+  } else {
+    try {
+      done[dev].push_back(Entry{fn, bytes});
+    } catch (const std::bad_alloc&) {  // (the next launch makes the driver call again)
+    }
   }
   return e;
 }

@@ -85,3 +85,53 @@ def test_no_function_spills(name):
             if m.group(1) != "0" or m.group(2) != "0":
                 spilling.append((function, line.strip()))
     assert seen and not spilling, spilling
+
+
+HARNESS = r"""
+#include <cuda_runtime_api.h>
+#include <cstdio>
+static int calls = 0, device = 0;
+static cudaError_t answer = cudaSuccess;
+extern "C" {
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { ++calls; return answer; }
+cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+const char* cudaGetErrorString(cudaError_t) { return ""; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { *v = 1; return cudaSuccess; }
+void** __cudaRegisterFatBinary(void*) { return nullptr; }
+void __cudaRegisterFatBinaryEnd(void**) {}
+void __cudaUnregisterFatBinary(void**) {}
+}
+namespace gs { cudaError_t max_dynamic_smem(const void* fn, int bytes); }
+static char kernels[100];
+static void all(int bytes) {  // driver calls for a launch of each kernel
+  const int before = calls;
+  for (char& k : kernels) gs::max_dynamic_smem(&k, bytes);
+  printf("%d ", calls - before);
+}
+int main() {
+  answer = cudaErrorInvalidValue;
+  all(100);  // a refused size is not remembered
+  answer = cudaSuccess;
+  all(100), all(100), all(50), all(200), all(100);
+  device = 1;
+  all(200), all(200);
+}
+"""
+
+
+def test_shared_memory_of_a_kernel_is_raised_once(tmp_path):
+    """The driver is called once for a kernel and device, however many kernels there are, and again for more bytes."""
+    nvcc, gxx = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc", shutil.which("g++")
+    if not os.path.exists(nvcc) or not gxx:
+        pytest.skip("nvcc or g++ not available")
+    from gaussian_splatting_gb300 import build
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    (tmp_path / "harness.cpp").write_text(HARNESS)
+    obj, exe = str(tmp_path / "api.o"), str(tmp_path / "harness")
+    for cmd in ([nvcc, *build.NVCC_FLAGS, "-c", os.path.join(build.CSRC, "api.cu"), "-o", obj],
+                [gxx, "-std=c++17", "-I", include, str(tmp_path / "harness.cpp"), obj, "-o", exe, "-lpthread"]):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-2000:]
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert out.stdout.split() == ["100", "100", "0", "0", "100", "0", "100", "0"]
