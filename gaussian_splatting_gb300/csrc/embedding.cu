@@ -625,13 +625,17 @@ __global__ void __launch_bounds__(kThreads) k_embedding_join(const SumArgs a) {
 // rows.  A block of the second step takes a bucket, or a part of `cap` rows of one that has more, sorts it in shared memory
 // and sums it up as above.  Whole buckets are written at once, zeros included; the sums of parts go to the workspace, for a
 // third step that joins them in order.
+// Parts' sums take a place for each of a bucket's codes, and most buckets may have little more rows than a part: places for all of
+// these would be two thirds as many sums as dy has rows.  Where that is much, there are places for one part of every bucket that can
+// have several and an eighth more; where the indices are such that these are too few, parts have 2, 4, .. times `cap` rows, which a
+// block takes in turn.
 constexpr int kPartWarps = kPartThreads / 32, kPartItems = 16;  // pairs of a thread in a tile
 constexpr int kMostBuckets = 2048, kMostCodes = 2048;  // a thread has four of either
 constexpr int kMostRows = 6144;                        // of a part
 struct Part {
   uint32_t bucket, begin, end, slot;  // its pairs; where the sums go, or kWhole
 };
-struct Bucket {  // of several parts
+struct Bucket {  // of more than `cap` rows
   uint32_t bucket, slot, parts, unused;
 };
 constexpr uint32_t kWhole = 0xffffffffu;
@@ -641,11 +645,11 @@ struct PartArgs {
   uint32_t* counts;    // [tiles][padded buckets]
   uint32_t* totals;    // of the buckets
   Part* parts;
-  Bucket* many;        // buckets of several parts
+  Bucket* many;        // buckets of more than `cap` rows
   uint32_t* numbers;   // of parts and of those buckets
-  float* sums;         // [parts of those][codes][ldp]
-  uint32_t* seen;      // [parts of those][words]: codes that have rows
-  int tiles, buckets, padded, shift, codes, cap;
+  float* sums;         // [slots][codes][ldp]
+  uint32_t* seen;      // [slots][words]: codes that have rows
+  int tiles, buckets, padded, shift, codes, cap, slots;
 };
 
 // How many pairs with the same digit the warp had before, in its row of counters: what an atomic addition returns, unless
@@ -771,24 +775,30 @@ __global__ void __launch_bounds__(1024) k_embedding_bucket_scan(const PartArgs a
 // own: inlined, it makes the kernel spill.)
 __device__ __noinline__ void list_parts(const PartArgs& a, uint4 sizes, uint4 first, uint32_t* s_sums) {
   const uint32_t size[4] = {sizes.x, sizes.y, sizes.z, sizes.w}, from[4] = {first.x, first.y, first.z, first.w};
-  uint32_t parts[4], all = 0, several = 0, buckets = 0;
+  uint32_t parts[4], all, several, buckets, sum_several;
+  uint32_t slot;
+  for (uint32_t cap = a.cap;; cap *= 2) {  // (as large as all rows at last: one for each such bucket, which fits)
+    all = several = buckets = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    parts[j] = (int)threadIdx.x * 4 + j >= a.buckets ? 0u : size[j] <= (uint32_t)a.cap ? 1u : (size[j] - 1) / (uint32_t)a.cap + 1;
-    all += parts[j];
-    if (parts[j] > 1) several += parts[j], ++buckets;
+    for (int j = 0; j < 4; ++j) {
+      parts[j] = (int)threadIdx.x * 4 + j >= a.buckets ? 0u : size[j] <= (uint32_t)a.cap ? 1u : (size[j] - 1) / cap + 1;
+      all += parts[j];
+      if (size[j] > (uint32_t)a.cap) several += parts[j], ++buckets;
+    }
+    slot = block_scan<kPartThreads>(several, s_sums, sum_several);
+    if (sum_several <= (uint32_t)a.slots || cap >> 31) break;
   }
-  uint32_t sum_all, sum_several, sum_buckets;
-  uint32_t to = block_scan<kPartThreads>(all, s_sums, sum_all), slot = block_scan<kPartThreads>(several, s_sums, sum_several),
-           list = block_scan<kPartThreads>(buckets, s_sums, sum_buckets);
+  uint32_t sum_all, sum_buckets;
+  uint32_t to = block_scan<kPartThreads>(all, s_sums, sum_all), list = block_scan<kPartThreads>(buckets, s_sums, sum_buckets);
   if (threadIdx.x == 0) a.numbers[0] = sum_all, a.numbers[1] = sum_buckets;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t d = threadIdx.x * 4 + j, n = parts[j];
-    if (n > 1) a.many[list++] = Bucket{d, slot, n, 0u};
+    const bool whole = size[j] <= (uint32_t)a.cap;
+    if (n && !whole) a.many[list++] = Bucket{d, slot, n, 0u};
     const uint32_t rows = n ? (size[j] + n - 1) / n : 0u;
     for (uint32_t p = 0; p < n; ++p)
-      a.parts[to++] = Part{d, from[j] + min(p * rows, size[j]), from[j] + min((p + 1) * rows, size[j]), n > 1 ? slot++ : kWhole};
+      a.parts[to++] = Part{d, from[j] + min(p * rows, size[j]), from[j] + min((p + 1) * rows, size[j]), whole ? kWhole : slot++};
   }
 }
 
@@ -857,15 +867,15 @@ size_t part_bytes(int cap, int codes, int ve) {
   const size_t ring = 4 * 16 * kPartThreads;  // (not used where vectors are shorter)
   return 4 * (digits + 4) + std::max(2 * kPartWarps * digits, 6 * list + 4 * kPartThreads * (2 * (size_t)ve + 1) + ring);
 }
-template <typename T, int VE>
-__global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartArgs p, const int g) {
-  follow();
-  if (blockIdx.x >= p.numbers[0]) return;
+// `m` rows of a part from pair `from` on, `cap` at most.  TURNS: there may be more of the part; s_seen: those of its codes that had
+// rows before these.
+template <typename T, int VE, bool TURNS>
+__device__ __forceinline__ void sum_rows(const PartArgs& p, const int g, const Part& part, const uint32_t from, const int m,
+                                         uint32_t* s_seen) {
   extern __shared__ __align__(16) uint32_t s_dyn[];
   __shared__ uint32_t s_sums[kPartWarps];
   const SumArgs& a = p.s;
-  const Part part = p.parts[blockIdx.x];
-  const int m = (int)(part.end - part.begin), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int digits = max(p.codes, 4), list = p.cap + 8;
   uint32_t* s_start = s_dyn;
   uint16_t* counters = reinterpret_cast<uint16_t*>(s_dyn + digits + 4);
@@ -883,7 +893,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   for (int i = 0; i < kItems; ++i) {
     key[i] = 0u;
     if (i * 32 < share && i0 + i * 32 < m) {
-      const uint32_t v = p.pairs[part.begin + i0 + i * 32].x;
+      const uint32_t v = p.pairs[from + i0 + i * 32].x;
       key[i] = v & (uint32_t)(p.codes - 1);
     }
   }
@@ -908,7 +918,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   for (int i = 0; i < kItems; ++i)
     if (i * 32 < share && i0 + i * 32 < m) {
       const uint32_t to = key[i] >> 16;
-      s_key[to] = (uint16_t)key[i], s_row[to] = p.pairs[part.begin + i0 + i * 32].y;
+      s_key[to] = (uint16_t)key[i], s_row[to] = p.pairs[from + i0 + i * 32].y;
     }
   __syncthreads();
   // the sums
@@ -924,8 +934,20 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
       write_sum<T, VE>(a, code0 + c, col, sum);
     } else if (col < a.width) {
       float* to = p.sums + ((int64_t)part.slot * p.codes + c) * a.ldp + col;
+      float f[VE];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) to[e] = sum[e];
+      for (int e = 0; e < VE; ++e) f[e] = sum[e];
+      if (TURNS && from != part.begin && (s_seen[c >> 5] >> (c & 31) & 1u)) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = to[e] + f[e];
+      }
+      if constexpr (VE >= 4) {  // (rows of `ldp`, a multiple of 8)
+#pragma unroll
+        for (int e = 0; e < VE; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) to[e] = f[e];
+      }
     }
   };
   uint32_t code;
@@ -936,15 +958,19 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
   if (wl == 0 && walker < walkers) flags[walker] = flag;
   // codes without rows
   const int words = (p.codes + 31) / 32;
-  for (int w = warp; w < words; w += kPartWarps) {
+  auto have = [&](int w, bool there) {
+    const int c = w * 32 + lane;
+    return __ballot_sync(0xffffffffu, there && s_start[min(c, digits - 1)] != s_start[min(c, digits - 1) + 1]);
+  };
+  for (int w = warp; (whole || !TURNS) && w < words; w += kPartWarps) {
     const int c = w * 32 + lane;
     const bool there = c < p.codes && code0 + c < (uint32_t)a.n;
-    const uint32_t have = __ballot_sync(0xffffffffu, there && s_start[min(c, digits - 1)] != s_start[min(c, digits - 1) + 1]);
+    const uint32_t now = have(w, there);
     if (whole) {
-      const uint32_t empty = __ballot_sync(0xffffffffu, there) & ~have;
+      const uint32_t empty = __ballot_sync(0xffffffffu, there) & ~now;
       if (empty) write_zeros<T, VE>(a, empty, code0 + w * 32, g, blockIdx.y);
     } else if (lane == 0 && blockIdx.y == 0) {
-      p.seen[(int64_t)part.slot * words + w] = have;
+      p.seen[(int64_t)part.slot * words + w] = now;
     }
   }
   __syncthreads();
@@ -952,6 +978,36 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
     float acc[VE];
     join<VE>(tail, ends, flags, true, walker, walkers, g, wl, acc);
     put(code, acc);
+  }
+  if (!TURNS || whole) return;
+  __syncthreads();
+  for (int w = warp; w < words; w += kPartWarps) {
+    const uint32_t now = have(w, w * 32 + lane < p.codes);
+    if (lane == 0) s_seen[w] = from != part.begin ? s_seen[w] | now : now;
+  }
+}
+// TURNS: parts may have more than `cap` rows.  (11M rows of 32 float32, 2M codes: 396 us either way.  Where most buckets have two
+// parts, which then are one in two turns: 11M of 32 float32, codes from 600K of 2M, 567 and 513 us; 8M of 64 bfloat16, 600K codes, 427
+// and 439.)
+template <typename T, int VE, bool TURNS>
+__global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartArgs p, const int g) {
+  follow();
+  if (blockIdx.x >= p.numbers[0]) return;
+  const Part part = p.parts[blockIdx.x];
+  if constexpr (!TURNS) {
+    sum_rows<T, VE, false>(p, g, part, part.begin, (int)(part.end - part.begin), nullptr);
+  } else {
+    __shared__ uint32_t s_seen[kMostCodes / 32];
+    for (uint32_t from = part.begin;; from += p.cap) {
+      sum_rows<T, VE, true>(p, g, part, from, (int)min(part.end - from, (uint32_t)p.cap), s_seen);
+      if (part.end - from <= (uint32_t)p.cap) break;
+      __syncthreads();  // (the next rows take the same memory)
+    }
+    if (part.slot == kWhole) return;
+    if (blockIdx.y != 0) return;
+    __syncthreads();
+    const int words = (p.codes + 31) / 32;
+    for (int w = threadIdx.x; w < words; w += kPartThreads) p.seen[(int64_t)part.slot * words + w] = s_seen[w];
   }
 }
 
@@ -1233,7 +1289,8 @@ int64_t blocks_of(int64_t rows, int g, int ve) {
 
 struct Buckets {
   int shift, count, padded, codes, cap, tiles;
-  int64_t parts, several, many, words;  // at most: parts, those of buckets with more than one, such buckets; of a part's codes
+  bool turns;  // parts may have several times `cap` rows
+  int64_t parts, slots, many, words;  // at most: parts, buckets of more than `cap` rows; places of their parts' sums; of a part's codes
 };
 // Whether the buckets take a call, and how.  They save passes over the pairs, but the sort's shorter kernels are done sooner
 // where there is little to sort.  Us by the sort and by buckets: 4,096 codes of 64 bfloat16 1M rows 60 and 66, 2M 107 and 94,
@@ -1251,7 +1308,12 @@ bool buckets_take(const gs_embedding_desc* d, Buckets& b) {
   while (b.shift < 11 && (d->rows << (b.shift + 1)) / d->n <= b.cap * 15 / 16 && (8 << b.shift) <= b.cap) ++b.shift;
   b.count = (int)((d->n - 1) >> b.shift) + 1, b.padded = (b.count + 3) / 4 * 4, b.codes = 1 << b.shift;
   b.tiles = (int)((d->rows + kPartThreads * kPartItems - 1) / (kPartThreads * kPartItems));
-  b.many = d->rows / b.cap, b.parts = b.count + b.many, b.several = 2 * b.many;
+  b.many = std::min<int64_t>(d->rows / b.cap, b.count);
+  // places for any number of parts (two for each that can be full) where they take little space beside dy
+  b.slots = 2 * (d->rows / b.cap);
+  if (4 * b.slots * b.codes * ((d->width + 7) / 8 * 8) > std::max<int64_t>(64 << 20, d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) / 4))
+    b.turns = true, b.slots = b.many + d->rows / b.cap / 8;
+  b.parts = b.count + b.slots;
   b.words = (b.codes + 31) / 32;
   return true;
 }
@@ -1270,12 +1332,12 @@ size_t carve(PartArgs* a, char* base, const gs_embedding_desc* d, const Buckets&
   t.parts = (Part*)take(sizeof(Part) * (size_t)b.parts);
   t.many = (Bucket*)take(sizeof(Bucket) * (size_t)b.many);
   t.numbers = (uint32_t*)take(8);
-  t.sums = (float*)take(4 * (size_t)b.several * b.codes * ldp);
-  t.seen = (uint32_t*)take(4 * (size_t)b.several * b.words);
+  t.sums = (float*)take(4 * (size_t)b.slots * b.codes * ldp);
+  t.seen = (uint32_t*)take(4 * (size_t)b.slots * b.words);
   if (a) {
     t.s = a->s;
     t.s.ldp = ldp;
-    t.tiles = b.tiles, t.buckets = b.count, t.padded = b.padded, t.shift = b.shift, t.codes = b.codes, t.cap = b.cap;
+    t.tiles = b.tiles, t.buckets = b.count, t.padded = b.padded, t.shift = b.shift, t.codes = b.codes, t.cap = b.cap, t.slots = (int)b.slots;
     *a = t;
   }
   return at;
@@ -1362,11 +1424,12 @@ gs_status launch_buckets(const char* where, const PartArgs& a, cudaStream_t st) 
 template <typename T, int VE>
 gs_status launch_parts(const char* where, const PartArgs& a, const Buckets& b, cudaStream_t st) {
   const int vectors = (a.s.width + VE - 1) / VE;
-  const cudaError_t e = gs::max_dynamic_smem((const void*)k_embedding_part<T, VE>, (int)part_bytes(kMostRows, kMostCodes, VE));
+  const auto kernel = b.turns ? k_embedding_part<T, VE, true> : k_embedding_part<T, VE, false>;
+  const cudaError_t e = gs::max_dynamic_smem((const void*)kernel, (int)part_bytes(kMostRows, kMostCodes, VE));
   if (e != cudaSuccess) return gs::set_error(GS_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
   // as many lanes to a walker as a row has vectors, or equal slabs of up to 32
   const int slabs = (vectors + 31) / 32, lanes = (vectors + slabs - 1) / slabs;
-  gs::launch(k_embedding_part<T, VE>, dim3((unsigned)b.parts, (unsigned)slabs), kPartThreads, part_bytes(b.cap, b.codes, VE), st, a, lanes);
+  gs::launch(kernel, dim3((unsigned)b.parts, (unsigned)slabs), kPartThreads, part_bytes(b.cap, b.codes, VE), st, a, lanes);
   if (b.many) {
     const int g = lanes_of(a.s.width, VE), walkers = kThreads / g, codes = std::min(walkers, b.codes);
     const int64_t runs = b.many * ((b.codes + codes - 1) / codes);

@@ -556,7 +556,8 @@ gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy, const voi
  *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the sizes and the indices
  *   decide: no atomics on values, the same bits each run.
  *   workspace  gs_embedding_bwd_workspace_size(d) bytes, 256-byte aligned (may be 0: NULL).  From 1.5M rows on it may
- *              hold float32 sums, two thirds as many rows of them as dy has.
+ *              hold float32 sums: up to 64 MB or a quarter of dy's bytes, or a row of them for each code and for
+ *              each 24 of dy's rows (three eighths as many rows as dy has at most).
  * rows == 0 writes zeros.
  */
 typedef struct {

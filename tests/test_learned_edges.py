@@ -135,3 +135,20 @@ def test_shared_memory_of_a_kernel_is_raised_once(tmp_path):
         assert r.returncode == 0, r.stderr[-2000:]
     out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert out.stdout.split() == ["100", "100", "0", "0", "100", "0", "100", "0"]
+
+
+@pytest.mark.parametrize("bits", [16, 32])
+@pytest.mark.parametrize("width", [1, 4, 27, 64, 100, 600])
+def test_embedding_gradient_workspace_is_bounded(lib, bits, width):
+    """Besides sums, 20 bytes a row (lists of the sort, twice 8, and its counts; or pairs and theirs), a bit a code, the sums at the
+    ends of the sort's parts (a quarter of dy's values at most) and a few MB."""
+    padded = (width + 7) // 8 * 8
+    for rows in (9_000, 100_000, 1_572_864, 2_000_000, 4_000_001, 11_000_000, 50_000_000, 400_000_000):
+        for n in (1, 257, 5_000, 70_000, 300_000, 1_000_001, 1 << 21, (1 << 22) - 3, 1 << 22, 20_000_000):
+            d = N.EmbeddingDesc(rows, n, width, width, width, N.GS_BF16 if bits == 16 else N.GS_F32, 32, 1.0)
+            need = lib.gs_embedding_bwd_workspace_size(C.addressof(d))
+            dy = rows * width * bits // 8
+            of_rows = min(n + 2048 + rows // 24, rows * 3 // 8)
+            sums = max(64 << 20, dy // 4, 4 * padded * of_rows)
+            ends = rows * padded if rows < 1 << 21 or n > 1 << 22 else 0
+            assert need <= sums + 20 * rows + n // 8 + ends + (8 << 20), (rows, n, need, sums)

@@ -18,13 +18,36 @@ sys.path.insert(0, os.path.join(ROOT, "tests"))
 
 from gaussian_splatting_gb300 import dense  # noqa: E402
 from gaussian_splatting_gb300._native import GSError  # noqa: E402
-from test_learned_gpu import BF16, CHAIN, F32, ROUND, TINY, U, _close, _norm_case, _norm_grads, _rand, _sum_u  # noqa: E402
+from test_learned_gpu import BF16, CHAIN, F32, ROUND, TINY, U, _close, _gen, _gradient, _norm_case, _norm_grads, _rand, _sum_u  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 both = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 # rows of a map: a block holds a group, or two passes do; rows on 16 bytes, or one value a thread
 forms = pytest.mark.parametrize("rows", [50, 20_011], ids=["one-kernel", "two-passes"])
 vectors = pytest.mark.parametrize("pad,shift", [(0, 0), (2, 2), (1, 1)], ids=["whole", "pairs", "single"])
+
+
+# ------------------------------------------------------------------ code lookup
+# codes that have rows, out of n: buckets of little more rows than a block takes at once, of many times as many, some of either
+FULL = [(1_600_000, 1_000_000, 204_800, 32), (1_600_000, 1_000_000, 204_800, 9), (1_700_000, 1 << 22, 600_000, 12),
+        (12_000_000, 2000, 2000, 40), (8_000_000, 300, 280, 40)]
+
+
+@both
+@pytest.mark.parametrize("case", FULL, ids=str)
+def test_embedding_buckets_of_more_parts_than_places(case, dtype):
+    """Parts' sums have places for a part of each bucket and a few more: with indices that make most buckets take two, or few
+    buckets hundreds, blocks take several runs of rows in turn."""
+    rows, n, used, width = case
+    idx = (torch.rand(rows, generator=_gen(5), device="cuda", dtype=torch.float64) * used).int().clamp(max=used - 1)
+    idx[::1000] = n - 1 - idx[::1000]
+    idx[7::5003] = -1
+    dy = _rand((rows, width), dtype, 6, 1e-3)
+    got = dense.embedding_bwd(dy, idx, n, -2.0, dtable=torch.ones((n, width), dtype=dtype, device="cuda"))
+    want, mag, counts = _gradient(dy, idx, n, -2.0)
+    _close(got, want, (8 + 2 * counts.double().sqrt())[:, None] * U * mag + 1.01 * ROUND[dtype] * want.abs() + TINY, "dtable")
+    assert not got[counts == 0].any()
+    assert torch.equal(dense.embedding_bwd(dy, idx, n, -2.0), got)
 
 
 # ------------------------------------------------------------------ group norm
