@@ -1,4 +1,5 @@
-"""Code lookup, group norm and AdamW where their arithmetic is at its ends.
+"""Code lookup, group norm and AdamW where their arithmetic is at its ends, past 2^31 elements, and in graphs that are replayed
+on inputs of their own.
 
 u = 2^-24 (a 32-bit rounding); what each tolerance counts stands at its test.
 """
@@ -18,7 +19,8 @@ sys.path.insert(0, os.path.join(ROOT, "tests"))
 
 from gaussian_splatting_gb300 import dense  # noqa: E402
 from gaussian_splatting_gb300._native import GSError  # noqa: E402
-from test_learned_gpu import BF16, CHAIN, F32, ROUND, TINY, U, _close, _gen, _gradient, _norm_case, _norm_grads, _rand, _sum_u  # noqa: E402
+from test_learned_gpu import (BF16, CHAIN, F32, ROUND, TINY, U, _check_norm_fwd, _close, _gen, _gradient, _indices,  # noqa: E402
+                              _norm_case, _norm_grads, _rand, _sum_u, _tensors)
 
 pytestmark = pytest.mark.gpu
 both = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
@@ -179,6 +181,36 @@ def test_groupnorm_first_rows_unlike_the_others(shape):
     _close(mean, X.mean((1, 3)), 57 * U * X.abs().mean((1, 3)), "mean")
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_groupnorm_offsets_past_2_to_31(act):
+    """Rows far apart: the same results as from their copies."""
+    samples, rows, width, groups = 2, 40, 48, 3
+    far = [torch.empty((samples * rows, 1 << 26), dtype=BF16, device="cuda")[:, :width] for _ in range(2)]
+    near, gamma, beta = _norm_case(samples, rows, width, groups, BF16, 9)
+    dy = _rand(near.shape, BF16, 10)
+    far[0].copy_(near)
+    want = dense.groupnorm_fwd(near, gamma, beta, groups, samples, act)
+    got = dense.groupnorm_fwd(far[0], gamma, beta, groups, samples, act, out=far[1])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    grads = dense.groupnorm_bwd(dy, near, gamma, beta, *want[1:], act=act, skip=dy)
+    far[1].copy_(dy)
+    got = dense.groupnorm_bwd(far[1], far[0], gamma, beta, *want[1:], act=act, skip=far[1], dx=far[1])
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    del far, got
+    # more than 2^31 values
+    x = torch.empty((2, 1 << 21, 520), dtype=BF16, device="cuda")
+    x[:] = _rand((1 << 10, 520), BF16, 11).repeat(1 << 11, 1)
+    gamma, beta = _rand((520,), BF16, 12, 0.1, mean=1.0), _rand((520,), BF16, 13)
+    few = x[0, :1 << 10].contiguous()
+    y, mean, rstd = dense.groupnorm_fwd(x.view(-1, 520), gamma, beta, 65, 2, act)
+    _check_norm_fwd(1, 1 << 10, 65, few, gamma, beta, act, 1e-5, (y[-(1 << 10):], mean[1:], rstd[1:]))
+    assert torch.equal(y[:1 << 10], y[-(1 << 10):]) and torch.equal(mean[0], mean[1])
+    dx, _, _ = dense.groupnorm_bwd(x.view(-1, 520), x.view(-1, 520), gamma, beta, mean, rstd, act=act, need_dparams=False)
+    want = _norm_grads(1, 65, few, few, gamma, beta, mean[:1], rstd[:1], act, None)["dx"]
+    _close(dx[-(1 << 10):], *want, "dx")
+    assert torch.equal(dx[:1 << 10], dx[-(1 << 10):])
+
+
 # ------------------------------------------------------------------ AdamW
 def _off(n, dtype, shift):
     return torch.zeros(n + shift, dtype=dtype, device="cuda")[shift:]
@@ -237,3 +269,68 @@ def test_adamw_refuses_arrays_that_overlap():
     # a gradient is only read: two tensors may share one; what lies side by side does not overlap
     dense.adamw(**args(grads=[one[:900], one[:900]]), step=1)
     dense.adamw(**args(params=[one[:900], one[900:1800]]), step=1)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_adamw_offsets_past_2_to_31(shift):
+    """More than 2^31 values in a tensor: the first and the last of them as a tensor of their own."""
+    n, run = (1 << 31) + 5_000, 256
+    p, g = _off(n, F32, shift), _off(n, BF16, shift)
+    (m,), (v,), scales = dense.adamw_state([p], 8)
+    few = {}
+    for at in (0, (n - 4_000) // run * run):
+        part = slice(at, at + 4_000)
+        p[part], g[part] = _rand((p[part].numel(),), F32, 2), _rand((g[part].numel(),), BF16, 3)
+        few[at] = (part, p[part].clone(), g[part].clone())
+    dense.adamw([p], [g], [m], [v], 1, weight_decay=0.1, scales=scales)
+    for at, (part, q, h) in few.items():
+        m2, v2, s2 = dense.adamw_state([q], 8)
+        dense.adamw([q], [h], m2, v2, 1, weight_decay=0.1, scales=s2)
+        assert torch.equal(q, p[part]) and (q != 0).any()
+        assert torch.equal(s2[0][0][:15], scales[0][0][at // run:at // run + 15])
+    assert not p[5_000:1 << 20].any() and not p[-(1 << 20):-5_000].any()
+
+
+# ------------------------------------------------------------------ graphs
+def _inputs(seed):
+    return [_rand((300, 24), F32, seed), _indices(5000, 300, "skewed", seed), _rand((24,), F32, seed + 1, 0.1, mean=1.0),
+            _rand((24,), F32, seed + 2)], _tensors([300 * 24, 24, 24], F32, seed + 3, 0, 8)
+
+
+def _live(state):
+    p, _, m, v, scales = state
+    return [*p, *[t.view(torch.uint8) for t in (*m, *v)], *scales[0], *scales[1]]
+
+
+def _calls(inputs, state, step):
+    table, idx, gamma, beta = inputs
+    y = dense.embedding_fwd(table, idx, 2.0)
+    z, mean, rstd = dense.groupnorm_fwd(y, gamma, beta, 4, 5, "silu")
+    dx, dg, db = dense.groupnorm_bwd(z, y, gamma, beta, mean, rstd, act="silu")
+    dt = dense.embedding_bwd(dx, idx, 300, 2.0)
+    p, _, m, v, scales = state
+    dense.adamw(p, [dt.view(-1), dg, db], m, v, step, scales=scales)
+    return [y, z, mean, rstd, dx, dg, db, dt]
+
+
+def test_graphs_replayed_on_new_inputs():
+    """Two graphs that share a pool of memory, replayed in turn on inputs that they were not captured with: every output and
+    every state that a replay leaves is that of plain calls."""
+    pool, graphs = torch.cuda.graph_pool_handle(), []
+    _calls(*_inputs(29), 5)  # (loads the kernels)
+    torch.cuda.synchronize()
+    for seed in (30, 40):
+        inputs, state = _inputs(seed)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            out = _calls(inputs, state, 5)
+        graphs.append((graph, inputs, state, out))
+    for seed in (30, 50, 60, 50):
+        for graph, inputs, state, out in graphs:
+            fresh, fresh_state = _inputs(seed)
+            for a, b in zip(inputs + _live(state), fresh + _live(fresh_state)):
+                a.copy_(b)
+            want = _calls(fresh, fresh_state, 5)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want + _live(fresh_state), out + _live(state)))
