@@ -370,7 +370,7 @@ PyObject* embedding_bwd(PyObject*, PyObject* const* o, Py_ssize_t count) {
 // samples maps of equally many rows
 void maps(gs_groupnorm_desc& d, int64_t rows, int64_t width, int64_t samples, int64_t groups) {
   if (width > INT32_MAX) throw Refused{"too many features"};
-  if (samples < 0 || (samples == 0 ? rows != 0 : rows % samples != 0))
+  if (samples < 0 || samples > INT32_MAX || (samples == 0 ? rows != 0 : rows % samples != 0))
     throw Refused{std::to_string(rows) + " rows are not " + std::to_string(samples) + " maps of equal size"};
   if (groups < 1 || groups > width || width % groups != 0)
     throw Refused{std::to_string(width) + " channels do not form " + std::to_string(groups) + " groups"};

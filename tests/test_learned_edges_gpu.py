@@ -211,6 +211,14 @@ def test_groupnorm_offsets_past_2_to_31(act):
     assert torch.equal(dx[:1 << 10], dx[-(1 << 10):])
 
 
+def test_groupnorm_refuses_more_maps_than_it_can_number():
+    """Before anything is allocated for them."""
+    x, v = torch.zeros((0, 64), device="cuda"), torch.zeros(64, device="cuda")
+    with pytest.raises(ValueError, match="maps"):
+        dense.groupnorm_fwd(x, v, v, 64, samples=1 << 40)
+    assert dense.groupnorm_fwd(x, v, v, 64, samples=3)[1].shape == (3, 64)
+
+
 # ------------------------------------------------------------------ AdamW
 def _off(n, dtype, shift):
     return torch.zeros(n + shift, dtype=dtype, device="cuda")[shift:]
