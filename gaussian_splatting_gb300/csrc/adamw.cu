@@ -6,8 +6,9 @@
 //   of one: what the second adds to p joins the step, and that sum p keep, with one rounding of p's size.
 // An 8-bit moment is code x scale; v is kept as its root, whose range the type holds (2^-9 to 448: of v 2^35).
 //
-// Bound by memory: 28 bytes a value with 32-bit moments and gradients, 16.1 with 8-bit ones (176M values: 453 us, 417 at the
-// copy's rate; 17M with bfloat16 gradients and copies: 48 and 40).  The tensors' addresses are
+// Bound by memory: 28 bytes a value with 32-bit moments and gradients (80M values: 316 us, 330 at the copy's rate), 16.1 with 8-bit
+// moments (176M values: 430 us, 417 at the copy's rate; 17M with bfloat16 gradients and copies: 48 and 40).  Tensors off 16 bytes
+// take one value an access: 20M values 87 us with 32-bit moments and 74 with 8-bit ones (83 and 47 at the copy's rate).  The tensors' addresses are
 // launch parameters (no table in device memory to fill and wait for), a block looks its tensor up in them.  A warp takes
 // runs of 256 values, eight a lane: the run's largest magnitudes, by which its scales go, are one reduction over the warp.
 #include <algorithm>
@@ -85,7 +86,8 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h = (h ^ (h >> 15)) * 0xBB67AE85u;
   return h ^ (h >> 16);
 }
-// To four significant bits, up where 16 random bits carry from the 16 below them.  The largest value's quotient may be
+// To four significant bits, up where 16 random bits carry from the 16 below them.  (The type has fewer below 2^-6, which the
+// conversion then rounds to the nearest of: a moment fades no further than to 2^-7 or, its root, 2^-6 of a scale that stays.)  The largest value's quotient may be
 // a unit in the last place above 448, and what that is rounded up to is saturated by the conversion.
 __device__ __forceinline__ float at_random(float q, uint32_t noise) {
   return __uint_as_float((__float_as_uint(q) + (noise << 4)) & 0xfff00000u);
@@ -246,7 +248,7 @@ __device__ __forceinline__ void run_of_256(const Tensor& t, int64_t at, int lane
 }
 
 // 40 warps to an SM for 8-bit moments, 48 registers: instructions bound that form as much as memory does, and more warps hide
-// both (176M values: 453 us, 475 with 32 warps and 64 registers).
+// both (176M values: 428 us, 464 with 32 warps and 64 registers).
 template <typename G, int BITS, int MOST>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 10 : 8) k_adamw(const __grid_constant__ Args<MOST> a) {
   follow();

@@ -60,7 +60,9 @@ inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t s
 
 // ------------------------------------------------------------------ device helpers
 // First in every dense-layer kernel: lets the kernel after it be set up, and waits until the one before it is done and
-// its writes are visible (at once where there is none to wait for).  Nothing in memory is touched before.
+// its writes are visible (at once where there is none to wait for).  Nothing in memory is touched before, with one exception: the
+// second pass of the group norm reads the call's inputs before its wait (start_and_follow), for which its first pass lets it begin
+// only after a wait of its own (wait_for_inputs).  What is launched between those two must not write these inputs.
 __device__ __forceinline__ void follow() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -8,7 +8,7 @@
 // All of it in 32 bits, rounded once when stored.
 //
 // Both directions are bound by memory, and both need two passes over a map: one for its sums, one for its output (but a small
-// map's group fits in a block's registers, and one kernel does: 16 maps of 32 x 32 x 64 float32 6.4 us, 10.2 in two).  Blocks
+// map's group fits in a block's registers, and one kernel does: 16 maps of 32 x 32 x 64 float32 6.2 us, 10.2 in two).  Blocks
 // take chunks of a map's rows; a thread owns one vector of neighbouring channels and walks down the rows, so that gamma, beta and
 // the statistics stay in registers and every access of a warp is a run of whole sectors.  The variance is taken about a value of the
 // thread's own rows (their first), so that a mean far from zero costs nothing: a pivot p among a thread's n values with
@@ -17,9 +17,9 @@
 // What a block of the second pass needs of the chunks' sums it adds up by itself, a few kilobytes from L2, or a small kernel
 // between the passes does.
 //
-// 16 maps of 15,965 x 256 bfloat16, SiLU: 68 us, 58 for two readings and a writing at the copy's rate (in one pass, a slab of
+// 16 maps of 15,965 x 256 bfloat16, SiLU: 69 us, 58 for two readings and a writing at the copy's rate (in one pass, a slab of
 // groups held in the shared memory of a cluster of blocks, it took 124: 16 to 24 warps an SM do not hide the arithmetic's
-// latency).  4 images of 1236 x 820 x 64 bfloat16 backward: 390 us, 382 for the two passes' bytes.
+// latency).  4 images of 1236 x 820 x 64 bfloat16 backward: 395 us, 382 for the two passes' bytes.
 #include <algorithm>
 #include <cmath>
 

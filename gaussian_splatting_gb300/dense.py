@@ -143,7 +143,9 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999),
 
     The moments (``adamw_state`` makes them) are float32, or with ``scales`` float8_e4m3fn: ``exp_avg_sq`` then holds the
     root of the second moment, and each 256 neighbouring values of a tensor share a scale.  They are rounded at random, by
-    ``seed`` and ``step`` alone: the same call gives the same bits.  ``copies`` (bfloat16, like ``params``) receive the
+    ``seed`` and ``step`` alone: the same call gives the same bits.  (So does a captured one each time it is replayed, with the
+    same bias corrections: ``step`` and ``lr`` are taken when it is captured.)  A value without gradients in a run whose
+    scales stay keeps a small rest of its moments, which ``gs.h`` states; 32-bit ones fade to zero.  ``copies`` (bfloat16, like ``params``) receive the
     updated parameters, for layers that compute in bfloat16.  With ``counts`` (int64 [records, 2], as
     ``AttributeHead.status`` or ``StepResult.status``) the step is skipped on the device where any record's second
     entry is not zero.  Tensors are contiguous; none may overlap another, but for gradients among

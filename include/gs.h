@@ -553,8 +553,8 @@ gs_status gs_layernorm_bwd(const gs_layernorm_desc* d, const void* dy, const voi
  * gs_embedding_bwd -- the table's gradient, from dy [rows][width] (stride ldy):
  *   dtable[v] = scale (sum of dy[r] over the rows r with idx[r] = v), n x width, stride ldt, every row overwritten (a
  *   code that no row has gets zeros).  dtable must not overlap dy or idx.
- *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the sizes and the indices
- *   decide: no atomics on values, the same bits each run.
+ *   Rows are sorted by index, stably, and each sum is taken in 32 bits in an order that the sizes, the
+ *   indices, the strides and the arrays' alignment decide: no atomics on values, the same call gives the same bits.
  *   workspace  gs_embedding_bwd_workspace_size(d) bytes, 256-byte aligned (may be 0: NULL).  From 1.5M rows on it may
  *              hold float32 sums: up to 64 MB or a quarter of dy's bytes, or a row of them for each code and for
  *              each 24 of dy's rows (three eighths as many rows as dy has at most).
@@ -626,6 +626,13 @@ gs_status gs_groupnorm_bwd(const gs_groupnorm_desc* d, const void* dy, const voi
  * and the value's place in the call, counting every tensor from a multiple of 256: with c that count,
  *   h = c 0x9E3779B1 + seed 0x6A09E667 + step 0xBB67AE85; h = (h ^ h >> 16) 0x6A09E667; h = (h ^ h >> 15) 0xBB67AE85;
  *   h = h ^ h >> 16  (modulo 2^32): its low half for m, its high half for v.
+ * Rounding to the nearest below 2^-6 scale has a consequence.  Where a value gets no gradients any more while its run's scales
+ * stay (a code that is hardly ever looked up, beside common ones), its m fades to 2^-7 of m's scale and its root to 2^-6 of the
+ * root's (1 / 57,344 and 1 / 28,672 of the run's largest) and no further: p then moves on by up to lr / 2 times the ratio of the
+ * two scales a step, besides its decay.  Moments in 32 bits fade to zero.
+ * step, lr and the other numbers are those of the call.  A call captured into a graph keeps them: each replay has the same
+ * bias corrections and adds the same random bits, so that 8-bit moments are no longer rounded without bias over steps.  Capture
+ * a step of its own for each number, or update outside the graph.
  * The 8-bit moments' arithmetic is IEEE single precision, one rounding an operation, so that their bits are defined.  A
  * NaN or an infinity in g spoils its value's moments, of 8 bits those of its whole run.
  *   tensors    HOST array of `count` descriptions.  param float32; grad of grad_dtype; exp_avg, exp_avg_sq; their scales
