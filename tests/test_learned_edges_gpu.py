@@ -32,6 +32,7 @@ vectors = pytest.mark.parametrize("pad,shift", [(0, 0), (2, 2), (1, 1)], ids=["w
 # ------------------------------------------------------------------ code lookup
 # codes that have rows, out of n: buckets of little more rows than a block takes at once, of many times as many, some of either
 FULL = [(1_600_000, 1_000_000, 204_800, 32), (1_600_000, 1_000_000, 204_800, 9), (1_700_000, 1 << 22, 600_000, 12),
+        (1_700_000, 1 << 22, 400_000, 20), (26_000_000, 1_000_000, 1_000_000, 8), (2_000_000, 1_000_000, 3, 64),
         (12_000_000, 2000, 2000, 40), (8_000_000, 300, 280, 40)]
 
 
