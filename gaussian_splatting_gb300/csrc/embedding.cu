@@ -11,7 +11,8 @@
 // first sorted by code, stably, and then added up in equal parts of the sorted rows by groups of lanes ("walkers"), in registers
 // as long as the code stays the same.  A code whose rows lie inside one walker's part is written at once; the sums at a
 // part's ends are joined in order, first among the walkers of a block in shared memory, then among blocks by another kernel.
-// The parts follow from the sizes, the indices and the vector that strides and alignment allow, so the same call gives the same bits.  Three forms, by size:
+// The parts follow from the sizes, the indices and the vector that strides and alignment allow, so the same call gives the
+// same bits.  Three forms, by size:
 //   few rows     one kernel, whose blocks own runs of codes, pick their rows out of all indices and sort them in shared memory;
 //   more         a radix sort of (code, row) pairs, up to eight bits a pass, each pass three kernels (digit counts of tiles,
 //                their scan by digit, a scatter through shared memory), then the sums;
@@ -1003,8 +1004,7 @@ __global__ void __launch_bounds__(kPartThreads, 2) k_embedding_part(const PartAr
       if (part.end - from <= (uint32_t)p.cap) break;
       __syncthreads();  // (the next rows take the same memory)
     }
-    if (part.slot == kWhole) return;
-    if (blockIdx.y != 0) return;
+    if (part.slot == kWhole || blockIdx.y != 0) return;
     __syncthreads();
     const int words = (p.codes + 31) / 32;
     for (int w = threadIdx.x; w < words; w += kPartThreads) p.seen[(int64_t)part.slot * words + w] = s_seen[w];
@@ -1311,9 +1311,10 @@ bool buckets_take(const gs_embedding_desc* d, Buckets& b) {
   b.many = std::min<int64_t>(d->rows / b.cap, b.count);
   // places for any number of parts (two for each that can be full) where they take little space beside dy
   b.slots = 2 * (d->rows / b.cap);
-  if (4 * b.slots * b.codes * ((d->width + 7) / 8 * 8) > std::max<int64_t>(64 << 20, d->rows * d->width * (int64_t)gs::dtype_size(d->dtype) / 4))
+  const int64_t sums = 4 * b.slots * b.codes * ((d->width + 7) / 8 * 8), dy = d->rows * d->width * (int64_t)gs::dtype_size(d->dtype);
+  if (sums > std::max<int64_t>(64 << 20, dy / 4))
     b.turns = true, b.slots = b.many + d->rows / b.cap / 8;
-  b.parts = b.count + b.slots;
+  b.parts = b.count + std::min(b.slots, d->rows / b.cap);  // (a bucket of more than `cap` rows has one more than it can fill)
   b.words = (b.codes + 31) / 32;
   return true;
 }
