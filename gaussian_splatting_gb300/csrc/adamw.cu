@@ -304,10 +304,16 @@ gs_status run_all(const char* where, const gs_adamw_desc* d, const gs_adamw_tens
     const size_t ss = d->state_bits / 8;
     const bool wide = at4(s.param, 4) && at4(s.grad, gs::dtype_size(d->grad_dtype)) && at4(s.exp_avg, ss) &&
                       at4(s.exp_avg_sq, ss) && at4(s.copy, 2);
-    const double keep = 1.0 - s.lr * s.weight_decay;
+    // keep's float towards zero, so that what it lacks has its sign and an infinite parameter stays what it is; nothing is the
+    // smallest float then, which no finite parameter notices
+    const double exact = 1.0 - s.lr * s.weight_decay;
+    float keep = (float)exact;
+    if (std::fabs((double)keep) > std::fabs(exact)) keep = std::nextafter(keep, 0.f);
+    float rest = (float)(exact - keep);
+    if (rest == 0.f && keep != 0.f) rest = std::copysign(FLT_TRUE_MIN, keep);
     a.t[a.count++] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.exp_avg_scale, s.exp_avg_sq_scale,
                             static_cast<__nv_bfloat16*>(s.copy), s.n, (uint32_t)tiles, (uint32_t)place,
-                            (float)keep, (float)(keep - (float)keep), (float)(s.lr / bc1), wide};
+                            keep, rest, (float)(s.lr / bc1), wide};
     tiles += need;
     place += (uint64_t)(s.n + kRun - 1) / kRun * kRun;
   }

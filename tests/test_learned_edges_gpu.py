@@ -247,6 +247,24 @@ def test_adamw_decay_is_not_rounded(decay, bits, shift):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 1e-7, 1e-3, 0.25, 1.5])
+def test_adamw_leaves_the_ends_of_the_range(decay, bits):
+    """Parameters that are infinite, zero, or among the smallest and largest floats, without gradients."""
+    tiny, most = torch.finfo(F32).smallest_normal, torch.finfo(F32).max
+    p = torch.tensor([math.inf, -math.inf, 0.0, -0.0, tiny, -tiny, 2.0 ** -149, most, -most, 1.0], device="cuda").repeat(60)
+    before = p.double()
+    m, v, scales = dense.adamw_state([p], bits)
+    dense.adamw([p], [torch.zeros_like(p)], m, v, 1, 1e-3, weight_decay=decay / 1e-3, scales=scales)
+    keep = 1 - 1e-3 * (decay / 1e-3)
+    assert torch.equal(p.isinf(), before.isinf()) and (p[:2] == before[:2].float() * (1 if keep > 0 else -1)).all()
+    finite = ~before.isinf()
+    want = before[finite] * keep
+    _close(p[finite], want, 1.0001 * U * want.abs() + 2.0 ** -149, "p")
+    if decay == 0.0:
+        assert torch.equal(p, before.float())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("eps", [1e-46, 1e-40, 1.1e-38, 1e-30])
 def test_adamw_smallest_eps(eps, bits):
     """A value that no gradient has reached yet stays where it is, and others move by lr at the first step."""
